@@ -168,8 +168,10 @@ def _values(c):
 def _pack(ck, cv, ek, ev):
     """The library's page blocks [pages, heads, 32 hd + 32] of codes [pages, heads, 16, hd] and exponents."""
     P, H, _, hd = ck.shape
-    k = ck.view(P, H, 4, 2, 2, hd // 64, 4, 16).permute(0, 1, 5, 3, 2, 4, 6, 7).reshape(P, H, -1)
-    v = cv.view(P, H, 4, 4, hd // 32, 8, 4).permute(0, 1, 4, 5, 2, 6, 3).reshape(P, H, -1)
+    t, i = torch.arange(PAGE, device=ck.device)[:, None], torch.arange(hd // 16, device=ck.device)[None, :]
+    at_k, at_v = (i ^ (4 * (t % 2)), i ^ (2 * (t // 4))) if hd == 128 else (i + 0 * t, i ^ (t // 4))
+    k = ck.view(P, H, PAGE, hd // 16, 16)[:, :, t, at_k].reshape(P, H, -1)
+    v = cv.view(P, H, PAGE, hd // 16, 16)[:, :, t, at_v].reshape(P, H, -1)
     tail = torch.zeros((P, H, 8), dtype=torch.float32, device=ck.device)
     tail[..., 0], tail[..., 1] = _pow2(ek), _pow2(ev)
     return torch.cat([k, v, tail.view(torch.uint8).view(P, H, 32)], -1).contiguous()
