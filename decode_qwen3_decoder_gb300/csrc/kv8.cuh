@@ -1,0 +1,90 @@
+// The 8-bit paged KV cache's block format and the conversions its kernels share.
+//
+// A block holds one page (16 tokens) of one KV head: 16 rows of HD K codes, 16 rows of V codes
+// (e4m3, a row's 16-byte chunks permuted by token, see kv8_k_pos / kv8_v_pos), the scales 2^ek
+// and 2^ev as fp32, 24 spare bytes. 32 HD + 32 bytes, so blocks stay 32-byte aligned and one
+// bulk copy brings codes and scales together.
+#pragma once
+
+#include "qw_internal.h"
+
+namespace {
+
+constexpr int KV8_PAGE = 16;
+constexpr int KV8_EMIN = -32;  // exponent of a page of zeros; fp16 values never need less
+
+template <int HD>
+struct Kv8 {
+    static constexpr int CH = HD / 16;        // 16-byte chunks of a row
+    static constexpr int VOFF = 16 * HD;      // V codes
+    static constexpr int SOFF = 32 * HD;      // scales: K, V
+    static constexpr int BLK = 32 * HD + 32;
+};
+
+// 16-byte position of chunk `i` of token `t` in its K row. A fragment load of 8 lanes takes 4
+// chunks of two neighbouring tokens: the odd token's other half keeps them on different banks.
+template <int HD>
+__device__ __forceinline__ int kv8_k_pos(int t, int i) {
+    return HD == 128 ? i ^ ((t & 1) << 2) : i;
+}
+// ... in its V row: there 8 lanes take 2 chunks of tokens t, t + 4, t + 8, t + 12.
+template <int HD>
+__device__ __forceinline__ int kv8_v_pos(int t, int i) {
+    return HD == 128 ? i ^ ((t >> 2) << 1) : i ^ (t >> 2);
+}
+
+__device__ __forceinline__ float kv8_pow2(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
+__device__ __forceinline__ int kv8_log2(float p) { return (int)((__float_as_uint(p) >> 23) & 255) - 127; }  // of a power of two
+
+// Smallest e >= KV8_EMIN with amax <= 448 * 2^e = 1.75 * 2^(e + 8), amax an fp16 value >= 0.
+__device__ __forceinline__ int kv8_exponent(float amax) {
+    const uint32_t u = __float_as_uint(amax);
+    const int x = (int)(u >> 23) - 127;
+    return amax > 0.f ? max(KV8_EMIN, x - 8 + ((u & 0x7FFFFFu) > 0x600000u)) : KV8_EMIN;
+}
+
+// Two e4m3 codes (low byte first) to two halves and back (round to nearest even, |x| <= 448).
+__device__ __forceinline__ uint32_t kv8_dec2(uint32_t codes16) {
+    uint32_t r;
+    const unsigned short c = (unsigned short)codes16;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
+    return r;
+}
+__device__ __forceinline__ uint32_t kv8_enc2(float lo, float hi) {
+    unsigned short r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ void kv8_dec16(const uint4& u, float* x) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t a = kv8_dec2(w[i] & 0xFFFFu), b = kv8_dec2(w[i] >> 16);
+        x[4 * i] = h_lo(a);
+        x[4 * i + 1] = h_hi(a);
+        x[4 * i + 2] = h_lo(b);
+        x[4 * i + 3] = h_hi(b);
+    }
+}
+__device__ __forceinline__ uint4 kv8_enc16(const float* x, float mul) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] = kv8_enc2(x[4 * i] * mul, x[4 * i + 1] * mul) | (kv8_enc2(x[4 * i + 2] * mul, x[4 * i + 3] * mul) << 16);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+}  // namespace
+
+// Host-side check of a view; QW_OK or the recorded error.
+qw_status kv8_check(const qw_kv8* kv, int B, const char* what);
+
+// Device view passed to the kernels.
+struct Kv8View {
+    uint8_t* blocks;
+    const int* table;
+    int n_pages, max_pages, n_kv;
+};
+inline Kv8View kv8_view(const qw_kv8* kv) {
+    return {(uint8_t*)kv->dev_blocks, kv->dev_page_table, kv->n_pages, kv->max_pages, kv->n_kv_heads};
+}

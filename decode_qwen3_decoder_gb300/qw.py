@@ -50,6 +50,21 @@ class qw_weight_ptrs(ctypes.Structure):
                 ("layers", ctypes.POINTER(qw_layer_ptrs))]
 
 
+class qw_kv8(ctypes.Structure):
+    _fields_ = [("dev_blocks", ctypes.c_void_p), ("dev_page_table", ctypes.c_void_p), ("n_pages", ctypes.c_int),
+                ("max_pages", ctypes.c_int), ("n_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int)]
+
+
+class qw_kv8_attn_args(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("max_len", ctypes.c_int), ("max_keys", ctypes.c_int),
+                ("n_heads", ctypes.c_int), ("dtype", ctypes.c_int), ("dev_start", ctypes.c_void_p),
+                ("dev_cu", ctypes.c_void_p), ("dev_q", ctypes.c_void_p), ("ld_q", ctypes.c_size_t),
+                ("scale", ctypes.c_float), ("dev_out", ctypes.c_void_p), ("ld_out", ctypes.c_size_t),
+                ("dev_lse", ctypes.c_void_p), ("dev_score_in", ctypes.c_void_p), ("dev_score_out", ctypes.c_void_p),
+                ("ld_score", ctypes.c_size_t), ("dev_ws", ctypes.c_void_p), ("ws_bytes", ctypes.c_size_t),
+                ("dev_status", ctypes.c_void_p)]
+
+
 _LIB: Optional[ctypes.CDLL] = None
 _VP, _I, _SZ, _P = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.POINTER
 
@@ -87,6 +102,12 @@ SIGNATURES = {
     "qw_profile_set": (_I, [_VP, _I, _P(_VP), _I]),
     "qw_set_option": (_I, [_VP, _I, _I]),
     "qw_trace_set": (_I, [_VP, _VP, _I]),
+    "qw_kv8_block_bytes": (_SZ, [_I]),
+    "qw_kv8_append": (_I, [_P(qw_kv8), _I, _I, _I, _VP, _VP, _VP, _SZ, _VP, _SZ, _I, _VP, _VP]),
+    "qw_kv8_read": (_I, [_P(qw_kv8), _I, _I, _I, _VP, _VP, _VP, _SZ, _VP, _SZ, _I, _VP, _VP]),
+    "qw_kv8_attn_ws_bytes": (_SZ, [_P(qw_kv8), _I, _I, _I, _I, _I, _I]),
+    "qw_kv8_attn": (_I, [_P(qw_kv8), _P(qw_kv8_attn_args), _VP]),
+    "qw_kv8_evict": (_I, [_P(qw_kv8), _I, _I, _VP, _I, _I, _VP, _VP, _VP, _SZ, _VP, _VP, _VP, _VP]),
     "qw_lm_head_argmax_noalloc": (_I, [_VP, _I, _VP, _VP, _VP, _VP]),
 }
 
@@ -270,6 +291,64 @@ def qw_kv_fill_synthetic(kv: int, seq_id: int, n_tokens: int, seed: int, stream=
 
 def qw_last_launch_count(model: int) -> int:
     return load().qw_last_launch_count(model)
+
+
+QW_F16, QW_BF16, QW_F32 = 0, 1, 2
+
+QW_KV8_MAX_BATCH = 1024
+QW_KV8_TIMEOUT = 2
+QW_KV8_BAD_POS = 4
+QW_KV8_RANGE = 8
+
+
+def qw_kv8_block_bytes(head_dim: int) -> int:
+    return load().qw_kv8_block_bytes(head_dim)
+
+
+def qw_kv8_view(blocks_ptr: int, n_pages: int, n_kv_heads: int, head_dim: int, page_table_ptr: int,
+                max_pages: int) -> qw_kv8:
+    """The descriptor of an 8-bit paged cache in the caller's memory; see include/qw.h."""
+    return qw_kv8(dev_blocks=blocks_ptr, dev_page_table=page_table_ptr, n_pages=n_pages, max_pages=max_pages,
+                  n_kv_heads=n_kv_heads, head_dim=head_dim)
+
+
+def qw_kv8_append(kv: qw_kv8, B: int, T: int, max_len: int, start_ptr: int, cu_ptr: int, k_ptr: int, ld_k: int,
+                  v_ptr: int, ld_v: int, dtype: int, status_ptr: int, stream=None) -> None:
+    _check(load().qw_kv8_append(ctypes.byref(kv), B, T, max_len, start_ptr, cu_ptr, k_ptr, ld_k, v_ptr, ld_v, dtype,
+                                status_ptr, _stream(stream)))
+
+
+def qw_kv8_read(kv: qw_kv8, B: int, T: int, max_len: int, start_ptr: int, cu_ptr: int, k_ptr: int, ld_k: int,
+                v_ptr: int, ld_v: int, dtype: int, status_ptr: int, stream=None) -> None:
+    _check(load().qw_kv8_read(ctypes.byref(kv), B, T, max_len, start_ptr, cu_ptr, k_ptr, ld_k, v_ptr, ld_v, dtype,
+                              status_ptr, _stream(stream)))
+
+
+def qw_kv8_attn_ws_bytes(kv: qw_kv8, B: int, T: int, max_len: int, max_keys: int, n_heads: int,
+                         with_score: bool) -> int:
+    return load().qw_kv8_attn_ws_bytes(ctypes.byref(kv), B, T, max_len, max_keys, n_heads, int(with_score))
+
+
+def qw_kv8_attn(kv: qw_kv8, B: int, T: int, max_len: int, max_keys: int, start_ptr: int, cu_ptr: int, q_ptr: int,
+                ld_q: int, n_heads: int, dtype: int, scale: float, out_ptr: int, ld_out: int, lse_ptr: int,
+                score_in_ptr: int, score_out_ptr: int, ld_score: int, ws_ptr: int, ws_bytes: int, status_ptr: int,
+                stream=None) -> None:
+    """lse, score_in and score_out may be 0 (not wanted); see include/qw.h."""
+    a = qw_kv8_attn_args(B=B, T=T, max_len=max_len, max_keys=max_keys, n_heads=n_heads, dtype=dtype,
+                         dev_start=start_ptr, dev_cu=cu_ptr, dev_q=q_ptr, ld_q=ld_q, scale=scale, dev_out=out_ptr,
+                         ld_out=ld_out, dev_lse=lse_ptr or None, dev_score_in=score_in_ptr or None,
+                         dev_score_out=score_out_ptr or None, ld_score=ld_score, dev_ws=ws_ptr, ws_bytes=ws_bytes,
+                         dev_status=status_ptr)
+    _check(load().qw_kv8_attn(ctypes.byref(kv), ctypes.byref(a), _stream(stream)))
+
+
+def qw_kv8_evict(kv: qw_kv8, B: int, max_len: int, len_ptr: int, n_keep: int, n_recent: int, dst_table_ptr: int,
+                 score_ptr: int, score_out_ptr: int, ld_score: int, kept_ptr: int, new_len_ptr: int, status_ptr: int,
+                 stream=None) -> None:
+    """dst_table 0: in place; see include/qw.h."""
+    _check(load().qw_kv8_evict(ctypes.byref(kv), B, max_len, len_ptr, n_keep, n_recent, dst_table_ptr or None,
+                               score_ptr, score_out_ptr, ld_score, kept_ptr, new_len_ptr, status_ptr,
+                               _stream(stream)))
 
 
 def qw_lm_head_argmax_noalloc(model: int, B: int, x_ptr: int, logits_ptr: int, next_ptr: int,

@@ -358,6 +358,122 @@ qw_status qw_quantize_weights(qw_model* m, int bits, void* dev_buf, size_t bytes
 qw_status qw_sample_top_p(int B, int vocab, const float* dev_logits, size_t ld, float temperature, float top_p,
                           const float* dev_uniform, int32_t* dev_next_ids, void* stream);
 
+/* ---- 8-bit paged KV cache: append, attention, eviction ----------------------------------
+ *
+ * Operators on a caller-owned paged cache that holds K and V as 8-bit floats (e4m3) with one
+ * scale for each block of 16 tokens (a page), KV head and tensor: 8.25 bits per element, half
+ * the bytes of the fp16 cache above. They need no model, keep no state between calls and take
+ * every length from device memory, so a captured graph can replay them as lengths change.
+ *
+ * Held values. x is the fp16 rounding (nearest even) of a given element. A page's exponent e is
+ * the smallest integer with max|x| <= 448 * 2^e over its tokens (-32 for a page of zeros); the
+ * code of x is e4m3(x * 2^-e), nearest even, and stands for code * 2^e. Scales are powers of
+ * two so that growing one (a later token of the page is larger) moves the codes already there
+ * exactly, but for those that become e4m3 subnormals.
+ *
+ * Batch description, shared by the calls: entry b of B has dev_start[b] tokens in the cache
+ * before the call and takes rows [dev_cu[b], dev_cu[b + 1]) of the call's T rows (dev_cu is
+ * [B + 1] int32, dev_cu[0] = 0, dev_cu[B] <= T; an entry may have no row). Row i of entry b is
+ * position dev_start[b] + i. max_len (and max_keys, dev_start + rows) bound the entries on the
+ * host, where they size the launch. Position p of entry b lives in slot p % 16 of page
+ * dev_page_table[b * max_pages + p / 16]. Rows of the tensors are ld elements apart and hold
+ * n heads * head_dim contiguous elements; pointers are 16-byte aligned and so is every row
+ * (ld a multiple of 8, of 4 for QW_F32), else QW_ERR_INVALID_ARG. Sequences may share pages
+ * that no call writes.
+ *
+ * Errors found on the device set bits of *dev_status (QW_KV8_*; never cleared here): an entry
+ * whose lengths break their bounds or whose pages are not in [0, n_pages) sets QW_KV8_BAD_POS
+ * and is left out (append: its bad pages are not written; read: its rows are zeros; evict: nothing
+ * moves), or, in attention, its outputs are not valid. Calls on several streams may overlap unless one
+ * writes what another uses; two calls that may overlap need two workspaces. */
+#define QW_KV8_MAX_BATCH 1024
+#define QW_KV8_TIMEOUT 2 /* a bounded wait inside a kernel gave up: outputs not valid       */
+#define QW_KV8_BAD_POS 4 /* see above                                                        */
+#define QW_KV8_RANGE 8   /* an appended value had |x| > 65504 or was NaN: stored as 0        */
+
+/* Element types of the operators' tensors. */
+enum { QW_F16 = 0, QW_BF16 = 1, QW_F32 = 2 };
+
+typedef struct {
+    void* dev_blocks;              /* [n_pages][n_kv_heads] blocks, 32-byte aligned             */
+    const int32_t* dev_page_table; /* [B][max_pages]                                            */
+    int n_pages;
+    int max_pages;
+    int n_kv_heads;
+    int head_dim;                  /* 64 or 128 (else QW_ERR_UNSUPPORTED)                       */
+} qw_kv8;
+
+/* Bytes of one (page, KV head) block: 32 * head_dim code bytes and 32 bytes of scales; 0 for a
+ * head_dim without kernels. A block: 16 rows of head_dim K codes (row = token), 16 rows of V codes,
+ * then the K and the V scale (2^e) as fp32 and 24 bytes unused. The 16-byte chunks of a row are
+ * permuted so that fragment loads meet no bank twice: chunk i of token t (dims 16 i .. + 15) sits
+ * at position i ^ 4 (t % 2) of a K row and i ^ 2 (t / 4) of a V row for head_dim 128; at i and
+ * i ^ (t / 4) for head_dim 64. */
+size_t qw_kv8_block_bytes(int head_dim);
+
+/* Append: quantises the rows of dev_k and dev_v ([T][n_kv_heads * head_dim] of `dtype`) into
+ * their pages. Tokens that a page already holds before dev_start stay (re-coded when the
+ * exponent grows); slots after the last appended one become zeros. Appending the same rows at
+ * the same positions again changes nothing. */
+qw_status qw_kv8_append(const qw_kv8* kv, int B, int T, int max_len, const int32_t* dev_start, const int32_t* dev_cu,
+                        const void* dev_k, size_t ld_k, const void* dev_v, size_t ld_v, int dtype, int32_t* dev_status,
+                        void* stream);
+
+/* Read back: writes the held values of positions dev_start[b] + i to row dev_cu[b] + i of
+ * dev_k and dev_v, rounded to `dtype` (QW_F16: at most 65504). Rows past dev_cu[B] are not written. */
+qw_status qw_kv8_read(const qw_kv8* kv, int B, int T, int max_len, const int32_t* dev_start, const int32_t* dev_cu,
+                      void* dev_k, size_t ld_k, void* dev_v, size_t ld_v, int dtype, int32_t* dev_status,
+                      void* stream);
+
+/* Attention of T query rows ([T][n_heads * head_dim], QW_F16 or QW_BF16) over the cache: the
+ * query at position p of its entry sees the cached positions 0 .. p (its own row among them:
+ * append first). Query head h reads KV head h / (n_heads / n_kv_heads); 1 to 16 query heads
+ * share one. out = softmax(scale * q k) v in the type of q, scale > 0; dev_lse (optional,
+ * [T][n_heads] fp32) gets the natural log of the softmax sums. One query per entry is a decode
+ * step, more are a prompt or a chunk of one.
+ * dev_score_out (optional, [B][n_kv_heads][ld_score] fp32, ld_score >= max_keys): for each cached
+ * position j < dev_start[b] + rows of an entry with rows, dev_score_in (NULL: zeros; may be
+ * dev_score_out) plus the weights that the call's queries give to j, summed over the queries
+ * and the heads of the group; other elements are not written. The order of every sum is fixed:
+ * equal inputs give equal bits.
+ * dev_ws: at least qw_kv8_attn_ws_bytes of the same sizes, 256-byte aligned; any contents. */
+typedef struct {
+    int B, T, max_len, max_keys, n_heads, dtype;
+    const int32_t* dev_start;
+    const int32_t* dev_cu;
+    const void* dev_q;
+    size_t ld_q;
+    float scale;
+    void* dev_out;
+    size_t ld_out;
+    float* dev_lse;
+    const float* dev_score_in;
+    float* dev_score_out;
+    size_t ld_score;
+    void* dev_ws;
+    size_t ws_bytes;
+    int32_t* dev_status;
+} qw_kv8_attn_args;
+size_t qw_kv8_attn_ws_bytes(const qw_kv8* kv, int B, int T, int max_len, int max_keys, int n_heads, int with_score);
+qw_status qw_kv8_attn(const qw_kv8* kv, const qw_kv8_attn_args* args, void* stream);
+
+/* Eviction by accumulated weight: an entry of dev_len[b] > n_keep tokens (dev_len <= max_len)
+ * keeps, for each KV head, its last n_recent positions and of the others the n_keep - n_recent
+ * with the largest dev_score ([B][n_kv_heads][ld_score], ld_score >= max_len; the lowest position
+ * first among equals; NaN counts as largest), 0 <= n_recent <= n_keep, n_keep >= 1. The kept
+ * tokens take positions 0 .. n_keep - 1 in their order, in the pages of dev_dst_table
+ * ([B][max_pages]; NULL: the entry's own pages, in place), whose exponents follow from the
+ * held values as for an append. dev_kept ([B][n_kv_heads][n_keep]) gets the position that each new
+ * position had (-1 past the new length), dev_new_len[b] min(dev_len[b], n_keep), and
+ * dev_score_out (may be dev_score) the kept scores, with zeros from the new length to
+ * dev_len[b]. Keys keep the rotation of the position they were appended at. Entries within the
+ * budget keep every token (copied when dev_dst_table is given). dev_dst_table must name other
+ * pages than the entries' own, or the same ones in the same order; dev_new_len must not be
+ * dev_len. */
+qw_status qw_kv8_evict(const qw_kv8* kv, int B, int max_len, const int32_t* dev_len, int n_keep, int n_recent,
+                       const int32_t* dev_dst_table, const float* dev_score, float* dev_score_out, size_t ld_score,
+                       int32_t* dev_kept, int32_t* dev_new_len, int32_t* dev_status, void* stream);
+
 /* ---- For callers that cannot allocate device memory ---------------------------------- */
 
 /* The page has no counterpart to this entry point; it serves callers that must not call
