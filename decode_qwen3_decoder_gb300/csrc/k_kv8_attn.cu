@@ -13,6 +13,8 @@
 
 #include <algorithm>
 
+#include "tc_sm103.cuh"
+
 namespace {
 
 constexpr float KV8_LOG2E = 1.4426950408889634f, KV8_LN2 = 0.6931471805599453f;
@@ -134,6 +136,74 @@ __device__ __forceinline__ void load_k(const uint8_t* codes, int g, int c, uint3
     }
 }
 
+// O^T += V^T P^T of one page. Lane (g, c) takes dims HD/8 g .. of tokens 4 c + k; byte permutes pair
+// two tokens of a dim. Tile 2 w + u of the accumulators: dims 4 w + 2 u, + 1 of the lane's HD / 8.
+template <int HD, int NT>
+__device__ __forceinline__ void mma_pv(const uint8_t* codes, int g, int c, const uint32_t (*pb)[2], float (*o)[HD / 16][4]) {
+    constexpr int DW = HD / 32;
+    uint32_t v[4][DW];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int t = 4 * c + k;
+        const uint8_t* row = codes + t * HD;
+        if constexpr (HD == 128) {
+            const uint4 u = *reinterpret_cast<const uint4*>(row + kv8_v_pos<HD>(t, g) * 16);
+            v[k][0] = u.x;
+            v[k][1] = u.y;
+            v[k][2] = u.z;
+            v[k][3] = u.w;
+        } else {
+            const uint2 u = *reinterpret_cast<const uint2*>(row + kv8_v_pos<HD>(t, g >> 1) * 16 + (g & 1) * 8);
+            v[k][0] = u.x;
+            v[k][1] = u.y;
+        }
+    }
+#pragma unroll
+    for (int w = 0; w < DW; ++w) {
+        const uint32_t a01 = __byte_perm(v[0][w], v[1][w], 0x5140), b01 = __byte_perm(v[0][w], v[1][w], 0x7362);
+        const uint32_t a23 = __byte_perm(v[2][w], v[3][w], 0x5140), b23 = __byte_perm(v[2][w], v[3][w], 0x7362);
+        const uint32_t f0[4] = {kv8_dec2(a01 & 0xFFFFu), kv8_dec2(a01 >> 16), kv8_dec2(a23 & 0xFFFFu), kv8_dec2(a23 >> 16)};
+        const uint32_t f1[4] = {kv8_dec2(b01 & 0xFFFFu), kv8_dec2(b01 >> 16), kv8_dec2(b23 & 0xFFFFu), kv8_dec2(b23 >> 16)};
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            mma16816(o[nt][2 * w], f0, pb[nt][0], pb[nt][1]);
+            mma16816(o[nt][2 * w + 1], f1, pb[nt][0], pb[nt][1]);
+        }
+    }
+}
+
+// One page's share of the online softmax for the lane's two columns of a tile: scores d (raw
+// q.k) become weights for the PV product. f: logit factor; v0, v1: the two keys are visible.
+template <int HD>
+__device__ __forceinline__ void softmax_page(const float* d, const float* f, const bool* v0, const bool* v1, int ev, float inv_sv,
+                                             float* R, float* l, float (*o)[4], uint32_t* pb) {
+    float w[4];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const float t0 = v0[e] ? fmaf(d[e], f[e], (float)ev) : -INFINITY;
+        const float t1 = v1[e] ? fmaf(d[2 + e], f[e], (float)ev) : -INFINITY;
+        float m = fmaxf(t0, t1);
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+        if (m > R[e] + KV8_SLACK) {
+            const float al = ex2(R[e] - m);
+            R[e] = m;
+            l[e] *= al;
+#pragma unroll
+            for (int i = 0; i < HD / 16; ++i) {
+                o[i][e] *= al;
+                o[i][2 + e] *= al;
+            }
+        }
+        w[e] = ex2(t0 - R[e] + KV8_LIFT);
+        w[2 + e] = ex2(t1 - R[e] + KV8_LIFT);
+        l[e] += (w[e] + w[2 + e]) * inv_sv;
+    }
+    pb[0] = movmatrix(pack_h2(w[0], w[1]));
+    pb[1] = movmatrix(pack_h2(w[2], w[3]));
+}
+
 // Pages of 16 rows (8 warps split the pages of one row tile).
 template <int HD, int DT>
 __global__ void __launch_bounds__(KR_WARPS * 32) k_kv8_attn_rows(const __grid_constant__ Kv8AttnP p) {
@@ -201,64 +271,12 @@ __global__ void __launch_bounds__(KR_WARPS * 32) k_kv8_attn_rows(const __grid_co
             float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int k = 0; k < KS; ++k) mma16816(d, a[k], qf[nt][k][0], qf[nt][k][1]);
-            float w[4];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float f = qmul[nt][e] * sk;
-                const int p0 = pi * KV8_PAGE + kv8_tok(g, 0);
-                float t0 = p0 <= limit[nt][e] ? fmaf(d[e], f, (float)ev) : -INFINITY;
-                float t1 = p0 + 2 <= limit[nt][e] ? fmaf(d[2 + e], f, (float)ev) : -INFINITY;
-                float m = fmaxf(t0, t1);
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-                if (m > R[nt][e] + KV8_SLACK) {
-                    const float al = ex2(R[nt][e] - m);
-                    R[nt][e] = m;
-                    l[nt][e] *= al;
-#pragma unroll
-                    for (int i = 0; i < 2 * DW; ++i) {
-                        o[nt][i][e] *= al;
-                        o[nt][i][2 + e] *= al;
-                    }
-                }
-                w[e] = ex2(t0 - R[nt][e] + KV8_LIFT);
-                w[2 + e] = ex2(t1 - R[nt][e] + KV8_LIFT);
-                l[nt][e] += (w[e] + w[2 + e]) * inv_sv;
-            }
-            pb[nt][0] = movmatrix(pack_h2(w[0], w[1]));
-            pb[nt][1] = movmatrix(pack_h2(w[2], w[3]));
+            const int p0 = pi * KV8_PAGE + kv8_tok(g, 0);
+            const float f[2] = {qmul[nt][0] * sk, qmul[nt][1] * sk};
+            const bool v0[2] = {p0 <= limit[nt][0], p0 <= limit[nt][1]}, v1[2] = {p0 + 2 <= limit[nt][0], p0 + 2 <= limit[nt][1]};
+            softmax_page<HD>(d, f, v0, v1, ev, inv_sv, R[nt], l[nt], o[nt], pb[nt]);
         }
-        // V: lane (g, c) takes dims HD/8 g .. of tokens 4 c + k; byte permutes pair two tokens of a dim
-        uint32_t v[4][DW];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int t = 4 * c + k;
-            const uint8_t* row = blk + Kv8<HD>::VOFF + t * HD;
-            if (HD == 128) {
-                const uint4 u = *reinterpret_cast<const uint4*>(row + kv8_v_pos<HD>(t, g) * 16);
-                v[k][0] = u.x;
-                v[k][1] = u.y;
-                v[k][DW - 2] = u.z;
-                v[k][DW - 1] = u.w;
-            } else {
-                const uint2 u = *reinterpret_cast<const uint2*>(row + kv8_v_pos<HD>(t, g >> 1) * 16 + (g & 1) * 8);
-                v[k][0] = u.x;
-                v[k][1] = u.y;
-            }
-        }
-#pragma unroll
-        for (int w = 0; w < DW; ++w) {
-            const uint32_t a01 = __byte_perm(v[0][w], v[1][w], 0x5140), b01 = __byte_perm(v[0][w], v[1][w], 0x7362);
-            const uint32_t a23 = __byte_perm(v[2][w], v[3][w], 0x5140), b23 = __byte_perm(v[2][w], v[3][w], 0x7362);
-            const uint32_t f0[4] = {kv8_dec2(a01 & 0xFFFFu), kv8_dec2(a01 >> 16), kv8_dec2(a23 & 0xFFFFu), kv8_dec2(a23 >> 16)};
-            const uint32_t f1[4] = {kv8_dec2(b01 & 0xFFFFu), kv8_dec2(b01 >> 16), kv8_dec2(b23 & 0xFFFFu), kv8_dec2(b23 >> 16)};
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                mma16816(o[nt][2 * w], f0, pb[nt][0], pb[nt][1]);
-                mma16816(o[nt][2 * w + 1], f1, pb[nt][0], pb[nt][1]);
-            }
-        }
+        mma_pv<HD, NT>(blk + Kv8<HD>::VOFF, g, c, pb, o);
     }
     // ---- merge the warps ----
 #pragma unroll
@@ -366,18 +384,591 @@ __global__ void __launch_bounds__(128) k_kv8_score(const __grid_constant__ Kv8At
     }
 }
 
+// =======================================================================================
+// k_kv8_decode: few query rows per KV head (a decode step, up to 16 rows of tokens x heads).
+//
+// Reading the cache bounds it: 32 HD + 32 bytes per page and head against ~150 instructions of a
+// warp. The items (entry, KV head, page), entry-major, are cut into equal runs, one per CTA and
+// again one per warp, so ragged lengths cost no imbalance and a warp needs no other warp: it
+// streams its pages through its own ring with one bulk copy per block (codes and scales are
+// contiguous), multiplies with the keys as the M of the MMA (16 keys of a page, 8 query rows as N)
+// and keeps the online softmax in registers. A run that covers a whole (entry, head) pair writes
+// the output; the pieces of a pair inside a CTA are merged in shared memory, and pairs that cross
+// CTAs go through two partial slots per CTA, merged by k_kv8_combine (launched early, in the
+// order of the slots, so sums have one order). With `pair_mode` (short caches) a CTA takes one
+// pair and nothing is left to combine.
+// With scores, the logits also go to `tbuf`, from which the combine kernel forms the weights
+// once the normalisers are known: 8 bytes a row and key instead of K again.
+// =======================================================================================
+constexpr int KD_WARPS = 8;
+
+struct Kv8DecP {
+    Kv8AttnP a;
+    int B, nrow;      // rows (max_len * G) a pair has at most
+    int stages;
+    int pair_mode;
+    float* part_o;    // [CTAs][2][nrow][HD]
+    float* part_ml;   // [CTAs][2][nrow][2]
+    float* tbuf;      // optional [B * n_kv][nrow][ld_t] logits in log2 units
+    size_t ld_t;
+    int n_cta;        // CTAs of the decode kernel
+};
+
+__device__ __forceinline__ int kd_pages(const Kv8AttnP& p, int b) {
+    int s, r0, n;
+    const bool ok = attn_entry(p, b, s, r0, n);
+    return ok && n > 0 ? (s + n + KV8_PAGE - 1) / KV8_PAGE : 0;
+}
+
+// cum[b] = pages of the entries before b (b <= B), by all 256 threads of the CTA.
+__device__ __forceinline__ void kd_prefix(const Kv8AttnP& p, int B, int* cum, int* ws) {
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+    int base = 0;
+    for (int b0 = 0; b0 < B; b0 += KD_WARPS * 32) {
+        const int v = b0 + tid < B ? kd_pages(p, b0 + tid) : 0;
+        int x = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int t = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += t;
+        }
+        if (lane == 31) ws[w] = x;
+        __syncthreads();
+        int before = base, all = base;
+#pragma unroll
+        for (int i = 0; i < KD_WARPS; ++i) {
+            if (i < w) before += ws[i];
+            all += ws[i];
+        }
+        if (b0 + tid < B) cum[b0 + tid] = before + x - v;
+        base = all;
+        __syncthreads();
+    }
+    if (tid == 0) cum[B] = base;
+    __syncthreads();
+}
+
+// The entry whose pages hold page number `pg` of all entries' pages laid end to end.
+__device__ __forceinline__ int kd_find(const int* cum, int B, int pg) {
+    int lo = 0, hi = B;  // cum[lo] <= pg < cum[hi]
+    while (hi - lo > 1) {
+        const int m = (lo + hi) >> 1;
+        if (cum[m] <= pg) lo = m;
+        else hi = m;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+// 2 N consecutive output elements of one row from fp32 (N words, 16-byte aligned).
+template <int DT, int N>
+__device__ __forceinline__ void store_row(void* base, size_t off, const float* x) {
+    uint32_t w[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = DT == QW_F16 ? pack_h2(x[2 * i], x[2 * i + 1]) : pack_bf2(x[2 * i], x[2 * i + 1]);
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+        *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(base) + off + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+}
+
+template <int HD, int DT, int NT>
+__global__ void __launch_bounds__(KD_WARPS * 32, NT == 1 ? 2 : 1) k_kv8_decode(const __grid_constant__ Kv8DecP P) {
+    constexpr int KS = HD / 16, BLK = Kv8<HD>::BLK, LD = HD / 8;  // LD: output dims of a lane
+    const Kv8AttnP& p = P.a;
+    extern __shared__ __align__(128) uint8_t kd_smem[];  // [warps][stages][BLK], then the slots
+    __shared__ uint64_t bars[KD_WARPS][8];
+    __shared__ int cum[QW_KV8_MAX_BATCH + 1];
+    __shared__ int ws[KD_WARPS], slot_pair[2 * KD_WARPS], s_abort;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+    const int H = p.kv.n_kv, S = P.stages;
+    float* slot_o = reinterpret_cast<float*>(kd_smem + (size_t)KD_WARPS * S * BLK);  // [warps][2][nrow][HD]
+    float* slot_ml = slot_o + (size_t)2 * KD_WARPS * P.nrow * HD;                    // [warps][2][nrow][2]
+    if (!P.pair_mode) pdl_launch();
+    if (lane == 0)
+        for (int i = 0; i < S; ++i) mbar_init(smem_u32(&bars[warp][i]), 1);
+    if (tid == 0) {
+        s_abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (tid < 2 * KD_WARPS) slot_pair[tid] = -1;
+    // ---- this CTA's and this warp's run of items ----
+    int c0, c1;
+    if (P.pair_mode) {
+        c0 = 0;
+        c1 = kd_pages(p, blockIdx.x / H);
+    } else {
+        kd_prefix(p, P.B, cum, ws);
+        const long long items = (long long)cum[P.B] * H;
+        c0 = (int)(items * blockIdx.x / gridDim.x);
+        c1 = (int)(items * (blockIdx.x + 1) / gridDim.x);
+    }
+    if (blockIdx.x == 0 && !P.pair_mode)  // entries left out: reported, their rows zeroed
+        for (int b = warp; b < P.B; b += KD_WARPS) {
+            int s, r0, n;
+            if (attn_entry(p, b, s, r0, n)) continue;
+            if (lane == 0) atomicOr(p.status, QW_KV8_BAD_POS);
+            if (r0 < 0 || n < 0 || n > p.max_len || r0 > p.T - n) continue;
+            for (int i = 0; i < n; ++i)
+                for (int d = lane * 8; d < p.n_heads * HD; d += 256)
+                    *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + (size_t)(r0 + i) * p.ld_out + d) = make_uint4(0u, 0u, 0u, 0u);
+        }
+    if (P.pair_mode && c1 == 0) {
+        const int b = blockIdx.x / H, head = blockIdx.x % H;
+        int s, r0, n;
+        if (!attn_entry(p, b, s, r0, n)) {
+            if (tid == 0) atomicOr(p.status, QW_KV8_BAD_POS);
+            if (r0 < 0 || n < 0 || n > p.max_len || r0 > p.T - n) return;
+            for (int x = tid; x < n * p.G * HD; x += KD_WARPS * 32) {
+                const int r = x / HD;
+                reinterpret_cast<uint16_t*>(p.out)[(size_t)(r0 + r / p.G) * p.ld_out + (size_t)(head * p.G + r % p.G) * HD + x % HD] = 0;
+            }
+        }
+        return;
+    }
+    __syncthreads();
+    const int i0 = c0 + (int)((long long)(c1 - c0) * warp / KD_WARPS), i1 = c0 + (int)((long long)(c1 - c0) * (warp + 1) / KD_WARPS);
+    auto locate = [&](int j, int& b, int& head, int& page, int& pages) {
+        if (P.pair_mode) {
+            b = blockIdx.x / H;
+            head = blockIdx.x % H;
+            page = j;
+            pages = c1;
+        } else {
+            b = kd_find(cum, P.B, j / H);
+            pages = cum[b + 1] - cum[b];
+            const int off = j - cum[b] * H;
+            head = off / pages;
+            page = off - head * pages;
+        }
+    };
+    const uint32_t ring = smem_u32(kd_smem) + warp * S * BLK;
+    // lane l holds the block address of the l-th item of the batch of 32 being issued, and of the next
+    auto address = [&](int j) -> const uint8_t* {
+        if (j >= i1) return nullptr;
+        int b, head, page, pages;
+        locate(j, b, head, page, pages);
+        int id = p.kv.table[(size_t)b * p.kv.max_pages + page];
+        if (id < 0 || id >= p.kv.n_pages) {
+            atomicOr(p.status, QW_KV8_BAD_POS);
+            id = 0;
+        }
+        return p.kv.blocks + ((size_t)id * H + head) * BLK;
+    };
+    const uint8_t* cur = address(i0 + lane);
+    const uint8_t* nxt = address(i0 + 32 + lane);
+    int issued = 0;
+    auto issue = [&](int st) {
+        if (i0 + issued >= i1) return;
+        if (issued && (issued & 31) == 0) {
+            cur = nxt;
+            nxt = address(i0 + issued + 32 + lane);
+        }
+        if (lane == (issued & 31)) {
+            const uint32_t bar = smem_u32(&bars[warp][st]);
+            mbar_expect_tx(bar, BLK);
+            bulk_copy(ring + st * BLK, cur, BLK, bar);
+        }
+        ++issued;
+    };
+    for (int i = 0; i < S; ++i) issue(i);
+
+    uint32_t qf[NT][KS][2];
+    float qmul[NT][2], R[NT][2], l[NT][2], o[NT][KS][4];
+    int limit[NT][2];
+    int b = 0, head = 0, page = 0, pages = 0, page_lo = 0, n_slots = 0, s = 0, r0 = 0, rows = 0;
+    auto flush = [&]() {  // the segment [page_lo, page) of the pair (b, head)
+        const bool whole = page_lo == 0 && page == pages;
+        const int slot = warp * 2 + n_slots;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float x = l[nt][e];
+                x += __shfl_xor_sync(0xffffffffu, x, 4);
+                x += __shfl_xor_sync(0xffffffffu, x, 8);
+                x += __shfl_xor_sync(0xffffffffu, x, 16);
+                const int r = 8 * nt + 2 * c + e;
+                if (r >= rows) continue;
+                float v[LD];
+#pragma unroll
+                for (int i = 0; i < KS; ++i) {
+                    v[2 * i] = o[nt][i][e];
+                    v[2 * i + 1] = o[nt][i][2 + e];
+                }
+                if (whole) {
+                    const float inv = 1.f / x;
+#pragma unroll
+                    for (int i = 0; i < LD; ++i) v[i] *= inv;
+                    const int tok = r0 + r / p.G, h = head * p.G + r % p.G;
+                    store_row<DT, LD / 2>(p.out, (size_t)tok * p.ld_out + (size_t)h * HD + g * LD, v);
+                    if (g == 0) {
+                        const float z = log2f(x) + R[nt][e] - KV8_LIFT;
+                        if (p.lse2) p.lse2[(size_t)tok * p.n_heads + h] = z;
+                        if (p.lse) p.lse[(size_t)tok * p.n_heads + h] = z * KV8_LN2;
+                    }
+                } else {
+                    float* dst = slot_o + ((size_t)slot * P.nrow + r) * HD + g * LD;
+#pragma unroll
+                    for (int i = 0; i < LD; i += 4) *reinterpret_cast<float4*>(dst + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                    if (g == 0) {
+                        slot_ml[((size_t)slot * P.nrow + r) * 2] = R[nt][e];
+                        slot_ml[((size_t)slot * P.nrow + r) * 2 + 1] = x;
+                    }
+                }
+            }
+        if (!whole) {
+            if (lane == 0) slot_pair[slot] = b * H + head;
+            ++n_slots;
+        }
+    };
+    int st = 0, ph = 0;
+    for (int j = i0; j < i1; ++j) {
+        if (j == i0 || page == pages) {
+            if (j > i0) flush();
+            locate(j, b, head, page, pages);
+            page_lo = page;
+            int n;
+            attn_entry(p, b, s, r0, n);
+            rows = n * p.G;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const int r = 8 * nt + g;
+                const bool v = r < rows;
+                const int i = v ? r / p.G : 0, h = head * p.G + (v ? r % p.G : 0);
+                float mul;
+                load_q<HD, DT>(p, v, (size_t)(r0 + i) * p.ld_q + (size_t)h * HD, c, qf[nt], mul);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    qmul[nt][e] = __shfl_sync(0xffffffffu, mul, (2 * c + e) * 4) * p.scale_log2;
+                    const int rr = 8 * nt + 2 * c + e;
+                    limit[nt][e] = rr < rows ? s + rr / p.G : -1;
+                    R[nt][e] = -1e30f;
+                    l[nt][e] = 0.f;
+                }
+#pragma unroll
+                for (int i2 = 0; i2 < KS; ++i2) o[nt][i2][0] = o[nt][i2][1] = o[nt][i2][2] = o[nt][i2][3] = 0.f;
+            }
+        }
+        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars[warp][st]), ph, &s_abort))) {
+            // give up: the outputs are not valid. The copies in flight land before the CTA ends.
+            if (lane == 0) {
+                atomicOr(p.status, QW_KV8_TIMEOUT);
+                s_abort = 1;
+            }
+            const uint64_t t0 = globaltimer_ns();
+            for (int k = j; k < i0 + issued; ++k) {
+                while (!mbar_try_wait(smem_u32(&bars[warp][st]), ph) && globaltimer_ns() - t0 < kTcWaitNs) {
+                }
+                if (++st == S) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            }
+            break;
+        }
+        const uint8_t* blk = kd_smem + ((size_t)warp * S + st) * BLK;
+        const float2 sc = *reinterpret_cast<const float2*>(blk + Kv8<HD>::SOFF);
+        const int ev = kv8_log2(sc.y);
+        const float inv_sv = kv8_pow2(-ev);
+        uint32_t a[KS][4], pb[NT][2];
+        load_k<HD>(blk, g, c, a);
+        const int p0 = page * KV8_PAGE + kv8_tok(g, 0);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < KS; ++k) mma16816(d, a[k], qf[nt][k][0], qf[nt][k][1]);
+            const float f[2] = {qmul[nt][0] * sc.x, qmul[nt][1] * sc.x};
+            const bool v0[2] = {p0 <= limit[nt][0], p0 <= limit[nt][1]}, v1[2] = {p0 + 2 <= limit[nt][0], p0 + 2 <= limit[nt][1]};
+            if (P.tbuf) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float* tr = P.tbuf + ((size_t)(b * H + head) * P.nrow + 8 * nt + 2 * c + e) * P.ld_t + p0;
+                    if (v0[e]) tr[0] = d[e] * f[e];
+                    if (v1[e]) tr[2] = d[2 + e] * f[e];
+                }
+            }
+            softmax_page<HD>(d, f, v0, v1, ev, inv_sv, R[nt], l[nt], o[nt], pb[nt]);
+        }
+        mma_pv<HD, NT>(blk + Kv8<HD>::VOFF, g, c, pb, o);
+        __syncwarp();
+        issue(st);
+        ++page;
+        if (++st == S) {
+            st = 0;
+            ph ^= 1;
+        }
+    }
+    if (i1 > i0 && !s_abort) flush();
+    __syncthreads();
+    if (s_abort) return;
+    // ---- merge the pieces of a pair that several warps hold ----
+    for (int a0 = 0; a0 < 2 * KD_WARPS;) {
+        const int pair = slot_pair[a0];
+        if (pair < 0) {
+            ++a0;
+            continue;
+        }
+        int a1 = a0 + 1;
+        while (a1 < 2 * KD_WARPS && (slot_pair[a1] == pair || slot_pair[a1] < 0)) ++a1;
+        const int pb_ = pair / H, ph_ = pair % H;
+        int es, er0, en;
+        attn_entry(p, pb_, es, er0, en);
+        const int erows = en * p.G;
+        int first = 0, last = c1;  // the pair's items
+        if (!P.pair_mode) {
+            const int np = cum[pb_ + 1] - cum[pb_];
+            first = cum[pb_] * H + ph_ * np;
+            last = first + np;
+        }
+        const bool all = first >= c0 && last <= c1;
+        const int gslot = first >= c0 ? (first == c0 ? 0 : 1) : 0;
+        for (int x = tid; x < erows * (HD / 4); x += KD_WARPS * 32) {
+            const int r = x / (HD / 4), d = (x % (HD / 4)) * 4;
+            float M = -1e30f;
+            for (int k = a0; k < a1; ++k)
+                if (slot_pair[k] == pair) M = fmaxf(M, slot_ml[((size_t)k * P.nrow + r) * 2]);
+            float L = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = a0; k < a1; ++k) {
+                if (slot_pair[k] != pair) continue;
+                const float f = ex2(slot_ml[((size_t)k * P.nrow + r) * 2] - M);
+                L += slot_ml[((size_t)k * P.nrow + r) * 2 + 1] * f;
+                const float4 v = *reinterpret_cast<const float4*>(slot_o + ((size_t)k * P.nrow + r) * HD + d);
+                acc.x += v.x * f;
+                acc.y += v.y * f;
+                acc.z += v.z * f;
+                acc.w += v.w * f;
+            }
+            if (all) {
+                const float inv = 1.f / L;
+                const int tok = er0 + r / p.G, h = ph_ * p.G + r % p.G;
+                const float v[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+                uint2 w;
+                w.x = DT == QW_F16 ? pack_h2(v[0], v[1]) : pack_bf2(v[0], v[1]);
+                w.y = DT == QW_F16 ? pack_h2(v[2], v[3]) : pack_bf2(v[2], v[3]);
+                *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) + (size_t)tok * p.ld_out + (size_t)h * HD + d) = w;
+                if (d == 0) {
+                    const float z = log2f(L) + M - KV8_LIFT;
+                    if (p.lse2) p.lse2[(size_t)tok * p.n_heads + h] = z;
+                    if (p.lse) p.lse[(size_t)tok * p.n_heads + h] = z * KV8_LN2;
+                }
+            } else {
+                const size_t at = ((size_t)blockIdx.x * 2 + gslot) * P.nrow + r;
+                *reinterpret_cast<float4*>(P.part_o + at * HD + d) = acc;
+                if (d == 0) {
+                    P.part_ml[at * 2] = M;
+                    P.part_ml[at * 2 + 1] = L;
+                }
+            }
+        }
+        a0 = a1;
+    }
+}
+
+// Pairs that cross CTAs of k_kv8_decode: out = sum of the slots' partials. With scores also the
+// weights of a chunk of KC_KEYS keys (blockIdx.y) from the stored logits.
+constexpr int KC_KEYS = 1024;
 template <int HD, int DT>
-cudaError_t run_attn(const Kv8AttnP& p, int B, cudaStream_t st) {
-    const int smem = KR_WARPS * KR_ROWS * HD * 4;
-    cudaError_t e = cudaFuncSetAttribute(k_kv8_attn_rows<HD, DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
+__global__ void __launch_bounds__(KD_WARPS * 32) k_kv8_combine(const __grid_constant__ Kv8DecP P) {
+    const Kv8AttnP& p = P.a;
+    __shared__ int cum[QW_KV8_MAX_BATCH + 1];
+    __shared__ int ws[KD_WARPS];
+    __shared__ float s_m[16], s_l[16];
+    __shared__ float4 s_acc[KD_WARPS][HD / 4];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, H = p.kv.n_kv;
+    const int b = blockIdx.x / H, head = blockIdx.x % H, key0 = blockIdx.y * KC_KEYS;
+    int s, r0, n;
+    if (!attn_entry(p, b, s, r0, n) || n == 0 || key0 >= s + n) return;
+    const int rows = n * p.G;
+    bool split = false;
+    int w0 = 0, w1 = 0, first = 0;
+    long long items = 0;
+    if (!P.pair_mode) {
+        kd_prefix(p, P.B, cum, ws);
+        items = (long long)cum[P.B] * H;
+        const int np = cum[b + 1] - cum[b];
+        first = cum[b] * H + head * np;
+        w0 = (int)((((long long)first + 1) * P.n_cta - 1) / items);
+        w1 = (int)((((long long)first + np) * P.n_cta - 1) / items);
+        split = w1 > w0;
+    }
+    if (!split && !p.score_out) return;
+    pdl_wait();
+    auto slot = [&](int w) {
+        const int i0 = (int)(items * w / P.n_cta);
+        return (size_t)w * 2 + (i0 >= first ? 0 : 1);
+    };
+    for (int r = warp; r < rows; r += KD_WARPS) {  // each row's maximum and sum over the slots
+        float M = -1e30f, L = 0.f;
+        if (split) {
+            for (int w = w0 + lane; w <= w1; w += 32) M = fmaxf(M, P.part_ml[(slot(w) * P.nrow + r) * 2]);
+            M = warp_max(M);
+            for (int w = w0 + lane; w <= w1; w += 32) {
+                const float* ml = P.part_ml + (slot(w) * P.nrow + r) * 2;
+                L += ml[1] * ex2(ml[0] - M);
+            }
+            L = warp_sum(L);
+        }
+        if (lane == 0) {
+            s_m[r] = M;
+            // with scores only the log of the sum is needed of a pair that is done
+            s_l[r] = split ? L : p.lse2[(size_t)(r0 + r / p.G) * p.n_heads + head * p.G + r % p.G];
+        }
+    }
+    __syncthreads();
+    if (split && blockIdx.y == 0) {
+        for (int r = 0; r < rows; ++r) {
+            const float M = s_m[r];
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (lane < HD / 4) {
+#pragma unroll 4
+                for (int w = w0 + warp; w <= w1; w += KD_WARPS) {
+                    const size_t at = slot(w) * P.nrow + r;
+                    const float f = ex2(P.part_ml[at * 2] - M);
+                    const float4 v = *reinterpret_cast<const float4*>(P.part_o + at * HD + lane * 4);
+                    acc.x += v.x * f;
+                    acc.y += v.y * f;
+                    acc.z += v.z * f;
+                    acc.w += v.w * f;
+                }
+                s_acc[warp][lane] = acc;
+            }
+            __syncthreads();
+            if (tid < HD / 4) {
+                float4 t = s_acc[0][tid];
+#pragma unroll
+                for (int k = 1; k < KD_WARPS; ++k) {
+                    const float4 v = s_acc[k][tid];
+                    t.x += v.x;
+                    t.y += v.y;
+                    t.z += v.z;
+                    t.w += v.w;
+                }
+                const float inv = 1.f / s_l[r];
+                const int tok = r0 + r / p.G, h = head * p.G + r % p.G;
+                uint2 w;
+                w.x = DT == QW_F16 ? pack_h2(t.x * inv, t.y * inv) : pack_bf2(t.x * inv, t.y * inv);
+                w.y = DT == QW_F16 ? pack_h2(t.z * inv, t.w * inv) : pack_bf2(t.z * inv, t.w * inv);
+                *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) + (size_t)tok * p.ld_out + (size_t)h * HD + tid * 4) = w;
+                if (tid == 0 && p.lse) p.lse[(size_t)tok * p.n_heads + h] = (log2f(s_l[r]) + M - KV8_LIFT) * KV8_LN2;
+            }
+            __syncthreads();
+        }
+    }
+    if (!p.score_out) return;
+    const size_t base = ((size_t)b * H + head) * p.ld_score;
+    const int end = min(s + n, key0 + KC_KEYS);
+    for (int j = key0 + tid; j < end; j += KD_WARPS * 32) {
+        float acc = 0.f;
+        for (int r = 0; r < rows; ++r) {
+            const float z = split ? log2f(s_l[r]) + s_m[r] - KV8_LIFT : s_l[r];
+            if (j <= s + r / p.G) acc += ex2(P.tbuf[((size_t)(b * H + head) * P.nrow + r) * P.ld_t + j] - z);
+        }
+        p.score_out[base + j] = (p.score_in ? p.score_in[base + j] : 0.f) + acc;
+    }
+}
+
+// ---- which kernels a call runs, and its workspace ---------------------------------------
+
+struct Plan {
+    bool decode;       // k_kv8_decode (max_len * G <= 16 rows)
+    bool pair_mode;
+    bool tbuf;         // scores from stored logits
+    int nrow, stages, n_cta, smem;
+    size_t off_o, off_ml, off_t, bytes;
+};
+
+int sm_count() {
+    static const int n = [] {
+        int dev = 0, v = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) v = 0;
+        return v > 0 ? v : 152;
+    }();
+    return n;
+}
+
+Plan make_plan(const qw_kv8* kv, int B, int T, int max_len, int max_keys, int n_heads, bool score) {
+    Plan q = {};
+    const int G = n_heads / kv->n_kv_heads, HD = kv->head_dim, BLK = 32 * HD + 32;
+    auto put = [&](size_t n) {
+        const size_t at = q.bytes;
+        q.bytes = (at + n + 255) & ~(size_t)255;
+        return at;
+    };
+    put(score ? (size_t)T * n_heads * 4 : 0);  // lse2
+    const long long rows = (long long)std::min(max_len, std::max(T, 1)) * G;
+    q.decode = rows <= 16;
+    if (q.decode) {
+        q.nrow = (int)rows;
+        const int slots = 2 * KD_WARPS * q.nrow * (HD + 2) * 4;
+        // two CTAs an SM where their rings and slots fit (rows <= 4 at head_dim 128), else one
+        const int per_sm = KD_WARPS * 2 * BLK + slots <= 106 * 1024 && rows <= 8 ? 2 : 1;
+        q.stages = std::min(8, ((per_sm == 2 ? 106 : 200) * 1024 - slots) / (KD_WARPS * BLK));
+        q.smem = KD_WARPS * q.stages * BLK + slots;
+        q.pair_mode = max_keys <= 512;
+        q.n_cta = q.pair_mode ? B * kv->n_kv_heads : per_sm * sm_count();
+        // a row's logits are written and read once (8 bytes a key) instead of its K (HD bytes)
+        q.tbuf = score && rows <= 8;
+        q.off_o = put(q.pair_mode ? 0 : (size_t)q.n_cta * 2 * q.nrow * HD * 4);
+        q.off_ml = put(q.pair_mode ? 0 : (size_t)q.n_cta * 2 * q.nrow * 2 * 4);
+        q.off_t = put(q.tbuf ? (size_t)B * kv->n_kv_heads * q.nrow * (((size_t)max_keys + 3) & ~(size_t)3) * 4 : 0);
+    }
+    q.bytes = std::max(q.bytes, (size_t)256);
+    return q;
+}
+
+template <typename K>
+cudaError_t allow_smem(K kern, int bytes) {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+template <int HD, int DT>
+cudaError_t run_score(const Kv8AttnP& p, int B, cudaStream_t st) {
     LaunchCtx c = {st, false, nullptr};
+    const unsigned pages = (unsigned)((p.max_keys + KV8_PAGE - 1) / KV8_PAGE);
+    return launch_k(c, k_kv8_score<HD, DT>, dim3((pages + 3) / 4, p.kv.n_kv, B), dim3(128), 0, p);
+}
+
+template <int HD, int DT>
+cudaError_t run_attn(const Kv8AttnP& p, const Plan& q, int B, char* ws, cudaStream_t st) {
+    LaunchCtx c = {st, false, nullptr};
+    cudaError_t e;
+    if (q.decode) {
+        Kv8DecP P = {};
+        P.a = p;
+        P.B = B;
+        P.nrow = q.nrow;
+        P.stages = q.stages;
+        P.pair_mode = q.pair_mode;
+        P.part_o = (float*)(ws + q.off_o);
+        P.part_ml = (float*)(ws + q.off_ml);
+        P.tbuf = q.tbuf ? (float*)(ws + q.off_t) : nullptr;
+        P.ld_t = ((size_t)p.max_keys + 3) & ~(size_t)3;
+        P.n_cta = q.n_cta;
+        auto kern = q.nrow <= 8 ? k_kv8_decode<HD, DT, 1> : k_kv8_decode<HD, DT, 2>;
+        if ((e = allow_smem(kern, q.smem)) != cudaSuccess) return e;
+        if ((e = launch_k(c, kern, dim3(q.n_cta), dim3(KD_WARPS * 32), (size_t)q.smem, P)) != cudaSuccess) return e;
+        if (!q.tbuf) P.a.score_out = nullptr;
+        if (!q.pair_mode || q.tbuf) {
+            const unsigned chunks = q.tbuf ? (unsigned)((p.max_keys + KC_KEYS - 1) / KC_KEYS) : 1;
+            if (!q.pair_mode) c.pdl = true;
+            e = launch_k(c, k_kv8_combine<HD, DT>, dim3(B * p.kv.n_kv, chunks), dim3(KD_WARPS * 32), 0, P);
+            if (e != cudaSuccess) return e;
+        }
+        return p.score_out && !q.tbuf ? run_score<HD, DT>(p, B, st) : cudaSuccess;
+    }
+    const int smem = KR_WARPS * KR_ROWS * HD * 4;
+    if ((e = allow_smem(k_kv8_attn_rows<HD, DT>, smem)) != cudaSuccess) return e;
     const int len = std::min(p.max_len, p.T);
     const unsigned tiles = (unsigned)(((long long)len * p.G + KR_ROWS - 1) / KR_ROWS);
     e = launch_k(c, k_kv8_attn_rows<HD, DT>, dim3(tiles, p.kv.n_kv, B), dim3(KR_WARPS * 32), (size_t)smem, p);
-    if (e != cudaSuccess || !p.score_out) return e;
-    const unsigned pages = (unsigned)((p.max_keys + KV8_PAGE - 1) / KV8_PAGE);
-    return launch_k(c, k_kv8_score<HD, DT>, dim3((pages + 3) / 4, p.kv.n_kv, B), dim3(128), 0, p);
+    return e == cudaSuccess && p.score_out ? run_score<HD, DT>(p, B, st) : e;
 }
 
 }  // namespace
@@ -389,6 +980,8 @@ static qw_status attn_sizes(const qw_kv8* kv, int B, int T, int max_len, int max
         return qw_fail(QW_ERR_INVALID_ARG, "attn: max_keys outside [1, 16 max_pages]");
     if (n_heads < kv->n_kv_heads || n_heads % kv->n_kv_heads)
         return qw_fail(QW_ERR_INVALID_ARG, "attn: n_heads is not a multiple of n_kv_heads");
+    if ((long long)B * ((max_keys + 15) / 16) * kv->n_kv_heads > 0x7fffffffll)
+        return qw_fail(QW_ERR_UNSUPPORTED, "attn: B * max_keys * n_kv_heads too large");
     if (n_heads / kv->n_kv_heads > 16) return qw_fail(QW_ERR_UNSUPPORTED, "attn: more than 16 query heads per KV head");
     return QW_OK;
 }
@@ -396,7 +989,7 @@ static qw_status attn_sizes(const qw_kv8* kv, int B, int T, int max_len, int max
 extern "C" size_t qw_kv8_attn_ws_bytes(const qw_kv8* kv, int B, int T, int max_len, int max_keys, int n_heads,
                                        int with_score) {
     if (attn_sizes(kv, B, T, max_len, max_keys, n_heads)) return 0;
-    return with_score ? (((size_t)T * n_heads * 4 + 255) & ~(size_t)255) : 256;
+    return make_plan(kv, B, T, max_len, max_keys, n_heads, with_score != 0).bytes;
 }
 
 extern "C" qw_status qw_kv8_attn(const qw_kv8* kv, const qw_kv8_attn_args* a, void* stream) {
@@ -413,8 +1006,8 @@ extern "C" qw_status qw_kv8_attn(const qw_kv8* kv, const qw_kv8_attn_args* a, vo
     if (!(a->scale > 0.f) || !(a->scale < 1e30f)) return qw_fail(QW_ERR_INVALID_ARG, "attn: scale not positive and finite");
     if (a->dev_score_in && !a->dev_score_out) return qw_fail(QW_ERR_INVALID_ARG, "attn: score_in without score_out");
     if (a->dev_score_out && a->ld_score < (size_t)a->max_keys) return qw_fail(QW_ERR_INVALID_ARG, "attn: ld_score < max_keys");
-    if ((uintptr_t)a->dev_ws & 255 ||
-        a->ws_bytes < qw_kv8_attn_ws_bytes(kv, a->B, a->T, a->max_len, a->max_keys, a->n_heads, a->dev_score_out != nullptr))
+    const Plan q = make_plan(kv, a->B, a->T, a->max_len, a->max_keys, a->n_heads, a->dev_score_out != nullptr);
+    if ((uintptr_t)a->dev_ws & 255 || a->ws_bytes < q.bytes)
         return qw_fail(QW_ERR_INVALID_ARG, "attn: workspace too small or not 256-byte aligned");
     if (a->T == 0) return QW_OK;
     Kv8AttnP p = {};
@@ -438,7 +1031,10 @@ extern "C" qw_status qw_kv8_attn(const qw_kv8* kv, const qw_kv8_attn_args* a, vo
     p.ld_score = a->ld_score;
     p.status = a->dev_status;
     cudaStream_t st = (cudaStream_t)stream;
-    const cudaError_t e = kv->head_dim == 128 ? (a->dtype == QW_F16 ? run_attn<128, QW_F16>(p, a->B, st) : run_attn<128, QW_BF16>(p, a->B, st))
-                                              : (a->dtype == QW_F16 ? run_attn<64, QW_F16>(p, a->B, st) : run_attn<64, QW_BF16>(p, a->B, st));
+    char* ws = (char*)a->dev_ws;
+    const bool h = a->dtype == QW_F16;
+    const cudaError_t e = kv->head_dim == 128
+                              ? (h ? run_attn<128, QW_F16>(p, q, a->B, ws, st) : run_attn<128, QW_BF16>(p, q, a->B, ws, st))
+                              : (h ? run_attn<64, QW_F16>(p, q, a->B, ws, st) : run_attn<64, QW_BF16>(p, q, a->B, ws, st));
     return e == cudaSuccess ? QW_OK : qw_fail(QW_ERR_CUDA, "attn: %s", cudaGetErrorString(e));
 }
