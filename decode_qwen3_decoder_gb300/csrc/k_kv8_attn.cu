@@ -19,7 +19,6 @@ namespace {
 
 constexpr float KV8_LOG2E = 1.4426950408889634f, KV8_LN2 = 0.6931471805599453f;
 constexpr float KV8_LIFT = 8.f, KV8_SLACK = 7.f;  // weights aim at 2^8 and may grow to 2^15
-constexpr int KR_WARPS = 8, KR_ROWS = 16;
 
 struct Kv8AttnP {
     Kv8View kv;
@@ -202,130 +201,6 @@ __device__ __forceinline__ void softmax_page(const float* d, const float* f, con
     }
     pb[0] = movmatrix(pack_h2(w[0], w[1]));
     pb[1] = movmatrix(pack_h2(w[2], w[3]));
-}
-
-// Pages of 16 rows (8 warps split the pages of one row tile).
-template <int HD, int DT>
-__global__ void __launch_bounds__(KR_WARPS * 32) k_kv8_attn_rows(const __grid_constant__ Kv8AttnP p) {
-    constexpr int NT = KR_ROWS / 8, KS = HD / 16, DW = HD / 32;  // DW: words of 4 dims of a lane's V row share
-    extern __shared__ float sm_o[];                              // [warps][16][HD]
-    __shared__ float sm_m[KR_WARPS][KR_ROWS], sm_l[KR_WARPS][KR_ROWS];
-    __shared__ int sm_bad;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
-    const int b = blockIdx.z, head = blockIdx.y, row0 = blockIdx.x * KR_ROWS;
-    int s, r0, n;
-    const bool alive = attn_entry(p, b, s, r0, n);
-    if (!alive) {
-        if (threadIdx.x == 0) atomicOr(p.status, QW_KV8_BAD_POS);
-        if (r0 < 0 || n < 0 || n > p.max_len || r0 > p.T - n) return;
-    }
-    const int rows = n * p.G;
-    if (row0 >= rows) return;
-    if (threadIdx.x == 0) sm_bad = !alive;
-    __syncthreads();
-    const int last_row = min(row0 + KR_ROWS, rows) - 1;
-    const int n_pages = alive ? (s + last_row / p.G) / KV8_PAGE + 1 : 0;
-    const int* table = p.kv.table + (size_t)b * p.kv.max_pages;
-
-    uint32_t qf[NT][KS][2];
-    float qmul[NT][2];   // of the lane's columns: rows 8 nt + 2 c, + 1
-    int limit[NT][2];    // last visible position of the columns
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        const int r = row0 + 8 * nt + g;
-        const bool v = r < rows;
-        const int i = v ? r / p.G : 0, h = head * p.G + (v ? r % p.G : 0);
-        float mul;
-        load_q<HD, DT>(p, v, (size_t)(r0 + i) * p.ld_q + (size_t)h * HD, c, qf[nt], mul);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            qmul[nt][e] = __shfl_sync(0xffffffffu, mul, (2 * c + e) * 4) * p.scale_log2;
-            const int rr = row0 + 8 * nt + 2 * c + e;
-            limit[nt][e] = rr < rows ? s + rr / p.G : -1;
-        }
-    }
-    float R[NT][2], l[NT][2], o[NT][2 * DW][4];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        R[nt][0] = R[nt][1] = -1e30f;
-        l[nt][0] = l[nt][1] = 0.f;
-#pragma unroll
-        for (int i = 0; i < 2 * DW; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
-    }
-    for (int pi = warp; pi < n_pages; pi += KR_WARPS) {
-        const int page = table[pi];
-        if (page < 0 || page >= p.kv.n_pages) {
-            sm_bad = 1;
-            continue;
-        }
-        const uint8_t* blk = p.kv.blocks + ((size_t)page * p.kv.n_kv + head) * Kv8<HD>::BLK;
-        const float sk = reinterpret_cast<const float*>(blk + Kv8<HD>::SOFF)[0];
-        const float sv = reinterpret_cast<const float*>(blk + Kv8<HD>::SOFF)[1];
-        const int ev = kv8_log2(sv);
-        const float inv_sv = kv8_pow2(-ev);
-        uint32_t a[KS][4];
-        load_k<HD>(blk, g, c, a);
-        uint32_t pb[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int k = 0; k < KS; ++k) mma16816(d, a[k], qf[nt][k][0], qf[nt][k][1]);
-            const int p0 = pi * KV8_PAGE + kv8_tok(g, 0);
-            const float f[2] = {qmul[nt][0] * sk, qmul[nt][1] * sk};
-            const bool v0[2] = {p0 <= limit[nt][0], p0 <= limit[nt][1]}, v1[2] = {p0 + 2 <= limit[nt][0], p0 + 2 <= limit[nt][1]};
-            softmax_page<HD>(d, f, v0, v1, ev, inv_sv, R[nt], l[nt], o[nt], pb[nt]);
-        }
-        mma_pv<HD, NT>(blk + Kv8<HD>::VOFF, g, c, pb, o);
-    }
-    // ---- merge the warps ----
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            float x = l[nt][e];
-            x += __shfl_xor_sync(0xffffffffu, x, 4);
-            x += __shfl_xor_sync(0xffffffffu, x, 8);
-            x += __shfl_xor_sync(0xffffffffu, x, 16);
-            const int r = 8 * nt + 2 * c + e;
-            if (g == 0) {
-                sm_m[warp][r] = R[nt][e];
-                sm_l[warp][r] = x;
-            }
-            float* dst = sm_o + ((size_t)warp * KR_ROWS + r) * HD + g * (HD / 8);
-#pragma unroll
-            for (int i = 0; i < 2 * DW; ++i) {  // tile i: dims 2 i, 2 i + 1 of the lane's HD / 8
-                dst[2 * i] = o[nt][i][e];
-                dst[2 * i + 1] = o[nt][i][2 + e];
-            }
-        }
-    __syncthreads();
-    const bool bad = sm_bad;
-    if (bad && threadIdx.x == 0) atomicOr(p.status, QW_KV8_BAD_POS);
-    for (int x = threadIdx.x; x < KR_ROWS * HD / 2; x += KR_WARPS * 32) {
-        const int r = x / (HD / 2), d = (x % (HD / 2)) * 2;
-        if (row0 + r >= rows) break;
-        float M = -1e30f;
-        for (int w = 0; w < KR_WARPS; ++w) M = fmaxf(M, sm_m[w][r]);
-        float L = 0.f, o0 = 0.f, o1 = 0.f;
-        for (int w = 0; w < KR_WARPS; ++w) {
-            const float f = ex2(sm_m[w][r] - M);
-            L += sm_l[w][r] * f;
-            o0 += sm_o[((size_t)w * KR_ROWS + r) * HD + d] * f;
-            o1 += sm_o[((size_t)w * KR_ROWS + r) * HD + d + 1] * f;
-        }
-        const float inv = bad ? 0.f : 1.f / L;
-        if (bad) o0 = o1 = 0.f;
-        const int i = (row0 + r) / p.G, h = head * p.G + (row0 + r) % p.G;
-        const uint32_t v = DT == QW_F16 ? pack_h2(o0 * inv, o1 * inv) : pack_bf2(o0 * inv, o1 * inv);
-        *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(p.out) + (size_t)(r0 + i) * p.ld_out + (size_t)h * HD + d) = v;
-        if (d == 0) {
-            const float z = log2f(L) + M - KV8_LIFT;
-            const size_t at = (size_t)(r0 + i) * p.n_heads + h;
-            if (p.lse2) p.lse2[at] = bad ? __int_as_float(0x7fffffff) : z;
-            if (p.lse) p.lse[at] = bad ? 0.f : z * KV8_LN2;
-        }
-    }
 }
 
 // Scores: score_out[j] = score_in[j] + sum over the rows of 2^(t_j - lse2). One warp per page: it
@@ -874,13 +749,454 @@ __global__ void __launch_bounds__(KD_WARPS * 32) k_kv8_combine(const __grid_cons
     }
 }
 
+// =======================================================================================
+// k_kv8_chunk: many query rows (prompts and chunks of them) on tcgen05.
+//
+// A CTA takes 128 rows of one (entry, KV head): rows are (token, head of the group) pairs, token
+// major, so any group size fills the MMA. Per tile of 128 keys (8 pages):
+//   converters (4 warps): codes -> fp16 operands in shared memory, K and V alike as [key][dim] rows
+//                  in the 128-byte swizzle; the next tile's codes are already in registers;
+//   S = Q K^T      S in TMEM (128 columns); a thread of the first softmax warp issues the MMAs
+//                  (8 warps a CTA leave each thread 128 registers with two CTAs an SM);
+//   softmax        four warps, thread = row = TMEM lane; the page scales enter the exponent's FMA;
+//                  P (fp16) overwrites the first half of S;
+//   O += P V       A = P from TMEM, B = V, O in TMEM (HD columns).
+// Tensor work bounds long chunks: 2 * 128 * 128 * HD MACs a tile against ~5 instructions and one
+// exponential per score. 96 KB of shared memory and 256 TMEM columns let two CTAs share an SM, so
+// one's softmax overlaps the other's MMAs without a second copy of anything. When the rows give
+// too few CTAs, the keys are split (`splits`) and k_kv8_chunk_combine adds the partials in order.
+// Every wait is bounded.
+// =======================================================================================
+constexpr int CT_WARPS = 8, CT_THREADS = CT_WARPS * 32;  // 0-3 softmax (0 issues the MMAs), 4-7 converters
+constexpr int CT_BK = 128, CT_ROWS = 128;
+constexpr int CT_SUB = 128 * 128;      // [128 rows][64 dims] fp16, swizzled
+constexpr int CT_TMEM = 256, CT_O = 128;
+
+template <int HD>
+struct Ct {
+    static constexpr int MAT = CT_SUB * (HD / 64);
+    static constexpr int OFF_K = MAT, OFF_V = 2 * MAT, OFF_BAR = 3 * MAT;
+    static constexpr int SMEM = 1024 + OFF_BAR + 512;
+};
+
+struct Kv8ChunkP {
+    Kv8AttnP a;
+    int splits;
+    float* part_o;   // [B * n_kv][tiles][splits][128][HD]
+    float* part_ml;  // [B * n_kv][tiles][splits][128][2]
+    int tiles;
+};
+
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void sts128(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+template <int HD, int DT>
+__global__ void __launch_bounds__(CT_THREADS, 2) k_kv8_chunk(const __grid_constant__ Kv8ChunkP P) {
+    const Kv8AttnP& p = P.a;
+    constexpr int MAT = Ct<HD>::MAT, NSUB = HD / 64, CH = HD / 16, RP = 128 / CH, NP = CT_BK / RP;
+    extern __shared__ uint8_t ct_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ct_raw) + 1023) & ~(uintptr_t)1023);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Ct<HD>::OFF_BAR);
+    uint64_t *k_full = bars, *v_full = bars + 1, *k_empty = bars + 2, *pv_done = bars + 3, *s_full = bars + 4, *p_full = bars + 5,
+             *q_ready = bars + 6, *mma_fin = bars + 7;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 8);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    float2* scales = reinterpret_cast<float2*>(bars + 10);  // [2][8]: 2^ek and ev of the tile's pages
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int b = blockIdx.z, head = blockIdx.y;
+    const int tile = P.tiles - 1 - (int)(blockIdx.x / P.splits), split = blockIdx.x % P.splits;  // long rows first
+    const int row0 = tile * CT_ROWS;
+    int s, r0, n;
+    if (!attn_entry(p, b, s, r0, n)) {
+        if (threadIdx.x == 0) atomicOr(p.status, QW_KV8_BAD_POS);
+        if (split || r0 < 0 || n < 0 || n > p.max_len || r0 > p.T - n) return;
+        const int rows = n * p.G;
+        for (int x = threadIdx.x; x < CT_ROWS * (HD / 8); x += CT_THREADS) {
+            const int r = row0 + x / (HD / 8);
+            if (r >= rows) break;
+            *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + (size_t)(r0 + r / p.G) * p.ld_out +
+                                      (size_t)(head * p.G + r % p.G) * HD + (x % (HD / 8)) * 8) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        return;
+    }
+    const int rows = n * p.G;
+    if (row0 >= rows) return;
+    const int kend = s + (min(row0 + CT_ROWS, rows) - 1) / p.G + 1;  // keys the tile's last row sees
+    const int n_kt = (kend + CT_BK - 1) / CT_BK;
+    const int j0 = (int)((long long)n_kt * split / P.splits), j1 = (int)((long long)n_kt * (split + 1) / P.splits);
+    const size_t part = (((size_t)b * p.kv.n_kv + head) * P.tiles + tile) * P.splits + split;
+    if (j0 == j1) {  // nothing to add
+        if (threadIdx.x < CT_ROWS) {
+            P.part_ml[(part * CT_ROWS + threadIdx.x) * 2] = -1e30f;
+            P.part_ml[(part * CT_ROWS + threadIdx.x) * 2 + 1] = 0.f;
+        }
+        return;
+    }
+    auto wait = [&](uint64_t* bar, int parity) { return mbar_wait(smem_u32(bar), (uint32_t)parity & 1u, abort_flag); };
+    if (threadIdx.x == 0) {
+        mbar_init(smem_u32(k_full), 4);
+        mbar_init(smem_u32(v_full), 4);
+        mbar_init(smem_u32(k_empty), 1);
+        mbar_init(smem_u32(pv_done), 1);
+        mbar_init(smem_u32(s_full), 1);
+        mbar_init(smem_u32(p_full), 4);
+        mbar_init(smem_u32(q_ready), 4);
+        mbar_init(smem_u32(mma_fin), 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 4) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(CT_TMEM)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp >= 4) {
+        // ---------------- converters ----------------
+        // Thread (row, pos) of a pass of RP rows takes 16 codes at 16-byte position pos of its row.
+        const int t = threadIdx.x - 4 * 32, pos = t % CH, prow = t / CH;
+        const int* table = p.kv.table + (size_t)b * p.kv.max_pages;
+        const int key_pages = (kend + KV8_PAGE - 1) / KV8_PAGE;
+        // lane l < 8 of each warp: block of the tile's page l
+        auto block_of = [&](int j) -> const uint8_t* {
+            const int pi = j * 8 + (lane & 7);
+            if (j >= j1 || pi >= key_pages) return nullptr;
+            int id = table[pi];
+            if (id < 0 || id >= p.kv.n_pages) {
+                atomicOr(p.status, QW_KV8_BAD_POS);
+                id = 0;
+            }
+            return p.kv.blocks + ((size_t)id * p.kv.n_kv + head) * Kv8<HD>::BLK;
+        };
+        uint4 kr[NP], vr[NP];
+        auto load = [&](const uint8_t* blk, int j, uint4* r, int off) {
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                const int row = prow + i * RP;
+                const uint8_t* base = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, (unsigned long long)blk, row >> 4));
+                // rows past the keys are zeros: weight 0 must add exactly 0
+                r[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (j * CT_BK + row < kend) r[i] = *reinterpret_cast<const uint4*>(base + off + (row & 15) * HD + pos * 16);
+            }
+        };
+        auto store = [&](const uint4* r, uint32_t mat, bool is_v) {
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                const int row = prow + i * RP, tk = row & 15;
+                const int ch = is_v ? kv8_v_pos<HD>(tk, pos) : kv8_k_pos<HD>(tk, pos);  // its own inverse
+                const uint32_t at = mat + (ch >> 2) * CT_SUB + row * 128;
+                const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
+                uint32_t h[8];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    h[2 * k] = kv8_dec2(w[k] & 0xFFFFu);
+                    h[2 * k + 1] = kv8_dec2(w[k] >> 16);
+                }
+                // the second 64 dims start with their odd chunk, so 8 lanes of a row meet 8 positions
+                const bool odd = HD == 128 && (ch & 4);
+                const int c0 = 2 * (ch & 3);
+                sts128(at + (((c0 + odd) ^ (row & 7)) << 4), odd ? h[4] : h[0], odd ? h[5] : h[1], odd ? h[6] : h[2], odd ? h[7] : h[3]);
+                sts128(at + (((c0 + !odd) ^ (row & 7)) << 4), odd ? h[0] : h[4], odd ? h[1] : h[5], odd ? h[2] : h[6], odd ? h[3] : h[7]);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+        };
+        const uint8_t* blk = block_of(j0);
+        const uint8_t* nxt = block_of(j0 + 1);
+        float2 sc = make_float2(1.f, 1.f);  // of no page: masked scores stay -inf
+        auto load_scales = [&](const uint8_t* bl) {
+            if (warp == 4 && lane < 8) sc = bl ? *reinterpret_cast<const float2*>(bl + Kv8<HD>::SOFF) : make_float2(1.f, 1.f);
+        };
+        load(blk, j0, kr, 0);
+        load_scales(blk);
+        load(blk, j0, vr, Kv8<HD>::VOFF);
+        for (int j = j0, i = 0; j < j1; ++j, ++i) {
+            if (i && !__all_sync(0xffffffffu, wait(k_empty, i - 1))) break;
+            if (warp == 4 && lane < 8) scales[(i & 1) * 8 + lane] = make_float2(sc.x, (float)kv8_log2(sc.y));
+            store(kr, smem_u32(sm + Ct<HD>::OFF_K), false);
+            if (lane == 0) mbar_arrive(smem_u32(k_full));
+            if (j + 1 < j1) {
+                load(nxt, j + 1, kr, 0);
+                load_scales(nxt);
+            }
+            if (i && !__all_sync(0xffffffffu, wait(pv_done, i - 1))) break;
+            store(vr, smem_u32(sm + Ct<HD>::OFF_V), true);
+            if (lane == 0) mbar_arrive(smem_u32(v_full));
+            if (j + 1 < j1) load(nxt, j + 1, vr, Kv8<HD>::VOFF);
+            nxt = block_of(j + 2);
+        }
+    } else {
+        // ---------------- softmax / output: thread = row = TMEM lane ----------------
+        const int r = threadIdx.x, row = row0 + r;
+        const bool valid = row < rows;
+        const int tok = r0 + (valid ? row / p.G : 0), hq = head * p.G + (valid ? row % p.G : 0);
+        const int qpos = valid ? s + row / p.G : -1;
+        const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
+        auto wwait = [&](uint64_t* bar, int parity) { return __all_sync(0xffffffffu, wait(bar, parity)); };
+        float qmul = p.scale_log2;
+        {
+            // the Q row as a swizzled operand; a bf16 row is divided by the power of two of its largest
+            // value (see load_q)
+            const uint16_t* src = reinterpret_cast<const uint16_t*>(p.q) + (size_t)tok * p.ld_q + (size_t)hq * HD;
+            float inv = 1.f;
+            if (DT == QW_BF16) {
+                float am = 0.f;
+#pragma unroll 4
+                for (int ch = 0; ch < HD / 8; ++ch) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(src + ch * 8);
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) am = fmaxf(am, fmaxf(fabsf(bf_lo(w[k])), fabsf(bf_hi(w[k]))));
+                }
+                const int x = min(max(kv8_log2(am), -100), 100);
+                qmul *= kv8_pow2(x);
+                inv = kv8_pow2(-x);
+            }
+#pragma unroll 4
+            for (int ch = 0; ch < HD / 8; ++ch) {
+                uint4 v = *reinterpret_cast<const uint4*>(src + ch * 8);
+                if (DT == QW_BF16) {
+                    v.x = pack_h2(bf_lo(v.x) * inv, bf_hi(v.x) * inv);
+                    v.y = pack_h2(bf_lo(v.y) * inv, bf_hi(v.y) * inv);
+                    v.z = pack_h2(bf_lo(v.z) * inv, bf_hi(v.z) * inv);
+                    v.w = pack_h2(bf_lo(v.w) * inv, bf_hi(v.w) * inv);
+                }
+                if (!valid) v = make_uint4(0u, 0u, 0u, 0u);
+                sts128(smem_u32(sm) + (ch >> 3) * CT_SUB + r * 128 + (((ch & 7) ^ (r & 7)) << 4), v.x, v.y, v.z, v.w);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(q_ready));
+        }
+        // Thread 0 issues the MMAs between its softmax tiles. S of tile i overwrites the columns of
+        // P of tile i - 1, so it waits until that tile's P V has finished.
+        const uint32_t qa = smem_u32(sm), ka = smem_u32(sm + Ct<HD>::OFF_K), va = smem_u32(sm + Ct<HD>::OFF_V);
+        auto issue_s = [&](int i) {
+            if (!(i ? wait(pv_done, i - 1) : wait(q_ready, 0)) || !wait(k_full, i)) {
+                *abort_flag = 1;
+                return;
+            }
+            tc_fence_after();
+#pragma unroll
+            for (int sub = 0; sub < NSUB; ++sub)
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    umma_f16(tmem, sw128_desc(qa + sub * CT_SUB) + 2 * kk, sw128_desc(ka + sub * CT_SUB) + 2 * kk,
+                             idesc_f16(128, CT_BK), (sub | kk) ? 1u : 0u);
+            umma_commit(smem_u32(s_full));
+            umma_commit(smem_u32(k_empty));
+        };
+        auto issue_pv = [&](int i) {
+            if (!wait(p_full, i) || !wait(v_full, i)) {
+                *abort_flag = 1;
+                return;
+            }
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < CT_BK / 16; ++kk)
+                umma_f16_ts(tmem + CT_O, tmem + kk * 8, sw128_desc_mn(va + kk * 16 * 128, CT_SUB), idesc_f16(128, HD) | kIdescBMajorMN,
+                            (i | kk) ? 1u : 0u);
+            umma_commit(smem_u32(pv_done));
+        };
+        float R = -1e30f, l = 0.f;
+        bool good = true;
+        const int first_masked = s + row0 / p.G;  // tiles that end at or before it need no mask
+        for (int j = j0, i = 0; j < j1; ++j, ++i) {
+            if (threadIdx.x == 0) issue_s(i);
+            __syncwarp();
+            if (!wwait(s_full, i)) {
+                good = false;
+                break;
+            }
+            tc_fence_after();
+            const float2* scl = scales + (i & 1) * 8;
+            const int k0 = j * CT_BK;
+            const bool masked = k0 + CT_BK - 1 > first_masked || !valid;
+            float mt = -INFINITY;
+#pragma unroll
+            for (int cc = 0; cc < 4; ++cc) {
+                uint32_t x[32];
+                TMEM_LD32(lane_base + cc * 32, x);
+                tmem_wait_ld();
+                if (masked) {
+#pragma unroll
+                    for (int u = 0; u < 32; ++u)
+                        if (k0 + cc * 32 + u > qpos) x[u] = 0xFF800000u;
+                }
+#pragma unroll
+                for (int pg = 0; pg < 2; ++pg) {
+                    float a[4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) a[u] = __uint_as_float(x[16 * pg + u]);
+#pragma unroll
+                    for (int u = 4; u < 16; ++u) a[u & 3] = fmaxf(a[u & 3], __uint_as_float(x[16 * pg + u]));
+                    const float2 sc = scl[2 * cc + pg];
+                    const float m = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
+                    mt = fmaxf(mt, m == -INFINITY ? m : fmaf(m, qmul * sc.x, sc.y));
+                }
+            }
+            const bool move = mt > R + KV8_SLACK;
+            if (__any_sync(0xffffffffu, move)) {
+                const float al = move ? ex2(R - mt) : 1.f;
+                if (move) R = mt;
+                l *= al;
+                if (i > 0) {  // P V of the tile before has finished: S of this one was issued after it
+#pragma unroll 1
+                    for (int cc = 0; cc < HD / 32; ++cc) {
+                        uint32_t x[32];
+                        TMEM_LD32(lane_base + CT_O + cc * 32, x);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int u = 0; u < 32; ++u) x[u] = __float_as_uint(__uint_as_float(x[u]) * al);
+                        TMEM_ST32(lane_base + CT_O + cc * 32, x);
+                    }
+                }
+            }
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                uint32_t h[32];
+#pragma unroll
+                for (int c2 = 0; c2 < 2; ++c2) {
+                    const int cc = half * 2 + c2;
+                    uint32_t x[32];
+                    TMEM_LD32(lane_base + cc * 32, x);
+                    tmem_wait_ld();
+                    if (masked) {
+#pragma unroll
+                        for (int u = 0; u < 32; ++u)
+                            if (k0 + cc * 32 + u > qpos) x[u] = 0xFF800000u;
+                    }
+#pragma unroll
+                    for (int pg = 0; pg < 2; ++pg) {
+                        const float2 sc = scl[2 * cc + pg];
+                        const float f = qmul * sc.x, a = sc.y - R + KV8_LIFT;
+                        float sum[2] = {0.f, 0.f};
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) {
+                            const float e0 = ex2(fmaf(__uint_as_float(x[16 * pg + 2 * u]), f, a));
+                            const float e1 = ex2(fmaf(__uint_as_float(x[16 * pg + 2 * u + 1]), f, a));
+                            sum[u & 1] += e0 + e1;
+                            h[c2 * 16 + pg * 8 + u] = pack_h2(e0, e1);
+                        }
+                        l = fmaf(sum[0] + sum[1], kv8_pow2(-(int)sc.y), l);
+                    }
+                }
+                TMEM_ST32(lane_base + half * 32, h);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(p_full));
+            if (threadIdx.x == 0) issue_pv(i);
+            __syncwarp();
+        }
+        if (threadIdx.x == 0) {
+            // the commits' asynchronous arrivals land before the CTA ends
+            umma_commit(smem_u32(mma_fin));
+            const uint64_t t0 = globaltimer_ns();
+            while (!mbar_try_wait(smem_u32(mma_fin), 0) && globaltimer_ns() - t0 < kTcWaitNs) {
+            }
+        }
+        __syncwarp();
+        if (good && wwait(pv_done, j1 - j0 - 1)) {
+            tc_fence_after();
+            const float inv = P.splits == 1 ? 1.f / l : 1.f;
+#pragma unroll 1
+            for (int cc = 0; cc < HD / 32; ++cc) {
+                uint32_t x[32];
+                TMEM_LD32(lane_base + CT_O + cc * 32, x);
+                tmem_wait_ld();
+                if (valid && P.splits == 1) {
+                    float v[32];
+#pragma unroll
+                    for (int u = 0; u < 32; ++u) v[u] = __uint_as_float(x[u]) * inv;
+                    store_row<DT, 16>(p.out, (size_t)tok * p.ld_out + (size_t)hq * HD + cc * 32, v);
+                } else if (valid) {
+                    float* dst = P.part_o + (part * CT_ROWS + r) * HD + cc * 32;
+#pragma unroll
+                    for (int u = 0; u < 32; u += 4)
+                        *reinterpret_cast<uint4*>(dst + u) = make_uint4(x[u], x[u + 1], x[u + 2], x[u + 3]);
+                }
+                __syncwarp();
+            }
+            if (valid && P.splits == 1) {
+                const float z = log2f(l) + R - KV8_LIFT;
+                if (p.lse2) p.lse2[(size_t)tok * p.n_heads + hq] = z;
+                if (p.lse) p.lse[(size_t)tok * p.n_heads + hq] = z * KV8_LN2;
+            } else if (valid) {
+                P.part_ml[(part * CT_ROWS + r) * 2] = R;
+                P.part_ml[(part * CT_ROWS + r) * 2 + 1] = l;
+            }
+        } else {
+            *abort_flag = 1;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (*abort_flag && threadIdx.x == 0) atomicOr(p.status, QW_KV8_TIMEOUT);
+    if (warp == 4) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(CT_TMEM) : "memory");
+    }
+}
+
+// Adds a row tile's partials over the splits, in order; 8 rows a CTA, a warp a row.
+template <int HD, int DT>
+__global__ void __launch_bounds__(256) k_kv8_chunk_combine(const __grid_constant__ Kv8ChunkP P) {
+    const Kv8AttnP& p = P.a;
+    const int lane = threadIdx.x & 31, b = blockIdx.z, head = blockIdx.y, row = blockIdx.x * 8 + (threadIdx.x >> 5);
+    int s, r0, n;
+    if (!attn_entry(p, b, s, r0, n) || row >= n * p.G) return;
+    pdl_wait();
+    const size_t part = (((size_t)b * p.kv.n_kv + head) * P.tiles + row / CT_ROWS) * P.splits;
+    float M = -1e30f, L = 0.f;
+    for (int k = 0; k < P.splits; ++k) M = fmaxf(M, P.part_ml[((part + k) * CT_ROWS + row % CT_ROWS) * 2]);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < P.splits; ++k) {
+        const size_t at = (part + k) * CT_ROWS + row % CT_ROWS;
+        const float l = P.part_ml[at * 2 + 1];
+        if (l == 0.f) continue;  // that split has no partial
+        const float f = ex2(P.part_ml[at * 2] - M);
+        L += l * f;
+        if (lane < HD / 4) {
+            const float4 v = *reinterpret_cast<const float4*>(P.part_o + at * HD + lane * 4);
+            acc.x += v.x * f;
+            acc.y += v.y * f;
+            acc.z += v.z * f;
+            acc.w += v.w * f;
+        }
+    }
+    const float inv = 1.f / L;
+    const int tok = r0 + row / p.G, h = head * p.G + row % p.G;
+    if (lane < HD / 4) {
+        uint2 w;
+        w.x = DT == QW_F16 ? pack_h2(acc.x * inv, acc.y * inv) : pack_bf2(acc.x * inv, acc.y * inv);
+        w.y = DT == QW_F16 ? pack_h2(acc.z * inv, acc.w * inv) : pack_bf2(acc.z * inv, acc.w * inv);
+        *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) + (size_t)tok * p.ld_out + (size_t)h * HD + lane * 4) = w;
+    }
+    if (lane == 0) {
+        const float z = log2f(L) + M - KV8_LIFT;
+        if (p.lse2) p.lse2[(size_t)tok * p.n_heads + h] = z;
+        if (p.lse) p.lse[(size_t)tok * p.n_heads + h] = z * KV8_LN2;
+    }
+}
+
 // ---- which kernels a call runs, and its workspace ---------------------------------------
 
 struct Plan {
     bool decode;       // k_kv8_decode (max_len * G <= 16 rows)
     bool pair_mode;
     bool tbuf;         // scores from stored logits
-    int nrow, stages, n_cta, smem;
+    int nrow, stages, n_cta, smem;  // decode
+    int tiles, splits;              // k_kv8_chunk
     size_t off_o, off_ml, off_t, bytes;
 };
 
@@ -918,6 +1234,16 @@ Plan make_plan(const qw_kv8* kv, int B, int T, int max_len, int max_keys, int n_
         q.off_o = put(q.pair_mode ? 0 : (size_t)q.n_cta * 2 * q.nrow * HD * 4);
         q.off_ml = put(q.pair_mode ? 0 : (size_t)q.n_cta * 2 * q.nrow * 2 * 4);
         q.off_t = put(q.tbuf ? (size_t)B * kv->n_kv_heads * q.nrow * (((size_t)max_keys + 3) & ~(size_t)3) * 4 : 0);
+    }
+    if (!q.decode) {
+        q.tiles = (int)((rows + CT_ROWS - 1) / CT_ROWS);
+        // two CTAs an SM; few row tiles split their keys, at least two key tiles each
+        const long long ctas = (long long)q.tiles * kv->n_kv_heads * B;
+        const int kt = (max_keys + CT_BK - 1) / CT_BK;
+        q.splits = (int)std::max(1ll, std::min({2ll * sm_count() / ctas, (long long)kt / 2, 64ll}));
+        const size_t part = q.splits == 1 ? 0 : (size_t)ctas * q.splits * CT_ROWS;
+        q.off_o = put(part * HD * 4);
+        q.off_ml = put(part * 2 * 4);
     }
     q.bytes = std::max(q.bytes, (size_t)256);
     return q;
@@ -963,11 +1289,16 @@ cudaError_t run_attn(const Kv8AttnP& p, const Plan& q, int B, char* ws, cudaStre
         }
         return p.score_out && !q.tbuf ? run_score<HD, DT>(p, B, st) : cudaSuccess;
     }
-    const int smem = KR_WARPS * KR_ROWS * HD * 4;
-    if ((e = allow_smem(k_kv8_attn_rows<HD, DT>, smem)) != cudaSuccess) return e;
-    const int len = std::min(p.max_len, p.T);
-    const unsigned tiles = (unsigned)(((long long)len * p.G + KR_ROWS - 1) / KR_ROWS);
-    e = launch_k(c, k_kv8_attn_rows<HD, DT>, dim3(tiles, p.kv.n_kv, B), dim3(KR_WARPS * 32), (size_t)smem, p);
+    Kv8ChunkP P = {};
+    P.a = p;
+    P.splits = q.splits;
+    P.part_o = (float*)(ws + q.off_o);
+    P.part_ml = (float*)(ws + q.off_ml);
+    P.tiles = q.tiles;
+    if ((e = allow_smem(k_kv8_chunk<HD, DT>, Ct<HD>::SMEM)) != cudaSuccess) return e;
+    e = launch_k(c, k_kv8_chunk<HD, DT>, dim3(q.tiles * q.splits, p.kv.n_kv, B), dim3(CT_THREADS), (size_t)Ct<HD>::SMEM, P);
+    if (e == cudaSuccess && q.splits > 1)
+        e = launch_k(c, k_kv8_chunk_combine<HD, DT>, dim3(q.tiles * CT_ROWS / 8, p.kv.n_kv, B), dim3(256), 0, P);
     return e == cudaSuccess && p.score_out ? run_score<HD, DT>(p, B, st) : e;
 }
 
