@@ -203,62 +203,6 @@ __device__ __forceinline__ void softmax_page(const float* d, const float* f, con
     pb[1] = movmatrix(pack_h2(w[2], w[3]));
 }
 
-// Scores: score_out[j] = score_in[j] + sum over the rows of 2^(t_j - lse2). One warp per page: it
-// keeps the page's K as the A operand and walks the query rows in tiles of 8.
-template <int HD, int DT>
-__global__ void __launch_bounds__(128) k_kv8_score(const __grid_constant__ Kv8AttnP p) {
-    constexpr int KS = HD / 16;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
-    const int b = blockIdx.z, head = blockIdx.y, pi = blockIdx.x * 4 + warp;
-    int s, r0, n;
-    if (!attn_entry(p, b, s, r0, n) || n == 0 || pi * KV8_PAGE >= s + n) return;
-    const int rows = n * p.G;
-    const float z0 = p.lse2[(size_t)r0 * p.n_heads + head * p.G];
-    if (__float_as_uint(z0) == 0x7fffffffu) return;  // an entry left out
-    const int page = p.kv.table[(size_t)b * p.kv.max_pages + pi];
-    if (page < 0 || page >= p.kv.n_pages) return;
-    const uint8_t* blk = p.kv.blocks + ((size_t)page * p.kv.n_kv + head) * Kv8<HD>::BLK;
-    const float sk = reinterpret_cast<const float*>(blk + Kv8<HD>::SOFF)[0];
-    uint32_t a[KS][4];
-    load_k<HD>(blk, g, c, a);
-    const int p0 = pi * KV8_PAGE + kv8_tok(g, 0);
-    float acc0 = 0.f, acc1 = 0.f;
-    // rows of tokens before the page's first position see nothing of it
-    const int first = max(0, pi * KV8_PAGE - s) * p.G;
-    for (int row0 = first & ~7; row0 < rows; row0 += 8) {
-        const int r = row0 + g;
-        const bool v = r < rows;
-        const int i = v ? r / p.G : 0, h = head * p.G + (v ? r % p.G : 0);
-        uint32_t qf[KS][2];
-        float mul;
-        load_q<HD, DT>(p, v, (size_t)(r0 + i) * p.ld_q + (size_t)h * HD, c, qf, mul);
-        const float z = v ? p.lse2[(size_t)(r0 + i) * p.n_heads + h] : 0.f;
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int k = 0; k < KS; ++k) mma16816(d, a[k], qf[k][0], qf[k][1]);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const float f = __shfl_sync(0xffffffffu, mul, (2 * c + e) * 4) * p.scale_log2 * sk;
-            const float zc = __shfl_sync(0xffffffffu, z, (2 * c + e) * 4);
-            const int rr = row0 + 2 * c + e, lim = rr < rows ? s + rr / p.G : -1;
-            if (p0 <= lim) acc0 += ex2(fmaf(d[e], f, -zc));
-            if (p0 + 2 <= lim) acc1 += ex2(fmaf(d[2 + e], f, -zc));
-        }
-    }
-#pragma unroll
-    for (int m = 1; m <= 2; m <<= 1) {
-        acc0 += __shfl_xor_sync(0xffffffffu, acc0, m);
-        acc1 += __shfl_xor_sync(0xffffffffu, acc1, m);
-    }
-    if (c < 2) {
-        const int pos = p0 + 2 * c;
-        if (pos < s + n) {
-            const size_t at = ((size_t)b * p.kv.n_kv + head) * p.ld_score + pos;
-            p.score_out[at] = (p.score_in ? p.score_in[at] : 0.f) + (c ? acc1 : acc0);
-        }
-    }
-}
-
 // =======================================================================================
 // k_kv8_decode: few query rows per KV head (a decode step, up to 16 rows of tokens x heads).
 //
@@ -797,7 +741,7 @@ __device__ __forceinline__ void sts128(uint32_t at, uint32_t a, uint32_t b, uint
 template <int HD, int DT>
 __global__ void __launch_bounds__(CT_THREADS, 2) k_kv8_chunk(const __grid_constant__ Kv8ChunkP P) {
     const Kv8AttnP& p = P.a;
-    constexpr int MAT = Ct<HD>::MAT, NSUB = HD / 64, CH = HD / 16, RP = 128 / CH, NP = CT_BK / RP;
+    constexpr int NSUB = HD / 64, CH = HD / 16, RP = 128 / CH, NP = CT_BK / RP;
     extern __shared__ uint8_t ct_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ct_raw) + 1023) & ~(uintptr_t)1023);
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Ct<HD>::OFF_BAR);
@@ -919,7 +863,10 @@ __global__ void __launch_bounds__(CT_THREADS, 2) k_kv8_chunk(const __grid_consta
         load_scales(blk);
         load(blk, j0, vr, Kv8<HD>::VOFF);
         for (int j = j0, i = 0; j < j1; ++j, ++i) {
-            if (i && !__all_sync(0xffffffffu, wait(k_empty, i - 1))) break;
+            if (i && !__all_sync(0xffffffffu, wait(k_empty, i - 1))) {
+                *abort_flag = 1;
+                break;
+            }
             if (warp == 4 && lane < 8) scales[(i & 1) * 8 + lane] = make_float2(sc.x, (float)kv8_log2(sc.y));
             store(kr, smem_u32(sm + Ct<HD>::OFF_K), false);
             if (lane == 0) mbar_arrive(smem_u32(k_full));
@@ -927,7 +874,10 @@ __global__ void __launch_bounds__(CT_THREADS, 2) k_kv8_chunk(const __grid_consta
                 load(nxt, j + 1, kr, 0);
                 load_scales(nxt);
             }
-            if (i && !__all_sync(0xffffffffu, wait(pv_done, i - 1))) break;
+            if (i && !__all_sync(0xffffffffu, wait(pv_done, i - 1))) {
+                *abort_flag = 1;
+                break;
+            }
             store(vr, smem_u32(sm + Ct<HD>::OFF_V), true);
             if (lane == 0) mbar_arrive(smem_u32(v_full));
             if (j + 1 < j1) load(nxt, j + 1, vr, Kv8<HD>::VOFF);
@@ -1189,6 +1139,206 @@ __global__ void __launch_bounds__(256) k_kv8_chunk_combine(const __grid_constant
     }
 }
 
+// =======================================================================================
+// k_kv8_score: score_out[j] = score_in[j] + sum over the query rows of 2^(t_j - lse2), on tcgen05.
+//
+// The normalisers are known, so the weights need only S again, and the sum over rows is a thread's
+// own if the keys are the rows of the MMA: a CTA keeps 128 keys of one (entry, head) as the A operand
+// and walks the query rows in tiles of 128 (B, two buffers). S^T = K Q^T lands in TMEM (two
+// buffers); thread = key adds the exponentials of its row in order, so equal inputs give equal
+// bits. 2 HD MACs and one exponential a (row, key) pair; four warps load and convert the next
+// query tile meanwhile and one of their threads issues the MMAs. Two CTAs share an SM.
+// =======================================================================================
+template <int HD>
+struct Cs {
+    static constexpr int MAT = CT_SUB * (HD / 64);
+    static constexpr int OFF_Q = MAT, OFF_ROW = 3 * MAT, OFF_BAR = OFF_ROW + 4 * CT_ROWS * 16;
+    static constexpr int SMEM = 1024 + OFF_BAR + 256;
+};
+
+template <int HD, int DT>
+__global__ void __launch_bounds__(CT_THREADS, 2) k_kv8_score(const __grid_constant__ Kv8AttnP p) {
+    constexpr int MAT = Cs<HD>::MAT, NSUB = HD / 64, CH = HD / 16;
+    extern __shared__ uint8_t cs_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(cs_raw) + 1023) & ~(uintptr_t)1023);
+    float4* rowc = reinterpret_cast<float4*>(sm + Cs<HD>::OFF_ROW);  // [4][128]: logit factor, lse2, last visible position
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Cs<HD>::OFF_BAR);
+    uint64_t *q_full = bars, *q_empty = bars + 2, *s_full = bars + 4, *s_empty = bars + 6, *mma_fin = bars + 8;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 9);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int b = blockIdx.z, head = blockIdx.y, key0 = blockIdx.x * CT_BK;
+    int s, r0, n;
+    if (!attn_entry(p, b, s, r0, n) || n == 0 || key0 >= s + n) return;
+    const int rows = n * p.G, kend = s + n;
+    const int t0 = max(0, key0 - s) * p.G / CT_ROWS, t1 = (rows + CT_ROWS - 1) / CT_ROWS;  // row tiles that see a key of these
+    auto wait = [&](uint64_t* bar, int parity) { return mbar_wait(smem_u32(bar), (uint32_t)parity & 1u, abort_flag); };
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(q_full + i), 4);
+            mbar_init(smem_u32(q_empty + i), 1);
+            mbar_init(smem_u32(s_full + i), 1);
+            mbar_init(smem_u32(s_empty + i), 4);
+        }
+        mbar_init(smem_u32(mma_fin), 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 4) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(CT_TMEM)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int* table = p.kv.table + (size_t)b * p.kv.max_pages;
+    auto block_of = [&](int pi) -> const uint8_t* {
+        int id = table[pi];
+        if (id < 0 || id >= p.kv.n_pages) {
+            atomicOr(p.status, QW_KV8_BAD_POS);
+            id = 0;
+        }
+        return p.kv.blocks + ((size_t)id * p.kv.n_kv + head) * Kv8<HD>::BLK;
+    };
+    if (warp >= 4) {
+        // ---------------- loaders: the keys once, then the query tiles ----------------
+        const int t = threadIdx.x - 128;
+        {
+            const int row = t, tk = row & 15;  // thread = key
+            const bool on = key0 + row < kend;
+            const uint8_t* src = on ? block_of(key0 / KV8_PAGE + (row >> 4)) + tk * HD : nullptr;
+#pragma unroll 4
+            for (int pos = 0; pos < CH; ++pos) {
+                const int ch = kv8_k_pos<HD>(tk, pos);
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (on) v = *reinterpret_cast<const uint4*>(src + pos * 16);
+                const uint32_t at = smem_u32(sm) + (ch >> 2) * CT_SUB + row * 128;
+                const int c0 = 2 * (ch & 3);
+                sts128(at + ((c0 ^ (row & 7)) << 4), kv8_dec2(v.x & 0xFFFFu), kv8_dec2(v.x >> 16), kv8_dec2(v.y & 0xFFFFu), kv8_dec2(v.y >> 16));
+                sts128(at + (((c0 + 1) ^ (row & 7)) << 4), kv8_dec2(v.z & 0xFFFFu), kv8_dec2(v.z >> 16), kv8_dec2(v.w & 0xFFFFu), kv8_dec2(v.w >> 16));
+            }
+        }
+        for (int rt = t0, i = 0; rt < t1; ++rt, ++i) {
+            const int buf = i & 1, row = rt * CT_ROWS + t;
+            const bool v = row < rows;
+            const int tok = r0 + (v ? row / p.G : 0), hq = head * p.G + (v ? row % p.G : 0);
+            const uint16_t* src = reinterpret_cast<const uint16_t*>(p.q) + (size_t)tok * p.ld_q + (size_t)hq * HD;
+            uint4 x[HD / 8];
+#pragma unroll
+            for (int ch = 0; ch < HD / 8; ++ch) x[ch] = *reinterpret_cast<const uint4*>(src + ch * 8);
+            const float z = p.lse2[(size_t)tok * p.n_heads + hq];
+            float mul = 1.f;
+            if (DT == QW_BF16) {  // as load_q
+                float am = 0.f;
+#pragma unroll
+                for (int ch = 0; ch < HD / 8; ++ch) {
+                    const uint32_t w[4] = {x[ch].x, x[ch].y, x[ch].z, x[ch].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) am = fmaxf(am, fmaxf(fabsf(bf_lo(w[k])), fabsf(bf_hi(w[k]))));
+                }
+                const int e = min(max(kv8_log2(am), -100), 100);
+                mul = kv8_pow2(e);
+                const float inv = kv8_pow2(-e);
+#pragma unroll
+                for (int ch = 0; ch < HD / 8; ++ch) {
+                    x[ch].x = pack_h2(bf_lo(x[ch].x) * inv, bf_hi(x[ch].x) * inv);
+                    x[ch].y = pack_h2(bf_lo(x[ch].y) * inv, bf_hi(x[ch].y) * inv);
+                    x[ch].z = pack_h2(bf_lo(x[ch].z) * inv, bf_hi(x[ch].z) * inv);
+                    x[ch].w = pack_h2(bf_lo(x[ch].w) * inv, bf_hi(x[ch].w) * inv);
+                }
+            }
+            if (i >= 2 && !__all_sync(0xffffffffu, wait(q_empty + buf, (i >> 1) - 1))) {
+                *abort_flag = 1;
+                break;
+            }
+            const uint32_t at = smem_u32(sm + Cs<HD>::OFF_Q + buf * MAT) + t * 128;
+#pragma unroll
+            for (int ch = 0; ch < HD / 8; ++ch)
+                sts128(at + (ch >> 3) * CT_SUB + (((ch & 7) ^ (t & 7)) << 4), x[ch].x, x[ch].y, x[ch].z, x[ch].w);
+            // [i % 4]: the tile four before has been summed, as S^T of the tile two before was issued
+            rowc[(i & 3) * CT_ROWS + t] = make_float4(mul * p.scale_log2, z, __int_as_float(v ? s + row / p.G : -1), 0.f);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(q_full + buf));
+            if (t == 0) {
+                if (!wait(q_full + buf, i >> 1) || (i >= 2 && !wait(s_empty + buf, (i >> 1) - 1))) {
+                    *abort_flag = 1;
+                } else {
+                    tc_fence_after();
+                    const uint32_t ka = smem_u32(sm), qa = smem_u32(sm + Cs<HD>::OFF_Q + buf * MAT);
+#pragma unroll
+                    for (int sub = 0; sub < NSUB; ++sub)
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            umma_f16(tmem + buf * 128, sw128_desc(ka + sub * CT_SUB) + 2 * kk, sw128_desc(qa + sub * CT_SUB) + 2 * kk,
+                                     idesc_f16(128, CT_ROWS), (sub | kk) ? 1u : 0u);
+                    umma_commit(smem_u32(s_full + buf));
+                    umma_commit(smem_u32(q_empty + buf));
+                }
+            }
+            __syncwarp();
+        }
+        if (t == 0) {
+            // the commits' asynchronous arrivals land before the CTA ends
+            umma_commit(smem_u32(mma_fin));
+            const uint64_t w0 = globaltimer_ns();
+            while (!mbar_try_wait(smem_u32(mma_fin), 0) && globaltimer_ns() - w0 < kTcWaitNs) {
+            }
+        }
+        __syncwarp();
+    } else {
+        // ---------------- sums: thread = key = TMEM lane ----------------
+        const int key = key0 + threadIdx.x;
+        const bool on = key < kend;
+        const float sk = on ? *reinterpret_cast<const float*>(block_of(key / KV8_PAGE) + Kv8<HD>::SOFF) : 1.f;
+        const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
+        float acc = 0.f;
+        bool good = true;
+        for (int rt = t0, i = 0; rt < t1; ++rt, ++i) {
+            const int buf = i & 1;
+            if (!__all_sync(0xffffffffu, wait(s_full + buf, i >> 1))) {
+                good = false;
+                break;
+            }
+            tc_fence_after();
+            const float4* rc = rowc + (i & 3) * CT_ROWS;
+            // rows of the tile before the last key's token see not all of these keys
+            const bool masked = s + rt * CT_ROWS / p.G < key0 + CT_BK - 1 || (rt + 1) * CT_ROWS > rows;
+            float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+            for (int cc = 0; cc < 4; ++cc) {
+                uint32_t x[32];
+                TMEM_LD32(lane_base + buf * 128 + cc * 32, x);
+                tmem_wait_ld();
+#pragma unroll
+                for (int u = 0; u < 32; ++u) {
+                    const float4 c = rc[cc * 32 + u];
+                    const float e = ex2(fmaf(__uint_as_float(x[u]), c.x * sk, -c.y));
+                    part[u & 3] += !masked || key <= __float_as_int(c.z) ? e : 0.f;
+                }
+            }
+            acc += (part[0] + part[1]) + (part[2] + part[3]);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(s_empty + buf));
+        }
+        if (good && on) {
+            const size_t at = ((size_t)b * p.kv.n_kv + head) * p.ld_score + key;
+            p.score_out[at] = (p.score_in ? p.score_in[at] : 0.f) + acc;
+        }
+        if (!good) *abort_flag = 1;
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (*abort_flag && threadIdx.x == 0) atomicOr(p.status, QW_KV8_TIMEOUT);
+    if (warp == 4) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(CT_TMEM) : "memory");
+    }
+}
+
 // ---- which kernels a call runs, and its workspace ---------------------------------------
 
 struct Plan {
@@ -1257,8 +1407,9 @@ cudaError_t allow_smem(K kern, int bytes) {
 template <int HD, int DT>
 cudaError_t run_score(const Kv8AttnP& p, int B, cudaStream_t st) {
     LaunchCtx c = {st, false, nullptr};
-    const unsigned pages = (unsigned)((p.max_keys + KV8_PAGE - 1) / KV8_PAGE);
-    return launch_k(c, k_kv8_score<HD, DT>, dim3((pages + 3) / 4, p.kv.n_kv, B), dim3(128), 0, p);
+    if (cudaError_t e = allow_smem(k_kv8_score<HD, DT>, Cs<HD>::SMEM)) return e;
+    const unsigned tiles = (unsigned)((p.max_keys + CT_BK - 1) / CT_BK);
+    return launch_k(c, k_kv8_score<HD, DT>, dim3(tiles, p.kv.n_kv, B), dim3(CT_THREADS), (size_t)Cs<HD>::SMEM, p);
 }
 
 template <int HD, int DT>
