@@ -27,6 +27,7 @@ struct Kv8AttnP {
     const void* q;
     size_t ld_q;
     int T, max_len, max_keys, n_heads, G;
+    uint32_t gmul;  // ceil(2^32 / G) (0: G = 1): row / G by a multiplication, exact for rows < 2^28
     float scale_log2;
     void* out;
     size_t ld_out;
@@ -37,6 +38,9 @@ struct Kv8AttnP {
     size_t ld_score;
     int* status;
 };
+
+// token of row r of an entry (rows are token major, G heads a token)
+__device__ __forceinline__ int row_token(const Kv8AttnP& p, int r) { return p.gmul ? (int)__umulhi((uint32_t)r, p.gmul) : r; }
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -719,7 +723,7 @@ constexpr int CT_TMEM = 256, CT_O = 128;
 template <int HD>
 struct Ct {
     static constexpr int MAT = CT_SUB * (HD / 64);
-    static constexpr int OFF_K = MAT, OFF_V = 2 * MAT, OFF_BAR = 3 * MAT;
+    static constexpr int OFF_K = MAT, OFF_V = 2 * MAT, OFF_MUL = 3 * MAT, OFF_BAR = OFF_MUL + CT_ROWS * 4;
     static constexpr int SMEM = 1024 + OFF_BAR + 512;
 };
 
@@ -738,6 +742,55 @@ __device__ __forceinline__ void sts128(uint32_t at, uint32_t a, uint32_t b, uint
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+// Rows [row0, row0 + 128) of an entry's (token, head) rows as a swizzled fp16 operand, by four warps
+// (w = 0 .. 3), fetched into registers and stored in two steps: HD / 8 lanes take a row's 16-byte
+// chunks, so a request covers whole rows. A bf16 row is divided by the power of two of its largest
+// value (see load_q), which goes to put(row, mul); rows past the entry are zeros.
+template <int HD>
+struct QTile {
+    static constexpr int LPR = HD / 8, RPI = 32 / LPR, NI = 32 / RPI;  // lanes a row, rows a request, requests a warp
+    uint4 x[NI];
+};
+template <int HD>
+__device__ __forceinline__ void fetch_q(QTile<HD>& q, const Kv8AttnP& p, int r0, int head, int row0, int rows, int w, int lane) {
+    const int ch = lane % QTile<HD>::LPR, rw = w * 32 + lane / QTile<HD>::LPR;
+#pragma unroll
+    for (int i = 0; i < QTile<HD>::NI; ++i) {
+        const int row = row0 + rw + i * QTile<HD>::RPI, tok = row_token(p, row);
+        q.x[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (row < rows)
+            q.x[i] = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.q) + (size_t)(r0 + tok) * p.ld_q +
+                                                     (size_t)(head * p.G + row - tok * p.G) * HD + ch * 8);
+    }
+}
+template <int HD, int DT, typename Put>
+__device__ __forceinline__ void store_q(QTile<HD>& q, int w, int lane, uint32_t mat, Put put) {
+    constexpr int LPR = QTile<HD>::LPR;
+    const int ch = lane % LPR, rw = w * 32 + lane / LPR;
+#pragma unroll
+    for (int i = 0; i < QTile<HD>::NI; ++i) {
+        const int r = rw + i * QTile<HD>::RPI;
+        float mul = 1.f;
+        uint4& x = q.x[i];
+        if (DT == QW_BF16) {
+            uint32_t v[4] = {x.x, x.y, x.z, x.w};
+            float am = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) am = fmaxf(am, fmaxf(fabsf(bf_lo(v[k])), fabsf(bf_hi(v[k]))));
+#pragma unroll
+            for (int o = 1; o < LPR; o <<= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+            const int e = min(max(kv8_log2(am), -100), 100);
+            mul = kv8_pow2(e);
+            const float inv = kv8_pow2(-e);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = pack_h2(bf_lo(v[k]) * inv, bf_hi(v[k]) * inv);
+            x = make_uint4(v[0], v[1], v[2], v[3]);
+        }
+        sts128(mat + (ch >> 3) * CT_SUB + r * 128 + (((ch & 7) ^ (r & 7)) << 4), x.x, x.y, x.z, x.w);
+        if (ch == 0) put(r, mul);
+    }
+}
+
 template <int HD, int DT>
 __global__ void __launch_bounds__(CT_THREADS, 2) k_kv8_chunk(const __grid_constant__ Kv8ChunkP P) {
     const Kv8AttnP& p = P.a;
@@ -751,8 +804,8 @@ __global__ void __launch_bounds__(CT_THREADS, 2) k_kv8_chunk(const __grid_consta
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     float2* scales = reinterpret_cast<float2*>(bars + 10);  // [2][8]: 2^ek and ev of the tile's pages
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int b = blockIdx.z, head = blockIdx.y;
-    const int tile = P.tiles - 1 - (int)(blockIdx.x / P.splits), split = blockIdx.x % P.splits;  // long rows first
+    const int b = blockIdx.y, head = blockIdx.x;
+    const int tile = P.tiles - 1 - (int)(blockIdx.z / P.splits), split = blockIdx.z % P.splits;  // the longest rows start first
     const int row0 = tile * CT_ROWS;
     int s, r0, n;
     if (!attn_entry(p, b, s, r0, n)) {
@@ -805,6 +858,8 @@ __global__ void __launch_bounds__(CT_THREADS, 2) k_kv8_chunk(const __grid_consta
 
     if (warp >= 4) {
         // ---------------- converters ----------------
+        // 88 registers a thread here and 168 for the softmax rows: the 128 of the launch, split again
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         // Thread (row, pos) of a pass of RP rows takes 16 codes at 16-byte position pos of its row.
         const int t = threadIdx.x - 4 * 32, pos = t % CH, prow = t / CH;
         const int* table = p.kv.table + (size_t)b * p.kv.max_pages;
@@ -885,47 +940,24 @@ __global__ void __launch_bounds__(CT_THREADS, 2) k_kv8_chunk(const __grid_consta
         }
     } else {
         // ---------------- softmax / output: thread = row = TMEM lane ----------------
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
         const int r = threadIdx.x, row = row0 + r;
         const bool valid = row < rows;
-        const int tok = r0 + (valid ? row / p.G : 0), hq = head * p.G + (valid ? row % p.G : 0);
-        const int qpos = valid ? s + row / p.G : -1;
+        const int qt_ = valid ? row_token(p, row) : 0;
+        const int tok = r0 + qt_, hq = head * p.G + (valid ? row - qt_ * p.G : 0);
+        const int qpos = valid ? s + qt_ : -1;
         const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
         auto wwait = [&](uint64_t* bar, int parity) { return __all_sync(0xffffffffu, wait(bar, parity)); };
-        float qmul = p.scale_log2;
+        float* muls = reinterpret_cast<float*>(sm + Ct<HD>::OFF_MUL);  // written and read by the same warp
         {
-            // the Q row as a swizzled operand; a bf16 row is divided by the power of two of its largest
-            // value (see load_q)
-            const uint16_t* src = reinterpret_cast<const uint16_t*>(p.q) + (size_t)tok * p.ld_q + (size_t)hq * HD;
-            float inv = 1.f;
-            if (DT == QW_BF16) {
-                float am = 0.f;
-#pragma unroll 4
-                for (int ch = 0; ch < HD / 8; ++ch) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(src + ch * 8);
-                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) am = fmaxf(am, fmaxf(fabsf(bf_lo(w[k])), fabsf(bf_hi(w[k]))));
-                }
-                const int x = min(max(kv8_log2(am), -100), 100);
-                qmul *= kv8_pow2(x);
-                inv = kv8_pow2(-x);
-            }
-#pragma unroll 4
-            for (int ch = 0; ch < HD / 8; ++ch) {
-                uint4 v = *reinterpret_cast<const uint4*>(src + ch * 8);
-                if (DT == QW_BF16) {
-                    v.x = pack_h2(bf_lo(v.x) * inv, bf_hi(v.x) * inv);
-                    v.y = pack_h2(bf_lo(v.y) * inv, bf_hi(v.y) * inv);
-                    v.z = pack_h2(bf_lo(v.z) * inv, bf_hi(v.z) * inv);
-                    v.w = pack_h2(bf_lo(v.w) * inv, bf_hi(v.w) * inv);
-                }
-                if (!valid) v = make_uint4(0u, 0u, 0u, 0u);
-                sts128(smem_u32(sm) + (ch >> 3) * CT_SUB + r * 128 + (((ch & 7) ^ (r & 7)) << 4), v.x, v.y, v.z, v.w);
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(q_ready));
+            QTile<HD> qt;
+            fetch_q<HD>(qt, p, r0, head, row0, rows, warp, lane);
+            store_q<HD, DT>(qt, warp, lane, smem_u32(sm), [&](int rr, float mul) { muls[rr] = mul; });
         }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(q_ready));
+        const float qmul = p.scale_log2 * muls[r];
         // Thread 0 issues the MMAs between its softmax tiles. S of tile i overwrites the columns of
         // P of tile i - 1, so it waits until that tile's P V has finished.
         const uint32_t qa = smem_u32(sm), ka = smem_u32(sm + Ct<HD>::OFF_K), va = smem_u32(sm + Ct<HD>::OFF_V);
@@ -969,29 +1001,27 @@ __global__ void __launch_bounds__(CT_THREADS, 2) k_kv8_chunk(const __grid_consta
             tc_fence_after();
             const float2* scl = scales + (i & 1) * 8;
             const int k0 = j * CT_BK;
-            const bool masked = k0 + CT_BK - 1 > first_masked || !valid;
+            uint32_t x[CT_BK];  // the row's scores stay in registers
+            TMEM_LD32(lane_base, x);
+            TMEM_LD32(lane_base + 32, (x + 32));
+            TMEM_LD32(lane_base + 64, (x + 64));
+            TMEM_LD32(lane_base + 96, (x + 96));
+            tmem_wait_ld();
+            if (k0 + CT_BK - 1 > first_masked) {
+#pragma unroll
+                for (int u = 0; u < CT_BK; ++u)
+                    if (k0 + u > qpos) x[u] = 0xFF800000u;
+            }
             float mt = -INFINITY;
 #pragma unroll
-            for (int cc = 0; cc < 4; ++cc) {
-                uint32_t x[32];
-                TMEM_LD32(lane_base + cc * 32, x);
-                tmem_wait_ld();
-                if (masked) {
+            for (int pg = 0; pg < 8; ++pg) {
+                float a[4];
 #pragma unroll
-                    for (int u = 0; u < 32; ++u)
-                        if (k0 + cc * 32 + u > qpos) x[u] = 0xFF800000u;
-                }
+                for (int u = 0; u < 4; ++u) a[u] = __uint_as_float(x[16 * pg + u]);
 #pragma unroll
-                for (int pg = 0; pg < 2; ++pg) {
-                    float a[4];
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) a[u] = __uint_as_float(x[16 * pg + u]);
-#pragma unroll
-                    for (int u = 4; u < 16; ++u) a[u & 3] = fmaxf(a[u & 3], __uint_as_float(x[16 * pg + u]));
-                    const float2 sc = scl[2 * cc + pg];
-                    const float m = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
-                    mt = fmaxf(mt, m == -INFINITY ? m : fmaf(m, qmul * sc.x, sc.y));
-                }
+                for (int u = 4; u < 16; ++u) a[u & 3] = fmaxf(a[u & 3], __uint_as_float(x[16 * pg + u]));
+                const float2 sc = scl[pg];
+                mt = fmaxf(mt, fmaf(fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])), qmul * sc.x, sc.y));
             }
             const bool move = mt > R + KV8_SLACK;
             if (__any_sync(0xffffffffu, move)) {
@@ -1000,13 +1030,13 @@ __global__ void __launch_bounds__(CT_THREADS, 2) k_kv8_chunk(const __grid_consta
                 l *= al;
                 if (i > 0) {  // P V of the tile before has finished: S of this one was issued after it
 #pragma unroll 1
-                    for (int cc = 0; cc < HD / 32; ++cc) {
-                        uint32_t x[32];
-                        TMEM_LD32(lane_base + CT_O + cc * 32, x);
+                    for (int cc = 0; cc < HD / 8; ++cc) {
+                        uint32_t y[8];
+                        TMEM_LD8(lane_base + CT_O + cc * 8, y);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int u = 0; u < 32; ++u) x[u] = __float_as_uint(__uint_as_float(x[u]) * al);
-                        TMEM_ST32(lane_base + CT_O + cc * 32, x);
+                        for (int u = 0; u < 8; ++u) y[u] = __float_as_uint(__uint_as_float(y[u]) * al);
+                        TMEM_ST8(lane_base + CT_O + cc * 8, y);
                     }
                 }
             }
@@ -1014,30 +1044,18 @@ __global__ void __launch_bounds__(CT_THREADS, 2) k_kv8_chunk(const __grid_consta
             for (int half = 0; half < 2; ++half) {
                 uint32_t h[32];
 #pragma unroll
-                for (int c2 = 0; c2 < 2; ++c2) {
-                    const int cc = half * 2 + c2;
-                    uint32_t x[32];
-                    TMEM_LD32(lane_base + cc * 32, x);
-                    tmem_wait_ld();
-                    if (masked) {
+                for (int pg = 0; pg < 4; ++pg) {
+                    const float2 sc = scl[half * 4 + pg];
+                    const float f = qmul * sc.x, a = sc.y - R + KV8_LIFT;
+                    float sum[2] = {0.f, 0.f};
 #pragma unroll
-                        for (int u = 0; u < 32; ++u)
-                            if (k0 + cc * 32 + u > qpos) x[u] = 0xFF800000u;
+                    for (int u = 0; u < 8; ++u) {
+                        const float e0 = ex2(fmaf(__uint_as_float(x[64 * half + 16 * pg + 2 * u]), f, a));
+                        const float e1 = ex2(fmaf(__uint_as_float(x[64 * half + 16 * pg + 2 * u + 1]), f, a));
+                        sum[u & 1] += e0 + e1;
+                        h[pg * 8 + u] = pack_h2(e0, e1);
                     }
-#pragma unroll
-                    for (int pg = 0; pg < 2; ++pg) {
-                        const float2 sc = scl[2 * cc + pg];
-                        const float f = qmul * sc.x, a = sc.y - R + KV8_LIFT;
-                        float sum[2] = {0.f, 0.f};
-#pragma unroll
-                        for (int u = 0; u < 8; ++u) {
-                            const float e0 = ex2(fmaf(__uint_as_float(x[16 * pg + 2 * u]), f, a));
-                            const float e1 = ex2(fmaf(__uint_as_float(x[16 * pg + 2 * u + 1]), f, a));
-                            sum[u & 1] += e0 + e1;
-                            h[c2 * 16 + pg * 8 + u] = pack_h2(e0, e1);
-                        }
-                        l = fmaf(sum[0] + sum[1], kv8_pow2(-(int)sc.y), l);
-                    }
+                    l = fmaf(sum[0] + sum[1], kv8_pow2(-(int)sc.y), l);
                 }
                 TMEM_ST32(lane_base + half * 32, h);
             }
@@ -1059,16 +1077,25 @@ __global__ void __launch_bounds__(CT_THREADS, 2) k_kv8_chunk(const __grid_consta
         if (good && wwait(pv_done, j1 - j0 - 1)) {
             tc_fence_after();
             const float inv = P.splits == 1 ? 1.f / l : 1.f;
+            // With the whole row at hand the output goes through the warp's rows of the Q operand (no MMA
+            // reads it any more), so that stores cover whole rows; partials are the thread's own.
 #pragma unroll 1
             for (int cc = 0; cc < HD / 32; ++cc) {
                 uint32_t x[32];
                 TMEM_LD32(lane_base + CT_O + cc * 32, x);
                 tmem_wait_ld();
-                if (valid && P.splits == 1) {
-                    float v[32];
+                if (P.splits == 1) {
 #pragma unroll
-                    for (int u = 0; u < 32; ++u) v[u] = __uint_as_float(x[u]) * inv;
-                    store_row<DT, 16>(p.out, (size_t)tok * p.ld_out + (size_t)hq * HD + cc * 32, v);
+                    for (int u = 0; u < 4; ++u) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float e0 = __uint_as_float(x[8 * u + 2 * k]) * inv, e1 = __uint_as_float(x[8 * u + 2 * k + 1]) * inv;
+                            w[k] = DT == QW_F16 ? pack_h2(e0, e1) : pack_bf2(e0, e1);
+                        }
+                        const int ch = cc * 4 + u;
+                        sts128(qa + (ch >> 3) * CT_SUB + r * 128 + (((ch & 7) ^ (r & 7)) << 4), w[0], w[1], w[2], w[3]);
+                    }
                 } else if (valid) {
                     float* dst = P.part_o + (part * CT_ROWS + r) * HD + cc * 32;
 #pragma unroll
@@ -1076,6 +1103,16 @@ __global__ void __launch_bounds__(CT_THREADS, 2) k_kv8_chunk(const __grid_consta
                         *reinterpret_cast<uint4*>(dst + u) = make_uint4(x[u], x[u + 1], x[u + 2], x[u + 3]);
                 }
                 __syncwarp();
+            }
+            if (P.splits == 1) {
+                constexpr int LPR = HD / 8;
+                const int ch = lane % LPR;
+                for (int rr = warp * 32 + lane / LPR; rr < warp * 32 + 32 && row0 + rr < rows; rr += 32 / LPR) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(sm + (ch >> 3) * CT_SUB + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4));
+                    const int tk = row_token(p, row0 + rr);
+                    *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + (size_t)(r0 + tk) * p.ld_out +
+                                              (size_t)(head * p.G + row0 + rr - tk * p.G) * HD + ch * 8) = v;
+                }
             }
             if (valid && P.splits == 1) {
                 const float z = log2f(l) + R - KV8_LIFT;
@@ -1220,45 +1257,32 @@ __global__ void __launch_bounds__(CT_THREADS, 2) k_kv8_score(const __grid_consta
                 sts128(at + (((c0 + 1) ^ (row & 7)) << 4), kv8_dec2(v.z & 0xFFFFu), kv8_dec2(v.z >> 16), kv8_dec2(v.w & 0xFFFFu), kv8_dec2(v.w >> 16));
             }
         }
+        auto row_lse = [&](int rt) {
+            const int row = min(rt * CT_ROWS + t, rows - 1), tok = row_token(p, row);
+            return p.lse2[(size_t)(r0 + tok) * p.n_heads + head * p.G + row - tok * p.G];
+        };
+        QTile<HD> qt;
+        fetch_q<HD>(qt, p, r0, head, t0 * CT_ROWS, rows, warp - 4, lane);
+        float z = row_lse(t0);
         for (int rt = t0, i = 0; rt < t1; ++rt, ++i) {
-            const int buf = i & 1, row = rt * CT_ROWS + t;
+            const int buf = i & 1;
+            // thread's row of the tile: what the sums need of it
+            const int row = rt * CT_ROWS + t;
             const bool v = row < rows;
-            const int tok = r0 + (v ? row / p.G : 0), hq = head * p.G + (v ? row % p.G : 0);
-            const uint16_t* src = reinterpret_cast<const uint16_t*>(p.q) + (size_t)tok * p.ld_q + (size_t)hq * HD;
-            uint4 x[HD / 8];
-#pragma unroll
-            for (int ch = 0; ch < HD / 8; ++ch) x[ch] = *reinterpret_cast<const uint4*>(src + ch * 8);
-            const float z = p.lse2[(size_t)tok * p.n_heads + hq];
-            float mul = 1.f;
-            if (DT == QW_BF16) {  // as load_q
-                float am = 0.f;
-#pragma unroll
-                for (int ch = 0; ch < HD / 8; ++ch) {
-                    const uint32_t w[4] = {x[ch].x, x[ch].y, x[ch].z, x[ch].w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) am = fmaxf(am, fmaxf(fabsf(bf_lo(w[k])), fabsf(bf_hi(w[k]))));
-                }
-                const int e = min(max(kv8_log2(am), -100), 100);
-                mul = kv8_pow2(e);
-                const float inv = kv8_pow2(-e);
-#pragma unroll
-                for (int ch = 0; ch < HD / 8; ++ch) {
-                    x[ch].x = pack_h2(bf_lo(x[ch].x) * inv, bf_hi(x[ch].x) * inv);
-                    x[ch].y = pack_h2(bf_lo(x[ch].y) * inv, bf_hi(x[ch].y) * inv);
-                    x[ch].z = pack_h2(bf_lo(x[ch].z) * inv, bf_hi(x[ch].z) * inv);
-                    x[ch].w = pack_h2(bf_lo(x[ch].w) * inv, bf_hi(x[ch].w) * inv);
-                }
-            }
+            const int tok = v ? row_token(p, row) : 0;
             if (i >= 2 && !__all_sync(0xffffffffu, wait(q_empty + buf, (i >> 1) - 1))) {
                 *abort_flag = 1;
                 break;
             }
-            const uint32_t at = smem_u32(sm + Cs<HD>::OFF_Q + buf * MAT) + t * 128;
-#pragma unroll
-            for (int ch = 0; ch < HD / 8; ++ch)
-                sts128(at + (ch >> 3) * CT_SUB + (((ch & 7) ^ (t & 7)) << 4), x[ch].x, x[ch].y, x[ch].z, x[ch].w);
-            // [i % 4]: the tile four before has been summed, as S^T of the tile two before was issued
-            rowc[(i & 3) * CT_ROWS + t] = make_float4(mul * p.scale_log2, z, __int_as_float(v ? s + row / p.G : -1), 0.f);
+            // rowc[i % 4]: the tile four before has been summed, as S^T of the tile two before was issued
+            float4* rc = rowc + (i & 3) * CT_ROWS;
+            store_q<HD, DT>(qt, warp - 4, lane, smem_u32(sm + Cs<HD>::OFF_Q + buf * MAT), [&](int r, float mul) { rc[r].x = mul * p.scale_log2; });
+            rc[t].y = z;
+            rc[t].z = __int_as_float(v ? s + tok : -1);
+            if (rt + 1 < t1) {  // the next tile is on its way while this one is multiplied
+                fetch_q<HD>(qt, p, r0, head, (rt + 1) * CT_ROWS, rows, warp - 4, lane);
+                z = row_lse(rt + 1);
+            }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(q_full + buf));
@@ -1447,7 +1471,7 @@ cudaError_t run_attn(const Kv8AttnP& p, const Plan& q, int B, char* ws, cudaStre
     P.part_ml = (float*)(ws + q.off_ml);
     P.tiles = q.tiles;
     if ((e = allow_smem(k_kv8_chunk<HD, DT>, Ct<HD>::SMEM)) != cudaSuccess) return e;
-    e = launch_k(c, k_kv8_chunk<HD, DT>, dim3(q.tiles * q.splits, p.kv.n_kv, B), dim3(CT_THREADS), (size_t)Ct<HD>::SMEM, P);
+    e = launch_k(c, k_kv8_chunk<HD, DT>, dim3(p.kv.n_kv, B, q.tiles * q.splits), dim3(CT_THREADS), (size_t)Ct<HD>::SMEM, P);
     if (e == cudaSuccess && q.splits > 1)
         e = launch_k(c, k_kv8_chunk_combine<HD, DT>, dim3(q.tiles * CT_ROWS / 8, p.kv.n_kv, B), dim3(256), 0, P);
     return e == cudaSuccess && p.score_out ? run_score<HD, DT>(p, B, st) : e;
@@ -1464,6 +1488,8 @@ static qw_status attn_sizes(const qw_kv8* kv, int B, int T, int max_len, int max
         return qw_fail(QW_ERR_INVALID_ARG, "attn: n_heads is not a multiple of n_kv_heads");
     if ((long long)B * ((max_keys + 15) / 16) * kv->n_kv_heads > 0x7fffffffll)
         return qw_fail(QW_ERR_UNSUPPORTED, "attn: B * max_keys * n_kv_heads too large");
+    if ((long long)std::min(max_len, T) * (n_heads / kv->n_kv_heads) >= 1ll << 28)
+        return qw_fail(QW_ERR_UNSUPPORTED, "attn: more than 2^28 query rows of one KV head");
     if (n_heads / kv->n_kv_heads > 16) return qw_fail(QW_ERR_UNSUPPORTED, "attn: more than 16 query heads per KV head");
     return QW_OK;
 }
@@ -1503,6 +1529,7 @@ extern "C" qw_status qw_kv8_attn(const qw_kv8* kv, const qw_kv8_attn_args* a, vo
     p.max_keys = a->max_keys;
     p.n_heads = a->n_heads;
     p.G = a->n_heads / kv->n_kv_heads;
+    p.gmul = p.G == 1 ? 0u : (uint32_t)(((1ull << 32) + p.G - 1) / p.G);
     p.scale_log2 = a->scale * KV8_LOG2E;
     p.out = a->dev_out;
     p.ld_out = a->ld_out;
