@@ -700,32 +700,45 @@ __global__ void __launch_bounds__(KD_WARPS * 32) k_kv8_combine(const __grid_cons
 // =======================================================================================
 // k_kv8_chunk: many query rows (prompts and chunks of them) on tcgen05.
 //
-// A CTA takes 128 rows of one (entry, KV head): rows are (token, head of the group) pairs, token
-// major, so any group size fills the MMA. Per tile of 128 keys (8 pages):
-//   converters (4 warps): codes -> fp16 operands in shared memory, K and V alike as [key][dim] rows
-//                  in the 128-byte swizzle; the next tile's codes are already in registers;
-//   S = Q K^T      S in TMEM (128 columns); a thread of the first softmax warp issues the MMAs
-//                  (8 warps a CTA leave each thread 128 registers with two CTAs an SM);
-//   softmax        four warps, thread = row = TMEM lane; the page scales enter the exponent's FMA;
-//                  P (fp16) overwrites the first half of S;
-//   O += P V       A = P from TMEM, B = V, O in TMEM (HD columns).
-// Tensor work bounds long chunks: 2 * 128 * 128 * HD MACs a tile against ~5 instructions and one
-// exponential per score. 96 KB of shared memory and 256 TMEM columns let two CTAs share an SM, so
-// one's softmax overlaps the other's MMAs without a second copy of anything. When the rows give
-// too few CTAs, the keys are split (`splits`) and k_kv8_chunk_combine adds the partials in order.
-// Every wait is bounded.
+// A CTA takes two tiles of 128 rows of one (entry, KV head): rows are (token, head of the group)
+// pairs, token major, so any group size fills the MMA. Per step of 128 keys (8 pages):
+//   copies         a lane a page brings the codes with bulk copies through a ring (a block's K and
+//                  its V are contiguous, so no tensor map is needed) and the page's scales;
+//   converters     four warps: codes -> fp16 operands for both row tiles, K and V alike as
+//                  [key][dim] rows in the 128-byte swizzle;
+//   S = Q K^T      S in TMEM, 128 columns a row tile;
+//   softmax        four warps a row tile, thread = row = TMEM lane, its 128 scores in registers;
+//                  the page scales enter the exponent's FMA, P (fp16) overwrites half of S;
+//   O += P V       A = P from TMEM, B = V, O in TMEM.
+// Each row tile has its own issuing warp and its own chain S -> softmax -> P V -> S; the other
+// tile's chain fills the tensor pipe meanwhile. What bounds it is that chain and the hand-overs
+// between its warps (~0.1 us each), not the pipe: so steps are as large as TMEM allows (64-key
+// steps with two CTAs an SM took 1.4x longer a key). Registers go by role (setmaxnreg). When the
+// rows give too few CTAs, the keys are split (`splits`) and k_kv8_chunk_combine adds the partials in
+// order. Every wait is bounded.
 // =======================================================================================
-constexpr int CT_WARPS = 8, CT_THREADS = CT_WARPS * 32;  // 0-3 softmax (0 issues the MMAs), 4-7 converters
+constexpr int CT_THREADS = 512;        // warps 0-3, 4-7 softmax; 8-11 converters; 12, 13 MMA; 14 copies; 15 idle
+constexpr int CT_REGS = 128;           // a thread's at launch: 512 x 128 = 128 x (176 + 176 + 104 + 56)
 constexpr int CT_BK = 128, CT_ROWS = 128;
 constexpr int CT_SUB = 128 * 128;      // [128 rows][64 dims] fp16, swizzled
-constexpr int CT_TMEM = 256, CT_O = 128;
+constexpr int CT_TMEM = 512, CT_O = 256;
 
 template <int HD>
 struct Ct {
-    static constexpr int MAT = CT_SUB * (HD / 64);
-    static constexpr int OFF_K = MAT, OFF_V = 2 * MAT, OFF_MUL = 3 * MAT, OFF_BAR = OFF_MUL + CT_ROWS * 4;
-    static constexpr int SMEM = 1024 + OFF_BAR + 512;
+    static constexpr int MAT = CT_SUB * (HD / 64), RAW = CT_BK * HD;
+    static constexpr int RING = HD == 128 ? 5 : 8;  // code tiles (K or V) in flight
+    static constexpr int OFF_K = 2 * MAT, OFF_V = 3 * MAT, OFF_R = 4 * MAT;
+    static constexpr int OFF_MUL = OFF_R + RING * RAW, OFF_SC = OFF_MUL + 2 * CT_ROWS * 4, OFF_BAR = OFF_SC + 8 * 8 * 16;
+    static constexpr int SMEM = 1024 + OFF_BAR + 256;
 };
+
+// mbar_wait that looks at the clock only after 64 failed tries.
+__device__ __forceinline__ bool ct_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+#pragma unroll 1
+    for (int n = 0; n < 64; ++n)
+        if (mbar_try_wait(bar, parity)) return true;
+    return mbar_wait(bar, parity, abort_flag);
+}
 
 struct Kv8ChunkP {
     Kv8AttnP a;
@@ -735,6 +748,45 @@ struct Kv8ChunkP {
     int tiles;
 };
 
+__device__ __forceinline__ float fl(uint32_t x) { return __uint_as_float(x); }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// pairs of fp32 in one 64-bit register: one instruction for two operations
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t pack2u(uint32_t a, uint32_t b) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -792,27 +844,27 @@ __device__ __forceinline__ void store_q(QTile<HD>& q, int w, int lane, uint32_t 
 }
 
 template <int HD, int DT>
-__global__ void __launch_bounds__(CT_THREADS, 2) k_kv8_chunk(const __grid_constant__ Kv8ChunkP P) {
+__global__ void __launch_bounds__(CT_THREADS, 1) k_kv8_chunk(const __grid_constant__ Kv8ChunkP P) {
     const Kv8AttnP& p = P.a;
-    constexpr int NSUB = HD / 64, CH = HD / 16, RP = 128 / CH, NP = CT_BK / RP;
+    constexpr int NSUB = HD / 64, CH = HD / 16, RP = 128 / CH, NU = CT_BK / RP, MAT = Ct<HD>::MAT, RAW = Ct<HD>::RAW, RING = Ct<HD>::RING;
     extern __shared__ uint8_t ct_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ct_raw) + 1023) & ~(uintptr_t)1023);
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Ct<HD>::OFF_BAR);
-    uint64_t *k_full = bars, *v_full = bars + 1, *k_empty = bars + 2, *pv_done = bars + 3, *s_full = bars + 4, *p_full = bars + 5,
-             *q_ready = bars + 6, *mma_fin = bars + 7;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 8);
+    uint64_t *r_full = bars, *r_empty = bars + 8, *k_full = bars + 16, *k_empty = bars + 17, *v_full = bars + 18, *v_empty = bars + 19,
+             *s_full = bars + 20, *p_full = bars + 22, *pv_done = bars + 24, *q_ready = bars + 26, *mma_fin = bars + 28;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 30);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    float2* scales = reinterpret_cast<float2*>(bars + 10);  // [2][8]: 2^ek and ev of the tile's pages
+    float4* scales = reinterpret_cast<float4*>(sm + Ct<HD>::OFF_SC);  // [8][8]: 2^ek, ev, 2^-ev of the pages of step i % 8
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int b = blockIdx.y, head = blockIdx.x;
-    const int tile = P.tiles - 1 - (int)(blockIdx.z / P.splits), split = blockIdx.z % P.splits;  // the longest rows start first
-    const int row0 = tile * CT_ROWS;
+    const int tile = (P.tiles + 1) / 2 - 1 - (int)(blockIdx.z / P.splits), split = blockIdx.z % P.splits;  // the longest rows start first
+    const int row0 = tile * 2 * CT_ROWS;
     int s, r0, n;
     if (!attn_entry(p, b, s, r0, n)) {
         if (threadIdx.x == 0) atomicOr(p.status, QW_KV8_BAD_POS);
         if (split || r0 < 0 || n < 0 || n > p.max_len || r0 > p.T - n) return;
         const int rows = n * p.G;
-        for (int x = threadIdx.x; x < CT_ROWS * (HD / 8); x += CT_THREADS) {
+        for (int x = threadIdx.x; x < 2 * CT_ROWS * (HD / 8); x += CT_THREADS) {
             const int r = row0 + x / (HD / 8);
             if (r >= rows) break;
             *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + (size_t)(r0 + r / p.G) * p.ld_out +
@@ -822,31 +874,41 @@ __global__ void __launch_bounds__(CT_THREADS, 2) k_kv8_chunk(const __grid_consta
     }
     const int rows = n * p.G;
     if (row0 >= rows) return;
-    const int kend = s + (min(row0 + CT_ROWS, rows) - 1) / p.G + 1;  // keys the tile's last row sees
+    const int n_rt = row0 + CT_ROWS < rows ? 2 : 1;                      // row tiles with rows
+    const int kend = s + (min(row0 + 2 * CT_ROWS, rows) - 1) / p.G + 1;  // keys the last row sees
     const int n_kt = (kend + CT_BK - 1) / CT_BK;
-    const int j0 = (int)((long long)n_kt * split / P.splits), j1 = (int)((long long)n_kt * (split + 1) / P.splits);
-    const size_t part = (((size_t)b * p.kv.n_kv + head) * P.tiles + tile) * P.splits + split;
-    if (j0 == j1) {  // nothing to add
-        if (threadIdx.x < CT_ROWS) {
-            P.part_ml[(part * CT_ROWS + threadIdx.x) * 2] = -1e30f;
-            P.part_ml[(part * CT_ROWS + threadIdx.x) * 2 + 1] = 0.f;
+    const int j0 = (int)((long long)n_kt * split / P.splits), j1 = (int)((long long)n_kt * (split + 1) / P.splits), nt = j1 - j0;
+    // partials of row tile t: part(t) [128 rows]
+    auto part = [&](int t) { return (((size_t)b * p.kv.n_kv + head) * P.tiles + 2 * tile + t) * P.splits + split; };
+    if (nt == 0) {  // nothing to add
+        const int t = threadIdx.x / CT_ROWS;
+        if (t < n_rt) {
+            P.part_ml[(part(t) * CT_ROWS + threadIdx.x % CT_ROWS) * 2] = -1e30f;
+            P.part_ml[(part(t) * CT_ROWS + threadIdx.x % CT_ROWS) * 2 + 1] = 0.f;
         }
         return;
     }
-    auto wait = [&](uint64_t* bar, int parity) { return mbar_wait(smem_u32(bar), (uint32_t)parity & 1u, abort_flag); };
     if (threadIdx.x == 0) {
+        for (int i = 0; i < RING; ++i) {
+            mbar_init(smem_u32(r_full + i), 1);
+            mbar_init(smem_u32(r_empty + i), 4);
+        }
         mbar_init(smem_u32(k_full), 4);
+        mbar_init(smem_u32(k_empty), n_rt);
         mbar_init(smem_u32(v_full), 4);
-        mbar_init(smem_u32(k_empty), 1);
-        mbar_init(smem_u32(pv_done), 1);
-        mbar_init(smem_u32(s_full), 1);
-        mbar_init(smem_u32(p_full), 4);
-        mbar_init(smem_u32(q_ready), 4);
-        mbar_init(smem_u32(mma_fin), 1);
+        mbar_init(smem_u32(v_empty), n_rt);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(s_full + i), 1);
+            mbar_init(smem_u32(p_full + i), 4);
+            mbar_init(smem_u32(pv_done + i), 1);
+            mbar_init(smem_u32(q_ready + i), 4);
+            mbar_init(smem_u32(mma_fin + i), 1);
+        }
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
-    if (warp == 4) {
+    if (warp == 12) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(CT_TMEM)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -855,281 +917,324 @@ __global__ void __launch_bounds__(CT_THREADS, 2) k_kv8_chunk(const __grid_consta
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    // warp-uniform outcome of a bounded wait
+    auto wait = [&](uint64_t* bar, int parity) {
+        return __all_sync(0xffffffffu, ct_wait(smem_u32(bar), (uint32_t)parity & 1u, abort_flag));
+    };
 
-    if (warp >= 4) {
-        // ---------------- converters ----------------
-        // 88 registers a thread here and 168 for the softmax rows: the 128 of the launch, split again
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-        // Thread (row, pos) of a pass of RP rows takes 16 codes at 16-byte position pos of its row.
-        const int t = threadIdx.x - 4 * 32, pos = t % CH, prow = t / CH;
-        const int* table = p.kv.table + (size_t)b * p.kv.max_pages;
-        const int key_pages = (kend + KV8_PAGE - 1) / KV8_PAGE;
-        // lane l < 8 of each warp: block of the tile's page l
-        auto block_of = [&](int j) -> const uint8_t* {
-            const int pi = j * 8 + (lane & 7);
-            if (j >= j1 || pi >= key_pages) return nullptr;
-            int id = table[pi];
-            if (id < 0 || id >= p.kv.n_pages) {
-                atomicOr(p.status, QW_KV8_BAD_POS);
-                id = 0;
-            }
-            return p.kv.blocks + ((size_t)id * p.kv.n_kv + head) * Kv8<HD>::BLK;
-        };
-        uint4 kr[NP], vr[NP];
-        auto load = [&](const uint8_t* blk, int j, uint4* r, int off) {
-#pragma unroll
-            for (int i = 0; i < NP; ++i) {
-                const int row = prow + i * RP;
-                const uint8_t* base = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, (unsigned long long)blk, row >> 4));
-                // rows past the keys are zeros: weight 0 must add exactly 0
-                r[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (j * CT_BK + row < kend) r[i] = *reinterpret_cast<const uint4*>(base + off + (row & 15) * HD + pos * 16);
-            }
-        };
-        auto store = [&](const uint4* r, uint32_t mat, bool is_v) {
-#pragma unroll
-            for (int i = 0; i < NP; ++i) {
-                const int row = prow + i * RP, tk = row & 15;
-                const int ch = is_v ? kv8_v_pos<HD>(tk, pos) : kv8_k_pos<HD>(tk, pos);  // its own inverse
-                const uint32_t at = mat + (ch >> 2) * CT_SUB + row * 128;
-                const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
-                uint32_t h[8];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    h[2 * k] = kv8_dec2(w[k] & 0xFFFFu);
-                    h[2 * k + 1] = kv8_dec2(w[k] >> 16);
+    if (warp >= 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == 14) {
+            // ---------------- copies: lane l < 8 brings page l of each step ----------------
+            const int* table = p.kv.table + (size_t)b * p.kv.max_pages;
+            const int key_pages = (kend + KV8_PAGE - 1) / KV8_PAGE;
+            bool ok = true;
+            int st = 0, use = 0, issued = 0;  // ring stage and its use count
+            auto block_of = [&](int i) -> const uint8_t* {
+                const int pi = (j0 + i) * 8 + lane;
+                if (lane >= 8 || i >= nt || pi >= key_pages) return nullptr;
+                int id = table[pi];
+                if (id < 0 || id >= p.kv.n_pages) {
+                    atomicOr(p.status, QW_KV8_BAD_POS);
+                    id = 0;
                 }
-                // the second 64 dims start with their odd chunk, so 8 lanes of a row meet 8 positions
-                const bool odd = HD == 128 && (ch & 4);
-                const int c0 = 2 * (ch & 3);
-                sts128(at + (((c0 + odd) ^ (row & 7)) << 4), odd ? h[4] : h[0], odd ? h[5] : h[1], odd ? h[6] : h[2], odd ? h[7] : h[3]);
-                sts128(at + (((c0 + !odd) ^ (row & 7)) << 4), odd ? h[0] : h[4], odd ? h[1] : h[5], odd ? h[2] : h[6], odd ? h[3] : h[7]);
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-        };
-        const uint8_t* blk = block_of(j0);
-        const uint8_t* nxt = block_of(j0 + 1);
-        float2 sc = make_float2(1.f, 1.f);  // of no page: masked scores stay -inf
-        auto load_scales = [&](const uint8_t* bl) {
-            if (warp == 4 && lane < 8) sc = bl ? *reinterpret_cast<const float2*>(bl + Kv8<HD>::SOFF) : make_float2(1.f, 1.f);
-        };
-        load(blk, j0, kr, 0);
-        load_scales(blk);
-        load(blk, j0, vr, Kv8<HD>::VOFF);
-        for (int j = j0, i = 0; j < j1; ++j, ++i) {
-            if (i && !__all_sync(0xffffffffu, wait(k_empty, i - 1))) {
-                *abort_flag = 1;
-                break;
-            }
-            if (warp == 4 && lane < 8) scales[(i & 1) * 8 + lane] = make_float2(sc.x, (float)kv8_log2(sc.y));
-            store(kr, smem_u32(sm + Ct<HD>::OFF_K), false);
-            if (lane == 0) mbar_arrive(smem_u32(k_full));
-            if (j + 1 < j1) {
-                load(nxt, j + 1, kr, 0);
-                load_scales(nxt);
-            }
-            if (i && !__all_sync(0xffffffffu, wait(pv_done, i - 1))) {
-                *abort_flag = 1;
-                break;
-            }
-            store(vr, smem_u32(sm + Ct<HD>::OFF_V), true);
-            if (lane == 0) mbar_arrive(smem_u32(v_full));
-            if (j + 1 < j1) load(nxt, j + 1, vr, Kv8<HD>::VOFF);
-            nxt = block_of(j + 2);
-        }
-    } else {
-        // ---------------- softmax / output: thread = row = TMEM lane ----------------
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
-        const int r = threadIdx.x, row = row0 + r;
-        const bool valid = row < rows;
-        const int qt_ = valid ? row_token(p, row) : 0;
-        const int tok = r0 + qt_, hq = head * p.G + (valid ? row - qt_ * p.G : 0);
-        const int qpos = valid ? s + qt_ : -1;
-        const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
-        auto wwait = [&](uint64_t* bar, int parity) { return __all_sync(0xffffffffu, wait(bar, parity)); };
-        float* muls = reinterpret_cast<float*>(sm + Ct<HD>::OFF_MUL);  // written and read by the same warp
-        {
-            QTile<HD> qt;
-            fetch_q<HD>(qt, p, r0, head, row0, rows, warp, lane);
-            store_q<HD, DT>(qt, warp, lane, smem_u32(sm), [&](int rr, float mul) { muls[rr] = mul; });
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(q_ready));
-        const float qmul = p.scale_log2 * muls[r];
-        // Thread 0 issues the MMAs between its softmax tiles. S of tile i overwrites the columns of
-        // P of tile i - 1, so it waits until that tile's P V has finished.
-        const uint32_t qa = smem_u32(sm), ka = smem_u32(sm + Ct<HD>::OFF_K), va = smem_u32(sm + Ct<HD>::OFF_V);
-        auto issue_s = [&](int i) {
-            if (!(i ? wait(pv_done, i - 1) : wait(q_ready, 0)) || !wait(k_full, i)) {
-                *abort_flag = 1;
-                return;
-            }
-            tc_fence_after();
-#pragma unroll
-            for (int sub = 0; sub < NSUB; ++sub)
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    umma_f16(tmem, sw128_desc(qa + sub * CT_SUB) + 2 * kk, sw128_desc(ka + sub * CT_SUB) + 2 * kk,
-                             idesc_f16(128, CT_BK), (sub | kk) ? 1u : 0u);
-            umma_commit(smem_u32(s_full));
-            umma_commit(smem_u32(k_empty));
-        };
-        auto issue_pv = [&](int i) {
-            if (!wait(p_full, i) || !wait(v_full, i)) {
-                *abort_flag = 1;
-                return;
-            }
-            tc_fence_after();
-#pragma unroll
-            for (int kk = 0; kk < CT_BK / 16; ++kk)
-                umma_f16_ts(tmem + CT_O, tmem + kk * 8, sw128_desc_mn(va + kk * 16 * 128, CT_SUB), idesc_f16(128, HD) | kIdescBMajorMN,
-                            (i | kk) ? 1u : 0u);
-            umma_commit(smem_u32(pv_done));
-        };
-        float R = -1e30f, l = 0.f;
-        bool good = true;
-        const int first_masked = s + row0 / p.G;  // tiles that end at or before it need no mask
-        for (int j = j0, i = 0; j < j1; ++j, ++i) {
-            if (threadIdx.x == 0) issue_s(i);
-            __syncwarp();
-            if (!wwait(s_full, i)) {
-                good = false;
-                break;
-            }
-            tc_fence_after();
-            const float2* scl = scales + (i & 1) * 8;
-            const int k0 = j * CT_BK;
-            uint32_t x[CT_BK];  // the row's scores stay in registers
-            TMEM_LD32(lane_base, x);
-            TMEM_LD32(lane_base + 32, (x + 32));
-            TMEM_LD32(lane_base + 64, (x + 64));
-            TMEM_LD32(lane_base + 96, (x + 96));
-            tmem_wait_ld();
-            if (k0 + CT_BK - 1 > first_masked) {
-#pragma unroll
-                for (int u = 0; u < CT_BK; ++u)
-                    if (k0 + u > qpos) x[u] = 0xFF800000u;
-            }
-            float mt = -INFINITY;
-#pragma unroll
-            for (int pg = 0; pg < 8; ++pg) {
-                float a[4];
-#pragma unroll
-                for (int u = 0; u < 4; ++u) a[u] = __uint_as_float(x[16 * pg + u]);
-#pragma unroll
-                for (int u = 4; u < 16; ++u) a[u & 3] = fmaxf(a[u & 3], __uint_as_float(x[16 * pg + u]));
-                const float2 sc = scl[pg];
-                mt = fmaxf(mt, fmaf(fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])), qmul * sc.x, sc.y));
-            }
-            const bool move = mt > R + KV8_SLACK;
-            if (__any_sync(0xffffffffu, move)) {
-                const float al = move ? ex2(R - mt) : 1.f;
-                if (move) R = mt;
-                l *= al;
-                if (i > 0) {  // P V of the tile before has finished: S of this one was issued after it
-#pragma unroll 1
-                    for (int cc = 0; cc < HD / 8; ++cc) {
-                        uint32_t y[8];
-                        TMEM_LD8(lane_base + CT_O + cc * 8, y);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int u = 0; u < 8; ++u) y[u] = __float_as_uint(__uint_as_float(y[u]) * al);
-                        TMEM_ST8(lane_base + CT_O + cc * 8, y);
-                    }
+                return p.kv.blocks + ((size_t)id * p.kv.n_kv + head) * Kv8<HD>::BLK;
+            };
+            // of no page 1 and 1: masked scores stay -inf
+            auto scale_of = [&](const uint8_t* blk) {
+                return blk ? *reinterpret_cast<const float2*>(blk + Kv8<HD>::SOFF) : make_float2(1.f, 1.f);
+            };
+            auto put = [&](int i, const uint8_t* blk, bool is_v, float2 sc) {
+                if (use && !wait(r_empty + st, use - 1)) return false;
+                // [i % 8]: the ring is less than 5 steps deep, so the softmax of step i - 8 has passed
+                if (!is_v && lane < 8) {
+                    const int ev = kv8_log2(sc.y);
+                    scales[(i & 7) * 8 + lane] = make_float4(sc.x, (float)ev, kv8_pow2(-ev), 0.f);
                 }
-            }
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                uint32_t h[32];
-#pragma unroll
-                for (int pg = 0; pg < 4; ++pg) {
-                    const float2 sc = scl[half * 4 + pg];
-                    const float f = qmul * sc.x, a = sc.y - R + KV8_LIFT;
-                    float sum[2] = {0.f, 0.f};
-#pragma unroll
-                    for (int u = 0; u < 8; ++u) {
-                        const float e0 = ex2(fmaf(__uint_as_float(x[64 * half + 16 * pg + 2 * u]), f, a));
-                        const float e1 = ex2(fmaf(__uint_as_float(x[64 * half + 16 * pg + 2 * u + 1]), f, a));
-                        sum[u & 1] += e0 + e1;
-                        h[pg * 8 + u] = pack_h2(e0, e1);
-                    }
-                    l = fmaf(sum[0] + sum[1], kv8_pow2(-(int)sc.y), l);
+                __syncwarp();
+                const int n = min(8, key_pages - (j0 + i) * 8);  // pages of the step that hold keys
+                const uint32_t bar = smem_u32(r_full + st);
+                if (lane == 0) mbar_expect_tx(bar, n * KV8_PAGE * HD);
+                __syncwarp();
+                if (blk) bulk_copy(smem_u32(sm + Ct<HD>::OFF_R + st * RAW + lane * KV8_PAGE * HD), blk + (is_v ? Kv8<HD>::VOFF : 0), KV8_PAGE * HD, bar);
+                ++issued;
+                if (++st == RING) {
+                    st = 0;
+                    ++use;
                 }
-                TMEM_ST32(lane_base + half * 32, h);
+                return true;
+            };
+            const uint8_t* blk = block_of(0);
+            float2 sc = scale_of(blk);
+            for (int i = 0; i < nt && ok; ++i) {
+                const uint8_t* next = block_of(i + 1);
+                ok = put(i, blk, false, sc) && put(i, blk, true, sc);
+                blk = next;
+                sc = scale_of(blk);
             }
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(p_full));
-            if (threadIdx.x == 0) issue_pv(i);
-            __syncwarp();
-        }
-        if (threadIdx.x == 0) {
-            // the commits' asynchronous arrivals land before the CTA ends
-            umma_commit(smem_u32(mma_fin));
-            const uint64_t t0 = globaltimer_ns();
-            while (!mbar_try_wait(smem_u32(mma_fin), 0) && globaltimer_ns() - t0 < kTcWaitNs) {
-            }
-        }
-        __syncwarp();
-        if (good && wwait(pv_done, j1 - j0 - 1)) {
-            tc_fence_after();
-            const float inv = P.splits == 1 ? 1.f / l : 1.f;
-            // With the whole row at hand the output goes through the warp's rows of the Q operand (no MMA
-            // reads it any more), so that stores cover whole rows; partials are the thread's own.
-#pragma unroll 1
-            for (int cc = 0; cc < HD / 32; ++cc) {
-                uint32_t x[32];
-                TMEM_LD32(lane_base + CT_O + cc * 32, x);
-                tmem_wait_ld();
-                if (P.splits == 1) {
+            if (!ok) *abort_flag = 1;
+            // the copies issued land before the CTA ends
+            const uint64_t w0 = globaltimer_ns();
+            for (int i = max(0, issued - RING); i < issued; ++i)
+                while (!mbar_try_wait(smem_u32(r_full + i % RING), (i / RING) & 1) && globaltimer_ns() - w0 < kTcWaitNs) {
+                }
+        } else if (warp - 12 < n_rt) {
+            // ---------------- MMA issuer of row tile t: S_0, PV_0, S_1, PV_1, ... ----------------
+            // The whole warp walks the loop and one elected lane issues, so addresses and descriptors are
+            // the warp's. S_{i+1} overwrites the columns of P_i: it waits until P V of step i has finished.
+            const int t = warp - 12;
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0) + t * 128;
+            const uint64_t qd = sw128_desc(smem_u32(sm + t * MAT)), kd = sw128_desc(smem_u32(sm + Ct<HD>::OFF_K));
+            const uint64_t vd = sw128_desc_mn(smem_u32(sm + Ct<HD>::OFF_V), CT_SUB);
+            bool ok = wait(q_ready + t, 0);
+            for (int i = 0; i < nt && ok; ++i) {
+                if (!wait(k_full, i) || (i && !wait(pv_done + t, i - 1))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        uint32_t w[4];
+                    for (int sub = 0; sub < NSUB; ++sub)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float e0 = __uint_as_float(x[8 * u + 2 * k]) * inv, e1 = __uint_as_float(x[8 * u + 2 * k + 1]) * inv;
-                            w[k] = DT == QW_F16 ? pack_h2(e0, e1) : pack_bf2(e0, e1);
-                        }
-                        const int ch = cc * 4 + u;
-                        sts128(qa + (ch >> 3) * CT_SUB + r * 128 + (((ch & 7) ^ (r & 7)) << 4), w[0], w[1], w[2], w[3]);
-                    }
-                } else if (valid) {
-                    float* dst = P.part_o + (part * CT_ROWS + r) * HD + cc * 32;
+                        for (int kk = 0; kk < 4; ++kk)
+                            umma_f16(tm, qd + sub * (CT_SUB >> 4) + 2 * kk, kd + sub * (CT_SUB >> 4) + 2 * kk, idesc_f16(128, CT_BK),
+                                     (sub | kk) ? 1u : 0u);
+                    umma_commit(smem_u32(s_full + t));
+                    umma_commit(smem_u32(k_empty));
+                }
+                __syncwarp();
+                if (!wait(v_full, i) || !wait(p_full + t, i)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
-                    for (int u = 0; u < 32; u += 4)
-                        *reinterpret_cast<uint4*>(dst + u) = make_uint4(x[u], x[u + 1], x[u + 2], x[u + 3]);
+                    for (int kk = 0; kk < CT_BK / 16; ++kk)
+                        umma_f16_ts(tm + CT_O, tm + kk * 8, vd + kk * (16 * 128 >> 4), idesc_f16(128, HD) | kIdescBMajorMN,
+                                    (i | kk) ? 1u : 0u);
+                    umma_commit(smem_u32(pv_done + t));
+                    umma_commit(smem_u32(v_empty));
                 }
                 __syncwarp();
             }
-            if (P.splits == 1) {
-                constexpr int LPR = HD / 8;
-                const int ch = lane % LPR;
-                for (int rr = warp * 32 + lane / LPR; rr < warp * 32 + 32 && row0 + rr < rows; rr += 32 / LPR) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(sm + (ch >> 3) * CT_SUB + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4));
-                    const int tk = row_token(p, row0 + rr);
-                    *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + (size_t)(r0 + tk) * p.ld_out +
-                                              (size_t)(head * p.G + row0 + rr - tk * p.G) * HD + ch * 8) = v;
+            if (!ok) *abort_flag = 1;
+            // the commits' asynchronous arrivals land before the CTA ends
+            if (elect_one()) umma_commit(smem_u32(mma_fin + t));
+            __syncwarp();
+            const uint64_t w0 = globaltimer_ns();
+            while (!mbar_try_wait(smem_u32(mma_fin + t), 0) && globaltimer_ns() - w0 < kTcWaitNs) {
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 8) {
+        // ---------------- converters ----------------
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        // Thread t takes the 16 codes at 16-byte position t % CH of key rows t / CH + i RP: RP is 16 or 32,
+        // so its token within a page, and with it every swizzle, is the same for all i.
+        const int t = threadIdx.x - 8 * 32, prow = t / CH, pos = t % CH, tk = prow & 15;
+        // the two 16-byte chunks of 8 halves that a unit becomes; the second 64 dims start with their
+        // odd chunk, so 8 lanes of a row meet 8 positions
+        auto dest = [&](int ch, bool second) {
+            const int c = 2 * (ch & 3) + (second != (HD == 128 && (ch & 4) != 0));
+            return (uint32_t)((ch >> 2) * CT_SUB + prow * 128 + ((c ^ (prow & 7)) << 4));
+        };
+        const int kch = kv8_k_pos<HD>(tk, pos), vch = kv8_v_pos<HD>(tk, pos);  // the permutations are their own inverses
+        const uint32_t kd0 = smem_u32(sm + Ct<HD>::OFF_K) + dest(kch, false), kd1 = smem_u32(sm + Ct<HD>::OFF_K) + dest(kch, true);
+        const uint32_t vd0 = smem_u32(sm + Ct<HD>::OFF_V) + dest(vch, false), vd1 = smem_u32(sm + Ct<HD>::OFF_V) + dest(vch, true);
+        const bool kodd = HD == 128 && (kch & 4), vodd = HD == 128 && (vch & 4);
+        int st = 0, use = 0;
+        // one tile: waits for its codes and for the operand buffer, converts, hands both on
+        auto take = [&](int i, uint64_t* full, uint64_t* empty, uint32_t d0, uint32_t d1, bool odd) {
+            if (!wait(r_full + st, use)) return false;
+            const uint8_t* raw = sm + Ct<HD>::OFF_R + st * RAW + t * 16;
+            const int left = kend - (j0 + i) * CT_BK - prow;  // > u RP: the row holds a key
+            uint4 r[NU];
+#pragma unroll
+            for (int u = 0; u < NU; ++u) {
+                r[u] = *reinterpret_cast<const uint4*>(raw + u * RP * HD);
+                // rows past the keys are zeros: weight 0 must add exactly 0
+                if (left <= u * RP) r[u] = make_uint4(0u, 0u, 0u, 0u);
+            }
+            if (i && !wait(empty, i - 1)) return false;
+#pragma unroll
+            for (int u = 0; u < NU; ++u) {
+                const uint32_t a = odd ? r[u].z : r[u].x, a2 = odd ? r[u].w : r[u].y, c = odd ? r[u].x : r[u].z, c2 = odd ? r[u].y : r[u].w;
+                sts128(d0 + u * RP * 128, kv8_dec2(a & 0xFFFFu), kv8_dec2(a >> 16), kv8_dec2(a2 & 0xFFFFu), kv8_dec2(a2 >> 16));
+                sts128(d1 + u * RP * 128, kv8_dec2(c & 0xFFFFu), kv8_dec2(c >> 16), kv8_dec2(c2 & 0xFFFFu), kv8_dec2(c2 >> 16));
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(smem_u32(full));
+                mbar_arrive(smem_u32(r_empty + st));
+            }
+            if (++st == RING) {
+                st = 0;
+                ++use;
+            }
+            return true;
+        };
+        bool ok = true;
+        for (int i = 0; i < nt && ok; ++i) ok = take(i, k_full, k_empty, kd0, kd1, kodd) && take(i, v_full, v_empty, vd0, vd1, vodd);
+        if (!ok) *abort_flag = 1;
+    } else {
+        // ---------------- softmax / output: thread = row = TMEM lane of row tile t ----------------
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+        const int t = warp >> 2, wq = warp & 3, r = threadIdx.x & 127, rt0 = row0 + t * CT_ROWS, row = rt0 + r;
+        if (t < n_rt) {
+            const bool valid = row < rows;
+            const int qt_ = valid ? row_token(p, row) : 0;
+            const int tok = r0 + qt_, hq = head * p.G + (valid ? row - qt_ * p.G : 0);
+            const int qpos = valid ? s + qt_ : -1;
+            const uint32_t lane_base = tmem + t * 128 + ((uint32_t)(wq * 32) << 16), qa = smem_u32(sm + t * MAT);
+            float* muls = reinterpret_cast<float*>(sm + Ct<HD>::OFF_MUL) + t * CT_ROWS;  // written and read by the same warp
+            {
+                QTile<HD> qt;
+                fetch_q<HD>(qt, p, r0, head, rt0, rows, wq, lane);
+                store_q<HD, DT>(qt, wq, lane, qa, [&](int rr, float mul) { muls[rr] = mul; });
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(q_ready + t));
+            const float qmul = p.scale_log2 * muls[r];
+            float R = -1e30f, l = 0.f;
+            bool good = true;
+            const int first_masked = s + rt0 / p.G;  // steps that end at or before it need no mask
+            for (int i = 0; i < nt; ++i) {
+                const int k0 = (j0 + i) * CT_BK;
+                if (!wait(s_full + t, i)) {
+                    good = false;
+                    break;
                 }
+                tc_fence_after();
+                const float4* scl = scales + (i & 7) * 8;
+                uint32_t x[CT_BK];  // the row's scores stay in registers
+                TMEM_LD32(lane_base, x);
+                TMEM_LD32(lane_base + 32, (x + 32));
+                TMEM_LD32(lane_base + 64, (x + 64));
+                TMEM_LD32(lane_base + 96, (x + 96));
+                tmem_wait_ld();
+                if (k0 + CT_BK - 1 > first_masked) {
+#pragma unroll
+                    for (int u = 0; u < CT_BK; ++u)
+                        if (k0 + u > qpos) x[u] = 0xFF800000u;
+                }
+                float mt = -INFINITY;
+#pragma unroll
+                for (int pg = 0; pg < CT_BK / 16; ++pg) {
+                    const uint32_t* y = x + 16 * pg;  // three-way maxima
+                    const float m0 = max3(max3(fl(y[0]), fl(y[1]), fl(y[2])), fl(y[3]), fl(y[4]));
+                    const float m1 = max3(max3(fl(y[5]), fl(y[6]), fl(y[7])), fl(y[8]), fl(y[9]));
+                    const float m2 = max3(max3(fl(y[10]), fl(y[11]), fl(y[12])), fl(y[13]), fl(y[14]));
+                    const float4 sc = scl[pg];
+                    mt = fmaxf(mt, fmaf(max3(max3(m0, m1, m2), fl(y[15]), m0), qmul * sc.x, sc.y));
+                }
+                const bool move = mt > R + KV8_SLACK;
+                if (__any_sync(0xffffffffu, move)) {
+                    const float al = move ? ex2(R - mt) : 1.f;
+                    if (move) R = mt;
+                    l *= al;
+                    if (i > 0) {  // P V of the step before has finished: S of this one was issued after it
+#pragma unroll 1
+                        for (int cc = 0; cc < HD / 16; ++cc) {
+                            uint32_t y[16];
+                            TMEM_LD16(lane_base + CT_O + cc * 16, y);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int u = 0; u < 16; ++u) y[u] = __float_as_uint(__uint_as_float(y[u]) * al);
+                            TMEM_ST16(lane_base + CT_O + cc * 16, y);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t h[32];
+#pragma unroll
+                    for (int pg = 0; pg < 4; ++pg) {
+                        const float4 sc = scl[half * 4 + pg];
+                        const uint64_t f = pack2(qmul * sc.x, qmul * sc.x);
+                        const float a0 = sc.y - R + KV8_LIFT;
+                        const uint64_t a = pack2(a0, a0);
+                        uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) {
+                            const int at = 64 * half + 16 * pg + 2 * u;
+                            float t0, t1;
+                            unpack2(fma2(pack2u(x[at], x[at + 1]), f, a), t0, t1);
+                            const float e0 = ex2(t0), e1 = ex2(t1);
+                            sum[u & 1] = add2(sum[u & 1], pack2(e0, e1));
+                            h[pg * 8 + u] = pack_h2(e0, e1);
+                        }
+                        float s0, s1;
+                        unpack2(add2(sum[0], sum[1]), s0, s1);
+                        l = fmaf(s0 + s1, sc.z, l);
+                    }
+                    TMEM_ST32(lane_base + half * 32, h);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(p_full + t));
             }
-            if (valid && P.splits == 1) {
-                const float z = log2f(l) + R - KV8_LIFT;
-                if (p.lse2) p.lse2[(size_t)tok * p.n_heads + hq] = z;
-                if (p.lse) p.lse[(size_t)tok * p.n_heads + hq] = z * KV8_LN2;
-            } else if (valid) {
-                P.part_ml[(part * CT_ROWS + r) * 2] = R;
-                P.part_ml[(part * CT_ROWS + r) * 2 + 1] = l;
+            if (good && wait(pv_done + t, nt - 1)) {
+                tc_fence_after();
+                const float inv = P.splits == 1 ? 1.f / l : 1.f;
+                // With the whole row at hand the output goes through the warp's rows of the Q operand (no MMA
+                // reads it any more), so that stores cover whole rows; partials are the thread's own.
+#pragma unroll 1
+                for (int cc = 0; cc < HD / 32; ++cc) {
+                    uint32_t x[32];
+                    TMEM_LD32(lane_base + CT_O + cc * 32, x);
+                    tmem_wait_ld();
+                    if (P.splits == 1) {
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const float e0 = fl(x[8 * u + 2 * k]) * inv, e1 = fl(x[8 * u + 2 * k + 1]) * inv;
+                                w[k] = DT == QW_F16 ? pack_h2(e0, e1) : pack_bf2(e0, e1);
+                            }
+                            const int ch = cc * 4 + u;
+                            sts128(qa + (ch >> 3) * CT_SUB + r * 128 + (((ch & 7) ^ (r & 7)) << 4), w[0], w[1], w[2], w[3]);
+                        }
+                    } else if (valid) {
+                        float* dst = P.part_o + (part(t) * CT_ROWS + r) * HD + cc * 32;
+#pragma unroll
+                        for (int u = 0; u < 32; u += 4)
+                            *reinterpret_cast<uint4*>(dst + u) = make_uint4(x[u], x[u + 1], x[u + 2], x[u + 3]);
+                    }
+                    __syncwarp();
+                }
+                if (P.splits == 1) {
+                    constexpr int LPR = HD / 8;
+                    const int ch = lane % LPR;
+                    for (int rr = wq * 32 + lane / LPR; rr < wq * 32 + 32 && rt0 + rr < rows; rr += 32 / LPR) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(sm + t * MAT + (ch >> 3) * CT_SUB + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4));
+                        const int tk = row_token(p, rt0 + rr);
+                        *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + (size_t)(r0 + tk) * p.ld_out +
+                                                  (size_t)(head * p.G + rt0 + rr - tk * p.G) * HD + ch * 8) = v;
+                    }
+                }
+                if (valid && P.splits == 1) {
+                    const float z = log2f(l) + R - KV8_LIFT;
+                    if (p.lse2) p.lse2[(size_t)tok * p.n_heads + hq] = z;
+                    if (p.lse) p.lse[(size_t)tok * p.n_heads + hq] = z * KV8_LN2;
+                } else if (valid) {
+                    P.part_ml[(part(t) * CT_ROWS + r) * 2] = R;
+                    P.part_ml[(part(t) * CT_ROWS + r) * 2 + 1] = l;
+                }
+            } else {
+                *abort_flag = 1;
             }
-        } else {
-            *abort_flag = 1;
         }
     }
     tc_fence_before();
     __syncthreads();
     if (*abort_flag && threadIdx.x == 0) atomicOr(p.status, QW_KV8_TIMEOUT);
-    if (warp == 4) {
+    if (warp == 12) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(CT_TMEM) : "memory");
     }
@@ -1186,25 +1291,28 @@ __global__ void __launch_bounds__(256) k_kv8_chunk_combine(const __grid_constant
 // bits. 2 HD MACs and one exponential a (row, key) pair; four warps load and convert the next
 // query tile meanwhile and one of their threads issues the MMAs. Two CTAs share an SM.
 // =======================================================================================
+constexpr int CS_TMEM = 256;
+constexpr int CS_THREADS = 256;  // warps 0-3 sums, 4-7 loaders (4 issues the MMAs too)
 template <int HD>
 struct Cs {
+    static constexpr int KEYS = 128;
     static constexpr int MAT = CT_SUB * (HD / 64);
-    static constexpr int OFF_Q = MAT, OFF_ROW = 3 * MAT, OFF_BAR = OFF_ROW + 4 * CT_ROWS * 16;
+    static constexpr int OFF_Q = MAT, OFF_ROW = 3 * MAT, OFF_BAR = OFF_ROW + 4 * 3 * CT_ROWS * 4;
     static constexpr int SMEM = 1024 + OFF_BAR + 256;
 };
 
 template <int HD, int DT>
-__global__ void __launch_bounds__(CT_THREADS, 2) k_kv8_score(const __grid_constant__ Kv8AttnP p) {
+__global__ void __launch_bounds__(CS_THREADS, 2) k_kv8_score(const __grid_constant__ Kv8AttnP p) {
     constexpr int MAT = Cs<HD>::MAT, NSUB = HD / 64, CH = HD / 16;
     extern __shared__ uint8_t cs_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(cs_raw) + 1023) & ~(uintptr_t)1023);
-    float4* rowc = reinterpret_cast<float4*>(sm + Cs<HD>::OFF_ROW);  // [4][128]: logit factor, lse2, last visible position
+    float* rowc = reinterpret_cast<float*>(sm + Cs<HD>::OFF_ROW);  // [4][3][128]: -lse2, logit factor, last visible position
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Cs<HD>::OFF_BAR);
     uint64_t *q_full = bars, *q_empty = bars + 2, *s_full = bars + 4, *s_empty = bars + 6, *mma_fin = bars + 8;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 9);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int b = blockIdx.z, head = blockIdx.y, key0 = blockIdx.x * CT_BK;
+    const int b = blockIdx.z, head = blockIdx.y, key0 = blockIdx.x * Cs<HD>::KEYS;
     int s, r0, n;
     if (!attn_entry(p, b, s, r0, n) || n == 0 || key0 >= s + n) return;
     const int rows = n * p.G, kend = s + n;
@@ -1222,7 +1330,7 @@ __global__ void __launch_bounds__(CT_THREADS, 2) k_kv8_score(const __grid_consta
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 4) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(CT_TMEM)
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(CS_TMEM)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
@@ -1261,6 +1369,8 @@ __global__ void __launch_bounds__(CT_THREADS, 2) k_kv8_score(const __grid_consta
             const int row = min(rt * CT_ROWS + t, rows - 1), tok = row_token(p, row);
             return p.lse2[(size_t)(r0 + tok) * p.n_heads + head * p.G + row - tok * p.G];
         };
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint64_t kd = sw128_desc(smem_u32(sm)), qd = sw128_desc(smem_u32(sm + Cs<HD>::OFF_Q));
         QTile<HD> qt;
         fetch_q<HD>(qt, p, r0, head, t0 * CT_ROWS, rows, warp - 4, lane);
         float z = row_lse(t0);
@@ -1275,10 +1385,10 @@ __global__ void __launch_bounds__(CT_THREADS, 2) k_kv8_score(const __grid_consta
                 break;
             }
             // rowc[i % 4]: the tile four before has been summed, as S^T of the tile two before was issued
-            float4* rc = rowc + (i & 3) * CT_ROWS;
-            store_q<HD, DT>(qt, warp - 4, lane, smem_u32(sm + Cs<HD>::OFF_Q + buf * MAT), [&](int r, float mul) { rc[r].x = mul * p.scale_log2; });
-            rc[t].y = z;
-            rc[t].z = __int_as_float(v ? s + tok : -1);
+            float* rc = rowc + (i & 3) * 3 * CT_ROWS;
+            store_q<HD, DT>(qt, warp - 4, lane, smem_u32(sm + Cs<HD>::OFF_Q + buf * MAT), [&](int r, float mul) { rc[CT_ROWS + r] = mul * p.scale_log2; });
+            rc[t] = -z;
+            rc[2 * CT_ROWS + t] = __int_as_float(v ? s + tok : -1);
             if (rt + 1 < t1) {  // the next tile is on its way while this one is multiplied
                 fetch_q<HD>(qt, p, r0, head, (rt + 1) * CT_ROWS, rows, warp - 4, lane);
                 z = row_lse(rt + 1);
@@ -1286,17 +1396,19 @@ __global__ void __launch_bounds__(CT_THREADS, 2) k_kv8_score(const __grid_consta
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(q_full + buf));
-            if (t == 0) {
-                if (!wait(q_full + buf, i >> 1) || (i >= 2 && !wait(s_empty + buf, (i >> 1) - 1))) {
+            if (warp == 4) {
+                if (!__all_sync(0xffffffffu, wait(q_full + buf, i >> 1) && (i < 2 || wait(s_empty + buf, (i >> 1) - 1)))) {
                     *abort_flag = 1;
-                } else {
-                    tc_fence_after();
-                    const uint32_t ka = smem_u32(sm), qa = smem_u32(sm + Cs<HD>::OFF_Q + buf * MAT);
+                    break;
+                }
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t q0 = qd + (uint32_t)(buf * (MAT >> 4));
 #pragma unroll
                     for (int sub = 0; sub < NSUB; ++sub)
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            umma_f16(tmem + buf * 128, sw128_desc(ka + sub * CT_SUB) + 2 * kk, sw128_desc(qa + sub * CT_SUB) + 2 * kk,
+                            umma_f16(tm + buf * 128, kd + sub * (CT_SUB >> 4) + 2 * kk, q0 + sub * (CT_SUB >> 4) + 2 * kk,
                                      idesc_f16(128, CT_ROWS), (sub | kk) ? 1u : 0u);
                     umma_commit(smem_u32(s_full + buf));
                     umma_commit(smem_u32(q_empty + buf));
@@ -1304,9 +1416,10 @@ __global__ void __launch_bounds__(CT_THREADS, 2) k_kv8_score(const __grid_consta
             }
             __syncwarp();
         }
-        if (t == 0) {
+        if (warp == 4) {
             // the commits' asynchronous arrivals land before the CTA ends
-            umma_commit(smem_u32(mma_fin));
+            if (elect_one()) umma_commit(smem_u32(mma_fin));
+            __syncwarp();
             const uint64_t w0 = globaltimer_ns();
             while (!mbar_try_wait(smem_u32(mma_fin), 0) && globaltimer_ns() - w0 < kTcWaitNs) {
             }
@@ -1327,23 +1440,46 @@ __global__ void __launch_bounds__(CT_THREADS, 2) k_kv8_score(const __grid_consta
                 break;
             }
             tc_fence_after();
-            const float4* rc = rowc + (i & 3) * CT_ROWS;
+            const float* rc = rowc + (i & 3) * 3 * CT_ROWS;
             // rows of the tile before the last key's token see not all of these keys
-            const bool masked = s + rt * CT_ROWS / p.G < key0 + CT_BK - 1 || (rt + 1) * CT_ROWS > rows;
-            float part[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-            for (int cc = 0; cc < 4; ++cc) {
-                uint32_t x[32];
-                TMEM_LD32(lane_base + buf * 128 + cc * 32, x);
-                tmem_wait_ld();
+            const bool masked = s + rt * CT_ROWS / p.G < key0 + Cs<HD>::KEYS - 1 || (rt + 1) * CT_ROWS > rows;
+            uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
+            const float f16 = p.scale_log2 * sk;
+            uint32_t x[2][32];
+            TMEM_LD32(lane_base + buf * 128, x[0]);
 #pragma unroll
-                for (int u = 0; u < 32; ++u) {
-                    const float4 c = rc[cc * 32 + u];
-                    const float e = ex2(fmaf(__uint_as_float(x[u]), c.x * sk, -c.y));
-                    part[u & 3] += !masked || key <= __float_as_int(c.z) ? e : 0.f;
+            for (int cc = 0; cc < 4; ++cc) {
+                tmem_wait_ld();
+                if (cc < 3) TMEM_LD32(lane_base + buf * 128 + (cc + 1) * 32, x[(cc + 1) & 1]);
+                const uint32_t* y = x[cc & 1];
+                // four rows a turn: their constants are one or two 16-byte broadcasts
+#pragma unroll
+                for (int u = 0; u < 32; u += 4) {
+                    const float4 z = *reinterpret_cast<const float4*>(rc + cc * 32 + u);
+                    uint64_t fa = pack2(f16, f16), fb = fa;
+                    if (DT == QW_BF16) {
+                        const float4 f = *reinterpret_cast<const float4*>(rc + CT_ROWS + cc * 32 + u);
+                        const uint64_t k2 = pack2(sk, sk);
+                        fa = mul2(pack2(f.x, f.y), k2);
+                        fb = mul2(pack2(f.z, f.w), k2);
+                    }
+                    float t0, t1, t2, t3;
+                    unpack2(fma2(pack2u(y[u], y[u + 1]), fa, pack2(z.x, z.y)), t0, t1);
+                    unpack2(fma2(pack2u(y[u + 2], y[u + 3]), fb, pack2(z.z, z.w)), t2, t3);
+                    if (masked) {
+                        const int4 lim = *reinterpret_cast<const int4*>(rc + 2 * CT_ROWS + cc * 32 + u);
+                        t0 = key <= lim.x ? t0 : -INFINITY;
+                        t1 = key <= lim.y ? t1 : -INFINITY;
+                        t2 = key <= lim.z ? t2 : -INFINITY;
+                        t3 = key <= lim.w ? t3 : -INFINITY;
+                    }
+                    sum[(u >> 1) & 3] = add2(sum[(u >> 1) & 3], pack2(ex2(t0), ex2(t1)));
+                    sum[((u >> 1) + 1) & 3] = add2(sum[((u >> 1) + 1) & 3], pack2(ex2(t2), ex2(t3)));
                 }
             }
-            acc += (part[0] + part[1]) + (part[2] + part[3]);
+            float e0, e1;
+            unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), e0, e1);
+            acc += e0 + e1;
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(s_empty + buf));
@@ -1359,7 +1495,7 @@ __global__ void __launch_bounds__(CT_THREADS, 2) k_kv8_score(const __grid_consta
     if (*abort_flag && threadIdx.x == 0) atomicOr(p.status, QW_KV8_TIMEOUT);
     if (warp == 4) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(CT_TMEM) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(CS_TMEM) : "memory");
     }
 }
 
@@ -1411,11 +1547,15 @@ Plan make_plan(const qw_kv8* kv, int B, int T, int max_len, int max_keys, int n_
     }
     if (!q.decode) {
         q.tiles = (int)((rows + CT_ROWS - 1) / CT_ROWS);
-        // two CTAs an SM; few row tiles split their keys, at least two key tiles each
-        const long long ctas = (long long)q.tiles * kv->n_kv_heads * B;
-        const int kt = (max_keys + CT_BK - 1) / CT_BK;
-        q.splits = (int)std::max(1ll, std::min({2ll * sm_count() / ctas, (long long)kt / 2, 64ll}));
-        const size_t part = q.splits == 1 ? 0 : (size_t)ctas * q.splits * CT_ROWS;
+        // A CTA an SM. Row tiles that leave the last wave of CTAs part empty split their keys, if that
+        // fills waves by a quarter better and each split keeps 512 keys.
+        const long long ctas = (long long)(q.tiles + 1) / 2 * kv->n_kv_heads * B, slots = sm_count();
+        auto fill = [&](long long n) { return (double)n / (double)((n + slots - 1) / slots * slots); };
+        q.splits = 1;
+        const int most = std::min(64, max_keys / 512);
+        for (int n = 2; n <= most && ctas * n < 4 * slots; ++n)
+            if (fill(ctas * n) >= 1.25 * fill(ctas * q.splits)) q.splits = n;
+        const size_t part = q.splits == 1 ? 0 : (size_t)B * kv->n_kv_heads * q.tiles * q.splits * CT_ROWS;
         q.off_o = put(part * HD * 4);
         q.off_ml = put(part * 2 * 4);
     }
@@ -1432,8 +1572,8 @@ template <int HD, int DT>
 cudaError_t run_score(const Kv8AttnP& p, int B, cudaStream_t st) {
     LaunchCtx c = {st, false, nullptr};
     if (cudaError_t e = allow_smem(k_kv8_score<HD, DT>, Cs<HD>::SMEM)) return e;
-    const unsigned tiles = (unsigned)((p.max_keys + CT_BK - 1) / CT_BK);
-    return launch_k(c, k_kv8_score<HD, DT>, dim3(tiles, p.kv.n_kv, B), dim3(CT_THREADS), (size_t)Cs<HD>::SMEM, p);
+    const unsigned tiles = (unsigned)((p.max_keys + Cs<HD>::KEYS - 1) / Cs<HD>::KEYS);
+    return launch_k(c, k_kv8_score<HD, DT>, dim3(tiles, p.kv.n_kv, B), dim3(CS_THREADS), (size_t)Cs<HD>::SMEM, p);
 }
 
 template <int HD, int DT>
@@ -1470,8 +1610,14 @@ cudaError_t run_attn(const Kv8AttnP& p, const Plan& q, int B, char* ws, cudaStre
     P.part_o = (float*)(ws + q.off_o);
     P.part_ml = (float*)(ws + q.off_ml);
     P.tiles = q.tiles;
+    // the roles' register counts add up only if the kernel was given exactly CT_REGS a thread
+    static const int regs = [] {
+        cudaFuncAttributes fa = {};
+        return cudaFuncGetAttributes(&fa, k_kv8_chunk<HD, DT>) == cudaSuccess ? fa.numRegs : 0;
+    }();
+    if (regs != CT_REGS) return cudaErrorInvalidKernelImage;
     if ((e = allow_smem(k_kv8_chunk<HD, DT>, Ct<HD>::SMEM)) != cudaSuccess) return e;
-    e = launch_k(c, k_kv8_chunk<HD, DT>, dim3(p.kv.n_kv, B, q.tiles * q.splits), dim3(CT_THREADS), (size_t)Ct<HD>::SMEM, P);
+    e = launch_k(c, k_kv8_chunk<HD, DT>, dim3(p.kv.n_kv, B, (q.tiles + 1) / 2 * q.splits), dim3(CT_THREADS), (size_t)Ct<HD>::SMEM, P);
     if (e == cudaSuccess && q.splits > 1)
         e = launch_k(c, k_kv8_chunk_combine<HD, DT>, dim3(q.tiles * CT_ROWS / 8, p.kv.n_kv, B), dim3(256), 0, P);
     return e == cudaSuccess && p.score_out ? run_score<HD, DT>(p, B, st) : e;
