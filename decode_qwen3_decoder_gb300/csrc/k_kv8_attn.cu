@@ -594,16 +594,20 @@ __global__ void __launch_bounds__(KD_WARPS * 32, NT == 1 ? 2 : 1) k_kv8_decode(c
     }
 }
 
-// Pairs that cross CTAs of k_kv8_decode: out = sum of the slots' partials. With scores also the
-// weights of a chunk of KC_KEYS keys (blockIdx.y) from the stored logits.
+// Pairs that cross CTAs of k_kv8_decode: out = sum of the slots' partials. Warp w takes slots w0 + w,
+// + 8, ... for all rows, loading a slot's maximum, sum and values together; one exchange through
+// shared memory joins the warps. With scores also the weights of a chunk of KC_KEYS keys
+// (blockIdx.y) from the stored logits, four keys a thread.
 constexpr int KC_KEYS = 1024;
+inline int kc_smem(int nrow, int hd) { return KD_WARPS * nrow * (hd + 2) * 4; }
+
 template <int HD, int DT>
 __global__ void __launch_bounds__(KD_WARPS * 32) k_kv8_combine(const __grid_constant__ Kv8DecP P) {
     const Kv8AttnP& p = P.a;
+    extern __shared__ __align__(16) float kc_o[];  // [warps][nrow][HD], then (M, L) of [warps][nrow]
     __shared__ int cum[QW_KV8_MAX_BATCH + 1];
     __shared__ int ws[KD_WARPS];
-    __shared__ float s_m[16], s_l[16];
-    __shared__ float4 s_acc[KD_WARPS][HD / 4];
+    __shared__ float s_z[16];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, H = p.kv.n_kv;
     const int b = blockIdx.x / H, head = blockIdx.x % H, key0 = blockIdx.y * KC_KEYS;
     int s, r0, n;
@@ -623,78 +627,92 @@ __global__ void __launch_bounds__(KD_WARPS * 32) k_kv8_combine(const __grid_cons
     }
     if (!split && !p.score_out) return;
     pdl_wait();
-    auto slot = [&](int w) {
-        const int i0 = (int)(items * w / P.n_cta);
-        return (size_t)w * 2 + (i0 >= first ? 0 : 1);
-    };
-    for (int r = warp; r < rows; r += KD_WARPS) {  // each row's maximum and sum over the slots
-        float M = -1e30f, L = 0.f;
-        if (split) {
-            for (int w = w0 + lane; w <= w1; w += 32) M = fmaxf(M, P.part_ml[(slot(w) * P.nrow + r) * 2]);
-            M = warp_max(M);
-            for (int w = w0 + lane; w <= w1; w += 32) {
-                const float* ml = P.part_ml + (slot(w) * P.nrow + r) * 2;
-                L += ml[1] * ex2(ml[0] - M);
-            }
-            L = warp_sum(L);
-        }
-        if (lane == 0) {
-            s_m[r] = M;
-            // with scores only the log of the sum is needed of a pair that is done
-            s_l[r] = split ? L : p.lse2[(size_t)(r0 + r / p.G) * p.n_heads + head * p.G + r % p.G];
-        }
-    }
-    __syncthreads();
-    if (split && blockIdx.y == 0) {
+    const bool merge = split && blockIdx.y == 0;
+    if (split) {
+        float2* ml = reinterpret_cast<float2*>(kc_o + (size_t)KD_WARPS * P.nrow * HD);
         for (int r = 0; r < rows; ++r) {
-            const float M = s_m[r];
+            float M = -1e30f, L = 0.f;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (lane < HD / 4) {
-#pragma unroll 4
-                for (int w = w0 + warp; w <= w1; w += KD_WARPS) {
-                    const size_t at = slot(w) * P.nrow + r;
-                    const float f = ex2(P.part_ml[at * 2] - M);
-                    const float4 v = *reinterpret_cast<const float4*>(P.part_o + at * HD + lane * 4);
-                    acc.x += v.x * f;
-                    acc.y += v.y * f;
-                    acc.z += v.z * f;
-                    acc.w += v.w * f;
-                }
-                s_acc[warp][lane] = acc;
+#pragma unroll 2
+            for (int w = w0 + warp; w <= w1; w += KD_WARPS) {
+                const int i0 = (int)(items * w / P.n_cta);
+                const size_t at = ((size_t)w * 2 + (i0 >= first ? 0 : 1)) * P.nrow + r;
+                const float2 x = *reinterpret_cast<const float2*>(P.part_ml + at * 2);
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (merge && lane < HD / 4) v = *reinterpret_cast<const float4*>(P.part_o + at * HD + lane * 4);
+                const float m = fmaxf(M, x.x), fo = ex2(M - m), fn = ex2(x.x - m);
+                L = L * fo + x.y * fn;
+                acc.x = acc.x * fo + v.x * fn;
+                acc.y = acc.y * fo + v.y * fn;
+                acc.z = acc.z * fo + v.z * fn;
+                acc.w = acc.w * fo + v.w * fn;
+                M = m;
             }
-            __syncthreads();
-            if (tid < HD / 4) {
-                float4 t = s_acc[0][tid];
-#pragma unroll
-                for (int k = 1; k < KD_WARPS; ++k) {
-                    const float4 v = s_acc[k][tid];
-                    t.x += v.x;
-                    t.y += v.y;
-                    t.z += v.z;
-                    t.w += v.w;
-                }
-                const float inv = 1.f / s_l[r];
-                const int tok = r0 + r / p.G, h = head * p.G + r % p.G;
-                uint2 w;
-                w.x = DT == QW_F16 ? pack_h2(t.x * inv, t.y * inv) : pack_bf2(t.x * inv, t.y * inv);
-                w.y = DT == QW_F16 ? pack_h2(t.z * inv, t.w * inv) : pack_bf2(t.z * inv, t.w * inv);
-                *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) + (size_t)tok * p.ld_out + (size_t)h * HD + tid * 4) = w;
-                if (tid == 0 && p.lse) p.lse[(size_t)tok * p.n_heads + h] = (log2f(s_l[r]) + M - KV8_LIFT) * KV8_LN2;
-            }
-            __syncthreads();
+            if (merge && lane < HD / 4) *reinterpret_cast<float4*>(kc_o + ((size_t)warp * P.nrow + r) * HD + lane * 4) = acc;
+            if (lane == 0) ml[warp * P.nrow + r] = make_float2(M, L);
         }
+        __syncthreads();
+        for (int x = tid; x < rows * (HD / 4); x += KD_WARPS * 32) {
+            const int r = x / (HD / 4), d = (x % (HD / 4)) * 4;
+            float M = -1e30f, L = 0.f;
+#pragma unroll
+            for (int w = 0; w < KD_WARPS; ++w) M = fmaxf(M, ml[w * P.nrow + r].x);
+            float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < KD_WARPS; ++w) {
+                const float2 y = ml[w * P.nrow + r];
+                const float f = ex2(y.x - M);
+                L += y.y * f;
+                if (!merge) continue;
+                const float4 v = *reinterpret_cast<const float4*>(kc_o + ((size_t)w * P.nrow + r) * HD + d);
+                t.x += v.x * f;
+                t.y += v.y * f;
+                t.z += v.z * f;
+                t.w += v.w * f;
+            }
+            const float z = log2f(L) + M - KV8_LIFT;
+            if (d == 0) s_z[r] = z;
+            if (!merge) continue;
+            const float inv = 1.f / L;
+            const int tok = r0 + r / p.G, h = head * p.G + r % p.G;
+            uint2 w;
+            w.x = DT == QW_F16 ? pack_h2(t.x * inv, t.y * inv) : pack_bf2(t.x * inv, t.y * inv);
+            w.y = DT == QW_F16 ? pack_h2(t.z * inv, t.w * inv) : pack_bf2(t.z * inv, t.w * inv);
+            *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) + (size_t)tok * p.ld_out + (size_t)h * HD + d) = w;
+            if (d == 0 && p.lse) p.lse[(size_t)tok * p.n_heads + h] = z * KV8_LN2;
+        }
+    } else if (tid < rows) {
+        s_z[tid] = p.lse2[(size_t)(r0 + tid / p.G) * p.n_heads + head * p.G + tid % p.G];
     }
     if (!p.score_out) return;
     const size_t base = ((size_t)b * H + head) * p.ld_score;
-    const int end = min(s + n, key0 + KC_KEYS);
-    for (int j = key0 + tid; j < end; j += KD_WARPS * 32) {
-        float acc = 0.f;
-        for (int r = 0; r < rows; ++r) {
-            const float z = split ? log2f(s_l[r]) + s_m[r] - KV8_LIFT : s_l[r];
-            if (j <= s + r / p.G) acc += ex2(P.tbuf[((size_t)(b * H + head) * P.nrow + r) * P.ld_t + j] - z);
-        }
-        p.score_out[base + j] = (p.score_in ? p.score_in[base + j] : 0.f) + acc;
+    const int j = key0 + tid * 4, end = s + n;
+    float in[4] = {0.f, 0.f, 0.f, 0.f};
+    float4 t[8];  // the logits are stored for at most 8 rows
+    if (j < end) {
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+            if (r < rows) t[r] = *reinterpret_cast<const float4*>(P.tbuf + ((size_t)(b * H + head) * P.nrow + r) * P.ld_t + j);
+        if (p.score_in)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (j + k < end) in[k] = p.score_in[base + j + k];
     }
+    __syncthreads();
+    if (j >= end) return;
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+        if (r >= rows) break;
+        const float z = s_z[r];
+        const int lim = s + r / p.G;  // keys past it have no logit of this row
+        const float v[4] = {t[r].x, t[r].y, t[r].z, t[r].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[k] += j + k <= lim ? ex2(v[k] - z) : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (j + k < end) p.score_out[base + j + k] = in[k] + acc[k];
 }
 
 // =======================================================================================
@@ -1599,7 +1617,9 @@ cudaError_t run_attn(const Kv8AttnP& p, const Plan& q, int B, char* ws, cudaStre
         if (!q.pair_mode || q.tbuf) {
             const unsigned chunks = q.tbuf ? (unsigned)((p.max_keys + KC_KEYS - 1) / KC_KEYS) : 1;
             if (!q.pair_mode) c.pdl = true;
-            e = launch_k(c, k_kv8_combine<HD, DT>, dim3(B * p.kv.n_kv, chunks), dim3(KD_WARPS * 32), 0, P);
+            const int smem = q.pair_mode ? 0 : kc_smem(q.nrow, HD);
+            if ((e = allow_smem(k_kv8_combine<HD, DT>, smem)) != cudaSuccess) return e;
+            e = launch_k(c, k_kv8_combine<HD, DT>, dim3(B * p.kv.n_kv, chunks), dim3(KD_WARPS * 32), (size_t)smem, P);
             if (e != cudaSuccess) return e;
         }
         return p.score_out && !q.tbuf ? run_score<HD, DT>(p, B, st) : cudaSuccess;
