@@ -73,19 +73,27 @@ __device__ __forceinline__ bool attn_entry(const Kv8AttnP& p, int b, int& s, int
 // the 16 dims 64 h + 16 c .. of row g. fp16 rows go in as they are; a bf16 row is first divided by
 // the power of two of its largest value (`mul` gives it back), so every element within 2^-17 of that
 // is exact in fp16 and smaller ones are off by 2^-25 of it.
+template <int HD>
+__device__ __forceinline__ void fetch_row(const Kv8AttnP& p, bool valid, size_t off, int c, uint4 (*w)[2]) {
+#pragma unroll
+    for (int h = 0; h < HD / 64; ++h)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            w[h][u] = make_uint4(0u, 0u, 0u, 0u);
+            if (valid) w[h][u] = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.q) + off + 64 * h + 16 * c + 8 * u);
+        }
+}
 template <int HD, int DT>
-__device__ __forceinline__ void load_q(const Kv8AttnP& p, bool valid, size_t off, int c, uint32_t (*qf)[2], float& mul) {
+__device__ __forceinline__ void row_operand(const uint4 (*x)[2], uint32_t (*qf)[2], float& mul) {
     uint32_t w[HD / 64][8];
 #pragma unroll
     for (int h = 0; h < HD / 64; ++h)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (valid) v = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.q) + off + 64 * h + 16 * c + 8 * u);
-            w[h][4 * u] = v.x;
-            w[h][4 * u + 1] = v.y;
-            w[h][4 * u + 2] = v.z;
-            w[h][4 * u + 3] = v.w;
+            w[h][4 * u] = x[h][u].x;
+            w[h][4 * u + 1] = x[h][u].y;
+            w[h][4 * u + 2] = x[h][u].z;
+            w[h][4 * u + 3] = x[h][u].w;
         }
     mul = 1.f;
     if (DT == QW_BF16) {
@@ -96,9 +104,9 @@ __device__ __forceinline__ void load_q(const Kv8AttnP& p, bool valid, size_t off
             for (int i = 0; i < 8; ++i) a = fmaxf(a, fmaxf(fabsf(bf_lo(w[h][i])), fabsf(bf_hi(w[h][i]))));
         a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
         a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
-        const int x = min(max(kv8_log2(a), -100), 100);
-        mul = kv8_pow2(x);
-        const float inv = kv8_pow2(-x);
+        const int e = min(max(kv8_log2(a), -100), 100);
+        mul = kv8_pow2(e);
+        const float inv = kv8_pow2(-e);
 #pragma unroll
         for (int h = 0; h < HD / 64; ++h)
 #pragma unroll
@@ -237,18 +245,19 @@ struct Kv8DecP {
     int n_cta;        // CTAs of the decode kernel
 };
 
-__device__ __forceinline__ int kd_pages(const Kv8AttnP& p, int b) {
-    int s, r0, n;
-    const bool ok = attn_entry(p, b, s, r0, n);
-    return ok && n > 0 ? (s + n + KV8_PAGE - 1) / KV8_PAGE : 0;
-}
-
-// cum[b] = pages of the entries before b (b <= B), by all 256 threads of the CTA.
-__device__ __forceinline__ void kd_prefix(const Kv8AttnP& p, int B, int* cum, int* ws) {
+// cum[b] = pages of the entries before b (b <= B), by all 256 threads of the CTA; with `ent` also
+// (start, first row) of each entry.
+__device__ __forceinline__ void kd_prefix(const Kv8AttnP& p, int B, int* cum, int* ws, int2* ent) {
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     int base = 0;
     for (int b0 = 0; b0 < B; b0 += KD_WARPS * 32) {
-        const int v = b0 + tid < B ? kd_pages(p, b0 + tid) : 0;
+        int v = 0;
+        if (b0 + tid < B) {
+            int s, r0, n;
+            const bool ok = attn_entry(p, b0 + tid, s, r0, n);
+            v = ok && n > 0 ? (s + n + KV8_PAGE - 1) / KV8_PAGE : 0;
+            if (ent) ent[b0 + tid] = make_int2(s, r0);
+        }
         int x = v;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -303,7 +312,7 @@ template <int HD, int DT, int NT>
 __global__ void __launch_bounds__(KD_WARPS * 32, NT == 1 ? 2 : 1) k_kv8_decode(const __grid_constant__ Kv8DecP P) {
     constexpr int KS = HD / 16, BLK = Kv8<HD>::BLK, LD = HD / 8;  // LD: output dims of a lane
     const Kv8AttnP& p = P.a;
-    extern __shared__ __align__(128) uint8_t kd_smem[];  // [warps][stages][BLK], then the slots
+    extern __shared__ __align__(128) uint8_t kd_smem[];  // [warps][stages][BLK], the slots, then [B] (start, first row)
     __shared__ uint64_t bars[KD_WARPS][8];
     __shared__ int cum[QW_KV8_MAX_BATCH + 1];
     __shared__ int ws[KD_WARPS], slot_pair[2 * KD_WARPS], s_abort;
@@ -311,6 +320,7 @@ __global__ void __launch_bounds__(KD_WARPS * 32, NT == 1 ? 2 : 1) k_kv8_decode(c
     const int H = p.kv.n_kv, S = P.stages;
     float* slot_o = reinterpret_cast<float*>(kd_smem + (size_t)KD_WARPS * S * BLK);  // [warps][2][nrow][HD]
     float* slot_ml = slot_o + (size_t)2 * KD_WARPS * P.nrow * HD;                    // [warps][2][nrow][2]
+    int2* ent = reinterpret_cast<int2*>(slot_ml + (size_t)2 * KD_WARPS * P.nrow * 2);
     if (!P.pair_mode) pdl_launch();
     if (lane == 0)
         for (int i = 0; i < S; ++i) mbar_init(smem_u32(&bars[warp][i]), 1);
@@ -321,11 +331,18 @@ __global__ void __launch_bounds__(KD_WARPS * 32, NT == 1 ? 2 : 1) k_kv8_decode(c
     if (tid < 2 * KD_WARPS) slot_pair[tid] = -1;
     // ---- this CTA's and this warp's run of items ----
     int c0, c1;
+    // entry of the pair that the warp works on: b, its start, first row and rows of a KV head
+    int b = 0, head = 0, page = 0, pages = 0, s = 0, r0 = 0, rows = 0;
     if (P.pair_mode) {
+        int n;
+        b = blockIdx.x / H;
+        head = blockIdx.x % H;
+        const bool ok = attn_entry(p, b, s, r0, n);
+        rows = n * p.G;
         c0 = 0;
-        c1 = kd_pages(p, blockIdx.x / H);
+        c1 = ok && n > 0 ? (s + n + KV8_PAGE - 1) / KV8_PAGE : 0;
     } else {
-        kd_prefix(p, P.B, cum, ws);
+        kd_prefix(p, P.B, cum, ws, ent);
         const long long items = (long long)cum[P.B] * H;
         c0 = (int)(items * blockIdx.x / gridDim.x);
         c1 = (int)(items * (blockIdx.x + 1) / gridDim.x);
@@ -341,8 +358,7 @@ __global__ void __launch_bounds__(KD_WARPS * 32, NT == 1 ? 2 : 1) k_kv8_decode(c
                     *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + (size_t)(r0 + i) * p.ld_out + d) = make_uint4(0u, 0u, 0u, 0u);
         }
     if (P.pair_mode && c1 == 0) {
-        const int b = blockIdx.x / H, head = blockIdx.x % H;
-        int s, r0, n;
+        int n;
         if (!attn_entry(p, b, s, r0, n)) {
             if (tid == 0) atomicOr(p.status, QW_KV8_BAD_POS);
             if (r0 < 0 || n < 0 || n > p.max_len || r0 > p.T - n) return;
@@ -357,8 +373,6 @@ __global__ void __launch_bounds__(KD_WARPS * 32, NT == 1 ? 2 : 1) k_kv8_decode(c
     const int i0 = c0 + (int)((long long)(c1 - c0) * warp / KD_WARPS), i1 = c0 + (int)((long long)(c1 - c0) * (warp + 1) / KD_WARPS);
     auto locate = [&](int j, int& b, int& head, int& page, int& pages) {
         if (P.pair_mode) {
-            b = blockIdx.x / H;
-            head = blockIdx.x % H;
             page = j;
             pages = c1;
         } else {
@@ -369,18 +383,36 @@ __global__ void __launch_bounds__(KD_WARPS * 32, NT == 1 ? 2 : 1) k_kv8_decode(c
             page = off - head * pages;
         }
     };
+    uint4 qx[NT][HD / 64][2];
+    // the pair of item j: where it begins, and its query rows on the way
+    auto enter = [&](int j) {
+        locate(j, b, head, page, pages);
+        if (!P.pair_mode) {
+            s = ent[b].x;
+            r0 = ent[b].y;
+            rows = (p.cu[b + 1] - r0) * p.G;
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int r = 8 * nt + g;
+            const bool v = r < rows;
+            const int i = v ? row_token(p, r) : 0, h = head * p.G + (v ? r - i * p.G : 0);
+            fetch_row<HD>(p, v, (size_t)(r0 + i) * p.ld_q + (size_t)h * HD, c, qx[nt]);
+        }
+    };
+    if (i0 < i1) enter(i0);  // before the page table and the first pages, which take as long
     const uint32_t ring = smem_u32(kd_smem) + warp * S * BLK;
     // lane l holds the block address of the l-th item of the batch of 32 being issued, and of the next
     auto address = [&](int j) -> const uint8_t* {
         if (j >= i1) return nullptr;
-        int b, head, page, pages;
-        locate(j, b, head, page, pages);
-        int id = p.kv.table[(size_t)b * p.kv.max_pages + page];
+        int b2 = b, head2 = head, page2, pages2;
+        locate(j, b2, head2, page2, pages2);
+        int id = p.kv.table[(size_t)b2 * p.kv.max_pages + page2];
         if (id < 0 || id >= p.kv.n_pages) {
             atomicOr(p.status, QW_KV8_BAD_POS);
             id = 0;
         }
-        return p.kv.blocks + ((size_t)id * H + head) * BLK;
+        return p.kv.blocks + ((size_t)id * H + head2) * BLK;
     };
     const uint8_t* cur = address(i0 + lane);
     const uint8_t* nxt = address(i0 + 32 + lane);
@@ -403,7 +435,7 @@ __global__ void __launch_bounds__(KD_WARPS * 32, NT == 1 ? 2 : 1) k_kv8_decode(c
     uint32_t qf[NT][KS][2];
     float qmul[NT][2], R[NT][2], l[NT][2], o[NT][KS][4];
     int limit[NT][2];
-    int b = 0, head = 0, page = 0, pages = 0, page_lo = 0, n_slots = 0, s = 0, r0 = 0, rows = 0;
+    int page_lo = 0, n_slots = 0;
     auto flush = [&]() {  // the segment [page_lo, page) of the pair (b, head)
         const bool whole = page_lo == 0 && page == pages;
         const int slot = warp * 2 + n_slots;
@@ -427,7 +459,7 @@ __global__ void __launch_bounds__(KD_WARPS * 32, NT == 1 ? 2 : 1) k_kv8_decode(c
                     const float inv = 1.f / x;
 #pragma unroll
                     for (int i = 0; i < LD; ++i) v[i] *= inv;
-                    const int tok = r0 + r / p.G, h = head * p.G + r % p.G;
+                    const int i = row_token(p, r), tok = r0 + i, h = head * p.G + r - i * p.G;
                     store_row<DT, LD / 2>(p.out, (size_t)tok * p.ld_out + (size_t)h * HD + g * LD, v);
                     if (g == 0) {
                         const float z = log2f(x) + R[nt][e] - KV8_LIFT;
@@ -449,33 +481,31 @@ __global__ void __launch_bounds__(KD_WARPS * 32, NT == 1 ? 2 : 1) k_kv8_decode(c
             ++n_slots;
         }
     };
+    auto begin = [&]() {
+        page_lo = page;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float mul;
+            row_operand<HD, DT>(qx[nt], qf[nt], mul);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                qmul[nt][e] = __shfl_sync(0xffffffffu, mul, (2 * c + e) * 4) * p.scale_log2;
+                const int rr = 8 * nt + 2 * c + e;
+                limit[nt][e] = rr < rows ? s + row_token(p, rr) : -1;
+                R[nt][e] = -1e30f;
+                l[nt][e] = 0.f;
+            }
+#pragma unroll
+            for (int i2 = 0; i2 < KS; ++i2) o[nt][i2][0] = o[nt][i2][1] = o[nt][i2][2] = o[nt][i2][3] = 0.f;
+        }
+    };
+    if (i0 < i1) begin();
     int st = 0, ph = 0;
     for (int j = i0; j < i1; ++j) {
-        if (j == i0 || page == pages) {
-            if (j > i0) flush();
-            locate(j, b, head, page, pages);
-            page_lo = page;
-            int n;
-            attn_entry(p, b, s, r0, n);
-            rows = n * p.G;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const int r = 8 * nt + g;
-                const bool v = r < rows;
-                const int i = v ? r / p.G : 0, h = head * p.G + (v ? r % p.G : 0);
-                float mul;
-                load_q<HD, DT>(p, v, (size_t)(r0 + i) * p.ld_q + (size_t)h * HD, c, qf[nt], mul);
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    qmul[nt][e] = __shfl_sync(0xffffffffu, mul, (2 * c + e) * 4) * p.scale_log2;
-                    const int rr = 8 * nt + 2 * c + e;
-                    limit[nt][e] = rr < rows ? s + rr / p.G : -1;
-                    R[nt][e] = -1e30f;
-                    l[nt][e] = 0.f;
-                }
-#pragma unroll
-                for (int i2 = 0; i2 < KS; ++i2) o[nt][i2][0] = o[nt][i2][1] = o[nt][i2][2] = o[nt][i2][3] = 0.f;
-            }
+        if (page == pages) {
+            flush();
+            enter(j);
+            begin();
         }
         if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars[warp][st]), ph, &s_abort))) {
             // give up: the outputs are not valid. The copies in flight land before the CTA ends.
@@ -531,66 +561,64 @@ __global__ void __launch_bounds__(KD_WARPS * 32, NT == 1 ? 2 : 1) k_kv8_decode(c
     __syncthreads();
     if (s_abort) return;
     // ---- merge the pieces of a pair that several warps hold ----
-    for (int a0 = 0; a0 < 2 * KD_WARPS;) {
-        const int pair = slot_pair[a0];
-        if (pair < 0) {
-            ++a0;
-            continue;
-        }
-        int a1 = a0 + 1;
-        while (a1 < 2 * KD_WARPS && (slot_pair[a1] == pair || slot_pair[a1] < 0)) ++a1;
-        const int pb_ = pair / H, ph_ = pair % H;
-        int es, er0, en;
-        attn_entry(p, pb_, es, er0, en);
-        const int erows = en * p.G;
+    // Lane k < 16 holds slot k's pair; `heads` marks the first slot of each pair (slots are in item order).
+    const int mine = lane < 2 * KD_WARPS ? slot_pair[lane] : -1;
+    const uint32_t used = __ballot_sync(0xffffffffu, mine >= 0);
+    const uint32_t below = used & ((1u << lane) - 1u);
+    const int before = __shfl_sync(0xffffffffu, mine, below ? 31 - __clz(below) : 0);
+    const uint32_t heads = __ballot_sync(0xffffffffu, mine >= 0 && (!below || before != mine));
+    const int per = P.nrow * (HD / 4), total = __popc(heads) * per;  // groups x (row, 4 dims)
+    for (int x0 = 0; x0 < total; x0 += KD_WARPS * 32) {
+        const int x = x0 + tid, gi = min(x, total - 1) / per, y = min(x, total - 1) - gi * per;
+        uint32_t m = heads;
+        for (int i = 0; i < gi; ++i) m &= m - 1;
+        const int a0 = __ffs(m) - 1;
+        m &= m - 1;
+        const int a1 = m ? __ffs(m) - 1 : 2 * KD_WARPS;
+        const int pair = slot_pair[a0], eb = P.pair_mode ? b : pair / H, eh = P.pair_mode ? head : pair - eb * H;
+        const int er0 = P.pair_mode ? r0 : ent[eb].y, erows = P.pair_mode ? rows : (p.cu[eb + 1] - er0) * p.G;
+        const int r = y / (HD / 4), d = (y - r * (HD / 4)) * 4;
+        if (x >= total || r >= erows) continue;
         int first = 0, last = c1;  // the pair's items
         if (!P.pair_mode) {
-            const int np = cum[pb_ + 1] - cum[pb_];
-            first = cum[pb_] * H + ph_ * np;
+            const int np = cum[eb + 1] - cum[eb];
+            first = cum[eb] * H + eh * np;
             last = first + np;
         }
-        const bool all = first >= c0 && last <= c1;
-        const int gslot = first >= c0 ? (first == c0 ? 0 : 1) : 0;
-        for (int x = tid; x < erows * (HD / 4); x += KD_WARPS * 32) {
-            const int r = x / (HD / 4), d = (x % (HD / 4)) * 4;
-            float M = -1e30f;
-            for (int k = a0; k < a1; ++k)
-                if (slot_pair[k] == pair) M = fmaxf(M, slot_ml[((size_t)k * P.nrow + r) * 2]);
-            float L = 0.f;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int k = a0; k < a1; ++k) {
-                if (slot_pair[k] != pair) continue;
-                const float f = ex2(slot_ml[((size_t)k * P.nrow + r) * 2] - M);
-                L += slot_ml[((size_t)k * P.nrow + r) * 2 + 1] * f;
-                const float4 v = *reinterpret_cast<const float4*>(slot_o + ((size_t)k * P.nrow + r) * HD + d);
-                acc.x += v.x * f;
-                acc.y += v.y * f;
-                acc.z += v.z * f;
-                acc.w += v.w * f;
+        float M = -1e30f, L = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = a0; k < a1; ++k) {
+            if (!(used >> k & 1)) continue;
+            const float2 ml = *reinterpret_cast<const float2*>(slot_ml + ((size_t)k * P.nrow + r) * 2);
+            const float4 v = *reinterpret_cast<const float4*>(slot_o + ((size_t)k * P.nrow + r) * HD + d);
+            const float mm = fmaxf(M, ml.x), fo = ex2(M - mm), fn = ex2(ml.x - mm);
+            M = mm;
+            L = L * fo + ml.y * fn;
+            acc.x = acc.x * fo + v.x * fn;
+            acc.y = acc.y * fo + v.y * fn;
+            acc.z = acc.z * fo + v.z * fn;
+            acc.w = acc.w * fo + v.w * fn;
+        }
+        if (first >= c0 && last <= c1) {
+            const float inv = 1.f / L;
+            const int i = row_token(p, r), tok = er0 + i, h = eh * p.G + r - i * p.G;
+            uint2 w;
+            w.x = DT == QW_F16 ? pack_h2(acc.x * inv, acc.y * inv) : pack_bf2(acc.x * inv, acc.y * inv);
+            w.y = DT == QW_F16 ? pack_h2(acc.z * inv, acc.w * inv) : pack_bf2(acc.z * inv, acc.w * inv);
+            *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) + (size_t)tok * p.ld_out + (size_t)h * HD + d) = w;
+            if (d == 0) {
+                const float z = log2f(L) + M - KV8_LIFT;
+                if (p.lse2) p.lse2[(size_t)tok * p.n_heads + h] = z;
+                if (p.lse) p.lse[(size_t)tok * p.n_heads + h] = z * KV8_LN2;
             }
-            if (all) {
-                const float inv = 1.f / L;
-                const int tok = er0 + r / p.G, h = ph_ * p.G + r % p.G;
-                const float v[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
-                uint2 w;
-                w.x = DT == QW_F16 ? pack_h2(v[0], v[1]) : pack_bf2(v[0], v[1]);
-                w.y = DT == QW_F16 ? pack_h2(v[2], v[3]) : pack_bf2(v[2], v[3]);
-                *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) + (size_t)tok * p.ld_out + (size_t)h * HD + d) = w;
-                if (d == 0) {
-                    const float z = log2f(L) + M - KV8_LIFT;
-                    if (p.lse2) p.lse2[(size_t)tok * p.n_heads + h] = z;
-                    if (p.lse) p.lse[(size_t)tok * p.n_heads + h] = z * KV8_LN2;
-                }
-            } else {
-                const size_t at = ((size_t)blockIdx.x * 2 + gslot) * P.nrow + r;
-                *reinterpret_cast<float4*>(P.part_o + at * HD + d) = acc;
-                if (d == 0) {
-                    P.part_ml[at * 2] = M;
-                    P.part_ml[at * 2 + 1] = L;
-                }
+        } else {
+            const size_t at = ((size_t)blockIdx.x * 2 + (first > c0 ? 1 : 0)) * P.nrow + r;
+            *reinterpret_cast<float4*>(P.part_o + at * HD + d) = acc;
+            if (d == 0) {
+                P.part_ml[at * 2] = M;
+                P.part_ml[at * 2 + 1] = L;
             }
         }
-        a0 = a1;
     }
 }
 
@@ -617,7 +645,7 @@ __global__ void __launch_bounds__(KD_WARPS * 32) k_kv8_combine(const __grid_cons
     int w0 = 0, w1 = 0, first = 0;
     long long items = 0;
     if (!P.pair_mode) {
-        kd_prefix(p, P.B, cum, ws);
+        kd_prefix(p, P.B, cum, ws, nullptr);
         items = (long long)cum[P.B] * H;
         const int np = cum[b + 1] - cum[b];
         first = cum[b] * H + head * np;
@@ -815,7 +843,7 @@ __device__ __forceinline__ void sts128(uint32_t at, uint32_t a, uint32_t b, uint
 // Rows [row0, row0 + 128) of an entry's (token, head) rows as a swizzled fp16 operand, by four warps
 // (w = 0 .. 3), fetched into registers and stored in two steps: HD / 8 lanes take a row's 16-byte
 // chunks, so a request covers whole rows. A bf16 row is divided by the power of two of its largest
-// value (see load_q), which goes to put(row, mul); rows past the entry are zeros.
+// value (see row_operand), which goes to put(row, mul); rows past the entry are zeros.
 template <int HD>
 struct QTile {
     static constexpr int LPR = HD / 8, RPI = 32 / LPR, NI = 32 / RPI;  // lanes a row, rows a request, requests a warp
@@ -1550,11 +1578,11 @@ Plan make_plan(const qw_kv8* kv, int B, int T, int max_len, int max_keys, int n_
     q.decode = rows <= 16;
     if (q.decode) {
         q.nrow = (int)rows;
-        const int slots = 2 * KD_WARPS * q.nrow * (HD + 2) * 4;
+        const int slots = 2 * KD_WARPS * q.nrow * (HD + 2) * 4, ent = B * 8;
         // two CTAs an SM where their rings and slots fit (rows <= 4 at head_dim 128), else one
-        const int per_sm = KD_WARPS * 2 * BLK + slots <= 106 * 1024 && rows <= 8 ? 2 : 1;
-        q.stages = std::min(8, ((per_sm == 2 ? 106 : 200) * 1024 - slots) / (KD_WARPS * BLK));
-        q.smem = KD_WARPS * q.stages * BLK + slots;
+        const int per_sm = KD_WARPS * 2 * BLK + slots + ent <= 106 * 1024 && rows <= 8 ? 2 : 1;
+        q.stages = std::min(8, ((per_sm == 2 ? 106 : 200) * 1024 - slots - ent) / (KD_WARPS * BLK));
+        q.smem = KD_WARPS * q.stages * BLK + slots + ent;
         q.pair_mode = max_keys <= 512;
         q.n_cta = q.pair_mode ? B * kv->n_kv_heads : per_sm * sm_count();
         // a row's logits are written and read once (8 bytes a key) instead of its K (HD bytes)
