@@ -75,6 +75,8 @@ __global__ void __launch_bounds__(KA_WARPS * 32) k_kv8_append(const __grid_const
     const int lane = threadIdx.x & 31, b = blockIdx.y;
     const int job = blockIdx.x * KA_WARPS + (threadIdx.x >> 5);
     const int which = job & 1, head = (job >> 1) % p.kv.n_kv, pi = (job >> 1) / p.kv.n_kv;
+    pdl_wait();
+    pdl_launch();
     if (pi >= p.pages) return;
     int s, r0, n;
     if (!kv8_entry(p.kv, p.start, p.cu, b, p.T, p.max_len, s, r0, n)) {
@@ -175,6 +177,8 @@ __global__ void __launch_bounds__(KA_WARPS * 32) k_kv8_read(const __grid_constan
     const int lane = threadIdx.x & 31, b = blockIdx.y;
     const int job = blockIdx.x * KA_WARPS + (threadIdx.x >> 5);
     const int which = job & 1, head = (job >> 1) % p.kv.n_kv, pi = (job >> 1) / p.kv.n_kv;
+    pdl_wait();
+    pdl_launch();
     if (pi >= p.pages) return;
     int s, r0, n;
     if (!kv8_entry(p.kv, p.start, p.cu, b, p.T, p.max_len, s, r0, n)) {
@@ -212,7 +216,7 @@ __global__ void __launch_bounds__(KA_WARPS * 32) k_kv8_read(const __grid_constan
 
 template <typename P, typename K>
 cudaError_t launch_pages(K kern, const P& p, int B, int n_kv, cudaStream_t st) {
-    LaunchCtx c = {st, false, nullptr};
+    LaunchCtx c = {st, true, nullptr};
     const long long jobs = 2ll * p.pages * n_kv;
     return launch_k(c, kern, dim3((unsigned)((jobs + KA_WARPS - 1) / KA_WARPS), B), dim3(KA_WARPS * 32), 0, p);
 }

@@ -317,11 +317,12 @@ __global__ void __launch_bounds__(KD_WARPS * 32, NT == 1 ? 2 : 1) k_kv8_decode(c
     __shared__ int cum[QW_KV8_MAX_BATCH + 1];
     __shared__ int ws[KD_WARPS], slot_pair[2 * KD_WARPS], s_abort;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+    pdl_wait();
+    pdl_launch();
     const int H = p.kv.n_kv, S = P.stages;
     float* slot_o = reinterpret_cast<float*>(kd_smem + (size_t)KD_WARPS * S * BLK);  // [warps][2][nrow][HD]
     float* slot_ml = slot_o + (size_t)2 * KD_WARPS * P.nrow * HD;                    // [warps][2][nrow][2]
     int2* ent = reinterpret_cast<int2*>(slot_ml + (size_t)2 * KD_WARPS * P.nrow * 2);
-    if (!P.pair_mode) pdl_launch();
     if (lane == 0)
         for (int i = 0; i < S; ++i) mbar_init(smem_u32(&bars[warp][i]), 1);
     if (tid == 0) {
@@ -638,13 +639,14 @@ __global__ void __launch_bounds__(KD_WARPS * 32) k_kv8_combine(const __grid_cons
     __shared__ float s_z[16];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, H = p.kv.n_kv;
     const int b = blockIdx.x / H, head = blockIdx.x % H, key0 = blockIdx.y * KC_KEYS;
+    pdl_launch();
     int s, r0, n;
-    if (!attn_entry(p, b, s, r0, n) || n == 0 || key0 >= s + n) return;
+    const bool on = attn_entry(p, b, s, r0, n) && n > 0 && key0 < s + n;
     const int rows = n * p.G;
     bool split = false;
     int w0 = 0, w1 = 0, first = 0;
     long long items = 0;
-    if (!P.pair_mode) {
+    if (on && !P.pair_mode) {
         kd_prefix(p, P.B, cum, ws, nullptr);
         items = (long long)cum[P.B] * H;
         const int np = cum[b + 1] - cum[b];
@@ -653,8 +655,8 @@ __global__ void __launch_bounds__(KD_WARPS * 32) k_kv8_combine(const __grid_cons
         w1 = (int)((((long long)first + np) * P.n_cta - 1) / items);
         split = w1 > w0;
     }
-    if (!split && !p.score_out) return;
-    pdl_wait();
+    pdl_wait();  // in every CTA: what follows this kernel must not pass the one before it
+    if (!on || (!split && !p.score_out)) return;
     const bool merge = split && blockIdx.y == 0;
     if (split) {
         float2* ml = reinterpret_cast<float2*>(kc_o + (size_t)KD_WARPS * P.nrow * HD);
@@ -901,6 +903,8 @@ __global__ void __launch_bounds__(CT_THREADS, 1) k_kv8_chunk(const __grid_consta
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 30);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     float4* scales = reinterpret_cast<float4*>(sm + Ct<HD>::OFF_SC);  // [8][8]: 2^ek, ev, 2^-ev of the pages of step i % 8
+    pdl_wait();
+    pdl_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int b = blockIdx.y, head = blockIdx.x;
     const int tile = (P.tiles + 1) / 2 - 1 - (int)(blockIdx.z / P.splits), split = blockIdx.z % P.splits;  // the longest rows start first
@@ -1291,9 +1295,10 @@ template <int HD, int DT>
 __global__ void __launch_bounds__(256) k_kv8_chunk_combine(const __grid_constant__ Kv8ChunkP P) {
     const Kv8AttnP& p = P.a;
     const int lane = threadIdx.x & 31, b = blockIdx.z, head = blockIdx.y, row = blockIdx.x * 8 + (threadIdx.x >> 5);
+    pdl_wait();
+    pdl_launch();
     int s, r0, n;
     if (!attn_entry(p, b, s, r0, n) || row >= n * p.G) return;
-    pdl_wait();
     const size_t part = (((size_t)b * p.kv.n_kv + head) * P.tiles + row / CT_ROWS) * P.splits;
     float M = -1e30f, L = 0.f;
     for (int k = 0; k < P.splits; ++k) M = fmaxf(M, P.part_ml[((part + k) * CT_ROWS + row % CT_ROWS) * 2]);
@@ -1359,6 +1364,8 @@ __global__ void __launch_bounds__(CS_THREADS, 2) k_kv8_score(const __grid_consta
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int b = blockIdx.z, head = blockIdx.y, key0 = blockIdx.x * Cs<HD>::KEYS;
+    pdl_wait();
+    pdl_launch();
     int s, r0, n;
     if (!attn_entry(p, b, s, r0, n) || n == 0 || key0 >= s + n) return;
     const int rows = n * p.G, kend = s + n;
@@ -1616,7 +1623,7 @@ cudaError_t allow_smem(K kern, int bytes) {
 
 template <int HD, int DT>
 cudaError_t run_score(const Kv8AttnP& p, int B, cudaStream_t st) {
-    LaunchCtx c = {st, false, nullptr};
+    LaunchCtx c = {st, true, nullptr};
     if (cudaError_t e = allow_smem(k_kv8_score<HD, DT>, Cs<HD>::SMEM)) return e;
     const unsigned tiles = (unsigned)((p.max_keys + Cs<HD>::KEYS - 1) / Cs<HD>::KEYS);
     return launch_k(c, k_kv8_score<HD, DT>, dim3(tiles, p.kv.n_kv, B), dim3(CS_THREADS), (size_t)Cs<HD>::SMEM, p);
@@ -1624,7 +1631,7 @@ cudaError_t run_score(const Kv8AttnP& p, int B, cudaStream_t st) {
 
 template <int HD, int DT>
 cudaError_t run_attn(const Kv8AttnP& p, const Plan& q, int B, char* ws, cudaStream_t st) {
-    LaunchCtx c = {st, false, nullptr};
+    LaunchCtx c = {st, true, nullptr};
     cudaError_t e;
     if (q.decode) {
         Kv8DecP P = {};
@@ -1644,7 +1651,6 @@ cudaError_t run_attn(const Kv8AttnP& p, const Plan& q, int B, char* ws, cudaStre
         if (!q.tbuf) P.a.score_out = nullptr;
         if (!q.pair_mode || q.tbuf) {
             const unsigned chunks = q.tbuf ? (unsigned)((p.max_keys + KC_KEYS - 1) / KC_KEYS) : 1;
-            if (!q.pair_mode) c.pdl = true;
             const int smem = q.pair_mode ? 0 : kc_smem(q.nrow, HD);
             if ((e = allow_smem(k_kv8_combine<HD, DT>, smem)) != cudaSuccess) return e;
             e = launch_k(c, k_kv8_combine<HD, DT>, dim3(B * p.kv.n_kv, chunks), dim3(KD_WARPS * 32), (size_t)smem, P);

@@ -1,11 +1,20 @@
 // Eviction from the 8-bit paged KV cache by accumulated attention weight (qw_kv8_evict).
 //
-// For each (entry, KV head) of L > n_keep tokens: the m = n_keep - n_recent largest scores among
-// the first L - n_recent positions are found by a radix select over sortable 32-bit keys (8 bits a
-// pass, integer counts, so ties and order are exact), the kept positions are written in
-// ascending order by a scan, and the rows and scores move to positions 0 .. n_keep - 1. New
-// position j takes the row of kept[j] >= j, so moving page after page in order, with a barrier
-// between a batch's reads and its writes, is safe in place.
+// For each (entry, KV head) of L > n_keep tokens, the m = n_keep - n_recent largest scores among the
+// first L - n_recent positions are kept, with the last n_recent; the kept rows and their scores move
+// to positions 0 .. n_keep - 1 in order. Bytes bound it: the scores once, the kept rows in and out.
+//
+// k_kv8_select finds the positions: a radix select over sortable 32-bit keys (8 bits a pass,
+// integer counts, so ties and order are exact), then a scan writes them in ascending order. The
+// select is a chain of passes, so long entries get a cluster of C CTAs a head, which keep their
+// slices of the keys in shared memory and add each other's 256-bin histograms through distributed
+// shared memory (2048 bins, one pass less, cost 60 us a pass in remote loads).
+// k_kv8_move copies rows and scores to their new places, all of them at once.
+// k_kv8_move_inplace does it where source and destination are the same memory: new position j takes
+// the row of kept[j] >= j, so one CTA a head moves batches of ascending pages with a barrier between
+// a batch's reads and its writes. (One kernel of clusters for everything took 243 us for 28 layers of
+// 4k tokens halved; the two take 80.) k_kv8_evict_one does both for short entries, where a second
+// launch would cost more than it moves.
 #include "kv8.cuh"
 
 #include <algorithm>
@@ -13,6 +22,11 @@
 namespace {
 
 constexpr int EV_T = 512, EV_W = EV_T / 32;
+constexpr int EV_BINS = 256;
+constexpr int EV_CAP = 6144;           // keys of a CTA's slice kept in shared memory; the rest is read again
+constexpr int EV_C = 8;                // CTAs of a long entry's cluster
+constexpr int EV_ONE_CTA = 6144;       // longest entry (max_len) whose positions one CTA selects
+constexpr int EV_ONE_KEEP = 512;       // most kept tokens that the same CTA moves (two rounds of its warps)
 
 struct Kv8EvictP {
     Kv8View kv;
@@ -58,138 +72,300 @@ __device__ __forceinline__ int ev_scan(int v, int* ws, int& total) {
     return before + s - v;
 }
 
-template <int HD>
-__global__ void __launch_bounds__(EV_T) k_kv8_evict(const __grid_constant__ Kv8EvictP p) {
-    constexpr int CH = Kv8<HD>::CH, TSTEP = 32 / CH, UPL = KV8_PAGE / TSTEP;
-    __shared__ int hist[EV_W][256];
+// Barrier of the cluster's CTAs (of the CTA for C = 1), ordering shared and global memory.
+template <int C>
+__device__ __forceinline__ void ev_sync() {
+    if (C == 1)
+        __syncthreads();
+    else
+        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The 32-bit word at `p` (this CTA's shared memory) in CTA `rank` of the cluster.
+template <int C>
+__device__ __forceinline__ int ev_peer(const int* p, int rank) {
+    if (C == 1) return *p;
+    uint32_t a = (uint32_t)__cvta_generic_to_shared(p);
+    int v;
+    asm volatile("{\n\t.reg .b32 t;\n\tmapa.shared::cluster.u32 t, %1, %2;\n\tld.shared::cluster.s32 %0, [t];\n\t}"
+                 : "=r"(v)
+                 : "r"(a), "r"(rank)
+                 : "memory");
+    return v;
+}
+
+// Writes kept and new_len of (entry b, head); false if the entry is left out.
+template <int C>
+__device__ __forceinline__ bool select_kept(const Kv8EvictP& p, int rank, int head, int b) {
+    __shared__ uint32_t keys[EV_CAP];
+    __shared__ int hist[EV_W][EV_BINS];  // a warp its own: equal scores would queue on one bin
+    __shared__ int sums[2][EV_BINS];
     __shared__ int ws[EV_W];
-    __shared__ int s_digit, s_above, s_bad;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int head = blockIdx.x, b = blockIdx.y;
+    __shared__ int s_digit, s_above, s_bad, pub[2];
+    const int tid = threadIdx.x, warp = tid >> 5;
     const int L = p.len[b];
     const int* table = p.kv.table + (size_t)b * p.kv.max_pages;
     const int* dst = p.dst + (size_t)b * p.kv.max_pages;
     const float* score = p.score + ((size_t)b * p.kv.n_kv + head) * p.ld_score;
-    float* score_out = p.score_out + ((size_t)b * p.kv.n_kv + head) * p.ld_score;
     int* kept = p.kept + ((size_t)b * p.kv.n_kv + head) * p.keep;
     const int n = min(L, p.keep);
-
-    if (tid == 0) s_bad = L < 0 || L > p.max_len || (long long)L > (long long)p.kv.max_pages * KV8_PAGE;
+    const int m = p.keep - p.recent, cand = max(0, L - p.recent);  // m of the first cand positions are kept
+    const bool fits = L >= 0 && L <= p.max_len && (long long)L <= (long long)p.kv.max_pages * KV8_PAGE;
+    const bool select = fits && L > p.keep && m > 0;
+    const int slice = (cand + C - 1) / C, k0 = min(cand, rank * slice), nk = min(cand, k0 + slice) - k0;
+    if (tid == 0) s_bad = !fits;
+    if (select)
+        for (int j = tid; j < min(nk, EV_CAP); j += EV_T) keys[j] = ev_key(score[k0 + j]);
+    for (int i = tid; i < EV_W * EV_BINS; i += EV_T) hist[0][i] = 0;
     __syncthreads();
-    if (!s_bad) {
+    // the entry's pages: every CTA of the cluster comes to the same answer
+    if (fits)
         for (int i = tid; i * KV8_PAGE < L; i += EV_T)
-            if (table[i] < 0 || table[i] >= p.kv.n_pages || (i * KV8_PAGE < n && (dst[i] < 0 || dst[i] >= p.kv.n_pages)))
-                s_bad = 1;
-    }
+            if (table[i] < 0 || table[i] >= p.kv.n_pages || (i * KV8_PAGE < n && (dst[i] < 0 || dst[i] >= p.kv.n_pages))) s_bad = 1;
     __syncthreads();
-    const bool bad = s_bad;
-    if (bad) {
-        if (tid == 0) atomicOr(p.status, QW_KV8_BAD_POS);
-        for (int j = tid; j < p.keep; j += EV_T) kept[j] = -1;
-        if (head == 0 && tid == 0) p.new_len[b] = L;
-        return;
+    if (s_bad) {
+        if (rank == 0) {
+            if (tid == 0) atomicOr(p.status, QW_KV8_BAD_POS);
+            for (int j = tid; j < p.keep; j += EV_T) kept[j] = -1;  // nothing moves
+            if (head == 0 && tid == 0) p.new_len[b] = L;
+        }
+        return false;
     }
+    auto key = [&](int j) { return j < EV_CAP ? keys[j] : ev_key(score[k0 + j]); };
+    if (head == 0 && rank == 0 && tid == 0) p.new_len[b] = n;
     if (L <= p.keep) {
-        for (int j = tid; j < p.keep; j += EV_T) kept[j] = j < L ? j : -1;
-    } else {
-        const int m = p.keep - p.recent, C = L - p.recent;
-        uint32_t prefix = 0;
-        int need = m;  // of the keys that match the prefix
-        for (int shift = 24; shift >= 0 && m > 0; shift -= 8) {
-            for (int i = tid; i < EV_W * 256; i += EV_T) (&hist[0][0])[i] = 0;
-            __syncthreads();
-            for (int j = tid; j < C; j += EV_T) {
-                const uint32_t k = ev_key(score[j]);
-                if (shift == 24 || (k >> (shift + 8)) == prefix) atomicAdd(&hist[warp][(k >> shift) & 255], 1);
-            }
-            __syncthreads();
-            int cnt = 0;
-            if (tid < 256)
-                for (int w = 0; w < EV_W; ++w) cnt += hist[w][255 - tid];  // thread t: digit 255 - t
-            int total;
-            const int above = ev_scan(cnt, ws, total);
-            if (above < need && above + cnt >= need) {
-                s_digit = 255 - tid;
-                s_above = above;
-            }
-            __syncthreads();
-            prefix = (prefix << 8) | (uint32_t)s_digit;
-            need -= s_above;
-            __syncthreads();
-        }
-        int gt0 = 0, tie0 = 0;
-        for (int j0 = 0; j0 < C && m > 0; j0 += EV_T) {
-            const int j = j0 + tid;
-            const uint32_t k = j < C ? ev_key(score[j]) : 0u;
-            const int gt = j < C && k > prefix, tie = j < C && k == prefix;
-            int total;
-            const int before = ev_scan(gt | (tie << 16), ws, total);
-            const int gb = gt0 + (before & 0xFFFF), tb = tie0 + (before >> 16);
-            if (gt || (tie && tb < need)) kept[gb + min(tb, need)] = j;
-            gt0 += total & 0xFFFF;
-            tie0 += total >> 16;
-        }
-        for (int i = tid; i < p.recent; i += EV_T) kept[m + i] = C + i;
+        for (int j = rank * EV_T + tid; j < p.keep; j += C * EV_T) kept[j] = j < L ? j : -1;
+        return true;
     }
-    if (head == 0 && tid == 0) p.new_len[b] = n;
-    __syncthreads();
-    // ---- scores ----
-    if (L > p.keep || score_out != score) {
-        for (int j0 = 0; j0 < n; j0 += EV_T) {
-            const int j = j0 + tid;
-            const float v = j < n ? score[kept[j]] : 0.f;
-            __syncthreads();
-            if (j < n) score_out[j] = v;
+    for (int i = rank * EV_T + tid; i < p.recent; i += C * EV_T) kept[m + i] = cand + i;
+    if (!select) return true;
+    uint32_t prefix = 0;
+    int need = m;  // of the keys that match the prefix
+    for (int shift = 24; shift >= 0; shift -= 8) {
+        for (int j = tid; j < nk; j += EV_T) {
+            const uint32_t k = key(j);
+            if (shift == 24 || (k >> (shift + 8)) == prefix) atomicAdd(&hist[warp][(k >> shift) & 255], 1);
         }
         __syncthreads();
-        for (int j = n + tid; j < L; j += EV_T) score_out[j] = 0.f;
-    }
-    if (L <= p.keep && p.in_place) return;
-    // ---- rows: a warp moves one tensor of one destination page ----
-    const int which = warp & 1, ch = lane % CH, t0 = lane / CH;
-    for (int d0 = 0; d0 * KV8_PAGE < n; d0 += EV_W / 2) {
-        const int d = d0 + (warp >> 1);
-        const bool on = d * KV8_PAGE < n;
-        uint4 code[UPL];
-        float sc[UPL];
-        if (on) {
+        int* mine = sums[(shift >> 3) & 1];  // two in turn: the other is read until the next barrier
+        const int digit = EV_BINS - 1 - tid;  // thread t < 256: the t-th largest digit
+        if (tid < EV_BINS) {
+            int c = 0;
 #pragma unroll
-            for (int u = 0; u < UPL; ++u) {
-                const int j = d * KV8_PAGE + t0 + u * TSTEP;
-                code[u] = make_uint4(0u, 0u, 0u, 0u);
-                sc[u] = 0.f;
-                if (j < n) {
-                    const int src = kept[j], t = src % KV8_PAGE;
-                    const uint8_t* blk = p.kv.blocks + ((size_t)table[src / KV8_PAGE] * p.kv.n_kv + head) * Kv8<HD>::BLK;
-                    const int at = which ? kv8_v_pos<HD>(t, ch) : kv8_k_pos<HD>(t, ch);
-                    code[u] = *reinterpret_cast<const uint4*>(blk + (which ? Kv8<HD>::VOFF : 0) + t * HD + at * 16);
-                    sc[u] = reinterpret_cast<const float*>(blk + Kv8<HD>::SOFF)[which];
-                }
+            for (int w = 0; w < EV_W; ++w) {
+                c += hist[w][digit];
+                hist[w][digit] = 0;
             }
+            mine[digit] = c;
+        }
+        ev_sync<C>();
+        int cnt = 0;
+        if (tid < EV_BINS)
+#pragma unroll
+            for (int r = 0; r < C; ++r) cnt += ev_peer<C>(mine + digit, r);
+        int total;
+        const int above = ev_scan(cnt, ws, total);
+        if (above < need && above + cnt >= need) {
+            s_digit = digit;
+            s_above = above;
         }
         __syncthreads();
-        if (on) {
+        prefix = (prefix << 8) | (uint32_t)s_digit;
+        need -= s_above;
+        __syncthreads();
+    }
+    // ---- kept positions in order: thread t looks at a run of the slice ----
+    const int per = (nk + EV_T - 1) / EV_T, a0 = min(nk, tid * per), a1 = min(nk, a0 + per);
+    int gt = 0, tie = 0;
+    for (int j = a0; j < a1; ++j) {
+        const uint32_t k = key(j);
+        gt += k > prefix;
+        tie += k == prefix;
+    }
+    int gt_all, tie_all;
+    int gb = ev_scan(gt, ws, gt_all), tb = ev_scan(tie, ws, tie_all);
+    if (C > 1) {
+        if (tid == 0) {
+            pub[0] = gt_all;
+            pub[1] = tie_all;
+        }
+        ev_sync<C>();
+        for (int r = 0; r < rank; ++r) {
+            gb += ev_peer<C>(pub, r);
+            tb += ev_peer<C>(pub + 1, r);
+        }
+    }
+    for (int j = a0; j < a1; ++j) {
+        const uint32_t k = key(j);
+        const bool t = k == prefix;
+        if (k > prefix || (t && tb < need)) kept[gb + min(tb, need)] = k0 + j;
+        gb += k > prefix;
+        tb += t;
+    }
+    if (C > 1) ev_sync<C>();  // no CTA leaves while another may read its shared memory
+    return true;
+}
+
+template <int C>
+__global__ void __launch_bounds__(EV_T) k_kv8_select(const __grid_constant__ Kv8EvictP p) {
+    pdl_wait();
+    pdl_launch();
+    select_kept<C>(p, blockIdx.x % C, blockIdx.x / C, blockIdx.y);
+}
+
+// One destination page (K and V), by one warp: fetch its rows' codes, then store them under the
+// page's own exponents.
+template <int HD>
+struct RowMove {
+    static constexpr int CH = Kv8<HD>::CH, TSTEP = 32 / CH, UPL = KV8_PAGE / TSTEP;
+    uint4 code[2][UPL];
+    float2 sc[UPL];
+    __device__ __forceinline__ void fetch(const Kv8EvictP& p, const int* table, const int* kept, int head, int d, int n, int lane) {
+        const int ch = lane % CH, t0 = lane / CH;
+        int src[UPL], pg[UPL];
+#pragma unroll
+        for (int u = 0; u < UPL; ++u) {
+            const int j = d * KV8_PAGE + t0 + u * TSTEP;
+            src[u] = j < n ? kept[j] : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < UPL; ++u) pg[u] = src[u] >= 0 ? table[src[u] / KV8_PAGE] : 0;
+#pragma unroll
+        for (int u = 0; u < UPL; ++u) {
+            code[0][u] = code[1][u] = make_uint4(0u, 0u, 0u, 0u);
+            sc[u] = make_float2(0.f, 0.f);
+            if (src[u] < 0) continue;
+            const int t = src[u] % KV8_PAGE;
+            const uint8_t* blk = p.kv.blocks + ((size_t)pg[u] * p.kv.n_kv + head) * Kv8<HD>::BLK;
+            code[0][u] = *reinterpret_cast<const uint4*>(blk + t * HD + kv8_k_pos<HD>(t, ch) * 16);
+            code[1][u] = *reinterpret_cast<const uint4*>(blk + Kv8<HD>::VOFF + t * HD + kv8_v_pos<HD>(t, ch) * 16);
+            sc[u] = *reinterpret_cast<const float2*>(blk + Kv8<HD>::SOFF);
+        }
+    }
+    __device__ __forceinline__ void store(const Kv8EvictP& p, int page, int head, int lane) {
+        const int ch = lane % CH, t0 = lane / CH;
+        uint8_t* blk = p.kv.blocks + ((size_t)page * p.kv.n_kv + head) * Kv8<HD>::BLK;
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
             float amax = 0.f;
 #pragma unroll
             for (int u = 0; u < UPL; ++u) {
                 float x[16];
-                kv8_dec16(code[u], x);
+                kv8_dec16(code[which][u], x);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]) * sc[u]);
+                for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]) * (which ? sc[u].y : sc[u].x));
             }
             const int e = kv8_exponent(warp_max(amax));
             const float mul = kv8_pow2(-e);
-            uint8_t* blk = p.kv.blocks + ((size_t)dst[d] * p.kv.n_kv + head) * Kv8<HD>::BLK;
 #pragma unroll
             for (int u = 0; u < UPL; ++u) {
                 const int t = t0 + u * TSTEP, at = which ? kv8_v_pos<HD>(t, ch) : kv8_k_pos<HD>(t, ch);
                 float x[16];
-                kv8_dec16(code[u], x);
-                *reinterpret_cast<uint4*>(blk + (which ? Kv8<HD>::VOFF : 0) + t * HD + at * 16) = kv8_enc16(x, sc[u] * mul);
+                kv8_dec16(code[which][u], x);
+                *reinterpret_cast<uint4*>(blk + (which ? Kv8<HD>::VOFF : 0) + t * HD + at * 16) =
+                    kv8_enc16(x, (which ? sc[u].y : sc[u].x) * mul);
             }
             if (lane == 0) reinterpret_cast<float*>(blk + Kv8<HD>::SOFF)[which] = kv8_pow2(e);
         }
     }
+};
+
+constexpr int MV_W = 8;
+// blockIdx.x < row_ctas: MV_W pages of one (entry, head); above: 4 MV_W * 32 of its scores.
+template <int HD>
+__global__ void __launch_bounds__(MV_W * 32) k_kv8_move(const __grid_constant__ Kv8EvictP p, int row_ctas, bool scores) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, head = blockIdx.y, b = blockIdx.z;
+    const int* kept = p.kept + ((size_t)b * p.kv.n_kv + head) * p.keep;
+    pdl_wait();
+    pdl_launch();
+    const int L = p.len[b], n = min(L, p.keep);
+    if (L <= 0 || kept[0] < 0) return;  // empty, or an entry left out
+    if ((int)blockIdx.x < row_ctas) {
+        const int d = blockIdx.x * MV_W + warp;
+        if (d * KV8_PAGE >= n) return;
+        RowMove<HD> mv;
+        mv.fetch(p, p.kv.table + (size_t)b * p.kv.max_pages, kept, head, d, n, lane);
+        mv.store(p, p.dst[(size_t)b * p.kv.max_pages + d], head, lane);
+    } else if (scores) {
+        const int j0 = ((int)blockIdx.x - row_ctas) * 4 * MV_W * 32 + tid;
+        const float* score = p.score + ((size_t)b * p.kv.n_kv + head) * p.ld_score;
+        float* out = p.score_out + ((size_t)b * p.kv.n_kv + head) * p.ld_score;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int j = j0 + u * MV_W * 32;
+            if (j < L) out[j] = j < n ? score[kept[j]] : 0.f;
+        }
+    }
+}
+
+// Moves the scores and rows of (entry b, head), by one CTA, in an order that is safe within one memory.
+template <int HD>
+__device__ __forceinline__ void move_ordered(const Kv8EvictP& p, int head, int b, bool scores, bool rows) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int* kept = p.kept + ((size_t)b * p.kv.n_kv + head) * p.keep;
+    const int L = p.len[b], n = min(L, p.keep);
+    if (scores) {
+        const float* score = p.score + ((size_t)b * p.kv.n_kv + head) * p.ld_score;
+        float* out = p.score_out + ((size_t)b * p.kv.n_kv + head) * p.ld_score;
+        for (int j0 = 0; j0 < n; j0 += EV_T) {
+            const int j = j0 + tid;
+            const float v = j < n ? score[kept[j]] : 0.f;
+            __syncthreads();
+            if (j < n) out[j] = v;
+        }
+        __syncthreads();
+        for (int j = n + tid; j < L; j += EV_T) out[j] = 0.f;
+    }
+    if (!rows) return;
+    const int* table = p.kv.table + (size_t)b * p.kv.max_pages;
+    const int* dst = p.dst + (size_t)b * p.kv.max_pages;
+    for (int d0 = 0; d0 * KV8_PAGE < n; d0 += EV_W) {
+        const int d = d0 + warp;
+        RowMove<HD> mv;
+        mv.fetch(p, table, kept, head, d, n, lane);
+        __syncthreads();
+        if (d * KV8_PAGE < n) mv.store(p, dst[d], head, lane);
+    }
+}
+
+// What is moved within one memory: rows (p.in_place), scores (score_out == score), or both.
+template <int HD>
+__global__ void __launch_bounds__(EV_T) k_kv8_move_inplace(const __grid_constant__ Kv8EvictP p) {
+    const int head = blockIdx.x, b = blockIdx.y;
+    pdl_wait();
+    pdl_launch();
+    if (p.len[b] <= p.keep || p.kept[((size_t)b * p.kv.n_kv + head) * p.keep] < 0) return;  // nothing to move
+    move_ordered<HD>(p, head, b, p.score_out == p.score, p.in_place);
+}
+
+template <int HD>
+__global__ void __launch_bounds__(EV_T) k_kv8_evict_one(const __grid_constant__ Kv8EvictP p) {
+    const int head = blockIdx.x, b = blockIdx.y;
+    pdl_wait();
+    pdl_launch();
+    if (!select_kept<1>(p, 0, head, b)) return;
+    __syncthreads();
+    const bool same = p.len[b] <= p.keep;  // every token stays: what is in place is left alone
+    move_ordered<HD>(p, head, b, !(same && p.score_out == p.score), !(same && p.in_place));
+}
+
+template <int HD>
+cudaError_t run_evict(const Kv8EvictP& p, int B, cudaStream_t st) {
+    LaunchCtx c = {st, true, nullptr};
+    if (p.max_len <= EV_ONE_CTA && std::min(p.keep, p.max_len) <= EV_ONE_KEEP)
+        return launch_k(c, k_kv8_evict_one<HD>, dim3(p.kv.n_kv, B), dim3(EV_T), 0, p);
+    cudaError_t e = p.max_len <= EV_ONE_CTA ? launch_k(c, k_kv8_select<1>, dim3(p.kv.n_kv, B), dim3(EV_T), 0, p)
+                                            : launch_kc(c, k_kv8_select<EV_C>, dim3(EV_C * p.kv.n_kv, B), dim3(EV_T), 0, EV_C, p);
+    if (e != cudaSuccess) return e;
+    const bool alias = p.score_out == p.score;
+    if (!p.in_place || !alias) {
+        const int pages = (std::min(p.keep, p.max_len) + KV8_PAGE - 1) / KV8_PAGE;
+        const int row_ctas = p.in_place ? 0 : (pages + MV_W - 1) / MV_W;
+        const int score_ctas = alias ? 0 : (p.max_len + 4 * MV_W * 32 - 1) / (4 * MV_W * 32);
+        e = launch_k(c, k_kv8_move<HD>, dim3(row_ctas + score_ctas, p.kv.n_kv, B), dim3(MV_W * 32), 0, p, row_ctas, !alias);
+        if (e != cudaSuccess) return e;
+    }
+    if (p.in_place || alias) e = launch_k(c, k_kv8_move_inplace<HD>, dim3(p.kv.n_kv, B), dim3(EV_T), 0, p);
+    return e;
 }
 
 }  // namespace
@@ -210,9 +386,7 @@ extern "C" qw_status qw_kv8_evict(const qw_kv8* kv, int B, int max_len, const in
     Kv8EvictP p = {kv8_view(kv), dev_len, dev_dst_table ? dev_dst_table : kv->dev_page_table,
                    !dev_dst_table || dev_dst_table == kv->dev_page_table, max_len, n_keep, n_recent, dev_score, dev_score_out,
                    ld_score, dev_kept, dev_new_len, dev_status};
-    LaunchCtx c = {(cudaStream_t)stream, false, nullptr};
-    const dim3 grid(kv->n_kv_heads, B);
-    const cudaError_t e = kv->head_dim == 128 ? launch_k(c, k_kv8_evict<128>, grid, dim3(EV_T), 0, p)
-                                              : launch_k(c, k_kv8_evict<64>, grid, dim3(EV_T), 0, p);
+    cudaStream_t st = (cudaStream_t)stream;
+    const cudaError_t e = kv->head_dim == 128 ? run_evict<128>(p, B, st) : run_evict<64>(p, B, st);
     return e == cudaSuccess ? QW_OK : qw_fail(QW_ERR_CUDA, "evict: %s", cudaGetErrorString(e));
 }

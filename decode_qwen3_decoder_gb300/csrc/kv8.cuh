@@ -8,6 +8,10 @@
 
 #include "qw_internal.h"
 
+// Every kernel here is launched with programmatic stream serialization, and each of its CTAs waits for
+// the kernels before it (pdl_wait) before it reads anything or ends: a CTA that ended without
+// waiting could let the kernel after this one start before the one in front has finished.
+
 namespace {
 
 constexpr int KV8_PAGE = 16;

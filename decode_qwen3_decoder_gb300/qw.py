@@ -140,10 +140,18 @@ def _ints(vals: Sequence[int]):
     return arr
 
 
+_current_stream = None  # the current stream's handle of the current device
+
+
 def _stream(stream) -> int:
+    global _current_stream
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _current_stream is None:
+            import torch
+            raw, dev = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+            torch.cuda.init()
+            _current_stream = lambda: raw(dev())  # noqa: E731
+        return _current_stream()
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 

@@ -467,9 +467,9 @@ qw_status qw_kv8_attn(const qw_kv8* kv, const qw_kv8_attn_args* args, void* stre
  * position had (-1 past the new length), dev_new_len[b] min(dev_len[b], n_keep), and
  * dev_score_out (may be dev_score) the kept scores, with zeros from the new length to
  * dev_len[b]. Keys keep the rotation of the position they were appended at. Entries within the
- * budget keep every token (copied when dev_dst_table is given). dev_dst_table must name other
- * pages than the entries' own, or the same ones in the same order; dev_new_len must not be
- * dev_len. */
+ * budget keep every token (copied when dev_dst_table is given). The pages of dev_dst_table must
+ * be other pages than those of any entry (pass NULL, not a copy of the table, to evict in place);
+ * dev_score_out is dev_score itself or other memory, and dev_new_len must not be dev_len. */
 qw_status qw_kv8_evict(const qw_kv8* kv, int B, int max_len, const int32_t* dev_len, int n_keep, int n_recent,
                        const int32_t* dev_dst_table, const float* dev_score, float* dev_score_out, size_t ld_score,
                        int32_t* dev_kept, int32_t* dev_new_len, int32_t* dev_status, void* stream);

@@ -369,6 +369,55 @@ def test_attention_captured_and_replayed_with_new_lengths(qw):
     assert c.bits() == 0
 
 
+def test_captured_behind_copies_and_other_streams(qw):
+    """Calls captured right after a copy, after a join with another captured stream, and after each
+    other: every one sees what came before it in the graph."""
+    import torch
+    c = Case(qw, [300, 40], 2, 128, seed=15)
+    c.append([0, 0], [300, 40])
+    k, v, ds, dc, T, ml = c.last
+    lens = np.array([300, 40])
+    q, qf = c.rows(2, 4, F16)
+    src = torch.zeros_like(q)
+    start, cu = c.i32(lens - 1), c.i32([0, 1, 2])
+    hk, hv = torch.zeros_like(k), torch.zeros_like(v)
+    out = torch.zeros((2, 512), dtype=torch.float16, device="cuda")
+    nb = c.qw.qw_kv8_attn_ws_bytes(c.view, 2, 2, 1, 304, 4, False)
+    ws = torch.zeros(nb, dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        hk.copy_(k)
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            hv.copy_(v)
+            src.copy_(q)
+        main.wait_stream(side)
+        c.qw.qw_kv8_append(c.view, 2, T, ml, ds.data_ptr(), dc.data_ptr(), hk.data_ptr(), 256, hv.data_ptr(), 256, c.qw.QW_F16, c.status.data_ptr())
+        c.qw.qw_kv8_attn(c.view, 2, 2, 1, 304, start.data_ptr(), cu.data_ptr(), src.data_ptr(), 512, 4, c.qw.QW_F16, 128 ** -0.5,
+                         out.data_ptr(), 512, 0, 0, 0, 0, ws.data_ptr(), nb, c.status.data_ptr())
+        again = out.clone()
+    for seed in range(3):
+        new = [torch.randn(x.shape, device="cuda").half() for x in (k, v, q)]
+        for x, y in zip((k, v, q), new):
+            x.copy_(y)
+        c.blocks.fill_(0x7F)
+        g.replay()
+        torch.cuda.synchronize()
+        at = 0
+        for b in range(2):
+            x = [y[at:at + lens[b]].double().cpu().numpy().reshape(-1, 2, 128) for y in new[:2]]
+            at += int(lens[b])
+            c.orc.append(c.table[b], 0, x)
+            want = c.orc.attention(c.table[b], int(lens[b]) - 1, new[2][b].double().cpu().numpy().reshape(1, 4, 128), 128 ** -0.5)
+            got = again[b].double().cpu().numpy().reshape(1, 4, 128)
+            assert np.all(np.abs(got - want[0]) <= want[3] * 2.0 ** -10 + np.abs(want[0]) * 2.0 ** -11 + 2.0 ** -24)
+        c.check_cache(lens.tolist())
+    assert c.bits() == 0
+
+
 def test_two_streams_with_their_own_workspaces(qw):
     import torch
     c = Case(qw, [900, 700], 2, 128, seed=12)
