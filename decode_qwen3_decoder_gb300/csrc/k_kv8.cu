@@ -22,6 +22,7 @@ struct Kv8AppendP {
     const void* src[2];
     size_t ld[2];
     int T, max_len, pages;  // pages: most pages an entry can touch
+    bool staged;            // source rows in pages of 16 tokens
     int* status;
 };
 
@@ -85,12 +86,12 @@ __global__ void __launch_bounds__(KA_WARPS * 32) k_kv8_append(const __grid_const
     }
     const int page_i = s / KV8_PAGE + pi;
     if (n == 0 || page_i * KV8_PAGE >= s + n) return;
-    const int page = p.kv.table[(size_t)b * p.kv.max_pages + page_i];
+    const int page = kv8_row(p.kv, p.kv.table, b)[page_i];
     if (page < 0 || page >= p.kv.n_pages) {
         if (lane == 0) atomicOr(p.status, QW_KV8_BAD_POS);
         return;
     }
-    uint8_t* blk = p.kv.blocks + ((size_t)page * p.kv.n_kv + head) * Kv8<HD>::BLK;
+    uint8_t* blk = kv8_block(p.kv, b, page, head, Kv8<HD>::BLK);
     uint8_t* codes = blk + (which ? Kv8<HD>::VOFF : 0);
     float* scale = reinterpret_cast<float*>(blk + Kv8<HD>::SOFF) + which;
     const int ch = lane % CH, t0 = lane / CH;
@@ -103,7 +104,10 @@ __global__ void __launch_bounds__(KA_WARPS * 32) k_kv8_append(const __grid_const
     for (int u = 0; u < UPL; ++u) {
         const int pos = page_i * KV8_PAGE + t0 + u * TSTEP;
         if (pos >= s && pos < s + n) {
-            load16<DT>(src, (size_t)(r0 + pos - s) * p.ld[which] + head * HD + ch * 16, x[u], bad);
+            const int row = r0 + pos - s;
+            const size_t at = p.staged ? (((size_t)(row >> 4) * p.kv.n_kv + head) * 16 + (row & 15)) * HD
+                                       : (size_t)row * p.ld[which] + head * HD;
+            load16<DT>(src, at + ch * 16, x[u], bad);
 #pragma unroll
             for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[u][i]));
         } else {
@@ -194,10 +198,10 @@ __global__ void __launch_bounds__(KA_WARPS * 32) k_kv8_read(const __grid_constan
     }
     const int page_i = s / KV8_PAGE + pi;
     if (n == 0 || page_i * KV8_PAGE >= s + n) return;
-    const int page = p.kv.table[(size_t)b * p.kv.max_pages + page_i];
+    const int page = kv8_row(p.kv, p.kv.table, b)[page_i];
     const bool ok = page >= 0 && page < p.kv.n_pages;
     if (!ok && lane == 0) atomicOr(p.status, QW_KV8_BAD_POS);
-    const uint8_t* blk = p.kv.blocks + ((size_t)(ok ? page : 0) * p.kv.n_kv + head) * Kv8<HD>::BLK;
+    const uint8_t* blk = kv8_block(p.kv, b, ok ? page : 0, head, Kv8<HD>::BLK);
     const uint8_t* codes = blk + (which ? Kv8<HD>::VOFF : 0);
     const float scale = reinterpret_cast<const float*>(blk + Kv8<HD>::SOFF)[which];
     const int ch = lane % CH, t0 = lane / CH;
@@ -215,8 +219,9 @@ __global__ void __launch_bounds__(KA_WARPS * 32) k_kv8_read(const __grid_constan
 }
 
 template <typename P, typename K>
-cudaError_t launch_pages(K kern, const P& p, int B, int n_kv, cudaStream_t st) {
-    LaunchCtx c = {st, true, nullptr};
+cudaError_t launch_pages(K kern, const P& p, int B, cudaStream_t st, int* launches) {
+    const int n_kv = p.kv.n_kv;
+    LaunchCtx c = {st, true, launches};
     const long long jobs = 2ll * p.pages * n_kv;
     return launch_k(c, kern, dim3((unsigned)((jobs + KA_WARPS - 1) / KA_WARPS), B), dim3(KA_WARPS * 32), 0, p);
 }
@@ -252,15 +257,23 @@ static qw_status kv8_rows_check(const qw_kv8* kv, int B, int T, int max_len, con
 }
 
 #define KV8_DISPATCH(kern, hd, dt, p)                                                                         \
-    ((hd) == 128 ? ((dt) == QW_F16    ? launch_pages(kern<128, QW_F16>, p, B, kv->n_kv_heads, st)             \
-                    : (dt) == QW_BF16 ? launch_pages(kern<128, QW_BF16>, p, B, kv->n_kv_heads, st)            \
-                                      : launch_pages(kern<128, QW_F32>, p, B, kv->n_kv_heads, st))            \
-                 : ((dt) == QW_F16    ? launch_pages(kern<64, QW_F16>, p, B, kv->n_kv_heads, st)              \
-                    : (dt) == QW_BF16 ? launch_pages(kern<64, QW_BF16>, p, B, kv->n_kv_heads, st)             \
-                                      : launch_pages(kern<64, QW_F32>, p, B, kv->n_kv_heads, st)))
+    ((hd) == 128 ? ((dt) == QW_F16    ? launch_pages(kern<128, QW_F16>, p, B, st, launches)             \
+                    : (dt) == QW_BF16 ? launch_pages(kern<128, QW_BF16>, p, B, st, launches)            \
+                                      : launch_pages(kern<128, QW_F32>, p, B, st, launches))            \
+                 : ((dt) == QW_F16    ? launch_pages(kern<64, QW_F16>, p, B, st, launches)              \
+                    : (dt) == QW_BF16 ? launch_pages(kern<64, QW_BF16>, p, B, st, launches)             \
+                                      : launch_pages(kern<64, QW_F32>, p, B, st, launches)))
 
 extern "C" size_t qw_kv8_block_bytes(int head_dim) {
     return head_dim == 64 || head_dim == 128 ? 32 * (size_t)head_dim + 32 : 0;
+}
+
+qw_status kv8_append(const Kv8View& v, int head_dim, int B, int T, int max_len, const int* start, const int* cu, const void* k,
+                     size_t ld_k, const void* val, size_t ld_v, int dtype, bool staged, int* status, cudaStream_t st, int* launches) {
+    const int len = std::min(max_len, T);
+    Kv8AppendP p = {v, start, cu, {k, val}, {ld_k, ld_v}, T, max_len, (len + 14) / 16 + 1, staged, status};
+    cudaError_t e = KV8_DISPATCH(k_kv8_append, head_dim, dtype, p);
+    return e == cudaSuccess ? QW_OK : qw_fail(QW_ERR_CUDA, "append: %s", cudaGetErrorString(e));
 }
 
 extern "C" qw_status qw_kv8_append(const qw_kv8* kv, int B, int T, int max_len, const int32_t* dev_start,
@@ -270,11 +283,8 @@ extern "C" qw_status qw_kv8_append(const qw_kv8* kv, int B, int T, int max_len, 
                                      "append"))
         return s;
     if (T == 0) return QW_OK;
-    cudaStream_t st = (cudaStream_t)stream;
-    const int len = std::min(max_len, T);
-    Kv8AppendP p = {kv8_view(kv), dev_start, dev_cu, {dev_k, dev_v}, {ld_k, ld_v}, T, max_len, (len + 14) / 16 + 1, dev_status};
-    cudaError_t e = KV8_DISPATCH(k_kv8_append, kv->head_dim, dtype, p);
-    return e == cudaSuccess ? QW_OK : qw_fail(QW_ERR_CUDA, "append: %s", cudaGetErrorString(e));
+    return kv8_append(kv8_view(kv), kv->head_dim, B, T, max_len, dev_start, dev_cu, dev_k, ld_k, dev_v, ld_v, dtype, false,
+                      dev_status, (cudaStream_t)stream);
 }
 
 extern "C" qw_status qw_kv8_read(const qw_kv8* kv, int B, int T, int max_len, const int32_t* dev_start,
@@ -286,6 +296,7 @@ extern "C" qw_status qw_kv8_read(const qw_kv8* kv, int B, int T, int max_len, co
     if (T == 0) return QW_OK;
     cudaStream_t st = (cudaStream_t)stream;
     const int len = std::min(max_len, T);
+    int* launches = nullptr;
     Kv8ReadP p = {kv8_view(kv), dev_start, dev_cu, {dev_k, dev_v}, {ld_k, ld_v}, T, max_len, (len + 14) / 16 + 1, dev_status};
     cudaError_t e = KV8_DISPATCH(k_kv8_read, kv->head_dim, dtype, p);
     return e == cudaSuccess ? QW_OK : qw_fail(QW_ERR_CUDA, "read: %s", cudaGetErrorString(e));

@@ -36,9 +36,14 @@ struct Kv8AttnP {
     const float* score_in;
     float* score_out;
     size_t ld_score;
+    int score_mul, score_add;  // see kv8_attn
     int* status;
 };
 
+__device__ __forceinline__ size_t score_row(const Kv8AttnP& p, int b, int head) {
+    const size_t e = (size_t)p.score_mul * (p.kv.row ? p.kv.row[b] : b) + p.score_add;
+    return (e * p.kv.n_kv + head) * p.ld_score;
+}
 // token of row r of an entry (rows are token major, G heads a token)
 __device__ __forceinline__ int row_token(const Kv8AttnP& p, int r) { return p.gmul ? (int)__umulhi((uint32_t)r, p.gmul) : r; }
 
@@ -408,12 +413,12 @@ __global__ void __launch_bounds__(KD_WARPS * 32, NT == 1 ? 2 : 1) k_kv8_decode(c
         if (j >= i1) return nullptr;
         int b2 = b, head2 = head, page2, pages2;
         locate(j, b2, head2, page2, pages2);
-        int id = p.kv.table[(size_t)b2 * p.kv.max_pages + page2];
+        int id = kv8_row(p.kv, p.kv.table, b2)[page2];
         if (id < 0 || id >= p.kv.n_pages) {
             atomicOr(p.status, QW_KV8_BAD_POS);
             id = 0;
         }
-        return p.kv.blocks + ((size_t)id * H + head2) * BLK;
+        return kv8_block(p.kv, b2, id, head2, BLK);
     };
     const uint8_t* cur = address(i0 + lane);
     const uint8_t* nxt = address(i0 + 32 + lane);
@@ -715,7 +720,7 @@ __global__ void __launch_bounds__(KD_WARPS * 32) k_kv8_combine(const __grid_cons
         s_z[tid] = p.lse2[(size_t)(r0 + tid / p.G) * p.n_heads + head * p.G + tid % p.G];
     }
     if (!p.score_out) return;
-    const size_t base = ((size_t)b * H + head) * p.ld_score;
+    const size_t base = score_row(p, b, head);
     const int j = key0 + tid * 4, end = s + n;
     float in[4] = {0.f, 0.f, 0.f, 0.f};
     float4 t[8];  // the logits are stored for at most 8 rows
@@ -976,7 +981,7 @@ __global__ void __launch_bounds__(CT_THREADS, 1) k_kv8_chunk(const __grid_consta
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == 14) {
             // ---------------- copies: lane l < 8 brings page l of each step ----------------
-            const int* table = p.kv.table + (size_t)b * p.kv.max_pages;
+            const int* table = kv8_row(p.kv, p.kv.table, b);
             const int key_pages = (kend + KV8_PAGE - 1) / KV8_PAGE;
             bool ok = true;
             int st = 0, use = 0, issued = 0;  // ring stage and its use count
@@ -988,7 +993,7 @@ __global__ void __launch_bounds__(CT_THREADS, 1) k_kv8_chunk(const __grid_consta
                     atomicOr(p.status, QW_KV8_BAD_POS);
                     id = 0;
                 }
-                return p.kv.blocks + ((size_t)id * p.kv.n_kv + head) * Kv8<HD>::BLK;
+                return kv8_block(p.kv, b, id, head, Kv8<HD>::BLK);
             };
             // of no page 1 and 1: masked scores stay -inf
             auto scale_of = [&](const uint8_t* blk) {
@@ -1391,14 +1396,14 @@ __global__ void __launch_bounds__(CS_THREADS, 2) k_kv8_score(const __grid_consta
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int* table = p.kv.table + (size_t)b * p.kv.max_pages;
+    const int* table = kv8_row(p.kv, p.kv.table, b);
     auto block_of = [&](int pi) -> const uint8_t* {
         int id = table[pi];
         if (id < 0 || id >= p.kv.n_pages) {
             atomicOr(p.status, QW_KV8_BAD_POS);
             id = 0;
         }
-        return p.kv.blocks + ((size_t)id * p.kv.n_kv + head) * Kv8<HD>::BLK;
+        return kv8_block(p.kv, b, id, head, Kv8<HD>::BLK);
     };
     if (warp >= 4) {
         // ---------------- loaders: the keys once, then the query tiles ----------------
@@ -1538,7 +1543,7 @@ __global__ void __launch_bounds__(CS_THREADS, 2) k_kv8_score(const __grid_consta
             if (lane == 0) mbar_arrive(smem_u32(s_empty + buf));
         }
         if (good && on) {
-            const size_t at = ((size_t)b * p.kv.n_kv + head) * p.ld_score + key;
+            const size_t at = score_row(p, b, head) + key;
             p.score_out[at] = (p.score_in ? p.score_in[at] : 0.f) + acc;
         }
         if (!good) *abort_flag = 1;
@@ -1572,9 +1577,10 @@ int sm_count() {
     return n;
 }
 
-Plan make_plan(const qw_kv8* kv, int B, int T, int max_len, int max_keys, int n_heads, bool score) {
+// `avail`: most bytes that a decode's stored logits may take.
+Plan make_plan(int n_kv, int HD, int B, int T, int max_len, int max_keys, int n_heads, bool score, size_t avail) {
     Plan q = {};
-    const int G = n_heads / kv->n_kv_heads, HD = kv->head_dim, BLK = 32 * HD + 32;
+    const int G = n_heads / n_kv, BLK = 32 * HD + 32;
     auto put = [&](size_t n) {
         const size_t at = q.bytes;
         q.bytes = (at + n + 255) & ~(size_t)255;
@@ -1591,24 +1597,25 @@ Plan make_plan(const qw_kv8* kv, int B, int T, int max_len, int max_keys, int n_
         q.stages = std::min(8, ((per_sm == 2 ? 106 : 200) * 1024 - slots - ent) / (KD_WARPS * BLK));
         q.smem = KD_WARPS * q.stages * BLK + slots + ent;
         q.pair_mode = max_keys <= 512;
-        q.n_cta = q.pair_mode ? B * kv->n_kv_heads : per_sm * sm_count();
+        q.n_cta = q.pair_mode ? B * n_kv : per_sm * sm_count();
         // a row's logits are written and read once (8 bytes a key) instead of its K (HD bytes)
-        q.tbuf = score && rows <= 8;
+        const size_t logits = (size_t)B * n_kv * q.nrow * (((size_t)max_keys + 3) & ~(size_t)3) * 4;
+        q.tbuf = score && rows <= 8 && logits <= avail;
         q.off_o = put(q.pair_mode ? 0 : (size_t)q.n_cta * 2 * q.nrow * HD * 4);
         q.off_ml = put(q.pair_mode ? 0 : (size_t)q.n_cta * 2 * q.nrow * 2 * 4);
-        q.off_t = put(q.tbuf ? (size_t)B * kv->n_kv_heads * q.nrow * (((size_t)max_keys + 3) & ~(size_t)3) * 4 : 0);
+        q.off_t = put(q.tbuf ? logits : 0);
     }
     if (!q.decode) {
         q.tiles = (int)((rows + CT_ROWS - 1) / CT_ROWS);
         // A CTA an SM. Row tiles that leave the last wave of CTAs part empty split their keys, if that
         // fills waves by a quarter better and each split keeps 512 keys.
-        const long long ctas = (long long)(q.tiles + 1) / 2 * kv->n_kv_heads * B, slots = sm_count();
+        const long long ctas = (long long)(q.tiles + 1) / 2 * n_kv * B, slots = sm_count();
         auto fill = [&](long long n) { return (double)n / (double)((n + slots - 1) / slots * slots); };
         q.splits = 1;
         const int most = std::min(64, max_keys / 512);
         for (int n = 2; n <= most && ctas * n < 4 * slots; ++n)
             if (fill(ctas * n) >= 1.25 * fill(ctas * q.splits)) q.splits = n;
-        const size_t part = q.splits == 1 ? 0 : (size_t)B * kv->n_kv_heads * q.tiles * q.splits * CT_ROWS;
+        const size_t part = q.splits == 1 ? 0 : (size_t)B * n_kv * q.tiles * q.splits * CT_ROWS;
         q.off_o = put(part * HD * 4);
         q.off_ml = put(part * 2 * 4);
     }
@@ -1622,16 +1629,16 @@ cudaError_t allow_smem(K kern, int bytes) {
 }
 
 template <int HD, int DT>
-cudaError_t run_score(const Kv8AttnP& p, int B, cudaStream_t st) {
-    LaunchCtx c = {st, true, nullptr};
+cudaError_t run_score(const Kv8AttnP& p, int B, cudaStream_t st, int* launches) {
+    LaunchCtx c = {st, true, launches};
     if (cudaError_t e = allow_smem(k_kv8_score<HD, DT>, Cs<HD>::SMEM)) return e;
     const unsigned tiles = (unsigned)((p.max_keys + Cs<HD>::KEYS - 1) / Cs<HD>::KEYS);
     return launch_k(c, k_kv8_score<HD, DT>, dim3(tiles, p.kv.n_kv, B), dim3(CS_THREADS), (size_t)Cs<HD>::SMEM, p);
 }
 
 template <int HD, int DT>
-cudaError_t run_attn(const Kv8AttnP& p, const Plan& q, int B, char* ws, cudaStream_t st) {
-    LaunchCtx c = {st, true, nullptr};
+cudaError_t run_attn(const Kv8AttnP& p, const Plan& q, int B, char* ws, cudaStream_t st, int* launches) {
+    LaunchCtx c = {st, true, launches};
     cudaError_t e;
     if (q.decode) {
         Kv8DecP P = {};
@@ -1656,7 +1663,7 @@ cudaError_t run_attn(const Kv8AttnP& p, const Plan& q, int B, char* ws, cudaStre
             e = launch_k(c, k_kv8_combine<HD, DT>, dim3(B * p.kv.n_kv, chunks), dim3(KD_WARPS * 32), (size_t)smem, P);
             if (e != cudaSuccess) return e;
         }
-        return p.score_out && !q.tbuf ? run_score<HD, DT>(p, B, st) : cudaSuccess;
+        return p.score_out && !q.tbuf ? run_score<HD, DT>(p, B, st, launches) : cudaSuccess;
     }
     Kv8ChunkP P = {};
     P.a = p;
@@ -1674,7 +1681,7 @@ cudaError_t run_attn(const Kv8AttnP& p, const Plan& q, int B, char* ws, cudaStre
     e = launch_k(c, k_kv8_chunk<HD, DT>, dim3(p.kv.n_kv, B, (q.tiles + 1) / 2 * q.splits), dim3(CT_THREADS), (size_t)Ct<HD>::SMEM, P);
     if (e == cudaSuccess && q.splits > 1)
         e = launch_k(c, k_kv8_chunk_combine<HD, DT>, dim3(q.tiles * CT_ROWS / 8, p.kv.n_kv, B), dim3(256), 0, P);
-    return e == cudaSuccess && p.score_out ? run_score<HD, DT>(p, B, st) : e;
+    return e == cudaSuccess && p.score_out ? run_score<HD, DT>(p, B, st, launches) : e;
 }
 
 }  // namespace
@@ -1694,10 +1701,48 @@ static qw_status attn_sizes(const qw_kv8* kv, int B, int T, int max_len, int max
     return QW_OK;
 }
 
+qw_status kv8_attn(const Kv8View& v, int head_dim, const qw_kv8_attn_args& a, int score_mul, int score_add, cudaStream_t st,
+                   int* launches) {
+    // a caller's workspace always has room for the logits; a model's may not
+    Plan q = make_plan(v.n_kv, head_dim, a.B, a.T, a.max_len, a.max_keys, a.n_heads, a.dev_score_out != nullptr, SIZE_MAX);
+    if (q.bytes > a.ws_bytes)
+        q = make_plan(v.n_kv, head_dim, a.B, a.T, a.max_len, a.max_keys, a.n_heads, a.dev_score_out != nullptr, 0);
+    if (q.bytes > a.ws_bytes) return qw_fail(QW_ERR_INVALID_ARG, "attn: workspace too small");
+    Kv8AttnP p = {};
+    p.kv = v;
+    p.start = a.dev_start;
+    p.cu = a.dev_cu;
+    p.q = a.dev_q;
+    p.ld_q = a.ld_q;
+    p.T = a.T;
+    p.max_len = a.max_len;
+    p.max_keys = a.max_keys;
+    p.n_heads = a.n_heads;
+    p.G = a.n_heads / v.n_kv;
+    p.gmul = p.G == 1 ? 0u : (uint32_t)(((1ull << 32) + p.G - 1) / p.G);
+    p.scale_log2 = a.scale * KV8_LOG2E;
+    p.out = a.dev_out;
+    p.ld_out = a.ld_out;
+    p.lse = a.dev_lse;
+    p.lse2 = a.dev_score_out ? (float*)a.dev_ws : nullptr;
+    p.score_in = a.dev_score_in;
+    p.score_out = a.dev_score_out;
+    p.ld_score = a.ld_score;
+    p.score_mul = score_mul;
+    p.score_add = score_add;
+    p.status = a.dev_status;
+    char* ws = (char*)a.dev_ws;
+    const bool h = a.dtype == QW_F16;
+    const cudaError_t e = head_dim == 128
+                              ? (h ? run_attn<128, QW_F16>(p, q, a.B, ws, st, launches) : run_attn<128, QW_BF16>(p, q, a.B, ws, st, launches))
+                              : (h ? run_attn<64, QW_F16>(p, q, a.B, ws, st, launches) : run_attn<64, QW_BF16>(p, q, a.B, ws, st, launches));
+    return e == cudaSuccess ? QW_OK : qw_fail(QW_ERR_CUDA, "attn: %s", cudaGetErrorString(e));
+}
+
 extern "C" size_t qw_kv8_attn_ws_bytes(const qw_kv8* kv, int B, int T, int max_len, int max_keys, int n_heads,
                                        int with_score) {
     if (attn_sizes(kv, B, T, max_len, max_keys, n_heads)) return 0;
-    return make_plan(kv, B, T, max_len, max_keys, n_heads, with_score != 0).bytes;
+    return make_plan(kv->n_kv_heads, kv->head_dim, B, T, max_len, max_keys, n_heads, with_score != 0, SIZE_MAX).bytes;
 }
 
 extern "C" qw_status qw_kv8_attn(const qw_kv8* kv, const qw_kv8_attn_args* a, void* stream) {
@@ -1714,36 +1759,9 @@ extern "C" qw_status qw_kv8_attn(const qw_kv8* kv, const qw_kv8_attn_args* a, vo
     if (!(a->scale > 0.f) || !(a->scale < 1e30f)) return qw_fail(QW_ERR_INVALID_ARG, "attn: scale not positive and finite");
     if (a->dev_score_in && !a->dev_score_out) return qw_fail(QW_ERR_INVALID_ARG, "attn: score_in without score_out");
     if (a->dev_score_out && a->ld_score < (size_t)a->max_keys) return qw_fail(QW_ERR_INVALID_ARG, "attn: ld_score < max_keys");
-    const Plan q = make_plan(kv, a->B, a->T, a->max_len, a->max_keys, a->n_heads, a->dev_score_out != nullptr);
-    if ((uintptr_t)a->dev_ws & 255 || a->ws_bytes < q.bytes)
+    if ((uintptr_t)a->dev_ws & 255 ||
+        a->ws_bytes < qw_kv8_attn_ws_bytes(kv, a->B, a->T, a->max_len, a->max_keys, a->n_heads, a->dev_score_out != nullptr))
         return qw_fail(QW_ERR_INVALID_ARG, "attn: workspace too small or not 256-byte aligned");
     if (a->T == 0) return QW_OK;
-    Kv8AttnP p = {};
-    p.kv = kv8_view(kv);
-    p.start = a->dev_start;
-    p.cu = a->dev_cu;
-    p.q = a->dev_q;
-    p.ld_q = a->ld_q;
-    p.T = a->T;
-    p.max_len = a->max_len;
-    p.max_keys = a->max_keys;
-    p.n_heads = a->n_heads;
-    p.G = a->n_heads / kv->n_kv_heads;
-    p.gmul = p.G == 1 ? 0u : (uint32_t)(((1ull << 32) + p.G - 1) / p.G);
-    p.scale_log2 = a->scale * KV8_LOG2E;
-    p.out = a->dev_out;
-    p.ld_out = a->ld_out;
-    p.lse = a->dev_lse;
-    p.lse2 = a->dev_score_out ? (float*)a->dev_ws : nullptr;
-    p.score_in = a->dev_score_in;
-    p.score_out = a->dev_score_out;
-    p.ld_score = a->ld_score;
-    p.status = a->dev_status;
-    cudaStream_t st = (cudaStream_t)stream;
-    char* ws = (char*)a->dev_ws;
-    const bool h = a->dtype == QW_F16;
-    const cudaError_t e = kv->head_dim == 128
-                              ? (h ? run_attn<128, QW_F16>(p, q, a->B, ws, st) : run_attn<128, QW_BF16>(p, q, a->B, ws, st))
-                              : (h ? run_attn<64, QW_F16>(p, q, a->B, ws, st) : run_attn<64, QW_BF16>(p, q, a->B, ws, st));
-    return e == cudaSuccess ? QW_OK : qw_fail(QW_ERR_CUDA, "attn: %s", cudaGetErrorString(e));
+    return kv8_attn(kv8_view(kv), kv->head_dim, *a, 1, 0, (cudaStream_t)stream);
 }

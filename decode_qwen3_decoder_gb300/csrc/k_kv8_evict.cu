@@ -31,6 +31,7 @@ constexpr int EV_ONE_KEEP = 512;       // most kept tokens that the same CTA mov
 struct Kv8EvictP {
     Kv8View kv;
     const int* len;
+    int len_step;    // 0: one length for every entry
     const int* dst;  // destination page table (the entry's own when in place)
     bool in_place;
     int max_len, keep, recent;
@@ -102,9 +103,9 @@ __device__ __forceinline__ bool select_kept(const Kv8EvictP& p, int rank, int he
     __shared__ int ws[EV_W];
     __shared__ int s_digit, s_above, s_bad, pub[2];
     const int tid = threadIdx.x, warp = tid >> 5;
-    const int L = p.len[b];
-    const int* table = p.kv.table + (size_t)b * p.kv.max_pages;
-    const int* dst = p.dst + (size_t)b * p.kv.max_pages;
+    const int L = p.len[b * p.len_step];
+    const int* table = kv8_row(p.kv, p.kv.table, b);
+    const int* dst = kv8_row(p.kv, p.dst, b);
     const float* score = p.score + ((size_t)b * p.kv.n_kv + head) * p.ld_score;
     int* kept = p.kept + ((size_t)b * p.kv.n_kv + head) * p.keep;
     const int n = min(L, p.keep);
@@ -219,7 +220,7 @@ struct RowMove {
     static constexpr int CH = Kv8<HD>::CH, TSTEP = 32 / CH, UPL = KV8_PAGE / TSTEP;
     uint4 code[2][UPL];
     float2 sc[UPL];
-    __device__ __forceinline__ void fetch(const Kv8EvictP& p, const int* table, const int* kept, int head, int d, int n, int lane) {
+    __device__ __forceinline__ void fetch(const Kv8EvictP& p, const int* table, const int* kept, int b, int head, int d, int n, int lane) {
         const int ch = lane % CH, t0 = lane / CH;
         int src[UPL], pg[UPL];
 #pragma unroll
@@ -235,15 +236,15 @@ struct RowMove {
             sc[u] = make_float2(0.f, 0.f);
             if (src[u] < 0) continue;
             const int t = src[u] % KV8_PAGE;
-            const uint8_t* blk = p.kv.blocks + ((size_t)pg[u] * p.kv.n_kv + head) * Kv8<HD>::BLK;
+            const uint8_t* blk = kv8_block(p.kv, b, pg[u], head, Kv8<HD>::BLK);
             code[0][u] = *reinterpret_cast<const uint4*>(blk + t * HD + kv8_k_pos<HD>(t, ch) * 16);
             code[1][u] = *reinterpret_cast<const uint4*>(blk + Kv8<HD>::VOFF + t * HD + kv8_v_pos<HD>(t, ch) * 16);
             sc[u] = *reinterpret_cast<const float2*>(blk + Kv8<HD>::SOFF);
         }
     }
-    __device__ __forceinline__ void store(const Kv8EvictP& p, int page, int head, int lane) {
+    __device__ __forceinline__ void store(const Kv8EvictP& p, int page, int b, int head, int lane) {
         const int ch = lane % CH, t0 = lane / CH;
-        uint8_t* blk = p.kv.blocks + ((size_t)page * p.kv.n_kv + head) * Kv8<HD>::BLK;
+        uint8_t* blk = kv8_block(p.kv, b, page, head, Kv8<HD>::BLK);
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
             float amax = 0.f;
@@ -277,14 +278,14 @@ __global__ void __launch_bounds__(MV_W * 32) k_kv8_move(const __grid_constant__ 
     const int* kept = p.kept + ((size_t)b * p.kv.n_kv + head) * p.keep;
     pdl_wait();
     pdl_launch();
-    const int L = p.len[b], n = min(L, p.keep);
+    const int L = p.len[b * p.len_step], n = min(L, p.keep);
     if (L <= 0 || kept[0] < 0) return;  // empty, or an entry left out
     if ((int)blockIdx.x < row_ctas) {
         const int d = blockIdx.x * MV_W + warp;
         if (d * KV8_PAGE >= n) return;
         RowMove<HD> mv;
-        mv.fetch(p, p.kv.table + (size_t)b * p.kv.max_pages, kept, head, d, n, lane);
-        mv.store(p, p.dst[(size_t)b * p.kv.max_pages + d], head, lane);
+        mv.fetch(p, kv8_row(p.kv, p.kv.table, b), kept, b, head, d, n, lane);
+        mv.store(p, kv8_row(p.kv, p.dst, b)[d], b, head, lane);
     } else if (scores) {
         const int j0 = ((int)blockIdx.x - row_ctas) * 4 * MV_W * 32 + tid;
         const float* score = p.score + ((size_t)b * p.kv.n_kv + head) * p.ld_score;
@@ -302,7 +303,7 @@ template <int HD>
 __device__ __forceinline__ void move_ordered(const Kv8EvictP& p, int head, int b, bool scores, bool rows) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int* kept = p.kept + ((size_t)b * p.kv.n_kv + head) * p.keep;
-    const int L = p.len[b], n = min(L, p.keep);
+    const int L = p.len[b * p.len_step], n = min(L, p.keep);
     if (scores) {
         const float* score = p.score + ((size_t)b * p.kv.n_kv + head) * p.ld_score;
         float* out = p.score_out + ((size_t)b * p.kv.n_kv + head) * p.ld_score;
@@ -316,14 +317,14 @@ __device__ __forceinline__ void move_ordered(const Kv8EvictP& p, int head, int b
         for (int j = n + tid; j < L; j += EV_T) out[j] = 0.f;
     }
     if (!rows) return;
-    const int* table = p.kv.table + (size_t)b * p.kv.max_pages;
-    const int* dst = p.dst + (size_t)b * p.kv.max_pages;
+    const int* table = kv8_row(p.kv, p.kv.table, b);
+    const int* dst = kv8_row(p.kv, p.dst, b);
     for (int d0 = 0; d0 * KV8_PAGE < n; d0 += EV_W) {
         const int d = d0 + warp;
         RowMove<HD> mv;
-        mv.fetch(p, table, kept, head, d, n, lane);
+        mv.fetch(p, table, kept, b, head, d, n, lane);
         __syncthreads();
-        if (d * KV8_PAGE < n) mv.store(p, dst[d], head, lane);
+        if (d * KV8_PAGE < n) mv.store(p, dst[d], b, head, lane);
     }
 }
 
@@ -333,7 +334,7 @@ __global__ void __launch_bounds__(EV_T) k_kv8_move_inplace(const __grid_constant
     const int head = blockIdx.x, b = blockIdx.y;
     pdl_wait();
     pdl_launch();
-    if (p.len[b] <= p.keep || p.kept[((size_t)b * p.kv.n_kv + head) * p.keep] < 0) return;  // nothing to move
+    if (p.len[b * p.len_step] <= p.keep || p.kept[((size_t)b * p.kv.n_kv + head) * p.keep] < 0) return;  // nothing to move
     move_ordered<HD>(p, head, b, p.score_out == p.score, p.in_place);
 }
 
@@ -344,7 +345,7 @@ __global__ void __launch_bounds__(EV_T) k_kv8_evict_one(const __grid_constant__ 
     pdl_launch();
     if (!select_kept<1>(p, 0, head, b)) return;
     __syncthreads();
-    const bool same = p.len[b] <= p.keep;  // every token stays: what is in place is left alone
+    const bool same = p.len[b * p.len_step] <= p.keep;  // every token stays: what is in place is left alone
     move_ordered<HD>(p, head, b, !(same && p.score_out == p.score), !(same && p.in_place));
 }
 
@@ -370,6 +371,15 @@ cudaError_t run_evict(const Kv8EvictP& p, int B, cudaStream_t st) {
 
 }  // namespace
 
+qw_status kv8_evict(const Kv8View& v, int head_dim, int B, int max_len, const int* len, int len_step, int keep, int recent,
+                    const int* dst, const float* score, float* score_out, size_t ld_score, int* kept, int* new_len, int* status,
+                    cudaStream_t st) {
+    Kv8EvictP p = {v, len, len_step, dst ? dst : v.table, !dst || dst == v.table, max_len, keep, recent, score, score_out, ld_score,
+                   kept, new_len, status};
+    const cudaError_t e = head_dim == 128 ? run_evict<128>(p, B, st) : run_evict<64>(p, B, st);
+    return e == cudaSuccess ? QW_OK : qw_fail(QW_ERR_CUDA, "evict: %s", cudaGetErrorString(e));
+}
+
 extern "C" qw_status qw_kv8_evict(const qw_kv8* kv, int B, int max_len, const int32_t* dev_len, int n_keep, int n_recent,
                                   const int32_t* dev_dst_table, const float* dev_score, float* dev_score_out,
                                   size_t ld_score, int32_t* dev_kept, int32_t* dev_new_len, int32_t* dev_status,
@@ -383,10 +393,6 @@ extern "C" qw_status qw_kv8_evict(const qw_kv8* kv, int B, int max_len, const in
         return qw_fail(QW_ERR_INVALID_ARG, "evict: n_keep < 1 or n_recent outside [0, n_keep]");
     if (ld_score < (size_t)max_len) return qw_fail(QW_ERR_INVALID_ARG, "evict: ld_score < max_len");
     if (dev_new_len == dev_len) return qw_fail(QW_ERR_INVALID_ARG, "evict: dev_new_len is dev_len");
-    Kv8EvictP p = {kv8_view(kv), dev_len, dev_dst_table ? dev_dst_table : kv->dev_page_table,
-                   !dev_dst_table || dev_dst_table == kv->dev_page_table, max_len, n_keep, n_recent, dev_score, dev_score_out,
-                   ld_score, dev_kept, dev_new_len, dev_status};
-    cudaStream_t st = (cudaStream_t)stream;
-    const cudaError_t e = kv->head_dim == 128 ? run_evict<128>(p, B, st) : run_evict<64>(p, B, st);
-    return e == cudaSuccess ? QW_OK : qw_fail(QW_ERR_CUDA, "evict: %s", cudaGetErrorString(e));
+    return kv8_evict(kv8_view(kv), kv->head_dim, B, max_len, dev_len, 1, n_keep, n_recent, dev_dst_table, dev_score, dev_score_out,
+                     ld_score, dev_kept, dev_new_len, dev_status, (cudaStream_t)stream);
 }

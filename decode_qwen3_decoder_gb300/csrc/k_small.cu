@@ -74,13 +74,21 @@ __global__ void __launch_bounds__(256) k_step_begin(StepDesc sd, const int32_t* 
     }
     if (threadIdx.x == 0) {
         const int seq = sd.seq[b];
-        const int pos = kv.len[seq] + (t - sd.start[b]);
+        const int len = kv.len[seq], at = len + (t - sd.start[b]);
         tv.seq[t] = seq;
-        tv.pos[t] = pos;
+        tv.pos[t] = at + (kv.shift ? kv.shift[seq] : 0);
         // the token's KV slot, the same for every layer (kernels that append report a missing page)
-        const int pi = pos >> 4;
+        const int pi = at >> 4;
         const int page = (pi < kv.max_pages_per_seq) ? kv.page_table[(size_t)seq * kv.max_pages_per_seq + pi] : -1;
-        tv.slot[t] = (page >= 0 && page < kv.n_pages) ? page * 16 + (pos & 15) : -1;
+        tv.slot[t] = (page >= 0 && page < kv.n_pages) ? (kv.staged ? t : page * 16 + (at & 15)) : -1;
+        if (kv.staged) {
+            if (t == sd.start[b]) {
+                kv.e_seq[b] = seq;
+                kv.e_start[b] = len;
+                kv.e_cu[b] = t;
+            }
+            if (t == sd.T - 1) kv.e_cu[sd.B] = sd.T;
+        }
         if (t == sd.start[b + 1] - 1) tv.last[b] = t;
         if (bad) atomicOr(status, QW_DEV_BAD_TOKEN);
     }
@@ -682,16 +690,22 @@ __global__ void __launch_bounds__(256) k_qknorm_rope_append(
             const int g = (hh - n_heads) % n_kv;
             const int seq = tv.seq[t];
             const int pi = pos >> 4;
-            const int page = (pi < kv.max_pages_per_seq) ? kv.page_table[(size_t)seq * kv.max_pages_per_seq + pi] : -1;
+            int page = (pi < kv.max_pages_per_seq) ? kv.page_table[(size_t)seq * kv.max_pages_per_seq + pi] : -1;
+            int at = pos & 15;
+            if (kv.staged) {  // the token's row of the staging pages
+                const int slot = tv.slot[t];
+                page = slot < 0 ? -1 : slot >> 4;
+                at = slot & 15;
+            }
             if (page < 0 || page >= kv.n_pages) {
                 if (lane == 0) atomicOr(status, QW_DEV_BAD_POS);
             } else {
                 f16* pool = (which == 0 ? kv.k : kv.v) + (size_t)layer * kv.layer_stride;
-                f16* dst = pool + (((size_t)page * n_kv + g) * 16 + (pos & 15)) * 128 + lane * 4;
+                f16* dst = pool + (((size_t)page * n_kv + g) * 16 + at) * 128 + lane * 4;
                 *reinterpret_cast<uint2*>(dst) = packed;
                 if (dbg_pos && which == 0 && g == 0 && lane == 0) {
                     dbg_pos[t] = pos;
-                    dbg_slot[t] = page * 16 + (pos & 15);
+                    dbg_slot[t] = page * 16 + at;
                 }
             }
         }

@@ -83,12 +83,39 @@ __device__ __forceinline__ uint4 kv8_enc16(const float* x, float mul) {
 // Host-side check of a view; QW_OK or the recorded error.
 qw_status kv8_check(const qw_kv8* kv, int B, const char* what);
 
-// Device view passed to the kernels.
+// Device view passed to the kernels. A model's cache differs from a caller's in how entries find
+// their pages: through the sequence ids of the batch (row), or every entry (a layer) through the same
+// row of the table with its own range of blocks (row_stride 0, page_step).
 struct Kv8View {
     uint8_t* blocks;
     const int* table;
     int n_pages, max_pages, n_kv;
+    const int* row;   // optional [B]: the table row of entry b
+    int row_stride;   // ints between rows
+    int page_step;    // added to the page ids of entry b, b times
 };
 inline Kv8View kv8_view(const qw_kv8* kv) {
-    return {(uint8_t*)kv->dev_blocks, kv->dev_page_table, kv->n_pages, kv->max_pages, kv->n_kv_heads};
+    return {(uint8_t*)kv->dev_blocks, kv->dev_page_table, kv->n_pages, kv->max_pages, kv->n_kv_heads, nullptr, kv->max_pages, 0};
 }
+#ifdef __CUDACC__
+__device__ __forceinline__ const int* kv8_row(const Kv8View& v, const int* table, int b) {
+    return table + (size_t)(v.row ? v.row[b] : b) * v.row_stride;
+}
+__device__ __forceinline__ uint8_t* kv8_block(const Kv8View& v, int b, int page, int head, int blk) {
+    return v.blocks + ((size_t)(page + b * v.page_step) * v.n_kv + head) * blk;
+}
+#endif
+
+// The operators behind the C entry points (arguments checked by the caller); errors recorded.
+// staged: K and V rows in pages of 16 tokens, [T / 16][n_kv][16][head_dim] fp16.
+qw_status kv8_append(const Kv8View& v, int head_dim, int B, int T, int max_len, const int* start, const int* cu, const void* k,
+                     size_t ld_k, const void* val, size_t ld_v, int dtype, bool staged, int* status, cudaStream_t st,
+                     int* launches = nullptr);
+// Scores of entry b: rows (score_mul * row[b] + score_add) * n_kv .. of the score arrays.
+// ws_bytes also decides whether the logits of a decode with scores are kept.
+qw_status kv8_attn(const Kv8View& v, int head_dim, const qw_kv8_attn_args& a, int score_mul, int score_add, cudaStream_t st,
+                   int* launches = nullptr);
+// len_step 0: one length for every entry.
+qw_status kv8_evict(const Kv8View& v, int head_dim, int B, int max_len, const int* len, int len_step, int keep, int recent,
+                    const int* dst, const float* score, float* score_out, size_t ld_score, int* kept, int* new_len, int* status,
+                    cudaStream_t st);

@@ -37,6 +37,11 @@ struct KVView {
     int max_pages_per_seq;
     int n_pages;
     long long layer_stride; // elements per layer of the K (or V) pool
+    // An 8-bit cache: a layer's new K/V rows are staged as fp16 in pages of 16 of the call's tokens
+    // (k, v, layer_stride 0) and then quantised into their blocks.
+    int staged;
+    const int* shift;       // optional [max_seqs]: tokens evicted from a sequence (its positions run on)
+    int *e_seq, *e_start, *e_cu;  // staged: the step's entries, written by its first kernel ([B], [B], [B + 1])
 };
 
 // Per-token bookkeeping written by the step-begin kernel.

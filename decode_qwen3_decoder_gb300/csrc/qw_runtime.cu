@@ -17,6 +17,7 @@
 #include <string>
 #include <vector>
 
+#include "kv8.cuh"
 #include "qw_internal.h"
 
 // ---------------------------------------------------------------------------------------
@@ -249,9 +250,27 @@ struct qw_kv {
     std::vector<int> len;
     std::vector<std::vector<int>> pt;
     std::set<int> free_pages;
+    // 8-bit cache (qw_kv8_alloc): k and v are the staging rows of a call
+    bool b8 = false;
+    uint8_t* blocks;       // [n_layers][n_pages][n_kv] blocks
+    size_t layer_bytes;
+    int *e_seq, *e_start, *e_cu, *d_shift;
+    std::vector<int> shift;
+    float* score;          // optional [max_seqs][n_layers][n_kv][ld_score]
+    size_t ld_score;
+    int *kept, *new_len;   // eviction: [n_layers][n_kv][max_context], [n_layers]
+    char* ws8;             // attention workspace
+    size_t ws8_bytes;
 
     KVView view() const {
-        KVView v_;
+        KVView v_ = {};
+        if (b8) {
+            v_.staged = 1;
+            v_.shift = d_shift;
+            v_.e_seq = e_seq;
+            v_.e_start = e_start;
+            v_.e_cu = e_cu;
+        }
         v_.len = d_len;
         v_.page_table = d_pt;
         v_.k = k;
@@ -754,6 +773,8 @@ static size_t kv_meta_bytes(const qw_model* m, int max_seqs) {
     return align_up((size_t)max_seqs * 4, 256) + align_up((size_t)max_seqs * maxp * 4, 256);
 }
 
+static size_t kv8_score_floats(const qw_model* m, int max_seqs);
+
 static size_t kv_page_bytes(const qw_model* m) {  // K + V, all layers, one page
     return (size_t)m->cfg.n_layers * 2 * m->cfg.n_kv_heads * 16 * m->cfg.head_dim * 2;
 }
@@ -805,6 +826,132 @@ extern "C" qw_status qw_kv_alloc(qw_model* m, void* dev_pool, size_t pool_bytes,
     return QW_OK;
 }
 
+// ---- 8-bit cache ----
+// Pool: lengths, page tables, shifts, the step's entries, eviction results, scores, staging rows,
+// the attention workspace, then the blocks.
+static size_t kv8_score_floats(const qw_model* m, int max_seqs) {
+    return (size_t)max_seqs * m->cfg.n_layers * m->cfg.n_kv_heads * align_up(m->cfg.max_context, 4);
+}
+
+struct Kv8Layout {
+    size_t len, pt, shift, e_seq, e_start, e_cu, kept, new_len, score, stage, ws, ws_bytes, blocks, page;
+};
+
+static Kv8Layout kv8_layout(const qw_model* m, int max_seqs, bool scores) {
+    const qw_config& c = m->cfg;
+    Kv8Layout L = {};
+    size_t at = 0;
+    auto put = [&](size_t n) {
+        const size_t a = at;
+        at = align_up(at + n, 256);
+        return a;
+    };
+    const size_t maxp = (c.max_context + 15) / 16;
+    L.len = put((size_t)max_seqs * 4);
+    L.pt = put((size_t)max_seqs * maxp * 4);
+    L.shift = put((size_t)max_seqs * 4);
+    L.e_seq = put((size_t)c.max_batch * 4);
+    L.e_start = put((size_t)c.max_batch * 4);
+    L.e_cu = put((size_t)(c.max_batch + 1) * 4);
+    L.kept = put(scores ? (size_t)c.n_layers * c.n_kv_heads * c.max_context * 4 : 0);
+    L.new_len = put((size_t)c.n_layers * 4);
+    L.score = put(scores ? kv8_score_floats(m, max_seqs) * 4 : 0);
+    L.stage = put(align_up(c.max_tokens, 16) * 2 * c.n_kv_heads * c.head_dim * 2);
+    // normalisers of every row and the partials of a call that splits its keys (fewer than 5 CTAs an
+    // SM, two tiles of 128 rows each); logits kept for the scores take what is left
+    L.ws_bytes = align_up((size_t)c.max_tokens * c.n_heads * 4, 256) + (size_t)5 * m->num_sms * 256 * (c.head_dim + 2) * 4 + 4096;
+    L.ws = put(L.ws_bytes);
+    L.blocks = at;
+    L.page = (size_t)c.n_layers * c.n_kv_heads * qw_kv8_block_bytes(c.head_dim);
+    return L;
+}
+
+extern "C" size_t qw_kv8_pool_bytes(const qw_model* m, int n_pages, int max_seqs, int keep_scores) {
+    if (!m || n_pages < 1 || max_seqs < 1) return 0;
+    const Kv8Layout L = kv8_layout(m, max_seqs, keep_scores != 0);
+    return L.blocks + L.page * (size_t)n_pages;
+}
+
+extern "C" qw_status qw_kv8_alloc(qw_model* m, void* dev_pool, size_t pool_bytes, int max_seqs, int keep_scores, void* stream_,
+                                  qw_kv** out) {
+    if (!out) return fail(QW_ERR_INVALID_ARG, "out is NULL");
+    *out = nullptr;
+    if (!m || !dev_pool || !aligned(dev_pool, 256)) return fail(QW_ERR_INVALID_ARG, "model/pool NULL or pool not 256-byte aligned");
+    if (max_seqs < 1 || max_seqs > (1 << 20)) return fail(QW_ERR_INVALID_ARG, "max_seqs out of range");
+    const Kv8Layout L = kv8_layout(m, max_seqs, keep_scores != 0);
+    if (pool_bytes < L.blocks + L.page) return fail(QW_ERR_INVALID_ARG, "pool too small for one page");
+    const long long n_pages = (long long)((pool_bytes - L.blocks) / L.page);
+    if (n_pages * m->cfg.n_layers > 0x7fffffffll) return fail(QW_ERR_INVALID_ARG, "pool too large");
+    cudaStream_t st = (cudaStream_t)stream_;
+    qw_kv* kv = new qw_kv();
+    kv->m = m;
+    kv->pool = (char*)dev_pool;
+    kv->max_seqs = max_seqs;
+    kv->n_pages = (int)n_pages;
+    kv->maxp = (m->cfg.max_context + 15) / 16;
+    kv->b8 = true;
+    kv->d_len = (int*)(kv->pool + L.len);
+    kv->d_pt = (int*)(kv->pool + L.pt);
+    kv->d_shift = (int*)(kv->pool + L.shift);
+    kv->e_seq = (int*)(kv->pool + L.e_seq);
+    kv->e_start = (int*)(kv->pool + L.e_start);
+    kv->e_cu = (int*)(kv->pool + L.e_cu);
+    kv->kept = keep_scores ? (int*)(kv->pool + L.kept) : nullptr;
+    kv->new_len = (int*)(kv->pool + L.new_len);
+    kv->score = keep_scores ? (float*)(kv->pool + L.score) : nullptr;
+    kv->ld_score = align_up(m->cfg.max_context, 4);
+    kv->k = (f16*)(kv->pool + L.stage);
+    kv->v = kv->k + align_up(m->cfg.max_tokens, 16) * m->cfg.n_kv_heads * m->cfg.head_dim;
+    kv->ws8 = kv->pool + L.ws;
+    kv->ws8_bytes = L.ws_bytes;
+    kv->blocks = (uint8_t*)(kv->pool + L.blocks);
+    kv->layer_bytes = (size_t)n_pages * m->cfg.n_kv_heads * qw_kv8_block_bytes(m->cfg.head_dim);
+    kv->len.assign(max_seqs, 0);
+    kv->shift.assign(max_seqs, 0);
+    kv->pt.assign(max_seqs, std::vector<int>());
+    for (int i = 0; i < kv->n_pages; ++i) kv->free_pages.insert(i);
+    if (cudaMemsetAsync(kv->d_len, 0, (size_t)max_seqs * 4, st) != cudaSuccess ||
+        cudaMemsetAsync(kv->d_shift, 0, (size_t)max_seqs * 4, st) != cudaSuccess ||
+        cudaMemsetAsync(kv->d_pt, 0xFF, (size_t)max_seqs * kv->maxp * 4, st) != cudaSuccess ||
+        (kv->score && cudaMemsetAsync(kv->score, 0, kv8_score_floats(m, max_seqs) * 4, st) != cudaSuccess)) {
+        delete kv;
+        return fail(QW_ERR_CUDA, "KV metadata clear failed");
+    }
+    *out = kv;
+    return QW_OK;
+}
+
+extern "C" qw_status qw_kv8_scores(const qw_kv* kv, float** dev_score, size_t* ld_score) {
+    if (!kv || !dev_score) return fail(QW_ERR_INVALID_ARG, "NULL argument");
+    if (!kv->b8 || !kv->score) return fail(QW_ERR_UNSUPPORTED, "this cache keeps no scores");
+    *dev_score = kv->score;
+    if (ld_score) *ld_score = kv->ld_score;
+    return QW_OK;
+}
+
+extern "C" qw_status qw_kv_evict(qw_kv* kv, int seq, int n_keep, int n_recent, void* stream_) {
+    if (!kv) return fail(QW_ERR_INVALID_ARG, "kv is NULL");
+    if (seq < 0 || seq >= kv->max_seqs) return fail(QW_ERR_INVALID_ARG, "seq id %d out of range", seq);
+    if (!kv->b8 || !kv->score) return fail(QW_ERR_UNSUPPORTED, "eviction needs an 8-bit cache that keeps scores");
+    if (n_keep < 1 || n_recent < 0 || n_recent > n_keep)
+        return fail(QW_ERR_INVALID_ARG, "n_keep < 1 or n_recent outside [0, n_keep]");
+    const int len = kv->len[seq];
+    if (len <= n_keep) return QW_OK;
+    const qw_config& c = kv->m->cfg;
+    cudaStream_t st = (cudaStream_t)stream_;
+    // every layer is an entry: the sequence's page table, the layer's blocks
+    const Kv8View v = {kv->blocks, kv->d_pt + (size_t)seq * kv->maxp, kv->n_pages, kv->maxp, c.n_kv_heads, nullptr, 0, kv->n_pages};
+    float* score = kv->score + seq * kv8_score_floats(kv->m, 1);
+    QW_TRY(kv8_evict(v, c.head_dim, c.n_layers, len, kv->d_len + seq, 0, n_keep, n_recent, nullptr, score, score, kv->ld_score, kv->kept,
+                     kv->new_len, kv->m->status, st));
+    const int shift = kv->shift[seq] + len - n_keep;
+    CUDA_TRY(cudaMemcpyAsync(kv->d_len + seq, &n_keep, 4, cudaMemcpyHostToDevice, st));
+    CUDA_TRY(cudaMemcpyAsync(kv->d_shift + seq, &shift, 4, cudaMemcpyHostToDevice, st));
+    kv->len[seq] = n_keep;
+    kv->shift[seq] = shift;
+    return QW_OK;
+}
+
 extern "C" void qw_free_kv(qw_kv* kv) { delete kv; }
 
 extern "C" qw_status qw_kv_reserve(qw_kv* kv, int seq, int total_tokens, void* stream_) {
@@ -832,6 +979,12 @@ extern "C" qw_status qw_kv_reset(qw_kv* kv, int seq, void* stream_) {
     if (seq < -1 || seq >= kv->max_seqs) return fail(QW_ERR_INVALID_ARG, "seq id %d out of range", seq);
     cudaStream_t st = (cudaStream_t)stream_;
     const int a = seq < 0 ? 0 : seq, b = seq < 0 ? kv->max_seqs : seq + 1;
+    if (kv->b8) {
+        for (int s = a; s < b; ++s) kv->shift[s] = 0;
+        CUDA_TRY(cudaMemsetAsync(kv->d_shift + a, 0, (size_t)(b - a) * 4, st));
+        const size_t per = kv8_score_floats(kv->m, 1);
+        if (kv->score) CUDA_TRY(cudaMemsetAsync(kv->score + a * per, 0, (size_t)(b - a) * per * 4, st));
+    }
     for (int s = a; s < b; ++s) {
         for (int p : kv->pt[s]) kv->free_pages.insert(p);
         kv->pt[s].clear();
@@ -849,6 +1002,11 @@ extern "C" qw_status qw_kv_truncate(qw_kv* kv, int seq, int n_tokens, void* stre
         return fail(QW_ERR_INVALID_ARG, "n_tokens %d outside [0, length %d]", n_tokens, kv->len[seq]);
     const int n = n_tokens;
     CUDA_TRY(cudaMemcpyAsync(kv->d_len + seq, &n, 4, cudaMemcpyHostToDevice, (cudaStream_t)stream_));
+    if (kv->b8 && kv->score && n < kv->len[seq]) {  // dropped positions start again without weight
+        const size_t rows = (size_t)kv->m->cfg.n_layers * kv->m->cfg.n_kv_heads;
+        CUDA_TRY(cudaMemset2DAsync(kv->score + (size_t)seq * rows * kv->ld_score + n, kv->ld_score * 4, 0, (size_t)(kv->len[seq] - n) * 4,
+                                   rows, (cudaStream_t)stream_));
+    }
     kv->len[seq] = n_tokens;
     return QW_OK;
 }
@@ -870,8 +1028,8 @@ extern "C" int qw_kv_page_table(const qw_kv* kv, int seq, int32_t* host_out, int
 
 extern "C" qw_status qw_kv_pool_ptrs(const qw_kv* kv, void** dev_k, void** dev_v, int* n_pages) {
     if (!kv) return fail(QW_ERR_INVALID_ARG, "kv is NULL");
-    if (dev_k) *dev_k = kv->k;
-    if (dev_v) *dev_v = kv->v;
+    if (dev_k) *dev_k = kv->b8 ? (void*)kv->blocks : (void*)kv->k;
+    if (dev_v) *dev_v = kv->b8 ? nullptr : (void*)kv->v;
     if (n_pages) *n_pages = kv->n_pages;
     return QW_OK;
 }
@@ -879,6 +1037,7 @@ extern "C" qw_status qw_kv_pool_ptrs(const qw_kv* kv, void** dev_k, void** dev_v
 extern "C" qw_status qw_kv_fill_synthetic(qw_kv* kv, int seq, int n_tokens, uint64_t seed, void* stream_) {
     if (!kv) return fail(QW_ERR_INVALID_ARG, "kv is NULL");
     if (seq < 0 || seq >= kv->max_seqs) return fail(QW_ERR_INVALID_ARG, "seq id out of range");
+    if (kv->b8) return fail(QW_ERR_UNSUPPORTED, "no synthetic fill of an 8-bit cache");
     if (n_tokens < 0 || n_tokens > (1 << 22)) return fail(QW_ERR_INVALID_ARG, "n_tokens out of range");
     if (kv->len[seq] != 0) return fail(QW_ERR_BAD_STATE, "sequence %d is not empty", seq);
     if ((int)kv->pt[seq].size() * 16 < n_tokens) return fail(QW_ERR_KV_FULL, "sequence %d reserved for fewer tokens", seq);
@@ -915,8 +1074,8 @@ static SplitPlan plan_splits(const qw_model* m, int T, int max_keys) {
 
 // A decode step of one token (bf16 weights, short cache) runs each layer as two cluster
 // launches; the LM head then adds the last layer's down_proj partials to x.
-static bool dec1_step(const qw_model* m, const StepDesc& sd, bool prefill, int max_keys) {
-    return m->use_dec1 && !prefill && sd.T == 1 && m->qbits == 16 && max_keys <= dec1_max_keys();
+static bool dec1_step(const qw_model* m, const qw_kv* kv, const StepDesc& sd, bool prefill, int max_keys) {
+    return m->use_dec1 && !kv->b8 && !prefill && sd.T == 1 && m->qbits == 16 && max_keys <= dec1_max_keys();
 }
 
 // Token rows [t0, t0 + n) of a step through every layer, on stream st. The rows of a
@@ -945,7 +1104,7 @@ static qw_status run_layers(qw_model* m, qw_kv* kv, const StepDesc& sd, bool pre
     const bool long_decode = !prefill && small && (long long)T * max_keys >= kLongDecodeKeys;
     // decode of one token over a short cache (bf16 weights): attention and o_proj in one kernel,
     // its per-KV-head partials added to x by the gate/up and down_proj kernels
-    const bool fuse_ao = !prefill && small && !long_decode && m->qbits == 16 && T == 1 &&
+    const bool fuse_ao = !kv->b8 && !prefill && small && !long_decode && m->qbits == 16 && T == 1 &&
                          max_keys <= attn_oproj_max_keys() && D % 32 == 0;
     const float* xadd = fuse_ao ? m->op_part : nullptr;
     float* x = m->x + (size_t)t0 * D;
@@ -965,7 +1124,7 @@ static qw_status run_layers(qw_model* m, qw_kv* kv, const StepDesc& sd, bool pre
     // keys on one box: 3029 us per step with every GEMM spread over all SMs, 2908 with 1/2,
     // 2760 with 1/3, 2687 with 3/8, 3000 with 1/4.
     const int gsms = (!prefill && T < sd.T) ? std::max(8, m->num_sms * 3 / 8) : m->num_sms;
-    if (dec1_step(m, sd, prefill, max_keys)) {
+    if (dec1_step(m, kv, sd, prefill, max_keys)) {
         // x (m->x) -> [attention kernel: x + partials into d1_y, o_proj partials] -> [MLP
         // kernel: d1_y + o_proj partials into m->x, down_proj partials] -> next layer
         const int np = dec1_parts();
@@ -1034,7 +1193,25 @@ static qw_status run_layers(qw_model* m, qw_kv* kv, const StepDesc& sd, bool pre
             g.dbg_pos = lpos; g.dbg_slot = lslot;
             LAUNCH(launch_gemm_tc(lc, EPI_QKV_HEADS, g));
         }
-        if (small) {
+        if (kv->b8) {
+            // the new rows are staged, quantised into their blocks, then attended to like the rest
+            if (small) {
+                PROF(QW_PROF_ROPE);
+                LAUNCH(launch_qknorm_rope_append(lc, T, l, qkv, w_qn, w_kn, c.rms_eps, m->rcos, m->rsin, c.n_heads, c.n_kv_heads,
+                                                 tv, kvv, q, lpos, lslot, m->status));
+            }
+            PROF(QW_PROF_ATTN);
+            int max_len = 1;
+            for (int b = 0; b < sd.B; ++b) max_len = std::max(max_len, sd.start[b + 1] - sd.start[b]);
+            const Kv8View v8 = {kv->blocks + l * kv->layer_bytes, kv->d_pt, kv->n_pages, kv->maxp, c.n_kv_heads, kv->e_seq, kv->maxp, 0};
+            QW_TRY(kv8_append(v8, d, sd.B, T, max_len, kv->e_start, kv->e_cu, kv->k, 0, kv->v, 0, QW_F16, true, m->status, st, launches));
+            qw_kv8_attn_args a = {};
+            a.B = sd.B; a.T = T; a.max_len = max_len; a.max_keys = max_keys; a.n_heads = c.n_heads; a.dtype = QW_F16;
+            a.dev_start = kv->e_start; a.dev_cu = kv->e_cu; a.dev_q = q; a.ld_q = QD; a.scale = 0.08838834764831845f;  // 128^-0.5
+            a.dev_out = attn; a.ld_out = QD; a.dev_score_in = kv->score; a.dev_score_out = kv->score; a.ld_score = kv->ld_score;
+            a.dev_ws = kv->ws8; a.ws_bytes = kv->ws8_bytes; a.dev_status = m->status;
+            QW_TRY(kv8_attn(v8, d, a, c.n_layers, l, st, launches));
+        } else if (small) {
             if (prefill) {
                 {
                     PROF(QW_PROF_ROPE);
@@ -1155,7 +1332,7 @@ static qw_status run_step(qw_model* m, qw_kv* kv, const StepDesc& sd, bool prefi
     // is launched early (programmatic overlap with the previous step's last kernel) but lets
     // its dependents start only once its own dependency wait has returned.
     const LaunchCtx lc0 = {st, m->chain_step && m->pdl && m->prof_kind == QW_PROF_OFF, launches};
-    const bool engine = !prefill && m->use_step && m->qbits == 16 && T >= 16 && T <= 2 * kStepMaxHalf &&
+    const bool engine = !kv->b8 && !prefill && m->use_step && m->qbits == 16 && T >= 16 && T <= 2 * kStepMaxHalf &&
                         (m->prof_kind == QW_PROF_OFF || m->prof_kind == QW_PROF_STEP);
     CUDA_TRY(launch_step_begin(lc0, sd, tokens, m->embed, c.vocab, D, m->x, tv, kvv, m->status,
                                engine ? m->st_ss : nullptr, m->norms, m->st_xw));
@@ -1203,7 +1380,7 @@ static qw_status run_step(qw_model* m, qw_kv* kv, const StepDesc& sd, bool prefi
     // A decode batch of >= 16 sequences runs as two halves on two streams, so that one
     // half's latency-bound projections overlap the other half's HBM-bound attention.
     // With the debug dumps on, each half writes its own rows of them (the same kernels run).
-    const bool two = !engine && !prefill && !small && m->prof_kind == QW_PROF_OFF && m->split_decode && T >= 16;
+    const bool two = !kv->b8 && !engine && !prefill && !small && m->prof_kind == QW_PROF_OFF && m->split_decode && T >= 16;
     if (engine) {
         // the layers ran above
     } else if (two) {
@@ -1225,7 +1402,7 @@ static qw_status run_step(qw_model* m, qw_kv* kv, const StepDesc& sd, bool prefi
     // products cost more than the tensor-core GEMM, which streams the head once for any B.
     if (B < kLmGemmMinRows) {
         PROF(QW_PROF_LMHEAD);
-        const bool d1 = !engine && dec1_step(m, sd, prefill, max_keys);  // x + the last down_proj partials
+        const bool d1 = !engine && dec1_step(m, kv, sd, prefill, max_keys);  // x + the last down_proj partials
         if (d1) lc.pdl = pdl_on;
         if (B == 1 && lmhead1_ok(D, c.vocab)) {
             // the head's last CTA also ends the step (id, length): no finalize launch
@@ -1286,7 +1463,7 @@ extern "C" qw_status qw_prefill(qw_model* m, qw_kv* kv, int B, const int* seq_id
         if (lens[b] < 1) return fail(QW_ERR_INVALID_ARG, "lens[%d] = %d < 1", b, lens[b]);
         // the prompt continues the sequence's cache (chunked prefill): positions kv->len[s] ..
         const long long keys = (long long)kv->len[s] + lens[b];
-        if (keys > m->cfg.max_context) return fail(QW_ERR_INVALID_ARG, "cache + prompt longer than max_context");
+        if (keys + (kv->b8 ? kv->shift[s] : 0) > m->cfg.max_context) return fail(QW_ERR_INVALID_ARG, "cache + prompt longer than max_context");
         if ((long long)kv->pt[s].size() * 16 < keys)
             return fail(QW_ERR_KV_FULL, "sequence %d reserved for %zu tokens < %lld", s, kv->pt[s].size() * 16, keys);
         sd.seq[b] = s;
@@ -1317,7 +1494,7 @@ static qw_status decode_prepare(qw_model* m, qw_kv* kv, int B, const int* seq_id
     cap = 0;
     for (int b = 0; b < B; ++b) {
         const int s = seq_ids[b];
-        const int capacity = std::min((int)kv->pt[s].size() * 16, m->cfg.max_context);
+        const int capacity = std::min((int)kv->pt[s].size() * 16, m->cfg.max_context - (kv->b8 ? kv->shift[s] : 0));
         if ((long long)kv->len[s] + n_steps > capacity)
             return fail(QW_ERR_KV_FULL, "sequence %d has no reserved slot for position %d", s,
                         std::max(kv->len[s], capacity));

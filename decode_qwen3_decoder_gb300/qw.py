@@ -102,6 +102,10 @@ SIGNATURES = {
     "qw_profile_set": (_I, [_VP, _I, _P(_VP), _I]),
     "qw_set_option": (_I, [_VP, _I, _I]),
     "qw_trace_set": (_I, [_VP, _VP, _I]),
+    "qw_kv8_pool_bytes": (_SZ, [_VP, _I, _I, _I]),
+    "qw_kv8_alloc": (_I, [_VP, _VP, _SZ, _I, _I, _VP, _P(_VP)]),
+    "qw_kv8_scores": (_I, [_VP, _P(_VP), _P(_SZ)]),
+    "qw_kv_evict": (_I, [_VP, _I, _I, _I, _VP]),
     "qw_kv8_block_bytes": (_SZ, [_I]),
     "qw_kv8_append": (_I, [_P(qw_kv8), _I, _I, _I, _VP, _VP, _VP, _SZ, _VP, _SZ, _I, _VP, _VP]),
     "qw_kv8_read": (_I, [_P(qw_kv8), _I, _I, _I, _VP, _VP, _VP, _SZ, _VP, _SZ, _I, _VP, _VP]),
@@ -309,6 +313,27 @@ QW_KV8_BAD_POS = 4
 QW_KV8_RANGE = 8
 
 
+def qw_kv8_pool_bytes(model: int, n_pages: int, max_seqs: int, keep_scores: bool = False) -> int:
+    return load().qw_kv8_pool_bytes(model, n_pages, max_seqs, int(keep_scores))
+
+
+def qw_kv8_alloc(model: int, pool_ptr: int, pool_bytes: int, max_seqs: int, keep_scores: bool = False, stream=None) -> int:
+    out = ctypes.c_void_p()
+    _check(load().qw_kv8_alloc(model, pool_ptr, pool_bytes, max_seqs, int(keep_scores), _stream(stream), ctypes.byref(out)))
+    return out.value
+
+
+def qw_kv8_scores(kv: int):
+    """(device pointer, row stride) of an 8-bit cache's accumulated attention weights."""
+    p, ld = ctypes.c_void_p(), ctypes.c_size_t()
+    _check(load().qw_kv8_scores(kv, ctypes.byref(p), ctypes.byref(ld)))
+    return p.value, ld.value
+
+
+def qw_kv_evict(kv: int, seq_id: int, n_keep: int, n_recent: int, stream=None) -> None:
+    _check(load().qw_kv_evict(kv, seq_id, n_keep, n_recent, _stream(stream)))
+
+
 def qw_kv8_block_bytes(head_dim: int) -> int:
     return load().qw_kv8_block_bytes(head_dim)
 
@@ -404,10 +429,12 @@ class Engine:
     """Allocates (torch) the workspace, weights and KV pool that libqw borrows.
 
     ``weights`` maps HF tensor names to bf16 tensors already on the device (or to uint16
-    numpy arrays of bf16 bits, which are uploaded)."""
+    numpy arrays of bf16 bits, which are uploaded). ``kv_bits`` 8 gives an 8-bit KV cache,
+    ``keep_scores`` one that accumulates attention weights for ``qw_kv_evict``."""
 
     def __init__(self, shape, weights: Dict[str, object], max_tokens: int, max_batch: int,
-                 max_context: int, kv_pages: int, max_seqs: int, stream=None):
+                 max_context: int, kv_pages: int, max_seqs: int, stream=None, kv_bits: int = 16,
+                 keep_scores: bool = False):
         import numpy as np
         import torch
         self.shape = shape
@@ -438,9 +465,16 @@ class Engine:
         self.stream.synchronize()
         self.embed = self._w["model.embed_tokens.weight"]
         self._w = {"model.embed_tokens.weight": self.embed}
-        pool = qw_kv_pool_bytes(self.model, kv_pages, max_seqs)
-        self.pool = torch.empty(pool, dtype=torch.uint8, device=self.dev)
-        self.kv = qw_kv_alloc(self.model, self.pool.data_ptr(), pool, max_seqs, self.stream)
+        if kv_bits not in (8, 16):
+            raise ValueError("kv_bits must be 8 or 16")
+        if kv_bits == 8:
+            pool = qw_kv8_pool_bytes(self.model, kv_pages, max_seqs, keep_scores)
+            self.pool = torch.empty(pool, dtype=torch.uint8, device=self.dev)
+            self.kv = qw_kv8_alloc(self.model, self.pool.data_ptr(), pool, max_seqs, keep_scores, self.stream)
+        else:
+            pool = qw_kv_pool_bytes(self.model, kv_pages, max_seqs)
+            self.pool = torch.empty(pool, dtype=torch.uint8, device=self.dev)
+            self.kv = qw_kv_alloc(self.model, self.pool.data_ptr(), pool, max_seqs, self.stream)
         self.stream.synchronize()
 
     @staticmethod

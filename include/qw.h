@@ -474,6 +474,30 @@ qw_status qw_kv8_evict(const qw_kv8* kv, int B, int max_len, const int32_t* dev_
                        const int32_t* dev_dst_table, const float* dev_score, float* dev_score_out, size_t ld_score,
                        int32_t* dev_kept, int32_t* dev_new_len, int32_t* dev_status, void* stream);
 
+/* A model's KV cache in this format. qw_kv8_alloc binds a caller-owned pool (256-byte aligned, at
+ * least qw_kv8_pool_bytes) as an 8-bit cache: qw_kv_reserve, _reset, _truncate, _length and
+ * _page_table, qw_prefill, qw_decode_step(s) and qw_generate(_eos) take it like a cache of
+ * qw_kv_alloc, at half the bytes a token. Each layer's new K/V rows are staged as fp16 in the pool,
+ * appended as by qw_kv8_append and attended to as by qw_kv8_attn; the batch-1 cluster path, the
+ * two-stream split and the decode-step kernel are not used. qw_kv_fill_synthetic gives
+ * QW_ERR_UNSUPPORTED, qw_kv_pool_ptrs the blocks ([n_layers][n_pages][n_kv_heads]) as dev_k and a
+ * NULL dev_v, and the slots of qw_debug_set are the staging rows (the token's index in the call).
+ * keep_scores: the pool also holds, for every layer and KV head, the weight that each cached token
+ * has been given by all queries since it was appended (dropped positions start again at 0). */
+size_t qw_kv8_pool_bytes(const qw_model* m, int n_pages, int max_seqs, int keep_scores);
+qw_status qw_kv8_alloc(qw_model* m, void* dev_pool, size_t pool_bytes, int max_seqs, int keep_scores, void* stream, qw_kv** out);
+
+/* Those weights: [max_seqs][n_layers][n_kv_heads][*ld_score] fp32 in the pool (QW_ERR_UNSUPPORTED for a
+ * cache that keeps none). */
+qw_status qw_kv8_scores(const qw_kv* kv, float** dev_score, size_t* ld_score);
+
+/* Cuts sequence seq_id to n_keep cached tokens, as qw_kv8_evict in place, each layer and KV head
+ * choosing by its own weights (nothing happens if it has no more). The length becomes n_keep and
+ * the pages stay reserved; later tokens go on at the positions they would have had (RoPE), which
+ * therefore still count against max_context. Asynchronous on `stream`. QW_ERR_UNSUPPORTED for a
+ * cache without scores. */
+qw_status qw_kv_evict(qw_kv* kv, int seq_id, int n_keep, int n_recent, void* stream);
+
 /* ---- For callers that cannot allocate device memory ---------------------------------- */
 
 /* The page has no counterpart to this entry point; it serves callers that must not call
