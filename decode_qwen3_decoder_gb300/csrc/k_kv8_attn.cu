@@ -848,8 +848,8 @@ __device__ __forceinline__ void sts128(uint32_t at, uint32_t a, uint32_t b, uint
 }
 
 // Rows [row0, row0 + 128) of an entry's (token, head) rows as a swizzled fp16 operand, by four warps
-// (w = 0 .. 3), fetched into registers and stored in two steps: HD / 8 lanes take a row's 16-byte
-// chunks, so a request covers whole rows. A bf16 row is divided by the power of two of its largest
+// (w = 0 .. 3), fetched into registers and given to sink(byte offset, 16 bytes): HD / 8 lanes take a
+// row's 16-byte chunks, so a request covers whole rows. A bf16 row is divided by the power of two of its largest
 // value (see row_operand), which goes to put(row, mul); rows past the entry are zeros.
 template <int HD>
 struct QTile {
@@ -868,8 +868,8 @@ __device__ __forceinline__ void fetch_q(QTile<HD>& q, const Kv8AttnP& p, int r0,
                                                      (size_t)(head * p.G + row - tok * p.G) * HD + ch * 8);
     }
 }
-template <int HD, int DT, typename Put>
-__device__ __forceinline__ void store_q(QTile<HD>& q, int w, int lane, uint32_t mat, Put put) {
+template <int HD, int DT, typename Sink, typename Put>
+__device__ __forceinline__ void store_q(QTile<HD>& q, int w, int lane, Sink sink, Put put) {
     constexpr int LPR = QTile<HD>::LPR;
     const int ch = lane % LPR, rw = w * 32 + lane / LPR;
 #pragma unroll
@@ -891,7 +891,7 @@ __device__ __forceinline__ void store_q(QTile<HD>& q, int w, int lane, uint32_t 
             for (int k = 0; k < 4; ++k) v[k] = pack_h2(bf_lo(v[k]) * inv, bf_hi(v[k]) * inv);
             x = make_uint4(v[0], v[1], v[2], v[3]);
         }
-        sts128(mat + (ch >> 3) * CT_SUB + r * 128 + (((ch & 7) ^ (r & 7)) << 4), x.x, x.y, x.z, x.w);
+        sink((ch >> 3) * CT_SUB + r * 128 + (((ch & 7) ^ (r & 7)) << 4), x);
         if (ch == 0) put(r, mul);
     }
 }
@@ -1148,7 +1148,8 @@ __global__ void __launch_bounds__(CT_THREADS, 1) k_kv8_chunk(const __grid_consta
             {
                 QTile<HD> qt;
                 fetch_q<HD>(qt, p, r0, head, rt0, rows, wq, lane);
-                store_q<HD, DT>(qt, wq, lane, qa, [&](int rr, float mul) { muls[rr] = mul; });
+                store_q<HD, DT>(qt, wq, lane, [&](int off, const uint4& v) { sts128(qa + off, v.x, v.y, v.z, v.w); },
+                                [&](int rr, float mul) { muls[rr] = mul; });
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
@@ -1342,30 +1343,53 @@ __global__ void __launch_bounds__(256) k_kv8_chunk_combine(const __grid_constant
 //
 // The normalisers are known, so the weights need only S again, and the sum over rows is a thread's
 // own if the keys are the rows of the MMA: a CTA keeps 128 keys of one (entry, head) as the A operand
-// and walks the query rows in tiles of 128 (B, two buffers). S^T = K Q^T lands in TMEM (two
-// buffers); thread = key adds the exponentials of its row in order, so equal inputs give equal
-// bits. 2 HD MACs and one exponential a (row, key) pair; four warps load and convert the next
-// query tile meanwhile and one of their threads issues the MMAs. Two CTAs share an SM.
+// and walks the query rows in tiles of 128 (B). S^T = K Q^T lands in TMEM (two buffers); eight
+// warps, thread = key and half of the rows, add the exponentials in order, so equal inputs give
+// equal bits. 2 HD MACs and one exponential a (row, key) pair, and the exponentials bound it: every
+// key tile needs every query tile, so k_kv8_score_prep lays these out once as swizzled operands with
+// their rows' constants, and a tile costs two bulk copies (converting them here, in every CTA, took
+// 29 us of 127 and the warps that the sums wanted). Two CTAs share an SM.
 // =======================================================================================
+constexpr int CS_THREADS = 288;  // warps 0-7 sums, 8 copies and MMAs
 constexpr int CS_TMEM = 256;
-constexpr int CS_THREADS = 256;  // warps 0-3 sums, 4-7 loaders (4 issues the MMAs too)
 template <int HD>
 struct Cs {
     static constexpr int KEYS = 128;
-    static constexpr int MAT = CT_SUB * (HD / 64);
-    static constexpr int OFF_Q = MAT, OFF_ROW = 3 * MAT, OFF_BAR = OFF_ROW + 4 * 3 * CT_ROWS * 4;
-    static constexpr int SMEM = 1024 + OFF_BAR + 256;
+    static constexpr int MAT = CT_SUB * (HD / 64), ROWC = 3 * CT_ROWS * 4;  // operand; -lse2, logit factor, last visible position
+    static constexpr int PREP = MAT + ROWC;                                  // a prepared tile
+    static constexpr int RING = HD == 128 ? 2 : 4;
+    static constexpr int OFF_Q = MAT, OFF_ROW = OFF_Q + RING * MAT, OFF_ACC = OFF_ROW + 2 * RING * ROWC;
+    static constexpr int OFF_BAR = OFF_ACC + KEYS * 4, SMEM = 1024 + OFF_BAR + 256;
 };
 
+// One query tile of one (entry, head) into prep[(b * n_kv + head) * tiles + tile].
 template <int HD, int DT>
-__global__ void __launch_bounds__(CS_THREADS, 2) k_kv8_score(const __grid_constant__ Kv8AttnP p) {
-    constexpr int MAT = Cs<HD>::MAT, NSUB = HD / 64, CH = HD / 16;
+__global__ void __launch_bounds__(128) k_kv8_score_prep(const __grid_constant__ Kv8AttnP p, uint8_t* prep) {
+    pdl_wait();
+    pdl_launch();
+    const int t = threadIdx.x, b = blockIdx.z, head = blockIdx.y, tile = blockIdx.x;
+    int s, r0, n;
+    if (!attn_entry(p, b, s, r0, n) || tile * CT_ROWS >= n * p.G) return;
+    const int rows = n * p.G, row = tile * CT_ROWS + t, tok = min(row_token(p, row), n - 1);
+    uint8_t* at = prep + (((size_t)b * p.kv.n_kv + head) * gridDim.x + tile) * Cs<HD>::PREP;
+    float* rc = reinterpret_cast<float*>(at + Cs<HD>::MAT);
+    QTile<HD> qt;
+    fetch_q<HD>(qt, p, r0, head, tile * CT_ROWS, rows, t >> 5, t & 31);
+    const float z = row < rows ? p.lse2[(size_t)(r0 + tok) * p.n_heads + head * p.G + row - tok * p.G] : 0.f;
+    store_q<HD, DT>(qt, t >> 5, t & 31, [&](int off, const uint4& v) { *reinterpret_cast<uint4*>(at + off) = v; },
+                    [&](int r, float mul) { rc[CT_ROWS + r] = mul * p.scale_log2; });
+    rc[t] = -z;
+    rc[2 * CT_ROWS + t] = __int_as_float(row < rows ? s + tok : -1);
+}
+
+template <int HD, int DT>
+__global__ void __launch_bounds__(CS_THREADS, 2) k_kv8_score(const __grid_constant__ Kv8AttnP p, const uint8_t* prep, int tiles) {
+    constexpr int MAT = Cs<HD>::MAT, NSUB = HD / 64, CH = HD / 16, RING = Cs<HD>::RING, ROWC = Cs<HD>::ROWC;
     extern __shared__ uint8_t cs_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(cs_raw) + 1023) & ~(uintptr_t)1023);
-    float* rowc = reinterpret_cast<float*>(sm + Cs<HD>::OFF_ROW);  // [4][3][128]: -lse2, logit factor, last visible position
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Cs<HD>::OFF_BAR);
-    uint64_t *q_full = bars, *q_empty = bars + 2, *s_full = bars + 4, *s_empty = bars + 6, *mma_fin = bars + 8;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 9);
+    uint64_t *q_full = bars, *q_empty = bars + 4, *s_full = bars + 8, *s_empty = bars + 10, *mma_fin = bars + 12;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 13);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int b = blockIdx.z, head = blockIdx.y, key0 = blockIdx.x * Cs<HD>::KEYS;
@@ -1374,28 +1398,28 @@ __global__ void __launch_bounds__(CS_THREADS, 2) k_kv8_score(const __grid_consta
     int s, r0, n;
     if (!attn_entry(p, b, s, r0, n) || n == 0 || key0 >= s + n) return;
     const int rows = n * p.G, kend = s + n;
-    const int t0 = max(0, key0 - s) * p.G / CT_ROWS, t1 = (rows + CT_ROWS - 1) / CT_ROWS;  // row tiles that see a key of these
-    auto wait = [&](uint64_t* bar, int parity) { return mbar_wait(smem_u32(bar), (uint32_t)parity & 1u, abort_flag); };
+    const int t0 = max(0, key0 - s) * p.G / CT_ROWS, t1 = (rows + CT_ROWS - 1) / CT_ROWS, nt = t1 - t0;  // row tiles that see a key of these
+    auto wait = [&](uint64_t* bar, int parity) {
+        return __all_sync(0xffffffffu, ct_wait(smem_u32(bar), (uint32_t)parity & 1u, abort_flag));
+    };
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(q_full + i), 4);
+        for (int i = 0; i < RING; ++i) {
+            mbar_init(smem_u32(q_full + i), 1);
             mbar_init(smem_u32(q_empty + i), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(s_full + i), 1);
-            mbar_init(smem_u32(s_empty + i), 4);
+            mbar_init(smem_u32(s_empty + i), 8);
         }
         mbar_init(smem_u32(mma_fin), 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 4) {
+    if (warp == 8) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(CS_TMEM)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
     const int* table = kv8_row(p.kv, p.kv.table, b);
     auto block_of = [&](int pi) -> const uint8_t* {
         int id = table[pi];
@@ -1405,153 +1429,153 @@ __global__ void __launch_bounds__(CS_THREADS, 2) k_kv8_score(const __grid_consta
         }
         return kv8_block(p.kv, b, id, head, Kv8<HD>::BLK);
     };
-    if (warp >= 4) {
-        // ---------------- loaders: the keys once, then the query tiles ----------------
-        const int t = threadIdx.x - 128;
-        {
-            const int row = t, tk = row & 15;  // thread = key
-            const bool on = key0 + row < kend;
-            const uint8_t* src = on ? block_of(key0 / KV8_PAGE + (row >> 4)) + tk * HD : nullptr;
-#pragma unroll 4
-            for (int pos = 0; pos < CH; ++pos) {
-                const int ch = kv8_k_pos<HD>(tk, pos);
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (on) v = *reinterpret_cast<const uint4*>(src + pos * 16);
-                const uint32_t at = smem_u32(sm) + (ch >> 2) * CT_SUB + row * 128;
-                const int c0 = 2 * (ch & 3);
-                sts128(at + ((c0 ^ (row & 7)) << 4), kv8_dec2(v.x & 0xFFFFu), kv8_dec2(v.x >> 16), kv8_dec2(v.y & 0xFFFFu), kv8_dec2(v.y >> 16));
-                sts128(at + (((c0 + 1) ^ (row & 7)) << 4), kv8_dec2(v.z & 0xFFFFu), kv8_dec2(v.z >> 16), kv8_dec2(v.w & 0xFFFFu), kv8_dec2(v.w >> 16));
-            }
+    if (warp < 8) {  // the keys: thread = half a row
+        const int row = threadIdx.x >> 1, tk = row & 15;
+        const bool on = key0 + row < kend;
+        const uint8_t* src = on ? block_of(key0 / KV8_PAGE + (row >> 4)) + tk * HD : nullptr;
+#pragma unroll
+        for (int i = 0; i < CH / 2; ++i) {
+            const int pos = (threadIdx.x & 1) * (CH / 2) + i, ch = kv8_k_pos<HD>(tk, pos);
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (on) v = *reinterpret_cast<const uint4*>(src + pos * 16);
+            const uint32_t at = smem_u32(sm) + (ch >> 2) * CT_SUB + row * 128;
+            const int c0 = 2 * (ch & 3);
+            sts128(at + ((c0 ^ (row & 7)) << 4), kv8_dec2(v.x & 0xFFFFu), kv8_dec2(v.x >> 16), kv8_dec2(v.y & 0xFFFFu), kv8_dec2(v.y >> 16));
+            sts128(at + (((c0 + 1) ^ (row & 7)) << 4), kv8_dec2(v.z & 0xFFFFu), kv8_dec2(v.z >> 16), kv8_dec2(v.w & 0xFFFFu), kv8_dec2(v.w >> 16));
         }
-        auto row_lse = [&](int rt) {
-            const int row = min(rt * CT_ROWS + t, rows - 1), tok = row_token(p, row);
-            return p.lse2[(size_t)(r0 + tok) * p.n_heads + head * p.G + row - tok * p.G];
-        };
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    float acc = 0.f;
+    bool good = true;
+    const int key = key0 + (warp & 3) * 32 + lane;
+    const bool on = warp < 8 && key < kend;
+    if (warp == 8) {
+        // ---------------- copies and MMAs ----------------
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         const uint64_t kd = sw128_desc(smem_u32(sm)), qd = sw128_desc(smem_u32(sm + Cs<HD>::OFF_Q));
-        QTile<HD> qt;
-        fetch_q<HD>(qt, p, r0, head, t0 * CT_ROWS, rows, warp - 4, lane);
-        float z = row_lse(t0);
-        for (int rt = t0, i = 0; rt < t1; ++rt, ++i) {
-            const int buf = i & 1;
-            // thread's row of the tile: what the sums need of it
-            const int row = rt * CT_ROWS + t;
-            const bool v = row < rows;
-            const int tok = v ? row_token(p, row) : 0;
-            if (i >= 2 && !__all_sync(0xffffffffu, wait(q_empty + buf, (i >> 1) - 1))) {
-                *abort_flag = 1;
-                break;
-            }
-            // rowc[i % 4]: the tile four before has been summed, as S^T of the tile two before was issued
-            float* rc = rowc + (i & 3) * 3 * CT_ROWS;
-            store_q<HD, DT>(qt, warp - 4, lane, smem_u32(sm + Cs<HD>::OFF_Q + buf * MAT), [&](int r, float mul) { rc[CT_ROWS + r] = mul * p.scale_log2; });
-            rc[t] = -z;
-            rc[2 * CT_ROWS + t] = __int_as_float(v ? s + tok : -1);
-            if (rt + 1 < t1) {  // the next tile is on its way while this one is multiplied
-                fetch_q<HD>(qt, p, r0, head, (rt + 1) * CT_ROWS, rows, warp - 4, lane);
-                z = row_lse(rt + 1);
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(q_full + buf));
-            if (warp == 4) {
-                if (!__all_sync(0xffffffffu, wait(q_full + buf, i >> 1) && (i < 2 || wait(s_empty + buf, (i >> 1) - 1)))) {
-                    *abort_flag = 1;
-                    break;
-                }
-                tc_fence_after();
-                if (elect_one()) {
-                    const uint64_t q0 = qd + (uint32_t)(buf * (MAT >> 4));
-#pragma unroll
-                    for (int sub = 0; sub < NSUB; ++sub)
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            umma_f16(tm + buf * 128, kd + sub * (CT_SUB >> 4) + 2 * kk, q0 + sub * (CT_SUB >> 4) + 2 * kk,
-                                     idesc_f16(128, CT_ROWS), (sub | kk) ? 1u : 0u);
-                    umma_commit(smem_u32(s_full + buf));
-                    umma_commit(smem_u32(q_empty + buf));
-                }
+        const uint8_t* src = prep + (((size_t)b * p.kv.n_kv + head) * tiles + t0) * Cs<HD>::PREP;
+        int issued = 0;
+        auto copy = [&](int i) {
+            const int st = i % RING;
+            if (elect_one()) {
+                const uint32_t bar = smem_u32(q_full + st);
+                mbar_expect_tx(bar, Cs<HD>::PREP);
+                bulk_copy(smem_u32(sm + Cs<HD>::OFF_Q + st * MAT), src + (size_t)i * Cs<HD>::PREP, MAT, bar);
+                // two rings deep: copy i follows the MMA of tile i - RING + 1, which waited for the sums of i - RING - 1
+                bulk_copy(smem_u32(sm + Cs<HD>::OFF_ROW + (i % (2 * RING)) * ROWC), src + (size_t)i * Cs<HD>::PREP + MAT, ROWC, bar);
             }
             __syncwarp();
-        }
-        if (warp == 4) {
-            // the commits' asynchronous arrivals land before the CTA ends
-            if (elect_one()) umma_commit(smem_u32(mma_fin));
-            __syncwarp();
-            const uint64_t w0 = globaltimer_ns();
-            while (!mbar_try_wait(smem_u32(mma_fin), 0) && globaltimer_ns() - w0 < kTcWaitNs) {
-            }
-        }
-        __syncwarp();
-    } else {
-        // ---------------- sums: thread = key = TMEM lane ----------------
-        const int key = key0 + threadIdx.x;
-        const bool on = key < kend;
-        const float sk = on ? *reinterpret_cast<const float*>(block_of(key / KV8_PAGE) + Kv8<HD>::SOFF) : 1.f;
-        const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
-        float acc = 0.f;
-        bool good = true;
-        for (int rt = t0, i = 0; rt < t1; ++rt, ++i) {
-            const int buf = i & 1;
-            if (!__all_sync(0xffffffffu, wait(s_full + buf, i >> 1))) {
+            issued = i + 1;
+        };
+        for (int i = 0; i < min(RING - 1, nt); ++i) copy(i);
+        for (int i = 0; i < nt; ++i) {
+            const int st = i % RING, buf = i & 1;
+            if (!wait(q_full + st, i / RING) || (i >= 2 && !wait(s_empty + buf, (i >> 1) - 1))) {
                 good = false;
                 break;
             }
             tc_fence_after();
-            const float* rc = rowc + (i & 3) * 3 * CT_ROWS;
+            if (elect_one()) {
+                const uint64_t q0 = qd + (uint32_t)(st * (MAT >> 4));
+#pragma unroll
+                for (int sub = 0; sub < NSUB; ++sub)
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_f16(tm + buf * 128, kd + sub * (CT_SUB >> 4) + 2 * kk, q0 + sub * (CT_SUB >> 4) + 2 * kk,
+                                 idesc_f16(128, CT_ROWS), (sub | kk) ? 1u : 0u);
+                umma_commit(smem_u32(s_full + buf));
+                umma_commit(smem_u32(q_empty + st));
+            }
+            __syncwarp();
+            const int c = i + RING - 1;  // into the stage of tile i - 1
+            if (c < nt) {
+                if (i >= 1 && !wait(q_empty + c % RING, (i - 1) / RING)) {
+                    good = false;
+                    break;
+                }
+                copy(c);
+            }
+        }
+        if (!good) *abort_flag = 1;
+        // the copies and the commits' asynchronous arrivals land before the CTA ends
+        if (elect_one()) umma_commit(smem_u32(mma_fin));
+        __syncwarp();
+        const uint64_t w0 = globaltimer_ns();
+        while (!mbar_try_wait(smem_u32(mma_fin), 0) && globaltimer_ns() - w0 < kTcWaitNs) {
+        }
+        for (int i = max(0, issued - RING); i < issued; ++i)
+            while (!mbar_try_wait(smem_u32(q_full + i % RING), (i / RING) & 1) && globaltimer_ns() - w0 < kTcWaitNs) {
+            }
+        __syncwarp();
+    } else {
+        // ---------------- sums: thread = key = TMEM lane, warps 4-7 the second 64 rows of a tile ----------------
+        const int half = warp >> 2;
+        const float sk = on ? *reinterpret_cast<const float*>(block_of(key / KV8_PAGE) + Kv8<HD>::SOFF) : 1.f;
+        const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * 64;
+        const float f16 = p.scale_log2 * sk;
+        const uint64_t f2 = pack2(f16, f16), k2 = pack2(sk, sk);
+        for (int i = 0; i < nt; ++i) {
+            const int buf = i & 1, rt = t0 + i;
+            if (!wait(s_full + buf, i >> 1)) {
+                good = false;
+                break;
+            }
+            tc_fence_after();
+            const float* rc = reinterpret_cast<const float*>(sm + Cs<HD>::OFF_ROW + (i % (2 * RING)) * ROWC) + half * 64;
             // rows of the tile before the last key's token see not all of these keys
             const bool masked = s + rt * CT_ROWS / p.G < key0 + Cs<HD>::KEYS - 1 || (rt + 1) * CT_ROWS > rows;
             uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
-            const float f16 = p.scale_log2 * sk;
-            uint32_t x[2][32];
-            TMEM_LD32(lane_base + buf * 128, x[0]);
 #pragma unroll
-            for (int cc = 0; cc < 4; ++cc) {
+            for (int cc = 0; cc < 2; ++cc) {
+                uint32_t y[32];
+                TMEM_LD32(lane_base + buf * 128 + cc * 32, y);
                 tmem_wait_ld();
-                if (cc < 3) TMEM_LD32(lane_base + buf * 128 + (cc + 1) * 32, x[(cc + 1) & 1]);
-                const uint32_t* y = x[cc & 1];
                 // four rows a turn: their constants are one or two 16-byte broadcasts
 #pragma unroll
                 for (int u = 0; u < 32; u += 4) {
                     const float4 z = *reinterpret_cast<const float4*>(rc + cc * 32 + u);
-                    uint64_t fa = pack2(f16, f16), fb = fa;
+                    uint64_t fa = f2, fb = f2;
                     if (DT == QW_BF16) {
                         const float4 f = *reinterpret_cast<const float4*>(rc + CT_ROWS + cc * 32 + u);
-                        const uint64_t k2 = pack2(sk, sk);
                         fa = mul2(pack2(f.x, f.y), k2);
                         fb = mul2(pack2(f.z, f.w), k2);
                     }
-                    float t0, t1, t2, t3;
-                    unpack2(fma2(pack2u(y[u], y[u + 1]), fa, pack2(z.x, z.y)), t0, t1);
-                    unpack2(fma2(pack2u(y[u + 2], y[u + 3]), fb, pack2(z.z, z.w)), t2, t3);
+                    float e0, e1, e2, e3;
+                    unpack2(fma2(pack2u(y[u], y[u + 1]), fa, pack2(z.x, z.y)), e0, e1);
+                    unpack2(fma2(pack2u(y[u + 2], y[u + 3]), fb, pack2(z.z, z.w)), e2, e3);
                     if (masked) {
                         const int4 lim = *reinterpret_cast<const int4*>(rc + 2 * CT_ROWS + cc * 32 + u);
-                        t0 = key <= lim.x ? t0 : -INFINITY;
-                        t1 = key <= lim.y ? t1 : -INFINITY;
-                        t2 = key <= lim.z ? t2 : -INFINITY;
-                        t3 = key <= lim.w ? t3 : -INFINITY;
+                        e0 = key <= lim.x ? e0 : -INFINITY;
+                        e1 = key <= lim.y ? e1 : -INFINITY;
+                        e2 = key <= lim.z ? e2 : -INFINITY;
+                        e3 = key <= lim.w ? e3 : -INFINITY;
                     }
-                    sum[(u >> 1) & 3] = add2(sum[(u >> 1) & 3], pack2(ex2(t0), ex2(t1)));
-                    sum[((u >> 1) + 1) & 3] = add2(sum[((u >> 1) + 1) & 3], pack2(ex2(t2), ex2(t3)));
+                    sum[(u >> 1) & 3] = add2(sum[(u >> 1) & 3], pack2(ex2(e0), ex2(e1)));
+                    sum[((u >> 1) + 1) & 3] = add2(sum[((u >> 1) + 1) & 3], pack2(ex2(e2), ex2(e3)));
                 }
             }
-            float e0, e1;
-            unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), e0, e1);
-            acc += e0 + e1;
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(s_empty + buf));
-        }
-        if (good && on) {
-            const size_t at = score_row(p, b, head) + key;
-            p.score_out[at] = (p.score_in ? p.score_in[at] : 0.f) + acc;
+            float e0, e1;
+            unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), e0, e1);
+            acc += e0 + e1;
         }
         if (!good) *abort_flag = 1;
+        if (half) reinterpret_cast<float*>(sm + Cs<HD>::OFF_ACC)[key - key0] = acc;
     }
     tc_fence_before();
     __syncthreads();
     if (*abort_flag && threadIdx.x == 0) atomicOr(p.status, QW_KV8_TIMEOUT);
-    if (warp == 4) {
+    if (warp < 4 && on && !*abort_flag) {
+        const size_t at = score_row(p, b, head) + key;
+        p.score_out[at] = (p.score_in ? p.score_in[at] : 0.f) + (acc + reinterpret_cast<const float*>(sm + Cs<HD>::OFF_ACC)[key - key0]);
+    }
+    if (warp == 8) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(CS_TMEM) : "memory");
     }
@@ -1565,7 +1589,7 @@ struct Plan {
     bool tbuf;         // scores from stored logits
     int nrow, stages, n_cta, smem;  // decode
     int tiles, splits;              // k_kv8_chunk
-    size_t off_o, off_ml, off_t, bytes;
+    size_t off_o, off_ml, off_t, off_prep, bytes;
 };
 
 int sm_count() {
@@ -1576,6 +1600,8 @@ int sm_count() {
     }();
     return n;
 }
+
+int score_tiles(int max_len, int T, int G) { return (int)(((long long)std::min(max_len, std::max(T, 1)) * G + CT_ROWS - 1) / CT_ROWS); }
 
 // `avail`: most bytes that a decode's stored logits may take.
 Plan make_plan(int n_kv, int HD, int B, int T, int max_len, int max_keys, int n_heads, bool score, size_t avail) {
@@ -1619,6 +1645,8 @@ Plan make_plan(int n_kv, int HD, int B, int T, int max_len, int max_keys, int n_
         q.off_o = put(part * HD * 4);
         q.off_ml = put(part * 2 * 4);
     }
+    if (score && !q.tbuf)
+        q.off_prep = put((size_t)B * n_kv * score_tiles(max_len, T, G) * (CT_ROWS * HD * 2 + 3 * CT_ROWS * 4));
     q.bytes = std::max(q.bytes, (size_t)256);
     return q;
 }
@@ -1629,11 +1657,14 @@ cudaError_t allow_smem(K kern, int bytes) {
 }
 
 template <int HD, int DT>
-cudaError_t run_score(const Kv8AttnP& p, int B, cudaStream_t st, int* launches) {
+cudaError_t run_score(const Kv8AttnP& p, int B, uint8_t* prep, cudaStream_t st, int* launches) {
     LaunchCtx c = {st, true, launches};
     if (cudaError_t e = allow_smem(k_kv8_score<HD, DT>, Cs<HD>::SMEM)) return e;
+    const int rows = score_tiles(p.max_len, p.T, p.G);
+    cudaError_t e = launch_k(c, k_kv8_score_prep<HD, DT>, dim3(rows, p.kv.n_kv, B), dim3(128), 0, p, prep);
+    if (e != cudaSuccess) return e;
     const unsigned tiles = (unsigned)((p.max_keys + Cs<HD>::KEYS - 1) / Cs<HD>::KEYS);
-    return launch_k(c, k_kv8_score<HD, DT>, dim3(tiles, p.kv.n_kv, B), dim3(CS_THREADS), (size_t)Cs<HD>::SMEM, p);
+    return launch_k(c, k_kv8_score<HD, DT>, dim3(tiles, p.kv.n_kv, B), dim3(CS_THREADS), (size_t)Cs<HD>::SMEM, p, (const uint8_t*)prep, rows);
 }
 
 template <int HD, int DT>
@@ -1663,7 +1694,7 @@ cudaError_t run_attn(const Kv8AttnP& p, const Plan& q, int B, char* ws, cudaStre
             e = launch_k(c, k_kv8_combine<HD, DT>, dim3(B * p.kv.n_kv, chunks), dim3(KD_WARPS * 32), (size_t)smem, P);
             if (e != cudaSuccess) return e;
         }
-        return p.score_out && !q.tbuf ? run_score<HD, DT>(p, B, st, launches) : cudaSuccess;
+        return p.score_out && !q.tbuf ? run_score<HD, DT>(p, B, (uint8_t*)ws + q.off_prep, st, launches) : cudaSuccess;
     }
     Kv8ChunkP P = {};
     P.a = p;
@@ -1681,7 +1712,7 @@ cudaError_t run_attn(const Kv8AttnP& p, const Plan& q, int B, char* ws, cudaStre
     e = launch_k(c, k_kv8_chunk<HD, DT>, dim3(p.kv.n_kv, B, (q.tiles + 1) / 2 * q.splits), dim3(CT_THREADS), (size_t)Ct<HD>::SMEM, P);
     if (e == cudaSuccess && q.splits > 1)
         e = launch_k(c, k_kv8_chunk_combine<HD, DT>, dim3(q.tiles * CT_ROWS / 8, p.kv.n_kv, B), dim3(256), 0, P);
-    return e == cudaSuccess && p.score_out ? run_score<HD, DT>(p, B, st, launches) : e;
+    return e == cudaSuccess && p.score_out ? run_score<HD, DT>(p, B, (uint8_t*)ws + q.off_prep, st, launches) : e;
 }
 
 }  // namespace
