@@ -780,9 +780,10 @@ template <int HD>
 struct Ct {
     static constexpr int MAT = CT_SUB * (HD / 64), RAW = CT_BK * HD;
     static constexpr int RING = HD == 128 ? 5 : 8;  // code tiles (K or V) in flight
-    static constexpr int OFF_K = 2 * MAT, OFF_V = 3 * MAT, OFF_R = 4 * MAT;
+    static constexpr int NB = HD == 128 ? 1 : 2;    // operand buffers of K and of V
+    static constexpr int OFF_K = 2 * MAT, OFF_V = OFF_K + NB * MAT, OFF_R = OFF_V + NB * MAT;
     static constexpr int OFF_MUL = OFF_R + RING * RAW, OFF_SC = OFF_MUL + 2 * CT_ROWS * 4, OFF_BAR = OFF_SC + 8 * 8 * 16;
-    static constexpr int SMEM = 1024 + OFF_BAR + 256;
+    static constexpr int SMEM = 1024 + OFF_BAR + 512;
 };
 
 // mbar_wait that looks at the clock only after 64 failed tries.
@@ -899,13 +900,13 @@ __device__ __forceinline__ void store_q(QTile<HD>& q, int w, int lane, Sink sink
 template <int HD, int DT>
 __global__ void __launch_bounds__(CT_THREADS, 1) k_kv8_chunk(const __grid_constant__ Kv8ChunkP P) {
     const Kv8AttnP& p = P.a;
-    constexpr int NSUB = HD / 64, CH = HD / 16, RP = 128 / CH, NU = CT_BK / RP, MAT = Ct<HD>::MAT, RAW = Ct<HD>::RAW, RING = Ct<HD>::RING;
+    constexpr int NSUB = HD / 64, CH = HD / 16, RP = 128 / CH, NU = CT_BK / RP, MAT = Ct<HD>::MAT, NB = Ct<HD>::NB, RAW = Ct<HD>::RAW, RING = Ct<HD>::RING;
     extern __shared__ uint8_t ct_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ct_raw) + 1023) & ~(uintptr_t)1023);
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Ct<HD>::OFF_BAR);
-    uint64_t *r_full = bars, *r_empty = bars + 8, *k_full = bars + 16, *k_empty = bars + 17, *v_full = bars + 18, *v_empty = bars + 19,
-             *s_full = bars + 20, *p_full = bars + 22, *pv_done = bars + 24, *q_ready = bars + 26, *mma_fin = bars + 28;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 30);
+    uint64_t *r_full = bars, *r_empty = bars + 8, *k_full = bars + 16, *k_empty = bars + 18, *v_full = bars + 20, *v_empty = bars + 22;
+    uint64_t *s_full = bars + 24, *p_full = bars + 28, *pv_done = bars + 32, *q_ready = bars + 34, *mma_fin = bars + 36;  // s, p: [t][half]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 38);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     float4* scales = reinterpret_cast<float4*>(sm + Ct<HD>::OFF_SC);  // [8][8]: 2^ek, ev, 2^-ev of the pages of step i % 8
     pdl_wait();
@@ -948,13 +949,17 @@ __global__ void __launch_bounds__(CT_THREADS, 1) k_kv8_chunk(const __grid_consta
             mbar_init(smem_u32(r_full + i), 1);
             mbar_init(smem_u32(r_empty + i), 4);
         }
-        mbar_init(smem_u32(k_full), 4);
-        mbar_init(smem_u32(k_empty), n_rt);
-        mbar_init(smem_u32(v_full), 4);
-        mbar_init(smem_u32(v_empty), n_rt);
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < NB; ++i) {
+            mbar_init(smem_u32(k_full + i), 4);
+            mbar_init(smem_u32(k_empty + i), n_rt);
+            mbar_init(smem_u32(v_full + i), 4);
+            mbar_init(smem_u32(v_empty + i), n_rt);
+        }
+        for (int i = 0; i < 4; ++i) {
             mbar_init(smem_u32(s_full + i), 1);
             mbar_init(smem_u32(p_full + i), 4);
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(pv_done + i), 1);
             mbar_init(smem_u32(q_ready + i), 4);
             mbar_init(smem_u32(mma_fin + i), 1);
@@ -1001,7 +1006,8 @@ __global__ void __launch_bounds__(CT_THREADS, 1) k_kv8_chunk(const __grid_consta
             };
             auto put = [&](int i, const uint8_t* blk, bool is_v, float2 sc) {
                 if (use && !wait(r_empty + st, use - 1)) return false;
-                // [i % 8]: the ring is less than 5 steps deep, so the softmax of step i - 8 has passed
+                // [i % 8]: at most 4 steps are in the ring and 2 in the operand buffers, and S of a step follows
+                // the softmax of the step before, so the softmax of step i - 8 has passed
                 if (!is_v && lane < 8) {
                     const int ev = kv8_log2(sc.y);
                     scales[(i & 7) * 8 + lane] = make_float4(sc.x, (float)ev, kv8_pow2(-ev), 0.f);
@@ -1034,45 +1040,56 @@ __global__ void __launch_bounds__(CT_THREADS, 1) k_kv8_chunk(const __grid_consta
                 while (!mbar_try_wait(smem_u32(r_full + i % RING), (i / RING) & 1) && globaltimer_ns() - w0 < kTcWaitNs) {
                 }
         } else if (warp - 12 < n_rt) {
-            // ---------------- MMA issuer of row tile t: S_0, PV_0, S_1, PV_1, ... ----------------
+            // ---------------- MMA issuer of row tile t ----------------
             // The whole warp walks the loop and one elected lane issues, so addresses and descriptors are
-            // the warp's. S_{i+1} overwrites the columns of P_i: it waits until P V of step i has finished.
+            // the warp's. A step's keys go in two halves: while the softmax works on one, P V and the next
+            // step's S of the other run. S overwrites the columns of its half's P and waits for that P V.
             const int t = warp - 12;
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0) + t * 128;
             const uint64_t qd = sw128_desc(smem_u32(sm + t * MAT)), kd = sw128_desc(smem_u32(sm + Ct<HD>::OFF_K));
             const uint64_t vd = sw128_desc_mn(smem_u32(sm + Ct<HD>::OFF_V), CT_SUB);
-            bool ok = wait(q_ready + t, 0);
-            for (int i = 0; i < nt && ok; ++i) {
-                if (!wait(k_full, i) || (i && !wait(pv_done + t, i - 1))) {
-                    ok = false;
-                    break;
-                }
+            auto issue_s = [&](int i, int h) {
                 tc_fence_after();
                 if (elect_one()) {
+                    const uint64_t k0 = kd + (uint32_t)((i % NB) * (MAT >> 4) + h * (64 * 128 >> 4));
 #pragma unroll
                     for (int sub = 0; sub < NSUB; ++sub)
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            umma_f16(tm, qd + sub * (CT_SUB >> 4) + 2 * kk, kd + sub * (CT_SUB >> 4) + 2 * kk, idesc_f16(128, CT_BK),
+                            umma_f16(tm + h * 64, qd + sub * (CT_SUB >> 4) + 2 * kk, k0 + sub * (CT_SUB >> 4) + 2 * kk, idesc_f16(128, 64),
                                      (sub | kk) ? 1u : 0u);
-                    umma_commit(smem_u32(s_full + t));
-                    umma_commit(smem_u32(k_empty));
+                    umma_commit(smem_u32(s_full + 2 * t + h));
+                    if (h) umma_commit(smem_u32(k_empty + i % NB));
                 }
                 __syncwarp();
-                if (!wait(v_full, i) || !wait(p_full + t, i)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                if (elect_one()) {
+            };
+            bool ok = wait(q_ready + t, 0) && wait(k_full, 0);
+            if (ok) {
+                issue_s(0, 0);
+                issue_s(0, 1);
+            }
+            for (int i = 0; i < nt && ok; ++i) {
+                for (int h = 0; h < 2 && ok; ++h) {
+                    if ((!h && !wait(v_full + i % NB, i / NB)) || !wait(p_full + 2 * t + h, i)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint64_t v0 = vd + (uint32_t)((i % NB) * (MAT >> 4) + h * (64 * 128 >> 4));
 #pragma unroll
-                    for (int kk = 0; kk < CT_BK / 16; ++kk)
-                        umma_f16_ts(tm + CT_O, tm + kk * 8, vd + kk * (16 * 128 >> 4), idesc_f16(128, HD) | kIdescBMajorMN,
-                                    (i | kk) ? 1u : 0u);
-                    umma_commit(smem_u32(pv_done + t));
-                    umma_commit(smem_u32(v_empty));
+                        for (int kk = 0; kk < 4; ++kk)
+                            umma_f16_ts(tm + CT_O, tm + h * 64 + kk * 8, v0 + kk * (16 * 128 >> 4), idesc_f16(128, HD) | kIdescBMajorMN,
+                                        (i | h | kk) ? 1u : 0u);
+                        umma_commit(smem_u32(pv_done + t));
+                        if (h) umma_commit(smem_u32(v_empty + i % NB));
+                    }
+                    __syncwarp();
+                    if (i + 1 < nt) {
+                        ok = wait(pv_done + t, 2 * i + h) && (h || wait(k_full + (i + 1) % NB, (i + 1) / NB));
+                        if (ok) issue_s(i + 1, h);
+                    }
                 }
-                __syncwarp();
             }
             if (!ok) *abort_flag = 1;
             // the commits' asynchronous arrivals land before the CTA ends
@@ -1102,6 +1119,9 @@ __global__ void __launch_bounds__(CT_THREADS, 1) k_kv8_chunk(const __grid_consta
         int st = 0, use = 0;
         // one tile: waits for its codes and for the operand buffer, converts, hands both on
         auto take = [&](int i, uint64_t* full, uint64_t* empty, uint32_t d0, uint32_t d1, bool odd) {
+            const int buf = i % NB;
+            d0 += buf * MAT;
+            d1 += buf * MAT;
             if (!wait(r_full + st, use)) return false;
             const uint8_t* raw = sm + Ct<HD>::OFF_R + st * RAW + t * 16;
             const int left = kend - (j0 + i) * CT_BK - prow;  // > u RP: the row holds a key
@@ -1112,7 +1132,7 @@ __global__ void __launch_bounds__(CT_THREADS, 1) k_kv8_chunk(const __grid_consta
                 // rows past the keys are zeros: weight 0 must add exactly 0
                 if (left <= u * RP) r[u] = make_uint4(0u, 0u, 0u, 0u);
             }
-            if (i && !wait(empty, i - 1)) return false;
+            if (i >= NB && !wait(empty + buf, i / NB - 1)) return false;
 #pragma unroll
             for (int u = 0; u < NU; ++u) {
                 const uint32_t a = odd ? r[u].z : r[u].x, a2 = odd ? r[u].w : r[u].y, c = odd ? r[u].x : r[u].z, c2 = odd ? r[u].y : r[u].w;
@@ -1122,7 +1142,7 @@ __global__ void __launch_bounds__(CT_THREADS, 1) k_kv8_chunk(const __grid_consta
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(smem_u32(full));
+                mbar_arrive(smem_u32(full + buf));
                 mbar_arrive(smem_u32(r_empty + st));
             }
             if (++st == RING) {
@@ -1158,28 +1178,26 @@ __global__ void __launch_bounds__(CT_THREADS, 1) k_kv8_chunk(const __grid_consta
             float R = -1e30f, l = 0.f;
             bool good = true;
             const int first_masked = s + rt0 / p.G;  // steps that end at or before it need no mask
-            for (int i = 0; i < nt; ++i) {
-                const int k0 = (j0 + i) * CT_BK;
-                if (!wait(s_full + t, i)) {
+            for (int g = 0; g < 2 * nt; ++g) {  // half-steps of 64 keys
+                const int i = g >> 1, h = g & 1, k0 = (j0 + i) * CT_BK + h * 64;
+                if (!wait(s_full + 2 * t + h, i)) {
                     good = false;
                     break;
                 }
                 tc_fence_after();
-                const float4* scl = scales + (i & 7) * 8;
-                uint32_t x[CT_BK];  // the row's scores stay in registers
-                TMEM_LD32(lane_base, x);
-                TMEM_LD32(lane_base + 32, (x + 32));
-                TMEM_LD32(lane_base + 64, (x + 64));
-                TMEM_LD32(lane_base + 96, (x + 96));
+                const float4* scl = scales + (i & 7) * 8 + h * 4;
+                uint32_t x[64];  // the row's scores stay in registers
+                TMEM_LD32(lane_base + h * 64, x);
+                TMEM_LD32(lane_base + h * 64 + 32, (x + 32));
                 tmem_wait_ld();
-                if (k0 + CT_BK - 1 > first_masked) {
+                if (k0 + 63 > first_masked) {
 #pragma unroll
-                    for (int u = 0; u < CT_BK; ++u)
+                    for (int u = 0; u < 64; ++u)
                         if (k0 + u > qpos) x[u] = 0xFF800000u;
                 }
                 float mt = -INFINITY;
 #pragma unroll
-                for (int pg = 0; pg < CT_BK / 16; ++pg) {
+                for (int pg = 0; pg < 4; ++pg) {
                     const uint32_t* y = x + 16 * pg;  // three-way maxima
                     const float m0 = max3(max3(fl(y[0]), fl(y[1]), fl(y[2])), fl(y[3]), fl(y[4]));
                     const float m1 = max3(max3(fl(y[5]), fl(y[6]), fl(y[7])), fl(y[8]), fl(y[9]));
@@ -1192,7 +1210,12 @@ __global__ void __launch_bounds__(CT_THREADS, 1) k_kv8_chunk(const __grid_consta
                     const float al = move ? ex2(R - mt) : 1.f;
                     if (move) R = mt;
                     l *= al;
-                    if (i > 0) {  // P V of the step before has finished: S of this one was issued after it
+                    if (g > 0) {
+                        if (!wait(pv_done + t, g - 1)) {  // the half-step before may still be adding to O
+                            good = false;
+                            break;
+                        }
+                        tc_fence_after();
 #pragma unroll 1
                         for (int cc = 0; cc < HD / 16; ++cc) {
                             uint32_t y[16];
@@ -1204,37 +1227,35 @@ __global__ void __launch_bounds__(CT_THREADS, 1) k_kv8_chunk(const __grid_consta
                         }
                     }
                 }
+                uint32_t w[32];
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t h[32];
+                for (int pg = 0; pg < 4; ++pg) {
+                    const float4 sc = scl[pg];
+                    const uint64_t f = pack2(qmul * sc.x, qmul * sc.x);
+                    const float a0 = sc.y - R + KV8_LIFT;
+                    const uint64_t a = pack2(a0, a0);
+                    uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
-                    for (int pg = 0; pg < 4; ++pg) {
-                        const float4 sc = scl[half * 4 + pg];
-                        const uint64_t f = pack2(qmul * sc.x, qmul * sc.x);
-                        const float a0 = sc.y - R + KV8_LIFT;
-                        const uint64_t a = pack2(a0, a0);
-                        uint64_t sum[2] = {0ull, 0ull};
-#pragma unroll
-                        for (int u = 0; u < 8; ++u) {
-                            const int at = 64 * half + 16 * pg + 2 * u;
-                            float t0, t1;
-                            unpack2(fma2(pack2u(x[at], x[at + 1]), f, a), t0, t1);
-                            const float e0 = ex2(t0), e1 = ex2(t1);
-                            sum[u & 1] = add2(sum[u & 1], pack2(e0, e1));
-                            h[pg * 8 + u] = pack_h2(e0, e1);
-                        }
-                        float s0, s1;
-                        unpack2(add2(sum[0], sum[1]), s0, s1);
-                        l = fmaf(s0 + s1, sc.z, l);
+                    for (int u = 0; u < 8; ++u) {
+                        const int at = 16 * pg + 2 * u;
+                        float t0, t1;
+                        unpack2(fma2(pack2u(x[at], x[at + 1]), f, a), t0, t1);
+                        const float e0 = ex2(t0), e1 = ex2(t1);
+                        sum[u & 1] = add2(sum[u & 1], pack2(e0, e1));
+                        w[pg * 8 + u] = pack_h2(e0, e1);
                     }
-                    TMEM_ST32(lane_base + half * 32, h);
+                    float s0, s1;
+                    unpack2(add2(sum[0], sum[1]), s0, s1);
+                    l = fmaf(s0 + s1, sc.z, l);
                 }
+                TMEM_ST32(lane_base + h * 64, w);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(p_full + t));
+                if (lane == 0) mbar_arrive(smem_u32(p_full + 2 * t + h));
             }
-            if (good && wait(pv_done + t, nt - 1)) {
+            // both halves of the last step: a wait tells a phase only from the one before it
+            if (good && wait(pv_done + t, 2 * nt - 2) && wait(pv_done + t, 2 * nt - 1)) {
                 tc_fence_after();
                 const float inv = P.splits == 1 ? 1.f / l : 1.f;
                 // With the whole row at hand the output goes through the warp's rows of the Q operand (no MMA
