@@ -1383,7 +1383,14 @@ struct Cs {
     static constexpr int OFF_BAR = OFF_ACC + KEYS * 4, SMEM = 1024 + OFF_BAR + 256;
 };
 
-// One query tile of one (entry, head) into prep[(b * n_kv + head) * tiles + tile].
+// Prepared tiles lie [n_kv][T G / 128 + B]: entry b's begin at its first row / 128 + b, which leaves
+// room for every tile of the entries before it, whatever the bounds on one entry are.
+__host__ __device__ inline size_t prep_tiles(int B, int T, int G) { return (size_t)((long long)T * G / CT_ROWS) + B; }
+__device__ __forceinline__ size_t prep_at(const Kv8AttnP& p, int B, int b, int head, int r0) {
+    return head * prep_tiles(B, p.T, p.G) + (size_t)((long long)r0 * p.G / CT_ROWS) + b;
+}
+
+// One query tile of one (entry, head).
 template <int HD, int DT>
 __global__ void __launch_bounds__(128) k_kv8_score_prep(const __grid_constant__ Kv8AttnP p, uint8_t* prep) {
     pdl_wait();
@@ -1392,7 +1399,7 @@ __global__ void __launch_bounds__(128) k_kv8_score_prep(const __grid_constant__ 
     int s, r0, n;
     if (!attn_entry(p, b, s, r0, n) || tile * CT_ROWS >= n * p.G) return;
     const int rows = n * p.G, row = tile * CT_ROWS + t, tok = min(row_token(p, row), n - 1);
-    uint8_t* at = prep + (((size_t)b * p.kv.n_kv + head) * gridDim.x + tile) * Cs<HD>::PREP;
+    uint8_t* at = prep + (prep_at(p, gridDim.z, b, head, r0) + tile) * Cs<HD>::PREP;
     float* rc = reinterpret_cast<float*>(at + Cs<HD>::MAT);
     QTile<HD> qt;
     fetch_q<HD>(qt, p, r0, head, tile * CT_ROWS, rows, t >> 5, t & 31);
@@ -1404,7 +1411,7 @@ __global__ void __launch_bounds__(128) k_kv8_score_prep(const __grid_constant__ 
 }
 
 template <int HD, int DT>
-__global__ void __launch_bounds__(CS_THREADS, 2) k_kv8_score(const __grid_constant__ Kv8AttnP p, const uint8_t* prep, int tiles) {
+__global__ void __launch_bounds__(CS_THREADS, 2) k_kv8_score(const __grid_constant__ Kv8AttnP p, const uint8_t* prep) {
     constexpr int MAT = Cs<HD>::MAT, NSUB = HD / 64, CH = HD / 16, RING = Cs<HD>::RING, ROWC = Cs<HD>::ROWC;
     extern __shared__ uint8_t cs_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(cs_raw) + 1023) & ~(uintptr_t)1023);
@@ -1478,7 +1485,7 @@ __global__ void __launch_bounds__(CS_THREADS, 2) k_kv8_score(const __grid_consta
         // ---------------- copies and MMAs ----------------
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         const uint64_t kd = sw128_desc(smem_u32(sm)), qd = sw128_desc(smem_u32(sm + Cs<HD>::OFF_Q));
-        const uint8_t* src = prep + (((size_t)b * p.kv.n_kv + head) * tiles + t0) * Cs<HD>::PREP;
+        const uint8_t* src = prep + (prep_at(p, gridDim.z, b, head, r0) + t0) * Cs<HD>::PREP;
         int issued = 0;
         auto copy = [&](int i) {
             const int st = i % RING;
@@ -1604,6 +1611,8 @@ __global__ void __launch_bounds__(CS_THREADS, 2) k_kv8_score(const __grid_consta
 
 // ---- which kernels a call runs, and its workspace ---------------------------------------
 
+constexpr int KD_SMEM = 200 * 1024, KD_SMEM2 = 106 * 1024;  // k_kv8_decode's, with one and two CTAs an SM
+
 struct Plan {
     bool decode;       // k_kv8_decode (max_len * G <= 16 rows)
     bool pair_mode;
@@ -1622,8 +1631,6 @@ int sm_count() {
     return n;
 }
 
-int score_tiles(int max_len, int T, int G) { return (int)(((long long)std::min(max_len, std::max(T, 1)) * G + CT_ROWS - 1) / CT_ROWS); }
-
 // `avail`: most bytes that a decode's stored logits may take.
 Plan make_plan(int n_kv, int HD, int B, int T, int max_len, int max_keys, int n_heads, bool score, size_t avail) {
     Plan q = {};
@@ -1640,8 +1647,8 @@ Plan make_plan(int n_kv, int HD, int B, int T, int max_len, int max_keys, int n_
         q.nrow = (int)rows;
         const int slots = 2 * KD_WARPS * q.nrow * (HD + 2) * 4, ent = B * 8;
         // two CTAs an SM where their rings and slots fit (rows <= 4 at head_dim 128), else one
-        const int per_sm = KD_WARPS * 2 * BLK + slots + ent <= 106 * 1024 && rows <= 8 ? 2 : 1;
-        q.stages = std::min(8, ((per_sm == 2 ? 106 : 200) * 1024 - slots - ent) / (KD_WARPS * BLK));
+        const int per_sm = KD_WARPS * 2 * BLK + slots + ent <= KD_SMEM2 && rows <= 8 ? 2 : 1;
+        q.stages = std::min(8, ((per_sm == 2 ? KD_SMEM2 : KD_SMEM) - slots - ent) / (KD_WARPS * BLK));
         q.smem = KD_WARPS * q.stages * BLK + slots + ent;
         q.pair_mode = max_keys <= 512;
         q.n_cta = q.pair_mode ? B * n_kv : per_sm * sm_count();
@@ -1667,11 +1674,12 @@ Plan make_plan(int n_kv, int HD, int B, int T, int max_len, int max_keys, int n_
         q.off_ml = put(part * 2 * 4);
     }
     if (score && !q.tbuf)
-        q.off_prep = put((size_t)B * n_kv * score_tiles(max_len, T, G) * (CT_ROWS * HD * 2 + 3 * CT_ROWS * 4));
+        q.off_prep = put(kv8_prep_bytes(n_kv, HD, B, T, G));
     q.bytes = std::max(q.bytes, (size_t)256);
     return q;
 }
 
+// The most that any call gives the kernel, so that calls in several host threads agree.
 template <typename K>
 cudaError_t allow_smem(K kern, int bytes) {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
@@ -1681,11 +1689,11 @@ template <int HD, int DT>
 cudaError_t run_score(const Kv8AttnP& p, int B, uint8_t* prep, cudaStream_t st, int* launches) {
     LaunchCtx c = {st, true, launches};
     if (cudaError_t e = allow_smem(k_kv8_score<HD, DT>, Cs<HD>::SMEM)) return e;
-    const int rows = score_tiles(p.max_len, p.T, p.G);
+    const unsigned rows = (unsigned)(((long long)std::min(p.max_len, p.T) * p.G + CT_ROWS - 1) / CT_ROWS);
     cudaError_t e = launch_k(c, k_kv8_score_prep<HD, DT>, dim3(rows, p.kv.n_kv, B), dim3(128), 0, p, prep);
     if (e != cudaSuccess) return e;
     const unsigned tiles = (unsigned)((p.max_keys + Cs<HD>::KEYS - 1) / Cs<HD>::KEYS);
-    return launch_k(c, k_kv8_score<HD, DT>, dim3(tiles, p.kv.n_kv, B), dim3(CS_THREADS), (size_t)Cs<HD>::SMEM, p, (const uint8_t*)prep, rows);
+    return launch_k(c, k_kv8_score<HD, DT>, dim3(tiles, p.kv.n_kv, B), dim3(CS_THREADS), (size_t)Cs<HD>::SMEM, p, (const uint8_t*)prep);
 }
 
 template <int HD, int DT>
@@ -1705,13 +1713,13 @@ cudaError_t run_attn(const Kv8AttnP& p, const Plan& q, int B, char* ws, cudaStre
         P.ld_t = ((size_t)p.max_keys + 3) & ~(size_t)3;
         P.n_cta = q.n_cta;
         auto kern = q.nrow <= 8 ? k_kv8_decode<HD, DT, 1> : k_kv8_decode<HD, DT, 2>;
-        if ((e = allow_smem(kern, q.smem)) != cudaSuccess) return e;
+        if ((e = allow_smem(kern, KD_SMEM)) != cudaSuccess) return e;
         if ((e = launch_k(c, kern, dim3(q.n_cta), dim3(KD_WARPS * 32), (size_t)q.smem, P)) != cudaSuccess) return e;
         if (!q.tbuf) P.a.score_out = nullptr;
         if (!q.pair_mode || q.tbuf) {
             const unsigned chunks = q.tbuf ? (unsigned)((p.max_keys + KC_KEYS - 1) / KC_KEYS) : 1;
             const int smem = q.pair_mode ? 0 : kc_smem(q.nrow, HD);
-            if ((e = allow_smem(k_kv8_combine<HD, DT>, smem)) != cudaSuccess) return e;
+            if ((e = allow_smem(k_kv8_combine<HD, DT>, kc_smem(16, HD))) != cudaSuccess) return e;
             e = launch_k(c, k_kv8_combine<HD, DT>, dim3(B * p.kv.n_kv, chunks), dim3(KD_WARPS * 32), (size_t)smem, P);
             if (e != cudaSuccess) return e;
         }
@@ -1738,6 +1746,10 @@ cudaError_t run_attn(const Kv8AttnP& p, const Plan& q, int B, char* ws, cudaStre
 
 }  // namespace
 
+size_t kv8_prep_bytes(int n_kv, int head_dim, int B, int T, int G) {
+    return n_kv * prep_tiles(B, T, G) * (size_t)(head_dim == 128 ? Cs<128>::PREP : Cs<64>::PREP);
+}
+
 static qw_status attn_sizes(const qw_kv8* kv, int B, int T, int max_len, int max_keys, int n_heads) {
     if (qw_status s = kv8_check(kv, B, "attn")) return s;
     if (T < 0 || max_len < 1 || max_len > (1 << 26)) return qw_fail(QW_ERR_INVALID_ARG, "attn: T or max_len out of range");
@@ -1747,8 +1759,9 @@ static qw_status attn_sizes(const qw_kv8* kv, int B, int T, int max_len, int max
         return qw_fail(QW_ERR_INVALID_ARG, "attn: n_heads is not a multiple of n_kv_heads");
     if ((long long)B * ((max_keys + 15) / 16) * kv->n_kv_heads > 0x7fffffffll)
         return qw_fail(QW_ERR_UNSUPPORTED, "attn: B * max_keys * n_kv_heads too large");
-    if ((long long)std::min(max_len, T) * (n_heads / kv->n_kv_heads) >= 1ll << 28)
-        return qw_fail(QW_ERR_UNSUPPORTED, "attn: more than 2^28 query rows of one KV head");
+    // a launch has at most 65535 pairs of row tiles
+    if ((long long)std::min(max_len, T) * (n_heads / kv->n_kv_heads) > 65535ll * 2 * CT_ROWS)
+        return qw_fail(QW_ERR_UNSUPPORTED, "attn: more than 65535 * 256 query rows of one KV head and entry");
     if (n_heads / kv->n_kv_heads > 16) return qw_fail(QW_ERR_UNSUPPORTED, "attn: more than 16 query heads per KV head");
     return QW_OK;
 }

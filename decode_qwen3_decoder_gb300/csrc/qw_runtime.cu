@@ -858,8 +858,10 @@ static Kv8Layout kv8_layout(const qw_model* m, int max_seqs, bool scores) {
     L.score = put(scores ? kv8_score_floats(m, max_seqs) * 4 : 0);
     L.stage = put(align_up(c.max_tokens, 16) * 2 * c.n_kv_heads * c.head_dim * 2);
     // normalisers of every row and the partials of a call that splits its keys (fewer than 5 CTAs an
-    // SM, two tiles of 128 rows each); logits kept for the scores take what is left
-    L.ws_bytes = align_up((size_t)c.max_tokens * c.n_heads * 4, 256) + (size_t)5 * m->num_sms * 256 * (c.head_dim + 2) * 4 + 4096;
+    // SM, two tiles of 128 rows each), the query tiles that the scores read; logits kept for the scores
+    // take what is left
+    L.ws_bytes = align_up((size_t)c.max_tokens * c.n_heads * 4, 256) + (size_t)5 * m->num_sms * 256 * (c.head_dim + 2) * 4 +
+                 (scores ? kv8_prep_bytes(c.n_kv_heads, c.head_dim, c.max_batch, c.max_tokens, c.n_heads / c.n_kv_heads) : 0) + 4096;
     L.ws = put(L.ws_bytes);
     L.blocks = at;
     L.page = (size_t)c.n_layers * c.n_kv_heads * qw_kv8_block_bytes(c.head_dim);

@@ -283,6 +283,46 @@ def test_attention_with_loose_bounds(qw):
         assert c.bits() == 0
 
 
+@pytest.mark.parametrize("hd,G,dtype", [(64, 7, BF16), (128, 2, F16)])
+def test_scores_of_a_ragged_batch(qw, hd, G, dtype):
+    """Entries of many, one and no rows: each finds its own query tiles."""
+    starts, lens = [0, 50, 77, 3, 200, 16], [130, 0, 1, 257, 64, 0]
+    ends = np.add(starts, lens)
+    c = Case(qw, ends.tolist(), 2, hd, seed=31 + hd)
+    c.append([0] * len(ends), ends)
+    c.check_attn(c.attn(starts, lens, G, dtype, pad=16, score=_scores(c, ends)))
+    assert c.bits() == 0
+
+
+def test_calls_of_two_threads(qw):
+    """Decode calls of different sizes from two host threads, each on its own stream."""
+    import threading
+    cases = []
+    for seed, G, n in ((41, 1, 700), (42, 8, 900)):
+        c = Case(qw, [n, n + 31], 2, 128, seed=seed)
+        c.append([0, 0], [n, n + 31])
+        r = c.attn([n - 2, n + 29], [2, 2], G)
+        c.check_attn(r)
+        cases.append((c, r, r["out"].clone()))
+    c.torch.cuda.synchronize()
+    wrong = []
+
+    def work(c, r, want):
+        with c.torch.cuda.stream(c.torch.cuda.Stream()):
+            for _ in range(50):
+                r["out"].fill_(7.0)  # as the rows behind the last entry are
+                r["call"]()
+                if not c.torch.equal(r["out"], want):
+                    wrong.append(1)
+
+    threads = [threading.Thread(target=work, args=x) for x in cases]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong and all(x[0].bits() == 0 for x in cases)
+
+
 @pytest.mark.parametrize("lens", [[1, 1], [40, 80]])
 def test_attention_over_scales_far_apart(qw, lens):
     """Pages whose V differ by 2^30 and K rows that decide the softmax: a page of tiny values that

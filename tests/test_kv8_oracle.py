@@ -139,6 +139,18 @@ def test_attention_refuses(qw):
     assert qw.qw_kv8_attn_ws_bytes(_view(qw), 1, 1, 1, 1, 2, True) > 0
 
 
+def test_attention_row_limit_and_workspace(qw):
+    """65535 * 256 query rows of a KV head are one launch; the workspace follows the rows there are, not
+    the bound on one entry times the entries."""
+    big = _view(qw, max_pages=1 << 22, n_pages=1 << 22)
+    n = 65535 * 256 // 2
+    for T, want in ((n + 1, -7), (n, -1)):  # the second is refused for its workspace of 0 bytes only
+        assert _attn_call(qw, big, B=1, T=T, max_len=T, max_keys=T, ws_bytes=0) == want
+        assert (qw.qw_kv8_attn_ws_bytes(big, 1, T, T, T, 4, True) == 0) == (want == -7)
+    loose = qw.qw_kv8_attn_ws_bytes(big, 1024, 8192, 8192, 8192, 4, True)
+    assert loose < 1 << 30
+
+
 def test_evict_refuses(qw):
     def call(view, **kw):
         a = dict(B=2, max_len=64, len=P, keep=8, recent=2, dst=None, score=P, out=P, ld=64, kept=P, new=P + 64, status=P)
