@@ -985,14 +985,16 @@ __global__ void __launch_bounds__(CT_THREADS, 1) k_kv8_chunk(const __grid_consta
     if (warp >= 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == 14) {
-            // ---------------- copies: lane l < 8 brings page l of each step ----------------
+            // ---------------- copies: lane l brings page l % 8 of steps 4 q + l / 8 ----------------
+            // Table entries and scales come for four steps at once, ahead of their use, and the copies go out
+            // before the scales are needed.
             const int* table = kv8_row(p.kv, p.kv.table, b);
             const int key_pages = (kend + KV8_PAGE - 1) / KV8_PAGE;
             bool ok = true;
             int st = 0, use = 0, issued = 0;  // ring stage and its use count
-            auto block_of = [&](int i) -> const uint8_t* {
-                const int pi = (j0 + i) * 8 + lane;
-                if (lane >= 8 || i >= nt || pi >= key_pages) return nullptr;
+            auto block_of = [&](int q) -> const uint8_t* {
+                const int pi = j0 * 8 + q * 32 + lane;
+                if (pi >= min(key_pages, j1 * 8)) return nullptr;
                 int id = table[pi];
                 if (id < 0 || id >= p.kv.n_pages) {
                     atomicOr(p.status, QW_KV8_BAD_POS);
@@ -1004,34 +1006,40 @@ __global__ void __launch_bounds__(CT_THREADS, 1) k_kv8_chunk(const __grid_consta
             auto scale_of = [&](const uint8_t* blk) {
                 return blk ? *reinterpret_cast<const float2*>(blk + Kv8<HD>::SOFF) : make_float2(1.f, 1.f);
             };
-            auto put = [&](int i, const uint8_t* blk, bool is_v, float2 sc) {
-                if (use && !wait(r_empty + st, use - 1)) return false;
-                // [i % 8]: at most 4 steps are in the ring and 2 in the operand buffers, and S of a step follows
-                // the softmax of the step before, so the softmax of step i - 8 has passed
-                if (!is_v && lane < 8) {
-                    const int ev = kv8_log2(sc.y);
-                    scales[(i & 7) * 8 + lane] = make_float4(sc.x, (float)ev, kv8_pow2(-ev), 0.f);
-                }
-                __syncwarp();
-                const int n = min(8, key_pages - (j0 + i) * 8);  // pages of the step that hold keys
-                const uint32_t bar = smem_u32(r_full + st);
-                if (lane == 0) mbar_expect_tx(bar, n * KV8_PAGE * HD);
-                __syncwarp();
-                if (blk) bulk_copy(smem_u32(sm + Ct<HD>::OFF_R + st * RAW + lane * KV8_PAGE * HD), blk + (is_v ? Kv8<HD>::VOFF : 0), KV8_PAGE * HD, bar);
-                ++issued;
-                if (++st == RING) {
-                    st = 0;
-                    ++use;
-                }
-                return true;
-            };
-            const uint8_t* blk = block_of(0);
-            float2 sc = scale_of(blk);
+            const uint8_t *blk = block_of(0), *next = nullptr;
+            float2 sc = scale_of(blk), next_sc = make_float2(1.f, 1.f);
             for (int i = 0; i < nt && ok; ++i) {
-                const uint8_t* next = block_of(i + 1);
-                ok = put(i, blk, false, sc) && put(i, blk, true, sc);
-                blk = next;
-                sc = scale_of(blk);
+                if (i && (i & 3) == 0) {
+                    blk = next;
+                    sc = next_sc;
+                }
+                if ((i & 3) == 0) next = block_of(i / 4 + 1);
+                if ((i & 3) == 2) next_sc = scale_of(next);
+                const bool mine = lane >> 3 == (i & 3);
+                const int n = min(8, key_pages - (j0 + i) * 8);  // pages of the step that hold keys
+                for (int is_v = 0; is_v < 2; ++is_v) {
+                    if (use && !wait(r_empty + st, use - 1)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t bar = smem_u32(r_full + st);
+                    if (mine && blk)
+                        bulk_copy(smem_u32(sm + Ct<HD>::OFF_R + st * RAW + (lane & 7) * KV8_PAGE * HD), blk + (is_v ? Kv8<HD>::VOFF : 0), KV8_PAGE * HD, bar);
+                    // [i % 8]: at most 4 steps are in the ring and 2 in the operand buffers, and S of a step follows
+                    // the softmax of the step before, so the softmax of step i - 8 has passed
+                    if (!is_v && mine) {
+                        const int ev = kv8_log2(sc.y);
+                        scales[(i & 7) * 8 + (lane & 7)] = make_float4(sc.x, (float)ev, kv8_pow2(-ev), 0.f);
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_expect_tx(bar, n * KV8_PAGE * HD);  // the stage's one arrival
+                    __syncwarp();
+                    ++issued;
+                    if (++st == RING) {
+                        st = 0;
+                        ++use;
+                    }
+                }
             }
             if (!ok) *abort_flag = 1;
             // the copies issued land before the CTA ends
