@@ -763,12 +763,18 @@ __global__ void __launch_bounds__(KD_WARPS * 32) k_kv8_combine(const __grid_cons
 //   softmax        four warps a row tile, thread = row = TMEM lane, its 128 scores in registers;
 //                  the page scales enter the exponent's FMA, P (fp16) overwrites half of S;
 //   O += P V       A = P from TMEM, B = V, O in TMEM.
-// Each row tile has its own issuing warp and its own chain S -> softmax -> P V -> S; the other
-// tile's chain fills the tensor pipe meanwhile. What bounds it is that chain and the hand-overs
-// between its warps (~0.1 us each), not the pipe: so steps are as large as TMEM allows (64-key
-// steps with two CTAs an SM took 1.4x longer a key). Registers go by role (setmaxnreg). When the
-// rows give too few CTAs, the keys are split (`splits`) and k_kv8_chunk_combine adds the partials in
-// order. Every wait is bounded.
+// Each row tile has its own issuing warp, and a step's keys go in two halves of 64: while the softmax
+// works on one, P V and the next step's S of the other run (whole steps in turn took 1.13 to 1.2 times as long).
+// Registers go by role (setmaxnreg). When the rows give too few CTAs, the keys are split (`splits`)
+// and k_kv8_chunk_combine adds the partials in order. Every wait is bounded.
+//
+// What bounds it: a CTA's start and end. Of 512-token prompts (16 of them, 8 KV heads of 2, head_dim
+// 128: 48 us, 17 GFLOP and 84 MB) a CTA's 12 us are 4 until its first S (all CTAs fetch their queries
+// at the same time), 5 for its 2.5 steps, 2 for the output and 1 to the next CTA; a second query
+// buffer, which would overlap them, does not fit beside the operands. Long caches: a step of 128 keys
+// x 256 rows takes 1.7 us (head_dim 64; 102 us for 2 chunks of 400 tokens x 28 heads over 5k-9k keys,
+// 350 TFLOP/s), of which the softmax, the conversion and the MMAs each hide behind the others'
+// hand-overs (taking one out gains at most a tenth).
 // =======================================================================================
 constexpr int CT_THREADS = 512;        // warps 0-3, 4-7 softmax; 8-11 converters; 12, 13 MMA; 14 copies; 15 idle
 constexpr int CT_REGS = 128;           // a thread's at launch: 512 x 128 = 128 x (176 + 176 + 104 + 56)
@@ -797,7 +803,7 @@ __device__ __forceinline__ bool ct_wait(uint32_t bar, uint32_t parity, volatile 
 struct Kv8ChunkP {
     Kv8AttnP a;
     int splits;
-    float* part_o;   // [B * n_kv][tiles][splits][128][HD]
+    float* part_o;   // [B * n_kv][tiles][splits][HD / 4][128][4]: a warp, with a row a lane, writes whole lines
     float* part_ml;  // [B * n_kv][tiles][splits][128][2]
     int tiles;
 };
@@ -944,6 +950,11 @@ __global__ void __launch_bounds__(CT_THREADS, 1) k_kv8_chunk(const __grid_consta
         }
         return;
     }
+    // the first pages' table entries come while barriers and TMEM are set up
+    const int* table = kv8_row(p.kv, p.kv.table, b);
+    const int page_end = min((kend + KV8_PAGE - 1) / KV8_PAGE, j1 * 8);
+    int first_id = 0;
+    if (warp == 14 && j0 * 8 + lane < page_end) first_id = table[j0 * 8 + lane];
     if (threadIdx.x == 0) {
         for (int i = 0; i < RING; ++i) {
             mbar_init(smem_u32(r_full + i), 1);
@@ -988,14 +999,12 @@ __global__ void __launch_bounds__(CT_THREADS, 1) k_kv8_chunk(const __grid_consta
             // ---------------- copies: lane l brings page l % 8 of steps 4 q + l / 8 ----------------
             // Table entries and scales come for four steps at once, ahead of their use, and the copies go out
             // before the scales are needed.
-            const int* table = kv8_row(p.kv, p.kv.table, b);
-            const int key_pages = (kend + KV8_PAGE - 1) / KV8_PAGE;
             bool ok = true;
             int st = 0, use = 0, issued = 0;  // ring stage and its use count
             auto block_of = [&](int q) -> const uint8_t* {
                 const int pi = j0 * 8 + q * 32 + lane;
-                if (pi >= min(key_pages, j1 * 8)) return nullptr;
-                int id = table[pi];
+                if (pi >= page_end) return nullptr;
+                int id = q ? table[pi] : first_id;
                 if (id < 0 || id >= p.kv.n_pages) {
                     atomicOr(p.status, QW_KV8_BAD_POS);
                     id = 0;
@@ -1016,7 +1025,7 @@ __global__ void __launch_bounds__(CT_THREADS, 1) k_kv8_chunk(const __grid_consta
                 if ((i & 3) == 0) next = block_of(i / 4 + 1);
                 if ((i & 3) == 2) next_sc = scale_of(next);
                 const bool mine = lane >> 3 == (i & 3);
-                const int n = min(8, key_pages - (j0 + i) * 8);  // pages of the step that hold keys
+                const int n = min(8, page_end - (j0 + i) * 8);  // pages of the step that hold keys
                 for (int is_v = 0; is_v < 2; ++is_v) {
                     if (use && !wait(r_empty + st, use - 1)) {
                         ok = false;
@@ -1286,21 +1295,31 @@ __global__ void __launch_bounds__(CT_THREADS, 1) k_kv8_chunk(const __grid_consta
                             sts128(qa + (ch >> 3) * CT_SUB + r * 128 + (((ch & 7) ^ (r & 7)) << 4), w[0], w[1], w[2], w[3]);
                         }
                     } else if (valid) {
-                        float* dst = P.part_o + (part(t) * CT_ROWS + r) * HD + cc * 32;
+                        float* dst = P.part_o + part(t) * CT_ROWS * HD + (cc * 8 * CT_ROWS + r) * 4;
 #pragma unroll
                         for (int u = 0; u < 32; u += 4)
-                            *reinterpret_cast<uint4*>(dst + u) = make_uint4(x[u], x[u + 1], x[u + 2], x[u + 3]);
+                            *reinterpret_cast<uint4*>(dst + u * CT_ROWS) = make_uint4(x[u], x[u + 1], x[u + 2], x[u + 3]);
                     }
                     __syncwarp();
                 }
                 if (P.splits == 1) {
                     constexpr int LPR = HD / 8;
                     const int ch = lane % LPR;
-                    for (int rr = wq * 32 + lane / LPR; rr < wq * 32 + 32 && rt0 + rr < rows; rr += 32 / LPR) {
-                        const uint4 v = *reinterpret_cast<const uint4*>(sm + t * MAT + (ch >> 3) * CT_SUB + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4));
-                        const int tk = row_token(p, rt0 + rr);
-                        *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + (size_t)(r0 + tk) * p.ld_out +
-                                                  (size_t)(head * p.G + rt0 + rr - tk * p.G) * HD + ch * 8) = v;
+#pragma unroll
+                    for (int k0 = 0; k0 < LPR; k0 += 8) {  // eight rows' chunks at a time
+                        uint4 v[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const int rr = wq * 32 + (k0 + k) * (32 / LPR) + lane / LPR;
+                            v[k] = *reinterpret_cast<const uint4*>(sm + t * MAT + (ch >> 3) * CT_SUB + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4));
+                        }
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const int rr = wq * 32 + (k0 + k) * (32 / LPR) + lane / LPR, tk = row_token(p, rt0 + rr);
+                            if (rt0 + rr < rows)
+                                *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + (size_t)(r0 + tk) * p.ld_out +
+                                                          (size_t)(head * p.G + rt0 + rr - tk * p.G) * HD + ch * 8) = v[k];
+                        }
                     }
                 }
                 if (valid && P.splits == 1) {
@@ -1325,42 +1344,43 @@ __global__ void __launch_bounds__(CT_THREADS, 1) k_kv8_chunk(const __grid_consta
     }
 }
 
-// Adds a row tile's partials over the splits, in order; 8 rows a CTA, a warp a row.
+// Adds a row tile's partials over the splits, in order. A thread takes 4 dims of a row; neighbours are
+// rows, as the partials lie.
+template <int HD>
+constexpr int kCombineRows = 256 / (HD / 4);
+
 template <int HD, int DT>
 __global__ void __launch_bounds__(256) k_kv8_chunk_combine(const __grid_constant__ Kv8ChunkP P) {
     const Kv8AttnP& p = P.a;
-    const int lane = threadIdx.x & 31, b = blockIdx.z, head = blockIdx.y, row = blockIdx.x * 8 + (threadIdx.x >> 5);
+    constexpr int NR = kCombineRows<HD>;
+    const int b = blockIdx.z, head = blockIdx.y, row = blockIdx.x * NR + threadIdx.x % NR, d4 = threadIdx.x / NR;
     pdl_wait();
     pdl_launch();
     int s, r0, n;
     if (!attn_entry(p, b, s, r0, n) || row >= n * p.G) return;
     const size_t part = (((size_t)b * p.kv.n_kv + head) * P.tiles + row / CT_ROWS) * P.splits;
     float M = -1e30f, L = 0.f;
-    for (int k = 0; k < P.splits; ++k) M = fmaxf(M, P.part_ml[((part + k) * CT_ROWS + row % CT_ROWS) * 2]);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
     for (int k = 0; k < P.splits; ++k) {
-        const size_t at = (part + k) * CT_ROWS + row % CT_ROWS;
-        const float l = P.part_ml[at * 2 + 1];
-        if (l == 0.f) continue;  // that split has no partial
-        const float f = ex2(P.part_ml[at * 2] - M);
-        L += l * f;
-        if (lane < HD / 4) {
-            const float4 v = *reinterpret_cast<const float4*>(P.part_o + at * HD + lane * 4);
-            acc.x += v.x * f;
-            acc.y += v.y * f;
-            acc.z += v.z * f;
-            acc.w += v.w * f;
-        }
+        const float2 ml = *reinterpret_cast<const float2*>(P.part_ml + ((part + k) * CT_ROWS + row % CT_ROWS) * 2);
+        float4 v = *reinterpret_cast<const float4*>(P.part_o + (part + k) * CT_ROWS * HD + ((size_t)d4 * CT_ROWS + row % CT_ROWS) * 4);
+        if (ml.y == 0.f) continue;  // that split has no partial
+        const float m = fmaxf(M, ml.x), fo = ex2(M - m), fn = ex2(ml.x - m);
+        M = m;
+        L = L * fo + ml.y * fn;
+        acc.x = acc.x * fo + v.x * fn;
+        acc.y = acc.y * fo + v.y * fn;
+        acc.z = acc.z * fo + v.z * fn;
+        acc.w = acc.w * fo + v.w * fn;
     }
     const float inv = 1.f / L;
-    const int tok = r0 + row / p.G, h = head * p.G + row % p.G;
-    if (lane < HD / 4) {
-        uint2 w;
-        w.x = DT == QW_F16 ? pack_h2(acc.x * inv, acc.y * inv) : pack_bf2(acc.x * inv, acc.y * inv);
-        w.y = DT == QW_F16 ? pack_h2(acc.z * inv, acc.w * inv) : pack_bf2(acc.z * inv, acc.w * inv);
-        *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) + (size_t)tok * p.ld_out + (size_t)h * HD + lane * 4) = w;
-    }
-    if (lane == 0) {
+    const int tok = r0 + row_token(p, row), h = head * p.G + row - row_token(p, row) * p.G;
+    uint2 w;
+    w.x = DT == QW_F16 ? pack_h2(acc.x * inv, acc.y * inv) : pack_bf2(acc.x * inv, acc.y * inv);
+    w.y = DT == QW_F16 ? pack_h2(acc.z * inv, acc.w * inv) : pack_bf2(acc.z * inv, acc.w * inv);
+    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) + (size_t)tok * p.ld_out + (size_t)h * HD + d4 * 4) = w;
+    if (d4 == 0) {
         const float z = log2f(L) + M - KV8_LIFT;
         if (p.lse2) p.lse2[(size_t)tok * p.n_heads + h] = z;
         if (p.lse) p.lse[(size_t)tok * p.n_heads + h] = z * KV8_LN2;
@@ -1748,7 +1768,7 @@ cudaError_t run_attn(const Kv8AttnP& p, const Plan& q, int B, char* ws, cudaStre
     if ((e = allow_smem(k_kv8_chunk<HD, DT>, Ct<HD>::SMEM)) != cudaSuccess) return e;
     e = launch_k(c, k_kv8_chunk<HD, DT>, dim3(p.kv.n_kv, B, (q.tiles + 1) / 2 * q.splits), dim3(CT_THREADS), (size_t)Ct<HD>::SMEM, P);
     if (e == cudaSuccess && q.splits > 1)
-        e = launch_k(c, k_kv8_chunk_combine<HD, DT>, dim3(q.tiles * CT_ROWS / 8, p.kv.n_kv, B), dim3(256), 0, P);
+        e = launch_k(c, k_kv8_chunk_combine<HD, DT>, dim3(q.tiles * CT_ROWS / kCombineRows<HD>, p.kv.n_kv, B), dim3(256), 0, P);
     return e == cudaSuccess && p.score_out ? run_score<HD, DT>(p, B, (uint8_t*)ws + q.off_prep, st, launches) : e;
 }
 
