@@ -628,25 +628,27 @@ __global__ void __launch_bounds__(KD_WARPS * 32, NT == 1 ? 2 : 1) k_kv8_decode(c
     }
 }
 
-// Pairs that cross CTAs of k_kv8_decode: out = sum of the slots' partials. Warp w takes slots w0 + w,
-// + 8, ... for all rows, loading a slot's maximum, sum and values together; one exchange through
-// shared memory joins the warps. With scores also the weights of a chunk of KC_KEYS keys
-// (blockIdx.y) from the stored logits, four keys a thread.
+// Pairs that cross CTAs of k_kv8_decode: out = sum of the slots' partials. First a warp a row and a lane
+// a slot find each row's maximum and sum, then the warps add the slots' values and one exchange through
+// shared memory joins them. Few pairs deal their rows to several CTAs (blockIdx.y): one CTA with all 16
+// rows of 38 slots took 30 us. Many have one CTA each: 512 pairs of 16 rows with a CTA a row took 25 us
+// longer. With scores a pair has a CTA for each KC_KEYS keys, which also forms their weights from the
+// stored logits, four keys a thread.
 constexpr int KC_KEYS = 1024;
-inline int kc_smem(int nrow, int hd) { return KD_WARPS * nrow * (hd + 2) * 4; }
+inline int kc_smem(int nrow, int hd) { return KD_WARPS * nrow * hd * 4; }
 
 template <int HD, int DT>
 __global__ void __launch_bounds__(KD_WARPS * 32) k_kv8_combine(const __grid_constant__ Kv8DecP P) {
     const Kv8AttnP& p = P.a;
-    extern __shared__ __align__(16) float kc_o[];  // [warps][nrow][HD], then (M, L) of [warps][nrow]
+    extern __shared__ __align__(16) float kc_o[];  // [own rows][warps a row][HD]
     __shared__ int cum[QW_KV8_MAX_BATCH + 1];
     __shared__ int ws[KD_WARPS];
-    __shared__ float s_z[16];
+    __shared__ float s_m[16], s_l[16], s_z[16];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, H = p.kv.n_kv;
     const int b = blockIdx.x / H, head = blockIdx.x % H, key0 = blockIdx.y * KC_KEYS;
     pdl_launch();
     int s, r0, n;
-    const bool on = attn_entry(p, b, s, r0, n) && n > 0 && key0 < s + n;
+    const bool on = attn_entry(p, b, s, r0, n) && n > 0 && (!p.score_out || key0 < s + n);
     const int rows = n * p.G;
     bool split = false;
     int w0 = 0, w1 = 0, first = 0;
@@ -662,59 +664,72 @@ __global__ void __launch_bounds__(KD_WARPS * 32) k_kv8_combine(const __grid_cons
     }
     pdl_wait();  // in every CTA: what follows this kernel must not pass the one before it
     if (!on || (!split && !p.score_out)) return;
-    const bool merge = split && blockIdx.y == 0;
     if (split) {
-        float2* ml = reinterpret_cast<float2*>(kc_o + (size_t)KD_WARPS * P.nrow * HD);
-        for (int r = 0; r < rows; ++r) {
+        // this CTA's rows: y, y + ny, ...
+        const int y = blockIdx.y, ny = p.score_out ? (s + n + KC_KEYS - 1) / KC_KEYS : (int)gridDim.y;
+        auto slot = [&](int w) {  // of the pair in CTA w
+            return ((size_t)w * 2 + ((int)(items * w / P.n_cta) >= first ? 0 : 1)) * P.nrow;
+        };
+        for (int r = warp; r < rows; r += KD_WARPS) {
             float M = -1e30f, L = 0.f;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-            for (int w = w0 + warp; w <= w1; w += KD_WARPS) {
-                const int i0 = (int)(items * w / P.n_cta);
-                const size_t at = ((size_t)w * 2 + (i0 >= first ? 0 : 1)) * P.nrow + r;
-                const float2 x = *reinterpret_cast<const float2*>(P.part_ml + at * 2);
-                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (merge && lane < HD / 4) v = *reinterpret_cast<const float4*>(P.part_o + at * HD + lane * 4);
-                const float m = fmaxf(M, x.x), fo = ex2(M - m), fn = ex2(x.x - m);
-                L = L * fo + x.y * fn;
-                acc.x = acc.x * fo + v.x * fn;
-                acc.y = acc.y * fo + v.y * fn;
-                acc.z = acc.z * fo + v.z * fn;
-                acc.w = acc.w * fo + v.w * fn;
+            for (int w = w0 + lane; w <= w1; w += 32) {
+                const float2 x = *reinterpret_cast<const float2*>(P.part_ml + (slot(w) + r) * 2);
+                const float m = fmaxf(M, x.x);
+                L = L * ex2(M - m) + x.y * ex2(x.x - m);
                 M = m;
             }
-            if (merge && lane < HD / 4) *reinterpret_cast<float4*>(kc_o + ((size_t)warp * P.nrow + r) * HD + lane * 4) = acc;
-            if (lane == 0) ml[warp * P.nrow + r] = make_float2(M, L);
+            float m = M;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            L *= ex2(M - m);
+#pragma unroll
+            for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+            if (lane == 0) {
+                s_m[r] = m;
+                s_l[r] = L;
+                s_z[r] = log2f(L) + m - KV8_LIFT;
+            }
         }
         __syncthreads();
-        for (int x = tid; x < rows * (HD / 4); x += KD_WARPS * 32) {
-            const int r = x / (HD / 4), d = (x % (HD / 4)) * 4;
-            float M = -1e30f, L = 0.f;
-#pragma unroll
-            for (int w = 0; w < KD_WARPS; ++w) M = fmaxf(M, ml[w * P.nrow + r].x);
-            float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int w = 0; w < KD_WARPS; ++w) {
-                const float2 y = ml[w * P.nrow + r];
-                const float f = ex2(y.x - M);
-                L += y.y * f;
-                if (!merge) continue;
-                const float4 v = *reinterpret_cast<const float4*>(kc_o + ((size_t)w * P.nrow + r) * HD + d);
-                t.x += v.x * f;
-                t.y += v.y * f;
-                t.z += v.z * f;
-                t.w += v.w * f;
+        int per = 1;  // warps a row: as many as it has slots, the others take other rows
+        while (per < KD_WARPS && per <= w1 - w0) per <<= 1;
+        const int own = rows > y ? (rows - y + ny - 1) / ny : 0;
+        if (lane < HD / 4)
+            for (int k = warp / per; k < own; k += KD_WARPS / per) {
+                const int r = y + k * ny;
+                const float m = s_m[r];
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                for (int w = w0 + warp % per; w <= w1; w += per) {
+                    const size_t at = slot(w) + r;
+                    const float f = ex2(P.part_ml[at * 2] - m);
+                    const float4 v = *reinterpret_cast<const float4*>(P.part_o + at * HD + lane * 4);
+                    acc.x += v.x * f;
+                    acc.y += v.y * f;
+                    acc.z += v.z * f;
+                    acc.w += v.w * f;
+                }
+                *reinterpret_cast<float4*>(kc_o + ((size_t)k * per + warp % per) * HD + lane * 4) = acc;
             }
-            const float z = log2f(L) + M - KV8_LIFT;
-            if (d == 0) s_z[r] = z;
-            if (!merge) continue;
-            const float inv = 1.f / L;
+        __syncthreads();
+        for (int x = tid; x < own * (HD / 4); x += KD_WARPS * 32) {
+            const int k = x / (HD / 4), r = y + k * ny, d = (x - k * (HD / 4)) * 4;
+            float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int w = 0; w < per; ++w) {
+                const float4 v = *reinterpret_cast<const float4*>(kc_o + ((size_t)k * per + w) * HD + d);
+                t.x += v.x;
+                t.y += v.y;
+                t.z += v.z;
+                t.w += v.w;
+            }
+            const float inv = 1.f / s_l[r];
             const int tok = r0 + r / p.G, h = head * p.G + r % p.G;
             uint2 w;
             w.x = DT == QW_F16 ? pack_h2(t.x * inv, t.y * inv) : pack_bf2(t.x * inv, t.y * inv);
             w.y = DT == QW_F16 ? pack_h2(t.z * inv, t.w * inv) : pack_bf2(t.z * inv, t.w * inv);
             *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) + (size_t)tok * p.ld_out + (size_t)h * HD + d) = w;
-            if (d == 0 && p.lse) p.lse[(size_t)tok * p.n_heads + h] = z * KV8_LN2;
+            if (d == 0 && p.lse) p.lse[(size_t)tok * p.n_heads + h] = s_z[r] * KV8_LN2;
+            if (d == 0 && p.lse2 && !p.score_out) p.lse2[(size_t)tok * p.n_heads + h] = s_z[r];
         }
     } else if (tid < rows) {
         s_z[tid] = p.lse2[(size_t)(r0 + tid / p.G) * p.n_heads + head * p.G + tid % p.G];
@@ -1745,7 +1760,8 @@ cudaError_t run_attn(const Kv8AttnP& p, const Plan& q, int B, char* ws, cudaStre
         if ((e = launch_k(c, kern, dim3(q.n_cta), dim3(KD_WARPS * 32), (size_t)q.smem, P)) != cudaSuccess) return e;
         if (!q.tbuf) P.a.score_out = nullptr;
         if (!q.pair_mode || q.tbuf) {
-            const unsigned chunks = q.tbuf ? (unsigned)((p.max_keys + KC_KEYS - 1) / KC_KEYS) : 1;
+            const unsigned chunks = q.tbuf ? (unsigned)((p.max_keys + KC_KEYS - 1) / KC_KEYS)
+                                           : (unsigned)std::max(1, std::min(q.nrow, 2 * sm_count() / (B * p.kv.n_kv)));
             const int smem = q.pair_mode ? 0 : kc_smem(q.nrow, HD);
             if ((e = allow_smem(k_kv8_combine<HD, DT>, kc_smem(16, HD))) != cudaSuccess) return e;
             e = launch_k(c, k_kv8_combine<HD, DT>, dim3(B * p.kv.n_kv, chunks), dim3(KD_WARPS * 32), (size_t)smem, P);

@@ -294,6 +294,20 @@ def test_scores_of_a_ragged_batch(qw, hd, G, dtype):
     assert c.bits() == 0
 
 
+@pytest.mark.parametrize("n_kv,G,n,dtype,score", [(1, 16, 1, F16, True), (2, 12, 1, BF16, True), (2, 2, 6, F16, True),
+                                                  (1, 8, 1, F16, True), (3, 5, 3, BF16, False)])
+def test_few_rows_over_long_caches(qw, n_kv, G, n, dtype, score):
+    """Up to 16 rows a KV head whose keys many CTAs share, with and without scores."""
+    starts = [2900, 1500, 31]
+    c = Case(qw, [x + n for x in starts], n_kv, 128, seed=53 + G)
+    c.append([0] * 3, [x + n for x in starts])
+    r = c.attn(starts, [n] * 3, G, dtype, pad=8, score=_scores(c, [x + n for x in starts]) if score else None)
+    c.check_attn(r)
+    again = r["out"].clone()
+    r["call"]()
+    assert c.torch.equal(again, r["out"]) and c.bits() == 0
+
+
 def test_calls_of_two_threads(qw):
     """Decode calls of different sizes from two host threads, each on its own stream."""
     import threading
