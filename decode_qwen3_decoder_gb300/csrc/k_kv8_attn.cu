@@ -1665,15 +1665,6 @@ struct Plan {
     size_t off_o, off_ml, off_t, off_prep, bytes;
 };
 
-int sm_count() {
-    static const int n = [] {
-        int dev = 0, v = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) v = 0;
-        return v > 0 ? v : 152;
-    }();
-    return n;
-}
-
 // `avail`: most bytes that a decode's stored logits may take.
 Plan make_plan(int n_kv, int HD, int B, int T, int max_len, int max_keys, int n_heads, bool score, size_t avail) {
     Plan q = {};
@@ -1694,7 +1685,7 @@ Plan make_plan(int n_kv, int HD, int B, int T, int max_len, int max_keys, int n_
         q.stages = std::min(8, ((per_sm == 2 ? KD_SMEM2 : KD_SMEM) - slots - ent) / (KD_WARPS * BLK));
         q.smem = KD_WARPS * q.stages * BLK + slots + ent;
         q.pair_mode = max_keys <= 512;
-        q.n_cta = q.pair_mode ? B * n_kv : per_sm * sm_count();
+        q.n_cta = q.pair_mode ? B * n_kv : per_sm * kv8_sm_count();
         // a row's logits are written and read once (8 bytes a key) instead of its K (HD bytes)
         const size_t logits = (size_t)B * n_kv * q.nrow * (((size_t)max_keys + 3) & ~(size_t)3) * 4;
         q.tbuf = score && rows <= 8 && logits <= avail;
@@ -1706,7 +1697,7 @@ Plan make_plan(int n_kv, int HD, int B, int T, int max_len, int max_keys, int n_
         q.tiles = (int)((rows + CT_ROWS - 1) / CT_ROWS);
         // A CTA an SM. Row tiles that leave the last wave of CTAs part empty split their keys, if that
         // fills waves by a quarter better and each split keeps 512 keys.
-        const long long ctas = (long long)(q.tiles + 1) / 2 * n_kv * B, slots = sm_count();
+        const long long ctas = (long long)(q.tiles + 1) / 2 * n_kv * B, slots = kv8_sm_count();
         auto fill = [&](long long n) { return (double)n / (double)((n + slots - 1) / slots * slots); };
         q.splits = 1;
         const int most = std::min(64, max_keys / 512);
@@ -1761,7 +1752,7 @@ cudaError_t run_attn(const Kv8AttnP& p, const Plan& q, int B, char* ws, cudaStre
         if (!q.tbuf) P.a.score_out = nullptr;
         if (!q.pair_mode || q.tbuf) {
             const unsigned chunks = q.tbuf ? (unsigned)((p.max_keys + KC_KEYS - 1) / KC_KEYS)
-                                           : (unsigned)std::max(1, std::min(q.nrow, 2 * sm_count() / (B * p.kv.n_kv)));
+                                           : (unsigned)std::max(1, std::min(q.nrow, 2 * kv8_sm_count() / (B * p.kv.n_kv)));
             const int smem = q.pair_mode ? 0 : kc_smem(q.nrow, HD);
             if ((e = allow_smem(k_kv8_combine<HD, DT>, kc_smem(16, HD))) != cudaSuccess) return e;
             e = launch_k(c, k_kv8_combine<HD, DT>, dim3(B * p.kv.n_kv, chunks), dim3(KD_WARPS * 32), (size_t)smem, P);
@@ -1789,6 +1780,15 @@ cudaError_t run_attn(const Kv8AttnP& p, const Plan& q, int B, char* ws, cudaStre
 }
 
 }  // namespace
+
+int kv8_sm_count() {
+    static const int n = [] {
+        int dev = 0, v = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) v = 0;
+        return v > 0 ? v : 152;
+    }();
+    return n;
+}
 
 size_t kv8_prep_bytes(int n_kv, int head_dim, int B, int T, int G) {
     return n_kv * prep_tiles(B, T, G) * (size_t)(head_dim == 128 ? Cs<128>::PREP : Cs<64>::PREP);

@@ -8,8 +8,9 @@
 // integer counts, so ties and order are exact), then a scan writes them in ascending order. The
 // select is a chain of passes, so long entries get a cluster of C CTAs a head, which keep their
 // slices of the keys in shared memory and add each other's 256-bin histograms through distributed
-// shared memory (2048 bins, one pass less, cost 60 us a pass in remote loads).
-// k_kv8_move copies rows and scores to their new places, all of them at once.
+// shared memory (2048 bins, one pass less, cost 60 us a pass in remote loads). What bounds it is that
+// chain: 24 us for 224 heads of 4k tokens or for 64 of 1k-32k, of which the scores' bytes are 1.
+// k_kv8_move copies rows and scores to their new places, all of them at once, a warp a page.
 // k_kv8_move_inplace does it where source and destination are the same memory: new position j takes
 // the row of kept[j] >= j, so one CTA a head moves batches of ascending pages with a barrier between
 // a batch's reads and its writes. (One kernel of clusters for everything took 243 us for 28 layers of
@@ -24,8 +25,11 @@ namespace {
 constexpr int EV_T = 512, EV_W = EV_T / 32;
 constexpr int EV_BINS = 256;
 constexpr int EV_CAP = 6144;           // keys of a CTA's slice kept in shared memory; the rest is read again
-constexpr int EV_C = 8;                // CTAs of a long entry's cluster
-constexpr int EV_ONE_CTA = 6144;       // longest entry (max_len) whose positions one CTA selects
+// CTAs of a long entry's cluster: of 64 entries x heads of 1k-32k tokens 57 us with 8, 68 with 4, 209 with 1
+constexpr int EV_C = 8;
+// Longest entry (max_len) whose positions one CTA selects: 64 x 4k tokens 56 us, with a cluster 61 (28
+// layers of 8 heads: 145 and 188); 64 x 6k 48 and 45
+constexpr int EV_ONE_CTA = 6144;
 constexpr int EV_ONE_KEEP = 512;       // most kept tokens that the same CTA moves (two rounds of its warps)
 
 struct Kv8EvictP {
@@ -352,7 +356,9 @@ __global__ void __launch_bounds__(EV_T) k_kv8_evict_one(const __grid_constant__ 
 template <int HD>
 cudaError_t run_evict(const Kv8EvictP& p, int B, cudaStream_t st) {
     LaunchCtx c = {st, true, nullptr};
-    if (p.max_len <= EV_ONE_CTA && std::min(p.keep, p.max_len) <= EV_ONE_KEEP)
+    // One kernel saves a launch (1 x 200 tokens: 11.8 against 12.3 us with two; 8 x 1k -> 250: 15.9 against
+    // 18.4) while every (entry, head) has an SM to itself; 512 of them take 72 against 57 us.
+    if (p.max_len <= EV_ONE_CTA && std::min(p.keep, p.max_len) <= EV_ONE_KEEP && B * p.kv.n_kv <= kv8_sm_count())
         return launch_k(c, k_kv8_evict_one<HD>, dim3(p.kv.n_kv, B), dim3(EV_T), 0, p);
     cudaError_t e = p.max_len <= EV_ONE_CTA ? launch_k(c, k_kv8_select<1>, dim3(p.kv.n_kv, B), dim3(EV_T), 0, p)
                                             : launch_kc(c, k_kv8_select<EV_C>, dim3(EV_C * p.kv.n_kv, B), dim3(EV_T), 0, EV_C, p);

@@ -113,6 +113,7 @@ qw_status kv8_append(const Kv8View& v, int head_dim, int B, int T, int max_len, 
                      int* launches = nullptr);
 // Scores of entry b: rows (score_mul * row[b] + score_add) * n_kv .. of the score arrays.
 // ws_bytes also decides whether the logits of a decode with scores are kept.
+int kv8_sm_count();  // of the device that is current at the first call
 // Bytes of a call's query tiles laid out for the scores.
 size_t kv8_prep_bytes(int n_kv, int head_dim, int B, int T, int G);
 qw_status kv8_attn(const Kv8View& v, int head_dim, const qw_kv8_attn_args& a, int score_mul, int score_add, cudaStream_t st,
