@@ -3,7 +3,7 @@
 // Append. A page's exponent for one KV head and tensor is e = min{e : max|x| <= 448 * 2^e} over
 // its tokens and its codes are e4m3(x * 2^-e). Both follow exactly from the fp16 values, so
 // the result does not depend on any order. One warp owns the (page, head, tensor): it keeps the
-// page's 16 x HD values in registers (64 per lane at HD = 128), takes the maximum by shuffles
+// page's 16 x HD values in registers (64 per lane at HD = 128, in pairs), takes the maximum by shuffles
 // and writes the codes once. Tokens the page already holds are decoded, exact in fp32, and
 // re-coded with the larger exponent; a power of two leaves them as they are but for codes that
 // become subnormal. Bytes bound it: each input element is read once and each code written once.
@@ -36,18 +36,24 @@ __device__ __forceinline__ bool kv8_entry(const Kv8View& kv, const int* start, c
            (long long)s + n <= (long long)kv.max_pages * KV8_PAGE;
 }
 
-// 16 consecutive elements as their fp16 roundings; `bad` if one is outside the fp16 range (taken as 0).
+// Two elements as halves; one outside the fp16 range is taken as 0 and noted.
+__device__ __forceinline__ uint32_t pack_ok(float a, float b, bool& bad) {
+    const bool ba = f16_out_of_range(a), bb = f16_out_of_range(b);
+    bad |= ba || bb;
+    return pack_h2(ba ? 0.f : a, bb ? 0.f : b);
+}
+
+// 16 consecutive elements as their fp16 roundings, in pairs; `bad` if one is outside the fp16 range
+// (taken as 0).
 template <int DT>
-__device__ __forceinline__ void load16(const void* base, size_t off, float* x, bool& bad) {
+__device__ __forceinline__ void load16(const void* base, size_t off, uint32_t* x, bool& bad) {
     if (DT == QW_F32) {
         const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(base) + off);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float4 v = p[i];
-            x[4 * i] = v.x;
-            x[4 * i + 1] = v.y;
-            x[4 * i + 2] = v.z;
-            x[4 * i + 3] = v.w;
+            x[2 * i] = pack_ok(v.x, v.y, bad);
+            x[2 * i + 1] = pack_ok(v.z, v.w, bad);
         }
     } else {
         const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(base) + off);
@@ -57,16 +63,15 @@ __device__ __forceinline__ void load16(const void* base, size_t off, float* x, b
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                x[8 * i + 2 * k] = DT == QW_F16 ? h_lo(w[k]) : bf_lo(w[k]);
-                x[8 * i + 2 * k + 1] = DT == QW_F16 ? h_hi(w[k]) : bf_hi(w[k]);
+                uint32_t y = w[k];
+                if (DT == QW_BF16) {
+                    y = pack_ok(bf_lo(y), bf_hi(y), bad);
+                } else if ((y & 0x7C00u) == 0x7C00u || (y & 0x7C000000u) == 0x7C000000u) {  // infinity or NaN
+                    y = pack_ok(h_lo(y), h_hi(y), bad);
+                }
+                x[4 * i + k] = y;
             }
         }
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const bool b = f16_out_of_range(x[i]);
-        bad |= b;
-        x[i] = b ? 0.f : (DT == QW_F16 ? x[i] : __half2float(__float2half_rn(x[i])));
     }
 }
 
@@ -97,8 +102,8 @@ __global__ void __launch_bounds__(KA_WARPS * 32) k_kv8_append(const __grid_const
     const int ch = lane % CH, t0 = lane / CH;
     const int had = max(0, s - page_i * KV8_PAGE);  // tokens the page already holds
     const void* src = p.src[which];
-    float x[UPL][16];
-    float amax = 0.f;
+    uint32_t x[UPL][8];  // fp16 pairs
+    uint32_t m2 = 0u;
     bool bad = false;
 #pragma unroll
     for (int u = 0; u < UPL; ++u) {
@@ -109,34 +114,35 @@ __global__ void __launch_bounds__(KA_WARPS * 32) k_kv8_append(const __grid_const
                                        : (size_t)row * p.ld[which] + head * HD;
             load16<DT>(src, at + ch * 16, x[u], bad);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[u][i]));
+            for (int i = 0; i < 8; ++i) m2 = kv8_absmax2(m2, x[u][i]);
         } else {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[u][i] = 0.f;
+            for (int i = 0; i < 8; ++i) x[u][i] = 0u;
         }
     }
-    int e = kv8_exponent(warp_max(amax));
+    int e = kv8_exponent(warp_max(kv8_max2(m2)));
+    float so = 1.f;
     if (had) {
-        const float so = *scale;
+        so = *scale;
         e = max(e, kv8_log2(so));
-#pragma unroll
-        for (int u = 0; u < UPL; ++u) {
-            const int t = t0 + u * TSTEP;
-            if (t < had) {
-                const int at = which ? kv8_v_pos<HD>(t, ch) : kv8_k_pos<HD>(t, ch);
-                kv8_dec16(*reinterpret_cast<const uint4*>(codes + t * HD + at * 16), x[u]);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) x[u][i] *= so;
-            }
-        }
         __syncwarp();  // every lane has read the old scale
     }
     const float mul = kv8_pow2(-e);
 #pragma unroll
     for (int u = 0; u < UPL; ++u) {
         const int t = t0 + u * TSTEP;
-        const int at = which ? kv8_v_pos<HD>(t, ch) : kv8_k_pos<HD>(t, ch);
-        *reinterpret_cast<uint4*>(codes + t * HD + at * 16) = kv8_enc16(x[u], mul);
+        uint4* at = reinterpret_cast<uint4*>(codes + t * HD + (which ? kv8_v_pos<HD>(t, ch) : kv8_k_pos<HD>(t, ch)) * 16);
+        if (t < had) {
+            if (so * mul != 1.f) *at = kv8_recode16(*at, so * mul);
+        } else {
+            float f[16];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                f[2 * i] = h_lo(x[u][i]);
+                f[2 * i + 1] = h_hi(x[u][i]);
+            }
+            *at = kv8_enc16(f, mul);
+        }
     }
     if (lane == 0) *scale = kv8_pow2(e);
     if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(p.status, QW_KV8_RANGE);

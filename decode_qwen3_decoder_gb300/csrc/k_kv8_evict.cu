@@ -253,21 +253,14 @@ struct RowMove {
         for (int which = 0; which < 2; ++which) {
             float amax = 0.f;
 #pragma unroll
-            for (int u = 0; u < UPL; ++u) {
-                float x[16];
-                kv8_dec16(code[which][u], x);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]) * (which ? sc[u].y : sc[u].x));
-            }
+            for (int u = 0; u < UPL; ++u) amax = fmaxf(amax, kv8_absmax16(code[which][u]) * (which ? sc[u].y : sc[u].x));
             const int e = kv8_exponent(warp_max(amax));
             const float mul = kv8_pow2(-e);
 #pragma unroll
             for (int u = 0; u < UPL; ++u) {
                 const int t = t0 + u * TSTEP, at = which ? kv8_v_pos<HD>(t, ch) : kv8_k_pos<HD>(t, ch);
-                float x[16];
-                kv8_dec16(code[which][u], x);
                 *reinterpret_cast<uint4*>(blk + (which ? Kv8<HD>::VOFF : 0) + t * HD + at * 16) =
-                    kv8_enc16(x, (which ? sc[u].y : sc[u].x) * mul);
+                    kv8_recode16(code[which][u], (which ? sc[u].y : sc[u].x) * mul);
             }
             if (lane == 0) reinterpret_cast<float*>(blk + Kv8<HD>::SOFF)[which] = kv8_pow2(e);
         }
@@ -277,7 +270,7 @@ struct RowMove {
 constexpr int MV_W = 8;
 // blockIdx.x < row_ctas: MV_W pages of one (entry, head); above: 4 MV_W * 32 of its scores.
 template <int HD>
-__global__ void __launch_bounds__(MV_W * 32) k_kv8_move(const __grid_constant__ Kv8EvictP p, int row_ctas, bool scores) {
+__global__ void __launch_bounds__(MV_W * 32, 3) k_kv8_move(const __grid_constant__ Kv8EvictP p, int row_ctas, bool scores) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, head = blockIdx.y, b = blockIdx.z;
     const int* kept = p.kept + ((size_t)b * p.kv.n_kv + head) * p.keep;
     pdl_wait();

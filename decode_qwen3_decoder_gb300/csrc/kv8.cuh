@@ -78,6 +78,28 @@ __device__ __forceinline__ uint4 kv8_enc16(const float* x, float mul) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Largest magnitude of 16 codes (exact in fp16), and of pairs of halves.
+__device__ __forceinline__ uint32_t kv8_absmax2(uint32_t m, uint32_t x) {
+    uint32_t r;
+    asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(x & 0x7FFF7FFFu));
+    return r;
+}
+__device__ __forceinline__ float kv8_max2(uint32_t m) { return fmaxf(h_lo(m), h_hi(m)); }
+__device__ __forceinline__ float kv8_absmax16(const uint4& u) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = kv8_absmax2(kv8_absmax2(m, kv8_dec2(w[i] & 0xFFFFu)), kv8_dec2(w[i] >> 16));
+    return kv8_max2(m);
+}
+// 16 codes under a scale that is 1 / f times theirs, f a power of two.
+__device__ __forceinline__ uint4 kv8_recode16(const uint4& u, float f) {
+    if (f == 1.f) return u;
+    float x[16];
+    kv8_dec16(u, x);
+    return kv8_enc16(x, f);
+}
+
 }  // namespace
 
 // Host-side check of a view; QW_OK or the recorded error.
