@@ -223,8 +223,9 @@ __device__ __forceinline__ void softmax_page(const float* d, const float* f, con
 // =======================================================================================
 // k_kv8_decode: few query rows per KV head (a decode step, up to 16 rows of tokens x heads).
 //
-// Reading the cache bounds it: 32 HD + 32 bytes per page and head against ~150 instructions of a
-// warp. The items (entry, KV head, page), entry-major, are cut into equal runs, one per CTA and
+// Reading the cache bounds it: 32 HD + 32 bytes per page and head, once. 8 sequences of 1k-32k tokens
+// (289 MB): 53 us, 5.5 TB/s, of which ~6 are the start (lengths, page table, first pages) and ~4 the
+// merges; 64 of 1100 tokens (143 MB): 32 us. The items (entry, KV head, page), entry-major, are cut into equal runs, one per CTA and
 // again one per warp, so ragged lengths cost no imbalance and a warp needs no other warp: it
 // streams its pages through its own ring with one bulk copy per block (codes and scales are
 // contiguous), multiplies with the keys as the M of the MMA (16 keys of a page, 8 query rows as N)
@@ -232,7 +233,7 @@ __device__ __forceinline__ void softmax_page(const float* d, const float* f, con
 // the output; the pieces of a pair inside a CTA are merged in shared memory, and pairs that cross
 // CTAs go through two partial slots per CTA, merged by k_kv8_combine (launched early, in the
 // order of the slots, so sums have one order). With `pair_mode` (short caches) a CTA takes one
-// pair and nothing is left to combine.
+// pair and nothing is left to combine: 5 us for one sequence of 69 tokens, 10 without.
 // With scores, the logits also go to `tbuf`, from which the combine kernel forms the weights
 // once the normalisers are known: 8 bytes a row and key instead of K again.
 // =======================================================================================
@@ -787,9 +788,9 @@ __global__ void __launch_bounds__(KD_WARPS * 32) k_kv8_combine(const __grid_cons
 // 128: 48 us, 17 GFLOP and 84 MB) a CTA's 12 us are 4 until its first S (all CTAs fetch their queries
 // at the same time), 5 for its 2.5 steps, 2 for the output and 1 to the next CTA; a second query
 // buffer, which would overlap them, does not fit beside the operands. Long caches: a step of 128 keys
-// x 256 rows takes 1.7 us (head_dim 64; 102 us for 2 chunks of 400 tokens x 28 heads over 5k-9k keys,
-// 350 TFLOP/s), of which the softmax, the conversion and the MMAs each hide behind the others'
-// hand-overs (taking one out gains at most a tenth).
+// x 256 rows takes 1.7 us (head_dim 64; 2 chunks of 500 tokens x 28 heads over 6k-9k keys, 54 GFLOP:
+// 102 us, 530 TFLOP/s, and 12 to add the partials of 4 splits), of which the softmax, the conversion
+// and the MMAs each hide behind the others' hand-overs (taking one out gains at most a tenth).
 // =======================================================================================
 constexpr int CT_THREADS = 512;        // warps 0-3, 4-7 softmax; 8-11 converters; 12, 13 MMA; 14 copies; 15 idle
 constexpr int CT_REGS = 128;           // a thread's at launch: 512 x 128 = 128 x (176 + 176 + 104 + 56)
@@ -1412,7 +1413,10 @@ __global__ void __launch_bounds__(256) k_kv8_chunk_combine(const __grid_constant
 // equal bits. 2 HD MACs and one exponential a (row, key) pair, and the exponentials bound it: every
 // key tile needs every query tile, so k_kv8_score_prep lays these out once as swizzled operands with
 // their rows' constants, and a tile costs two bulk copies (converting them here, in every CTA, took
-// 29 us of 127 and the warps that the sums wanted). Two CTAs share an SM.
+// 29 us of 127 and the warps that the sums wanted). Two CTAs share an SM. 2 chunks of 500 tokens x 28
+// heads over 6k-9k keys (head_dim 64, 212 M pairs): 93 us and 6 to lay out, 290 TFLOP/s and 2.3 T
+// exponentials/s; at 32 a clock and SM these alone would take 23 us, the sums' other instructions and
+// TMEM reads share the warps with them.
 // =======================================================================================
 constexpr int CS_THREADS = 288;  // warps 0-7 sums, 8 copies and MMAs
 constexpr int CS_TMEM = 256;
@@ -1676,17 +1680,22 @@ Plan make_plan(int n_kv, int HD, int B, int T, int max_len, int max_keys, int n_
     };
     put(score ? (size_t)T * n_heads * 4 : 0);  // lse2
     const long long rows = (long long)std::min(max_len, std::max(T, 1)) * G;
+    // to 16 rows k_kv8_decode: 16 rows over 30k tokens of one sequence 23 us (k_kv8_chunk 31), over 64 x 1000
+    // tokens of 8 heads 55 (83), of 2 heads 26 (22); at 8 rows over 64 x 1000 tokens of 8 heads 40 (82)
     q.decode = rows <= 16;
     if (q.decode) {
         q.nrow = (int)rows;
         const int slots = 2 * KD_WARPS * q.nrow * (HD + 2) * 4, ent = B * 8;
-        // two CTAs an SM where their rings and slots fit (rows <= 4 at head_dim 128), else one
+        // two CTAs an SM where their rings and slots fit (rows <= 4 at head_dim 128), else one: 64 x 1100 tokens
+        // of 2 rows take 33 us with two and 38 with one
         const int per_sm = KD_WARPS * 2 * BLK + slots + ent <= KD_SMEM2 && rows <= 8 ? 2 : 1;
         q.stages = std::min(8, ((per_sm == 2 ? KD_SMEM2 : KD_SMEM) - slots - ent) / (KD_WARPS * BLK));
         q.smem = KD_WARPS * q.stages * BLK + slots + ent;
+        // 8 x 400 tokens 7.9 us, in runs 10.2; 64 x 400 20.0 and 19.8; 64 x 1100 33.7 and 33.3
         q.pair_mode = max_keys <= 512;
         q.n_cta = q.pair_mode ? B * n_kv : per_sm * kv8_sm_count();
-        // a row's logits are written and read once (8 bytes a key) instead of its K (HD bytes)
+        // a row's logits are written and read once (8 bytes a key) instead of its K (HD bytes): 8 x 4k tokens of
+        // 4 rows 27 us, with k_kv8_score 67
         const size_t logits = (size_t)B * n_kv * q.nrow * (((size_t)max_keys + 3) & ~(size_t)3) * 4;
         q.tbuf = score && rows <= 8 && logits <= avail;
         q.off_o = put(q.pair_mode ? 0 : (size_t)q.n_cta * 2 * q.nrow * HD * 4);
@@ -1696,7 +1705,8 @@ Plan make_plan(int n_kv, int HD, int B, int T, int max_len, int max_keys, int n_
     if (!q.decode) {
         q.tiles = (int)((rows + CT_ROWS - 1) / CT_ROWS);
         // A CTA an SM. Row tiles that leave the last wave of CTAs part empty split their keys, if that
-        // fills waves by a quarter better and each split keeps 512 keys.
+        // fills waves by a quarter better and each split keeps 512 keys: 2 chunks of 400 tokens (4 KV heads
+        // of 4, 5k-9k keys, 56 CTAs) 79 us, unsplit 150.
         const long long ctas = (long long)(q.tiles + 1) / 2 * n_kv * B, slots = kv8_sm_count();
         auto fill = [&](long long n) { return (double)n / (double)((n + slots - 1) / slots * slots); };
         q.splits = 1;

@@ -9,12 +9,15 @@
 // select is a chain of passes, so long entries get a cluster of C CTAs a head, which keep their
 // slices of the keys in shared memory and add each other's 256-bin histograms through distributed
 // shared memory (2048 bins, one pass less, cost 60 us a pass in remote loads). What bounds it is that
-// chain: 24 us for 224 heads of 4k tokens or for 64 of 1k-32k, of which the scores' bytes are 1.
-// k_kv8_move copies rows and scores to their new places, all of them at once, a warp a page.
+// chain: 15 us for 224 heads of 4k tokens, 27 for 64 of 1k-32k; their scores' bytes are 1.
+// k_kv8_move copies rows and scores to their new places, all of them at once, a warp a page: 58 us for
+// 28 layers of 4k tokens halved (235 MB of rows; rows are 128 bytes at 32-byte offsets, of which DRAM
+// reads 1.4 times the bytes: 245 MB, 4.2 TB/s). A warp for K and one for V took 70 us, more registers
+// than 80 a thread 73.
 // k_kv8_move_inplace does it where source and destination are the same memory: new position j takes
 // the row of kept[j] >= j, so one CTA a head moves batches of ascending pages with a barrier between
 // a batch's reads and its writes. (One kernel of clusters for everything took 243 us for 28 layers of
-// 4k tokens halved; the two take 80.) k_kv8_evict_one does both for short entries, where a second
+// 4k tokens halved; the two take 74.) k_kv8_evict_one does both for short entries, where a second
 // launch would cost more than it moves.
 #include "kv8.cuh"
 
