@@ -308,6 +308,72 @@ def test_few_rows_over_long_caches(qw, n_kv, G, n, dtype, score):
     assert c.torch.equal(again, r["out"]) and c.bits() == 0
 
 
+@pytest.mark.parametrize("lens", [[1, 1], [5, 3], [90, 70]])
+def test_query_rows_that_are_not_numbers_stay_alone(qw, lens):
+    """A NaN or an infinity in one query row: every other row keeps its bits."""
+    import torch
+    starts, G = [200, 410], 2
+    ends = np.add(starts, lens)
+    c = Case(qw, ends.tolist(), 2, 64, seed=61)
+    c.append([0, 0], ends)
+    r = c.attn(starts, lens, G, F16)
+    c.check_attn(r)
+    q, want = r["keep"][0], r["out"].clone()
+    T = sum(lens)
+    for row, head, x in ((0, 1, float("nan")), (T - 1, 2, float("inf"))):
+        q[row, head * 64 + 7] = x
+        r["out"].fill_(7.0)
+        r["call"]()
+        same = torch.ones(T, 4, dtype=torch.bool, device="cuda")
+        same[0, 1] = False
+        same[row, head] = False
+        got = r["out"][:T, :256].reshape(T, 4, 64)
+        assert torch.equal(got[same], want[:T, :256].reshape(T, 4, 64)[same])
+        assert bool(got[0, 1].isnan().all())
+    assert c.bits() == 0
+
+
+@pytest.mark.parametrize("lens", [[1, 1, 1], [40, 9, 100]])
+def test_entries_share_a_prefix(qw, lens):
+    """Three entries over the same first pages, each with its own last ones."""
+    own = [(300 + n + 15) // 16 * 16 for n in lens]
+    c = Case(qw, own, 2, 128, seed=67)
+    c.table[:, :18] = c.table[0, :18]
+    c.dtable.copy_(c.torch.from_numpy(c.table))
+    c.append([0, 288, 288], [288, 12, 12])       # the prefix once; positions 288 .. 299 of the other two
+    c.append([288, 300, 300], [12 + lens[0], lens[1], lens[2]])
+    r = c.attn([300] * 3, lens, 2, score=_scores(c, own))
+    c.check_attn(r)
+    assert c.bits() == 0
+
+
+@pytest.mark.parametrize("lens", [[1, 1], [100, 33]])
+def test_blocks_past_four_gib(qw, lens):
+    """The same pages at the start of a pool and behind its first 2^32 bytes give the same bits."""
+    import torch
+    ends = [500, 700]
+    starts = [e - n for e, n in zip(ends, lens)]
+    res = []
+    for far in (False, True):
+        c = Case(qw, ends, 8, 128, seed=71)
+        if far:
+            page = 8 * c.blk
+            off = 2 ** 32 // page + 3
+            big = torch.empty((off + c.n_pages) * page, dtype=torch.uint8, device="cuda")
+            big[off * page:] = c.blocks.reshape(-1)
+            c.blocks = big
+            c.dtable.copy_(torch.from_numpy(np.where(c.table >= 0, c.table + off, -1).astype(np.int32)))
+            c.view = c.qw.qw_kv8_view(big.data_ptr(), off + c.n_pages, 8, 128, c.dtable.data_ptr(), c.maxp)
+        c.append([0, 0], ends, oracle=False)
+        r = c.attn(starts, lens, 2, score=_scores(c, ends))
+        kept, new, so = _evict(c, ends, 200, 20, _scores(c, ends), True, None)
+        tail = c.blocks.reshape(-1)[-c.n_pages * 8 * c.blk:].clone()
+        res.append((r["out"], r["lse"], r["score"], torch.from_numpy(kept), torch.from_numpy(so), tail))
+        assert c.bits() == 0
+    for a, b in zip(*res):
+        assert torch.equal(a, b)
+
+
 def test_calls_of_two_threads(qw):
     """Decode calls of different sizes from two host threads, each on its own stream."""
     import threading
@@ -514,6 +580,9 @@ EVICT = [  # head_dim, n_kv, lens, keep, recent
     (128, 1, [1500, 40], 700, 0),
     (64, 2, [2100], 17, 3),
     (128, 8, [4100], 1000, 250),
+    (128, 2, [9000, 30, 6500], 1000, 250),             # a cluster a head
+    (64, 1, [50001], 3000, 100),                       # slices beyond a CTA's shared memory
+    (64, 1, [33 + i % 40 for i in range(160)], 40, 5),  # more short entries than SMs
 ]
 
 
