@@ -202,6 +202,32 @@ def test_read_returns_the_held_values(qw, hd, dtype):
     assert c.bits() == 0
 
 
+def test_read_of_bad_entries_gives_zeros(qw):
+    """A start past the table and a page outside the pool: zeros and the status bit, the rest as ever."""
+    import torch
+    c = Case(qw, [40, 40, 40], 2, 64, seed=19)
+    c.append([0, 0, 0], [40, 40, 40])
+    bad = c.table.copy()
+    bad[1, 1] = c.n_pages
+    c.dtable.copy_(torch.from_numpy(bad))
+    out = torch.full((2, 63, 128), 7.0, dtype=torch.float16, device="cuda")
+    ds, dc = c.i32([3, 0, 20]), c.i32([0, 20, 40, 60])
+    for start in (3, 10 ** 6):
+        ds[0] = start
+        c.status.zero_()
+        c.qw.qw_kv8_read(c.view, 3, 60, 20, ds.data_ptr(), dc.data_ptr(), out[0].data_ptr(), 128, out[1].data_ptr(), 128,
+                         c.qw.QW_F16, c.status.data_ptr())
+        assert c.bits() == c.qw.QW_KV8_BAD_POS
+        for w in range(2):
+            got = out[w].double().cpu().numpy().reshape(63, 2, 64)
+            want = np.concatenate([c.orc.rows(w, c.table[0], 23)[3:], c.orc.rows(w, c.table[1], 20), c.orc.rows(w, c.table[2], 40)[20:]])
+            want[36:40] = 0  # page 1 of entry 1
+            if start != 3:
+                want[:20] = 0
+            np.testing.assert_array_equal(got[:60], want)
+            assert np.all(got[60:] == 7.0)
+
+
 def test_append_flags_what_fp16_cannot_hold_and_bad_pages(qw):
     import torch
     c = Case(qw, [20, 20], 1, 128, seed=5)
@@ -617,6 +643,36 @@ def test_evict(qw, hd, n_kv, lens, keep, recent, in_place):
         np.testing.assert_array_equal(so[b, :, :n], want_s if n > keep or not in_place else sc[b, :, :n])
         np.testing.assert_array_equal(so[b, :, n:], sc[b, :, n:] if in_place else np.full_like(so[b, :, n:], -5.0))
     np.testing.assert_array_equal(new, np.minimum(lens, keep))
+    c.table = to
+    c.check_cache([min(n, keep) for n in lens])
+
+
+@pytest.mark.parametrize("rows_in_place", [False, True])
+@pytest.mark.parametrize("lens,keep,recent", [([200, 30], 64, 16), ([1500, 900], 700, 100), ([7000, 10], 600, 0)])
+def test_evict_rows_and_scores_apart(qw, lens, keep, recent, rows_in_place):
+    """Rows in place with the scores going elsewhere, and the reverse."""
+    import torch
+    c = Case(qw, lens, 2, 64, seed=83 + keep, spare=2 * ((keep + 15) // 16))
+    c.append([0, 0], lens)
+    sc = c.rng.random((2, 2, max(lens) + 5)).astype(np.float32)
+    dst = np.full_like(c.table, -1)
+    for b, n in enumerate(lens):
+        m = (min(n, keep) + 15) // 16
+        dst[b, :m] = c.free[b * ((keep + 15) // 16):][:m]
+    dsc = torch.from_numpy(sc).cuda()
+    so = torch.full_like(dsc, -5.0) if rows_in_place else dsc
+    kept = torch.full((2, 2, keep), -9, dtype=torch.int32, device="cuda")
+    new, dl, dd = c.i32([0, 0]), c.i32(lens), torch.from_numpy(dst).cuda()
+    c.qw.qw_kv8_evict(c.view, 2, max(lens), dl.data_ptr(), keep, recent, 0 if rows_in_place else dd.data_ptr(), dsc.data_ptr(),
+                      so.data_ptr(), sc.shape[2], kept.data_ptr(), new.data_ptr(), c.status.data_ptr())
+    assert c.bits() == 0 and new.tolist() == [min(n, keep) for n in lens]
+    to = c.table if rows_in_place else dst
+    got_s, kept = so.cpu().numpy(), kept.cpu().numpy()
+    for b, n in enumerate(lens):
+        own = c.table[b]
+        want_k, want_s = c.orc.evict(own, own if rows_in_place else dst[b], n, keep, recent, sc[b])
+        np.testing.assert_array_equal(kept[b], want_k)
+        np.testing.assert_array_equal(got_s[b, :, :n], want_s)
     c.table = to
     c.check_cache([min(n, keep) for n in lens])
 
