@@ -12,6 +12,7 @@
 #include "kv8.cuh"
 
 #include <algorithm>
+#include <type_traits>
 
 #include "tc_sm103.cuh"
 
@@ -1414,7 +1415,7 @@ __global__ void __launch_bounds__(256) k_kv8_chunk_combine(const __grid_constant
 // key tile needs every query tile, so k_kv8_score_prep lays these out once as swizzled operands with
 // their rows' constants, and a tile costs two bulk copies (converting them here, in every CTA, took
 // 29 us of 127 and the warps that the sums wanted). Two CTAs share an SM. 2 chunks of 500 tokens x 28
-// heads over 6k-9k keys (head_dim 64, 212 M pairs): 93 us and 6 to lay out, 290 TFLOP/s and 2.3 T
+// heads over 6k-9k keys (head_dim 64, 212 M pairs): 88 us and 6 to lay out, 310 TFLOP/s and 2.4 T
 // exponentials/s; at 32 a clock and SM these alone would take 23 us, the sums' other instructions and
 // TMEM reads share the warps with them.
 // =======================================================================================
@@ -1604,35 +1605,39 @@ __global__ void __launch_bounds__(CS_THREADS, 2) k_kv8_score(const __grid_consta
             // rows of the tile before the last key's token see not all of these keys
             const bool masked = s + rt * CT_ROWS / p.G < key0 + Cs<HD>::KEYS - 1 || (rt + 1) * CT_ROWS > rows;
             uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
+            auto tile = [&](auto with_mask) {  // with the test in the loop 5 us more
 #pragma unroll
-            for (int cc = 0; cc < 2; ++cc) {
-                uint32_t y[32];
-                TMEM_LD32(lane_base + buf * 128 + cc * 32, y);
-                tmem_wait_ld();
-                // four rows a turn: their constants are one or two 16-byte broadcasts
+                for (int cc = 0; cc < 2; ++cc) {
+                    uint32_t y[32];
+                    TMEM_LD32(lane_base + buf * 128 + cc * 32, y);
+                    tmem_wait_ld();
+                    // four rows a turn: their constants are one or two 16-byte broadcasts
 #pragma unroll
-                for (int u = 0; u < 32; u += 4) {
-                    const float4 z = *reinterpret_cast<const float4*>(rc + cc * 32 + u);
-                    uint64_t fa = f2, fb = f2;
-                    if (DT == QW_BF16) {
-                        const float4 f = *reinterpret_cast<const float4*>(rc + CT_ROWS + cc * 32 + u);
-                        fa = mul2(pack2(f.x, f.y), k2);
-                        fb = mul2(pack2(f.z, f.w), k2);
+                    for (int u = 0; u < 32; u += 4) {
+                        const float4 z = *reinterpret_cast<const float4*>(rc + cc * 32 + u);
+                        uint64_t fa = f2, fb = f2;
+                        if (DT == QW_BF16) {
+                            const float4 f = *reinterpret_cast<const float4*>(rc + CT_ROWS + cc * 32 + u);
+                            fa = mul2(pack2(f.x, f.y), k2);
+                            fb = mul2(pack2(f.z, f.w), k2);
+                        }
+                        float e0, e1, e2, e3;
+                        unpack2(fma2(pack2u(y[u], y[u + 1]), fa, pack2(z.x, z.y)), e0, e1);
+                        unpack2(fma2(pack2u(y[u + 2], y[u + 3]), fb, pack2(z.z, z.w)), e2, e3);
+                        if (decltype(with_mask)::value) {
+                            const int4 lim = *reinterpret_cast<const int4*>(rc + 2 * CT_ROWS + cc * 32 + u);
+                            e0 = key <= lim.x ? e0 : -INFINITY;
+                            e1 = key <= lim.y ? e1 : -INFINITY;
+                            e2 = key <= lim.z ? e2 : -INFINITY;
+                            e3 = key <= lim.w ? e3 : -INFINITY;
+                        }
+                        sum[(u >> 1) & 3] = add2(sum[(u >> 1) & 3], pack2(ex2(e0), ex2(e1)));
+                        sum[((u >> 1) + 1) & 3] = add2(sum[((u >> 1) + 1) & 3], pack2(ex2(e2), ex2(e3)));
                     }
-                    float e0, e1, e2, e3;
-                    unpack2(fma2(pack2u(y[u], y[u + 1]), fa, pack2(z.x, z.y)), e0, e1);
-                    unpack2(fma2(pack2u(y[u + 2], y[u + 3]), fb, pack2(z.z, z.w)), e2, e3);
-                    if (masked) {
-                        const int4 lim = *reinterpret_cast<const int4*>(rc + 2 * CT_ROWS + cc * 32 + u);
-                        e0 = key <= lim.x ? e0 : -INFINITY;
-                        e1 = key <= lim.y ? e1 : -INFINITY;
-                        e2 = key <= lim.z ? e2 : -INFINITY;
-                        e3 = key <= lim.w ? e3 : -INFINITY;
-                    }
-                    sum[(u >> 1) & 3] = add2(sum[(u >> 1) & 3], pack2(ex2(e0), ex2(e1)));
-                    sum[((u >> 1) + 1) & 3] = add2(sum[((u >> 1) + 1) & 3], pack2(ex2(e2), ex2(e3)));
                 }
-            }
+            };
+            if (masked) tile(std::true_type());
+            else tile(std::false_type());
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(s_empty + buf));
