@@ -205,7 +205,8 @@ __device__ __forceinline__ bool select_kept(const Kv8EvictP& p, int rank, int he
     for (int j = a0; j < a1; ++j) {
         const uint32_t k = key(j);
         const bool t = k == prefix;
-        if (k > prefix || (t && tb < need)) kept[gb + min(tb, need)] = k0 + j;
+        const int at = gb + min(tb, need);  // < m, unless the scores changed meanwhile
+        if ((k > prefix || (t && tb < need)) && at < m) kept[at] = k0 + j;
         gb += k > prefix;
         tb += t;
     }
