@@ -436,7 +436,9 @@ qw_status qw_kv8_read(const qw_kv8* kv, int B, int T, int max_len, const int32_t
  * dev_score_out) plus the weights that the call's queries give to j, summed over the queries
  * and the heads of the group; other elements are not written. The order of every sum is fixed:
  * equal inputs give equal bits.
- * dev_ws: at least qw_kv8_attn_ws_bytes of the same sizes, 256-byte aligned; any contents. */
+ * dev_ws: at least qw_kv8_attn_ws_bytes of the same sizes, 256-byte aligned; any contents. More than
+ * 65535 * 256 rows (tokens x heads of a KV head) of one entry, or 2^31 (entry, KV head, page)
+ * triples, give QW_ERR_UNSUPPORTED, and a workspace size of 0. */
 typedef struct {
     int B, T, max_len, max_keys, n_heads, dtype;
     const int32_t* dev_start;
