@@ -298,6 +298,12 @@ __device__ __forceinline__ int kd_find(const int* cum, int B, int pg) {
     return lo;
 }
 
+// The items are cut into `runs` equal runs, CTA w taking items [kd_start(w), kd_start(w + 1)): one run a CTA, but no
+// more runs than items, so every run has an item and its CTA writes each partial slot that the combine
+// kernel reads. CTAs past the last run get none.
+__device__ __forceinline__ int kd_runs(long long items, int n_cta) { return (int)min(items, (long long)n_cta); }
+__device__ __forceinline__ int kd_start(long long items, int runs, int w) { return (int)(w < runs ? items * w / runs : items); }
+
 __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                  "l"(src), "r"(bytes), "r"(bar)
@@ -352,8 +358,9 @@ __global__ void __launch_bounds__(KD_WARPS * 32, NT == 1 ? 2 : 1) k_kv8_decode(c
     } else {
         kd_prefix(p, P.B, cum, ws, ent);
         const long long items = (long long)cum[P.B] * H;
-        c0 = (int)(items * blockIdx.x / gridDim.x);
-        c1 = (int)(items * (blockIdx.x + 1) / gridDim.x);
+        const int runs = kd_runs(items, gridDim.x);
+        c0 = kd_start(items, runs, blockIdx.x);
+        c1 = kd_start(items, runs, blockIdx.x + 1);
     }
     if (blockIdx.x == 0 && !P.pair_mode)  // entries left out: reported, their rows zeroed
         for (int b = warp; b < P.B; b += KD_WARPS) {
@@ -653,15 +660,16 @@ __global__ void __launch_bounds__(KD_WARPS * 32) k_kv8_combine(const __grid_cons
     const bool on = attn_entry(p, b, s, r0, n) && n > 0 && (!p.score_out || key0 < s + n);
     const int rows = n * p.G;
     bool split = false;
-    int w0 = 0, w1 = 0, first = 0;
+    int w0 = 0, w1 = 0, first = 0, runs = 0;
     long long items = 0;
     if (on && !P.pair_mode) {
         kd_prefix(p, P.B, cum, ws, nullptr);
         items = (long long)cum[P.B] * H;
+        runs = kd_runs(items, P.n_cta);
         const int np = cum[b + 1] - cum[b];
         first = cum[b] * H + head * np;
-        w0 = (int)((((long long)first + 1) * P.n_cta - 1) / items);
-        w1 = (int)((((long long)first + np) * P.n_cta - 1) / items);
+        w0 = (int)((((long long)first + 1) * runs - 1) / items);
+        w1 = (int)((((long long)first + np) * runs - 1) / items);
         split = w1 > w0;
     }
     pdl_wait();  // in every CTA: what follows this kernel must not pass the one before it
@@ -670,7 +678,7 @@ __global__ void __launch_bounds__(KD_WARPS * 32) k_kv8_combine(const __grid_cons
         // this CTA's rows: y, y + ny, ...
         const int y = blockIdx.y, ny = p.score_out ? (s + n + KC_KEYS - 1) / KC_KEYS : (int)gridDim.y;
         auto slot = [&](int w) {  // of the pair in CTA w
-            return ((size_t)w * 2 + ((int)(items * w / P.n_cta) >= first ? 0 : 1)) * P.nrow;
+            return ((size_t)w * 2 + (kd_start(items, runs, w) >= first ? 0 : 1)) * P.nrow;
         };
         for (int r = warp; r < rows; r += KD_WARPS) {
             float M = -1e30f, L = 0.f;
