@@ -8,6 +8,7 @@
 // Page: "Dentro de un LLM: Inferencia en Python puro para Qwen3-0.6B en MLX".
 #include <algorithm>
 #include <array>
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -237,7 +238,15 @@ struct qw_model {
     CUtensorMap tm_h[3], tm_attn[3], tm_act[3];  // token boxes of 64, 128, 256 rows
 };
 
+// Number of a cache, never given twice: decode graphs are keyed by it, since a cache that was freed
+// leaves its host address to the next one.
+static unsigned long long next_kv_id() {
+    static std::atomic<unsigned long long> n{0};
+    return ++n;
+}
+
 struct qw_kv {
+    const unsigned long long id = next_kv_id();
     qw_model* m;
     char* pool;
     int max_seqs, n_pages, maxp;
@@ -1528,7 +1537,7 @@ static qw_status decode_graph(qw_model* m, qw_kv* kv, const StepDesc& sd, int ca
     key.push_back((long long)(uintptr_t)tokens);
     key.push_back((long long)(uintptr_t)logits);
     key.push_back((long long)(uintptr_t)next);
-    key.push_back((long long)(uintptr_t)kv);
+    key.push_back((long long)kv->id);
     key.push_back(sp.chunk);
     key.push_back(m->prof_kind);
     key.push_back(m->pdl ? 1 : 0);

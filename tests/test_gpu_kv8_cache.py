@@ -1,0 +1,66 @@
+"""Life of a model's caches: freed and bound again, emptied after an eviction, stopped on the way."""
+
+import numpy as np
+import pytest
+
+from gpu_util import LOGITS_ABS, Run, weights
+from test_gpu_kv8_model import MAXC, S, Check, _tokens, model  # noqa: F401 (a fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def eng(qw):
+    e = qw.qw.Engine(S, dict(weights(S).named()), max_tokens=256, max_batch=8, max_context=MAXC, kv_pages=200, max_seqs=8,
+                     kv_bits=8, keep_scores=True)
+    yield e
+    e.close()
+
+
+@pytest.fixture()
+def run(qw, eng):
+    qw.qw.qw_kv_reset(eng.kv, -1, eng.stream)
+    return Run(qw, eng)
+
+
+def test_caches_freed_and_bound_again(run):
+    """Caches of every kind, one after another at the same host address as a rule, decode the same batch
+    into the same buffers: none replays the kernels that another was captured with. Pools stay allocated."""
+    import torch
+    qw, eng = run.qw, run.eng
+    kinds = [("f16", False), ("8", False), ("f16", False), ("8", True), ("8", False), ("f16", False)]
+    tok, nxt = (torch.zeros(1, dtype=torch.int32, device="cuda") for _ in range(2))
+    lg = torch.zeros((1, S.vocab), device="cuda")
+    handles, pools, results = [], [], []
+    for i, (kind, scores) in enumerate(kinds):
+        n = qw.qw_kv_pool_bytes(eng.model, 6, 2) if kind == "f16" else qw.qw_kv8_pool_bytes(eng.model, 6, 2, scores)
+        pool = torch.zeros(n, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        kv = qw.qw_kv_alloc(eng.model, pool.data_ptr(), n, 2, eng.stream) if kind == "f16" else \
+            qw.qw_kv8_alloc(eng.model, pool.data_ptr(), n, 2, scores, eng.stream)
+        handles.append(kv)
+        pools.append((pool, None))
+        qw.qw_kv_reserve(kv, 0, 80, eng.stream)
+        prompt = torch.tensor(_tokens(12, 900 + i // 3), dtype=torch.int32, device="cuda")  # the last three have another prompt
+        steps = _tokens(3, 910)
+        torch.cuda.synchronize()
+        qw.qw_prefill(eng.model, kv, [0], [12], prompt.data_ptr(), 0, nxt.data_ptr(), eng.stream)
+        got = []
+        for t in steps:
+            eng.stream.synchronize()
+            tok.fill_(t)
+            torch.cuda.synchronize()
+            qw.qw_decode_step(eng.model, kv, [0], tok.data_ptr(), lg.data_ptr(), nxt.data_ptr(), eng.stream)
+            assert qw.qw_sync_status(eng.model, eng.stream) == 0
+            got.append(lg.cpu().numpy().astype(np.float64))
+        results.append(np.concatenate(got))
+        for p, before in pools[:-1]:  # nobody touched the pools of the freed caches
+            assert torch.equal(p, before)
+        qw.qw_free_kv(kv)
+        pools[-1] = (pool, pool.clone())
+    assert np.abs(results[0] - results[2]).max() <= LOGITS_ABS  # the same kind and prompt
+    np.testing.assert_array_equal(results[3], results[4])
+    # the kinds differ by the 8-bit codes only, the prompts by much more
+    assert np.abs(results[0] - results[3]).max() > 10 * LOGITS_ABS
+    assert np.abs(results[0] - results[1]).max() < np.abs(results[0] - results[3]).max() / 3
+    assert np.abs(results[5] - results[4]).max() < np.abs(results[0] - results[3]).max() / 3
