@@ -24,29 +24,29 @@ def run(qw, eng):
 
 
 def test_caches_freed_and_bound_again(run):
-    """Caches of every kind, one after another at the same host address as a rule, decode the same batch
-    into the same buffers: none replays the kernels that another was captured with. Pools stay allocated."""
+    """Caches of every kind, one after another at the same host address as a rule (each is bound right after
+    the one before is freed), decode the same batch into the same buffers: none replays the kernels that
+    another was captured with. Pools stay allocated."""
     import torch
     qw, eng = run.qw, run.eng
     kinds = [("f16", False), ("8", False), ("f16", False), ("8", True), ("8", False), ("f16", False)]
     tok, nxt = (torch.zeros(1, dtype=torch.int32, device="cuda") for _ in range(2))
     lg = torch.zeros((1, S.vocab), device="cuda")
-    handles, pools, results = [], [], []
-    for i, (kind, scores) in enumerate(kinds):
-        n = qw.qw_kv_pool_bytes(eng.model, 6, 2) if kind == "f16" else qw.qw_kv8_pool_bytes(eng.model, 6, 2, scores)
-        pool = torch.zeros(n, dtype=torch.uint8, device="cuda")
-        torch.cuda.synchronize()
-        kv = qw.qw_kv_alloc(eng.model, pool.data_ptr(), n, 2, eng.stream) if kind == "f16" else \
-            qw.qw_kv8_alloc(eng.model, pool.data_ptr(), n, 2, scores, eng.stream)
-        handles.append(kv)
-        pools.append((pool, None))
+    size = {k: qw.qw_kv_pool_bytes(eng.model, 6, 2) if k[0] == "f16" else qw.qw_kv8_pool_bytes(eng.model, 6, 2, k[1]) for k in kinds}
+    pools = [torch.zeros(size[k], dtype=torch.uint8, device="cuda") for k in kinds]
+    before, results, kv = [], [], None
+    torch.cuda.synchronize()
+    for i, k in enumerate(kinds):
+        ptr, n = pools[i].data_ptr(), size[k]
+        if kv is not None:
+            qw.qw_free_kv(kv)
+        kv = qw.qw_kv_alloc(eng.model, ptr, n, 2, eng.stream) if k[0] == "f16" else qw.qw_kv8_alloc(eng.model, ptr, n, 2, k[1], eng.stream)
         qw.qw_kv_reserve(kv, 0, 80, eng.stream)
         prompt = torch.tensor(_tokens(12, 900 + i // 3), dtype=torch.int32, device="cuda")  # the last three have another prompt
-        steps = _tokens(3, 910)
         torch.cuda.synchronize()
         qw.qw_prefill(eng.model, kv, [0], [12], prompt.data_ptr(), 0, nxt.data_ptr(), eng.stream)
         got = []
-        for t in steps:
+        for t in _tokens(3, 910):
             eng.stream.synchronize()
             tok.fill_(t)
             torch.cuda.synchronize()
@@ -54,10 +54,10 @@ def test_caches_freed_and_bound_again(run):
             assert qw.qw_sync_status(eng.model, eng.stream) == 0
             got.append(lg.cpu().numpy().astype(np.float64))
         results.append(np.concatenate(got))
-        for p, before in pools[:-1]:  # nobody touched the pools of the freed caches
-            assert torch.equal(p, before)
-        qw.qw_free_kv(kv)
-        pools[-1] = (pool, pool.clone())
+        for p, was in zip(pools, before):  # nobody touched the pools of the freed caches
+            assert torch.equal(p, was)
+        before.append(pools[i].clone())
+    qw.qw_free_kv(kv)
     assert np.abs(results[0] - results[2]).max() <= LOGITS_ABS  # the same kind and prompt
     np.testing.assert_array_equal(results[3], results[4])
     # the kinds differ by the 8-bit codes only, the prompts by much more
