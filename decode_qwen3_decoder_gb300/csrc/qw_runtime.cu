@@ -1013,6 +1013,10 @@ extern "C" qw_status qw_kv_truncate(qw_kv* kv, int seq, int n_tokens, void* stre
         return fail(QW_ERR_INVALID_ARG, "n_tokens %d outside [0, length %d]", n_tokens, kv->len[seq]);
     const int n = n_tokens;
     CUDA_TRY(cudaMemcpyAsync(kv->d_len + seq, &n, 4, cudaMemcpyHostToDevice, (cudaStream_t)stream_));
+    if (kv->b8 && n == 0 && kv->shift[seq]) {  // nothing left that a position could follow
+        CUDA_TRY(cudaMemsetAsync(kv->d_shift + seq, 0, 4, (cudaStream_t)stream_));
+        kv->shift[seq] = 0;
+    }
     if (kv->b8 && kv->score && n < kv->len[seq]) {  // dropped positions start again without weight
         const size_t rows = (size_t)kv->m->cfg.n_layers * kv->m->cfg.n_kv_heads;
         CUDA_TRY(cudaMemset2DAsync(kv->score + (size_t)seq * rows * kv->ld_score + n, kv->ld_score * 4, 0, (size_t)(kv->len[seq] - n) * 4,

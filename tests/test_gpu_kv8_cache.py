@@ -64,3 +64,28 @@ def test_caches_freed_and_bound_again(run):
     assert np.abs(results[0] - results[3]).max() > 10 * LOGITS_ABS
     assert np.abs(results[0] - results[1]).max() < np.abs(results[0] - results[3]).max() / 3
     assert np.abs(results[5] - results[4]).max() < np.abs(results[0] - results[3]).max() / 3
+
+
+def test_a_sequence_emptied_after_an_eviction_starts_again(run, model):  # noqa: F811
+    """Truncated to nothing it begins at position 0 with the whole context ahead of it."""
+    qw, eng = run.qw, run.eng
+    qw.qw_kv_reserve(eng.kv, 2, MAXC, eng.stream)
+    run.prefill([2], [_tokens(250, 1)], debug=False, reserve=False)
+    qw.qw_kv_evict(eng.kv, 2, 60, 10, eng.stream)
+    qw.qw_kv_truncate(eng.kv, 2, 0, eng.stream)
+    c = Check(run, model)
+    prompt = _tokens(20, 2)
+    g = run.prefill([2], [prompt], reserve=False)
+    c.after([2], [prompt], g)
+    step = g["next"].tolist()
+    c.after([2], [step], run.decode([2], step))
+    for n in (250, MAXC - 21 - 250):  # up to the last position
+        run.prefill([2], [_tokens(n, 3)], debug=False, reserve=False)
+    assert qw.qw_kv_length(eng.kv, 2) == MAXC
+    # generation into it: the prompt and the steps fill the context
+    qw.qw_kv_evict(eng.kv, 2, 30, 10, eng.stream)
+    qw.qw_kv_truncate(eng.kv, 2, 0, eng.stream)
+    out = np.zeros((1, 13), np.int32)
+    half = _tokens(250, 4)
+    qw.qw_generate(eng.model, eng.kv, [2], [250], np.asarray(half, np.int32), 12, out, eng.stream)
+    assert qw.qw_sync_status(eng.model, eng.stream) == 0 and qw.qw_kv_length(eng.kv, 2) == 262
