@@ -744,7 +744,7 @@ __global__ void __launch_bounds__(KD_WARPS * 32) k_kv8_combine(const __grid_cons
     } else if (tid < rows) {
         s_z[tid] = p.lse2[(size_t)(r0 + tid / p.G) * p.n_heads + head * p.G + tid % p.G];
     }
-    if (!p.score_out) return;
+    if (!p.score_out || kv8_stopped(p.kv, b)) return;
     const size_t base = score_row(p, b, head);
     const int j = key0 + tid * 4, end = s + n;
     float in[4] = {0.f, 0.f, 0.f, 0.f};
@@ -1480,7 +1480,7 @@ __global__ void __launch_bounds__(CS_THREADS, 2) k_kv8_score(const __grid_consta
     pdl_wait();
     pdl_launch();
     int s, r0, n;
-    if (!attn_entry(p, b, s, r0, n) || n == 0 || key0 >= s + n) return;
+    if (!attn_entry(p, b, s, r0, n) || n == 0 || key0 >= s + n || kv8_stopped(p.kv, b)) return;
     const int rows = n * p.G, kend = s + n;
     const int t0 = max(0, key0 - s) * p.G / CT_ROWS, t1 = (rows + CT_ROWS - 1) / CT_ROWS, nt = t1 - t0;  // row tiles that see a key of these
     auto wait = [&](uint64_t* bar, int parity) {

@@ -88,6 +88,7 @@ __global__ void __launch_bounds__(256) k_step_begin(StepDesc sd, const int32_t* 
                 kv.e_cu[b] = t;
             }
             if (t == sd.T - 1) kv.e_cu[sd.B] = sd.T;
+            if (kv.stopped && id == kv.eos) kv.stopped[seq] = 1;
         }
         if (t == sd.start[b + 1] - 1) tv.last[b] = t;
         if (bad) atomicOr(status, QW_DEV_BAD_TOKEN);

@@ -115,14 +115,16 @@ struct Kv8View {
     const int* row;   // optional [B]: the table row of entry b
     int row_stride;   // ints between rows
     int page_step;    // added to the page ids of entry b, b times
+    const int* stopped = nullptr;  // optional, by table row: non-zero leaves the row's scores as they are
 };
 inline Kv8View kv8_view(const qw_kv8* kv) {
-    return {(uint8_t*)kv->dev_blocks, kv->dev_page_table, kv->n_pages, kv->max_pages, kv->n_kv_heads, nullptr, kv->max_pages, 0};
+    return {(uint8_t*)kv->dev_blocks, kv->dev_page_table, kv->n_pages, kv->max_pages, kv->n_kv_heads, nullptr, kv->max_pages, 0, nullptr};
 }
 #ifdef __CUDACC__
 __device__ __forceinline__ const int* kv8_row(const Kv8View& v, const int* table, int b) {
     return table + (size_t)(v.row ? v.row[b] : b) * v.row_stride;
 }
+__device__ __forceinline__ bool kv8_stopped(const Kv8View& v, int b) { return v.stopped && v.stopped[v.row ? v.row[b] : b]; }
 __device__ __forceinline__ uint8_t* kv8_block(const Kv8View& v, int b, int page, int head, int blk) {
     return v.blocks + ((size_t)(page + b * v.page_step) * v.n_kv + head) * blk;
 }

@@ -42,6 +42,8 @@ struct KVView {
     int staged;
     const int* shift;       // optional [max_seqs]: tokens evicted from a sequence (its positions run on)
     int *e_seq, *e_start, *e_cu;  // staged: the step's entries, written by its first kernel ([B], [B], [B + 1])
+    int* stopped;           // optional [max_seqs]: set once a sequence is fed `eos`; its queries' weights no longer count
+    int eos;
 };
 
 // Per-token bookkeeping written by the step-begin kernel.

@@ -267,6 +267,8 @@ struct qw_kv {
     std::vector<int> shift;
     float* score;          // optional [max_seqs][n_layers][n_kv][ld_score]
     size_t ld_score;
+    int* stopped;          // with scores: [max_seqs] flags of qw_generate_eos, in use while eos >= 0
+    int eos = -1;
     int *kept, *new_len;   // eviction: [n_layers][n_kv][max_context], [n_layers]
     char* ws8;             // attention workspace
     size_t ws8_bytes;
@@ -279,6 +281,8 @@ struct qw_kv {
             v_.e_seq = e_seq;
             v_.e_start = e_start;
             v_.e_cu = e_cu;
+            v_.stopped = eos >= 0 ? stopped : nullptr;
+            v_.eos = eos;
         }
         v_.len = d_len;
         v_.page_table = d_pt;
@@ -836,14 +840,14 @@ extern "C" qw_status qw_kv_alloc(qw_model* m, void* dev_pool, size_t pool_bytes,
 }
 
 // ---- 8-bit cache ----
-// Pool: lengths, page tables, shifts, the step's entries, eviction results, scores, staging rows,
+// Pool: lengths, page tables, shifts, stop flags, the step's entries, eviction results, scores, staging rows,
 // the attention workspace, then the blocks.
 static size_t kv8_score_floats(const qw_model* m, int max_seqs) {
     return (size_t)max_seqs * m->cfg.n_layers * m->cfg.n_kv_heads * align_up(m->cfg.max_context, 4);
 }
 
 struct Kv8Layout {
-    size_t len, pt, shift, e_seq, e_start, e_cu, kept, new_len, score, stage, ws, ws_bytes, blocks, page;
+    size_t len, pt, shift, stopped, e_seq, e_start, e_cu, kept, new_len, score, stage, ws, ws_bytes, blocks, page;
 };
 
 static Kv8Layout kv8_layout(const qw_model* m, int max_seqs, bool scores) {
@@ -859,6 +863,7 @@ static Kv8Layout kv8_layout(const qw_model* m, int max_seqs, bool scores) {
     L.len = put((size_t)max_seqs * 4);
     L.pt = put((size_t)max_seqs * maxp * 4);
     L.shift = put((size_t)max_seqs * 4);
+    L.stopped = put(scores ? (size_t)max_seqs * 4 : 0);
     L.e_seq = put((size_t)c.max_batch * 4);
     L.e_start = put((size_t)c.max_batch * 4);
     L.e_cu = put((size_t)(c.max_batch + 1) * 4);
@@ -907,6 +912,7 @@ extern "C" qw_status qw_kv8_alloc(qw_model* m, void* dev_pool, size_t pool_bytes
     kv->e_seq = (int*)(kv->pool + L.e_seq);
     kv->e_start = (int*)(kv->pool + L.e_start);
     kv->e_cu = (int*)(kv->pool + L.e_cu);
+    kv->stopped = keep_scores ? (int*)(kv->pool + L.stopped) : nullptr;
     kv->kept = keep_scores ? (int*)(kv->pool + L.kept) : nullptr;
     kv->new_len = (int*)(kv->pool + L.new_len);
     kv->score = keep_scores ? (float*)(kv->pool + L.score) : nullptr;
@@ -1218,7 +1224,7 @@ static qw_status run_layers(qw_model* m, qw_kv* kv, const StepDesc& sd, bool pre
             PROF(QW_PROF_ATTN);
             int max_len = 1;
             for (int b = 0; b < sd.B; ++b) max_len = std::max(max_len, sd.start[b + 1] - sd.start[b]);
-            const Kv8View v8 = {kv->blocks + l * kv->layer_bytes, kv->d_pt, kv->n_pages, kv->maxp, c.n_kv_heads, kv->e_seq, kv->maxp, 0};
+            const Kv8View v8 = {kv->blocks + l * kv->layer_bytes, kv->d_pt, kv->n_pages, kv->maxp, c.n_kv_heads, kv->e_seq, kv->maxp, 0, kvv.stopped};
             QW_TRY(kv8_append(v8, d, sd.B, T, max_len, kv->e_start, kv->e_cu, kv->k, 0, kv->v, 0, QW_F16, true, m->status, st, launches));
             qw_kv8_attn_args a = {};
             a.B = sd.B; a.T = T; a.max_len = max_len; a.max_keys = max_keys; a.n_heads = c.n_heads; a.dtype = QW_F16;
@@ -1542,6 +1548,7 @@ static qw_status decode_graph(qw_model* m, qw_kv* kv, const StepDesc& sd, int ca
     key.push_back((long long)(uintptr_t)logits);
     key.push_back((long long)(uintptr_t)next);
     key.push_back((long long)kv->id);
+    key.push_back(kv->eos);
     key.push_back(sp.chunk);
     key.push_back(m->prof_kind);
     key.push_back(m->pdl ? 1 : 0);
@@ -1682,6 +1689,16 @@ static qw_status generate_impl(qw_model* m, qw_kv* kv, int B, const int* seq_ids
         return QW_OK;
     };
     if (eos_id >= 0) QW_TRY(look(0));
+    // A stopped sequence's further queries give no weight to the positions that it keeps: the first of
+    // them feeds the EOS, which the steps' kernels see.
+    struct StopFlags {
+        qw_kv* kv;
+        ~StopFlags() { kv->eos = -1; }
+    } flags = {kv};
+    if (eos_id >= 0 && kv->b8 && kv->score) {
+        CUDA_TRY(cudaMemsetAsync(kv->stopped, 0, (size_t)kv->max_seqs * 4, st));
+        kv->eos = eos_id;
+    }
     // picks i = 1 .. n_decode: each chunk of steps is one graph that feeds row i - 1 of gen_out
     // and writes row i (chunks of kEosCheck steps with an EOS, so the host can stop early; for
     // more than 8 sequences, whose steps are hundreds of launches each, chunks of kEosCheck too,

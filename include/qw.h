@@ -485,7 +485,9 @@ qw_status qw_kv8_evict(const qw_kv8* kv, int B, int max_len, const int32_t* dev_
  * QW_ERR_UNSUPPORTED, qw_kv_pool_ptrs the blocks ([n_layers][n_pages][n_kv_heads]) as dev_k and a
  * NULL dev_v, and the slots of qw_debug_set are the staging rows (the token's index in the call).
  * keep_scores: the pool also holds, for every layer and KV head, the weight that each cached token
- * has been given by all queries since it was appended (dropped positions start again at 0). */
+ * has been given by all queries since it was appended (dropped positions start again at 0; the
+ * queries of tokens that qw_kv_truncate dropped have counted, those of the steps that
+ * qw_generate_eos takes past a sequence's stop have not). */
 size_t qw_kv8_pool_bytes(const qw_model* m, int n_pages, int max_seqs, int keep_scores);
 qw_status qw_kv8_alloc(qw_model* m, void* dev_pool, size_t pool_bytes, int max_seqs, int keep_scores, void* stream, qw_kv** out);
 

@@ -89,3 +89,77 @@ def test_a_sequence_emptied_after_an_eviction_starts_again(run, model):  # noqa:
     half = _tokens(250, 4)
     qw.qw_generate(eng.model, eng.kv, [2], [250], np.asarray(half, np.int32), 12, out, eng.stream)
     assert qw.qw_sync_status(eng.model, eng.stream) == 0 and qw.qw_kv_length(eng.kv, 2) == 262
+
+
+@pytest.mark.parametrize("n", [3, 5])
+def test_a_stopped_sequence_gives_no_more_weight(run, n):
+    """After its EOS a sequence steps on with the batch; what its dropped tokens would have looked at is
+    not counted: each of its tokens has spread a weight of one for each head of the group."""
+    qw, eng, steps = run.qw, run.eng, 20
+    seqs, lens = list(range(n)), [6 + 5 * i for i in range(n)]
+    prompt = np.concatenate([np.asarray(_tokens(k, 400 + k), np.int32) for k in lens])
+
+    def reset():
+        qw.qw_kv_reset(eng.kv, -1, eng.stream)
+        for s, k in zip(seqs, lens):
+            qw.qw_kv_reserve(eng.kv, s, k + steps, eng.stream)
+    reset()
+    out = np.zeros((n, steps + 1), np.int32)
+    qw.qw_generate(eng.model, eng.kv, seqs, lens, prompt, steps, out, eng.stream)
+    c = Check(run, None)
+    for b in range(n):
+        np.testing.assert_allclose(c.scores(b).sum(-1), (lens[b] + steps) * S.n_heads / S.n_kv_heads, rtol=1e-5)
+    stopped = set()
+    for eos in (int(out[1, 4]), int(out[0, 11]), int(out[2, 0])):
+        reset()
+        cut, cnt = np.zeros((n, steps + 1), np.int32), np.zeros(n, np.int32)
+        qw.qw_generate_eos(eng.model, eng.kv, seqs, lens, prompt, steps, eos, cut, cnt, eng.stream)
+        for b in range(n):
+            length = qw.qw_kv_length(eng.kv, b)
+            sc = c.scores(b)
+            stopped |= {b} if cnt[b] <= steps else set()
+            np.testing.assert_allclose(sc.sum(-1), length * S.n_heads / S.n_kv_heads, rtol=1e-5)
+            assert np.all(sc[..., length:] == 0)
+    assert {0, 1, 2} <= stopped
+    # the sequences go on afterwards, their weights with them
+    more = [_tokens(3, 700 + b) for b in range(n)]
+    before = [qw.qw_kv_length(eng.kv, b) for b in range(n)]
+    for b in range(n):
+        qw.qw_kv_reserve(eng.kv, b, before[b] + 6, eng.stream)
+    g = run.prefill(seqs, more, debug=False, reserve=False)
+    run.decode(seqs, g["next"].tolist(), debug=False)
+    for b in range(n):
+        np.testing.assert_allclose(c.scores(b).sum(-1), (before[b] + 4) * S.n_heads / S.n_kv_heads, rtol=1e-5)
+
+
+def test_stopped_sequences_under_a_large_reservation(qw):
+    """As above where the logits of a step's bound no longer fit the workspace and the scores' own kernels run."""
+    B, steps = 24, 10
+    e = qw.qw.Engine(S, dict(weights(S).named()), max_tokens=256, max_batch=B, max_context=90000, kv_pages=5700, max_seqs=B,
+                     kv_bits=8, keep_scores=True)
+    try:
+        q, c = qw.qw, Check(Run(qw, e), None)
+        seqs, lens = list(range(B)), [5 + b % 4 for b in range(B)]
+        prompt = np.concatenate([np.asarray(_tokens(k, 500 + b), np.int32) for b, k in enumerate(lens)])
+        eos = -1
+        for _ in range(2):
+            q.qw_kv_reset(e.kv, -1, e.stream)
+            for s, k in zip(seqs, lens):
+                q.qw_kv_reserve(e.kv, s, 88000 if s == 5 else k + steps, e.stream)
+            out, cnt = np.zeros((B, steps + 1), np.int32), np.zeros(B, np.int32)
+            if eos < 0:
+                q.qw_generate(e.model, e.kv, seqs, lens, prompt, steps, out, e.stream)
+                eos = int(out[7, 2])
+            else:
+                q.qw_generate_eos(e.model, e.kv, seqs, lens, prompt, steps, eos, out, cnt, e.stream)
+                assert cnt[7] <= 3
+            assert q.qw_sync_status(e.model, e.stream) == 0
+            ptr, ld = q.qw_kv8_scores(e.kv)
+            off = ptr - e.pool.data_ptr()
+            sc = e.pool[off:off + 4 * B * S.n_layers * S.n_kv_heads * ld].view(c.run.torch.float32).view(B, S.n_layers * S.n_kv_heads, ld)
+            for b in range(B):
+                n = q.qw_kv_length(e.kv, b)
+                np.testing.assert_allclose(sc[b].sum(-1).cpu().numpy(), n * S.n_heads / S.n_kv_heads, rtol=1e-5)
+                assert not bool(sc[b, :, n:].any())
+    finally:
+        e.close()
