@@ -310,12 +310,22 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_
                  : "memory");
 }
 
+// Two output elements. A value next to 65504 is held as 65536 (see kv8.cuh), so fp16 outputs stop at 65504 as
+// values read back do; NaN stays NaN.
+template <int DT>
+__device__ __forceinline__ uint32_t pack_out(float lo, float hi) {
+    if (DT == QW_BF16) return pack_bf2(lo, hi);
+    uint32_t r;
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 // 2 N consecutive output elements of one row from fp32 (N words, 16-byte aligned).
 template <int DT, int N>
 __device__ __forceinline__ void store_row(void* base, size_t off, const float* x) {
     uint32_t w[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) w[i] = DT == QW_F16 ? pack_h2(x[2 * i], x[2 * i + 1]) : pack_bf2(x[2 * i], x[2 * i + 1]);
+    for (int i = 0; i < N; ++i) w[i] = pack_out<DT>(x[2 * i], x[2 * i + 1]);
 #pragma unroll
     for (int i = 0; i < N; i += 4)
         *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(base) + off + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
@@ -618,8 +628,8 @@ __global__ void __launch_bounds__(KD_WARPS * 32, NT == 1 ? 2 : 1) k_kv8_decode(c
             const float inv = 1.f / L;
             const int i = row_token(p, r), tok = er0 + i, h = eh * p.G + r - i * p.G;
             uint2 w;
-            w.x = DT == QW_F16 ? pack_h2(acc.x * inv, acc.y * inv) : pack_bf2(acc.x * inv, acc.y * inv);
-            w.y = DT == QW_F16 ? pack_h2(acc.z * inv, acc.w * inv) : pack_bf2(acc.z * inv, acc.w * inv);
+            w.x = pack_out<DT>(acc.x * inv, acc.y * inv);
+            w.y = pack_out<DT>(acc.z * inv, acc.w * inv);
             *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) + (size_t)tok * p.ld_out + (size_t)h * HD + d) = w;
             if (d == 0) {
                 const float z = log2f(L) + M - KV8_LIFT;
@@ -735,8 +745,8 @@ __global__ void __launch_bounds__(KD_WARPS * 32) k_kv8_combine(const __grid_cons
             const float inv = 1.f / s_l[r];
             const int tok = r0 + r / p.G, h = head * p.G + r % p.G;
             uint2 w;
-            w.x = DT == QW_F16 ? pack_h2(t.x * inv, t.y * inv) : pack_bf2(t.x * inv, t.y * inv);
-            w.y = DT == QW_F16 ? pack_h2(t.z * inv, t.w * inv) : pack_bf2(t.z * inv, t.w * inv);
+            w.x = pack_out<DT>(t.x * inv, t.y * inv);
+            w.y = pack_out<DT>(t.z * inv, t.w * inv);
             *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) + (size_t)tok * p.ld_out + (size_t)h * HD + d) = w;
             if (d == 0 && p.lse) p.lse[(size_t)tok * p.n_heads + h] = s_z[r] * KV8_LN2;
             if (d == 0 && p.lse2 && !p.score_out) p.lse2[(size_t)tok * p.n_heads + h] = s_z[r];
@@ -1314,7 +1324,7 @@ __global__ void __launch_bounds__(CT_THREADS, 1) k_kv8_chunk(const __grid_consta
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
                                 const float e0 = fl(x[8 * u + 2 * k]) * inv, e1 = fl(x[8 * u + 2 * k + 1]) * inv;
-                                w[k] = DT == QW_F16 ? pack_h2(e0, e1) : pack_bf2(e0, e1);
+                                w[k] = pack_out<DT>(e0, e1);
                             }
                             const int ch = cc * 4 + u;
                             sts128(qa + (ch >> 3) * CT_SUB + r * 128 + (((ch & 7) ^ (r & 7)) << 4), w[0], w[1], w[2], w[3]);
@@ -1402,8 +1412,8 @@ __global__ void __launch_bounds__(256) k_kv8_chunk_combine(const __grid_constant
     const float inv = 1.f / L;
     const int tok = r0 + row_token(p, row), h = head * p.G + row - row_token(p, row) * p.G;
     uint2 w;
-    w.x = DT == QW_F16 ? pack_h2(acc.x * inv, acc.y * inv) : pack_bf2(acc.x * inv, acc.y * inv);
-    w.y = DT == QW_F16 ? pack_h2(acc.z * inv, acc.w * inv) : pack_bf2(acc.z * inv, acc.w * inv);
+    w.x = pack_out<DT>(acc.x * inv, acc.y * inv);
+    w.y = pack_out<DT>(acc.z * inv, acc.w * inv);
     *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) + (size_t)tok * p.ld_out + (size_t)h * HD + d4 * 4) = w;
     if (d4 == 0) {
         const float z = log2f(L) + M - KV8_LIFT;

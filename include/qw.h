@@ -428,9 +428,9 @@ qw_status qw_kv8_read(const qw_kv8* kv, int B, int T, int max_len, const int32_t
 /* Attention of T query rows ([T][n_heads * head_dim], QW_F16 or QW_BF16) over the cache: the
  * query at position p of its entry sees the cached positions 0 .. p (its own row among them:
  * append first). Query head h reads KV head h / (n_heads / n_kv_heads); 1 to 16 query heads
- * share one. out = softmax(scale * q k) v in the type of q, scale > 0; dev_lse (optional,
- * [T][n_heads] fp32) gets the natural log of the softmax sums. One query per entry is a decode
- * step, more are a prompt or a chunk of one.
+ * share one. out = softmax(scale * q k) v in the type of q (QW_F16: at most 65504), scale > 0;
+ * dev_lse (optional, [T][n_heads] fp32) gets the natural log of the softmax sums. One query per
+ * entry is a decode step, more are a prompt or a chunk of one.
  * dev_score_out (optional, [B][n_kv_heads][ld_score] fp32, ld_score >= max_keys): for each cached
  * position j < dev_start[b] + rows of an entry with rows, dev_score_in (NULL: zeros; may be
  * dev_score_out) plus the weights that the call's queries give to j, summed over the queries
