@@ -1226,7 +1226,9 @@ __global__ void __launch_bounds__(CT_THREADS, 1) k_kv8_chunk(const __grid_consta
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(q_ready + t));
-            const float qmul = p.scale_log2 * muls[r];
+            // With a page's scale (2^-32 at least) the factor stays above 0, or hidden scores of -infinity would give NaN.
+            // Products of 2^33 at most over a row's scale make logits of this factor less than 2^-50.
+            const float qmul = fmaxf(p.scale_log2 * muls[r], 0x1p-94f);
             float R = -1e30f, l = 0.f;
             bool good = true;
             const int first_masked = s + rt0 / p.G;  // steps that end at or before it need no mask

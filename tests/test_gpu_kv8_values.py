@@ -50,3 +50,31 @@ def test_values_next_to_65504_stay_finite(qw, hd, n, rows):
         q = c.torch.from_numpy(c.rng.normal(0, 1, (rows, 4 * hd))).cuda().to(_dt(dtype))
         out, _ = _attn(c, q, [n - rows], [rows], 2, dtype, hd ** -0.5)
         assert np.all(out == top * sign)
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("n,rows", [(20, 1), (40, 6), (90, 90), (400, 150)])
+def test_logits_too_small_for_fp32_give_equal_weights(qw, hd, n, rows):
+    """bf16 queries of zeros and of the smallest values, keys of zeros and a small scale: the factor of a
+    logit underflows, every visible key gets the same weight and hidden ones none."""
+    c = Case(qw, [n], 1, hd, seed=6)
+    k, v = np.zeros((n, 1, hd)), c.rng.normal(0, 1, (n, 1, hd))
+    k[n // 2:] = c.rng.normal(0, 1, (n - n // 2, 1, hd))
+    _append(c, k, v)
+    q = c.torch.zeros((rows, 2 * hd), device="cuda")
+    q[:, hd:] = 2.0 ** -120
+    q = q.to(c.torch.bfloat16)
+    held = c.orc.rows(1, c.table[0], n)[:, 0]
+    for scale in (1e-6, 1e-30):
+        score = c.torch.zeros((1, 1, n), device="cuda")
+        out, lse = _attn(c, q, [n - rows], [rows], 2, BF16, scale, score)
+        want_s = np.zeros(n)
+        for i in range(rows):
+            m = n - rows + i + 1
+            want, mag = held[:m].mean(0), np.abs(held[:m]).mean(0)
+            # equal weights are powers of two, exact in fp16: fp32 sums of m terms and the output's rounding
+            assert np.all(np.abs(out[i] - want) <= mag * (m + 8) * 2.0 ** -23 + np.abs(want) * 2.0 ** -8)
+            assert np.all(np.abs(lse[i] - np.log(m)) <= (m + 8) * 2.0 ** -23 + np.log(m) * 2.0 ** -21)
+            want_s[:m] += 2.0 / m
+        got = score[0, 0].double().cpu().numpy()
+        assert np.all(np.abs(got - want_s) <= want_s * (2 * rows + n + 16) * 2.0 ** -22)
