@@ -301,8 +301,8 @@ __device__ __forceinline__ int kd_find(const int* cum, int B, int pg) {
 // The items are cut into `runs` equal runs, CTA w taking items [kd_start(w), kd_start(w + 1)): one run a CTA, but no
 // more runs than items, so every run has an item and its CTA writes each partial slot that the combine
 // kernel reads. CTAs past the last run get none.
-__device__ __forceinline__ int kd_runs(long long items, int n_cta) { return (int)min(items, (long long)n_cta); }
-__device__ __forceinline__ int kd_start(long long items, int runs, int w) { return (int)(w < runs ? items * w / runs : items); }
+__device__ __forceinline__ int kd_runs(int items, int n_cta) { return max(1, min(items, n_cta)); }
+__device__ __forceinline__ int kd_start(int items, int runs, int w) { return (int)((long long)items * min(w, runs) / runs); }
 
 __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
@@ -367,8 +367,7 @@ __global__ void __launch_bounds__(KD_WARPS * 32, NT == 1 ? 2 : 1) k_kv8_decode(c
         c1 = ok && n > 0 ? (s + n + KV8_PAGE - 1) / KV8_PAGE : 0;
     } else {
         kd_prefix(p, P.B, cum, ws, ent);
-        const long long items = (long long)cum[P.B] * H;
-        const int runs = kd_runs(items, gridDim.x);
+        const int items = cum[P.B] * H, runs = kd_runs(items, gridDim.x);
         c0 = kd_start(items, runs, blockIdx.x);
         c1 = kd_start(items, runs, blockIdx.x + 1);
     }
@@ -670,11 +669,10 @@ __global__ void __launch_bounds__(KD_WARPS * 32) k_kv8_combine(const __grid_cons
     const bool on = attn_entry(p, b, s, r0, n) && n > 0 && (!p.score_out || key0 < s + n);
     const int rows = n * p.G;
     bool split = false;
-    int w0 = 0, w1 = 0, first = 0, runs = 0;
-    long long items = 0;
+    int w0 = 0, w1 = 0, first = 0, items = 0, runs = 0;
     if (on && !P.pair_mode) {
         kd_prefix(p, P.B, cum, ws, nullptr);
-        items = (long long)cum[P.B] * H;
+        items = cum[P.B] * H;
         runs = kd_runs(items, P.n_cta);
         const int np = cum[b + 1] - cum[b];
         first = cum[b] * H + head * np;
