@@ -1720,7 +1720,8 @@ Plan make_plan(int n_kv, int HD, int B, int T, int max_len, int max_keys, int n_
         // a row's logits are written and read once (8 bytes a key) instead of its K (HD bytes): 8 x 4k tokens of
         // 4 rows 27 us, with k_kv8_score 67
         const size_t logits = (size_t)B * n_kv * q.nrow * (((size_t)max_keys + 3) & ~(size_t)3) * 4;
-        q.tbuf = score && rows <= 8 && logits <= avail;
+        // k_kv8_combine's launch has at most 65535 blocks of KC_KEYS keys
+        q.tbuf = score && rows <= 8 && logits <= avail && max_keys <= 65535 * KC_KEYS;
         q.off_o = put(q.pair_mode ? 0 : (size_t)q.n_cta * 2 * q.nrow * HD * 4);
         q.off_ml = put(q.pair_mode ? 0 : (size_t)q.n_cta * 2 * q.nrow * 2 * 4);
         q.off_t = put(q.tbuf ? logits : 0);

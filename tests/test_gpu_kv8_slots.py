@@ -65,3 +65,30 @@ def test_one_workspace_while_a_sequence_grows(qw, n_kv, score):
         c.check_attn(r)
         ws = mine.clone()
     assert c.bits() == 0
+
+
+def test_scores_under_a_bound_of_more_keys_than_a_launch_has_blocks(qw):
+    """Short entries under a bound of 65536 blocks of 1024 keys and some: scores as ever, the rest untouched."""
+    import torch
+    mk = (1 << 26) + 1024
+    c = Case(qw, [200, 33], 1, 64, seed=77, max_pages=mk // 16)
+    c.append([0, 0], [200, 33])
+    sc = c.rng.random((2, 1, 300)).astype(np.float32)
+    so = torch.zeros((2, 1, mk), device="cuda")
+    so[:, :, :300] = torch.from_numpy(sc).cuda()
+    q, qf = c.rows(2, 2, F16)
+    out = torch.empty((2, 128), dtype=torch.float16, device="cuda")
+    nb = c.qw.qw_kv8_attn_ws_bytes(c.view, 2, 2, 1, mk, 2, True)
+    ws = torch.full((nb,), 0xFF, dtype=torch.uint8, device="cuda")
+    ds, dc = c.i32([199, 32]), c.i32([0, 1, 2])
+    c.qw.qw_kv8_attn(c.view, 2, 2, 1, mk, ds.data_ptr(), dc.data_ptr(), q.data_ptr(), 128, 2, c.qw.QW_F16, 0.125, out.data_ptr(), 128, 0,
+                     so.data_ptr(), so.data_ptr(), mk, ws.data_ptr(), nb, c.status.data_ptr())
+    assert c.bits() == 0
+    for b, n in enumerate((200, 33)):
+        want, _, w, mag = c.orc.attention(c.table[b], n - 1, qf[b:b + 1], 0.125)
+        got = out[b].double().cpu().numpy().reshape(1, 2, 64)
+        assert np.all(np.abs(got - want) <= mag * 2.0 ** -10 + np.abs(want) * 2.0 ** -11 + 2.0 ** -24)
+        base = sc[b, 0].astype(np.float64)
+        base[:n] += w.reshape(2, n).sum(0)
+        np.testing.assert_allclose(so[b, 0, :300].double().cpu().numpy(), base, rtol=2e-5, atol=1e-6)
+    assert not bool(so[:, :, 300:].any())
