@@ -75,6 +75,10 @@ __device__ __forceinline__ bool attn_entry(const Kv8AttnP& p, int b, int& s, int
            (long long)s + n <= (long long)p.kv.max_pages * KV8_PAGE;
 }
 
+// Exponent of the power of two that a bf16 row with largest magnitude `a` is divided by; the range in which
+// 2^e and 2^-e are both normal.
+__device__ __forceinline__ int q_exponent(float a) { return min(max(kv8_log2(a), -126), 126); }
+
 // Lane (g, c)'s share of the 8-row query tile as the B operand of S^T = K Q^T: for each 64 dims h
 // the 16 dims 64 h + 16 c .. of row g. fp16 rows go in as they are; a bf16 row is first divided by
 // the power of two of its largest value (`mul` gives it back), so every element within 2^-17 of that
@@ -110,7 +114,7 @@ __device__ __forceinline__ void row_operand(const uint4 (*x)[2], uint32_t (*qf)[
             for (int i = 0; i < 8; ++i) a = fmaxf(a, fmaxf(fabsf(bf_lo(w[h][i])), fabsf(bf_hi(w[h][i]))));
         a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
         a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
-        const int e = min(max(kv8_log2(a), -100), 100);
+        const int e = q_exponent(a);
         mul = kv8_pow2(e);
         const float inv = kv8_pow2(-e);
 #pragma unroll
@@ -924,7 +928,7 @@ __device__ __forceinline__ void store_q(QTile<HD>& q, int w, int lane, Sink sink
             for (int k = 0; k < 4; ++k) am = fmaxf(am, fmaxf(fabsf(bf_lo(v[k])), fabsf(bf_hi(v[k]))));
 #pragma unroll
             for (int o = 1; o < LPR; o <<= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
-            const int e = min(max(kv8_log2(am), -100), 100);
+            const int e = q_exponent(am);
             mul = kv8_pow2(e);
             const float inv = kv8_pow2(-e);
 #pragma unroll

@@ -78,3 +78,19 @@ def test_logits_too_small_for_fp32_give_equal_weights(qw, hd, n, rows):
             want_s[:m] += 2.0 / m
         got = score[0, 0].double().cpu().numpy()
         assert np.all(np.abs(got - want_s) <= want_s * (2 * rows + n + 16) * 2.0 ** -22)
+
+
+@pytest.mark.parametrize("n,rows", [(20, 1), (40, 6), (90, 90)])
+def test_bf16_queries_beyond_the_fp16_range(qw, n, rows):
+    """Rows of any bf16 magnitude whose logits fit fp32: here the scale takes a power of two back."""
+    hd = 64
+    c = Case(qw, [n], 1, hd, seed=7)
+    k, v = c.rng.normal(0, 1, (n, 1, hd)), c.rng.normal(0, 1, (n, 1, hd))
+    _append(c, k, v)
+    q0 = c.torch.from_numpy(c.rng.normal(0, 1, (rows, 2 * hd))).cuda().to(c.torch.bfloat16)
+    want, wl = _attn(c, q0, [n - rows], [rows], 2, BF16, 0.125)
+    for e in (-102, -90, 100, 110, 118, 120):  # the products are those of the first call
+        q = (q0.float() * 2.0 ** e).to(c.torch.bfloat16)
+        out, lse = _attn(c, q, [n - rows], [rows], 2, BF16, 0.125 * 2.0 ** -e)
+        np.testing.assert_array_equal(out, want)
+        np.testing.assert_array_equal(lse, wl)
