@@ -10,8 +10,10 @@ from __future__ import annotations
 import concurrent.futures as cf
 import hashlib
 import os
+import re
 import shutil
 import subprocess
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -26,6 +28,24 @@ NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O3"
                      "--expt-relaxed-constexpr", "-I", INCLUDE]
 SOURCES = ["qw_runtime.cu", "k_small.cu", "k_attn.cu", "k_gemm.cu", "k_noalloc.cu", "k_sample.cu", "k_step.cu", "k_dec1.cu", "k_lmhead.cu",
            "k_kv8.cu", "k_kv8_attn.cu", "k_kv8_evict.cu"]
+# Kernels that share their registers out by role at run time: the shares add up only if the compiler gives
+# each thread exactly this many, and the library refuses to launch them otherwise.
+REGISTERS = {"k_kv8_attn.cu": {"k_kv8_chunk": 128}}
+
+
+def ptxas_log(src: str) -> str:
+    """What ptxas -v said of a source with an entry in REGISTERS at the last build."""
+    return os.path.join(BUILD, src.replace(".cu", ".ptxas"))
+
+
+def check_registers(wanted: dict, log: str) -> None:
+    """Raises unless every instance of the kernels in `wanted`, and one at least, has its number of registers in
+    the output of ptxas -v."""
+    used = re.findall(r"Compiling entry function '(\w+)'.*?Used (\d+) registers", log, re.S)
+    for name, n in wanted.items():
+        got = {int(r) for k, r in used if re.search(rf"\d{name}(?!_)", k)}
+        if got != {n}:
+            raise RuntimeError(f"{name} needs {n} registers a thread, the compiler gave {sorted(got)}")
 
 
 def _nvcc() -> str:
@@ -43,7 +63,7 @@ def _stamp() -> str:
             h.update(fh.read())
     with open(os.path.join(INCLUDE, "qw.h"), "rb") as fh:
         h.update(fh.read())
-    h.update(" ".join(NVCC_FLAGS).encode())
+    h.update((" ".join(NVCC_FLAGS) + repr(REGISTERS)).encode())
     return h.hexdigest()
 
 
@@ -60,12 +80,20 @@ def build(verbose: bool = False, force: bool = False, extra_flags=()) -> str:
 
     def compile_one(src: str) -> str:
         obj = os.path.join(BUILD, src.replace(".cu", ".o"))
-        cmd = [nvcc, *NVCC_FLAGS, *extra_flags, "-c", os.path.join(CSRC, src), "-o", obj]
+        verbose_ptxas = ["-Xptxas", "-v"] if src in REGISTERS else []
+        cmd = [nvcc, *NVCC_FLAGS, *verbose_ptxas, *extra_flags, "-c", os.path.join(CSRC, src), "-o", obj]
         if verbose:
             print(" ".join(cmd), flush=True)
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
+        if src in REGISTERS:
+            with open(ptxas_log(src), "w") as fh:
+                fh.write(r.stdout + r.stderr)
+            try:
+                check_registers(REGISTERS[src], r.stdout + r.stderr)
+            except RuntimeError as e:
+                warnings.warn(f"{e}: calls that need it will be refused")
         if verbose and (r.stdout or r.stderr):
             print(r.stdout + r.stderr, flush=True)
         return obj
