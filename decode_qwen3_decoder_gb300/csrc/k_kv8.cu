@@ -7,8 +7,9 @@
 // and writes the codes once. Tokens the page already holds are decoded, exact in fp32, and
 // re-coded with the larger exponent; a power of two leaves them as they are but for codes that
 // become subnormal. Bytes bound it: each input element is read once and each code written once. 16
-// prompts of 512 tokens (8 heads of 128, 50 MB): 15 us, 3.4 TB/s; values held as fp32 instead of
-// fp16 pairs took 17 (80 registers instead of 56). A step of 64 sequences is a launch, 4 us.
+// prompts of 512 tokens (8 heads of 128, 50 MB): 15 us, 3.4 TB/s, in a wave and a half of CTAs whose row
+// loads wait for the page id; values held as fp32 instead of fp16 pairs took 17 (80 registers instead
+// of 56). A step of 64 sequences is a launch, 4 us.
 //
 // Read. The same cut into warps; 28 layers of 2048 tokens (353 MB) take 60 us, 5.9 TB/s.
 #include "kv8.cuh"

@@ -6,9 +6,12 @@
 // is exact in fp16, so the products see exactly what the cache holds. The weight that goes into
 // the PV product is w_j = 2^(t_j + ev_j - R + 8): the V scale joins the exponent, so pages of
 // very different scales meet in one fp16 range, and the sum of the softmax takes w_j 2^-ev_j,
-// in fp32. The reference R of a row moves only when a weight would pass 2^15; the weights' fp16
-// rounding (2^-11 each, 2^-25 absolute where they are subnormal, against a largest weight of at
-// least 2^8) is the only rounding below 32 bits before the output's.
+// in fp32. The reference R of a row moves only when a weight would pass 2^15. Two roundings below 32
+// bits come before the output's. The weights' to fp16, the MMA's operand type (2^-11 each, 2^-25
+// absolute where they are subnormal, against a largest weight of at least 2^8): against 64 bits fp16
+// outputs are off by 2.1e-4 to 2.7e-4 in the mean, by 2.1e-4 with fp32 weights. And a bf16 query row's, whose
+// elements below 2^-17 of its largest lose bits as fp16 (see row_operand). Exponentials are the
+// hardware's (2^-22 relative).
 #include "kv8.cuh"
 
 #include <algorithm>

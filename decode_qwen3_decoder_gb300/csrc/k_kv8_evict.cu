@@ -16,7 +16,8 @@
 // than 80 a thread 73.
 // k_kv8_move_inplace does it where source and destination are the same memory: new position j takes
 // the row of kept[j] >= j, so one CTA a head moves batches of ascending pages with a barrier between
-// a batch's reads and its writes. (One kernel of clusters for everything took 243 us for 28 layers of
+// a batch's reads and its writes: with the select, 96 us for 28 layers of 4k tokens halved, 700 for 32k
+// (1.9 GB of rows, 2.7 TB/s). (One kernel of clusters for everything took 243 us for 28 layers of
 // 4k tokens halved; the two take 74.) k_kv8_evict_one does both for short entries, where a second
 // launch would cost more than it moves.
 #include "kv8.cuh"

@@ -479,7 +479,8 @@ qw_status qw_kv8_evict(const qw_kv8* kv, int B, int max_len, const int32_t* dev_
 /* A model's KV cache in this format. qw_kv8_alloc binds a caller-owned pool (256-byte aligned, at
  * least qw_kv8_pool_bytes) as an 8-bit cache: qw_kv_reserve, _reset, _truncate, _length and
  * _page_table, qw_prefill, qw_decode_step(s) and qw_generate(_eos) take it like a cache of
- * qw_kv_alloc, at half the bytes a token. Each layer's new K/V rows are staged as fp16 in the pool,
+ * qw_kv_alloc, at half the bytes a token and a fixed part of some 100 MB (partials of the attention)
+ * beside the staging rows of max_tokens tokens. Each layer's new K/V rows are staged as fp16 in the pool,
  * appended as by qw_kv8_append and attended to as by qw_kv8_attn; the batch-1 cluster path, the
  * two-stream split and the decode-step kernel are not used. qw_kv_fill_synthetic gives
  * QW_ERR_UNSUPPORTED, qw_kv_pool_ptrs the blocks ([n_layers][n_pages][n_kv_heads]) as dev_k and a
