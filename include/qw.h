@@ -500,7 +500,8 @@ qw_status qw_kv8_scores(const qw_kv* kv, float** dev_score, size_t* ld_score);
  * choosing by its own weights (nothing happens if it has no more). The length becomes n_keep and
  * the pages stay reserved; later tokens go on at the positions they would have had (RoPE), which
  * therefore still count against max_context until qw_kv_reset, or qw_kv_truncate to 0 tokens, lets the
- * sequence begin at position 0 again. Asynchronous on `stream`. QW_ERR_UNSUPPORTED for a cache
+ * sequence begin at position 0 again. Asynchronous on `stream`; evictions of one cache share its
+ * scratch, so those on several streams need an order between them. QW_ERR_UNSUPPORTED for a cache
  * without scores. */
 qw_status qw_kv_evict(qw_kv* kv, int seq_id, int n_keep, int n_recent, void* stream);
 
