@@ -258,8 +258,10 @@ static qw_status kv8_rows_check(const qw_kv8* kv, int B, int T, int max_len, con
                                 const char* what) {
     if (qw_status s = kv8_check(kv, B, what)) return s;
     if (T < 0 || max_len < 1 || max_len > (1 << 26)) return qw_fail(QW_ERR_INVALID_ARG, "%s: T or max_len out of range", what);
-    if (!start || !cu || !k || !v || !status) return qw_fail(QW_ERR_INVALID_ARG, "%s: NULL argument", what);
+    if (!start || !cu || !status) return qw_fail(QW_ERR_INVALID_ARG, "%s: NULL argument", what);
     if (dtype != QW_F16 && dtype != QW_BF16 && dtype != QW_F32) return qw_fail(QW_ERR_INVALID_ARG, "%s: dtype %d", what, dtype);
+    if (T == 0) return QW_OK;  // no rows to look at
+    if (!k || !v) return qw_fail(QW_ERR_INVALID_ARG, "%s: NULL argument", what);
     const size_t row = (size_t)kv->n_kv_heads * kv->head_dim, al = dtype == QW_F32 ? 4 : 8;
     if (ld_k < row || ld_v < row) return qw_fail(QW_ERR_INVALID_ARG, "%s: row stride below n_kv_heads * head_dim", what);
     if (!aligned16(k) || !aligned16(v) || ld_k % al || ld_v % al)

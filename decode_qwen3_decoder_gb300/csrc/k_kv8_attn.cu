@@ -1898,13 +1898,13 @@ extern "C" size_t qw_kv8_attn_ws_bytes(const qw_kv8* kv, int B, int T, int max_l
 extern "C" qw_status qw_kv8_attn(const qw_kv8* kv, const qw_kv8_attn_args* a, void* stream) {
     if (!a) return qw_fail(QW_ERR_INVALID_ARG, "attn: args is NULL");
     if (qw_status s = attn_sizes(kv, a->B, a->T, a->max_len, a->max_keys, a->n_heads)) return s;
-    if (!a->dev_start || !a->dev_cu || !a->dev_q || !a->dev_out || !a->dev_ws || !a->dev_status)
+    if (!a->dev_start || !a->dev_cu || !a->dev_ws || !a->dev_status || (a->T > 0 && (!a->dev_q || !a->dev_out)))
         return qw_fail(QW_ERR_INVALID_ARG, "attn: NULL argument");
     if (a->dtype != QW_F16 && a->dtype != QW_BF16)
         return qw_fail(QW_ERR_INVALID_ARG, "attn: dtype %d (QW_F16 and QW_BF16 are taken)", a->dtype);
     const size_t row = (size_t)a->n_heads * kv->head_dim;
-    if (a->ld_q < row || a->ld_out < row) return qw_fail(QW_ERR_INVALID_ARG, "attn: row stride below n_heads * head_dim");
-    if (((uintptr_t)a->dev_q | (uintptr_t)a->dev_out) & 15 || a->ld_q % 8 || a->ld_out % 8)
+    if (a->T > 0 && (a->ld_q < row || a->ld_out < row)) return qw_fail(QW_ERR_INVALID_ARG, "attn: row stride below n_heads * head_dim");
+    if (a->T > 0 && (((uintptr_t)a->dev_q | (uintptr_t)a->dev_out) & 15 || a->ld_q % 8 || a->ld_out % 8))
         return qw_fail(QW_ERR_INVALID_ARG, "attn: rows not 16-byte aligned");
     if (!(a->scale > 0.f) || !(a->scale < 1e30f)) return qw_fail(QW_ERR_INVALID_ARG, "attn: scale not positive and finite");
     if (a->dev_score_in && !a->dev_score_out) return qw_fail(QW_ERR_INVALID_ARG, "attn: score_in without score_out");

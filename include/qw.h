@@ -378,8 +378,8 @@ qw_status qw_sample_top_p(int B, int vocab, const float* dev_logits, size_t ld, 
  * host, where they size the launch. Position p of entry b lives in slot p % 16 of page
  * dev_page_table[b * max_pages + p / 16]. Rows of the tensors are ld elements apart and hold
  * n heads * head_dim contiguous elements; pointers are 16-byte aligned and so is every row
- * (ld a multiple of 8, of 4 for QW_F32), else QW_ERR_INVALID_ARG. Sequences may share pages
- * that no call writes.
+ * (ld a multiple of 8, of 4 for QW_F32), else QW_ERR_INVALID_ARG; with T = 0 they are not looked
+ * at. Sequences may share pages that no call writes.
  *
  * Errors found on the device set bits of *dev_status (QW_KV8_*; never cleared here): an entry
  * whose lengths break their bounds or whose pages are not in [0, n_pages) sets QW_KV8_BAD_POS
