@@ -27,7 +27,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O3",
                      "--expt-relaxed-constexpr", "-I", INCLUDE]
 SOURCES = ["qw_runtime.cu", "k_small.cu", "k_attn.cu", "k_gemm.cu", "k_noalloc.cu", "k_sample.cu", "k_step.cu", "k_dec1.cu", "k_lmhead.cu",
-           "k_kv8.cu", "k_kv8_attn.cu", "k_kv8_evict.cu"]
+           "k_kv8.cu", "k_kv8_attn.cu", "k_kv8_evict.cu", "k_mx.cu", "k_mx_gemm.cu"]
 # Kernels that share their registers out by role at run time: the shares add up only if the compiler gives
 # each thread exactly this many, and the library refuses to launch them otherwise.
 REGISTERS = {"k_kv8_attn.cu": {"k_kv8_chunk": 128}}

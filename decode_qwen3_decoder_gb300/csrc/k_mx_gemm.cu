@@ -1,0 +1,429 @@
+// Products of microscaled matrices (qw_mx_linear, qw_mx_swiglu) on the block-scaled tcgen05.mma. mx.cuh
+// states the format.
+//
+// The MMA reads codes and exponents as they lie: kind::mxf8f6f4 (X in e4m3, W in e4m3 or e2m1, 32 columns an
+// instruction) or kind::mxf4 (both e2m1, 64 columns), products exact, sums in fp32 in tensor memory. Codes go
+// through a ring of TMA tiles with the 128-byte swizzle, 128 bytes a row; e2m1 codes that meet e4m3 are
+// spread to 8-byte halves of 16-byte chunks by the copy itself (16U4_ALIGN16B). The exponents' 512-byte
+// tiles come by bulk copy and go to tensor memory by tcgen05.cp, in columns of their ring stage: a
+// stage is refilled only after its MMAs, so no exponent is overwritten under an MMA.
+//
+// k_mx_gemm. Tile: 128 rows of X (the M of the MMA, a TMEM lane a row) by 256 of W (N): two neighbouring
+// tiles of 128 for the linear product; the same 128 features of gate and up for SwiGLU, so that a thread has
+// both of a feature, and the 32 features of a run, in its registers. Persistent; 8 epilogue warps, one
+// producer, one MMA issuer.
+//
+// Every wait is bounded (about 2 s): then QW_MX_TIMEOUT is set and the CTA frees its TMEM and ends.
+#include <algorithm>
+
+#include "mx.cuh"
+#include "tc_sm103.cuh"
+
+namespace {
+
+constexpr int MG_THREADS = 320;
+constexpr int MG_STAGES = 4;
+constexpr int MG_X = 128 * 128, MG_W = 128 * 128;  // bytes of an operand tile in shared memory
+constexpr int MG_SF = 1024;                        // exponents of an operand tile of a stage (two atoms for 4 by 4 bits)
+constexpr int MG_STAGE = MG_X + 2 * MG_W + 3 * MG_SF;
+constexpr int MG_SMEM = MG_STAGES * MG_STAGE + 1024 + 256;
+constexpr int MG_SF_COL = 256, MG_SF_COLS = 32;  // TMEM columns of the exponents, a stage's
+
+struct MxGemmP {
+    int T, M, atoms;  // rows of X, rows of W (of gate and of up), atoms of 128 columns
+    int tiles_x, tiles_w, units;
+    const uint8_t *sx, *sa, *sb;  // exponents of X, of the tile's first and second W
+    int b_row;                    // first row of the second W, after the first's
+    int w_step;                   // W rows a tile
+    void* out;
+    size_t ld;
+    uint8_t *codes, *scales;  // SwiGLU's output
+    int oatoms;
+    int32_t* status;
+};
+
+__device__ __forceinline__ uint64_t sf_desc(uint32_t a) {  // no swizzle, 8-row groups of 16-byte rows 128 bytes apart
+    return (uint64_t)((a & 0x3FFFFu) >> 4) | ((uint64_t)8 << 32) | ((uint64_t)1 << 46);
+}
+// 32 rows of 16 bytes to 32 lanes by 4 columns, in each of the four lane quarters.
+__device__ __forceinline__ void sf_copy(uint32_t tmem, uint32_t smem) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(sf_desc(smem)) : "memory");
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+                 "r"(bytes), "r"(bar)
+                 : "memory");
+}
+template <bool F4>
+__device__ __forceinline__ void mma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb, uint32_t acc) {
+    if (F4)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(acc)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(acc)
+            : "memory");
+}
+// Instruction descriptor of the block-scaled kinds: exponent byte of B at bit 4 and of A at bit 29, formats of
+// A and B at 7 and 10 (mxf8f6f4: 0 e4m3, 5 e2m1; mxf4: 1 e2m1), N >> 3 at 17, ue8m0 scales at 23, M >> 4 at 24.
+constexpr uint32_t idesc_mx(uint32_t fa, uint32_t fb, int M, int N) {
+    return (fa << 7) | (fb << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 4) << 24);
+}
+
+// A thread's 32 sums of one row of the output, columns f .. f + 31.
+template <int DT>
+__device__ __forceinline__ void store_row(const MxGemmP& p, int t, int f, const uint32_t* r) {
+    const size_t at = (size_t)t * p.ld + f;
+#pragma unroll
+    for (int j = 0; j < 32; j += 8) {
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(r[j + i]);
+        if (p.M - f - j > 0) mx_store8<DT>(p.out, at + j, p.M - f - j, x);
+    }
+}
+
+// silu(g) u. exp and the division in their fast forms: 2^-20 relative at most, where a code has 4 bits.
+__device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.f + __expf(-g)) * u; }
+
+// A thread's run of 32 features of row t: codes and exponent. Features from M on are zeros.
+template <int BITS>
+__device__ __forceinline__ void store_run(const MxGemmP& p, int t, int f, const uint32_t* g, const uint32_t* u) {
+    float h[32];
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        h[i] = f + i < p.M ? silu_mul(__uint_as_float(g[i]), __uint_as_float(u[i])) : 0.f;
+        m = max(m, __float_as_uint(h[i]) & 0x7FFFFFFFu);
+    }
+    const int byte = mx_exp_byte<BITS>(m);
+    const float inv = mx_inv_scale(byte);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) h[i] *= inv;
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t q[2];
+        mx_enc8<BITS>(h + 8 * i, q);
+        if (BITS == 8) w[2 * i] = q[0], w[2 * i + 1] = q[1];
+        else w[i] = q[0];
+    }
+    uint4* at = reinterpret_cast<uint4*>(p.codes + (size_t)t * p.oatoms * (MX_ATOM * BITS / 8) + (size_t)f * BITS / 8);
+    at[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    if (BITS == 8) at[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    p.scales[mx_scale_word(t, f / MX_ATOM, p.oatoms) + (f / MX_RUN & 3)] = (uint8_t)byte;
+}
+
+// OUT: QW_F16, QW_BF16, QW_F32 (linear); 8, 4 (SwiGLU with codes of so many bits).
+template <int XB, int WB, int OUT>
+__global__ void __launch_bounds__(MG_THREADS, 1)
+    k_mx_gemm(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmA,
+              const __grid_constant__ CUtensorMap tmB, const __grid_constant__ MxGemmP p) {
+    constexpr bool F4 = XB == 4, GLU = OUT == 8 || OUT == 4;
+    constexpr int AT = F4 ? 2 : 1;                                     // atoms of 128 columns a stage
+    constexpr uint32_t W_TX = WB == 4 && !F4 ? MG_W / 2 : MG_W;        // a spread tile counts its bytes in memory
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + MG_STAGES * MG_STAGE);
+    uint64_t* empty = full + MG_STAGES;
+    uint64_t* accf = empty + MG_STAGES;
+    uint64_t* acce = accf + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acce + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int nk = (p.atoms + AT - 1) / AT;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < MG_STAGES; ++s) {
+            mbar_init(smem_u32(full + s), 1);
+            mbar_init(smem_u32(empty + s), 1);
+        }
+        mbar_init(smem_u32(accf), 1);
+        mbar_init(smem_u32(acce), 8);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == 8 && lane == 0) {
+        tma_prefetch_desc(&tmX);
+        tma_prefetch_desc(&tmA);
+        tma_prefetch_desc(&tmB);
+    }
+    if (warp == 9) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait();
+    pdl_launch();
+
+    if (warp == 8) {
+        if (lane == 0) {
+            uint32_t g = 0;
+            for (int u = blockIdx.x; u < p.units && !*abort_flag; u += gridDim.x) {
+                const int tw = u % p.tiles_w, tx = u / p.tiles_w;
+                const int wa = tw * p.w_step, wb = wa + p.b_row;
+                const bool two = wb < p.M;  // the second tile of W has rows
+                for (int kb = 0; kb < nk; ++kb, ++g) {
+                    const int s = g % MG_STAGES;
+                    if (!mbar_wait(smem_u32(empty + s), ((g / MG_STAGES) & 1u) ^ 1u, abort_flag)) {
+                        *abort_flag = 1;
+                        break;
+                    }
+                    const uint32_t st = smem_u32(smem + s * MG_STAGE), bar = smem_u32(full + s);
+                    const uint32_t sf = (uint32_t)min(AT, p.atoms - kb * AT) * MX_TILE_BYTES;
+                    mbar_expect_tx(bar, MG_X + 2 * W_TX + sf * (two ? 3 : 2));
+                    tma_load_2d(st, &tmX, bar, kb * 128, tx * 128);
+                    tma_load_2d(st + MG_X, &tmA, bar, kb * 128, wa);
+                    tma_load_2d(st + MG_X + MG_W, &tmB, bar, kb * 128, wb);
+                    const uint32_t sfs = st + MG_X + 2 * MG_W;
+                    bulk_load(sfs, p.sx + ((size_t)tx * p.atoms + kb * AT) * MX_TILE_BYTES, sf, bar);
+                    bulk_load(sfs + MG_SF, p.sa + ((size_t)(wa >> 7) * p.atoms + kb * AT) * MX_TILE_BYTES, sf, bar);
+                    if (two) bulk_load(sfs + 2 * MG_SF, p.sb + ((size_t)(wb >> 7) * p.atoms + kb * AT) * MX_TILE_BYTES, sf, bar);
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = idesc_mx(F4 ? 1 : 0, F4 ? 1 : WB == 4 ? 5 : 0, 128, 256);
+            uint32_t g = 0;
+            int i = 0;
+            bool ok = true;
+            for (int u = blockIdx.x; u < p.units && ok; u += gridDim.x, ++i) {
+                if (!mbar_wait(smem_u32(acce), ((uint32_t)i & 1u) ^ 1u, abort_flag)) {
+                    *abort_flag = 1;
+                    break;
+                }
+                tc_fence_after();
+                for (int kb = 0; kb < nk; ++kb, ++g) {
+                    const int s = g % MG_STAGES;
+                    if (!mbar_wait(smem_u32(full + s), (g / MG_STAGES) & 1u, abort_flag)) {
+                        ok = false;
+                        *abort_flag = 1;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t st = smem_u32(smem + s * MG_STAGE), sfs = st + MG_X + 2 * MG_W;
+                    const uint32_t ta = tmem + MG_SF_COL + s * MG_SF_COLS, tb = ta + 8;
+                    const int at = min(AT, p.atoms - kb * AT);
+                    for (int a = 0; a < at; ++a) {
+                        sf_copy(ta + 4 * a, sfs + a * MX_TILE_BYTES);
+                        sf_copy(tb + 8 * a, sfs + MG_SF + a * MX_TILE_BYTES);
+                        sf_copy(tb + 8 * a + 4, sfs + 2 * MG_SF + a * MX_TILE_BYTES);
+                    }
+                    const uint64_t ad = sw128_desc(st), bd = sw128_desc(st + MG_X);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        // 32 bytes of a row: 32 columns with the exponents' byte k, or 64 with bytes 2 k % 4 and the next
+                        const int a = F4 ? k / 2 : 0;
+                        const uint32_t id = F4 ? (uint32_t)(k & 1) * 2 : (uint32_t)k;
+                        if (a < at)
+                            mma_mx<F4>(tmem, ad + 2 * k, bd + 2 * k, idesc | (id << 4) | (id << 29), ta + 4 * a, tb + 8 * a, kb > 0 || k > 0);
+                    }
+                    umma_commit(smem_u32(empty + s));
+                }
+                if (ok) umma_commit(smem_u32(accf));
+            }
+        }
+        __syncwarp();
+    } else {
+        // warps w and w + 4 read the lanes 32 (w % 4) ..: the first half of the features and the second
+        const int half = warp >> 2;
+        const uint32_t row = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        int i = 0;
+        for (int u = blockIdx.x; u < p.units; u += gridDim.x, ++i) {
+            const int tw = u % p.tiles_w, tx = u / p.tiles_w;
+            const int t = tx * 128 + (warp & 3) * 32 + lane;
+            if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(accf), (uint32_t)i & 1u, abort_flag))) {
+                *abort_flag = 1;
+                break;
+            }
+            tc_fence_after();
+            auto release = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(acce)) : "memory");
+            };
+            if (GLU) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t gr[32], ur[32];
+                    const int f = half * 64 + c * 32;
+                    TMEM_LD32(row + f, gr);
+                    TMEM_LD32(row + 128 + f, ur);
+                    tmem_wait_ld();
+                    if (c == 1) release();
+                    if (t < p.T) store_run<OUT>(p, t, tw * 128 + f, gr, ur);
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t r[32];
+                    const int f = half * 128 + c * 32;
+                    TMEM_LD32(row + f, r);
+                    tmem_wait_ld();
+                    if (c == 3) release();
+                    if (t < p.T) store_row<OUT>(p, t, tw * 256 + f, r);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0 && *abort_flag) atomicOr(p.status, QW_MX_TIMEOUT);
+    if (warp == 9) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+}
+
+// ---- host ------------------------------------------------------------------------------------------------
+
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled find_encode() {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+        return nullptr;
+    return (EncodeTiled)f;
+}
+
+// Tiles of `box` rows by 128 bytes of shared memory. spread: 4-bit codes to 16-byte chunks of 16.
+bool encode(CUtensorMap* map, const qw_mx& m, bool spread, unsigned box) {
+    static const EncodeTiled enc = find_encode();
+    if (!enc) return false;
+    const cuuint64_t bytes = mx_row_bytes(m.bits, m.cols);
+    const cuuint64_t dims[2] = {spread ? 2 * bytes : bytes, (cuuint64_t)m.rows}, strides[1] = {bytes};
+    const cuuint32_t boxes[2] = {128, box}, es[2] = {1, 1};
+    return enc(map, spread ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, m.dev_codes, dims,
+               strides, boxes, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int sm_count() {  // of the current device
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 1;
+    return n;
+}
+
+struct Maps {
+    CUtensorMap x, a, b;
+};
+
+template <int XB, int WB, int OUT>
+cudaError_t launch_gemm(const Maps& m, const MxGemmP& p, cudaStream_t st) {
+    const cudaError_t e = cudaFuncSetAttribute(k_mx_gemm<XB, WB, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, MG_SMEM);
+    if (e != cudaSuccess) return e;
+    return launch_k({st, true, nullptr}, k_mx_gemm<XB, WB, OUT>, dim3(std::min(p.units, sm_count())), dim3(MG_THREADS), MG_SMEM,
+                    m.x, m.a, m.b, p);
+}
+
+template <int OUT>
+cudaError_t launch_formats(int xb, int wb, const Maps& m, const MxGemmP& p, cudaStream_t st) {
+    return xb == 4   ? launch_gemm<4, 4, OUT>(m, p, st)
+           : wb == 4 ? launch_gemm<8, 4, OUT>(m, p, st)
+                     : launch_gemm<8, 8, OUT>(m, p, st);
+}
+
+qw_status formats_check(const qw_mx* x, const qw_mx* w, const char* what) {
+    if (x->cols != w->cols) return qw_fail(QW_ERR_INVALID_ARG, "%s: x has %d columns, the weights %d", what, x->cols, w->cols);
+    if (x->bits == 4 && w->bits == 8)
+        return qw_fail(QW_ERR_UNSUPPORTED, "%s: 4-bit x with 8-bit weights (8 by 4, 4 by 4 and 8 by 8 are built)", what);
+    return QW_OK;
+}
+
+// Parameters and tensor maps that both products share; wb: the tiles' second matrix (linear: w itself).
+bool product(const qw_mx& x, const qw_mx& wa, const qw_mx& wb, bool glu, int32_t* status, MxGemmP& p, Maps& m) {
+    p = MxGemmP{};
+    p.T = x.rows;
+    p.M = wa.rows;
+    p.atoms = (int)mx_atoms(x.cols);
+    p.w_step = glu ? 128 : 256;
+    p.b_row = glu ? 0 : 128;
+    p.tiles_x = (int)(((long long)p.T + 127) / 128);
+    p.tiles_w = (int)(((long long)p.M + p.w_step - 1) / p.w_step);
+    p.units = p.tiles_x * p.tiles_w;
+    p.sx = (const uint8_t*)x.dev_scales;
+    p.sa = (const uint8_t*)wa.dev_scales;
+    p.sb = (const uint8_t*)wb.dev_scales;
+    p.status = status;
+    const bool spread = wa.bits == 4 && x.bits == 8;
+    return encode(&m.x, x, false, 128) && encode(&m.a, wa, spread, 128) && encode(&m.b, wb, spread, 128);
+}
+
+qw_status done(cudaError_t e, const char* what) {
+    return e == cudaSuccess ? QW_OK : qw_fail(QW_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+// Tiles are numbered in an int.
+bool too_many(int T, int M) { return (double)(T / 128 + 1) * (M / 128 + 1) > 2147483647.0; }
+
+}  // namespace
+
+extern "C" qw_status qw_mx_linear(const qw_mx* x, const qw_mx* w, void* dev_out, size_t ld_out, int dtype,
+                                  int32_t* dev_status, void* stream) {
+    const char* what = "mx_linear";
+    if (qw_status s = mx_check(x, what, "x")) return s;
+    if (qw_status s = mx_check(w, what, "w")) return s;
+    if (qw_status s = formats_check(x, w, what)) return s;
+    if (dtype != QW_F16 && dtype != QW_BF16 && dtype != QW_F32) return qw_fail(QW_ERR_INVALID_ARG, "%s: dtype %d", what, dtype);
+    if (!dev_status) return qw_fail(QW_ERR_INVALID_ARG, "%s: NULL status", what);
+    if (x->rows == 0 || w->rows == 0) return QW_OK;
+    if (!dev_out) return qw_fail(QW_ERR_INVALID_ARG, "%s: NULL out", what);
+    if (ld_out < (size_t)w->rows) return qw_fail(QW_ERR_INVALID_ARG, "%s: row stride of out below w's rows", what);
+    if (((uintptr_t)dev_out & 15) || ld_out % (dtype == QW_F32 ? 4 : 8))
+        return qw_fail(QW_ERR_INVALID_ARG, "%s: rows of out not 16-byte aligned", what);
+    if (too_many(x->rows, w->rows)) return qw_fail(QW_ERR_UNSUPPORTED, "%s: more than 2^31 tiles", what);
+    MxGemmP p;
+    Maps m;
+    if (!product(*x, *w, *w, false, dev_status, p, m)) return qw_fail(QW_ERR_CUDA, "%s: tensor map", what);
+    p.out = dev_out;
+    p.ld = ld_out;
+    const cudaStream_t st = (cudaStream_t)stream;
+    return done(dtype == QW_F16    ? launch_formats<QW_F16>(x->bits, w->bits, m, p, st)
+                : dtype == QW_BF16 ? launch_formats<QW_BF16>(x->bits, w->bits, m, p, st)
+                                   : launch_formats<QW_F32>(x->bits, w->bits, m, p, st),
+                what);
+}
+
+extern "C" qw_status qw_mx_swiglu(const qw_mx* x, const qw_mx* w_gate, const qw_mx* w_up, const qw_mx* out,
+                                  int32_t* dev_status, void* stream) {
+    const char* what = "mx_swiglu";
+    if (qw_status s = mx_check(x, what, "x")) return s;
+    if (qw_status s = mx_check(w_gate, what, "w_gate")) return s;
+    if (qw_status s = mx_check(w_up, what, "w_up")) return s;
+    if (w_gate->rows < 1) return qw_fail(QW_ERR_INVALID_ARG, "%s: w_gate has no rows", what);
+    if (qw_status s = mx_check(out, what, "out")) return s;
+    if (qw_status s = formats_check(x, w_gate, what)) return s;
+    if (w_up->rows != w_gate->rows || w_up->cols != w_gate->cols || w_up->bits != w_gate->bits)
+        return qw_fail(QW_ERR_INVALID_ARG, "%s: w_gate and w_up differ in shape or bits", what);
+    if (out->rows != x->rows || out->cols != w_gate->rows)
+        return qw_fail(QW_ERR_INVALID_ARG, "%s: out is not [rows of x][rows of w_gate]", what);
+    if (!dev_status) return qw_fail(QW_ERR_INVALID_ARG, "%s: NULL status", what);
+    if (x->rows == 0) return QW_OK;
+    if (too_many(x->rows, w_gate->rows)) return qw_fail(QW_ERR_UNSUPPORTED, "%s: more than 2^31 tiles", what);
+    MxGemmP p;
+    Maps m;
+    if (!product(*x, *w_gate, *w_up, true, dev_status, p, m)) return qw_fail(QW_ERR_CUDA, "%s: tensor map", what);
+    p.codes = (uint8_t*)out->dev_codes;
+    p.scales = (uint8_t*)out->dev_scales;
+    p.oatoms = (int)mx_atoms(out->cols);
+    const cudaStream_t st = (cudaStream_t)stream;
+    return done(out->bits == 8 ? launch_formats<8>(x->bits, w_gate->bits, m, p, st) : launch_formats<4>(x->bits, w_gate->bits, m, p, st),
+                what);
+}

@@ -65,6 +65,11 @@ class qw_kv8_attn_args(ctypes.Structure):
                 ("dev_status", ctypes.c_void_p)]
 
 
+class qw_mx(ctypes.Structure):
+    _fields_ = [("dev_codes", ctypes.c_void_p), ("dev_scales", ctypes.c_void_p), ("rows", ctypes.c_int),
+                ("cols", ctypes.c_int), ("bits", ctypes.c_int)]
+
+
 _LIB: Optional[ctypes.CDLL] = None
 _VP, _I, _SZ, _P = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.POINTER
 
@@ -112,6 +117,13 @@ SIGNATURES = {
     "qw_kv8_attn_ws_bytes": (_SZ, [_P(qw_kv8), _I, _I, _I, _I, _I, _I]),
     "qw_kv8_attn": (_I, [_P(qw_kv8), _P(qw_kv8_attn_args), _VP]),
     "qw_kv8_evict": (_I, [_P(qw_kv8), _I, _I, _VP, _I, _I, _VP, _VP, _VP, _SZ, _VP, _VP, _VP, _VP]),
+    "qw_mx_code_bytes": (_SZ, [_I, _I, _I]),
+    "qw_mx_scale_bytes": (_SZ, [_I, _I]),
+    "qw_mx_quantize": (_I, [_P(qw_mx), _VP, _SZ, _I, _VP]),
+    "qw_mx_read": (_I, [_P(qw_mx), _VP, _SZ, _I, _VP]),
+    "qw_mx_rmsnorm": (_I, [_P(qw_mx), _VP, _SZ, _I, _VP, _SZ, _I, _VP, _SZ, _VP, ctypes.c_float, _VP]),
+    "qw_mx_linear": (_I, [_P(qw_mx), _P(qw_mx), _VP, _SZ, _I, _VP, _VP]),
+    "qw_mx_swiglu": (_I, [_P(qw_mx), _P(qw_mx), _P(qw_mx), _P(qw_mx), _VP, _VP]),
     "qw_lm_head_argmax_noalloc": (_I, [_VP, _I, _VP, _VP, _VP, _VP]),
 }
 
@@ -389,6 +401,46 @@ def qw_kv8_evict(kv: qw_kv8, B: int, max_len: int, len_ptr: int, n_keep: int, n_
     """dst_table 0: in place; see include/qw.h."""
     _check(load().qw_kv8_evict(ctypes.byref(kv), B, max_len, len_ptr, n_keep, n_recent, dst_table_ptr or None,
                                score_ptr, score_out_ptr, ld_score, kept_ptr, new_len_ptr, status_ptr,
+                               _stream(stream)))
+
+
+QW_MX_TIMEOUT = 2
+
+
+def qw_mx_code_bytes(bits: int, rows: int, cols: int) -> int:
+    return load().qw_mx_code_bytes(bits, rows, cols)
+
+
+def qw_mx_scale_bytes(rows: int, cols: int) -> int:
+    return load().qw_mx_scale_bytes(rows, cols)
+
+
+def qw_mx_view(codes_ptr: int, scales_ptr: int, rows: int, cols: int, bits: int) -> qw_mx:
+    """The descriptor of a microscaled matrix in the caller's memory; see include/qw.h."""
+    return qw_mx(dev_codes=codes_ptr, dev_scales=scales_ptr, rows=rows, cols=cols, bits=bits)
+
+
+def qw_mx_quantize(out: qw_mx, x_ptr: int, ld_x: int, dtype: int, stream=None) -> None:
+    _check(load().qw_mx_quantize(ctypes.byref(out), x_ptr, ld_x, dtype, _stream(stream)))
+
+
+def qw_mx_read(m: qw_mx, x_ptr: int, ld_x: int, dtype: int, stream=None) -> None:
+    _check(load().qw_mx_read(ctypes.byref(m), x_ptr, ld_x, dtype, _stream(stream)))
+
+
+def qw_mx_rmsnorm(out: qw_mx, x_ptr: int, ld_x: int, x_dtype: int, add_ptr: int, ld_add: int, add_dtype: int,
+                  sum_ptr: int, ld_sum: int, weight_ptr: int, eps: float, stream=None) -> None:
+    """add and sum may be 0 (none, not wanted); see include/qw.h."""
+    _check(load().qw_mx_rmsnorm(ctypes.byref(out), x_ptr, ld_x, x_dtype, add_ptr or None, ld_add, add_dtype,
+                                sum_ptr or None, ld_sum, weight_ptr, eps, _stream(stream)))
+
+
+def qw_mx_linear(x: qw_mx, w: qw_mx, out_ptr: int, ld_out: int, dtype: int, status_ptr: int, stream=None) -> None:
+    _check(load().qw_mx_linear(ctypes.byref(x), ctypes.byref(w), out_ptr, ld_out, dtype, status_ptr, _stream(stream)))
+
+
+def qw_mx_swiglu(x: qw_mx, w_gate: qw_mx, w_up: qw_mx, out: qw_mx, status_ptr: int, stream=None) -> None:
+    _check(load().qw_mx_swiglu(ctypes.byref(x), ctypes.byref(w_gate), ctypes.byref(w_up), ctypes.byref(out), status_ptr,
                                _stream(stream)))
 
 

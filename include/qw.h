@@ -505,6 +505,69 @@ qw_status qw_kv8_scores(const qw_kv* kv, float** dev_score, size_t* ld_score);
  * without scores. */
 qw_status qw_kv_evict(qw_kv* kv, int seq_id, int n_keep, int n_recent, void* stream);
 
+/* ---- Microscaled matrices: quantisation, RMSNorm, products -------------------------------
+ *
+ * Operators on matrices whose elements are 8- or 4-bit floats with a power of two for each run of 32
+ * columns of a row (8.25 or 4.25 bits an element), as the tensor cores of sm_103a read them. They
+ * need no model, no workspace and keep no state between calls; a captured graph can replay them.
+ *
+ * Held values. L is 448 (8 bits, e4m3) or 6 (4 bits, e2m1). A run's exponent e is the smallest integer
+ * >= -127 with max|x| <= L * 2^e (-127 for a run of zeros); the code of x is x * 2^-e rounded to
+ * nearest even and stands for code * 2^e. A run with a NaN or an infinity is NaN as a whole, and so is
+ * every product that reads it.
+ *
+ * Layout. dev_codes: rows of ceil(cols / 128) * 128 codes, those past cols zeros; 4 bits: two a byte, the
+ * even column in the low half. dev_scales: one byte a run, e + 127 (255: NaN), in tiles of 128 rows by 4 runs,
+ * [ceil(rows / 128)][ceil(cols / 128)][512]; row r's run j is byte 16 (r % 32) + 4 (r / 32 % 4) + j % 4 of tile
+ * [r / 128][j / 4]; runs past cols have exponent -127, bytes of rows past the last one are not used. The
+ * operators write both, the padding of the rows that they write included.
+ *
+ * Rows of tensors (x, add, sum, out) are ld elements apart, and 16-byte aligned (ld a multiple of 8, of 4 for
+ * QW_F32), else QW_ERR_INVALID_ARG; elements between the columns and ld are neither read nor written. Any
+ * number of rows and 1 to QW_MX_MAX_COLS columns; without rows nothing happens and no memory is looked
+ * at. Outputs overlap no input but where it says so. QW_F16 results stop at 65504. All calls are asynchronous
+ * on `stream`, whose device has to be the current one. */
+#define QW_MX_MAX_COLS (1 << 20)
+#define QW_MX_TIMEOUT 2 /* bit of *dev_status (never cleared here): a bounded wait inside a kernel gave up, outputs not valid */
+
+typedef struct {
+    void* dev_codes;  /* qw_mx_code_bytes, 32-byte aligned  */
+    void* dev_scales; /* qw_mx_scale_bytes, 32-byte aligned */
+    int rows;
+    int cols;
+    int bits;         /* 8 or 4 (else QW_ERR_UNSUPPORTED)   */
+} qw_mx;
+
+/* Bytes of a matrix's codes and scales; 0 for sizes out of range. */
+size_t qw_mx_code_bytes(int bits, int rows, int cols);
+size_t qw_mx_scale_bytes(int rows, int cols);
+
+/* Quantises dev_x [out->rows][out->cols] of `dtype`: weights once, or activations before a product. */
+qw_status qw_mx_quantize(const qw_mx* out, const void* dev_x, size_t ld_x, int dtype, void* stream);
+
+/* Read back: the values that m holds, rounded to `dtype`. */
+qw_status qw_mx_read(const qw_mx* m, void* dev_x, size_t ld_x, int dtype, void* stream);
+
+/* The step between two branches of a layer: s = x + add, rounded to x_dtype (dev_add NULL: s = x; add_dtype is
+ * add's own type), written to dev_sum (x_dtype; NULL: not wanted; may be dev_x with the same stride), and
+ * y = s / sqrt(mean(s^2) + eps) * weight (dev_weight: [cols] bf16, 16-byte aligned; eps > 0) quantised to `out`.
+ * The codes are those of the real number y, whatever the order of the sums: equal inputs give equal bits
+ * on every launch shape. (|y| above fp32's range gives NaN.) */
+qw_status qw_mx_rmsnorm(const qw_mx* out, const void* dev_x, size_t ld_x, int x_dtype, const void* dev_add, size_t ld_add,
+                        int add_dtype, void* dev_sum, size_t ld_sum, const void* dev_weight, float eps, void* stream);
+
+/* out[t][m] = sum_k x[t][k] w[m][k], rounded once to `dtype`: x [T][K], w [M][K], out [T] rows of M. Products of
+ * codes are exact and sums are kept in fp32. x and w in 8 and 4, 4 and 4 or 8 and 8 bits (4 and 8:
+ * QW_ERR_UNSUPPORTED). The order of the sums is fixed for given sizes: equal inputs give equal bits. */
+qw_status qw_mx_linear(const qw_mx* x, const qw_mx* w, void* dev_out, size_t ld_out, int dtype, int32_t* dev_status,
+                       void* stream);
+
+/* out = quantise(SiLU(x w_gate^T) * (x w_up^T)): x [T][K], w_gate and w_up [I][K] of the same bits, out [T][I] in 8
+ * or 4 bits. The products as in qw_mx_linear; SiLU and the product of the two in fp32 (2^-20 relative), then
+ * quantised. */
+qw_status qw_mx_swiglu(const qw_mx* x, const qw_mx* w_gate, const qw_mx* w_up, const qw_mx* out, int32_t* dev_status,
+                       void* stream);
+
 /* ---- For callers that cannot allocate device memory ---------------------------------- */
 
 /* The page has no counterpart to this entry point; it serves callers that must not call
