@@ -22,11 +22,17 @@
 namespace {
 
 constexpr int MG_THREADS = 320;
-constexpr int MG_STAGES = 4;
 constexpr int MG_X = 128 * 128, MG_W = 128 * 128;  // bytes of an operand tile in shared memory
 constexpr int MG_SF = 1024;                        // exponents of an operand tile of a stage (two atoms for 4 by 4 bits)
 constexpr int MG_STAGE = MG_X + 2 * MG_W + 3 * MG_SF;
-constexpr int MG_SMEM = MG_STAGES * MG_STAGE + 1024 + 256;
+constexpr int MG_OUT = 32 * 128;                   // staged output of an epilogue warp: 32 rows of 128 bytes
+// Linear: three stages and two staged boxes a warp; SwiGLU, whose output is small, stores from registers: four stages.
+template <bool GLU>
+struct MgCfg {
+    static constexpr int STAGES = GLU ? 4 : 3;
+    static constexpr int OUT = GLU ? 0 : 8 * 2 * MG_OUT;
+    static constexpr int SMEM = 1024 + STAGES * MG_STAGE + OUT + 256;
+};
 constexpr int MG_SF_COL = 256, MG_SF_COLS = 32;  // TMEM columns of the exponents, a stage's
 
 struct MxGemmP {
@@ -35,7 +41,7 @@ struct MxGemmP {
     const uint8_t *sx, *sa, *sb;  // exponents of X, of the tile's first and second W
     int b_row;                    // first row of the second W, after the first's
     int w_step;                   // W rows a tile
-    void* out;
+    void* out;  // linear's output, rows of ld elements
     size_t ld;
     uint8_t *codes, *scales;  // SwiGLU's output
     int oatoms;
@@ -77,16 +83,54 @@ constexpr uint32_t idesc_mx(uint32_t fa, uint32_t fb, int M, int N) {
     return (fa << 7) | (fb << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 4) << 24);
 }
 
-// A thread's 32 sums of one row of the output, columns f .. f + 31.
+// A box of 32 rows by 128 bytes from a warp's shared memory to the output; rows and columns outside it are clipped.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"((uint64_t)map), "r"(x),
+                 "r"(y), "r"(src)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+// A warp's 32 rows (a row a lane) of 128 sums, to columns f .. f + 127 of the output through two boxes in turn. A
+// lane's 16-byte chunks go to the places that the 128-byte swizzle gives them, which no two of 8 lanes share. A
+// copy clips whole 16-byte chunks only: the map ends at the last whole one, what is left of M goes element by element.
 template <int DT>
-__device__ __forceinline__ void store_row(const MxGemmP& p, int t, int f, const uint32_t* r) {
-    const size_t at = (size_t)t * p.ld + f;
+__device__ __forceinline__ void store_rows(const CUtensorMap* map, const MxGemmP& p, uint8_t* box, int t0, int f, uint32_t (*r)[32]) {
+    constexpr int PER = DT == QW_F32 ? 32 : 64, BOXES = 128 / PER;  // columns of a box
+    const int lane = threadIdx.x & 31;
+    if (t0 >= p.T) return;
 #pragma unroll
-    for (int j = 0; j < 32; j += 8) {
-        float x[8];
+    for (int b = 0; b < BOXES; ++b) {
+        if (f + b * PER >= p.M) break;
+        uint8_t* at = box + (b & 1) * MG_OUT;
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // the box before last has been read
+        __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(r[j + i]);
-        if (p.M - f - j > 0) mx_store8<DT>(p.out, at + j, p.M - f - j, x);
+        for (int c = 0; c < 8; ++c) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (DT == QW_F32) {
+                    w[k] = r[b][4 * c + k];
+                } else {
+                    const uint32_t* v = r[2 * b + c / 4] + (c % 4) * 8 + 2 * k;
+                    w[k] = mx_pack2<DT>(__uint_as_float(v[0]), __uint_as_float(v[1]));
+                }
+            }
+            *reinterpret_cast<uint4*>(at + lane * 128 + ((c ^ (lane & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        const int whole = p.M & ~(PER / 8 - 1), x0 = f + b * PER;
+        if (lane == 0 && x0 < whole) tma_store_2d(map, smem_u32(at), x0, t0);
+        if (t0 + lane < p.T)
+            for (int x = max(whole, x0); x < min(p.M, x0 + PER); ++x) {
+                const int e = x - x0, es = 128 / PER;
+                const uint8_t* from = at + lane * 128 + ((e * es / 16 ^ (lane & 7)) * 16) + e * es % 16;
+                const size_t to = (size_t)(t0 + lane) * p.ld + x;
+                if (DT == QW_F32) reinterpret_cast<float*>(p.out)[to] = *reinterpret_cast<const float*>(from);
+                else reinterpret_cast<uint16_t*>(p.out)[to] = *reinterpret_cast<const uint16_t*>(from);
+            }
     }
 }
 
@@ -115,9 +159,13 @@ __device__ __forceinline__ void store_run(const MxGemmP& p, int t, int f, const 
         if (BITS == 8) w[2 * i] = q[0], w[2 * i + 1] = q[1];
         else w[i] = q[0];
     }
-    uint4* at = reinterpret_cast<uint4*>(p.codes + (size_t)t * p.oatoms * (MX_ATOM * BITS / 8) + (size_t)f * BITS / 8);
-    at[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    if (BITS == 8) at[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    uint8_t* at = p.codes + (size_t)t * p.oatoms * (MX_ATOM * BITS / 8) + (size_t)f * BITS / 8;
+    if (BITS == 8)  // a whole 32-byte sector
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                     "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    else
+        *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
     p.scales[mx_scale_word(t, f / MX_ATOM, p.oatoms) + (f / MX_RUN & 3)] = (uint8_t)byte;
 }
 
@@ -125,23 +173,26 @@ __device__ __forceinline__ void store_run(const MxGemmP& p, int t, int f, const 
 template <int XB, int WB, int OUT>
 __global__ void __launch_bounds__(MG_THREADS, 1)
     k_mx_gemm(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmA,
-              const __grid_constant__ CUtensorMap tmB, const __grid_constant__ MxGemmP p) {
+              const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmO,
+              const __grid_constant__ MxGemmP p) {
     constexpr bool F4 = XB == 4, GLU = OUT == 8 || OUT == 4;
+    using C = MgCfg<GLU>;
     constexpr int AT = F4 ? 2 : 1;                                     // atoms of 128 columns a stage
     constexpr uint32_t W_TX = WB == 4 && !F4 ? MG_W / 2 : MG_W;        // a spread tile counts its bytes in memory
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + MG_STAGES * MG_STAGE);
-    uint64_t* empty = full + MG_STAGES;
-    uint64_t* accf = empty + MG_STAGES;
+    uint8_t* boxes = smem + C::STAGES * MG_STAGE;
+    uint64_t* full = reinterpret_cast<uint64_t*>(boxes + C::OUT);
+    uint64_t* empty = full + C::STAGES;
+    uint64_t* accf = empty + C::STAGES;
     uint64_t* acce = accf + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acce + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int nk = (p.atoms + AT - 1) / AT;
+    const int nk = (p.atoms + AT - 1) / AT;  // stages a tile
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < MG_STAGES; ++s) {
+        for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(smem_u32(full + s), 1);
             mbar_init(smem_u32(empty + s), 1);
         }
@@ -155,6 +206,7 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
         tma_prefetch_desc(&tmX);
         tma_prefetch_desc(&tmA);
         tma_prefetch_desc(&tmB);
+        if (!GLU) tma_prefetch_desc(&tmO);
     }
     if (warp == 9) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot)) : "memory");
@@ -175,8 +227,8 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
                 const int wa = tw * p.w_step, wb = wa + p.b_row;
                 const bool two = wb < p.M;  // the second tile of W has rows
                 for (int kb = 0; kb < nk; ++kb, ++g) {
-                    const int s = g % MG_STAGES;
-                    if (!mbar_wait(smem_u32(empty + s), ((g / MG_STAGES) & 1u) ^ 1u, abort_flag)) {
+                    const int s = g % C::STAGES;
+                    if (!mbar_wait(smem_u32(empty + s), ((g / C::STAGES) & 1u) ^ 1u, abort_flag)) {
                         *abort_flag = 1;
                         break;
                     }
@@ -207,8 +259,8 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
                 }
                 tc_fence_after();
                 for (int kb = 0; kb < nk; ++kb, ++g) {
-                    const int s = g % MG_STAGES;
-                    if (!mbar_wait(smem_u32(full + s), (g / MG_STAGES) & 1u, abort_flag)) {
+                    const int s = g % C::STAGES;
+                    if (!mbar_wait(smem_u32(full + s), (g / C::STAGES) & 1u, abort_flag)) {
                         ok = false;
                         *abort_flag = 1;
                         break;
@@ -250,34 +302,33 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
                 break;
             }
             tc_fence_after();
-            auto release = [&]() {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(acce)) : "memory");
-            };
+            // into registers at once: the next tile's MMAs run while this one is converted and stored
+            uint32_t r[4][32];
             if (GLU) {
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t gr[32], ur[32];
-                    const int f = half * 64 + c * 32;
-                    TMEM_LD32(row + f, gr);
-                    TMEM_LD32(row + 128 + f, ur);
-                    tmem_wait_ld();
-                    if (c == 1) release();
-                    if (t < p.T) store_run<OUT>(p, t, tw * 128 + f, gr, ur);
+                TMEM_LD32(row + half * 64, r[0]);
+                TMEM_LD32(row + 128 + half * 64, r[1]);
+                TMEM_LD32(row + half * 64 + 32, r[2]);
+                TMEM_LD32(row + 128 + half * 64 + 32, r[3]);
+            } else {
+                TMEM_LD32(row + half * 128, r[0]);
+                TMEM_LD32(row + half * 128 + 32, r[1]);
+                TMEM_LD32(row + half * 128 + 64, r[2]);
+                TMEM_LD32(row + half * 128 + 96, r[3]);
+            }
+            tmem_wait_ld();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(acce)) : "memory");
+            if constexpr (GLU) {
+                if (t < p.T) {
+                    store_run<OUT>(p, t, tw * 128 + half * 64, r[0], r[1]);
+                    store_run<OUT>(p, t, tw * 128 + half * 64 + 32, r[2], r[3]);
                 }
             } else {
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t r[32];
-                    const int f = half * 128 + c * 32;
-                    TMEM_LD32(row + f, r);
-                    tmem_wait_ld();
-                    if (c == 3) release();
-                    if (t < p.T) store_row<OUT>(p, t, tw * 256 + f, r);
-                }
+                store_rows<OUT>(&tmO, p, boxes + warp * 2 * MG_OUT, t - lane, tw * 256 + half * 128, r);
             }
         }
+        if (!GLU && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
     tc_fence_before();
     __syncthreads();
@@ -315,6 +366,19 @@ bool encode(CUtensorMap* map, const qw_mx& m, bool spread, unsigned box) {
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Boxes of 32 rows by 128 bytes of an output.
+bool encode_out(CUtensorMap* map, void* out, int rows, int cols, size_t ld, int dtype) {
+    static const EncodeTiled enc = find_encode();
+    if (!enc) return false;
+    const cuuint64_t es = dtype == QW_F32 ? 4 : 2;
+    const cuuint64_t whole = std::max<cuuint64_t>(cols / (16 / es), 1) * (16 / es);  // 16-byte chunks
+    const cuuint64_t dims[2] = {whole, (cuuint64_t)rows}, strides[1] = {ld * es};
+    const cuuint32_t boxes[2] = {(cuuint32_t)(128 / es), 32}, steps[2] = {1, 1};
+    const CUtensorMapDataType type = dtype == QW_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16;
+    return enc(map, type, 2, out, dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int sm_count() {  // of the current device
     int dev = 0, n = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 1;
@@ -322,15 +386,16 @@ int sm_count() {  // of the current device
 }
 
 struct Maps {
-    CUtensorMap x, a, b;
+    CUtensorMap x, a, b, out;
 };
 
 template <int XB, int WB, int OUT>
 cudaError_t launch_gemm(const Maps& m, const MxGemmP& p, cudaStream_t st) {
-    const cudaError_t e = cudaFuncSetAttribute(k_mx_gemm<XB, WB, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, MG_SMEM);
+    constexpr int SMEM = MgCfg<OUT == 8 || OUT == 4>::SMEM;
+    const cudaError_t e = cudaFuncSetAttribute(k_mx_gemm<XB, WB, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return e;
-    return launch_k({st, true, nullptr}, k_mx_gemm<XB, WB, OUT>, dim3(std::min(p.units, sm_count())), dim3(MG_THREADS), MG_SMEM,
-                    m.x, m.a, m.b, p);
+    return launch_k({st, true, nullptr}, k_mx_gemm<XB, WB, OUT>, dim3(std::min(p.units, sm_count())), dim3(MG_THREADS), SMEM, m.x,
+                    m.a, m.b, m.out, p);
 }
 
 template <int OUT>
@@ -391,7 +456,8 @@ extern "C" qw_status qw_mx_linear(const qw_mx* x, const qw_mx* w, void* dev_out,
     if (too_many(x->rows, w->rows)) return qw_fail(QW_ERR_UNSUPPORTED, "%s: more than 2^31 tiles", what);
     MxGemmP p;
     Maps m;
-    if (!product(*x, *w, *w, false, dev_status, p, m)) return qw_fail(QW_ERR_CUDA, "%s: tensor map", what);
+    if (!product(*x, *w, *w, false, dev_status, p, m) || !encode_out(&m.out, dev_out, p.T, p.M, ld_out, dtype))
+        return qw_fail(QW_ERR_CUDA, "%s: tensor map", what);
     p.out = dev_out;
     p.ld = ld_out;
     const cudaStream_t st = (cudaStream_t)stream;
