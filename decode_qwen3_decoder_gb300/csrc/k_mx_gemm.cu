@@ -4,14 +4,15 @@
 // The MMA reads codes and exponents as they lie: kind::mxf8f6f4 (X in e4m3, W in e4m3 or e2m1, 32 columns an
 // instruction) or kind::mxf4 (both e2m1, 64 columns), products exact, sums in fp32 in tensor memory. Codes go
 // through a ring of TMA tiles with the 128-byte swizzle, 128 bytes a row; e2m1 codes that meet e4m3 are
-// spread to 8-byte halves of 16-byte chunks by the copy itself (16U4_ALIGN16B). The exponents' 512-byte
-// tiles come by bulk copy and go to tensor memory by tcgen05.cp, in columns of their ring stage: a
-// stage is refilled only after its MMAs, so no exponent is overwritten under an MMA.
+// spread to 8-byte halves of 16-byte chunks by the copy itself (16U4_ALIGN16B). The exponents' 512-byte tiles go
+// to tensor memory by tcgen05.cp, in columns of their ring stage: a stage is refilled only after its MMAs, so no
+// exponent is overwritten under an MMA.
 //
-// k_mx_gemm. Tile: 128 rows of X (the M of the MMA, a TMEM lane a row) by 256 of W (N): two neighbouring
-// tiles of 128 for the linear product; the same 128 features of gate and up for SwiGLU, so that a thread has
-// both of a feature, and the 32 features of a run, in its registers. Persistent; 8 epilogue warps, one
-// producer, one MMA issuer.
+// k_mx_gemm. A pair of CTAs on two SMs (tcgen05.mma.cta_group::2) has a tile of 256 rows of X (M; a TMEM lane a
+// row, 128 in each CTA) by 256 of W (N): two neighbouring tiles of 128 for the linear product; the same 128 features
+// of gate and up for SwiGLU, so that a thread has both of a feature, and the 32 features of a run, in its
+// registers. Each CTA loads its own 128 rows of X and one of the two W tiles, both the exponents of all of W.
+// Persistent; 8 epilogue warps, one producer, one MMA issuer (the leader's).
 //
 // Every wait is bounded (about 2 s): then QW_MX_TIMEOUT is set and the CTA frees its TMEM and ends.
 #include <algorithm>
@@ -21,26 +22,25 @@
 
 namespace {
 
-constexpr int MG_THREADS = 320;
-constexpr int MG_X = 128 * 128, MG_W = 128 * 128;  // bytes of an operand tile in shared memory
-constexpr int MG_SF = 1024;                        // exponents of an operand tile of a stage (two atoms for 4 by 4 bits)
-constexpr int MG_STAGE = MG_X + 2 * MG_W + 3 * MG_SF;
-constexpr int MG_OUT = 32 * 128;                   // staged output of an epilogue warp: 32 rows of 128 bytes
-// Linear: three stages and two staged boxes a warp; SwiGLU, whose output is small, stores from registers: four stages.
-template <bool GLU>
-struct MgCfg {
-    static constexpr int STAGES = GLU ? 4 : 3;
-    static constexpr int OUT = GLU ? 0 : 8 * 2 * MG_OUT;
-    static constexpr int SMEM = 1024 + STAGES * MG_STAGE + OUT + 256;
-};
+constexpr int MG_THREADS = 352;
+constexpr int MG_X = 128 * 128, MG_W = 128 * 128, MG_SF = 1024;  // bytes: operand tiles of a stage, exponents of 128 rows (two atoms)
+constexpr int MG_STAGE = MG_X + MG_W + 3 * MG_SF;
 constexpr int MG_SF_COL = 256, MG_SF_COLS = 32;  // TMEM columns of the exponents, a stage's
+// Linear: a warp stages its output in two boxes of 32 rows by 32 columns; SwiGLU's, which is small, is stored from registers.
+template <int OUT>
+struct MgCfg {
+    static constexpr bool GLU = OUT == 8 || OUT == 4;
+    static constexpr int BOX = GLU ? 0 : 32 * 32 * (OUT == QW_F32 ? 4 : 2);
+    static constexpr int STAGES = GLU ? 6 : OUT == QW_F32 ? 4 : 5;
+    static constexpr int SMEM = 1024 + STAGES * MG_STAGE + 16 * BOX + 256;
+    static_assert(SMEM <= 232448 && MG_SF_COL + STAGES * MG_SF_COLS <= 512, "shared or tensor memory");
+};
 
 struct MxGemmP {
     int T, M, atoms;  // rows of X, rows of W (of gate and of up), atoms of 128 columns
     int tiles_x, tiles_w, units;
-    const uint8_t *sx, *sa, *sb;  // exponents of X, of the tile's first and second W
-    int b_row;                    // first row of the second W, after the first's
-    int w_step;                   // W rows a tile
+    int b_row;   // first row of the tile's second W, after the first's
+    int w_step;  // W rows a tile
     void* out;  // linear's output, rows of ld elements
     size_t ld;
     uint8_t *codes, *scales;  // SwiGLU's output
@@ -48,34 +48,68 @@ struct MxGemmP {
     int32_t* status;
 };
 
+// A wait as in tc_sm103.cuh, but the thread sleeps until the phase completes: a warp that polls takes shared-memory
+// cycles from the MMAs, whose operands need nearly all of them.
+__device__ __forceinline__ bool try_sleep(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(1000000u)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+    if (try_sleep(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (!try_sleep(bar, parity))
+        if (*abort_flag || globaltimer_ns() - t0 > kTcWaitNs) return false;
+    return true;
+}
 __device__ __forceinline__ uint64_t sf_desc(uint32_t a) {  // no swizzle, 8-row groups of 16-byte rows 128 bytes apart
     return (uint64_t)((a & 0x3FFFFu) >> 4) | ((uint64_t)8 << 32) | ((uint64_t)1 << 46);
 }
-// 32 rows of 16 bytes to 32 lanes by 4 columns, in each of the four lane quarters.
+__device__ __forceinline__ uint32_t cta_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t map_to(uint32_t addr, uint32_t rank) {  // a shared address of this CTA in another's
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// 32 rows of 16 bytes to 32 lanes by 4 columns, in each of the four lane quarters; in each CTA of a pair from its own
+// shared memory.
+template <bool PAIR>
 __device__ __forceinline__ void sf_copy(uint32_t tmem, uint32_t smem) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(sf_desc(smem)) : "memory");
+    if (PAIR) asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(sf_desc(smem)) : "memory");
+    else asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(sf_desc(smem)) : "memory");
 }
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
-                 "r"(bytes), "r"(bar)
-                 : "memory");
+// One arrival at a barrier of this CTA when this thread's copies, of both CTAs of a pair, are complete.
+__device__ __forceinline__ void commit_here(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
-template <bool F4>
+#define MX_MMA(group, kind)                                                                                          \
+    asm volatile("{\n\t.reg .pred p;\n\t"                                                                            \
+                 "setp.ne.b32 p, %6, 0;\n\t"                                                                         \
+                 "tcgen05.mma.cta_group::" group ".kind::" kind " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),     \
+                 "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(acc)                                              \
+                 : "memory")
+template <bool F4, bool PAIR>
 __device__ __forceinline__ void mma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb, uint32_t acc) {
-    if (F4)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(acc)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(acc)
-            : "memory");
+    if (PAIR) {
+        if (F4) MX_MMA("2", "mxf4.block_scale.scale_vec::2X");
+        else MX_MMA("2", "mxf8f6f4.block_scale.scale_vec::1X");
+    } else {
+        if (F4) MX_MMA("1", "mxf4.block_scale.scale_vec::2X");
+        else MX_MMA("1", "mxf8f6f4.block_scale.scale_vec::1X");
+    }
 }
 // Instruction descriptor of the block-scaled kinds: exponent byte of B at bit 4 and of A at bit 29, formats of
 // A and B at 7 and 10 (mxf8f6f4: 0 e4m3, 5 e2m1; mxf4: 1 e2m1), N >> 3 at 17, ue8m0 scales at 23, M >> 4 at 24.
@@ -88,50 +122,43 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t sr
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"((uint64_t)map), "r"(x),
                  "r"(y), "r"(src)
                  : "memory");
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
-// A warp's 32 rows (a row a lane) of 128 sums, to columns f .. f + 127 of the output through two boxes in turn. A
-// lane's 16-byte chunks go to the places that the 128-byte swizzle gives them, which no two of 8 lanes share. A
-// copy clips whole 16-byte chunks only: the map ends at the last whole one, what is left of M goes element by element.
+// A warp's 32 rows (a row a lane) of 32 sums, to columns f .. f + 31 of the output. A lane's 16-byte chunks go to the
+// places that the copy's swizzle gives them (rows of 128 or 64 bytes), which no two of 8 lanes share. A copy clips
+// whole 16-byte chunks only: the map ends at the last whole one, what is left of M goes element by element. Every use of
+// a box, of the two that take turns, commits a group of copies.
 template <int DT>
-__device__ __forceinline__ void store_rows(const CUtensorMap* map, const MxGemmP& p, uint8_t* box, int t0, int f, uint32_t (*r)[32]) {
-    constexpr int PER = DT == QW_F32 ? 32 : 64, BOXES = 128 / PER;  // columns of a box
-    const int lane = threadIdx.x & 31;
-    if (t0 >= p.T) return;
+__device__ __forceinline__ void store_box(const CUtensorMap* map, const MxGemmP& p, uint8_t* two, uint32_t& uses, int t0, int f, const uint32_t* r) {
+    constexpr int ES = DT == QW_F32 ? 4 : 2, ROW = 32 * ES;
+    const int lane = threadIdx.x & 31, turn = DT == QW_F32 ? lane & 7 : (lane >> 1) & 3;
+    if (t0 >= p.T || f >= p.M) return;
+    uint8_t* box = two + (uses++ & 1) * 32 * ROW;
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // the box before last has been read
+    __syncwarp();
 #pragma unroll
-    for (int b = 0; b < BOXES; ++b) {
-        if (f + b * PER >= p.M) break;
-        uint8_t* at = box + (b & 1) * MG_OUT;
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // the box before last has been read
-        __syncwarp();
+    for (int c = 0; c < ROW / 16; ++c) {
+        uint32_t w[4];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            uint32_t w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if (DT == QW_F32) {
-                    w[k] = r[b][4 * c + k];
-                } else {
-                    const uint32_t* v = r[2 * b + c / 4] + (c % 4) * 8 + 2 * k;
-                    w[k] = mx_pack2<DT>(__uint_as_float(v[0]), __uint_as_float(v[1]));
-                }
-            }
-            *reinterpret_cast<uint4*>(at + lane * 128 + ((c ^ (lane & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        const int whole = p.M & ~(PER / 8 - 1), x0 = f + b * PER;
-        if (lane == 0 && x0 < whole) tma_store_2d(map, smem_u32(at), x0, t0);
-        if (t0 + lane < p.T)
-            for (int x = max(whole, x0); x < min(p.M, x0 + PER); ++x) {
-                const int e = x - x0, es = 128 / PER;
-                const uint8_t* from = at + lane * 128 + ((e * es / 16 ^ (lane & 7)) * 16) + e * es % 16;
-                const size_t to = (size_t)(t0 + lane) * p.ld + x;
-                if (DT == QW_F32) reinterpret_cast<float*>(p.out)[to] = *reinterpret_cast<const float*>(from);
-                else reinterpret_cast<uint16_t*>(p.out)[to] = *reinterpret_cast<const uint16_t*>(from);
-            }
+        for (int k = 0; k < 4; ++k)
+            w[k] = DT == QW_F32 ? r[4 * c + k] : mx_pack2<DT>(__uint_as_float(r[(8 * c + 2 * k) & 31]), __uint_as_float(r[(8 * c + 2 * k + 1) & 31]));
+        *reinterpret_cast<uint4*>(box + lane * ROW + (c ^ turn) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
     }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    const int whole = p.M & ~(16 / ES - 1);
+    if (lane == 0) {
+        if (f < whole) tma_store_2d(map, smem_u32(box), f, t0);
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
+    if (t0 + lane < p.T)
+        for (int x = max(whole, f); x < min(p.M, f + 32); ++x) {
+            const int b = (x - f) * ES;
+            const uint8_t* from = box + lane * ROW + ((b / 16) ^ turn) * 16 + b % 16;
+            const size_t to = (size_t)(t0 + lane) * p.ld + x;
+            if (DT == QW_F32) reinterpret_cast<float*>(p.out)[to] = *reinterpret_cast<const float*>(from);
+            else reinterpret_cast<uint16_t*>(p.out)[to] = *reinterpret_cast<const uint16_t*>(from);
+        }
 }
 
 // silu(g) u. exp and the division in their fast forms: 2^-20 relative at most, where a code has 4 bits.
@@ -169,51 +196,62 @@ __device__ __forceinline__ void store_run(const MxGemmP& p, int t, int f, const 
     p.scales[mx_scale_word(t, f / MX_ATOM, p.oatoms) + (f / MX_RUN & 3)] = (uint8_t)byte;
 }
 
+struct MgMaps {
+    CUtensorMap x, a, b;     // codes of X, of the tile's first and second W: boxes of 128 rows
+    CUtensorMap sx, sa, sb;  // their exponents: boxes of the 512-byte tiles of a stage
+    CUtensorMap out;         // boxes of 32 rows by 32 columns
+};
+
 // OUT: QW_F16, QW_BF16, QW_F32 (linear); 8, 4 (SwiGLU with codes of so many bits).
 template <int XB, int WB, int OUT>
-__global__ void __launch_bounds__(MG_THREADS, 1)
-    k_mx_gemm(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmA,
-              const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmO,
-              const __grid_constant__ MxGemmP p) {
-    constexpr bool F4 = XB == 4, GLU = OUT == 8 || OUT == 4;
-    using C = MgCfg<GLU>;
-    constexpr int AT = F4 ? 2 : 1;                                     // atoms of 128 columns a stage
-    constexpr uint32_t W_TX = WB == 4 && !F4 ? MG_W / 2 : MG_W;        // a spread tile counts its bytes in memory
+__global__ void __launch_bounds__(MG_THREADS, 1) k_mx_gemm(const __grid_constant__ MgMaps m, const __grid_constant__ MxGemmP p) {
+    constexpr bool F4 = XB == 4;
+    using C = MgCfg<OUT>;
+    constexpr bool GLU = C::GLU;
+    constexpr int AT = F4 ? 2 : 1;                               // atoms of 128 columns a stage
+    constexpr uint32_t W_TX = WB == 4 && !F4 ? MG_W / 2 : MG_W;  // a spread tile counts its bytes in memory
+    constexpr uint32_t TX = 2 * (MG_X + W_TX + 3 * AT * MX_TILE_BYTES);  // both CTAs' copies of a stage
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     uint8_t* boxes = smem + C::STAGES * MG_STAGE;
-    uint64_t* full = reinterpret_cast<uint64_t*>(boxes + C::OUT);
+    uint64_t* full = reinterpret_cast<uint64_t*>(boxes + 16 * C::BOX);
     uint64_t* empty = full + C::STAGES;
-    uint64_t* accf = empty + C::STAGES;
+    uint64_t* sready = empty + C::STAGES;  // the stage's exponents are in tensor memory (the leader's)
+    uint64_t* accf = sready + C::STAGES;
     uint64_t* acce = accf + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acce + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = (int)cta_rank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     const int nk = (p.atoms + AT - 1) / AT;  // stages a tile
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(smem_u32(full + s), 1);
             mbar_init(smem_u32(empty + s), 1);
+            mbar_init(smem_u32(sready + s), 1);
         }
         mbar_init(smem_u32(accf), 1);
-        mbar_init(smem_u32(acce), 8);
+        mbar_init(smem_u32(acce), 16);  // the epilogue warps of both CTAs
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     if (warp == 8 && lane == 0) {
-        tma_prefetch_desc(&tmX);
-        tma_prefetch_desc(&tmA);
-        tma_prefetch_desc(&tmB);
-        if (!GLU) tma_prefetch_desc(&tmO);
+        tma_prefetch_desc(&m.x);
+        tma_prefetch_desc(rank ? &m.b : &m.a);
+        tma_prefetch_desc(&m.sx);
+        tma_prefetch_desc(&m.sa);
+        tma_prefetch_desc(&m.sb);
+        if (!GLU) tma_prefetch_desc(&m.out);
     }
     if (warp == 9) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot)) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     tc_fence_before();
     __syncthreads();
+    cluster_sync();  // the peer's copies complete on the leader's barriers
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     pdl_wait();
@@ -222,58 +260,50 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
     if (warp == 8) {
         if (lane == 0) {
             uint32_t g = 0;
-            for (int u = blockIdx.x; u < p.units && !*abort_flag; u += gridDim.x) {
-                const int tw = u % p.tiles_w, tx = u / p.tiles_w;
+            for (int u = pair; u < p.units && !*abort_flag; u += pairs) {
+                const int tw = u % p.tiles_w, tx = 2 * (u / p.tiles_w) + rank;  // tiles of 128 rows of X
                 const int wa = tw * p.w_step, wb = wa + p.b_row;
-                const bool two = wb < p.M;  // the second tile of W has rows
                 for (int kb = 0; kb < nk; ++kb, ++g) {
                     const int s = g % C::STAGES;
-                    if (!mbar_wait(smem_u32(empty + s), ((g / C::STAGES) & 1u) ^ 1u, abort_flag)) {
+                    if (!wait_phase(smem_u32(empty + s), ((g / C::STAGES) & 1u) ^ 1u, abort_flag)) {
                         *abort_flag = 1;
                         break;
                     }
-                    const uint32_t st = smem_u32(smem + s * MG_STAGE), bar = smem_u32(full + s);
-                    const uint32_t sf = (uint32_t)min(AT, p.atoms - kb * AT) * MX_TILE_BYTES;
-                    mbar_expect_tx(bar, MG_X + 2 * W_TX + sf * (two ? 3 : 2));
-                    tma_load_2d(st, &tmX, bar, kb * 128, tx * 128);
-                    tma_load_2d(st + MG_X, &tmA, bar, kb * 128, wa);
-                    tma_load_2d(st + MG_X + MG_W, &tmB, bar, kb * 128, wb);
-                    const uint32_t sfs = st + MG_X + 2 * MG_W;
-                    bulk_load(sfs, p.sx + ((size_t)tx * p.atoms + kb * AT) * MX_TILE_BYTES, sf, bar);
-                    bulk_load(sfs + MG_SF, p.sa + ((size_t)(wa >> 7) * p.atoms + kb * AT) * MX_TILE_BYTES, sf, bar);
-                    if (two) bulk_load(sfs + 2 * MG_SF, p.sb + ((size_t)(wb >> 7) * p.atoms + kb * AT) * MX_TILE_BYTES, sf, bar);
+                    const uint32_t st = smem_u32(smem + s * MG_STAGE), sf = st + MG_X + MG_W, bar = map_to(smem_u32(full + s), 0);
+                    if (rank == 0) mbar_expect_tx(smem_u32(full + s), TX);
+                    // rows and tiles past a matrix's end arrive as zeros
+                    tma_load_2d_pair(st, &m.x, bar, kb * 128, tx * 128);
+                    tma_load_2d_pair(st + MG_X, rank ? &m.b : &m.a, bar, kb * 128, rank ? wb : wa);
+                    tma_load_2d_pair(sf, &m.sx, bar, 0, tx * p.atoms + kb * AT);
+                    tma_load_2d_pair(sf + MG_SF, &m.sa, bar, 0, (wa >> 7) * p.atoms + kb * AT);
+                    tma_load_2d_pair(sf + 2 * MG_SF, &m.sb, bar, 0, (wb >> 7) * p.atoms + kb * AT);
                 }
             }
         }
         __syncwarp();
     } else if (warp == 9) {
-        if (lane == 0) {
-            constexpr uint32_t idesc = idesc_mx(F4 ? 1 : 0, F4 ? 1 : WB == 4 ? 5 : 0, 128, 256);
+        if (lane == 0 && rank == 0) {
+            constexpr uint32_t idesc = idesc_mx(F4 ? 1 : 0, F4 ? 1 : WB == 4 ? 5 : 0, 256, 256);
             uint32_t g = 0;
             int i = 0;
             bool ok = true;
-            for (int u = blockIdx.x; u < p.units && ok; u += gridDim.x, ++i) {
-                if (!mbar_wait(smem_u32(acce), ((uint32_t)i & 1u) ^ 1u, abort_flag)) {
+            for (int u = pair; u < p.units && ok; u += pairs, ++i) {
+                if (!wait_phase(smem_u32(acce), ((uint32_t)i & 1u) ^ 1u, abort_flag)) {
                     *abort_flag = 1;
                     break;
                 }
                 tc_fence_after();
                 for (int kb = 0; kb < nk; ++kb, ++g) {
                     const int s = g % C::STAGES;
-                    if (!mbar_wait(smem_u32(full + s), (g / C::STAGES) & 1u, abort_flag)) {
+                    if (!wait_phase(smem_u32(sready + s), (g / C::STAGES) & 1u, abort_flag)) {
                         ok = false;
                         *abort_flag = 1;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t st = smem_u32(smem + s * MG_STAGE), sfs = st + MG_X + 2 * MG_W;
+                    const uint32_t st = smem_u32(smem + s * MG_STAGE);
                     const uint32_t ta = tmem + MG_SF_COL + s * MG_SF_COLS, tb = ta + 8;
                     const int at = min(AT, p.atoms - kb * AT);
-                    for (int a = 0; a < at; ++a) {
-                        sf_copy(ta + 4 * a, sfs + a * MX_TILE_BYTES);
-                        sf_copy(tb + 8 * a, sfs + MG_SF + a * MX_TILE_BYTES);
-                        sf_copy(tb + 8 * a + 4, sfs + 2 * MG_SF + a * MX_TILE_BYTES);
-                    }
                     const uint64_t ad = sw128_desc(st), bd = sw128_desc(st + MG_X);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
@@ -281,11 +311,33 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
                         const int a = F4 ? k / 2 : 0;
                         const uint32_t id = F4 ? (uint32_t)(k & 1) * 2 : (uint32_t)k;
                         if (a < at)
-                            mma_mx<F4>(tmem, ad + 2 * k, bd + 2 * k, idesc | (id << 4) | (id << 29), ta + 4 * a, tb + 8 * a, kb > 0 || k > 0);
+                            mma_mx<F4, true>(tmem, ad + 2 * k, bd + 2 * k, idesc | (id << 4) | (id << 29), ta + 4 * a, tb + 8 * a, kb > 0 || k > 0);
                     }
-                    umma_commit(smem_u32(empty + s));
+                    umma_commit_pair(smem_u32(empty + s));
                 }
-                if (ok) umma_commit(smem_u32(accf));
+                if (ok) umma_commit_pair(smem_u32(accf));
+            }
+        }
+        __syncwarp();
+    } else if (warp == 10) {
+        // exponents to tensor memory, in a thread of its own: a thread's waits for shared memory stand behind its copies
+        if (lane == 0 && rank == 0) {
+            const uint32_t total = (uint32_t)((p.units - pair + pairs - 1) / pairs) * nk;
+            for (uint32_t g = 0; g < total; ++g) {
+                const int s = g % C::STAGES;
+                if (!wait_phase(smem_u32(full + s), (g / C::STAGES) & 1u, abort_flag)) {
+                    *abort_flag = 1;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t sf = smem_u32(smem + s * MG_STAGE) + MG_X + MG_W, to = tmem + MG_SF_COL + s * MG_SF_COLS;
+#pragma unroll
+                for (int a = 0; a < AT; ++a) {
+                    sf_copy<true>(to + 4 * a, sf + a * MX_TILE_BYTES);
+                    sf_copy<true>(to + 8 + 8 * a, sf + MG_SF + a * MX_TILE_BYTES);
+                    sf_copy<true>(to + 8 + 8 * a + 4, sf + 2 * MG_SF + a * MX_TILE_BYTES);
+                }
+                commit_here(smem_u32(sready + s));
             }
         }
         __syncwarp();
@@ -293,11 +345,15 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
         // warps w and w + 4 read the lanes 32 (w % 4) ..: the first half of the features and the second
         const int half = warp >> 2;
         const uint32_t row = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t free_bar = map_to(smem_u32(acce), 0);
+        uint32_t uses = 0;
         int i = 0;
-        for (int u = blockIdx.x; u < p.units; u += gridDim.x, ++i) {
-            const int tw = u % p.tiles_w, tx = u / p.tiles_w;
+        for (int u = pair; u < p.units; u += pairs, ++i) {
+            const int tw = u % p.tiles_w, tx = 2 * (u / p.tiles_w) + rank;
             const int t = tx * 128 + (warp & 3) * 32 + lane;
-            if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(accf), (uint32_t)i & 1u, abort_flag))) {
+            int ok = 0;
+            if (lane == 0) ok = wait_phase(smem_u32(accf), (uint32_t)i & 1u, abort_flag);
+            if (!__shfl_sync(0xffffffffu, ok, 0)) {
                 *abort_flag = 1;
                 break;
             }
@@ -318,14 +374,17 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
             tmem_wait_ld();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(acce)) : "memory");
+            // only tensor memory is handed over, which the tcgen05 fences order: a release of all memory would take 0.4 us
+            if (lane == 0) asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(free_bar) : "memory");
             if constexpr (GLU) {
                 if (t < p.T) {
                     store_run<OUT>(p, t, tw * 128 + half * 64, r[0], r[1]);
                     store_run<OUT>(p, t, tw * 128 + half * 64 + 32, r[2], r[3]);
                 }
             } else {
-                store_rows<OUT>(&tmO, p, boxes + warp * 2 * MG_OUT, t - lane, tw * 256 + half * 128, r);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    store_box<OUT>(&m.out, p, boxes + 2 * warp * C::BOX, uses, t - lane, tw * 256 + half * 128 + 32 * k, r[k]);
             }
         }
         if (!GLU && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -333,9 +392,10 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == 0 && *abort_flag) atomicOr(p.status, QW_MX_TIMEOUT);
+    cluster_sync();  // no copy, MMA or arrival of the pair still targets this CTA
     if (warp == 9) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }
 }
 
@@ -366,17 +426,28 @@ bool encode(CUtensorMap* map, const qw_mx& m, bool spread, unsigned box) {
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Boxes of 32 rows by 128 bytes of an output.
+// A stage's exponents: `box` of the 512-byte tiles.
+bool encode_scales(CUtensorMap* map, const qw_mx& m, unsigned box) {
+    static const EncodeTiled enc = find_encode();
+    if (!enc) return false;
+    const cuuint64_t tiles = ((cuuint64_t)m.rows + 127) / 128 * mx_atoms(m.cols);
+    const cuuint64_t dims[2] = {MX_TILE_BYTES / 4, tiles}, strides[1] = {MX_TILE_BYTES};
+    const cuuint32_t boxes[2] = {MX_TILE_BYTES / 4, box}, es[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, m.dev_scales, dims, strides, boxes, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Boxes of 32 rows by 32 columns of an output.
 bool encode_out(CUtensorMap* map, void* out, int rows, int cols, size_t ld, int dtype) {
     static const EncodeTiled enc = find_encode();
     if (!enc) return false;
     const cuuint64_t es = dtype == QW_F32 ? 4 : 2;
     const cuuint64_t whole = std::max<cuuint64_t>(cols / (16 / es), 1) * (16 / es);  // 16-byte chunks
     const cuuint64_t dims[2] = {whole, (cuuint64_t)rows}, strides[1] = {ld * es};
-    const cuuint32_t boxes[2] = {(cuuint32_t)(128 / es), 32}, steps[2] = {1, 1};
+    const cuuint32_t boxes[2] = {32, 32}, steps[2] = {1, 1};
     const CUtensorMapDataType type = dtype == QW_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16;
-    return enc(map, type, 2, out, dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return enc(map, type, 2, out, dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               es == 4 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int sm_count() {  // of the current device
@@ -385,21 +456,17 @@ int sm_count() {  // of the current device
     return n;
 }
 
-struct Maps {
-    CUtensorMap x, a, b, out;
-};
-
 template <int XB, int WB, int OUT>
-cudaError_t launch_gemm(const Maps& m, const MxGemmP& p, cudaStream_t st) {
-    constexpr int SMEM = MgCfg<OUT == 8 || OUT == 4>::SMEM;
+cudaError_t launch_gemm(const MgMaps& m, const MxGemmP& p, cudaStream_t st) {
+    constexpr int SMEM = MgCfg<OUT>::SMEM;
     const cudaError_t e = cudaFuncSetAttribute(k_mx_gemm<XB, WB, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return e;
-    return launch_k({st, true, nullptr}, k_mx_gemm<XB, WB, OUT>, dim3(std::min(p.units, sm_count())), dim3(MG_THREADS), SMEM, m.x,
-                    m.a, m.b, m.out, p);
+    return launch_kc({st, true, nullptr}, k_mx_gemm<XB, WB, OUT>, dim3(2 * std::min(p.units, sm_count() / 2)), dim3(MG_THREADS),
+                     SMEM, 2, m, p);
 }
 
 template <int OUT>
-cudaError_t launch_formats(int xb, int wb, const Maps& m, const MxGemmP& p, cudaStream_t st) {
+cudaError_t launch_formats(int xb, int wb, const MgMaps& m, const MxGemmP& p, cudaStream_t st) {
     return xb == 4   ? launch_gemm<4, 4, OUT>(m, p, st)
            : wb == 4 ? launch_gemm<8, 4, OUT>(m, p, st)
                      : launch_gemm<8, 8, OUT>(m, p, st);
@@ -413,22 +480,22 @@ qw_status formats_check(const qw_mx* x, const qw_mx* w, const char* what) {
 }
 
 // Parameters and tensor maps that both products share; wb: the tiles' second matrix (linear: w itself).
-bool product(const qw_mx& x, const qw_mx& wa, const qw_mx& wb, bool glu, int32_t* status, MxGemmP& p, Maps& m) {
+bool product(const qw_mx& x, const qw_mx& wa, const qw_mx& wb, bool glu, int32_t* status, MxGemmP& p, MgMaps& m) {
     p = MxGemmP{};
     p.T = x.rows;
     p.M = wa.rows;
     p.atoms = (int)mx_atoms(x.cols);
+    p.oatoms = (int)mx_atoms(wa.rows);
     p.w_step = glu ? 128 : 256;
     p.b_row = glu ? 0 : 128;
-    p.tiles_x = (int)(((long long)p.T + 127) / 128);
+    p.tiles_x = (int)(((long long)p.T + 255) / 256);
     p.tiles_w = (int)(((long long)p.M + p.w_step - 1) / p.w_step);
     p.units = p.tiles_x * p.tiles_w;
-    p.sx = (const uint8_t*)x.dev_scales;
-    p.sa = (const uint8_t*)wa.dev_scales;
-    p.sb = (const uint8_t*)wb.dev_scales;
     p.status = status;
     const bool spread = wa.bits == 4 && x.bits == 8;
-    return encode(&m.x, x, false, 128) && encode(&m.a, wa, spread, 128) && encode(&m.b, wb, spread, 128);
+    const unsigned at = x.bits == 4 ? 2 : 1;
+    return encode(&m.x, x, false, 128) && encode(&m.a, wa, spread, 128) && encode(&m.b, wb, spread, 128) &&
+           encode_scales(&m.sx, x, at) && encode_scales(&m.sa, wa, at) && encode_scales(&m.sb, wb, at);
 }
 
 qw_status done(cudaError_t e, const char* what) {
@@ -436,7 +503,7 @@ qw_status done(cudaError_t e, const char* what) {
 }
 
 // Tiles are numbered in an int.
-bool too_many(int T, int M) { return (double)(T / 128 + 1) * (M / 128 + 1) > 2147483647.0; }
+bool too_many(int T, int M) { return (double)(T / 256 + 1) * (M / 128 + 1) > 2147483647.0; }
 
 }  // namespace
 
@@ -455,7 +522,7 @@ extern "C" qw_status qw_mx_linear(const qw_mx* x, const qw_mx* w, void* dev_out,
         return qw_fail(QW_ERR_INVALID_ARG, "%s: rows of out not 16-byte aligned", what);
     if (too_many(x->rows, w->rows)) return qw_fail(QW_ERR_UNSUPPORTED, "%s: more than 2^31 tiles", what);
     MxGemmP p;
-    Maps m;
+    MgMaps m;
     if (!product(*x, *w, *w, false, dev_status, p, m) || !encode_out(&m.out, dev_out, p.T, p.M, ld_out, dtype))
         return qw_fail(QW_ERR_CUDA, "%s: tensor map", what);
     p.out = dev_out;
@@ -484,11 +551,10 @@ extern "C" qw_status qw_mx_swiglu(const qw_mx* x, const qw_mx* w_gate, const qw_
     if (x->rows == 0) return QW_OK;
     if (too_many(x->rows, w_gate->rows)) return qw_fail(QW_ERR_UNSUPPORTED, "%s: more than 2^31 tiles", what);
     MxGemmP p;
-    Maps m;
+    MgMaps m;
     if (!product(*x, *w_gate, *w_up, true, dev_status, p, m)) return qw_fail(QW_ERR_CUDA, "%s: tensor map", what);
     p.codes = (uint8_t*)out->dev_codes;
     p.scales = (uint8_t*)out->dev_scales;
-    p.oatoms = (int)mx_atoms(out->cols);
     const cudaStream_t st = (cudaStream_t)stream;
     return done(out->bits == 8 ? launch_formats<8>(x->bits, w_gate->bits, m, p, st) : launch_formats<4>(x->bits, w_gate->bits, m, p, st),
                 what);
