@@ -161,19 +161,28 @@ __device__ __forceinline__ void store_box(const CUtensorMap* map, const MxGemmP&
         }
 }
 
-// silu(g) u. exp and the division in their fast forms: 2^-20 relative at most, where a code has 4 bits.
-__device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.f + __expf(-g)) * u; }
+// silu(g) u = g u / (1 + 2^(-g log2 e)). The hardware's exponential and reciprocal: 2^-20 relative at most, where a
+// code has 4 bits.
+__device__ __forceinline__ float silu_mul(float g, float u) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.44269504f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return g * r * u;
+}
 
 // A thread's run of 32 features of row t: codes and exponent. Features from M on are zeros.
 template <int BITS>
 __device__ __forceinline__ void store_run(const MxGemmP& p, int t, int f, const uint32_t* g, const uint32_t* u) {
     float h[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) h[i] = silu_mul(__uint_as_float(g[i]), __uint_as_float(u[i]));
+    if (f + 32 > p.M) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) h[i] = f + i < p.M ? h[i] : 0.f;
+    }
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        h[i] = f + i < p.M ? silu_mul(__uint_as_float(g[i]), __uint_as_float(u[i])) : 0.f;
-        m = max(m, __float_as_uint(h[i]) & 0x7FFFFFFFu);
-    }
+    for (int i = 0; i < 32; ++i) m = max(m, __float_as_uint(h[i]) & 0x7FFFFFFFu);
     const int byte = mx_exp_byte<BITS>(m);
     const float inv = mx_inv_scale(byte);
 #pragma unroll
