@@ -3,14 +3,15 @@
 //
 // Quantise and read. A thread has 8 columns, four a run, sixteen a row's scale word. The exponent follows
 // from the largest magnitude alone and x 2^-e is exact, so the codes are those of the definition bit for
-// bit. Bytes bound both.
+// bit. Bytes bound both: a warp of a large matrix asks for four pieces of 256 columns before it uses one.
 //
 // RMSNorm. s = x + add rounded to the stream's type, y = s / sqrt(mean(s^2) + eps) * w, codes of y. y has no
-// type of its own: the codes are those of the real y, whatever the order of the sums. To that end the row's
-// sum of squares is carried as an unevaluated pair of floats (the products' and sums' errors are added up;
-// about 2^-45 relative), y is computed in fp32 with a relative error below 2^-21, and a run in which a value
-// between y (1 - 2^-20) and y (1 + 2^-20) could get another code or exponent, one in 1500, is computed again
-// in fp64 from the pair. One CTA a row; a row's elements stay in registers between the two passes.
+// type of its own: the codes are those of the real y, whatever the order of the sums. y is computed in fp32 with a
+// relative error d below 18 2^-24; a run in which a value between y (1 - d) and y (1 + d) could get another code or
+// exponent, one in 1300, is computed again: the row's sum of squares as an unevaluated pair of floats (the
+// products' and sums' errors are added up; about 2^-45 relative), 1 / sqrt and the products as pairs. Pairs
+// for every value would cost twice the instructions, which then bound the kernel. One CTA a row; a row's elements stay
+// in registers between the passes.
 #include <algorithm>
 
 #include "mx.cuh"
@@ -26,6 +27,16 @@ __device__ __forceinline__ uint32_t mx_gather_word(int byte) {
     return w | (__shfl_down_sync(0xffffffffu, w, 8) << 16);
 }
 
+// A warp's pieces of 256 columns in row order: one division, then steps.
+struct Piece {
+    int row, c;  // this lane's first column
+    __device__ __forceinline__ Piece(unsigned u, unsigned per_row, int lane) : row((int)(u / per_row)), c((int)(u % per_row) * 256 + lane * 8) {}
+    __device__ __forceinline__ void next(unsigned per_row, int lane) {
+        c += 256;
+        if (c >= (int)per_row * 256) c = lane * 8, ++row;
+    }
+};
+
 struct MxRowsP {
     uint8_t* codes;
     uint8_t* scales;
@@ -36,59 +47,90 @@ struct MxRowsP {
     unsigned units, per_row;  // warps' pieces of 256 columns
 };
 
-template <int DT, int BITS>
+// U neighbouring pieces a warp.
+template <int DT, int BITS, int U>
 __global__ void __launch_bounds__(MQ_WARPS * 32) k_mx_quantize(const __grid_constant__ MxRowsP p) {
     pdl_wait();
     pdl_launch();
-    const unsigned u = blockIdx.x * MQ_WARPS + (threadIdx.x >> 5);
-    if (u >= p.units) return;
-    const int lane = threadIdx.x & 31, row = (int)(u / p.per_row), c = (int)(u % p.per_row) * 256 + lane * 8;
-    float x[8];
-    mx_load8<DT>(p.src, (size_t)row * p.ld + c, p.cols - c, x);
-    uint32_t m = 0;
+    const unsigned u0 = (blockIdx.x * MQ_WARPS + (threadIdx.x >> 5)) * U;
+    const int lane = threadIdx.x & 31;
+    const Piece first(u0, p.per_row, lane);
+    Piece t = first;
+    MxRaw raw[U];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    const int byte = mx_exp_byte<BITS>(m);
-    const float inv = mx_inv_scale(byte);
+    for (int k = 0; k < U; ++k) {
+        raw[k] = mx_fetch8<DT>(p.src, (size_t)t.row * p.ld + t.c, u0 + k < p.units ? p.cols - t.c : 0);
+        t.next(p.per_row, lane);
+    }
+    t = first;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] *= inv;
-    uint32_t w[2];
-    mx_enc8<BITS>(x, w);
-    const uint32_t sw = mx_gather_word(byte);
-    if (c >= p.atoms * MX_ATOM) return;
-    uint8_t* at = p.codes + (size_t)row * p.atoms * (MX_ATOM * BITS / 8) + (size_t)c * BITS / 8;
-    if (BITS == 8) *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
-    else *reinterpret_cast<uint32_t*>(at) = w[0];
-    if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(p.scales + mx_scale_word(row, c / MX_ATOM, p.atoms)) = sw;
+    for (int k = 0; k < U; ++k) {
+        mx_fill8<DT>(p.src, (size_t)t.row * p.ld + t.c, u0 + k < p.units ? p.cols - t.c : 0, raw[k]);
+        uint32_t m = mx_absmax8<DT>(raw[k]);
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        const int byte = mx_exp_byte<BITS>(m);
+        const float inv = mx_inv_scale(byte);
+        float x[8];
+        mx_unpack8<DT>(raw[k], x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] *= inv;
+        uint32_t w[2];
+        mx_enc8<BITS>(x, w);
+        const uint32_t sw = mx_gather_word(byte);
+        if (u0 + k < p.units && t.c < p.atoms * MX_ATOM) {
+            uint8_t* at = p.codes + (size_t)t.row * p.atoms * (MX_ATOM * BITS / 8) + (size_t)t.c * BITS / 8;
+            if (BITS == 8) *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
+            else *reinterpret_cast<uint32_t*>(at) = w[0];
+            if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(p.scales + mx_scale_word(t.row, t.c / MX_ATOM, p.atoms)) = sw;
+        }
+        t.next(p.per_row, lane);
+    }
 }
 
-template <int DT, int BITS>
+template <int DT, int BITS, int U>
 __global__ void __launch_bounds__(MQ_WARPS * 32) k_mx_read(const __grid_constant__ MxRowsP p) {
     pdl_wait();
     pdl_launch();
-    const unsigned u = blockIdx.x * MQ_WARPS + (threadIdx.x >> 5);
-    if (u >= p.units) return;
-    const int lane = threadIdx.x & 31, row = (int)(u / p.per_row), c = (int)(u % p.per_row) * 256 + lane * 8;
-    if (c >= p.cols) return;
-    const uint8_t* at = p.codes + (size_t)row * p.atoms * (MX_ATOM * BITS / 8) + (size_t)c * BITS / 8;
-    uint32_t w[2], h[4];
-    if (BITS == 8) {
-        const uint2 v = *reinterpret_cast<const uint2*>(at);
-        w[0] = v.x, w[1] = v.y;
-    } else {
-        w[0] = *reinterpret_cast<const uint32_t*>(at);
-    }
-    const float s = mx_scale(p.scales[mx_scale_word(row, c / MX_ATOM, p.atoms) + (c / MX_RUN & 3)]);
-    mx_dec8<BITS>(w, h);
-    float x[8];
+    const unsigned u0 = (blockIdx.x * MQ_WARPS + (threadIdx.x >> 5)) * U;
+    const int lane = threadIdx.x & 31;
+    const Piece first(u0, p.per_row, lane);
+    Piece t = first;
+    uint32_t w[U][2];
+    uint8_t e[U];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = h_lo(h[i]) * s;
-        x[2 * i + 1] = h_hi(h[i]) * s;
+    for (int k = 0; k < U; ++k) {
+        w[k][0] = w[k][1] = 0;
+        e[k] = 0;
+        if (u0 + k < p.units && t.c < p.cols) {
+            const uint8_t* at = p.codes + (size_t)t.row * p.atoms * (MX_ATOM * BITS / 8) + (size_t)t.c * BITS / 8;
+            if (BITS == 8) {
+                const uint2 v = *reinterpret_cast<const uint2*>(at);
+                w[k][0] = v.x, w[k][1] = v.y;
+            } else {
+                w[k][0] = *reinterpret_cast<const uint32_t*>(at);
+            }
+            e[k] = p.scales[mx_scale_word(t.row, t.c / MX_ATOM, p.atoms) + (t.c / MX_RUN & 3)];
+        }
+        t.next(p.per_row, lane);
     }
-    mx_store8<DT>(p.dst, (size_t)row * p.ld + c, p.cols - c, x);
+    t = first;
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        if (u0 + k < p.units && t.c < p.cols) {
+            uint32_t h[4];
+            mx_dec8<BITS>(w[k], h);
+            const float s = mx_scale(e[k]);
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[2 * i] = h_lo(h[i]) * s;
+                x[2 * i + 1] = h_hi(h[i]) * s;
+            }
+            mx_store8<DT>(p.dst, (size_t)t.row * p.ld + t.c, p.cols - t.c, x);
+        }
+        t.next(p.per_row, lane);
+    }
 }
 
 // ---- RMSNorm --------------------------------------------------------------------------------------------
@@ -104,6 +146,7 @@ struct MxNormP {
     size_t ld_x, ld_add, ld_sum;
     int dt_add;  // QW_F16, QW_BF16, QW_F32 or -1
     float eps;
+    double inv_n;  // 1 / cols
 };
 
 // A sum as an unevaluated pair: hi + lo.
@@ -134,47 +177,40 @@ __device__ __forceinline__ float round_to(float v) {
     return v;
 }
 
-// A double to the float that rounds like it to fewer bits: towards zero, the last bit set if inexact.
+// hi + lo to the float that rounds like it to fewer bits: towards zero, the last bit set if inexact. |lo| is at most
+// half a unit of hi's last place.
+__device__ __forceinline__ float to_odd(Pair t) {
+    if (t.lo == 0.f) return t.hi;
+    const uint32_t u = __float_as_uint(t.hi);
+    return __uint_as_float(((t.lo < 0.f) != (t.hi < 0.f) ? u - 1 : u) | 1u);
+}
 __device__ __forceinline__ float to_odd(double t) {
     const float f = __double2float_rz(t);
     return (double)f == t ? f : __uint_as_float(__float_as_uint(f) | 1u);
 }
 
-// The run's exponent byte and this thread's codes in fp64 (the four lanes of a run together).
-template <int BITS>
-__device__ __noinline__ int norm_exact(const float* s, const float* w, double rstd, uint32_t mask, uint32_t* codes) {
-    double y[8], m = 0.0;
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        y[i] = (double)s[i] * rstd * (double)w[i];
-        bad |= !(fabs(y[i]) <= 3.4028234663852886e38);
-        m = fmax(m, fabs(y[i]));
-    }
-    m = fmax(m, __shfl_xor_sync(mask, m, 1));
-    m = fmax(m, __shfl_xor_sync(mask, m, 2));
-    bad = __any_sync(mask, bad);
-    // e = min{e >= -127 : m <= L 2^e}; m = f 2^x, 1 <= f < 2
-    const long long b = __double_as_longlong(m);
-    const int x = (int)(b >> 52) - 1023;
-    const long long frac = b & 0xFFFFFFFFFFFFFll;
-    const int e = BITS == 8 ? x - 8 + (frac > 0xC000000000000ll) : x - 2 + (frac > 0x8000000000000ll);
-    const int byte = bad ? 255 : min(254, max(0, e + 127));
-    const double inv = byte == 255 ? 0.0 : __longlong_as_double((long long)(1023 + 127 - byte) << 52);
-    float f[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = to_odd(y[i] * inv);
-    mx_enc8<BITS>(f, codes);
-    return byte;
+// s r w to about 2^-45, r = 1 / sqrt as a pair.
+__device__ __forceinline__ Pair scale_pair(float s, Pair r, float w) {
+    const float a = __fmul_rn(s, r.hi), b = __fmaf_rn(s, r.lo, __fmaf_rn(s, r.hi, -a));
+    const float q = __fmul_rn(a, w), f = __fmaf_rn(b, w, __fmaf_rn(a, w, -q));
+    const float hi = __fadd_rn(q, f);
+    return {hi, __fsub_rn(f, __fsub_rn(hi, q))};
 }
 
-constexpr float NORM_LO = 1.f - 0x1p-20f, NORM_HI = 1.f + 0x1p-20f;
+// 1 / sqrt(a): one step of third order from an fp32 value (2^-22) leaves 2^-50.
+__device__ __forceinline__ double refine_rsqrt(double a, float r0) {
+    const double r = r0, e = fma(-a * r, r, 1.0);
+    return fma(r * e, fma(0.375, e, 0.5), r);
+}
 
-// Quantises 8 columns; the whole warp calls. inside: the columns are not padding, which is zeros whatever the row.
+// Roundings of y, in units of 2^-24: s rstd, times w, times the scale 1 each; rsqrtf 4 (2 units of the last place); its
+// argument 1 (two, halved by the root); the sum of squares at most 16 on the way of a term (see k_mx_rmsnorm), halved.
+constexpr float NORM_LO = 1.f - 0x1.2p-20f, NORM_HI = 1.f + 0x1.2p-20f;
+
+// Codes and exponent byte of 8 columns from fp32 values; the whole warp calls, with rstd 0 for padding. again: another
+// code or exponent is possible in this thread's part of the run.
 template <int BITS>
-__device__ __forceinline__ int norm_codes(const float* s, const float* w, bool inside, float rstd, Pair sum, double sum64, bool wide,
-                                          int n, float eps, uint32_t* codes) {
-    if (!inside) rstd = 0.f;
+__device__ __forceinline__ int norm_codes(const float* s, const float* w, float rstd, uint32_t* codes, bool& again) {
     float y[8];
     uint32_t m = 0;
 #pragma unroll
@@ -184,118 +220,300 @@ __device__ __forceinline__ int norm_codes(const float* s, const float* w, bool i
     }
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    const float am = __uint_as_float(m);
-    int byte = mx_exp_byte<BITS>(m);
-    // a run of tiny values: s rstd may have underflowed
-    bool again = wide || (am < 0x1p-30f && am > 0.f) ||
-                 mx_exp_byte<BITS>(__float_as_uint(am * NORM_LO)) != mx_exp_byte<BITS>(__float_as_uint(am * NORM_HI));
+    const int byte = mx_exp_byte<BITS>(m);
+    // the largest next to L 2^e (d of 1.75 is 16 units of the mantissa), or so small that s rstd may have underflowed
+    constexpr uint32_t M = BITS == 8 ? 0x600000u : 0x400000u;
+    again = ((m - M + 16u) & 0x7FFFFFu) <= 32u || (m < 0x30800000u && m != 0u);
     const float inv = mx_inv_scale(byte);
-    const float lo = inv * NORM_LO, hi = inv * NORM_HI;  // inv is a power of two: no rounding
-    float a[8], b[8];
+    const float lo = inv * NORM_LO, hi = inv * NORM_HI;
+    float a[8];
+    uint32_t cb[2];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] = y[i] * lo;
+    mx_enc8<BITS>(a, codes);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] = y[i] * hi;
+    mx_enc8<BITS>(a, cb);
+    again |= codes[0] != cb[0] || codes[1] != cb[1];
+    return byte;
+}
+
+// The same from pairs: r = 1 / sqrt as a pair (0 for padding). The four lanes of a run (mask) call together.
+template <int BITS>
+__device__ __forceinline__ int norm_pairs(const float* s, const float* w, Pair r, uint32_t mask, uint32_t* codes) {
+    // the largest |y|: the pair's first float decides but where it is L 2^e itself
+    float top = 0.f;
+    bool above = false, nan = false;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        a[i] = y[i] * lo;
-        b[i] = y[i] * hi;
+        const Pair t = scale_pair(s[i], r, w[i]);
+        const float h = fabsf(t.hi);
+        const bool more = t.lo != 0.f && (t.lo < 0.f) == (t.hi < 0.f);
+        nan |= !(h <= 3.402823466e38f);
+        if (h > top) top = h, above = more;
+        else if (h == top) above |= more;
     }
-    uint32_t cb[2];
+    uint32_t k = nan ? 0x7FC00000u : __float_as_uint(top);
+#pragma unroll
+    for (int o = 1; o <= 2; o <<= 1) {
+        const uint32_t ko = __shfl_xor_sync(mask, k, o);
+        const bool ao = __shfl_xor_sync(mask, (int)above, o);
+        above = ko > k ? ao : ko == k ? above || ao : above;
+        k = max(k, ko);
+    }
+    int byte = mx_exp_byte<BITS>(k);
+    if (above && byte < 254) byte = max(byte, mx_exp_byte<BITS>(k + 1));
+    const float inv = mx_inv_scale(byte);
+    float a[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const Pair t = scale_pair(s[i], r, w[i]);
+        a[i] = to_odd(Pair{t.hi * inv, t.lo * inv});
+    }
     mx_enc8<BITS>(a, codes);
-    mx_enc8<BITS>(b, cb);
-    again |= codes[0] != cb[0] || codes[1] != cb[1];
-    const uint32_t lane = threadIdx.x & 31, mask = 0xFu << (lane & 28u);
-    again = (__ballot_sync(0xffffffffu, again) & mask) != 0;
-    if (again) {
-        const double t = wide ? sum64 : (double)sum.hi + (double)sum.lo;
-        byte = norm_exact<BITS>(s, w, inside ? 1.0 / sqrt(t / n + (double)eps) : 0.0, mask, codes);
-    }
-    __syncwarp();
     return byte;
+}
+
+// x and add of 8 columns, asked for; their rounded sum.
+struct NormRaw {
+    MxRaw x, add;
+};
+template <int DT>
+__device__ __forceinline__ NormRaw norm_fetch(const MxNormP& p, size_t row, int c, int left) {
+    NormRaw r = {mx_fetch8<DT>(p.x, row * p.ld_x + c, left), {}};
+    if (p.dt_add == QW_F32) r.add = mx_fetch8<QW_F32>(p.add, row * p.ld_add + c, left);
+    else if (p.dt_add >= 0) r.add = mx_fetch8<QW_F16>(p.add, row * p.ld_add + c, left);
+    return r;
+}
+template <int DT>
+__device__ __forceinline__ void norm_sum(const MxNormP& p, size_t row, int c, int left, NormRaw& r, float* d) {
+    mx_fill8<DT>(p.x, row * p.ld_x + c, left, r.x);
+    mx_unpack8<DT>(r.x, d);
+    if (p.dt_add >= 0) {
+        float a[8];
+        const size_t at = row * p.ld_add + c;
+        if (p.dt_add == QW_F32) {
+            mx_fill8<QW_F32>(p.add, at, left, r.add);
+            mx_unpack8<QW_F32>(r.add, a);
+        } else {
+            mx_fill8<QW_F16>(p.add, at, left, r.add);
+            if (p.dt_add == QW_BF16) mx_unpack8<QW_BF16>(r.add, a);
+            else mx_unpack8<QW_F16>(r.add, a);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[i] = round_to<DT>(d[i] + a[i]);
+    }
+}
+template <int DT>
+__device__ __forceinline__ void norm_load(const MxNormP& p, size_t row, int c, int left, float* d) {
+    NormRaw r = norm_fetch<DT>(p, row, c, left);
+    norm_sum<DT>(p, row, c, left, r, d);
+}
+
+// 8 columns' codes; the scale word of 128 from each half warp's first lane (the whole warp calls).
+template <int BITS>
+__device__ __forceinline__ void norm_store(const MxNormP& p, size_t row, int v, const uint32_t* q) {
+    uint8_t* at = p.codes + row * p.atoms * (MX_ATOM * BITS / 8) + (size_t)v * BITS;
+    if (BITS == 8) *reinterpret_cast<uint2*>(at) = make_uint2(q[0], q[1]);
+    else *reinterpret_cast<uint32_t*>(at) = q[0];
+}
+__device__ __forceinline__ void norm_store_scales(const MxNormP& p, size_t row, int v, bool ok, int byte) {
+    const uint32_t sw = mx_gather_word(byte);
+    if (ok && (threadIdx.x & 15) == 0) *reinterpret_cast<uint32_t*>(p.scales + mx_scale_word((int)row, v / 16, p.atoms)) = sw;
+}
+
+// A row whose squares leave fp32, or that holds a NaN or an infinity: everything in fp64, read again from memory.
+template <int DT, int BITS>
+__device__ __noinline__ void norm_wide_row(const MxNormP& p, double* part) {
+    const int row = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const int vecs = p.atoms * (MX_ATOM / 8), steps = (vecs + blockDim.x - 1) / blockDim.x;
+    double sum = 0.0;
+    for (int j = 0; j < steps; ++j) {
+        const int v = j * blockDim.x + threadIdx.x;
+        float s[8];
+        norm_load<DT>(p, row, v * 8, v < vecs ? p.cols - v * 8 : 0, s);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum += (double)s[i] * (double)s[i];
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) part[warp] = sum;
+    __syncthreads();
+    sum = 0.0;
+    for (int i = 0; i < warps; ++i) sum += part[i];
+    const double rstd = 1.0 / sqrt(sum / p.cols + (double)p.eps);
+    for (int j = 0; j < steps; ++j) {
+        const int v = j * blockDim.x + threadIdx.x, left = v < vecs ? p.cols - v * 8 : 0;
+        float s[8], w[8];
+        norm_load<DT>(p, row, v * 8, left, s);
+        mx_load8<QW_BF16>(p.w, v * 8, left, w);
+        if (p.sum && left > 0) mx_store8<DT>(p.sum, row * p.ld_sum + v * 8, left, s);
+        double y[8], m = 0.0;
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            y[i] = left > 0 ? (double)s[i] * rstd * (double)w[i] : 0.0;
+            bad |= !(fabs(y[i]) <= 3.4028234663852886e38);
+            m = fmax(m, fabs(y[i]));
+        }
+        m = fmax(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = fmax(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        bad = (__ballot_sync(0xffffffffu, bad) & (0xFu << (lane & 28))) != 0;
+        // e = min{e >= -127 : m <= L 2^e}; m = (1 + frac 2^-52) 2^x
+        const long long b = __double_as_longlong(m);
+        const int x = (int)(b >> 52) - 1023;
+        const long long frac = b & 0xFFFFFFFFFFFFFll;
+        const int e = BITS == 8 ? x - 8 + (frac > 0xC000000000000ll) : x - 2 + (frac > 0x8000000000000ll);
+        const int byte = bad ? 255 : min(254, max(0, e + 127));
+        const double inv = bad ? 0.0 : __longlong_as_double((long long)(1023 + 127 - byte) << 52);
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = to_odd(y[i] * inv);
+        uint32_t q[2];
+        mx_enc8<BITS>(f, q);
+        if (v < vecs) norm_store<BITS>(p, row, v, q);
+        norm_store_scales(p, row, v, v < vecs, byte);
+    }
+}
+
+// A pair summed over the CTA.
+__device__ __forceinline__ Pair block_sum(Pair t, Pair* part) {
+    const int warps = blockDim.x >> 5;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) t = add_pairs(t, {__shfl_xor_sync(0xffffffffu, t.hi, o), __shfl_xor_sync(0xffffffffu, t.lo, o)});
+    if (warps == 1) return t;
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = t;
+    __syncthreads();
+    t = (int)(threadIdx.x & 15) < warps ? part[threadIdx.x & 15] : Pair{0.f, 0.f};
+#pragma unroll
+    for (int o = 8; o; o >>= 1) t = add_pairs(t, {__shfl_xor_sync(0xffffffffu, t.hi, o), __shfl_xor_sync(0xffffffffu, t.lo, o)});
+    return t;
 }
 
 // VPT: vectors of 8 columns a thread keeps in registers; 0: any number, read twice.
 template <int DT, int BITS, int VPT>
-__global__ void __launch_bounds__(512) k_mx_rmsnorm(const __grid_constant__ MxNormP p) {
+__global__ void __launch_bounds__(VPT == 1 ? 128 : 512, VPT == 1 ? 14 : VPT == 2 ? 2 : 1) k_mx_rmsnorm(const __grid_constant__ MxNormP p) {
     constexpr int N = VPT ? VPT : 1;
-    __shared__ Pair part[16];
-    __shared__ double part64[16];
+    __shared__ double part[16];  // of the warps: a pair of floats or, in a wide row, a double
     pdl_wait();
     pdl_launch();
     const int row = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    const int vecs = p.atoms * (MX_ATOM / 8), steps = (vecs + blockDim.x - 1) / blockDim.x;  // steps: VPT 0
-    const size_t rx = (size_t)row * p.ld_x, ra = (size_t)row * p.ld_add, rs = (size_t)row * p.ld_sum;
+    const int vecs = p.atoms * (MX_ATOM / 8), steps = VPT ? 1 : (vecs + blockDim.x - 1) / blockDim.x;
     float s[N][8];
-    auto load = [&](int v, float* d) {
-        const int c = v * 8, left = v < vecs ? p.cols - c : 0;
-        mx_load8<DT>(p.x, rx + c, left, d);
-        if (p.dt_add >= 0) {
-            float a[8];
-            if (p.dt_add == QW_F32) mx_load8<QW_F32>(p.add, ra + c, left, a);
-            else if (p.dt_add == QW_BF16) mx_load8<QW_BF16>(p.add, ra + c, left, a);
-            else mx_load8<QW_F16>(p.add, ra + c, left, a);
+    MxRaw wr[N];  // the weight, on its way during the first pass
+    {
+        NormRaw r[N];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) d[i] = round_to<DT>(d[i] + a[i]);
+        for (int k = 0; k < VPT; ++k) {
+            const int v = k * blockDim.x + threadIdx.x;
+            r[k] = norm_fetch<DT>(p, row, v * 8, v < vecs ? p.cols - v * 8 : 0);
         }
-    };
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int v = k * blockDim.x + threadIdx.x;
+            wr[k] = mx_fetch8<QW_BF16>(p.w, v * 8, v < vecs ? p.cols - v * 8 : 0);
+        }
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int v = k * blockDim.x + threadIdx.x;
+            norm_sum<DT>(p, row, v * 8, v < vecs ? p.cols - v * 8 : 0, r[k], s[k]);
+        }
+    }
+    // the sum of squares: at most 16 roundings on the way of each term (4 sums of VPT to 4 + 3 in a thread, 5 + 4 across
+    // the CTA); a row of any length in pairs
     Pair t = {0.f, 0.f};
+    float sum;
+    if (VPT) {
+        constexpr int A = VPT < 4 ? 4 : 8;
+        float acc[A] = {};
 #pragma unroll
-    for (int jj = 0; jj < N; ++jj) {
-        if (VPT) load(jj * blockDim.x + threadIdx.x, s[jj]);
-    }
+        for (int k = 0; k < N; ++k)
 #pragma unroll
-    for (int jj = 0; jj < N; ++jj) {
-        for (int j = jj; j < (VPT ? jj + 1 : steps); ++j) {
-            if (!VPT) load(j * blockDim.x + threadIdx.x, s[0]);
+            for (int i = 0; i < 8; ++i) acc[i % A] = fmaf(s[k][i], s[k][i], acc[i % A]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) add_square(t, s[jj][i]);
-        }
-    }
+        for (int o = A / 2; o; o >>= 1)
 #pragma unroll
-    for (int o = 16; o; o >>= 1) t = add_pairs(t, {__shfl_xor_sync(0xffffffffu, t.hi, o), __shfl_xor_sync(0xffffffffu, t.lo, o)});
-    if (warps > 1) {
-        if (lane == 0) part[warp] = t;
-        __syncthreads();
-        t = part[0];
-        for (int i = 1; i < warps; ++i) t = add_pairs(t, part[i]);
-    }
-    // squares that fp32 cannot hold (or not in a pair): the sum in fp64, and every run
-    const bool wide = !(t.hi > 0x1p-80f && t.hi < 0x1p120f);
-    double sum64 = 0.0;
-    if (wide) {
-#pragma unroll
-        for (int jj = 0; jj < N; ++jj) {
-            for (int j = jj; j < (VPT ? jj + 1 : steps); ++j) {
-                if (!VPT) load(j * blockDim.x + threadIdx.x, s[0]);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) sum64 += (double)s[jj][i] * (double)s[jj][i];
-            }
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) sum64 += __shfl_xor_sync(0xffffffffu, sum64, o);
+            for (int i = 0; i < o; ++i) acc[i] += acc[i + o];
+        sum = warp_sum(acc[0]);
         if (warps > 1) {
-            if (lane == 0) part64[warp] = sum64;
+            float* sums = reinterpret_cast<float*>(part);
+            if (lane == 0) sums[warp] = sum;
             __syncthreads();
-            sum64 = part64[0];
-            for (int i = 1; i < warps; ++i) sum64 += part64[i];
+            sum = (lane & 15) < warps ? sums[lane & 15] : 0.f;
+#pragma unroll
+            for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        }
+    } else {
+        for (int j = 0; j < steps; ++j) {
+            const int v = j * blockDim.x + threadIdx.x;
+            norm_load<DT>(p, row, v * 8, v < vecs ? p.cols - v * 8 : 0, s[0]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) add_square(t, s[0][i]);
+        }
+        t = block_sum(t, reinterpret_cast<Pair*>(part));
+        sum = t.hi;
+    }
+    if (!(sum > 0x1p-80f && sum < 0x1p120f)) {
+        __syncthreads();
+        norm_wide_row<DT, BITS>(p, part);
+        return;
+    }
+    const float rstd = rsqrtf(fmaf(sum, (float)p.inv_n, p.eps));
+    Pair r = {0.f, 0.f};
+    auto refine = [&]() {
+        const double d = refine_rsqrt(((double)t.hi + (double)t.lo) * p.inv_n + (double)p.eps, rstd);
+        r.hi = (float)d;
+        r.lo = (float)(d - (double)r.hi);
+    };
+    const uint32_t mask = 0xFu << (lane & 28);  // the four lanes of a run
+    bool again[N], any = false;
+    int byte[N];
+    if constexpr (!VPT) refine();
+    for (int j = 0; j < steps; ++j) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const int v = (VPT ? k : j) * blockDim.x + threadIdx.x, left = v < vecs ? p.cols - v * 8 : 0;
+            if (!VPT) {
+                norm_load<DT>(p, row, v * 8, left, s[0]);
+                wr[k] = mx_fetch8<QW_BF16>(p.w, v * 8, left);
+            }
+            float w[8];
+            mx_fill8<QW_BF16>(p.w, v * 8, left, wr[k]);
+            mx_unpack8<QW_BF16>(wr[k], w);
+            if (p.sum && left > 0) mx_store8<DT>(p.sum, row * p.ld_sum + v * 8, left, s[k]);
+            uint32_t q[2];
+            byte[k] = norm_codes<BITS>(s[k], w, left > 0 ? rstd : 0.f, q, again[k]);
+            if (!VPT && (__ballot_sync(0xffffffffu, again[k]) & mask))
+                byte[k] = norm_pairs<BITS>(s[k], w, left > 0 ? r : Pair{0.f, 0.f}, mask, q);
+            __syncwarp();
+            any |= again[k];
+            if (v < vecs) norm_store<BITS>(p, row, v, q);
+            norm_store_scales(p, row, v, v < vecs, byte[k]);
         }
     }
-    const float rstd = wide ? 0.f : 1.f / sqrtf(t.hi / p.cols + p.eps);
+    if constexpr (VPT > 0) {
+        if (!(warps > 1 ? __syncthreads_or(any) : __any_sync(0xffffffffu, any))) return;
+        // the runs in doubt again
 #pragma unroll
-    for (int jj = 0; jj < N; ++jj) {
-        for (int j = jj; j < (VPT ? jj + 1 : steps); ++j) {
-            const int v = j * blockDim.x + threadIdx.x, c = v * 8, left = v < vecs ? p.cols - c : 0;
-            float* d = s[jj];
-            if (!VPT) load(v, d);
-            float w[8];
-            mx_load8<QW_BF16>(p.w, c, left, w);
-            if (p.sum && left > 0) mx_store8<DT>(p.sum, rs + c, left, d);
-            uint32_t q[2];
-            const int byte = norm_codes<BITS>(d, w, left > 0, rstd, t, sum64, wide, p.cols, p.eps, q);
-            const uint32_t sw = mx_gather_word(byte);
-            if (v < vecs) {
-                uint8_t* at = p.codes + (size_t)row * p.atoms * (MX_ATOM * BITS / 8) + (size_t)c * BITS / 8;
-                if (BITS == 8) *reinterpret_cast<uint2*>(at) = make_uint2(q[0], q[1]);
-                else *reinterpret_cast<uint32_t*>(at) = q[0];
-                if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(p.scales + mx_scale_word(row, c / MX_ATOM, p.atoms)) = sw;
+        for (int k = 0; k < N; ++k)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) add_square(t, s[k][i]);
+        t = block_sum(t, reinterpret_cast<Pair*>(part));
+        refine();
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const int v = k * blockDim.x + threadIdx.x, left = v < vecs ? p.cols - v * 8 : 0;
+            const uint32_t doubt = __ballot_sync(0xffffffffu, again[k]);
+            if (!doubt) continue;
+            if (doubt & mask) {
+                float w[8];
+                mx_unpack8<QW_BF16>(wr[k], w);
+                uint32_t q[2];
+                byte[k] = norm_pairs<BITS>(s[k], w, left > 0 ? r : Pair{0.f, 0.f}, mask, q);
+                if (v < vecs) norm_store<BITS>(p, row, v, q);
             }
+            __syncwarp();
+            norm_store_scales(p, row, v, v < vecs, byte[k]);
         }
     }
 }
@@ -320,17 +538,22 @@ qw_status done(cudaError_t e, const char* what) {
     return e == cudaSuccess ? QW_OK : qw_fail(QW_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
+// Matrices of more than a wave of CTAs: four pieces a warp.
+bool many(const MxRowsP& p) { return p.units >= 8192u; }
+
 template <typename K>
-cudaError_t launch_rows(K kern, const MxRowsP& p, cudaStream_t st) {
-    return launch_k({st, true, nullptr}, kern, dim3((p.units + MQ_WARPS - 1) / MQ_WARPS), dim3(MQ_WARPS * 32), 0, p);
+cudaError_t launch_rows(K one, K four, const MxRowsP& p, cudaStream_t st) {
+    const unsigned per = MQ_WARPS * (many(p) ? 4 : 1);
+    return launch_k({st, true, nullptr}, many(p) ? four : one, dim3((p.units - 1) / per + 1), dim3(MQ_WARPS * 32), 0, p);
 }
 
 template <int DT, int BITS>
 cudaError_t launch_norm(const MxNormP& p, cudaStream_t st) {
     const LaunchCtx c = {st, true, nullptr};
     const int vecs = p.atoms * (MX_ATOM / 8);
-    // a row of up to 2048 columns has a thread for every 8; a longer one two or four vectors a thread
-    const int vpt = vecs <= 256 ? 1 : vecs <= 1024 ? 2 : vecs <= 2048 ? 4 : 0;
+    // up to 1024 columns a thread has 8 of them, to 8192 16, to 16384 32. Measured (us): 8192 x 1024 17.0 and 17.2 with 16 a
+    // thread; 4096 x 2048 18.7 with 8, 18.1 with 16; 2048 x 4096 24.9 with 8, 18.3 with 16, 20.1 with 32
+    const int vpt = vecs <= 128 ? 1 : vecs <= 1024 ? 2 : vecs <= 2048 ? 4 : 0;
     const dim3 block(vpt ? ((vecs + vpt - 1) / vpt + 31) / 32 * 32 : 512), grid(p.rows);
     switch (vpt) {
         case 1: return launch_k(c, k_mx_rmsnorm<DT, BITS, 1>, grid, block, 0, p);
@@ -370,7 +593,7 @@ extern "C" qw_status qw_mx_quantize(const qw_mx* out, const void* dev_x, size_t 
     if (qw_status s = rows_check(dev_x, ld_x, dtype, out->cols, "mx_quantize", "x")) return s;
     const MxRowsP p = rows_p(out, dev_x, nullptr, ld_x);
     const cudaStream_t st = (cudaStream_t)stream;
-#define MX_Q(dt, bits) launch_rows(k_mx_quantize<dt, bits>, p, st)
+#define MX_Q(dt, bits) launch_rows(k_mx_quantize<dt, bits, 1>, k_mx_quantize<dt, bits, 4>, p, st)
     return done(MX_DISPATCH(MX_Q, dtype, out->bits), "mx_quantize");
 }
 
@@ -380,7 +603,7 @@ extern "C" qw_status qw_mx_read(const qw_mx* m, void* dev_x, size_t ld_x, int dt
     if (qw_status s = rows_check(dev_x, ld_x, dtype, m->cols, "mx_read", "x")) return s;
     const MxRowsP p = rows_p(m, nullptr, dev_x, ld_x);
     const cudaStream_t st = (cudaStream_t)stream;
-#define MX_R(dt, bits) launch_rows(k_mx_read<dt, bits>, p, st)
+#define MX_R(dt, bits) launch_rows(k_mx_read<dt, bits, 1>, k_mx_read<dt, bits, 4>, p, st)
     return done(MX_DISPATCH(MX_R, dtype, m->bits), "mx_read");
 }
 
@@ -400,7 +623,7 @@ extern "C" qw_status qw_mx_rmsnorm(const qw_mx* out, const void* dev_x, size_t l
     }
     if (!dev_weight || !aligned16(dev_weight)) return qw_fail(QW_ERR_INVALID_ARG, "mx_rmsnorm: weight NULL or not 16-byte aligned");
     const MxNormP p = {(uint8_t*)out->dev_codes, (uint8_t*)out->dev_scales, out->rows, out->cols, (int)mx_atoms(out->cols), dev_x,
-                       dev_add, dev_sum, (const bf16*)dev_weight, ld_x, ld_add, ld_sum, dev_add ? add_dtype : -1, eps};
+                       dev_add, dev_sum, (const bf16*)dev_weight, ld_x, ld_add, ld_sum, dev_add ? add_dtype : -1, eps, 1.0 / out->cols};
     const cudaStream_t st = (cudaStream_t)stream;
 #define MX_N(dt, bits) launch_norm<dt, bits>(p, st)
     return done(MX_DISPATCH(MX_N, x_dtype, out->bits), "mx_rmsnorm");

@@ -197,9 +197,7 @@ __device__ __forceinline__ void store_run(const MxGemmP& p, int t, int f, const 
     }
     uint8_t* at = p.codes + (size_t)t * p.oatoms * (MX_ATOM * BITS / 8) + (size_t)f * BITS / 8;
     if (BITS == 8)  // a whole 32-byte sector
-        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
-                     "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                     : "memory");
+        mx_st32(at, w);
     else
         *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
     p.scales[mx_scale_word(t, f / MX_ATOM, p.oatoms) + (f / MX_RUN & 3)] = (uint8_t)byte;

@@ -87,35 +87,67 @@ __device__ __forceinline__ void mx_dec8(const uint32_t* w, uint32_t* h) {
     }
 }
 
-// 8 elements from `off` on of rows of type DT; those from the row's column `left` on are zeros
-// (left <= 0: nothing is read). The element is 16-byte aligned.
+// 32 bytes, 32-byte aligned: a whole sector.
+__device__ __forceinline__ void mx_st32(void* p, const uint32_t* w) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+// 8 elements of a row as they lie in memory: asked for first (vector loads of whole, 16-byte aligned groups), filled up
+// where a row ends inside, unpacked last, so that many can be on their way at once.
+struct MxRaw {
+    uint4 a, b;  // b: of QW_F32 only
+};
+template <int DT>
+__device__ __forceinline__ MxRaw mx_fetch8(const void* base, size_t off, int left) {
+    MxRaw r = {};
+    if (left >= 8) {
+        const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(base) + off * (DT == QW_F32 ? 4 : 2));
+        r.a = p[0];
+        if (DT == QW_F32) r.b = p[1];
+    }
+    return r;
+}
+template <int DT>
+__device__ __forceinline__ void mx_fill8(const void* base, size_t off, int left, MxRaw& r) {
+    if (left <= 0 || left >= 8) return;
+    uint32_t w[8] = {};
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+        if (i < left) {
+            if (DT == QW_F32) w[i] = reinterpret_cast<const uint32_t*>(base)[off + i];
+            else w[i / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(base)[off + i] << (i % 2 * 16);
+        }
+    r = {make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7])};
+}
+template <int DT>
+__device__ __forceinline__ void mx_unpack8(const MxRaw& r, float* x) {
+    const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        x[i] = DT == QW_F32    ? __uint_as_float(w[i])
+               : DT == QW_BF16 ? (i % 2 ? bf_hi(w[i / 2]) : bf_lo(w[i / 2]))
+                               : (i % 2 ? h_hi(w[i / 2]) : h_lo(w[i / 2]));
+}
+// Bits, as a float's, of the largest magnitude of 8 elements; NaN and infinities are above every number. 16-bit
+// elements are compared in pairs, as integers.
+template <int DT>
+__device__ __forceinline__ uint32_t mx_absmax8(const MxRaw& r) {
+    const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        m = DT == QW_F32 ? max(m, w[i] & 0x7FFFFFFFu) : i < 4 ? __vmaxu2(m, w[i] & 0x7FFF7FFFu) : m;
+    if (DT == QW_F32) return m;
+    m = max(m & 0xFFFFu, m >> 16);
+    return DT == QW_BF16 ? m << 16 : __float_as_uint(__half2float(__ushort_as_half((unsigned short)m))) & 0x7FFFFFFFu;
+}
 template <int DT>
 __device__ __forceinline__ void mx_load8(const void* base, size_t off, int left, float* x) {
-    if (left >= 8) {
-        if (DT == QW_F32) {
-            const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(base) + off);
-            const float4 a = p[0], b = p[1];
-            x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-        } else {
-            const uint4 v = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(base) + off);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[2 * i] = DT == QW_BF16 ? bf_lo(w[i]) : h_lo(w[i]);
-                x[2 * i + 1] = DT == QW_BF16 ? bf_hi(w[i]) : h_hi(w[i]);
-            }
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            x[i] = 0.f;
-            if (i < left) {
-                if (DT == QW_F32) x[i] = reinterpret_cast<const float*>(base)[off + i];
-                else if (DT == QW_BF16) x[i] = bf2f(reinterpret_cast<const bf16*>(base)[off + i]);
-                else x[i] = __half2float(reinterpret_cast<const f16*>(base)[off + i]);
-            }
-        }
-    }
+    MxRaw r = mx_fetch8<DT>(base, off, left);
+    mx_fill8<DT>(base, off, left, r);
+    mx_unpack8<DT>(r, x);
 }
 
 // fp16 results stop at 65504, as those of the 8-bit cache do; NaN stays.
