@@ -392,7 +392,7 @@ __device__ __forceinline__ Pair block_sum(Pair t, Pair* part) {
 
 // VPT: vectors of 8 columns a thread keeps in registers; 0: any number, read twice.
 template <int DT, int BITS, int VPT>
-__global__ void __launch_bounds__(VPT == 1 ? 128 : 512, VPT == 1 ? 14 : VPT == 2 ? 2 : 1) k_mx_rmsnorm(const __grid_constant__ MxNormP p) {
+__global__ void __launch_bounds__(VPT == 1 ? 128 : 512, VPT == 1 ? 12 : VPT == 2 ? 2 : 1) k_mx_rmsnorm(const __grid_constant__ MxNormP p) {
     constexpr int N = VPT ? VPT : 1;
     __shared__ double part[16];  // of the warps: a pair of floats or, in a wide row, a double
     pdl_wait();

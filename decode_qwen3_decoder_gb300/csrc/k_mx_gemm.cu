@@ -12,10 +12,16 @@
 // row, 128 in each CTA) by 256 of W (N): two neighbouring tiles of 128 for the linear product; the same 128 features
 // of gate and up for SwiGLU, so that a thread has both of a feature, and the 32 features of a run, in its
 // registers. Each CTA loads its own 128 rows of X and one of the two W tiles, both the exponents of all of W.
-// Persistent; 8 epilogue warps, one producer, one MMA issuer (the leader's).
+// Persistent; 8 epilogue warps, one producer, one MMA issuer and one copier of exponents (the leader's).
+//
+// k_mx_gemm_few. For few rows of X: W's rows are the M (128 of them, of gate and of up for SwiGLU), X's the N
+// (16 or 64). A cluster of up to 8 CTAs shares a tile's columns out; each sends its partial sums of an
+// equal part of X's rows to the CTA that owns the part (distributed shared memory), which adds them in order.
+// Where the tiles alone fill the GPU the CTAs walk them, with two accumulators: W streams on under the output.
 //
 // Every wait is bounded (about 2 s): then QW_MX_TIMEOUT is set and the CTA frees its TMEM and ends.
 #include <algorithm>
+#include <atomic>
 
 #include "mx.cuh"
 #include "tc_sm103.cuh"
@@ -70,6 +76,11 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volati
 }
 __device__ __forceinline__ uint64_t sf_desc(uint32_t a) {  // no swizzle, 8-row groups of 16-byte rows 128 bytes apart
     return (uint64_t)((a & 0x3FFFFu) >> 4) | ((uint64_t)8 << 32) | ((uint64_t)1 << 46);
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+                 "r"(bytes), "r"(bar)
+                 : "memory");
 }
 __device__ __forceinline__ uint32_t cta_rank() {
     uint32_t r;
@@ -295,18 +306,11 @@ __global__ void __launch_bounds__(MG_THREADS, 1) k_mx_gemm(const __grid_constant
             int i = 0;
             bool ok = true;
             for (int u = pair; u < p.units && ok; u += pairs, ++i) {
-                if (!wait_phase(smem_u32(acce), ((uint32_t)i & 1u) ^ 1u, abort_flag)) {
-                    *abort_flag = 1;
-                    break;
-                }
-                tc_fence_after();
-                for (int kb = 0; kb < nk; ++kb, ++g) {
+                ok = wait_phase(smem_u32(acce), ((uint32_t)i & 1u) ^ 1u, abort_flag);
+                for (int kb = 0; kb < nk && ok; ++kb, ++g) {
                     const int s = g % C::STAGES;
-                    if (!wait_phase(smem_u32(sready + s), (g / C::STAGES) & 1u, abort_flag)) {
-                        ok = false;
-                        *abort_flag = 1;
-                        break;
-                    }
+                    ok = wait_phase(smem_u32(sready + s), (g / C::STAGES) & 1u, abort_flag);
+                    if (!ok) break;
                     tc_fence_after();
                     const uint32_t st = smem_u32(smem + s * MG_STAGE);
                     const uint32_t ta = tmem + MG_SF_COL + s * MG_SF_COLS, tb = ta + 8;
@@ -324,6 +328,7 @@ __global__ void __launch_bounds__(MG_THREADS, 1) k_mx_gemm(const __grid_constant
                 }
                 if (ok) umma_commit_pair(smem_u32(accf));
             }
+            if (!ok) *abort_flag = 1;
         }
         __syncwarp();
     } else if (warp == 10) {
@@ -406,6 +411,316 @@ __global__ void __launch_bounds__(MG_THREADS, 1) k_mx_gemm(const __grid_constant
     }
 }
 
+// ---- few rows of X --------------------------------------------------------------------------------------------
+
+struct MfP {
+    int T, M, atoms, oatoms;
+    int tiles_w, lsplits;         // log2 of the CTAs that share a tile
+    const uint8_t *sx, *sa, *sb;  // exponents of X, W (gate) and up
+    int dtype, bits;              // of the output
+    void* out;
+    size_t ld;
+    uint8_t *codes, *scales;
+    int32_t* status;
+};
+struct MfMaps {
+    CUtensorMap x, a, b;
+};
+
+constexpr int MF_THREADS = 224;
+template <bool F4, bool GLU, int BN>
+struct MfCfg {
+    static constexpr int NW = GLU ? 2 : 1;  // tiles of W
+    static constexpr int AT = F4 ? 2 : 1;   // atoms of 128 columns a stage
+    static constexpr int STAGE = NW * MG_W + BN * 128 + (NW + 1) * MG_SF;
+    // two CTAs an SM. One row by 60000 x 4096 in 8 bits: 41 us, 6.0 TB/s; with 3 stages and three CTAs 52
+    static constexpr int STAGES = GLU ? 3 : BN == 16 ? 5 : 4;
+    static constexpr int SF_COLS = (NW + 1) * AT * 4, SF_COL = 2 * NW * BN;  // after two accumulators
+    static constexpr int COLS_USED = SF_COL + STAGES * SF_COLS;
+    static constexpr int COLS = COLS_USED <= 64 ? 64 : COLS_USED <= 128 ? 128 : 256;
+    // CTAs of a cluster wait for one another, so none may wait for tensor memory that another cluster holds: a CTA asks for
+    // as large a share of the SM's shared memory (228 KB, 1 of it taken) as of its tensor memory. Whatever shares an
+    // SM then has its columns.
+    static constexpr int NEED = 1024 + STAGES * STAGE + 256, SHARE = COLS * 456 - 1024;
+    static constexpr int SMEM = NEED > SHARE ? NEED : SHARE;
+    static constexpr int PER_SM = 233472 / (SMEM + 1024);  // CTAs that share an SM
+    static_assert(COLS_USED <= COLS && PER_SM * COLS <= 512, "tensor memory");
+    static_assert(NW * BN * 512 <= STAGES * STAGE, "partial sums");
+};
+
+// A lane's feature f of rows t .. t + min(n, N) - 1; 8 at a time, so that their loads, reductions and stores overlap.
+// GLU: the warp has a run of 32 features, lane l the l-th.
+template <int DT, int N>
+__device__ __forceinline__ void store_few(const MfP& p, int t, int n, int f, const float* v) {
+    const size_t at = (size_t)t * p.ld + f;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (i < n && f < p.M) {
+            if (DT == QW_F32) reinterpret_cast<float*>(p.out)[at + i * p.ld] = v[i];
+            else reinterpret_cast<uint16_t*>(p.out)[at + i * p.ld] = (uint16_t)mx_pack2<DT>(v[i], 0.f);
+        }
+}
+template <bool GLU, int N>
+__device__ __forceinline__ void finish_few(const MfP& p, int t, int n, int f, const float* a, const float* b) {
+    if (!GLU) {
+        if (p.dtype == QW_F32) store_few<QW_F32, N>(p, t, n, f, a);
+        else if (p.dtype == QW_BF16) store_few<QW_BF16, N>(p, t, n, f, a);
+        else store_few<QW_F16, N>(p, t, n, f, a);
+        return;
+    }
+    const int lane = threadIdx.x & 31;
+    float h[8] = {};
+    int byte[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) h[i] = f < p.M ? silu_mul(a[i], b[i]) : 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(h[i]) & 0x7FFFFFFFu);
+        byte[i] = p.bits == 8 ? mx_exp_byte<8>(m) : mx_exp_byte<4>(m);
+        h[i] *= mx_inv_scale(byte[i]);
+    }
+    const size_t row = (size_t)p.oatoms * (MX_ATOM * p.bits / 8);
+    uint8_t* at = p.codes + (size_t)t * row;
+    uint32_t q[2];
+    if (p.bits == 8) {
+        mx_enc8<8>(h, q);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < n) at[i * row + f] = (uint8_t)(q[i / 4] >> (8 * (i % 4)));
+    } else {
+        mx_enc8<4>(h, q);
+        const uint32_t next = __shfl_down_sync(0xffffffffu, q[0], 1);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < n && (lane & 1) == 0) at[i * row + f / 2] = (uint8_t)((q[0] >> (4 * i) & 15u) | (next >> (4 * i) & 15u) << 4);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (lane == i && i < n) p.scales[mx_scale_word(t + i, f / MX_ATOM, p.oatoms) + (f / MX_RUN & 3)] = (uint8_t)byte[i];
+}
+
+template <int XB, int WB, bool GLU, int BN>
+__global__ void __launch_bounds__(MF_THREADS) k_mx_gemm_few(const __grid_constant__ MfMaps m, const __grid_constant__ MfP p) {
+    constexpr bool F4 = XB == 4;
+    using C = MfCfg<F4, GLU, BN>;
+    constexpr int AT = C::AT, NW = C::NW;
+    constexpr uint32_t W_TX = WB == 4 && !F4 ? MG_W / 2 : MG_W;  // a spread tile counts its bytes in memory
+    constexpr int SF = NW * MG_W + BN * 128;                     // exponents of W, up and X in a stage
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::STAGES * C::STAGE);
+    uint64_t* empty = full + C::STAGES;
+    uint64_t* sready = empty + C::STAGES;
+    uint64_t* accf = sready + C::STAGES;  // [2] accumulator complete
+    uint64_t* acce = accf + 2;            // [2] accumulator read
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acce + 2);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int S = 1 << p.lsplits, z = S > 1 ? (int)cta_rank() : 0;
+    const int tw0 = blockIdx.x >> p.lsplits, step = S > 1 ? p.tiles_w : gridDim.x;  // this CTA's tiles; one if it shares it
+    const int nk_all = (p.atoms + AT - 1) / AT;
+    const int kb0 = (nk_all * z) >> p.lsplits, nk = ((nk_all * (z + 1)) >> p.lsplits) - kb0;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(smem_u32(full + s), 1);
+            mbar_init(smem_u32(empty + s), 1);
+            mbar_init(smem_u32(sready + s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_u32(accf + b), 1);
+            mbar_init(smem_u32(acce + b), 4);
+        }
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == 4 && lane == 0) {
+        tma_prefetch_desc(&m.a);
+        tma_prefetch_desc(&m.x);
+        if (GLU) tma_prefetch_desc(&m.b);
+    }
+    if (warp == 5) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(C::COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait();
+    pdl_launch();
+
+    if (warp == 4) {
+        if (lane == 0) {
+            uint32_t g = 0;
+            for (int tw = tw0; tw < p.tiles_w && !*abort_flag; tw += step)
+                for (int j = 0; j < nk; ++j, ++g) {
+                    const int s = g % C::STAGES, kb = kb0 + j;
+                    if (!wait_phase(smem_u32(empty + s), ((g / C::STAGES) & 1u) ^ 1u, abort_flag)) {
+                        *abort_flag = 1;
+                        break;
+                    }
+                    const uint32_t st = smem_u32(smem + s * C::STAGE), bar = smem_u32(full + s);
+                    const uint32_t n = (uint32_t)min(AT, p.atoms - kb * AT) * MX_TILE_BYTES;
+                    mbar_expect_tx(bar, NW * W_TX + BN * 128 + (NW + 1) * n);
+                    tma_load_2d(st, &m.a, bar, kb * 128, tw * 128);
+                    if (GLU) tma_load_2d(st + MG_W, &m.b, bar, kb * 128, tw * 128);
+                    tma_load_2d(st + NW * MG_W, &m.x, bar, kb * 128, 0);
+                    const size_t at = (size_t)kb * AT;
+                    bulk_load(st + SF, p.sa + ((size_t)tw * p.atoms + at) * MX_TILE_BYTES, n, bar);
+                    if (GLU) bulk_load(st + SF + MG_SF, p.sb + ((size_t)tw * p.atoms + at) * MX_TILE_BYTES, n, bar);
+                    bulk_load(st + SF + NW * MG_SF, p.sx + at * MX_TILE_BYTES, n, bar);
+                }
+        }
+        __syncwarp();
+    } else if (warp == 5) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = idesc_mx(F4 ? 1 : WB == 4 ? 5 : 0, F4 ? 1 : 0, 128, BN);
+            uint32_t g = 0;
+            int i = 0;
+            bool ok = true;
+            for (int tw = tw0; tw < p.tiles_w && ok; tw += step, ++i) {
+                const int buf = i & 1;
+                ok = wait_phase(smem_u32(acce + buf), ((uint32_t)(i >> 1) & 1u) ^ 1u, abort_flag);
+                const uint32_t d = tmem + buf * NW * BN;
+                for (int j = 0; j < nk && ok; ++j, ++g) {
+                    const int s = g % C::STAGES;
+                    ok = wait_phase(smem_u32(sready + s), (g / C::STAGES) & 1u, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t st = smem_u32(smem + s * C::STAGE), sf = tmem + C::SF_COL + s * C::SF_COLS;
+                    const int at = min(AT, p.atoms - (kb0 + j) * AT);
+                    const uint64_t xd = sw128_desc(st + NW * MG_W);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        // as in k_mx_gemm
+                        const int a = F4 ? k / 2 : 0;
+                        const uint32_t id = F4 ? (uint32_t)(k & 1) * 2 : (uint32_t)k;
+                        if (a >= at) continue;
+#pragma unroll
+                        for (int w = 0; w < NW; ++w)
+                            mma_mx<F4, false>(d + w * BN, sw128_desc(st + w * MG_W) + 2 * k, xd + 2 * k, idesc | (id << 4) | (id << 29),
+                                              sf + (w * AT + a) * 4, sf + (NW * AT + a) * 4, j > 0 || k > 0);
+                    }
+                    umma_commit(smem_u32(empty + s));
+                }
+                if (ok) umma_commit(smem_u32(accf + buf));
+            }
+            if (!ok) *abort_flag = 1;
+        }
+        __syncwarp();
+    } else if (warp == 6) {
+        if (lane == 0) {
+            const uint32_t total = (uint32_t)((p.tiles_w - tw0 + step - 1) / step) * nk;
+            for (uint32_t g = 0; g < total; ++g) {
+                const int s = g % C::STAGES;
+                if (!wait_phase(smem_u32(full + s), (g / C::STAGES) & 1u, abort_flag)) {
+                    *abort_flag = 1;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t from = smem_u32(smem + s * C::STAGE) + SF, to = tmem + C::SF_COL + s * C::SF_COLS;
+#pragma unroll
+                for (int w = 0; w <= NW; ++w)
+#pragma unroll
+                    for (int a = 0; a < AT; ++a) sf_copy<false>(to + (w * AT + a) * 4, from + w * MG_SF + a * MX_TILE_BYTES);
+                umma_commit(smem_u32(sready + s));
+            }
+        }
+        __syncwarp();
+    }
+    const int fl = warp * 32 + lane, ncols = p.T;
+    const uint32_t row = tmem + ((uint32_t)(warp * 32) << 16);
+    bool ok = true;
+    if (warp < 4) {
+        int i = 0;
+        for (int tw = tw0; tw < p.tiles_w; tw += step, ++i) {
+            const int buf = i & 1, f = tw * 128 + fl;
+            int got = 0;
+            if (lane == 0) got = wait_phase(smem_u32(accf + buf), (uint32_t)(i >> 1) & 1u, abort_flag);
+            ok = __shfl_sync(0xffffffffu, got, 0);
+            if (!ok) {
+                *abort_flag = 1;
+                break;
+            }
+            tc_fence_after();
+            if (S > 1) break;  // the sums of the others first
+            const uint32_t acc = row + buf * NW * BN;
+            for (int c0 = 0; c0 < ncols; c0 += 16) {
+                uint32_t r[NW][16];
+#pragma unroll
+                for (int w = 0; w < NW; ++w) TMEM_LD16(acc + w * BN + c0, r[w]);
+                tmem_wait_ld();
+                if (c0 + 16 >= ncols) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(acce + buf)) : "memory");
+                }
+                const float *a = reinterpret_cast<const float*>(r[0]), *b = reinterpret_cast<const float*>(r[NW - 1]);
+                if (ncols == 1) finish_few<GLU, 1>(p, 0, 1, f, a, b);
+                else finish_few<GLU, 8>(p, c0, ncols - c0, f, a, b);
+                if (c0 + 8 < ncols) finish_few<GLU, 8>(p, c0 + 8, ncols - c0 - 8, f, a + 8, b + 8);
+            }
+        }
+    }
+    if (S > 1) {
+        // partial sums [splits][own rows of X][NW][128], over the ring once every CTA of the cluster has done its MMAs
+        const int lown = (BN == 16 ? 4 : 6) - p.lsplits, own = 1 << lown, f = tw0 * 128 + fl;
+        const uint32_t red = smem_u32(smem);
+        cluster_sync();
+        if (warp < 4 && ok) {
+            for (int c0 = 0; c0 < ncols; c0 += 16) {
+                uint32_t r[NW][16];
+#pragma unroll
+                for (int g = 0; g < NW; ++g) TMEM_LD16(row + g * BN + c0, r[g]);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const int c = c0 + j;
+                    if (j && c >= ncols) continue;
+                    const uint32_t to = map_to(red + (((z << lown) + (c & (own - 1))) * NW * 128 + fl) * 4, (uint32_t)(c >> lown));
+#pragma unroll
+                    for (int g = 0; g < NW; ++g) asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(to + g * 512), "r"(r[g][j]) : "memory");
+                }
+            }
+        }
+        cluster_sync();
+        if (warp < 4 && ok) {
+            const float* part = reinterpret_cast<const float*>(smem);
+            const int mine = min(own, ncols - z * own);
+            if (ncols == 1) {
+                if (mine == 1) {
+                    float v[NW] = {};
+                    for (int s = 0; s < S; ++s)
+#pragma unroll
+                        for (int g = 0; g < NW; ++g) v[g] += part[((s << lown) * NW + g) * 128 + fl];
+                    finish_few<GLU, 1>(p, 0, 1, f, v, v + NW - 1);
+                }
+            } else {
+                for (int c = 0; c < mine; c += 8) {
+                    float v[NW][8] = {};
+                    for (int s = 0; s < S; ++s)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+#pragma unroll
+                            for (int g = 0; g < NW; ++g)
+                                if (c + i < mine) v[g][i] += part[(((s << lown) + c + i) * NW + g) * 128 + fl];
+                    finish_few<GLU, 8>(p, z * own + c, mine - c, f, v[0], v[NW - 1]);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0 && *abort_flag) atomicOr(p.status, QW_MX_TIMEOUT);
+    if (warp == 5) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::COLS) : "memory");
+    }
+}
+
 // ---- host ------------------------------------------------------------------------------------------------
 
 typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -457,19 +772,92 @@ bool encode_out(CUtensorMap* map, void* out, int rows, int cols, size_t ld, int 
                es == 4 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int sm_count() {  // of the current device
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 1;
-    return n;
+// The current device and its SMs; a kernel's shared memory is allowed once a device (these calls cost a microsecond
+// between them, a quarter of a small product).
+struct Device {
+    int id, sms;
+};
+Device device() {
+    static std::atomic<int> sms[64];
+    Device d = {0, 0};
+    if (cudaGetDevice(&d.id) != cudaSuccess) return {-1, 1};
+    if (d.id < 64) d.sms = sms[d.id].load(std::memory_order_relaxed);
+    if (d.sms == 0) {
+        if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, d.id) != cudaSuccess) return {-1, 1};
+        if (d.id < 64) sms[d.id].store(d.sms, std::memory_order_relaxed);
+    }
+    return d;
+}
+template <typename K>
+cudaError_t allow_smem(K kern, int bytes, const Device& d, std::atomic<unsigned long long>& done) {
+    const unsigned long long bit = d.id >= 0 && d.id < 64 ? 1ull << d.id : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
 }
 
 template <int XB, int WB, int OUT>
 cudaError_t launch_gemm(const MgMaps& m, const MxGemmP& p, cudaStream_t st) {
     constexpr int SMEM = MgCfg<OUT>::SMEM;
-    const cudaError_t e = cudaFuncSetAttribute(k_mx_gemm<XB, WB, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    static std::atomic<unsigned long long> done;
+    const Device d = device();
+    const cudaError_t e = allow_smem(k_mx_gemm<XB, WB, OUT>, SMEM, d, done);
     if (e != cudaSuccess) return e;
-    return launch_kc({st, true, nullptr}, k_mx_gemm<XB, WB, OUT>, dim3(2 * std::min(p.units, sm_count() / 2)), dim3(MG_THREADS),
+    return launch_kc({st, true, nullptr}, k_mx_gemm<XB, WB, OUT>, dim3(2 * std::min(p.units, std::max(d.sms / 2, 1))), dim3(MG_THREADS),
                      SMEM, 2, m, p);
+}
+
+template <int XB, int WB, bool GLU, int BN>
+cudaError_t launch_few(const MfMaps& m, const MfP& p, const Device& d, int slots, cudaStream_t st) {
+    constexpr int SMEM = MfCfg<XB == 4, GLU, BN>::SMEM;
+    const auto kern = k_mx_gemm_few<XB, WB, GLU, BN>;
+    static std::atomic<unsigned long long> done;
+    const cudaError_t e = allow_smem(kern, SMEM, d, done);
+    if (e != cudaSuccess) return e;
+    const LaunchCtx c = {st, true, nullptr};
+    return p.lsplits ? launch_kc(c, kern, dim3(p.tiles_w << p.lsplits), dim3(MF_THREADS), SMEM, 1u << p.lsplits, m, p)
+                     : launch_k(c, kern, dim3(std::min(p.tiles_w, slots)), dim3(MF_THREADS), SMEM, m, p);
+}
+
+template <int XB, int WB, bool GLU>
+cudaError_t launch_few_rows(const MfMaps& m, MfP& p, cudaStream_t st) {
+    const int nk = XB == 4 ? (p.atoms + 1) / 2 : p.atoms;
+    const Device d = device();
+    const int slots = d.sms * (GLU || p.T <= 16 ? MfCfg<XB == 4, GLU, 16>::PER_SM : MfCfg<XB == 4, false, 64>::PER_SM);
+    // the widest cluster whose CTAs all find a place and have two stages at least: one row by 4096 x 4096 5.0 us with 8 CTAs
+    // a tile, 7.4 with two, 11 with one; by 4096 x 1024 3.5 with four, 3.9 with 8 of one stage, 4.5 with one
+    p.lsplits = 0;
+    while (p.lsplits < 3 && (long long)p.tiles_w << (p.lsplits + 1) <= slots && 4 << p.lsplits <= nk) ++p.lsplits;
+    if constexpr (!GLU)
+        if (p.T > 16) return launch_few<XB, WB, GLU, 64>(m, p, d, slots, st);
+    return launch_few<XB, WB, GLU, 16>(m, p, d, slots, st);
+}
+
+template <bool GLU>
+cudaError_t launch_few_formats(int xb, int wb, const MfMaps& m, MfP& p, cudaStream_t st) {
+    return xb == 4   ? launch_few_rows<4, 4, GLU>(m, p, st)
+           : wb == 4 ? launch_few_rows<8, 4, GLU>(m, p, st)
+                     : launch_few_rows<8, 8, GLU>(m, p, st);
+}
+
+// Whether k_mx_gemm_few serves a product. Measured against k_mx_gemm (us): linear, 64 rows by 4096 x 4096 8.1 and 13.5, by 151936 x 1024
+// 25 and 38; SwiGLU, 16 rows by 3072 x 1024 5.5 and 6.7, 64 rows 8.9 and 6.8 (its runs lie across lanes here).
+bool few(int T, bool glu) { return T <= (glu ? 16 : 64); }
+
+bool product_few(const qw_mx& x, const qw_mx& wa, const qw_mx& wb, bool glu, int32_t* status, MfP& p, MfMaps& m) {
+    p = MfP{};
+    p.T = x.rows;
+    p.M = wa.rows;
+    p.atoms = (int)mx_atoms(x.cols);
+    p.oatoms = (int)mx_atoms(wa.rows);
+    p.tiles_w = p.oatoms;
+    p.sx = (const uint8_t*)x.dev_scales;
+    p.sa = (const uint8_t*)wa.dev_scales;
+    p.sb = (const uint8_t*)wb.dev_scales;
+    p.status = status;
+    const bool spread = wa.bits == 4 && x.bits == 8;
+    return encode(&m.x, x, false, p.T <= 16 ? 16 : 64) && encode(&m.a, wa, spread, 128) && (!glu || encode(&m.b, wb, spread, 128));
 }
 
 template <int OUT>
@@ -501,8 +889,10 @@ bool product(const qw_mx& x, const qw_mx& wa, const qw_mx& wb, bool glu, int32_t
     p.status = status;
     const bool spread = wa.bits == 4 && x.bits == 8;
     const unsigned at = x.bits == 4 ? 2 : 1;
-    return encode(&m.x, x, false, 128) && encode(&m.a, wa, spread, 128) && encode(&m.b, wb, spread, 128) &&
-           encode_scales(&m.sx, x, at) && encode_scales(&m.sa, wa, at) && encode_scales(&m.sb, wb, at);
+    if (!encode(&m.x, x, false, 128) || !encode(&m.a, wa, spread, 128) || !encode_scales(&m.sx, x, at) || !encode_scales(&m.sa, wa, at)) return false;
+    m.b = m.a;
+    m.sb = m.sa;
+    return !glu || (encode(&m.b, wb, spread, 128) && encode_scales(&m.sb, wb, at));
 }
 
 qw_status done(cudaError_t e, const char* what) {
@@ -528,6 +918,15 @@ extern "C" qw_status qw_mx_linear(const qw_mx* x, const qw_mx* w, void* dev_out,
     if (((uintptr_t)dev_out & 15) || ld_out % (dtype == QW_F32 ? 4 : 8))
         return qw_fail(QW_ERR_INVALID_ARG, "%s: rows of out not 16-byte aligned", what);
     if (too_many(x->rows, w->rows)) return qw_fail(QW_ERR_UNSUPPORTED, "%s: more than 2^31 tiles", what);
+    if (few(x->rows, false)) {
+        MfP p;
+        MfMaps m;
+        if (!product_few(*x, *w, *w, false, dev_status, p, m)) return qw_fail(QW_ERR_CUDA, "%s: tensor map", what);
+        p.dtype = dtype;
+        p.out = dev_out;
+        p.ld = ld_out;
+        return done(launch_few_formats<false>(x->bits, w->bits, m, p, (cudaStream_t)stream), what);
+    }
     MxGemmP p;
     MgMaps m;
     if (!product(*x, *w, *w, false, dev_status, p, m) || !encode_out(&m.out, dev_out, p.T, p.M, ld_out, dtype))
@@ -557,6 +956,15 @@ extern "C" qw_status qw_mx_swiglu(const qw_mx* x, const qw_mx* w_gate, const qw_
     if (!dev_status) return qw_fail(QW_ERR_INVALID_ARG, "%s: NULL status", what);
     if (x->rows == 0) return QW_OK;
     if (too_many(x->rows, w_gate->rows)) return qw_fail(QW_ERR_UNSUPPORTED, "%s: more than 2^31 tiles", what);
+    if (few(x->rows, true)) {
+        MfP p;
+        MfMaps m;
+        if (!product_few(*x, *w_gate, *w_up, true, dev_status, p, m)) return qw_fail(QW_ERR_CUDA, "%s: tensor map", what);
+        p.bits = out->bits;
+        p.codes = (uint8_t*)out->dev_codes;
+        p.scales = (uint8_t*)out->dev_scales;
+        return done(launch_few_formats<true>(x->bits, w_gate->bits, m, p, (cudaStream_t)stream), what);
+    }
     MxGemmP p;
     MgMaps m;
     if (!product(*x, *w_gate, *w_up, true, dev_status, p, m)) return qw_fail(QW_ERR_CUDA, "%s: tensor map", what);
