@@ -228,14 +228,14 @@ __global__ void __launch_bounds__(MG_THREADS, 1) k_mx_gemm(const __grid_constant
     constexpr bool GLU = C::GLU;
     constexpr int AT = F4 ? 2 : 1;                               // atoms of 128 columns a stage
     constexpr uint32_t W_TX = WB == 4 && !F4 ? MG_W / 2 : MG_W;  // a spread tile counts its bytes in memory
-    constexpr uint32_t TX = 2 * (MG_X + W_TX + 3 * AT * MX_TILE_BYTES);  // both CTAs' copies of a stage
+    constexpr uint32_t TX = 2 * (MG_X + W_TX), SF_TX = 2 * 3 * AT * MX_TILE_BYTES;  // both CTAs' copies of a stage
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     uint8_t* boxes = smem + C::STAGES * MG_STAGE;
-    uint64_t* full = reinterpret_cast<uint64_t*>(boxes + 16 * C::BOX);
+    uint64_t* full = reinterpret_cast<uint64_t*>(boxes + 16 * C::BOX);  // codes here, exponents in tensor memory (the leader's)
     uint64_t* empty = full + C::STAGES;
-    uint64_t* sready = empty + C::STAGES;  // the stage's exponents are in tensor memory (the leader's)
-    uint64_t* accf = sready + C::STAGES;
+    uint64_t* sfull = empty + C::STAGES;  // exponents in shared memory (the leader's)
+    uint64_t* accf = sfull + C::STAGES;
     uint64_t* acce = accf + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acce + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -245,9 +245,9 @@ __global__ void __launch_bounds__(MG_THREADS, 1) k_mx_gemm(const __grid_constant
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
-            mbar_init(smem_u32(full + s), 1);
+            mbar_init(smem_u32(full + s), 2);  // the producer, and the copies of exponents when they are complete
             mbar_init(smem_u32(empty + s), 1);
-            mbar_init(smem_u32(sready + s), 1);
+            mbar_init(smem_u32(sfull + s), 1);
         }
         mbar_init(smem_u32(accf), 1);
         mbar_init(smem_u32(acce), 16);  // the epilogue warps of both CTAs
@@ -287,14 +287,18 @@ __global__ void __launch_bounds__(MG_THREADS, 1) k_mx_gemm(const __grid_constant
                         *abort_flag = 1;
                         break;
                     }
-                    const uint32_t st = smem_u32(smem + s * MG_STAGE), sf = st + MG_X + MG_W, bar = map_to(smem_u32(full + s), 0);
-                    if (rank == 0) mbar_expect_tx(smem_u32(full + s), TX);
+                    const uint32_t st = smem_u32(smem + s * MG_STAGE), sf = st + MG_X + MG_W;
+                    const uint32_t bar = map_to(smem_u32(full + s), 0), sbar = map_to(smem_u32(sfull + s), 0);
+                    if (rank == 0) {
+                        mbar_expect_tx(smem_u32(sfull + s), SF_TX);
+                        mbar_expect_tx(smem_u32(full + s), TX);
+                    }
                     // rows and tiles past a matrix's end arrive as zeros
+                    tma_load_2d_pair(sf, &m.sx, sbar, 0, tx * p.atoms + kb * AT);
+                    tma_load_2d_pair(sf + MG_SF, &m.sa, sbar, 0, (wa >> 7) * p.atoms + kb * AT);
+                    tma_load_2d_pair(sf + 2 * MG_SF, &m.sb, sbar, 0, (wb >> 7) * p.atoms + kb * AT);
                     tma_load_2d_pair(st, &m.x, bar, kb * 128, tx * 128);
                     tma_load_2d_pair(st + MG_X, rank ? &m.b : &m.a, bar, kb * 128, rank ? wb : wa);
-                    tma_load_2d_pair(sf, &m.sx, bar, 0, tx * p.atoms + kb * AT);
-                    tma_load_2d_pair(sf + MG_SF, &m.sa, bar, 0, (wa >> 7) * p.atoms + kb * AT);
-                    tma_load_2d_pair(sf + 2 * MG_SF, &m.sb, bar, 0, (wb >> 7) * p.atoms + kb * AT);
                 }
             }
         }
@@ -309,7 +313,7 @@ __global__ void __launch_bounds__(MG_THREADS, 1) k_mx_gemm(const __grid_constant
                 ok = wait_phase(smem_u32(acce), ((uint32_t)i & 1u) ^ 1u, abort_flag);
                 for (int kb = 0; kb < nk && ok; ++kb, ++g) {
                     const int s = g % C::STAGES;
-                    ok = wait_phase(smem_u32(sready + s), (g / C::STAGES) & 1u, abort_flag);
+                    ok = wait_phase(smem_u32(full + s), (g / C::STAGES) & 1u, abort_flag);
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t st = smem_u32(smem + s * MG_STAGE);
@@ -337,7 +341,7 @@ __global__ void __launch_bounds__(MG_THREADS, 1) k_mx_gemm(const __grid_constant
             const uint32_t total = (uint32_t)((p.units - pair + pairs - 1) / pairs) * nk;
             for (uint32_t g = 0; g < total; ++g) {
                 const int s = g % C::STAGES;
-                if (!wait_phase(smem_u32(full + s), (g / C::STAGES) & 1u, abort_flag)) {
+                if (!wait_phase(smem_u32(sfull + s), (g / C::STAGES) & 1u, abort_flag)) {
                     *abort_flag = 1;
                     break;
                 }
@@ -349,7 +353,7 @@ __global__ void __launch_bounds__(MG_THREADS, 1) k_mx_gemm(const __grid_constant
                     sf_copy<true>(to + 8 + 8 * a, sf + MG_SF + a * MX_TILE_BYTES);
                     sf_copy<true>(to + 8 + 8 * a + 4, sf + 2 * MG_SF + a * MX_TILE_BYTES);
                 }
-                commit_here(smem_u32(sready + s));
+                commit_here(smem_u32(full + s));
             }
         }
         __syncwarp();
@@ -510,8 +514,8 @@ __global__ void __launch_bounds__(MF_THREADS) k_mx_gemm_few(const __grid_constan
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::STAGES * C::STAGE);
     uint64_t* empty = full + C::STAGES;
-    uint64_t* sready = empty + C::STAGES;
-    uint64_t* accf = sready + C::STAGES;  // [2] accumulator complete
+    uint64_t* sfull = empty + C::STAGES;
+    uint64_t* accf = sfull + C::STAGES;   // [2] accumulator complete
     uint64_t* acce = accf + 2;            // [2] accumulator read
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acce + 2);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -523,9 +527,9 @@ __global__ void __launch_bounds__(MF_THREADS) k_mx_gemm_few(const __grid_constan
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
-            mbar_init(smem_u32(full + s), 1);
+            mbar_init(smem_u32(full + s), 2);
             mbar_init(smem_u32(empty + s), 1);
-            mbar_init(smem_u32(sready + s), 1);
+            mbar_init(smem_u32(sfull + s), 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_u32(accf + b), 1);
@@ -562,16 +566,17 @@ __global__ void __launch_bounds__(MF_THREADS) k_mx_gemm_few(const __grid_constan
                         *abort_flag = 1;
                         break;
                     }
-                    const uint32_t st = smem_u32(smem + s * C::STAGE), bar = smem_u32(full + s);
+                    const uint32_t st = smem_u32(smem + s * C::STAGE), bar = smem_u32(full + s), sbar = smem_u32(sfull + s);
                     const uint32_t n = (uint32_t)min(AT, p.atoms - kb * AT) * MX_TILE_BYTES;
-                    mbar_expect_tx(bar, NW * W_TX + BN * 128 + (NW + 1) * n);
+                    mbar_expect_tx(sbar, (NW + 1) * n);
+                    mbar_expect_tx(bar, NW * W_TX + BN * 128);
+                    const size_t at = (size_t)kb * AT;
+                    bulk_load(st + SF, p.sa + ((size_t)tw * p.atoms + at) * MX_TILE_BYTES, n, sbar);
+                    if (GLU) bulk_load(st + SF + MG_SF, p.sb + ((size_t)tw * p.atoms + at) * MX_TILE_BYTES, n, sbar);
+                    bulk_load(st + SF + NW * MG_SF, p.sx + at * MX_TILE_BYTES, n, sbar);
                     tma_load_2d(st, &m.a, bar, kb * 128, tw * 128);
                     if (GLU) tma_load_2d(st + MG_W, &m.b, bar, kb * 128, tw * 128);
                     tma_load_2d(st + NW * MG_W, &m.x, bar, kb * 128, 0);
-                    const size_t at = (size_t)kb * AT;
-                    bulk_load(st + SF, p.sa + ((size_t)tw * p.atoms + at) * MX_TILE_BYTES, n, bar);
-                    if (GLU) bulk_load(st + SF + MG_SF, p.sb + ((size_t)tw * p.atoms + at) * MX_TILE_BYTES, n, bar);
-                    bulk_load(st + SF + NW * MG_SF, p.sx + at * MX_TILE_BYTES, n, bar);
                 }
         }
         __syncwarp();
@@ -587,7 +592,7 @@ __global__ void __launch_bounds__(MF_THREADS) k_mx_gemm_few(const __grid_constan
                 const uint32_t d = tmem + buf * NW * BN;
                 for (int j = 0; j < nk && ok; ++j, ++g) {
                     const int s = g % C::STAGES;
-                    ok = wait_phase(smem_u32(sready + s), (g / C::STAGES) & 1u, abort_flag);
+                    ok = wait_phase(smem_u32(full + s), (g / C::STAGES) & 1u, abort_flag);
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t st = smem_u32(smem + s * C::STAGE), sf = tmem + C::SF_COL + s * C::SF_COLS;
@@ -616,7 +621,7 @@ __global__ void __launch_bounds__(MF_THREADS) k_mx_gemm_few(const __grid_constan
             const uint32_t total = (uint32_t)((p.tiles_w - tw0 + step - 1) / step) * nk;
             for (uint32_t g = 0; g < total; ++g) {
                 const int s = g % C::STAGES;
-                if (!wait_phase(smem_u32(full + s), (g / C::STAGES) & 1u, abort_flag)) {
+                if (!wait_phase(smem_u32(sfull + s), (g / C::STAGES) & 1u, abort_flag)) {
                     *abort_flag = 1;
                     break;
                 }
@@ -626,7 +631,7 @@ __global__ void __launch_bounds__(MF_THREADS) k_mx_gemm_few(const __grid_constan
                 for (int w = 0; w <= NW; ++w)
 #pragma unroll
                     for (int a = 0; a < AT; ++a) sf_copy<false>(to + (w * AT + a) * 4, from + w * MG_SF + a * MX_TILE_BYTES);
-                umma_commit(smem_u32(sready + s));
+                umma_commit(smem_u32(full + s));
             }
         }
         __syncwarp();
