@@ -1,9 +1,11 @@
 // Microscaled matrices: quantisation of rows (qw_mx_quantize), their values (qw_mx_read) and RMSNorm with
 // the branch's addition and a quantised output (qw_mx_rmsnorm). mx.cuh states the format.
 //
-// Quantise and read. A thread has 8 columns, four a run, sixteen a row's scale word. The exponent follows
-// from the largest magnitude alone and x 2^-e is exact, so the codes are those of the definition bit for
-// bit. Bytes bound both: a warp of a large matrix asks for four pieces of 256 columns before it uses one.
+// Quantise. A thread has 8 columns of a run of 32, or 16 in a large matrix, where the instructions around the values
+// would otherwise bound the kernel (ALU: 69 of 132 instructions a thread's 8 values). The exponent follows from the
+// largest magnitude alone and x 2^-e is exact, so the codes are those of the definition bit for bit. Read. A thread
+// has 8 columns; a warp of a large matrix asks for four pieces of 256 before it uses one. Bytes bound both: 151936 x 1024
+// from bf16 to 4 bits 64 us, 6.1 TB/s, and back 67 us.
 //
 // RMSNorm. s = x + add rounded to the stream's type, y = s / sqrt(mean(s^2) + eps) * w, codes of y. y has no
 // type of its own: the codes are those of the real y, whatever the order of the sums. y is computed in fp32 with a
@@ -20,20 +22,22 @@ namespace {
 
 constexpr int MQ_WARPS = 8;
 
-// Four bytes of a run's first lane (lanes 0, 4, 8, 12 of each half warp) as a word, in the half warp's lane 0.
+// The bytes of four runs as a word, in the first lane of each group that has 128 columns, V a lane.
+template <int V>
 __device__ __forceinline__ uint32_t mx_gather_word(int byte) {
     uint32_t w = (uint32_t)byte;
-    w |= __shfl_down_sync(0xffffffffu, w, 4) << 8;
-    return w | (__shfl_down_sync(0xffffffffu, w, 8) << 16);
+    w |= __shfl_down_sync(0xffffffffu, w, 32 / V) << 8;
+    return w | (__shfl_down_sync(0xffffffffu, w, 64 / V) << 16);
 }
 
-// A warp's pieces of 256 columns in row order: one division, then steps.
+// A warp's pieces of 32 V columns in row order: one division, then steps.
+template <int V>
 struct Piece {
     int row, c;  // this lane's first column
-    __device__ __forceinline__ Piece(unsigned u, unsigned per_row, int lane) : row((int)(u / per_row)), c((int)(u % per_row) * 256 + lane * 8) {}
+    __device__ __forceinline__ Piece(unsigned u, unsigned per_row, int lane) : row((int)(u / per_row)), c((int)(u % per_row) * 32 * V + lane * V) {}
     __device__ __forceinline__ void next(unsigned per_row, int lane) {
-        c += 256;
-        if (c >= (int)per_row * 256) c = lane * 8, ++row;
+        c += 32 * V;
+        if (c >= (int)per_row * 32 * V) c = lane * V, ++row;
     }
 };
 
@@ -44,58 +48,60 @@ struct MxRowsP {
     const void* src;
     void* dst;
     size_t ld;
-    unsigned units, per_row;  // warps' pieces of 256 columns
+    unsigned units, per_row;  // warps' pieces
 };
 
-// U neighbouring pieces a warp.
-template <int DT, int BITS, int U>
+template <int DT, int BITS, int V>
 __global__ void __launch_bounds__(MQ_WARPS * 32) k_mx_quantize(const __grid_constant__ MxRowsP p) {
+    constexpr int G = V / 8;  // groups of 8 columns a lane
     pdl_wait();
     pdl_launch();
-    const unsigned u0 = (blockIdx.x * MQ_WARPS + (threadIdx.x >> 5)) * U;
+    const unsigned u = blockIdx.x * MQ_WARPS + (threadIdx.x >> 5);
+    if (u >= p.units) return;
     const int lane = threadIdx.x & 31;
-    const Piece first(u0, p.per_row, lane);
-    Piece t = first;
-    MxRaw raw[U];
+    const Piece<V> t(u, p.per_row, lane);
+    const size_t from = (size_t)t.row * p.ld + t.c;
+    const int left = p.cols - t.c;
+    MxRaw raw[G];
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-        raw[k] = mx_fetch8<DT>(p.src, (size_t)t.row * p.ld + t.c, u0 + k < p.units ? p.cols - t.c : 0);
-        t.next(p.per_row, lane);
+    for (int g = 0; g < G; ++g) raw[g] = mx_fetch8<DT>(p.src, from + 8 * g, left - 8 * g);
+    uint32_t m = 0;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        mx_fill8<DT>(p.src, from + 8 * g, left - 8 * g, raw[g]);
+        m = max(m, mx_absmax8<DT>(raw[g]));
     }
-    t = first;
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    if (V == 8) m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const int byte = mx_exp_byte<BITS>(m);
+    const float inv = mx_inv_scale(byte);
+    uint32_t w[2 * G];
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-        mx_fill8<DT>(p.src, (size_t)t.row * p.ld + t.c, u0 + k < p.units ? p.cols - t.c : 0, raw[k]);
-        uint32_t m = mx_absmax8<DT>(raw[k]);
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        const int byte = mx_exp_byte<BITS>(m);
-        const float inv = mx_inv_scale(byte);
+    for (int g = 0; g < G; ++g) {
         float x[8];
-        mx_unpack8<DT>(raw[k], x);
+        mx_unpack8<DT>(raw[g], x);
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] *= inv;
-        uint32_t w[2];
-        mx_enc8<BITS>(x, w);
-        const uint32_t sw = mx_gather_word(byte);
-        if (u0 + k < p.units && t.c < p.atoms * MX_ATOM) {
-            uint8_t* at = p.codes + (size_t)t.row * p.atoms * (MX_ATOM * BITS / 8) + (size_t)t.c * BITS / 8;
-            if (BITS == 8) *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
-            else *reinterpret_cast<uint32_t*>(at) = w[0];
-            if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(p.scales + mx_scale_word(t.row, t.c / MX_ATOM, p.atoms)) = sw;
-        }
-        t.next(p.per_row, lane);
+        mx_enc8<BITS>(x, w + g * (BITS / 4));
     }
+    const uint32_t sw = mx_gather_word<V>(byte);
+    if (t.c >= p.atoms * MX_ATOM) return;
+    uint8_t* at = p.codes + (size_t)t.row * p.atoms * (MX_ATOM * BITS / 8) + (size_t)t.c * BITS / 8;
+    if (V * BITS == 128) *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2 * G - 2], w[2 * G - 1]);
+    else if (V * BITS == 64) *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t*>(at) = w[0];
+    if (lane % (128 / V) == 0) *reinterpret_cast<uint32_t*>(p.scales + mx_scale_word(t.row, t.c / MX_ATOM, p.atoms)) = sw;
 }
 
+// U neighbouring pieces a warp.
 template <int DT, int BITS, int U>
 __global__ void __launch_bounds__(MQ_WARPS * 32) k_mx_read(const __grid_constant__ MxRowsP p) {
     pdl_wait();
     pdl_launch();
     const unsigned u0 = (blockIdx.x * MQ_WARPS + (threadIdx.x >> 5)) * U;
     const int lane = threadIdx.x & 31;
-    const Piece first(u0, p.per_row, lane);
-    Piece t = first;
+    const Piece<8> first(u0, p.per_row, lane);
+    Piece<8> t = first;
     uint32_t w[U][2];
     uint8_t e[U];
 #pragma unroll
@@ -318,7 +324,7 @@ __device__ __forceinline__ void norm_store(const MxNormP& p, size_t row, int v, 
     else *reinterpret_cast<uint32_t*>(at) = q[0];
 }
 __device__ __forceinline__ void norm_store_scales(const MxNormP& p, size_t row, int v, bool ok, int byte) {
-    const uint32_t sw = mx_gather_word(byte);
+    const uint32_t sw = mx_gather_word<8>(byte);
     if (ok && (threadIdx.x & 15) == 0) *reinterpret_cast<uint32_t*>(p.scales + mx_scale_word((int)row, v / 16, p.atoms)) = sw;
 }
 
@@ -529,22 +535,31 @@ qw_status rows_check(const void* x, size_t ld, int dtype, int cols, const char* 
 }
 
 MxRowsP rows_p(const qw_mx* m, const void* src, void* dst, size_t ld) {
-    const int atoms = (int)mx_atoms(m->cols);
-    const unsigned per = (unsigned)(atoms + 1) / 2;
-    return {(uint8_t*)m->dev_codes, (uint8_t*)m->dev_scales, m->rows, m->cols, atoms, src, dst, ld, (unsigned)m->rows * per, per};
+    return {(uint8_t*)m->dev_codes, (uint8_t*)m->dev_scales, m->rows, m->cols, (int)mx_atoms(m->cols), src, dst, ld, 0, 0};
 }
 
 qw_status done(cudaError_t e, const char* what) {
     return e == cudaSuccess ? QW_OK : qw_fail(QW_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-// Matrices of more than a wave of CTAs: four pieces a warp.
-bool many(const MxRowsP& p) { return p.units >= 8192u; }
-
+// `atoms` of 128 columns a piece, `pieces` a warp.
 template <typename K>
-cudaError_t launch_rows(K one, K four, const MxRowsP& p, cudaStream_t st) {
-    const unsigned per = MQ_WARPS * (many(p) ? 4 : 1);
-    return launch_k({st, true, nullptr}, many(p) ? four : one, dim3((p.units - 1) / per + 1), dim3(MQ_WARPS * 32), 0, p);
+cudaError_t launch_rows(K kern, MxRowsP p, unsigned atoms, unsigned pieces, cudaStream_t st) {
+    p.per_row = ((unsigned)p.atoms + atoms - 1) / atoms;
+    p.units = (unsigned)p.rows * p.per_row;
+    return launch_k({st, true, nullptr}, kern, dim3((p.units - 1) / (MQ_WARPS * pieces) + 1), dim3(MQ_WARPS * 32), 0, p);
+}
+// From some waves of CTAs on. Measured (us): 64 x 2048 from fp16 to 8 bits 1.3 small; 1024 x 2048 2.4 small, 2.3 large; 8192 x 2048
+// 12.1 and 8.9; 151936 x 1024 from bf16 to 4 bits 99 and 64.
+bool large(const MxRowsP& p) { return (double)p.rows * p.atoms >= 16384.0; }
+
+template <int DT, int BITS>
+cudaError_t launch_quantize(const MxRowsP& p, cudaStream_t st) {
+    return large(p) ? launch_rows(k_mx_quantize<DT, BITS, 16>, p, 4, 1, st) : launch_rows(k_mx_quantize<DT, BITS, 8>, p, 2, 1, st);
+}
+template <int DT, int BITS>
+cudaError_t launch_read(const MxRowsP& p, cudaStream_t st) {
+    return large(p) ? launch_rows(k_mx_read<DT, BITS, 4>, p, 2, 4, st) : launch_rows(k_mx_read<DT, BITS, 1>, p, 2, 1, st);
 }
 
 template <int DT, int BITS>
@@ -593,7 +608,7 @@ extern "C" qw_status qw_mx_quantize(const qw_mx* out, const void* dev_x, size_t 
     if (qw_status s = rows_check(dev_x, ld_x, dtype, out->cols, "mx_quantize", "x")) return s;
     const MxRowsP p = rows_p(out, dev_x, nullptr, ld_x);
     const cudaStream_t st = (cudaStream_t)stream;
-#define MX_Q(dt, bits) launch_rows(k_mx_quantize<dt, bits, 1>, k_mx_quantize<dt, bits, 4>, p, st)
+#define MX_Q(dt, bits) launch_quantize<dt, bits>(p, st)
     return done(MX_DISPATCH(MX_Q, dtype, out->bits), "mx_quantize");
 }
 
@@ -603,7 +618,7 @@ extern "C" qw_status qw_mx_read(const qw_mx* m, void* dev_x, size_t ld_x, int dt
     if (qw_status s = rows_check(dev_x, ld_x, dtype, m->cols, "mx_read", "x")) return s;
     const MxRowsP p = rows_p(m, nullptr, dev_x, ld_x);
     const cudaStream_t st = (cudaStream_t)stream;
-#define MX_R(dt, bits) launch_rows(k_mx_read<dt, bits, 1>, k_mx_read<dt, bits, 4>, p, st)
+#define MX_R(dt, bits) launch_read<dt, bits>(p, st)
     return done(MX_DISPATCH(MX_R, dtype, m->bits), "mx_read");
 }
 

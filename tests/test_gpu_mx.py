@@ -276,6 +276,50 @@ def test_linear(lib, T, K, M, dtype, xb, wb):
     _check_product(got, x.held, w.held, dtype)
 
 
+def _device_matrix(lib, rows, cols, bits, seed):
+    """A random matrix quantised on the GPU, and a function that reads some of its rows back in 64 bits."""
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn((rows, -(-cols // 8) * 8), generator=gen, device="cuda", dtype=torch.float16)
+    m = Matrix(lib, rows, cols, bits)
+    lib.qw_mx_quantize(m.view, x.data_ptr(), x.stride(0), lib.QW_F16)
+    v = torch.empty_like(x, dtype=torch.float32)
+    lib.qw_mx_read(m.view, v.data_ptr(), v.stride(0), lib.QW_F32)
+    m.keep, m.written = x, True
+    return m, lambda idx: v[torch.as_tensor(idx, device="cuda")][:, :cols].double().cpu().numpy()
+
+
+@pytest.mark.parametrize("xb,wb", FORMATS)
+@pytest.mark.parametrize("T,K,M", [(1, 130, 70000), (16, 260, 45000), (17, 384, 50001), (64, 128, 90001), (65, 300, 30000),
+                                   (2600, 260, 2300), (1500, 1100, 4000)])
+def test_linear_many_tiles(lib, T, K, M, xb, wb):
+    """More tiles than places: CTAs walk several, with their rings and accumulators wrapping. Some columns against 64 bits."""
+    x, xr = _device_matrix(lib, T, K, xb, 1)
+    w, wr = _device_matrix(lib, M, K, wb, 2)
+    for dtype in (F32, BF16):
+        got = _linear(lib, x, w, dtype)
+        t = np.unique(np.linspace(0, T - 1, 40).astype(int))
+        m = np.unique(np.concatenate([np.linspace(0, M - 1, 500).astype(int), np.arange(max(0, M - 140), M)]))
+        _check_product(got[t][:, m].double().cpu().numpy(), xr(t), wr(m), dtype)
+        assert bool(got.isfinite().all())
+
+
+@pytest.mark.parametrize("xb,wb", FORMATS)
+@pytest.mark.parametrize("T,K,I", [(1, 130, 45000), (16, 256, 40001), (17, 128, 20000), (2600, 260, 1200)])
+def test_swiglu_many_tiles(lib, T, K, I, xb, wb):
+    x, xr = _device_matrix(lib, T, K, xb, 1)
+    g, gr = _device_matrix(lib, I, K, wb, 2)
+    u, ur = _device_matrix(lib, I, K, wb, 3)
+    m = _swiglu(lib, x, g, u, 8)
+    c, e = m.get()
+    runs = np.unique(np.concatenate([np.linspace(0, I // 32 - 1, 30).astype(int), [-(-I // 32) - 1]]))
+    t = np.unique(np.linspace(0, T - 1, 30).astype(int))
+    for j in runs:  # a run of 32 features at a time
+        f = np.arange(32 * j, min(32 * j + 32, I))
+        part = type("Part", (), {"bits": 8, "values": lambda self: mx.values(c[t][:, j:j + 1], e[t][:, j:j + 1], 8, len(f))})()
+        _check_swiglu(part, xr(t), gr(f), ur(f))
+
+
 @pytest.mark.parametrize("xb,wb", FORMATS)
 @pytest.mark.parametrize("T", [2, 40, 200])
 def test_linear_nan_stays_in_its_row(lib, T, xb, wb):
@@ -463,6 +507,50 @@ def test_two_streams_and_threads(lib):
     assert not errors
     for layer, w in zip(layers, want):
         assert all(torch.equal(a, b) for a, b in zip(w, layer.outputs()))
+
+
+def test_beside_a_model(qw):
+    """A model's prefill and decode on one stream, a layer of products on another: kernels that share SMs and their
+    tensor memory, clusters among them."""
+    import threading
+
+    import torch
+
+    import synth
+    from gpu_util import Run, engine
+    lib = qw.qw
+    layers = [Layer(lib, t, 512, 384, 1000, 8, 4, seed=t) for t in (3, 600)]
+    want = []
+    for layer in layers:
+        layer.run()
+        want.append(layer.outputs())
+    eng = engine(qw, synth.ONE_BLOCK, max_tokens=256, max_batch=16, max_context=512, kv_pages=256)
+    r = Run(qw, eng)
+    prompt = [list(np.random.default_rng(b).integers(0, synth.ONE_BLOCK.vocab, 16)) for b in range(12)]
+    errors = []
+
+    def work():
+        try:
+            s = torch.cuda.Stream()
+            for _ in range(30):
+                for layer in layers:
+                    layer.run(s)
+            s.synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+    th = threading.Thread(target=work)
+    th.start()
+    for i in range(4):
+        r.prefill(list(range(12)), prompt, debug=False, logits=False, reserve_extra=8)
+        for _ in range(4):
+            r.decode(list(range(12)), [5] * 12, debug=False, logits=False)
+        lib.qw_kv_reset(eng.kv, -1, eng.stream)
+    th.join()
+    assert not errors
+    for layer, w in zip(layers, want):
+        assert all(torch.equal(a, b) for a, b in zip(w, layer.outputs()))
+        assert int(layer.status.item()) == 0
+    eng.close()
 
 
 def test_rows_do_not_depend_on_the_others(lib):
