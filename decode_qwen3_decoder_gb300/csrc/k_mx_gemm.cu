@@ -8,18 +8,35 @@
 // to tensor memory by tcgen05.cp, in columns of their ring stage: a stage is refilled only after its MMAs, so no
 // exponent is overwritten under an MMA.
 //
+// What the threads of a CTA do follows from three measurements (8192 x 8192 x 8192, 4 by 4 bits unless said; us):
+// - The thread that issues tcgen05.cp waits for nothing the MMAs wait for, and issues none: its waits for shared memory
+//   stand behind its copies (a stage of four MMAs 513 cycles alone, 643 to 810 with six copies and a wait in the same
+//   thread). Copies from a thread of their own are hidden: 278 with one thread, 176 with two, as without any copy.
+// - Waits sleep in the barrier (try_wait with a long limit): polling warps take shared-memory cycles from the MMAs,
+//   whose operands and the copies of the next ones need nearly all of them. Polling waits in the three threads 8 by 4
+//   bits 348 to 360, sleeping 293.
+// - Accumulators are handed back by relaxed arrivals between tcgen05 fences: an arrival that releases all memory to the
+//   cluster takes 0.4 us.
+// That leaves 640 cycles a stage instead of 512, with every stage's data there when it is asked for: copies write 35 KB into
+// shared memory while the MMAs read 32 KB from it. 161 us in 4 by 4 bits (6.8 PFLOP/s), 293 in 8 by 4 (3.8), 340 in 8 by 8.
+//
 // k_mx_gemm. A pair of CTAs on two SMs (tcgen05.mma.cta_group::2) has a tile of 256 rows of X (M; a TMEM lane a
 // row, 128 in each CTA) by 256 of W (N): two neighbouring tiles of 128 for the linear product; the same 128 features
 // of gate and up for SwiGLU, so that a thread has both of a feature, and the 32 features of a run, in its
 // registers. Each CTA loads its own 128 rows of X and one of the two W tiles, both the exponents of all of W.
-// Persistent; 8 epilogue warps, one producer, one MMA issuer and one copier of exponents (the leader's).
+// Persistent; 8 epilogue warps read a finished accumulator at once (130 cycles) and convert and store it from registers
+// under the next tile's MMAs; the hand-over between tiles takes 750 cycles, an eighth of a tile of 1024 columns. A second
+// accumulator would leave no tensor memory for exponents; tiles of 192 columns with two were slower (248 us above).
 //
 // k_mx_gemm_few. For few rows of X: W's rows are the M (128 of them, of gate and of up for SwiGLU), X's the N
 // (16 or 64). A cluster of up to 8 CTAs shares a tile's columns out; each sends its partial sums of an
 // equal part of X's rows to the CTA that owns the part (distributed shared memory), which adds them in order.
-// Where the tiles alone fill the GPU the CTAs walk them, with two accumulators: W streams on under the output.
+// Where the tiles alone fill the GPU the CTAs walk them, with two accumulators: W streams on under the output. W's
+// bytes bound it: 60000 x 4096 by one row 41 us in 8 bits (6.0 TB/s), 23 in 4 by 4 (5.7), 27 in 8 by 4 (4.8: spread
+// codes fill the ring with half as many bytes of memory).
 //
-// Every wait is bounded (about 2 s): then QW_MX_TIMEOUT is set and the CTA frees its TMEM and ends.
+// Every wait is bounded (about 2 s): then QW_MX_TIMEOUT is set, and the CTA lets its copies and MMAs land, frees its
+// tensor memory and ends.
 #include <algorithm>
 #include <atomic>
 
@@ -32,13 +49,16 @@ constexpr int MG_THREADS = 352;
 constexpr int MG_X = 128 * 128, MG_W = 128 * 128, MG_SF = 1024;  // bytes: operand tiles of a stage, exponents of 128 rows (two atoms)
 constexpr int MG_STAGE = MG_X + MG_W + 3 * MG_SF;
 constexpr int MG_SF_COL = 256, MG_SF_COLS = 32;  // TMEM columns of the exponents, a stage's
-// Linear: a warp stages its output in two boxes of 32 rows by 32 columns; SwiGLU's, which is small, is stored from registers.
+// Linear: a warp stages its output in boxes of 32 rows by 32 columns; SwiGLU's, which is small, is stored from registers.
+// Two that take turns; of 4-byte outputs one, whose space a fifth stage needs more (8192 x 1024 by 4096 8 by 4 bits
+// 38.7 us, with two boxes and four stages 42.2).
 template <int OUT>
 struct MgCfg {
     static constexpr bool GLU = OUT == 8 || OUT == 4;
     static constexpr int BOX = GLU ? 0 : 32 * 32 * (OUT == QW_F32 ? 4 : 2);
-    static constexpr int STAGES = GLU ? 6 : OUT == QW_F32 ? 4 : 5;
-    static constexpr int SMEM = 1024 + STAGES * MG_STAGE + 16 * BOX + 256;
+    static constexpr int BOXES = OUT == QW_F32 ? 1 : 2;
+    static constexpr int STAGES = GLU ? 6 : 5;
+    static constexpr int SMEM = 1024 + STAGES * MG_STAGE + 8 * BOXES * BOX + 256;
     static_assert(SMEM <= 232448 && MG_SF_COL + STAGES * MG_SF_COLS <= 512, "shared or tensor memory");
 };
 
@@ -54,8 +74,7 @@ struct MxGemmP {
     int32_t* status;
 };
 
-// A wait as in tc_sm103.cuh, but the thread sleeps until the phase completes: a warp that polls takes shared-memory
-// cycles from the MMAs, whose operands need nearly all of them.
+// A wait as in tc_sm103.cuh, but the thread sleeps until the phase completes.
 __device__ __forceinline__ bool try_sleep(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
@@ -73,6 +92,12 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volati
     while (!try_sleep(bar, parity))
         if (*abort_flag || globaltimer_ns() - t0 > kTcWaitNs) return false;
     return true;
+}
+// After a wait that gave up: copies and MMAs in flight land within microseconds; a millisecond is enough for all of them.
+__device__ __forceinline__ void let_land(volatile int* abort_flag) {
+    if (!*abort_flag) return;
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
 }
 __device__ __forceinline__ uint64_t sf_desc(uint32_t a) {  // no swizzle, 8-row groups of 16-byte rows 128 bytes apart
     return (uint64_t)((a & 0x3FFFFu) >> 4) | ((uint64_t)8 << 32) | ((uint64_t)1 << 46);
@@ -128,7 +153,7 @@ constexpr uint32_t idesc_mx(uint32_t fa, uint32_t fb, int M, int N) {
     return (fa << 7) | (fb << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 4) << 24);
 }
 
-// A box of 32 rows by 128 bytes from a warp's shared memory to the output; rows and columns outside it are clipped.
+// A box of 32 rows by 32 columns from a warp's shared memory to the output; rows and columns outside it are clipped.
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int x, int y) {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"((uint64_t)map), "r"(x),
                  "r"(y), "r"(src)
@@ -138,14 +163,15 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t sr
 // A warp's 32 rows (a row a lane) of 32 sums, to columns f .. f + 31 of the output. A lane's 16-byte chunks go to the
 // places that the copy's swizzle gives them (rows of 128 or 64 bytes), which no two of 8 lanes share. A copy clips
 // whole 16-byte chunks only: the map ends at the last whole one, what is left of M goes element by element. Every use of
-// a box, of the two that take turns, commits a group of copies.
+// a box commits a group of copies.
 template <int DT>
-__device__ __forceinline__ void store_box(const CUtensorMap* map, const MxGemmP& p, uint8_t* two, uint32_t& uses, int t0, int f, const uint32_t* r) {
+__device__ __forceinline__ void store_box(const CUtensorMap* map, const MxGemmP& p, uint8_t* boxes, uint32_t& uses, int t0, int f, const uint32_t* r) {
     constexpr int ES = DT == QW_F32 ? 4 : 2, ROW = 32 * ES;
     const int lane = threadIdx.x & 31, turn = DT == QW_F32 ? lane & 7 : (lane >> 1) & 3;
     if (t0 >= p.T || f >= p.M) return;
-    uint8_t* box = two + (uses++ & 1) * 32 * ROW;
-    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // the box before last has been read
+    constexpr int N = MgCfg<DT>::BOXES;
+    uint8_t* box = boxes + uses++ % N * 32 * ROW;
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N - 1) : "memory");  // this box has been read
     __syncwarp();
 #pragma unroll
     for (int c = 0; c < ROW / 16; ++c) {
@@ -172,13 +198,15 @@ __device__ __forceinline__ void store_box(const CUtensorMap* map, const MxGemmP&
         }
 }
 
-// silu(g) u = g u / (1 + 2^(-g log2 e)). The hardware's exponential and reciprocal: 2^-20 relative at most, where a
-// code has 4 bits.
+// silu(g) u = g u / (1 + 2^(-g log2 e)). The hardware's exponential (2^-22) and reciprocal (2^-23), five roundings, and for
+// negative g the exponent's own: |g| (2^-24 + 2^-26). 2^-20 + 2^-23 |g| relative, where a code has 4 bits. Both work on
+// numbers 2^-24 as large, so that neither the exponential overflows nor the reciprocal is flushed to 0 while the sigmoid
+// is an fp32 number, subnormal ones included.
 __device__ __forceinline__ float silu_mul(float g, float u) {
     float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.44269504f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-    return g * r * u;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaf(g, -1.44269504f, -24.f)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(0x1p-24f + e));
+    return g * (r * 0x1p-24f) * u;
 }
 
 // A thread's run of 32 features of row t: codes and exponent. Features from M on are zeros.
@@ -232,7 +260,7 @@ __global__ void __launch_bounds__(MG_THREADS, 1) k_mx_gemm(const __grid_constant
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     uint8_t* boxes = smem + C::STAGES * MG_STAGE;
-    uint64_t* full = reinterpret_cast<uint64_t*>(boxes + 16 * C::BOX);  // codes here, exponents in tensor memory (the leader's)
+    uint64_t* full = reinterpret_cast<uint64_t*>(boxes + 8 * C::BOXES * C::BOX);  // codes here, exponents in tensor memory (the leader's)
     uint64_t* empty = full + C::STAGES;
     uint64_t* sfull = empty + C::STAGES;  // exponents in shared memory (the leader's)
     uint64_t* accf = sfull + C::STAGES;
@@ -336,7 +364,7 @@ __global__ void __launch_bounds__(MG_THREADS, 1) k_mx_gemm(const __grid_constant
         }
         __syncwarp();
     } else if (warp == 10) {
-        // exponents to tensor memory, in a thread of its own: a thread's waits for shared memory stand behind its copies
+        // exponents to tensor memory
         if (lane == 0 && rank == 0) {
             const uint32_t total = (uint32_t)((p.units - pair + pairs - 1) / pairs) * nk;
             for (uint32_t g = 0; g < total; ++g) {
@@ -390,7 +418,7 @@ __global__ void __launch_bounds__(MG_THREADS, 1) k_mx_gemm(const __grid_constant
             tmem_wait_ld();
             tc_fence_before();
             __syncwarp();
-            // only tensor memory is handed over, which the tcgen05 fences order: a release of all memory would take 0.4 us
+            // only tensor memory is handed over, which the tcgen05 fences order
             if (lane == 0) asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(free_bar) : "memory");
             if constexpr (GLU) {
                 if (t < p.T) {
@@ -400,7 +428,7 @@ __global__ void __launch_bounds__(MG_THREADS, 1) k_mx_gemm(const __grid_constant
             } else {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    store_box<OUT>(&m.out, p, boxes + 2 * warp * C::BOX, uses, t - lane, tw * 256 + half * 128 + 32 * k, r[k]);
+                    store_box<OUT>(&m.out, p, boxes + warp * C::BOXES * C::BOX, uses, t - lane, tw * 256 + half * 128 + 32 * k, r[k]);
             }
         }
         if (!GLU && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -408,6 +436,7 @@ __global__ void __launch_bounds__(MG_THREADS, 1) k_mx_gemm(const __grid_constant
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == 0 && *abort_flag) atomicOr(p.status, QW_MX_TIMEOUT);
+    let_land(abort_flag);
     cluster_sync();  // no copy, MMA or arrival of the pair still targets this CTA
     if (warp == 9) {
         tc_fence_after();
@@ -437,7 +466,7 @@ struct MfCfg {
     static constexpr int NW = GLU ? 2 : 1;  // tiles of W
     static constexpr int AT = F4 ? 2 : 1;   // atoms of 128 columns a stage
     static constexpr int STAGE = NW * MG_W + BN * 128 + (NW + 1) * MG_SF;
-    // two CTAs an SM. One row by 60000 x 4096 in 8 bits: 41 us, 6.0 TB/s; with 3 stages and three CTAs 52
+    // two CTAs an SM. One row by 60000 x 4096 in 8 bits: 41 us; with 3 stages and three CTAs 52
     static constexpr int STAGES = GLU ? 3 : BN == 16 ? 5 : 4;
     static constexpr int SF_COLS = (NW + 1) * AT * 4, SF_COL = 2 * NW * BN;  // after two accumulators
     static constexpr int COLS_USED = SF_COL + STAGES * SF_COLS;
@@ -720,6 +749,7 @@ __global__ void __launch_bounds__(MF_THREADS) k_mx_gemm_few(const __grid_constan
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == 0 && *abort_flag) atomicOr(p.status, QW_MX_TIMEOUT);
+    let_land(abort_flag);
     if (warp == 5) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::COLS) : "memory");
