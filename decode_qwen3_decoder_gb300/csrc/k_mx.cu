@@ -11,9 +11,11 @@
 // type of its own: the codes are those of the real y, whatever the order of the sums. y is computed in fp32 with a
 // relative error d below 18 2^-24; a run in which a value between y (1 - d) and y (1 + d) could get another code or
 // exponent, one in 1300, is computed again: the row's sum of squares as an unevaluated pair of floats (the
-// products' and sums' errors are added up; about 2^-45 relative), 1 / sqrt and the products as pairs. Pairs
-// for every value would cost twice the instructions, which then bound the kernel. One CTA a row; a row's elements stay
-// in registers between the passes.
+// products' and sums' errors are added up), 1 / sqrt and the products as pairs, 2^-43 in all. (1 / sqrt in fp64, whose
+// rate is low here: 2048 x 8192 35.0 us, as pairs 31.2.) Instructions bound the kernel, 40 an element, and the runs in
+// doubt take a tenth to a fifth of the time: 8192 x 1024 fp32 with a bf16 branch 16.6 us, 92 MB; 2048 x 4096 bf16 15.9. Pairs
+// for every value would double the instructions; persistent CTAs that had the next row copied ahead took 22.3 us. One CTA
+// a row (up to 256 columns one warp); a row's elements stay in registers between the passes.
 #include <algorithm>
 
 #include "mx.cuh"
@@ -141,6 +143,11 @@ __global__ void __launch_bounds__(MQ_WARPS * 32) k_mx_read(const __grid_constant
 
 // ---- RMSNorm --------------------------------------------------------------------------------------------
 
+// A sum as an unevaluated pair: hi + lo.
+struct Pair {
+    float hi, lo;
+};
+
 struct MxNormP {
     uint8_t* codes;
     uint8_t* scales;
@@ -152,13 +159,9 @@ struct MxNormP {
     size_t ld_x, ld_add, ld_sum;
     int dt_add;  // QW_F16, QW_BF16, QW_F32 or -1
     float eps;
-    double inv_n;  // 1 / cols
+    Pair inv_n;  // 1 / cols
 };
 
-// A sum as an unevaluated pair: hi + lo.
-struct Pair {
-    float hi, lo;
-};
 __device__ __forceinline__ Pair two_sum(float a, float b) {
     const float s = __fadd_rn(a, b), z = __fsub_rn(s, a);
     return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, z)), __fsub_rn(b, z))};
@@ -195,7 +198,7 @@ __device__ __forceinline__ float to_odd(double t) {
     return (double)f == t ? f : __uint_as_float(__float_as_uint(f) | 1u);
 }
 
-// s r w to about 2^-45, r = 1 / sqrt as a pair.
+// s r w to 2^-45, r = 1 / sqrt as a pair.
 __device__ __forceinline__ Pair scale_pair(float s, Pair r, float w) {
     const float a = __fmul_rn(s, r.hi), b = __fmaf_rn(s, r.lo, __fmaf_rn(s, r.hi, -a));
     const float q = __fmul_rn(a, w), f = __fmaf_rn(b, w, __fmaf_rn(a, w, -q));
@@ -203,10 +206,18 @@ __device__ __forceinline__ Pair scale_pair(float s, Pair r, float w) {
     return {hi, __fsub_rn(f, __fsub_rn(hi, q))};
 }
 
-// 1 / sqrt(a): one step of third order from an fp32 value (2^-22) leaves 2^-50.
-__device__ __forceinline__ double refine_rsqrt(double a, float r0) {
-    const double r = r0, e = fma(-a * r, r, 1.0);
-    return fma(r * e, fma(0.375, e, 0.5), r);
+// 1 / sqrt(t inv_n + eps): one step of third order from an fp32 value r0 (2^-22), whose residual 1 - a r0^2 is taken from
+// exact products: 2^-44.
+__device__ __forceinline__ Pair refine_rsqrt(Pair t, Pair inv_n, float eps, float r0) {
+    const float m = __fmul_rn(t.hi, inv_n.hi);
+    const float ml = __fmaf_rn(t.hi, inv_n.lo, __fmaf_rn(t.lo, inv_n.hi, __fmaf_rn(t.hi, inv_n.hi, -m)));
+    const Pair a = add_pairs({m, ml}, {eps, 0.f});
+    const float q = __fmul_rn(r0, r0), ql = __fmaf_rn(r0, r0, -q);
+    const float b = __fmul_rn(a.hi, q), bl = __fmaf_rn(a.lo, q, __fmaf_rn(a.hi, ql, __fmaf_rn(a.hi, q, -b)));
+    const float e = __fsub_rn(__fsub_rn(1.f, b), bl);
+    const float d = __fmul_rn(__fmul_rn(r0, e), __fmaf_rn(0.375f, e, 0.5f));
+    const float hi = __fadd_rn(r0, d);
+    return {hi, __fsub_rn(d, __fsub_rn(hi, r0))};
 }
 
 // Roundings of y, in units of 2^-24: s rstd, times w, times the scale 1 each; rsqrtf 4 (2 units of the last place); its
@@ -328,10 +339,10 @@ __device__ __forceinline__ void norm_store_scales(const MxNormP& p, size_t row, 
     if (ok && (threadIdx.x & 15) == 0) *reinterpret_cast<uint32_t*>(p.scales + mx_scale_word((int)row, v / 16, p.atoms)) = sw;
 }
 
-// A row whose squares leave fp32, or that holds a NaN or an infinity: everything in fp64, read again from memory.
+// A row whose squares (or what pairs hold of them) leave fp32, or that holds a NaN or an infinity: everything in fp64, read again from memory.
 template <int DT, int BITS>
-__device__ __noinline__ void norm_wide_row(const MxNormP& p, double* part) {
-    const int row = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+__device__ __noinline__ void norm_wide_row(const MxNormP& p, int row, double* part) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
     const int vecs = p.atoms * (MX_ATOM / 8), steps = (vecs + blockDim.x - 1) / blockDim.x;
     double sum = 0.0;
     for (int j = 0; j < steps; ++j) {
@@ -343,10 +354,13 @@ __device__ __noinline__ void norm_wide_row(const MxNormP& p, double* part) {
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) part[warp] = sum;
-    __syncthreads();
-    sum = 0.0;
-    for (int i = 0; i < warps; ++i) sum += part[i];
+    if (warps > 1) {
+        __syncthreads();
+        if (lane == 0) part[warp] = sum;
+        __syncthreads();
+        sum = 0.0;
+        for (int i = 0; i < warps; ++i) sum += part[i];
+    }
     const double rstd = 1.0 / sqrt(sum / p.cols + (double)p.eps);
     for (int j = 0; j < steps; ++j) {
         const int v = j * blockDim.x + threadIdx.x, left = v < vecs ? p.cols - v * 8 : 0;
@@ -403,7 +417,8 @@ __global__ void __launch_bounds__(VPT == 1 ? 128 : 512, VPT == 1 ? 12 : VPT == 2
     __shared__ double part[16];  // of the warps: a pair of floats or, in a wide row, a double
     pdl_wait();
     pdl_launch();
-    const int row = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const int row = blockIdx.x * blockDim.y + threadIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    if ((unsigned)row >= (unsigned)p.rows) return;
     const int vecs = p.atoms * (MX_ATOM / 8), steps = VPT ? 1 : (vecs + blockDim.x - 1) / blockDim.x;
     float s[N][8];
     MxRaw wr[N];  // the weight, on its way during the first pass
@@ -459,22 +474,17 @@ __global__ void __launch_bounds__(VPT == 1 ? 128 : 512, VPT == 1 ? 12 : VPT == 2
         t = block_sum(t, reinterpret_cast<Pair*>(part));
         sum = t.hi;
     }
-    if (!(sum > 0x1p-80f && sum < 0x1p120f)) {
-        __syncthreads();
-        norm_wide_row<DT, BITS>(p, part);
+    const float mean = fmaf(sum, p.inv_n.hi, p.eps);
+    if (!(sum > 0x1p-80f && mean < 0x1p90f)) {
+        norm_wide_row<DT, BITS>(p, row, part);
         return;
     }
-    const float rstd = rsqrtf(fmaf(sum, (float)p.inv_n, p.eps));
+    const float rstd = rsqrtf(mean);
     Pair r = {0.f, 0.f};
-    auto refine = [&]() {
-        const double d = refine_rsqrt(((double)t.hi + (double)t.lo) * p.inv_n + (double)p.eps, rstd);
-        r.hi = (float)d;
-        r.lo = (float)(d - (double)r.hi);
-    };
     const uint32_t mask = 0xFu << (lane & 28);  // the four lanes of a run
     bool again[N], any = false;
     int byte[N];
-    if constexpr (!VPT) refine();
+    if constexpr (!VPT) r = refine_rsqrt(t, p.inv_n, p.eps, rstd);
     for (int j = 0; j < steps; ++j) {
 #pragma unroll
         for (int k = 0; k < N; ++k) {
@@ -505,7 +515,7 @@ __global__ void __launch_bounds__(VPT == 1 ? 128 : 512, VPT == 1 ? 12 : VPT == 2
 #pragma unroll
             for (int i = 0; i < 8; ++i) add_square(t, s[k][i]);
         t = block_sum(t, reinterpret_cast<Pair*>(part));
-        refine();
+        r = refine_rsqrt(t, p.inv_n, p.eps, rstd);
 #pragma unroll
         for (int k = 0; k < N; ++k) {
             const int v = k * blockDim.x + threadIdx.x, left = v < vecs ? p.cols - v * 8 : 0;
@@ -566,10 +576,13 @@ template <int DT, int BITS>
 cudaError_t launch_norm(const MxNormP& p, cudaStream_t st) {
     const LaunchCtx c = {st, true, nullptr};
     const int vecs = p.atoms * (MX_ATOM / 8);
-    // up to 1024 columns a thread has 8 of them, to 8192 16, to 16384 32. Measured (us): 8192 x 1024 17.0 and 17.2 with 16 a
-    // thread; 4096 x 2048 18.7 with 8, 18.1 with 16; 2048 x 4096 24.9 with 8, 18.3 with 16, 20.1 with 32
+    // up to 1024 columns a thread has 8 of them, to 8192 16, to 16384 32. Measured (us): 8192 x 1024 16.6 and 17.0 with 16 a
+    // thread; 4096 x 2048 18.7 with 8, 18.1 with 16; 2048 x 4096 24.9 with 8, 18.3 with 16, 20.1 with 32 (1 / sqrt in fp64)
     const int vpt = vecs <= 128 ? 1 : vecs <= 1024 ? 2 : vecs <= 2048 ? 4 : 0;
-    const dim3 block(vpt ? ((vecs + vpt - 1) / vpt + 31) / 32 * 32 : 512), grid(p.rows);
+    const unsigned threads = vpt ? ((vecs + vpt - 1) / vpt + 31) / 32 * 32 : 512;
+    // many rows of one warp: four a CTA (16384 x 256 7.7 us, one a CTA 17.1)
+    const unsigned rows = threads == 32 && p.rows >= 4096 ? 4 : 1;
+    const dim3 block(threads, rows), grid(((unsigned)p.rows + rows - 1) / rows);
     switch (vpt) {
         case 1: return launch_k(c, k_mx_rmsnorm<DT, BITS, 1>, grid, block, 0, p);
         case 2: return launch_k(c, k_mx_rmsnorm<DT, BITS, 2>, grid, block, 0, p);
@@ -637,8 +650,10 @@ extern "C" qw_status qw_mx_rmsnorm(const qw_mx* out, const void* dev_x, size_t l
         if (dev_sum == dev_add) return qw_fail(QW_ERR_INVALID_ARG, "mx_rmsnorm: sum over add");
     }
     if (!dev_weight || !aligned16(dev_weight)) return qw_fail(QW_ERR_INVALID_ARG, "mx_rmsnorm: weight NULL or not 16-byte aligned");
+    const double inv_n = 1.0 / out->cols;
     const MxNormP p = {(uint8_t*)out->dev_codes, (uint8_t*)out->dev_scales, out->rows, out->cols, (int)mx_atoms(out->cols), dev_x,
-                       dev_add, dev_sum, (const bf16*)dev_weight, ld_x, ld_add, ld_sum, dev_add ? add_dtype : -1, eps, 1.0 / out->cols};
+                       dev_add, dev_sum, (const bf16*)dev_weight, ld_x, ld_add, ld_sum, dev_add ? add_dtype : -1, eps,
+                       {(float)inv_n, (float)(inv_n - (float)inv_n)}};
     const cudaStream_t st = (cudaStream_t)stream;
 #define MX_N(dt, bits) launch_norm<dt, bits>(p, st)
     return done(MX_DISPATCH(MX_N, x_dtype, out->bits), "mx_rmsnorm");

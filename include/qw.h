@@ -551,8 +551,8 @@ qw_status qw_mx_read(const qw_mx* m, void* dev_x, size_t ld_x, int dtype, void* 
 /* The step between two branches of a layer: s = x + add, rounded to x_dtype (dev_add NULL: s = x; add_dtype is
  * add's own type), written to dev_sum (x_dtype; NULL: not wanted; may be dev_x with the same stride), and
  * y = s / sqrt(mean(s^2) + eps) * weight (dev_weight: [cols] bf16, 16-byte aligned; eps > 0) quantised to `out`.
- * The codes are those of the real number y, whatever the order of the sums: equal inputs give equal bits
- * on every launch shape. (|y| above fp32's range gives NaN.) */
+ * The codes are those of y computed to 2^-43 relative, whatever the order of the sums: equal inputs give equal
+ * bits on every launch shape. (|y| above fp32's range gives NaN.) */
 qw_status qw_mx_rmsnorm(const qw_mx* out, const void* dev_x, size_t ld_x, int x_dtype, const void* dev_add, size_t ld_add,
                         int add_dtype, void* dev_sum, size_t ld_sum, const void* dev_weight, float eps, void* stream);
 
@@ -563,8 +563,8 @@ qw_status qw_mx_linear(const qw_mx* x, const qw_mx* w, void* dev_out, size_t ld_
                        void* stream);
 
 /* out = quantise(SiLU(x w_gate^T) * (x w_up^T)): x [T][K], w_gate and w_up [I][K] of the same bits, out [T][I] in 8
- * or 4 bits. The products as in qw_mx_linear; SiLU and the product of the two in fp32 (2^-20 relative), then
- * quantised. */
+ * or 4 bits. The products as in qw_mx_linear; SiLU and the product of the two in fp32 (2^-20 relative,
+ * and 2^-23 |gate| more where the gate is negative, as long as SiLU is a normal number), then quantised. */
 qw_status qw_mx_swiglu(const qw_mx* x, const qw_mx* w_gate, const qw_mx* w_up, const qw_mx* out, int32_t* dev_status,
                        void* stream);
 

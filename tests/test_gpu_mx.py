@@ -225,6 +225,34 @@ def test_rmsnorm_odd_rows(lib, cols, bits):
             m.check(*mx.quantize(mx.rmsnorm(s, wf, float(np.float32(1e-6))), bits))
 
 
+@pytest.mark.parametrize("rows,cols", [(4099, 200), (4096, 256), (4097, 31)])
+def test_rmsnorm_many_short_rows(lib, rows, cols):
+    """Rows of one warp, several a CTA: ordinary ones beside ones in doubt, of odd sizes, a NaN."""
+    import torch
+    rng = np.random.default_rng(cols)
+    x = _norm_rows(rng, rows, cols)
+    x[5] *= 1e-30
+    x[6] *= 1e25
+    x[7, 3], x[rows - 1] = float("nan"), 0.0
+    a = torch.from_numpy(rng.normal(0, 1, (rows, cols)).astype(np.float32)) * (torch.arange(rows) > 7)[:, None]
+    w = 1 + 0.1 * rng.normal(0, 1, cols)
+    m, s, wf = _norm(lib, x, a, w, 8, F32, BF16)
+    with np.errstate(invalid="ignore"):
+        m.check(*mx.quantize(mx.rmsnorm(s, wf, float(np.float32(1e-6))), 8))
+
+
+@pytest.mark.parametrize("eps", [1e-30, 1.0, 1e20, 1e30, 3e38])
+def test_rmsnorm_any_eps(lib, eps):
+    """eps far above the squares and far below, rows on both sides of what pairs of floats hold (2^90)."""
+    rng = np.random.default_rng(0)
+    x = _norm_rows(rng, 8, 1000)
+    for i, f in enumerate([1e-11, 1e-3, 1.0, 1e9, 1e13, 3e13, 1e14, 1e18]):
+        x[i] *= f / float(x[i].abs().max())
+    w = 2.0 ** 60 * (1 + 0.1 * rng.normal(0, 1, 1000))
+    m, s, wf = _norm(lib, x, None, w, 8, F32, None, eps=eps)
+    m.check(*mx.quantize(mx.rmsnorm(s, wf, float(np.float32(eps))), 8))
+
+
 def _weights(rng, M, K):
     return rng.normal(0, 1, (M, K)) / np.sqrt(K) * 2.0 ** rng.integers(-3, 3, (M, 1))
 
@@ -343,13 +371,14 @@ def test_linear_fp16_stops(lib):
     np.testing.assert_array_equal(got, np.tile([65504.0, -65504.0], (3, 1)))
 
 
-def _check_swiglu(m, x, g, u):
+def _check_swiglu(m, x, g, u, exact=False):
     """q(h'), h' the fp32 value: |h' - h| follows from the products' errors (|silu'| <= 1.1, |silu(v)| <= |v|) and 2^-20
-    relative; half a code's step of h' on top, of the smallest codes half of theirs under a scale below 2 amax / L."""
+    relative, 2^-23 |g| more where g < 0 (the exponent -g log2 e is rounded, by 2^-24 relative at most, and log2 e itself by
+    2^-26: an error of |g| (2^-24 + 2^-26) in the logarithm of the exponential); half a code's step of h' on top, of the smallest codes half of theirs under a scale below 2 amax / L."""
     got, bits = m.values(), m.bits
     gv, uv, h = x @ g.T, x @ u.T, mx.swiglu(x, g, u)
-    eg, eu = _sum_error(x, g), _sum_error(x, u)
-    d = 1.1 * eg * (np.abs(uv) + eu) + (np.abs(gv) + eg) * eu + 2.0 ** -20 * np.abs(h)
+    eg, eu = (0.0, 0.0) if exact else (_sum_error(x, g), _sum_error(x, u))
+    d = 1.1 * eg * (np.abs(uv) + eu) + (np.abs(gv) + eg) * eu + (2.0 ** -20 + 2.0 ** -23 * np.maximum(-gv, 0)) * np.abs(h)
     pad = -h.shape[1] % 32
     top = np.pad(np.abs(h) + d, ((0, 0), (0, pad))).reshape(h.shape[0], -1, 32).max(-1).repeat(32, 1)[:, :h.shape[1]]
     half, small = (2.0 ** -4, 2.0 ** -10) if bits == 8 else (2.0 ** -2, 0.25)
@@ -394,6 +423,16 @@ def test_swiglu_nan_row_and_large_gates(lib):
     assert np.isnan(v[2]).all()
     for t in (0, 1, 3):
         np.testing.assert_array_equal(v[t], np.repeat([2048.0, 0.0], 32))
+
+
+def test_swiglu_negative_gates(lib):
+    """Gates from -2 to -86, up to u = 2^20: SiLU falls to 2^-117 and u's factor keeps; a run holds one gate's size. The sums of 32
+    codes of one exponent are exact."""
+    rng = np.random.default_rng(5)
+    xf, uf = np.ones((5, 32)), 2.0 ** rng.integers(0, 15, (640, 1)) * rng.uniform(0.5, 1, (640, 32))
+    gf = -np.linspace(2, 86, 20).repeat(32)[:, None] / 32 * np.ones((1, 32))
+    x, g, u = Matrix.of(lib, xf, 8), Matrix.of(lib, gf, 8), Matrix.of(lib, uf, 8)
+    _check_swiglu(_swiglu(lib, x, g, u, 8), x.held, g.held, u.held, exact=True)
 
 
 class Layer:
