@@ -198,15 +198,14 @@ __device__ __forceinline__ void store_box(const CUtensorMap* map, const MxGemmP&
         }
 }
 
-// silu(g) u = g u / (1 + 2^(-g log2 e)). The hardware's exponential (2^-22) and reciprocal (2^-23), five roundings, and for
-// negative g the exponent's own: |g| (2^-24 + 2^-26). 2^-20 + 2^-23 |g| relative, where a code has 4 bits. Both work on
-// numbers 2^-24 as large, so that neither the exponential overflows nor the reciprocal is flushed to 0 while the sigmoid
-// is an fp32 number, subnormal ones included.
+// silu(g) u = g u / (1 + 2^(-g log2 e)). The hardware's exponential (2^-22) and reciprocal (2^-23), four roundings, and for
+// negative g the exponent's own: |g| (2^-24 + 2^-26). 2^-20 + 2^-23 |g| relative, where a code has 4 bits. A quarter of
+// the denominator, so that the reciprocal is not flushed to 0 before the exponential leaves fp32 (g < -88.7).
 __device__ __forceinline__ float silu_mul(float g, float u) {
     float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaf(g, -1.44269504f, -24.f)));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(0x1p-24f + e));
-    return g * (r * 0x1p-24f) * u;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.44269504f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(e, 0.25f, 0.25f)));
+    return g * (r * 0.25f) * u;
 }
 
 // A thread's run of 32 features of row t: codes and exponent. Features from M on are zeros.
