@@ -189,10 +189,10 @@ __device__ __forceinline__ void store_box(const CUtensorMap* map, const MxGemmP&
         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     }
     if (t0 + lane < p.T)
-        for (int x = max(whole, f); x < min(p.M, f + 32); ++x) {
-            const int b = (x - f) * ES;
+        for (int j = max(whole - f, 0); j < min(p.M - f, 32); ++j) {
+            const int b = j * ES;
             const uint8_t* from = box + lane * ROW + ((b / 16) ^ turn) * 16 + b % 16;
-            const size_t to = (size_t)(t0 + lane) * p.ld + x;
+            const size_t to = (size_t)(t0 + lane) * p.ld + f + j;
             if (DT == QW_F32) reinterpret_cast<float*>(p.out)[to] = *reinterpret_cast<const float*>(from);
             else reinterpret_cast<uint16_t*>(p.out)[to] = *reinterpret_cast<const uint16_t*>(from);
         }
