@@ -179,9 +179,10 @@ __device__ __forceinline__ Pair add_pairs(Pair a, Pair b) {
     return {hi, __fsub_rn(lo, __fsub_rn(hi, s.hi))};
 }
 
+// A sum as DT holds it: fp16 stops at 65504, but an infinity that was there before stays one.
 template <int DT>
 __device__ __forceinline__ float round_to(float v) {
-    if (DT == QW_F16) return __half2float(__float2half_rn(v));
+    if (DT == QW_F16) return __half2float(__float2half_rn(fabsf(v) <= 3.402823466e38f ? mx_sat16(v) : v));
     if (DT == QW_BF16) return bf2f(__float2bfloat16_rn(v));
     return v;
 }
@@ -367,7 +368,7 @@ __device__ __noinline__ void norm_wide_row(const MxNormP& p, int row, double* pa
         float s[8], w[8];
         norm_load<DT>(p, row, v * 8, left, s);
         mx_load8<QW_BF16>(p.w, v * 8, left, w);
-        if (p.sum && left > 0) mx_store8<DT>(p.sum, row * p.ld_sum + v * 8, left, s);
+        if (p.sum && left > 0) mx_store8<DT, false>(p.sum, row * p.ld_sum + v * 8, left, s);
         double y[8], m = 0.0;
         bool bad = false;
 #pragma unroll
@@ -496,7 +497,7 @@ __global__ void __launch_bounds__(VPT == 1 ? 128 : 512, VPT == 1 ? 12 : VPT == 2
             float w[8];
             mx_fill8<QW_BF16>(p.w, v * 8, left, wr[k]);
             mx_unpack8<QW_BF16>(wr[k], w);
-            if (p.sum && left > 0) mx_store8<DT>(p.sum, row * p.ld_sum + v * 8, left, s[k]);
+            if (p.sum && left > 0) mx_store8<DT, false>(p.sum, row * p.ld_sum + v * 8, left, s[k]);
             uint32_t q[2];
             byte[k] = norm_codes<BITS>(s[k], w, left > 0 ? rstd : 0.f, q, again[k]);
             if (!VPT && (__ballot_sync(0xffffffffu, again[k]) & mask))

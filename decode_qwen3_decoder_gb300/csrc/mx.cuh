@@ -154,13 +154,13 @@ __device__ __forceinline__ void mx_load8(const void* base, size_t off, int left,
 __device__ __forceinline__ float mx_sat16(float v) { return fabsf(v) > 65504.f ? copysignf(65504.f, v) : v; }
 
 // Two elements of type DT (16 bits) as a word.
-template <int DT>
+template <int DT, bool SAT = true>
 __device__ __forceinline__ uint32_t mx_pack2(float a, float b) {
-    return DT == QW_F16 ? pack_h2(mx_sat16(a), mx_sat16(b)) : pack_bf2(a, b);
+    return DT == QW_F16 ? SAT ? pack_h2(mx_sat16(a), mx_sat16(b)) : pack_h2(a, b) : pack_bf2(a, b);
 }
 
-// 8 elements to `off`, the first `left` of them.
-template <int DT>
+// 8 elements to `off`, the first `left` of them. SAT false: values of the type itself, infinities among them.
+template <int DT, bool SAT = true>
 __device__ __forceinline__ void mx_store8(void* base, size_t off, int left, const float* x) {
     if (left >= 8) {
         if (DT == QW_F32) {
@@ -169,14 +169,14 @@ __device__ __forceinline__ void mx_store8(void* base, size_t off, int left, cons
             p[1] = make_float4(x[4], x[5], x[6], x[7]);
         } else {
             *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(base) + off) =
-                make_uint4(mx_pack2<DT>(x[0], x[1]), mx_pack2<DT>(x[2], x[3]), mx_pack2<DT>(x[4], x[5]), mx_pack2<DT>(x[6], x[7]));
+                make_uint4(mx_pack2<DT, SAT>(x[0], x[1]), mx_pack2<DT, SAT>(x[2], x[3]), mx_pack2<DT, SAT>(x[4], x[5]), mx_pack2<DT, SAT>(x[6], x[7]));
         }
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             if (i < left) {
                 if (DT == QW_F32) reinterpret_cast<float*>(base)[off + i] = x[i];
-                else reinterpret_cast<uint16_t*>(base)[off + i] = (uint16_t)mx_pack2<DT>(x[i], 0.f);
+                else reinterpret_cast<uint16_t*>(base)[off + i] = (uint16_t)mx_pack2<DT, SAT>(x[i], 0.f);
             }
         }
     }

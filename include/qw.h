@@ -551,6 +551,7 @@ qw_status qw_mx_read(const qw_mx* m, void* dev_x, size_t ld_x, int dtype, void* 
 /* The step between two branches of a layer: s = x + add, rounded to x_dtype (dev_add NULL: s = x; add_dtype is
  * add's own type), written to dev_sum (x_dtype; NULL: not wanted; may be dev_x with the same stride), and
  * y = s / sqrt(mean(s^2) + eps) * weight (dev_weight: [cols] bf16, 16-byte aligned; eps > 0) quantised to `out`.
+ * An fp16 s stops at 65504 too, but an infinity of x or add stays one in s and makes the runs that it reaches NaN.
  * The codes are those of y computed to 2^-43 relative, whatever the order of the sums: equal inputs give equal
  * bits on every launch shape. (|y| above fp32's range gives NaN.) */
 qw_status qw_mx_rmsnorm(const qw_mx* out, const void* dev_x, size_t ld_x, int x_dtype, const void* dev_add, size_t ld_add,

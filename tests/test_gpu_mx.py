@@ -253,6 +253,28 @@ def test_rmsnorm_any_eps(lib, eps):
     m.check(*mx.quantize(mx.rmsnorm(s, wf, float(np.float32(eps))), 8))
 
 
+@pytest.mark.parametrize("cols", [40, 1027, 20000])
+def test_rmsnorm_fp16_sums_stop(lib, cols):
+    """fp16 sums beyond 65504 stop there, in what is written and in what is normalised; infinities that were there stay."""
+    import torch
+    x = torch.full((4, cols), 60000.0)
+    x[0], x[1, 5], x[2, 3], x[3, 4] = -1.0, float("inf"), float("nan"), -60000.0
+    a = torch.full((4, cols), 9000.0)
+    a[3, 4] = -9000.0
+    xs, s = x.half().cuda(), torch.empty((4, -(-cols // 8) * 8), dtype=torch.float16, device="cuda")
+    t, b = _rows(x, F16), _rows(a, F32)
+    w = torch.ones(cols, dtype=torch.bfloat16, device="cuda")
+    m = Matrix(lib, 4, cols, 8)
+    lib.qw_mx_rmsnorm(m.view, t.data_ptr(), t.stride(0), lib.QW_F16, b.data_ptr(), b.stride(0), lib.QW_F32, s.data_ptr(), s.stride(0),
+                      w.data_ptr(), 1e-6)
+    v = xs.float() + a.cuda()
+    want = torch.where(v.isfinite(), v.clamp(-65504, 65504), v).half().cpu()
+    assert torch.equal(s[:, :cols].cpu().nan_to_num(nan=7.0, posinf=8.0), want.nan_to_num(nan=7.0, posinf=8.0))
+    assert float(want[0, 0]) == 9000.0 and float(want[3, 4]) == -65504.0 and float(want[1, 0]) == 65504.0
+    with np.errstate(invalid="ignore"):
+        m.check(*mx.quantize(mx.rmsnorm(want.double().numpy(), np.ones(cols), float(np.float32(1e-6))), 8))
+
+
 def _weights(rng, M, K):
     return rng.normal(0, 1, (M, K)) / np.sqrt(K) * 2.0 ** rng.integers(-3, 3, (M, 1))
 
