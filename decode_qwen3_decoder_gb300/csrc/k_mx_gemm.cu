@@ -29,7 +29,7 @@
 // accumulator would leave no tensor memory for exponents; tiles of 192 columns with two were slower (248 us above).
 //
 // k_mx_gemm_few. For few rows of X: W's rows are the M (128 of them, of gate and of up for SwiGLU), X's the N
-// (16 or 64). A cluster of up to 8 CTAs shares a tile's columns out; each sends its partial sums of an
+// (16, 64 or 128). A cluster of up to 8 CTAs shares a tile's columns out; each sends its partial sums of an
 // equal part of X's rows to the CTA that owns the part (distributed shared memory), which adds them in order.
 // Where the tiles alone fill the GPU the CTAs walk them, with two accumulators: W streams on under the output. W's
 // bytes bound it: 60000 x 4096 by one row 41 us in 8 bits (6.0 TB/s), 23 in 4 by 4 (5.7), 27 in 8 by 4 (4.8: spread
@@ -465,18 +465,18 @@ struct MfCfg {
     static constexpr int NW = GLU ? 2 : 1;  // tiles of W
     static constexpr int AT = F4 ? 2 : 1;   // atoms of 128 columns a stage
     static constexpr int STAGE = NW * MG_W + BN * 128 + (NW + 1) * MG_SF;
-    // two CTAs an SM. One row by 60000 x 4096 in 8 bits: 41 us; with 3 stages and three CTAs 52
-    static constexpr int STAGES = GLU ? 3 : BN == 16 ? 5 : 4;
+    // two CTAs an SM, or one with more rows of X. One row by 60000 x 4096 in 8 bits: 41 us; with 3 stages and three CTAs 52
+    static constexpr int STAGES = BN == 16 ? (GLU ? 3 : 5) : GLU ? 5 : BN == 64 ? 4 : 6;
     static constexpr int SF_COLS = (NW + 1) * AT * 4, SF_COL = 2 * NW * BN;  // after two accumulators
     static constexpr int COLS_USED = SF_COL + STAGES * SF_COLS;
-    static constexpr int COLS = COLS_USED <= 64 ? 64 : COLS_USED <= 128 ? 128 : 256;
+    static constexpr int COLS = COLS_USED <= 64 ? 64 : COLS_USED <= 128 ? 128 : COLS_USED <= 256 ? 256 : 512;
     // CTAs of a cluster wait for one another, so none may wait for tensor memory that another cluster holds: a CTA asks for
     // as large a share of the SM's shared memory (228 KB, 1 of it taken) as of its tensor memory. Whatever shares an
     // SM then has its columns.
     static constexpr int NEED = 1024 + STAGES * STAGE + 256, SHARE = COLS * 456 - 1024;
     static constexpr int SMEM = NEED > SHARE ? NEED : SHARE;
     static constexpr int PER_SM = 233472 / (SMEM + 1024);  // CTAs that share an SM
-    static_assert(COLS_USED <= COLS && PER_SM * COLS <= 512, "tensor memory");
+    static_assert(COLS_USED <= COLS && PER_SM >= 1 && PER_SM * COLS <= 512 && SMEM <= 232448, "shared or tensor memory");
     static_assert(NW * BN * 512 <= STAGES * STAGE, "partial sums");
 };
 
@@ -700,7 +700,7 @@ __global__ void __launch_bounds__(MF_THREADS) k_mx_gemm_few(const __grid_constan
     }
     if (S > 1) {
         // partial sums [splits][own rows of X][NW][128], over the ring once every CTA of the cluster has done its MMAs
-        const int lown = (BN == 16 ? 4 : 6) - p.lsplits, own = 1 << lown, f = tw0 * 128 + fl;
+        const int lown = (BN == 16 ? 4 : BN == 64 ? 6 : 7) - p.lsplits, own = 1 << lown, f = tw0 * 128 + fl;
         const uint32_t red = smem_u32(smem);
         cluster_sync();
         if (warp < 4 && ok) {
@@ -806,6 +806,9 @@ bool encode_out(CUtensorMap* map, void* out, int rows, int cols, size_t ld, int 
                es == 4 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Rows of X that k_mx_gemm_few's tiles have.
+int few_box(int T) { return T <= 16 ? 16 : T <= 64 ? 64 : 128; }
+
 // The current device and its SMs; a kernel's shared memory is allowed once a device (these calls cost a microsecond
 // between them, a quarter of a small product).
 struct Device {
@@ -854,18 +857,22 @@ cudaError_t launch_few(const MfMaps& m, const MfP& p, const Device& d, int slots
                      : launch_k(c, kern, dim3(std::min(p.tiles_w, slots)), dim3(MF_THREADS), SMEM, m, p);
 }
 
-template <int XB, int WB, bool GLU>
-cudaError_t launch_few_rows(const MfMaps& m, MfP& p, cudaStream_t st) {
+template <int XB, int WB, bool GLU, int BN>
+cudaError_t launch_few_split(const MfMaps& m, MfP& p, cudaStream_t st) {
     const int nk = XB == 4 ? (p.atoms + 1) / 2 : p.atoms;
     const Device d = device();
-    const int slots = d.sms * (GLU || p.T <= 16 ? MfCfg<XB == 4, GLU, 16>::PER_SM : MfCfg<XB == 4, false, 64>::PER_SM);
+    const int slots = d.sms * MfCfg<XB == 4, GLU, BN>::PER_SM;
     // the widest cluster whose CTAs all find a place and have two stages at least: one row by 4096 x 4096 5.0 us with 8 CTAs
     // a tile, 7.4 with two, 11 with one; by 4096 x 1024 3.5 with four, 3.9 with 8 of one stage, 4.5 with one
     p.lsplits = 0;
     while (p.lsplits < 3 && (long long)p.tiles_w << (p.lsplits + 1) <= slots && 4 << p.lsplits <= nk) ++p.lsplits;
+    return launch_few<XB, WB, GLU, BN>(m, p, d, slots, st);
+}
+template <int XB, int WB, bool GLU>
+cudaError_t launch_few_rows(const MfMaps& m, MfP& p, cudaStream_t st) {
     if constexpr (!GLU)
-        if (p.T > 16) return launch_few<XB, WB, GLU, 64>(m, p, d, slots, st);
-    return launch_few<XB, WB, GLU, 16>(m, p, d, slots, st);
+        if (few_box(p.T) == 128) return launch_few_split<XB, WB, GLU, 128>(m, p, st);
+    return few_box(p.T) == 64 ? launch_few_split<XB, WB, GLU, 64>(m, p, st) : launch_few_split<XB, WB, GLU, 16>(m, p, st);
 }
 
 template <bool GLU>
@@ -875,9 +882,15 @@ cudaError_t launch_few_formats(int xb, int wb, const MfMaps& m, MfP& p, cudaStre
                      : launch_few_rows<8, 8, GLU>(m, p, st);
 }
 
-// Whether k_mx_gemm_few serves a product. Measured against k_mx_gemm (us): linear, 64 rows by 4096 x 4096 8.1 and 13.5, by 151936 x 1024
-// 25 and 38; SwiGLU, 16 rows by 3072 x 1024 5.5 and 6.7, 64 rows 8.9 and 6.8 (its runs lie across lanes here).
-bool few(int T, bool glu) { return T <= (glu ? 16 : 64); }
+// Whether k_mx_gemm_few serves a product of nk stages and tiles of W. Measured against k_mx_gemm (us, 8 by 4 bits): linear, 64 rows
+// by 4096 x 4096 8.1 and 13.5, by 151936 x 1024 25 and 38; 128 rows by 1024 x 8192 9.0 and 22.9, by 4096 x 2048 8.3 and 9.0,
+// by 4096 x 1024 7.6 and 6.6. SwiGLU, whose runs lie across lanes here: 16 rows by 3072 x 1024 5.5 and 6.7; 64 rows by 4096 x 4096
+// 11.7 and 14.1, by 4096 x 1024 8.8 and 6.8, by 6144 x 2048 (two CTAs a tile) 12.6 and 9.7.
+bool few(const qw_mx& x, const qw_mx& w, bool glu) {
+    const size_t nk = x.bits == 4 ? (mx_atoms(x.cols) + 1) / 2 : mx_atoms(x.cols);
+    if (glu) return x.rows <= 16 || (x.rows <= 64 && nk >= 32 && 4 * mx_atoms(w.rows) <= (size_t)device().sms);
+    return x.rows <= 64 || (x.rows <= 128 && nk >= 16);
+}
 
 bool product_few(const qw_mx& x, const qw_mx& wa, const qw_mx& wb, bool glu, int32_t* status, MfP& p, MfMaps& m) {
     p = MfP{};
@@ -891,7 +904,7 @@ bool product_few(const qw_mx& x, const qw_mx& wa, const qw_mx& wb, bool glu, int
     p.sb = (const uint8_t*)wb.dev_scales;
     p.status = status;
     const bool spread = wa.bits == 4 && x.bits == 8;
-    return encode(&m.x, x, false, p.T <= 16 ? 16 : 64) && encode(&m.a, wa, spread, 128) && (!glu || encode(&m.b, wb, spread, 128));
+    return encode(&m.x, x, false, few_box(p.T)) && encode(&m.a, wa, spread, 128) && (!glu || encode(&m.b, wb, spread, 128));
 }
 
 template <int OUT>
@@ -952,7 +965,7 @@ extern "C" qw_status qw_mx_linear(const qw_mx* x, const qw_mx* w, void* dev_out,
     if (((uintptr_t)dev_out & 15) || ld_out % (dtype == QW_F32 ? 4 : 8))
         return qw_fail(QW_ERR_INVALID_ARG, "%s: rows of out not 16-byte aligned", what);
     if (too_many(x->rows, w->rows)) return qw_fail(QW_ERR_UNSUPPORTED, "%s: more than 2^31 tiles", what);
-    if (few(x->rows, false)) {
+    if (few(*x, *w, false)) {
         MfP p;
         MfMaps m;
         if (!product_few(*x, *w, *w, false, dev_status, p, m)) return qw_fail(QW_ERR_CUDA, "%s: tensor map", what);
@@ -990,7 +1003,7 @@ extern "C" qw_status qw_mx_swiglu(const qw_mx* x, const qw_mx* w_gate, const qw_
     if (!dev_status) return qw_fail(QW_ERR_INVALID_ARG, "%s: NULL status", what);
     if (x->rows == 0) return QW_OK;
     if (too_many(x->rows, w_gate->rows)) return qw_fail(QW_ERR_UNSUPPORTED, "%s: more than 2^31 tiles", what);
-    if (few(x->rows, true)) {
+    if (few(*x, *w_gate, true)) {
         MfP p;
         MfMaps m;
         if (!product_few(*x, *w_gate, *w_up, true, dev_status, p, m)) return qw_fail(QW_ERR_CUDA, "%s: tensor map", what);

@@ -420,6 +420,23 @@ def _swiglu(lib, x, g, u, bits, status=None, stream=None, out=None):
     return m
 
 
+@pytest.mark.parametrize("xb,wb", FORMATS)
+@pytest.mark.parametrize("T,K,M,dtype", [(65, 4096, 1000, BF16), (128, 4100, 260, F32), (100, 8192, 130, F16), (127, 4096, 20001, F32), (128, 16000, 1, BF16)])
+def test_linear_long_columns(lib, T, K, M, dtype, xb, wb):
+    """65 to 128 rows: shared by clusters of 8, 4, and a stream of more tiles than CTAs."""
+    rng = np.random.default_rng(T + K + M)
+    x, w = Matrix.of(lib, _acts(rng, T, K), xb), Matrix.of(lib, _weights(rng, M, K), wb)
+    _check_product(_linear(lib, x, w, dtype).double().cpu().numpy(), x.held, w.held, dtype)
+
+
+@pytest.mark.parametrize("xb,wb,ob", [(8, 4, 8), (4, 4, 4), (8, 8, 4), (4, 4, 8)])
+@pytest.mark.parametrize("T,K,I", [(17, 8192, 130), (64, 8100, 256), (33, 8192, 4800)])
+def test_swiglu_long_columns(lib, T, K, I, xb, wb, ob):
+    rng = np.random.default_rng(T + K + I)
+    x, g, u = Matrix.of(lib, _acts(rng, T, K), xb), Matrix.of(lib, _weights(rng, I, K), wb), Matrix.of(lib, _weights(rng, I, K), wb)
+    _check_swiglu(_swiglu(lib, x, g, u, ob), x.held, g.held, u.held)
+
+
 @pytest.mark.parametrize("xb,wb,ob", [(8, 4, 8), (4, 4, 4), (8, 8, 8), (8, 4, 4), (4, 4, 8)])
 @pytest.mark.parametrize("T,K,I", [(1, 1, 1), (1, 1024, 640), (3, 100, 33), (16, 512, 128), (20, 129, 200), (64, 1024, 384), (65, 640, 129),
                                    (128, 256, 1000), (200, 2048, 256), (300, 96, 2000), (2, 4096, 300)])
