@@ -199,7 +199,7 @@ __device__ __forceinline__ float to_odd(double t) {
     return (double)f == t ? f : __uint_as_float(__float_as_uint(f) | 1u);
 }
 
-// s r w to 2^-45, r = 1 / sqrt as a pair.
+// s r w to 2^-45, r = 1 / sqrt as a pair, of what norm_codes lets through: the products' rests are fp32 numbers there.
 __device__ __forceinline__ Pair scale_pair(float s, Pair r, float w) {
     const float a = __fmul_rn(s, r.hi), b = __fmaf_rn(s, r.lo, __fmaf_rn(s, r.hi, -a));
     const float q = __fmul_rn(a, w), f = __fmaf_rn(b, w, __fmaf_rn(a, w, -q));
@@ -225,23 +225,27 @@ __device__ __forceinline__ Pair refine_rsqrt(Pair t, Pair inv_n, float eps, floa
 // argument 1 (two, halved by the root); the sum of squares at most 16 on the way of a term (see k_mx_rmsnorm), halved.
 constexpr float NORM_LO = 1.f - 0x1.2p-20f, NORM_HI = 1.f + 0x1.2p-20f;
 
-// Codes and exponent byte of 8 columns from fp32 values; the whole warp calls, with rstd 0 for padding. again: another
-// code or exponent is possible in this thread's part of the run.
+// Codes and exponent byte of 8 columns from fp32 values; the whole warp calls, with rstd 0 for padding. again: this thread's
+// part of the run has to be computed again, as another code or exponent is possible (NORM_DOUBT) or as fp32 does not hold what
+// its products need (NORM_WIDE). Where the run's largest |y| is at least 2^-30 and no weight above 2^50, a |y| that does not
+// round to 0 (2^-19 of the largest, or more) has an |s| rstd of 2^-99 or more, normal with 24 bits to spare, and none nears fp32's end.
+enum : int { NORM_DOUBT = 1, NORM_WIDE = 2 };
 template <int BITS>
-__device__ __forceinline__ int norm_codes(const float* s, const float* w, float rstd, uint32_t* codes, bool& again) {
-    float y[8];
+__device__ __forceinline__ int norm_codes(const float* s, const float* w, float rstd, uint32_t* codes, int& again) {
+    float y[8], top = 0.f;
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         y[i] = s[i] * rstd * w[i];
         m = max(m, __float_as_uint(y[i]) & 0x7FFFFFFFu);
+        top = fmaxf(top, fabsf(w[i]));
     }
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
     const int byte = mx_exp_byte<BITS>(m);
-    // the largest next to L 2^e (d of 1.75 is 16 units of the mantissa), or so small that s rstd may have underflowed
+    // the largest next to L 2^e (d of 1.75 is 16 units of the mantissa)
     constexpr uint32_t M = BITS == 8 ? 0x600000u : 0x400000u;
-    again = ((m - M + 16u) & 0x7FFFFFu) <= 32u || (m < 0x30800000u && m != 0u);
+    again = ((m - M + 16u) & 0x7FFFFFu) <= 32u ? NORM_DOUBT : 0;
     const float inv = mx_inv_scale(byte);
     const float lo = inv * NORM_LO, hi = inv * NORM_HI;
     float a[8];
@@ -252,7 +256,13 @@ __device__ __forceinline__ int norm_codes(const float* s, const float* w, float 
 #pragma unroll
     for (int i = 0; i < 8; ++i) a[i] = y[i] * hi;
     mx_enc8<BITS>(a, cb);
-    again |= codes[0] != cb[0] || codes[1] != cb[1];
+    if (codes[0] != cb[0] || codes[1] != cb[1]) again = NORM_DOUBT;
+    if (top > 0x1p50f) again = NORM_WIDE;
+    if (m < 0x30800000u) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (s[i] != 0.f && w[i] != 0.f) again = NORM_WIDE;
+    }
     return byte;
 }
 
@@ -340,6 +350,54 @@ __device__ __forceinline__ void norm_store_scales(const MxNormP& p, size_t row, 
     if (ok && (threadIdx.x & 15) == 0) *reinterpret_cast<uint32_t*>(p.scales + mx_scale_word((int)row, v / 16, p.atoms)) = sw;
 }
 
+// Codes and exponent byte of 8 columns from 64-bit values; the four lanes of a run (mask) call together.
+template <int BITS>
+__device__ __forceinline__ int norm_codes64(const double* y, uint32_t mask, uint32_t* codes) {
+    double m = 0.0;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        bad |= !(fabs(y[i]) <= 3.4028234663852886e38);
+        m = fmax(m, fabs(y[i]));
+    }
+    m = fmax(m, __shfl_xor_sync(mask, m, 1));
+    m = fmax(m, __shfl_xor_sync(mask, m, 2));
+    bad = (__ballot_sync(mask, bad) & mask) != 0;
+    // e = min{e >= -127 : m <= L 2^e}; m = (1 + frac 2^-52) 2^x
+    const long long b = __double_as_longlong(m);
+    const int x = (int)(b >> 52) - 1023;
+    const long long frac = b & 0xFFFFFFFFFFFFFll;
+    const int e = BITS == 8 ? x - 8 + (frac > 0xC000000000000ll) : x - 2 + (frac > 0x8000000000000ll);
+    const int byte = bad ? 255 : min(254, max(0, e + 127));
+    const double inv = bad ? 0.0 : __longlong_as_double((long long)(1023 + 127 - byte) << 52);
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = to_odd(y[i] * inv);
+    mx_enc8<BITS>(f, codes);
+    return byte;
+}
+
+// 8 columns of a NORM_WIDE run, r = 1 / sqrt as a pair: s, read back if it was written (x may be under it), and y in 64 bits.
+// Such runs are rare: a call keeps what they need out of the others' registers.
+struct RunCodes {
+    uint32_t q[2];
+    int byte;
+};
+template <int DT, int BITS>
+__device__ __noinline__ RunCodes norm_wide_run(const MxNormP& p, int row, int v, int left, Pair r, uint32_t mask) {
+    float s[8], w[8];
+    if (p.sum) mx_load8<DT>(p.sum, (size_t)row * p.ld_sum + v * 8, left, s);
+    else norm_load<DT>(p, row, v * 8, left, s);
+    mx_load8<QW_BF16>(p.w, v * 8, left, w);
+    const double rstd = (double)r.hi + (double)r.lo;
+    double y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = left > 0 ? (double)s[i] * rstd * (double)w[i] : 0.0;
+    RunCodes c;
+    c.byte = norm_codes64<BITS>(y, mask, c.q);
+    return c;
+}
+
 // A row whose squares (or what pairs hold of them) leave fp32, or that holds a NaN or an infinity: everything in fp64, read again from memory.
 template <int DT, int BITS>
 __device__ __noinline__ void norm_wide_row(const MxNormP& p, int row, double* part) {
@@ -369,29 +427,11 @@ __device__ __noinline__ void norm_wide_row(const MxNormP& p, int row, double* pa
         norm_load<DT>(p, row, v * 8, left, s);
         mx_load8<QW_BF16>(p.w, v * 8, left, w);
         if (p.sum && left > 0) mx_store8<DT, false>(p.sum, row * p.ld_sum + v * 8, left, s);
-        double y[8], m = 0.0;
-        bool bad = false;
+        double y[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            y[i] = left > 0 ? (double)s[i] * rstd * (double)w[i] : 0.0;
-            bad |= !(fabs(y[i]) <= 3.4028234663852886e38);
-            m = fmax(m, fabs(y[i]));
-        }
-        m = fmax(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = fmax(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        bad = (__ballot_sync(0xffffffffu, bad) & (0xFu << (lane & 28))) != 0;
-        // e = min{e >= -127 : m <= L 2^e}; m = (1 + frac 2^-52) 2^x
-        const long long b = __double_as_longlong(m);
-        const int x = (int)(b >> 52) - 1023;
-        const long long frac = b & 0xFFFFFFFFFFFFFll;
-        const int e = BITS == 8 ? x - 8 + (frac > 0xC000000000000ll) : x - 2 + (frac > 0x8000000000000ll);
-        const int byte = bad ? 255 : min(254, max(0, e + 127));
-        const double inv = bad ? 0.0 : __longlong_as_double((long long)(1023 + 127 - byte) << 52);
-        float f[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = to_odd(y[i] * inv);
+        for (int i = 0; i < 8; ++i) y[i] = left > 0 ? (double)s[i] * rstd * (double)w[i] : 0.0;
         uint32_t q[2];
-        mx_enc8<BITS>(f, q);
+        const int byte = norm_codes64<BITS>(y, 0xFu << (lane & 28), q);
         if (v < vecs) norm_store<BITS>(p, row, v, q);
         norm_store_scales(p, row, v, v < vecs, byte);
     }
@@ -483,8 +523,8 @@ __global__ void __launch_bounds__(VPT == 1 ? 128 : 512, VPT == 1 ? 12 : VPT == 2
     const float rstd = rsqrtf(mean);
     Pair r = {0.f, 0.f};
     const uint32_t mask = 0xFu << (lane & 28);  // the four lanes of a run
-    bool again[N], any = false;
-    int byte[N];
+    int again[N], byte[N];
+    bool any = false;
     if constexpr (!VPT) r = refine_rsqrt(t, p.inv_n, p.eps, rstd);
     for (int j = 0; j < steps; ++j) {
 #pragma unroll
@@ -500,10 +540,17 @@ __global__ void __launch_bounds__(VPT == 1 ? 128 : 512, VPT == 1 ? 12 : VPT == 2
             if (p.sum && left > 0) mx_store8<DT, false>(p.sum, row * p.ld_sum + v * 8, left, s[k]);
             uint32_t q[2];
             byte[k] = norm_codes<BITS>(s[k], w, left > 0 ? rstd : 0.f, q, again[k]);
-            if (!VPT && (__ballot_sync(0xffffffffu, again[k]) & mask))
-                byte[k] = norm_pairs<BITS>(s[k], w, left > 0 ? r : Pair{0.f, 0.f}, mask, q);
-            __syncwarp();
-            any |= again[k];
+            if (!VPT) {
+                const uint32_t doubt = __ballot_sync(0xffffffffu, again[k]), wide = __ballot_sync(0xffffffffu, again[k] == NORM_WIDE);
+                if (wide & mask) {
+                    const RunCodes c = norm_wide_run<DT, BITS>(p, row, v, left, r, mask);
+                    byte[k] = c.byte, q[0] = c.q[0], q[1] = c.q[1];
+                } else if (doubt & mask) {
+                    byte[k] = norm_pairs<BITS>(s[k], w, left > 0 ? r : Pair{0.f, 0.f}, mask, q);
+                }
+                __syncwarp();
+            }
+            any |= again[k] != 0;
             if (v < vecs) norm_store<BITS>(p, row, v, q);
             norm_store_scales(p, row, v, v < vecs, byte[k]);
         }
@@ -520,9 +567,13 @@ __global__ void __launch_bounds__(VPT == 1 ? 128 : 512, VPT == 1 ? 12 : VPT == 2
 #pragma unroll
         for (int k = 0; k < N; ++k) {
             const int v = k * blockDim.x + threadIdx.x, left = v < vecs ? p.cols - v * 8 : 0;
-            const uint32_t doubt = __ballot_sync(0xffffffffu, again[k]);
+            const uint32_t doubt = __ballot_sync(0xffffffffu, again[k]), wide = __ballot_sync(0xffffffffu, again[k] == NORM_WIDE);
             if (!doubt) continue;
-            if (doubt & mask) {
+            if (wide & mask) {
+                const RunCodes c = norm_wide_run<DT, BITS>(p, row, v, left, r, mask);
+                byte[k] = c.byte;
+                if (v < vecs) norm_store<BITS>(p, row, v, c.q);
+            } else if (doubt & mask) {
                 float w[8];
                 mx_unpack8<QW_BF16>(wr[k], w);
                 uint32_t q[2];

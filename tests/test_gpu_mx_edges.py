@@ -1,4 +1,5 @@
-"""Microscaled matrices where a hair decides a code: SwiGLU's values next to the border between two codes."""
+"""Microscaled matrices where a hair decides a code: SwiGLU's values and RMSNorm's next to the border between two
+codes, runs that are tiny or huge beside their row."""
 
 import numpy as np
 import pytest
@@ -8,7 +9,7 @@ from oracle import mx
 
 pytestmark = pytest.mark.gpu
 
-F32 = base.F32
+F32, BF16 = base.F32, base.BF16
 
 
 @pytest.fixture
@@ -66,3 +67,82 @@ def test_swiglu_next_to_borders(lib, T, xb, wb, ob):
     for m, want in ((mg, g), (mu, u)):
         np.testing.assert_array_equal(base._linear(lib, x, m, F32).double().cpu().numpy(), np.tile(want, (T, 1)))
     base._swiglu(lib, x, mg, mu, ob).check(*mx.quantize(np.tile(h, (T, 1)), ob))
+
+
+def _check_norm(lib, x, add, w, bits, dtype, add_type, eps=1e-6, **kw):
+    """Codes and exponents are those of the real numbers; a |y| above fp32's range makes its run NaN."""
+    m, s, wf = base._norm(lib, x, add, w, bits, dtype, add_type, eps=eps, **kw)
+    y = mx.rmsnorm(s, wf, float(np.float32(eps)))
+    m.check(*mx.quantize(np.where(np.abs(y) > 3.4028234663852886e38, np.inf, y), bits))
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("cols", [96, 1024, 3000, 10000, 20000])
+def test_rmsnorm_tiny_runs(lib, cols, bits):
+    """Runs that are tiny beside their row, each value as near to a border between two codes of 2^-127 as an fp32 x can be: the
+    products by 1 / sqrt are subnormal, or their roundings' rests are."""
+    import torch
+    rng = np.random.default_rng(cols)
+    rows = 6
+    x = base._norm_rows(rng, rows, cols).double().numpy()
+    tiny = np.arange(cols) // 32 % 3 == 1
+    x[:, tiny] = 0.0
+    w = np.ones(cols)
+    w[32:64] = 2.0 ** -20  # and where it is the weight that makes them tiny
+    step = 2.0 ** -127 * (2.0 ** -9 if bits == 8 else 0.5)
+    for r in range(rows):
+        rstd = 1 / np.sqrt((x[r] * x[r]).mean() + float(np.float32(1e-6)))  # the tiny runs add nothing to it in 64 bits
+        n = tiny.sum()
+        border = (rng.integers(0, 8, (n, 200)) + 0.5) * step
+        c = border / rstd / w[tiny][:, None]
+        c32 = c.astype(np.float32).astype(np.float64)
+        off = np.abs(c32 / c - 1)
+        best = off.argmin(1)
+        x[r, tiny] = c32[np.arange(n), best] * rng.choice([-1.0, 1.0], n)
+    x[1, tiny] *= 2.0 ** rng.integers(0, 60)  # and a row whose tiny runs are less so
+    _check_norm(lib, torch.from_numpy(x.astype(np.float32)), None, w, bits, F32, None)
+    b = base._norm_rows(rng, rows, cols).to(torch.bfloat16)  # sums that cancel to a tiny rest, over x and unwritten
+    b[:, torch.from_numpy(tiny)] = 0
+    for kw in (dict(inplace=True), dict(want_sum=False)):
+        _check_norm(lib, torch.from_numpy(x.astype(np.float32)), b.float(), w, bits, F32, BF16, **kw)
+    xb = torch.from_numpy(x).float().to(torch.bfloat16).float()
+    _check_norm(lib, xb, None, w, bits, BF16, None)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("cols", [96, 1024, 3000, 20000])
+def test_rmsnorm_huge_and_tiny_weights(lib, cols, bits):
+    """Weights from 2^-133 to 2^127 before values from 2^-149 to the row's largest: y = 2^-17 with s / sqrt subnormal, y next to the
+    end of fp32 and beyond it."""
+    import torch
+    rng = np.random.default_rng(cols)
+    x = base._norm_rows(rng, 8, cols).double().numpy()
+    run = np.arange(cols) // 32 % 6
+    w = 1 + 0.1 * rng.normal(0, 1, cols)
+    w[run == 1] *= 2.0 ** 120
+    x[:, run == 1] = rng.integers(-5000, 5000, (8, (run == 1).sum())) * 2.0 ** -149
+    w[run == 2] *= 2.0 ** rng.integers(-130, -20, (run == 2).sum()).astype(float)
+    w[run == 4] *= 2.0 ** 77
+    x[:, run == 4] *= 2.0 ** -100
+    w[0] = 2.0 ** 127
+    if cols > 200:
+        w[64:96] = 2.0 ** 126
+    w = torch.from_numpy(w).to(torch.bfloat16).double().numpy()
+    _check_norm(lib, torch.from_numpy(x.astype(np.float32)), None, w, bits, F32, None)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+def test_rmsnorm_end_of_fp32(lib, bits):
+    """Rows of equal values, y = w s / sqrt(s^2 + eps): the largest |y| some 2^-24 around fp32's largest number."""
+    import torch
+    w = np.zeros(128)
+    w[0], w[40] = 2.0 ** 127 * (2 - 2.0 ** -7), 2.0 ** 127  # the largest bf16: y up to it, below fp32's largest
+    x = np.zeros((64, 128))
+    # y_0 = w_0 x_0 / sqrt(mean): mean = (x_0^2 + x_40^2) / 128; x_40 sets how far y_0 is from the end
+    end = 3.4028234663852886e38
+    for r in range(64):
+        x[r, 0] = 1.0
+        want = end * (1 + (r - 32) * 2.0 ** -25)
+        x[r, 40] = np.sqrt(128 * (w[0] / want) ** 2 - 1)
+    x = torch.from_numpy(x.astype(np.float32))
+    _check_norm(lib, x, None, w, bits, F32, None, eps=1e-20)
