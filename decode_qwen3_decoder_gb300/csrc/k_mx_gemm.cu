@@ -35,8 +35,11 @@
 // bytes bound it: 60000 x 4096 by one row 41 us in 8 bits (6.0 TB/s), 23 in 4 by 4 (5.7), 27 in 8 by 4 (4.8: spread
 // codes fill the ring with half as many bytes of memory).
 //
-// Every wait is bounded (about 2 s): then QW_MX_TIMEOUT is set, and the CTA lets its copies and MMAs land, frees its
-// tensor memory and ends.
+// Every wait for a copy, an MMA or a warp is bounded (2 s): then QW_MX_TIMEOUT is set, and the CTA lets its copies and MMAs
+// land, frees its tensor memory and ends. Two waits have no bound of their own: the cluster's barriers, which every CTA reaches
+// on this way too, and tcgen05.alloc, which waits for CTAs that have the SM's columns. These wait for no CTA that could wait
+// for this one's: kernels of the library whose CTAs wait for one another have an SM's shared memory to themselves, or a share
+// like that of its columns (MfCfg), so that none of them is on this SM without its columns.
 #include <algorithm>
 #include <atomic>
 
@@ -62,6 +65,13 @@ struct MgCfg {
     static_assert(SMEM <= 232448 && MG_SF_COL + STAGES * MG_SF_COLS <= 512, "shared or tensor memory");
 };
 
+// How long a wait lasts at most, and for tests the barriers that get an arrival too few (qw_mx_test_stall).
+struct MxWaits {
+    uint32_t ns;
+    int stall;
+};
+__device__ __forceinline__ uint32_t count_of(const MxWaits& w, int barrier, uint32_t n) { return n + ((w.stall & barrier) != 0); }
+
 struct MxGemmP {
     int T, M, atoms;  // rows of X, rows of W (of gate and of up), atoms of 128 columns
     int tiles_x, tiles_w, units;
@@ -72,6 +82,7 @@ struct MxGemmP {
     uint8_t *codes, *scales;  // SwiGLU's output
     int oatoms;
     int32_t* status;
+    MxWaits waits;
 };
 
 // A wait as in tc_sm103.cuh, but the thread sleeps until the phase completes.
@@ -86,11 +97,11 @@ __device__ __forceinline__ bool try_sleep(uint32_t bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
-__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int* abort_flag, const MxWaits& w) {
     if (try_sleep(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
     while (!try_sleep(bar, parity))
-        if (*abort_flag || globaltimer_ns() - t0 > kTcWaitNs) return false;
+        if (*abort_flag || globaltimer_ns() - t0 > w.ns) return false;
     return true;
 }
 // After a wait that gave up: copies and MMAs in flight land within microseconds; a millisecond is enough for all of them.
@@ -273,12 +284,12 @@ __global__ void __launch_bounds__(MG_THREADS, 1) k_mx_gemm(const __grid_constant
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
-            mbar_init(smem_u32(full + s), 2);  // the producer, and the copies of exponents when they are complete
-            mbar_init(smem_u32(empty + s), 1);
-            mbar_init(smem_u32(sfull + s), 1);
+            mbar_init(smem_u32(full + s), count_of(p.waits, QW_MX_STALL_FULL, 2));  // the producer, and the copies of exponents when they are complete
+            mbar_init(smem_u32(empty + s), count_of(p.waits, QW_MX_STALL_EMPTY, 1));
+            mbar_init(smem_u32(sfull + s), count_of(p.waits, QW_MX_STALL_SFULL, 1));
         }
-        mbar_init(smem_u32(accf), 1);
-        mbar_init(smem_u32(acce), 16);  // the epilogue warps of both CTAs
+        mbar_init(smem_u32(accf), count_of(p.waits, QW_MX_STALL_ACCF, 1));
+        mbar_init(smem_u32(acce), count_of(p.waits, QW_MX_STALL_ACCE, 16));  // the epilogue warps of both CTAs
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -311,7 +322,7 @@ __global__ void __launch_bounds__(MG_THREADS, 1) k_mx_gemm(const __grid_constant
                 const int wa = tw * p.w_step, wb = wa + p.b_row;
                 for (int kb = 0; kb < nk; ++kb, ++g) {
                     const int s = g % C::STAGES;
-                    if (!wait_phase(smem_u32(empty + s), ((g / C::STAGES) & 1u) ^ 1u, abort_flag)) {
+                    if (!wait_phase(smem_u32(empty + s), ((g / C::STAGES) & 1u) ^ 1u, abort_flag, p.waits)) {
                         *abort_flag = 1;
                         break;
                     }
@@ -338,10 +349,10 @@ __global__ void __launch_bounds__(MG_THREADS, 1) k_mx_gemm(const __grid_constant
             int i = 0;
             bool ok = true;
             for (int u = pair; u < p.units && ok; u += pairs, ++i) {
-                ok = wait_phase(smem_u32(acce), ((uint32_t)i & 1u) ^ 1u, abort_flag);
+                ok = wait_phase(smem_u32(acce), ((uint32_t)i & 1u) ^ 1u, abort_flag, p.waits);
                 for (int kb = 0; kb < nk && ok; ++kb, ++g) {
                     const int s = g % C::STAGES;
-                    ok = wait_phase(smem_u32(full + s), (g / C::STAGES) & 1u, abort_flag);
+                    ok = wait_phase(smem_u32(full + s), (g / C::STAGES) & 1u, abort_flag, p.waits);
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t st = smem_u32(smem + s * MG_STAGE);
@@ -369,7 +380,7 @@ __global__ void __launch_bounds__(MG_THREADS, 1) k_mx_gemm(const __grid_constant
             const uint32_t total = (uint32_t)((p.units - pair + pairs - 1) / pairs) * nk;
             for (uint32_t g = 0; g < total; ++g) {
                 const int s = g % C::STAGES;
-                if (!wait_phase(smem_u32(sfull + s), (g / C::STAGES) & 1u, abort_flag)) {
+                if (!wait_phase(smem_u32(sfull + s), (g / C::STAGES) & 1u, abort_flag, p.waits)) {
                     *abort_flag = 1;
                     break;
                 }
@@ -396,7 +407,7 @@ __global__ void __launch_bounds__(MG_THREADS, 1) k_mx_gemm(const __grid_constant
             const int tw = u % p.tiles_w, tx = 2 * (u / p.tiles_w) + rank;
             const int t = tx * 128 + (warp & 3) * 32 + lane;
             int ok = 0;
-            if (lane == 0) ok = wait_phase(smem_u32(accf), (uint32_t)i & 1u, abort_flag);
+            if (lane == 0) ok = wait_phase(smem_u32(accf), (uint32_t)i & 1u, abort_flag, p.waits);
             if (!__shfl_sync(0xffffffffu, ok, 0)) {
                 *abort_flag = 1;
                 break;
@@ -455,6 +466,7 @@ struct MfP {
     size_t ld;
     uint8_t *codes, *scales;
     int32_t* status;
+    MxWaits waits;
 };
 struct MfMaps {
     CUtensorMap x, a, b;
@@ -556,13 +568,13 @@ __global__ void __launch_bounds__(MF_THREADS) k_mx_gemm_few(const __grid_constan
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
-            mbar_init(smem_u32(full + s), 2);
-            mbar_init(smem_u32(empty + s), 1);
-            mbar_init(smem_u32(sfull + s), 1);
+            mbar_init(smem_u32(full + s), count_of(p.waits, QW_MX_STALL_FULL, 2));
+            mbar_init(smem_u32(empty + s), count_of(p.waits, QW_MX_STALL_EMPTY, 1));
+            mbar_init(smem_u32(sfull + s), count_of(p.waits, QW_MX_STALL_SFULL, 1));
         }
         for (int b = 0; b < 2; ++b) {
-            mbar_init(smem_u32(accf + b), 1);
-            mbar_init(smem_u32(acce + b), 4);
+            mbar_init(smem_u32(accf + b), count_of(p.waits, QW_MX_STALL_ACCF, 1));
+            mbar_init(smem_u32(acce + b), count_of(p.waits, QW_MX_STALL_ACCE, 4));
         }
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -591,7 +603,7 @@ __global__ void __launch_bounds__(MF_THREADS) k_mx_gemm_few(const __grid_constan
             for (int tw = tw0; tw < p.tiles_w && !*abort_flag; tw += step)
                 for (int j = 0; j < nk; ++j, ++g) {
                     const int s = g % C::STAGES, kb = kb0 + j;
-                    if (!wait_phase(smem_u32(empty + s), ((g / C::STAGES) & 1u) ^ 1u, abort_flag)) {
+                    if (!wait_phase(smem_u32(empty + s), ((g / C::STAGES) & 1u) ^ 1u, abort_flag, p.waits)) {
                         *abort_flag = 1;
                         break;
                     }
@@ -617,11 +629,11 @@ __global__ void __launch_bounds__(MF_THREADS) k_mx_gemm_few(const __grid_constan
             bool ok = true;
             for (int tw = tw0; tw < p.tiles_w && ok; tw += step, ++i) {
                 const int buf = i & 1;
-                ok = wait_phase(smem_u32(acce + buf), ((uint32_t)(i >> 1) & 1u) ^ 1u, abort_flag);
+                ok = wait_phase(smem_u32(acce + buf), ((uint32_t)(i >> 1) & 1u) ^ 1u, abort_flag, p.waits);
                 const uint32_t d = tmem + buf * NW * BN;
                 for (int j = 0; j < nk && ok; ++j, ++g) {
                     const int s = g % C::STAGES;
-                    ok = wait_phase(smem_u32(full + s), (g / C::STAGES) & 1u, abort_flag);
+                    ok = wait_phase(smem_u32(full + s), (g / C::STAGES) & 1u, abort_flag, p.waits);
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t st = smem_u32(smem + s * C::STAGE), sf = tmem + C::SF_COL + s * C::SF_COLS;
@@ -650,7 +662,7 @@ __global__ void __launch_bounds__(MF_THREADS) k_mx_gemm_few(const __grid_constan
             const uint32_t total = (uint32_t)((p.tiles_w - tw0 + step - 1) / step) * nk;
             for (uint32_t g = 0; g < total; ++g) {
                 const int s = g % C::STAGES;
-                if (!wait_phase(smem_u32(sfull + s), (g / C::STAGES) & 1u, abort_flag)) {
+                if (!wait_phase(smem_u32(sfull + s), (g / C::STAGES) & 1u, abort_flag, p.waits)) {
                     *abort_flag = 1;
                     break;
                 }
@@ -673,7 +685,7 @@ __global__ void __launch_bounds__(MF_THREADS) k_mx_gemm_few(const __grid_constan
         for (int tw = tw0; tw < p.tiles_w; tw += step, ++i) {
             const int buf = i & 1, f = tw * 128 + fl;
             int got = 0;
-            if (lane == 0) got = wait_phase(smem_u32(accf + buf), (uint32_t)(i >> 1) & 1u, abort_flag);
+            if (lane == 0) got = wait_phase(smem_u32(accf + buf), (uint32_t)(i >> 1) & 1u, abort_flag, p.waits);
             ok = __shfl_sync(0xffffffffu, got, 0);
             if (!ok) {
                 *abort_flag = 1;
@@ -757,6 +769,10 @@ __global__ void __launch_bounds__(MF_THREADS) k_mx_gemm_few(const __grid_constan
 }
 
 // ---- host ------------------------------------------------------------------------------------------------
+
+std::atomic<uint32_t> wait_ns{(uint32_t)kTcWaitNs};
+std::atomic<int> stall{0};
+MxWaits waits() { return {wait_ns.load(std::memory_order_relaxed), stall.load(std::memory_order_relaxed)}; }
 
 typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -904,6 +920,7 @@ bool product_few(const qw_mx& x, const qw_mx& wa, const qw_mx& wb, bool glu, int
     p.sa = (const uint8_t*)wa.dev_scales;
     p.sb = (const uint8_t*)wb.dev_scales;
     p.status = status;
+    p.waits = waits();
     const bool spread = wa.bits == 4 && x.bits == 8;
     return encode(&m.x, x, false, few_box(p.T)) && encode(&m.a, wa, spread, 128) && (!glu || encode(&m.b, wb, spread, 128));
 }
@@ -935,6 +952,7 @@ bool product(const qw_mx& x, const qw_mx& wa, const qw_mx& wb, bool glu, int32_t
     p.tiles_w = (int)(((long long)p.M + p.w_step - 1) / p.w_step);
     p.units = p.tiles_x * p.tiles_w;
     p.status = status;
+    p.waits = waits();
     const bool spread = wa.bits == 4 && x.bits == 8;
     const unsigned at = x.bits == 4 ? 2 : 1;
     if (!encode(&m.x, x, false, 128) || !encode(&m.a, wa, spread, 128) || !encode_scales(&m.sx, x, at) || !encode_scales(&m.sa, wa, at)) return false;
@@ -951,6 +969,14 @@ qw_status done(cudaError_t e, const char* what) {
 bool too_many(int T, int M) { return (double)(T / 256 + 1) * (M / 128 + 1) > 2147483647.0; }
 
 }  // namespace
+
+extern "C" qw_status qw_mx_test_stall(int barriers, int wait_us) {
+    if (barriers < 0 || barriers > 31) return qw_fail(QW_ERR_INVALID_ARG, "mx_test_stall: barriers %d", barriers);
+    if (wait_us != 0 && (wait_us < 100 || wait_us > 2000000)) return qw_fail(QW_ERR_INVALID_ARG, "mx_test_stall: wait_us %d", wait_us);
+    stall.store(barriers, std::memory_order_relaxed);
+    wait_ns.store(wait_us ? wait_us * 1000u : (uint32_t)kTcWaitNs, std::memory_order_relaxed);
+    return QW_OK;
+}
 
 extern "C" qw_status qw_mx_linear(const qw_mx* x, const qw_mx* w, void* dev_out, size_t ld_out, int dtype,
                                   int32_t* dev_status, void* stream) {

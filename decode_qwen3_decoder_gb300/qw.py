@@ -124,6 +124,7 @@ SIGNATURES = {
     "qw_mx_rmsnorm": (_I, [_P(qw_mx), _VP, _SZ, _I, _VP, _SZ, _I, _VP, _SZ, _VP, ctypes.c_float, _VP]),
     "qw_mx_linear": (_I, [_P(qw_mx), _P(qw_mx), _VP, _SZ, _I, _VP, _VP]),
     "qw_mx_swiglu": (_I, [_P(qw_mx), _P(qw_mx), _P(qw_mx), _P(qw_mx), _VP, _VP]),
+    "qw_mx_test_stall": (_I, [_I, _I]),
     "qw_lm_head_argmax_noalloc": (_I, [_VP, _I, _VP, _VP, _VP, _VP]),
 }
 
@@ -405,6 +406,7 @@ def qw_kv8_evict(kv: qw_kv8, B: int, max_len: int, len_ptr: int, n_keep: int, n_
 
 
 QW_MX_TIMEOUT = 2
+QW_MX_STALL_FULL, QW_MX_STALL_EMPTY, QW_MX_STALL_SFULL, QW_MX_STALL_ACCF, QW_MX_STALL_ACCE = 1, 2, 4, 8, 16
 
 
 def qw_mx_code_bytes(bits: int, rows: int, cols: int) -> int:
@@ -442,6 +444,11 @@ def qw_mx_linear(x: qw_mx, w: qw_mx, out_ptr: int, ld_out: int, dtype: int, stat
 def qw_mx_swiglu(x: qw_mx, w_gate: qw_mx, w_up: qw_mx, out: qw_mx, status_ptr: int, stream=None) -> None:
     _check(load().qw_mx_swiglu(ctypes.byref(x), ctypes.byref(w_gate), ctypes.byref(w_up), ctypes.byref(out), status_ptr,
                                _stream(stream)))
+
+
+def qw_mx_test_stall(barriers: int, wait_us: int) -> None:
+    """For tests: products that give up; see include/qw.h."""
+    _check(load().qw_mx_test_stall(barriers, wait_us))
 
 
 def qw_lm_head_argmax_noalloc(model: int, B: int, x_ptr: int, logits_ptr: int, next_ptr: int,

@@ -569,6 +569,16 @@ qw_status qw_mx_linear(const qw_mx* x, const qw_mx* w, void* dev_out, size_t ld_
 qw_status qw_mx_swiglu(const qw_mx* x, const qw_mx* w_gate, const qw_mx* w_up, const qw_mx* out, int32_t* dev_status,
                        void* stream);
 
+/* For tests: the products launched from now on, by any thread, expect an arrival that never comes at the barriers of
+ * the mask (QW_MX_STALL_*), and their waits give up after wait_us (100 to 2000000; 0: 2 s), so that they return with
+ * QW_MX_TIMEOUT in *dev_status. (0, 0) ends that. */
+#define QW_MX_STALL_FULL 1  /* a stage's operands   */
+#define QW_MX_STALL_EMPTY 2 /* a stage's release    */
+#define QW_MX_STALL_SFULL 4 /* a stage's exponents  */
+#define QW_MX_STALL_ACCF 8  /* a finished tile      */
+#define QW_MX_STALL_ACCE 16 /* a tile's release     */
+qw_status qw_mx_test_stall(int barriers, int wait_us);
+
 /* ---- For callers that cannot allocate device memory ---------------------------------- */
 
 /* The page has no counterpart to this entry point; it serves callers that must not call
