@@ -667,10 +667,36 @@ qw_status mx_check(const qw_mx* m, const char* what, const char* name) {
     return QW_OK;
 }
 
+bool mx_meet(const MxSpan& a, const MxSpan& b) {
+    if (a.rows == 0 || b.rows == 0) return false;
+    if (a.rows == 1 || a.len == a.step) {  // one block against rows
+        const uintptr_t lo = a.at, hi = a.at + (a.rows - 1) * a.step + a.len;
+        const size_t i = b.rows == 1 || lo <= b.at ? 0 : std::min(b.rows - 1, (lo - b.at) / b.step);  // the last row that begins before the block
+        const uintptr_t row = b.at + i * b.step;
+        return (lo < row + b.len && row < hi) || (i + 1 < b.rows && row + b.step < hi);
+    }
+    if (b.rows == 1 || b.len == b.step) return mx_meet(b, a);
+    if (a.step != b.step) return false;
+    // b's row j begins d bytes after a's row k + j
+    const long long step = (long long)a.step, off = (long long)(b.at - a.at), k = off >= 0 ? off / step : -((step - 1 - off) / step);
+    const size_t d = (size_t)(off - k * step);
+    const auto both = [&](long long first) { return first < (long long)a.rows && first + (long long)b.rows > 0; };
+    return (d < a.len && both(k)) || (d + b.len > a.step && both(k + 1));
+}
+bool mx_meet(const qw_mx& m, const MxSpan& b) {
+    const size_t codes = qw_mx_code_bytes(m.bits, m.rows, m.cols), scales = qw_mx_scale_bytes(m.rows, m.cols);
+    return m.rows && (mx_meet(MxSpan{(uintptr_t)m.dev_codes, 1, codes, codes}, b) || mx_meet(MxSpan{(uintptr_t)m.dev_scales, 1, scales, scales}, b));
+}
+bool mx_meet(const qw_mx& a, const qw_mx& b) {
+    const size_t codes = qw_mx_code_bytes(b.bits, b.rows, b.cols), scales = qw_mx_scale_bytes(b.rows, b.cols);
+    return b.rows && (mx_meet(a, MxSpan{(uintptr_t)b.dev_codes, 1, codes, codes}) || mx_meet(a, MxSpan{(uintptr_t)b.dev_scales, 1, scales, scales}));
+}
+
 extern "C" qw_status qw_mx_quantize(const qw_mx* out, const void* dev_x, size_t ld_x, int dtype, void* stream) {
     if (qw_status s = mx_check(out, "mx_quantize", "out")) return s;
     if (out->rows == 0) return QW_OK;
     if (qw_status s = rows_check(dev_x, ld_x, dtype, out->cols, "mx_quantize", "x")) return s;
+    if (mx_meet(*out, mx_rows_span(dev_x, out->rows, out->cols, ld_x, dtype))) return qw_fail(QW_ERR_INVALID_ARG, "mx_quantize: out overlaps x");
     const MxRowsP p = rows_p(out, dev_x, nullptr, ld_x);
     const cudaStream_t st = (cudaStream_t)stream;
 #define MX_Q(dt, bits) launch_quantize<dt, bits>(p, st)
@@ -681,6 +707,7 @@ extern "C" qw_status qw_mx_read(const qw_mx* m, void* dev_x, size_t ld_x, int dt
     if (qw_status s = mx_check(m, "mx_read", "m")) return s;
     if (m->rows == 0) return QW_OK;
     if (qw_status s = rows_check(dev_x, ld_x, dtype, m->cols, "mx_read", "x")) return s;
+    if (mx_meet(*m, mx_rows_span(dev_x, m->rows, m->cols, ld_x, dtype))) return qw_fail(QW_ERR_INVALID_ARG, "mx_read: x overlaps m");
     const MxRowsP p = rows_p(m, nullptr, dev_x, ld_x);
     const cudaStream_t st = (cudaStream_t)stream;
 #define MX_R(dt, bits) launch_read<dt, bits>(p, st)
@@ -702,6 +729,12 @@ extern "C" qw_status qw_mx_rmsnorm(const qw_mx* out, const void* dev_x, size_t l
         if (dev_sum == dev_add) return qw_fail(QW_ERR_INVALID_ARG, "mx_rmsnorm: sum over add");
     }
     if (!dev_weight || !aligned16(dev_weight)) return qw_fail(QW_ERR_INVALID_ARG, "mx_rmsnorm: weight NULL or not 16-byte aligned");
+    const MxSpan x = mx_rows_span(dev_x, out->rows, out->cols, ld_x, x_dtype), add = mx_rows_span(dev_add, out->rows, out->cols, ld_add, add_dtype),
+                 sum = mx_rows_span(dev_sum, out->rows, out->cols, ld_sum, x_dtype), w = mx_rows_span(dev_weight, 1, out->cols, out->cols, QW_BF16);
+    if ((dev_sum != dev_x && mx_meet(sum, x)) || mx_meet(sum, add) || mx_meet(sum, w))
+        return qw_fail(QW_ERR_INVALID_ARG, "mx_rmsnorm: sum overlaps an input that it is not");
+    if (mx_meet(*out, x) || mx_meet(*out, add) || mx_meet(*out, sum) || mx_meet(*out, w))
+        return qw_fail(QW_ERR_INVALID_ARG, "mx_rmsnorm: out overlaps another operand");
     const double inv_n = 1.0 / out->cols;
     const MxNormP p = {(uint8_t*)out->dev_codes, (uint8_t*)out->dev_scales, out->rows, out->cols, (int)mx_atoms(out->cols), dev_x,
                        dev_add, dev_sum, (const bf16*)dev_weight, ld_x, ld_add, ld_sum, dev_add ? add_dtype : -1, eps,

@@ -992,6 +992,8 @@ extern "C" qw_status qw_mx_linear(const qw_mx* x, const qw_mx* w, void* dev_out,
     if (((uintptr_t)dev_out & 15) || ld_out % (dtype == QW_F32 ? 4 : 8))
         return qw_fail(QW_ERR_INVALID_ARG, "%s: rows of out not 16-byte aligned", what);
     if (too_many(x->rows, w->rows)) return qw_fail(QW_ERR_UNSUPPORTED, "%s: more than 2^31 tiles", what);
+    const MxSpan rows = mx_rows_span(dev_out, x->rows, w->rows, ld_out, dtype);
+    if (mx_meet(*x, rows) || mx_meet(*w, rows)) return qw_fail(QW_ERR_INVALID_ARG, "%s: out overlaps x or w", what);
     if (few(*x, *w, false)) {
         MfP p;
         MfMaps m;
@@ -1030,6 +1032,7 @@ extern "C" qw_status qw_mx_swiglu(const qw_mx* x, const qw_mx* w_gate, const qw_
     if (!dev_status) return qw_fail(QW_ERR_INVALID_ARG, "%s: NULL status", what);
     if (x->rows == 0) return QW_OK;
     if (too_many(x->rows, w_gate->rows)) return qw_fail(QW_ERR_UNSUPPORTED, "%s: more than 2^31 tiles", what);
+    if (mx_meet(*out, *x) || mx_meet(*out, *w_gate) || mx_meet(*out, *w_up)) return qw_fail(QW_ERR_INVALID_ARG, "%s: out overlaps an input", what);
     if (few(*x, *w_gate, true)) {
         MfP p;
         MfMaps m;

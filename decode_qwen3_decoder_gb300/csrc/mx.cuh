@@ -186,3 +186,19 @@ __device__ __forceinline__ void mx_store8(void* base, size_t off, int left, cons
 
 // Host-side check of a matrix; QW_OK or the recorded error. A matrix without rows may have no memory.
 qw_status mx_check(const qw_mx* m, const char* what, const char* name);
+
+// Memory of an operand: `rows` of `len` bytes, `step` bytes apart.
+struct MxSpan {
+    uintptr_t at;
+    size_t rows, len, step;
+};
+inline MxSpan mx_rows_span(const void* p, int rows, int cols, size_t ld, int dtype) {
+    const size_t es = dtype == QW_F32 ? 4 : 2;
+    return {(uintptr_t)p, p ? (size_t)rows : 0, cols * es, ld * es};
+}
+// Whether two operands share a byte. Rows may lie between another's rows (column slices of one buffer, which have one
+// step); of two operands with gaps and different steps it is not looked at.
+bool mx_meet(const MxSpan& a, const MxSpan& b);
+// The same of an operand and a matrix's codes and exponents, and of two matrices.
+bool mx_meet(const qw_mx& m, const MxSpan& b);
+bool mx_meet(const qw_mx& a, const qw_mx& b);

@@ -525,8 +525,9 @@ qw_status qw_kv_evict(qw_kv* kv, int seq_id, int n_keep, int n_recent, void* str
  * Rows of tensors (x, add, sum, out) are ld elements apart, and 16-byte aligned (ld a multiple of 8, of 4 for
  * QW_F32), else QW_ERR_INVALID_ARG; elements between the columns and ld are neither read nor written. Any
  * number of rows and 1 to QW_MX_MAX_COLS columns; without rows nothing happens and no memory is looked
- * at. Outputs overlap no input but where it says so. QW_F16 results stop at 65504. All calls are asynchronous
- * on `stream`, whose device has to be the current one. */
+ * at. Outputs overlap no input and no other output but where it says so, else QW_ERR_INVALID_ARG (rows may lie between the
+ * rows of another tensor of the same stride in bytes; tensors with gaps and different strides are not compared). QW_F16 results
+ * stop at 65504. All calls are asynchronous on `stream`, whose device has to be the current one. */
 #define QW_MX_MAX_COLS (1 << 20)
 #define QW_MX_TIMEOUT 2 /* bit of *dev_status (never cleared here): a bounded wait inside a kernel gave up, outputs not valid */
 

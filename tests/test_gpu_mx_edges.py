@@ -146,3 +146,27 @@ def test_rmsnorm_end_of_fp32(lib, bits):
         x[r, 40] = np.sqrt(128 * (w[0] / want) ** 2 - 1)
     x = torch.from_numpy(x.astype(np.float32))
     _check_norm(lib, x, None, w, bits, F32, None, eps=1e-20)
+
+
+def test_operands_in_one_buffer(lib):
+    """Column slices of one buffer share no element: x, the branch, the sum and a product's output side by side, and codes next to
+    one another."""
+    import torch
+    rng = np.random.default_rng(0)
+    T, D = 70, 256
+    buf = torch.from_numpy(rng.normal(0, 1, (T, 4 * D))).float().cuda()
+    x, add, s, o = (buf[:, D * i:D * (i + 1)] for i in range(4))
+    want = (x + add).cpu()
+    nc, ns = lib.qw_mx_code_bytes(8, T, D), lib.qw_mx_scale_bytes(T, D)
+    codes, scales = torch.empty(2 * nc, dtype=torch.uint8, device="cuda"), torch.empty(2 * ns, dtype=torch.uint8, device="cuda")
+    a, b = (lib.qw_mx_view(codes.data_ptr() + nc * i, scales.data_ptr() + ns * i, T, D, 8) for i in range(2))
+    w = torch.ones(D, dtype=torch.bfloat16, device="cuda")
+    lib.qw_mx_rmsnorm(a, x.data_ptr(), 4 * D, lib.QW_F32, add.data_ptr(), 4 * D, lib.QW_F32, s.data_ptr(), 4 * D, w.data_ptr(), 1e-6)
+    m = base.Matrix.of(lib, rng.normal(0, 0.1, (D, D)), 8)
+    st = base._status()
+    lib.qw_mx_linear(a, m.view, o.data_ptr(), 4 * D, lib.QW_F32, st.data_ptr())
+    lib.qw_mx_swiglu(a, m.view, m.view, b, st.data_ptr())
+    torch.cuda.synchronize()
+    assert torch.equal(s.cpu(), want) and int(st.item()) == 0
+    h = mx.values(*mx.quantize(mx.rmsnorm(want.double().numpy(), 1.0, float(np.float32(1e-6))), 8), 8, D)
+    base._check_product(o.double().cpu().numpy(), h, m.held, F32)
