@@ -489,7 +489,7 @@ struct MfCfg {
     static constexpr int NEED = 1024 + STAGES * STAGE + 256, SHARE = COLS * 456 - 1024;
     static constexpr int SMEM = NEED > SHARE ? NEED : SHARE;
     static constexpr int PER_SM = 233472 / (SMEM + 1024);  // CTAs that share an SM
-    static_assert(COLS_USED <= COLS && PER_SM >= 1 && PER_SM * COLS <= 512 && SMEM <= 232448, "shared or tensor memory");
+    static_assert(COLS_USED <= COLS && (PER_SM == 1 || PER_SM == 2) && PER_SM * COLS <= 512 && SMEM <= 232448, "shared or tensor memory");
     static_assert(NW * BN * 512 <= STAGES * STAGE, "partial sums");
 };
 
@@ -862,29 +862,60 @@ cudaError_t launch_gemm(const MgMaps& m, const MxGemmP& p, cudaStream_t st) {
                      SMEM, 2, m, p);
 }
 
-template <int XB, int WB, bool GLU, int BN>
-cudaError_t launch_few(const MfMaps& m, const MfP& p, const Device& d, int slots, cudaStream_t st) {
-    constexpr int SMEM = MfCfg<XB == 4, GLU, BN>::SMEM;
-    const auto kern = k_mx_gemm_few<XB, WB, GLU, BN>;
-    static std::atomic<unsigned long long> done;
-    const cudaError_t e = allow_smem(kern, SMEM, d, done);
-    if (e != cudaSuccess) return e;
-    const LaunchCtx c = {st, true, nullptr};
-    return p.lsplits ? launch_kc(c, kern, dim3(p.tiles_w << p.lsplits), dim3(MF_THREADS), SMEM, 1u << p.lsplits, m, p)
-                     : launch_k(c, kern, dim3(std::min(p.tiles_w, slots)), dim3(MF_THREADS), SMEM, m, p);
+// Clusters of 2^l CTAs, each with an SM to itself, that the device holds at once; asked once for a device and size. A cluster
+// lies within one of the GPU's groups of SMs: 15 of 8, 36 of 4 and 76 of 2 fit on 152 SMs.
+template <typename K>
+int clusters_of_sms(K kern, int smem, int l, const Device& d, std::atomic<int>* known) {
+    std::atomic<int>* at = d.id >= 0 && d.id < 64 ? known + 4 * d.id + l : nullptr;
+    int n = at ? at->load(std::memory_order_relaxed) : 0;
+    if (n) return n - 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1u << l);
+    cfg.blockDim = dim3(MF_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1u << l;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        n = 0;
+    }
+    if (at) at->store(n + 1, std::memory_order_relaxed);
+    return n;
 }
 
 template <int XB, int WB, bool GLU, int BN>
 cudaError_t launch_few_split(const MfMaps& m, MfP& p, cudaStream_t st) {
+    using C = MfCfg<XB == 4, GLU, BN>;
+    const auto kern = k_mx_gemm_few<XB, WB, GLU, BN>;
+    static std::atomic<unsigned long long> done;
+    static std::atomic<int> known[64 * 4];
     const int nk = XB == 4 ? (p.atoms + 1) / 2 : p.atoms;
     const Device d = device();
-    const int slots = d.sms * MfCfg<XB == 4, GLU, BN>::PER_SM;
-    // the widest cluster whose CTAs all find a place and have two stages at least: one row by 4096 x 4096 5.0 us with 8 CTAs
-    // a tile, 7.4 with two, 11 with one; by 4096 x 1024 3.5 with four, 3.9 with 8 of one stage, 4.5 with one
+    const cudaError_t e = allow_smem(kern, C::SMEM, d, done);
+    if (e != cudaSuccess) return e;
+    const int slots = d.sms * C::PER_SM;
+    // the widest cluster that all tiles get at once and whose CTAs have two stages at least: one row by 4096 x 4096 5.0 us with 8
+    // CTAs a tile, 7.4 with two, 11 with one; by 4096 x 1024 3.5 with four, 3.9 with 8 of one stage, 4.5 with one. Clusters that
+    // come second cost most of another turn: 128 rows by 2048 x 12288 with 8 a tile (16 clusters where 15 fit) 16.6 us, with four
+    // 10.3. Where two CTAs share an SM, which the query does not count, a cluster takes half as many SMs; at once run 36 of 8,
+    // 74 of 4 (two of the 76 that it counts find no place) and 152 of 2: one row by 37 x 128 rows of 4096 columns with 8 a tile
+    // 8.1, with four 5.5, by 74 x 128 with four 6.3, by 75 x 128 10.3, with two 7.7
     p.lsplits = 0;
-    while (p.lsplits < 3 && (long long)p.tiles_w << (p.lsplits + 1) <= slots && 4 << p.lsplits <= nk) ++p.lsplits;
-    return launch_few<XB, WB, GLU, BN>(m, p, d, slots, st);
+    for (int l = 1; l <= 3 && (long long)p.tiles_w << l <= slots && 2 << l <= nk; ++l) {
+        const int at_once = C::PER_SM == 1 ? clusters_of_sms(kern, C::SMEM, l, d, known)
+                            : l == 1       ? 2 * clusters_of_sms(kern, C::SMEM, 1, d, known)
+                                           : clusters_of_sms(kern, C::SMEM, l - 1, d, known) - (l == 2 ? 2 : 0);
+        if (p.tiles_w <= at_once) p.lsplits = l;
+    }
+    const LaunchCtx c = {st, true, nullptr};
+    return p.lsplits ? launch_kc(c, kern, dim3(p.tiles_w << p.lsplits), dim3(MF_THREADS), C::SMEM, 1u << p.lsplits, m, p)
+                     : launch_k(c, kern, dim3(std::min(p.tiles_w, slots)), dim3(MF_THREADS), C::SMEM, m, p);
 }
+
 template <int XB, int WB, bool GLU>
 cudaError_t launch_few_rows(const MfMaps& m, MfP& p, cudaStream_t st) {
     if constexpr (!GLU)

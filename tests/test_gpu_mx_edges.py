@@ -170,3 +170,56 @@ def test_operands_in_one_buffer(lib):
     assert torch.equal(s.cpu(), want) and int(st.item()) == 0
     h = mx.values(*mx.quantize(mx.rmsnorm(want.double().numpy(), 1.0, float(np.float32(1e-6))), 8), 8, D)
     base._check_product(o.double().cpu().numpy(), h, m.held, F32)
+
+
+@pytest.mark.parametrize("xb,wb", base.FORMATS)
+@pytest.mark.parametrize("T", [2, 60, 120])
+def test_tiles_around_what_clusters_fit(lib, T, xb, wb):
+    """128 rows of w a tile, shared by as many CTAs as all tiles get at once: around 15, 36, 74 and 152 tiles."""
+    K = 4096 if xb == 4 else 2100
+    x, xr = base._device_matrix(lib, T, K, xb, 1)
+    for tiles in (14, 15, 16, 18, 19, 20, 30, 31, 36, 37, 38, 39, 72, 73, 75, 76, 77, 152, 153):
+        M = 128 * tiles - 5
+        w, wr = base._device_matrix(lib, M, K, wb, tiles)
+        m = np.unique(np.concatenate([np.arange(0, M, 97), np.arange(M - 130, M)]))
+        base._check_product(base._linear(lib, x, w, F32)[:, m].double().cpu().numpy(), xr(np.arange(T)), wr(m), F32)
+
+
+def test_first_calls_are_captured(qw):
+    """A process whose first products are captured: what the calls ask of the device once is asked under capture."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import sys
+sys.path[:0] = [%r, %r]
+import numpy as np, torch
+import decode_qwen3_decoder_gb300 as pkg
+import test_gpu_mx as base
+pkg._build_lib()
+lib = pkg.qw
+lib.load()
+rng = np.random.default_rng(0)
+graphs = []
+for T, K, M in ((2, 2048, 1200), (100, 2048, 2100), (200, 256, 300)):
+    x, w = base.Matrix.of(lib, rng.normal(0, 1, (T, K)), 8), base.Matrix.of(lib, rng.normal(0, 1, (M, K)), 8)
+    out, st = torch.zeros((T, -(-M // 8) * 8), device="cuda"), base._status()
+    h = base.Matrix(lib, T, M, 8)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        s = torch.cuda.current_stream()
+        lib.qw_mx_linear(x.view, w.view, out.data_ptr(), out.stride(0), lib.QW_F32, st.data_ptr(), s)
+        lib.qw_mx_swiglu(x.view, w.view, w.view, h.view, st.data_ptr(), s)
+    graphs.append((g, x, w, out, st, h, M))
+for g, x, w, out, st, h, M in graphs:
+    g.replay()
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    base._check_product(out[:, :M].double().cpu().numpy(), x.held, w.held, "f32")
+    base._check_swiglu(h, x.held, w.held, w.held)
+print("captured")
+"""
+    tests = os.path.dirname(os.path.abspath(__file__))
+    r = subprocess.run([sys.executable, "-c", code % (os.path.dirname(tests), tests)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stdout[-500:] + r.stderr[-2000:]
