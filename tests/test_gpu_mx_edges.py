@@ -223,3 +223,52 @@ print("captured")
     tests = os.path.dirname(os.path.abspath(__file__))
     r = subprocess.run([sys.executable, "-c", code % (os.path.dirname(tests), tests)], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "captured" in r.stdout, r.stdout[-500:] + r.stderr[-2000:]
+
+
+def _with_scales(lib, codes, exps, bits):
+    """A matrix of codes [rows, runs, 32] under any exponents [rows, runs]."""
+    import torch
+    m = base.Matrix(lib, codes.shape[0], codes.shape[1] * 32, bits)
+    cb, sb = mx.pack(codes, exps, bits)
+    m.codes[:m.nc], m.scales[:m.ns] = torch.from_numpy(cb).cuda(), torch.from_numpy(sb).cuda()
+    m.held, m.written = mx.values(codes, exps, bits, m.cols), True
+    return m
+
+
+@pytest.mark.parametrize("xb,wb", base.FORMATS)
+@pytest.mark.parametrize("T", [1, 16, 60, 200])
+def test_linear_any_scale(lib, T, xb, wb):
+    """Codes that are not 0 under the smallest and largest powers of two, 2^-127 and 2^127, that cancel in the product: exponent
+    bytes 0 to 254 in the tensor cores."""
+    rng = np.random.default_rng(T)
+    M, runs = 300, 24
+    top = {8: 126, 4: 7}  # the codes' magnitudes; e4m3's 127 is NaN
+    cx, cw = (np.where(rng.integers(0, 2, (r, runs, 32)) > 0, 1 << (b - 1), 0) | rng.integers(1, top[b] + 1, (r, runs, 32)) for r, b in ((T, xb), (M, wb)))
+    e = np.tile([-127, -126, -125, 126, 127, 0, -64, 100], 3)
+    ex, ew = np.tile(e, (T, 1)), np.tile(-e, (M, 1))
+    ew[:, e == -127] = 126
+    x, w = _with_scales(lib, cx.astype(np.uint8), ex, xb), _with_scales(lib, cw.astype(np.uint8), ew, wb)
+    got = base._linear(lib, x, w, F32).double().cpu().numpy()
+    base._check_product(got, x.held, w.held, F32)
+    # and the same values under ordinary scales give the same bits
+    x1, w1 = _with_scales(lib, cx.astype(np.uint8), ex * 0, xb), _with_scales(lib, cw.astype(np.uint8), ew + e, wb)
+    np.testing.assert_array_equal(base._linear(lib, x1, w1, F32).double().cpu().numpy(), got)
+
+
+@pytest.mark.parametrize("xb,wb,ob", [(8, 8, 8), (8, 4, 8), (4, 4, 4)])
+@pytest.mark.parametrize("T", [1, 16, 64, 200, 2000])
+def test_swiglu_codes_of_exact_sums(lib, T, xb, wb, ob):
+    """Random gates and ups whose sums are exact in fp32 (integers below 2^24): codes differ from those of the 64-bit values only
+    where the value lies within 2^-21 of a border."""
+    rng = np.random.default_rng(T)
+    K, I = 256, 640
+    whole = lambda r, s: rng.integers(-3, 4, (r, K)) * s  # noqa: E731
+    x, g, u = (base.Matrix.of(lib, a, b) for a, b in ((whole(T, 1.0), xb), (whole(I, 1 / 32), wb), (whole(I, 0.125), wb)))
+    gv, uv = x.held @ g.held.T, x.held @ u.held.T
+    h = gv / (1 + np.exp(-gv)) * uv
+    c, e = base._swiglu(lib, x, g, u, ob).get()
+    got = mx.values(c, e, ob, I)
+    near = np.sort(np.stack([mx.held(h * (1 + s * 2.0 ** -21), ob) for s in (-1, 1)]), axis=0)
+    assert ((got >= near[0]) & (got <= near[1])).all()
+    # the inputs alone: how many codes are left open (the sums take few values, so that some come together)
+    assert np.mean(near[0] != near[1]) < 1e-3
