@@ -1016,7 +1016,7 @@ extern "C" qw_status qw_mx_linear(const qw_mx* x, const qw_mx* w, void* dev_out,
     if (qw_status s = mx_check(w, what, "w")) return s;
     if (qw_status s = formats_check(x, w, what)) return s;
     if (dtype != QW_F16 && dtype != QW_BF16 && dtype != QW_F32) return qw_fail(QW_ERR_INVALID_ARG, "%s: dtype %d", what, dtype);
-    if (!dev_status) return qw_fail(QW_ERR_INVALID_ARG, "%s: NULL status", what);
+    if (!dev_status || ((uintptr_t)dev_status & 3)) return qw_fail(QW_ERR_INVALID_ARG, "%s: status NULL or not 4-byte aligned", what);
     if (x->rows == 0 || w->rows == 0) return QW_OK;
     if (!dev_out) return qw_fail(QW_ERR_INVALID_ARG, "%s: NULL out", what);
     if (ld_out < (size_t)w->rows) return qw_fail(QW_ERR_INVALID_ARG, "%s: row stride of out below w's rows", what);
@@ -1060,7 +1060,7 @@ extern "C" qw_status qw_mx_swiglu(const qw_mx* x, const qw_mx* w_gate, const qw_
         return qw_fail(QW_ERR_INVALID_ARG, "%s: w_gate and w_up differ in shape or bits", what);
     if (out->rows != x->rows || out->cols != w_gate->rows)
         return qw_fail(QW_ERR_INVALID_ARG, "%s: out is not [rows of x][rows of w_gate]", what);
-    if (!dev_status) return qw_fail(QW_ERR_INVALID_ARG, "%s: NULL status", what);
+    if (!dev_status || ((uintptr_t)dev_status & 3)) return qw_fail(QW_ERR_INVALID_ARG, "%s: status NULL or not 4-byte aligned", what);
     if (x->rows == 0) return QW_OK;
     if (too_many(x->rows, w_gate->rows)) return qw_fail(QW_ERR_UNSUPPORTED, "%s: more than 2^31 tiles", what);
     if (mx_meet(*out, *x) || mx_meet(*out, *w_gate) || mx_meet(*out, *w_up)) return qw_fail(QW_ERR_INVALID_ARG, "%s: out overlaps an input", what);

@@ -56,3 +56,15 @@ def test_operands_that_share_memory(qw):
     for codes, scales in ((A, 8 * A), (7 * A, A), (2 * A, 8 * A), (3 * A + 32, 8 * A), (7 * A, 6 * A), (7 * A, 5 * A + nc - 32)):
         st = L.qw_mx_swiglu(m(A, 2 * A), m(3 * A, 4 * A), m(5 * A, 6 * A), m(codes, scales, 200, 200), far, None)
         assert st == -1 and "overlaps" in qw.qw_last_error(), (codes, scales)
+
+
+def test_status_alignment(qw):
+    """The status word is written by a 32-bit atomic."""
+    import ctypes
+    L, ref = qw.load(), ctypes.byref
+    m = lambda at, rows=3, cols=256: ref(_m(qw, at, at + 65536, rows, cols, 8))  # noqa: E731
+    for off in (1, 2, 3):
+        assert L.qw_mx_linear(m(A), m(2 * A), 3 * A, 8, 0, 4 * A + off, None) == -1
+        assert "status" in qw.qw_last_error()
+        assert L.qw_mx_swiglu(m(A), m(2 * A), m(3 * A), m(4 * A, 3, 3), 5 * A + off, None) == -1
+        assert "status" in qw.qw_last_error()
