@@ -523,11 +523,12 @@ qw_status qw_kv_evict(qw_kv* kv, int seq_id, int n_keep, int n_recent, void* str
  * operators write both, the padding of the rows that they write included.
  *
  * Rows of tensors (x, add, sum, out) are ld elements apart, and 16-byte aligned (ld a multiple of 8, of 4 for
- * QW_F32), else QW_ERR_INVALID_ARG; elements between the columns and ld are neither read nor written. Any
- * number of rows and 1 to QW_MX_MAX_COLS columns; without rows nothing happens and no memory is looked
- * at. Outputs overlap no input and no other output but where it says so, else QW_ERR_INVALID_ARG (rows may lie between the
- * rows of another tensor of the same stride in bytes; tensors with gaps and different strides are not compared). QW_F16 results
- * stop at 65504. All calls are asynchronous on `stream`, whose device has to be the current one. */
+ * QW_F32), else QW_ERR_INVALID_ARG; elements between the columns and ld are neither read nor written. 1 to
+ * QW_MX_MAX_COLS columns and up to 2^31 - 1 pieces of 128 columns (rows x ceil(cols / 128)), else QW_ERR_INVALID_ARG;
+ * without rows nothing happens and no memory is looked at. Outputs overlap no input and no other output but where it
+ * says so, else QW_ERR_INVALID_ARG (rows may lie between the rows of another tensor of the same stride in bytes;
+ * tensors with gaps and different strides are not compared). QW_F16 results stop at 65504. All calls are asynchronous
+ * on `stream`, whose device has to be the current one. */
 #define QW_MX_MAX_COLS (1 << 20)
 #define QW_MX_TIMEOUT 2 /* bit of *dev_status (never cleared here): a bounded wait inside a kernel gave up, outputs not valid */
 
@@ -560,7 +561,8 @@ qw_status qw_mx_rmsnorm(const qw_mx* out, const void* dev_x, size_t ld_x, int x_
 
 /* out[t][m] = sum_k x[t][k] w[m][k], rounded once to `dtype`: x [T][K], w [M][K], out [T] rows of M. Products of
  * codes are exact and sums are kept in fp32. x and w in 8 and 4, 4 and 4 or 8 and 8 bits (4 and 8:
- * QW_ERR_UNSUPPORTED). The order of the sums is fixed for given sizes: equal inputs give equal bits. */
+ * QW_ERR_UNSUPPORTED). The order of the sums is fixed for given sizes: equal inputs give equal bits. More than 2^31
+ * tiles of 256 rows of x by 128 of w (QW_ERR_UNSUPPORTED) need more memory than there is. */
 qw_status qw_mx_linear(const qw_mx* x, const qw_mx* w, void* dev_out, size_t ld_out, int dtype, int32_t* dev_status,
                        void* stream);
 
