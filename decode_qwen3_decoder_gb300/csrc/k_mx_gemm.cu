@@ -209,15 +209,18 @@ __device__ __forceinline__ void store_box(const CUtensorMap* map, const MxGemmP&
         }
 }
 
-// silu(g) u = g u / (1 + e^-g). expf is within a unit of its last place (2^-23) wherever g lies, the hardware's reciprocal within
-// 2^-23; three roundings of 2^-24 with them: below 2^-21. (The hardware's 2^t of -g log2 e alone is faster, but t's own
-// rounding grows with g to 2^-18: 8192 x 1024 by 3072 in 8 by 4 bits 40.5 us, now 43.1; with an exact division too, 57.3, and
-// 2^-22.3 in place of 2^-22.) A quarter of the denominator, so that the reciprocal is a normal number wherever e^-g is finite
-// (g > -88.7), and g takes the quarter back, so that the sigmoid is never formed, which leaves the normal numbers earlier.
+// silu(g) u = g / (1 + e^-g) u. expf is within a unit of its last place (2^-23) wherever g lies; the sum, the quotient (the
+// hardware's reciprocal, 2^-23, and the remainder, which an FMA gives exactly) and the product are rounded once each:
+// 5 2^-24, as in plain fp32 arithmetic. A code has 4 bits: of 25 million (8192 x 1024 by 3072, 8 by 4 bits) 13 to 19 differ from
+// those of 64 bits, the same as there. 44.7 us; with a division 57.3; without the remainder 43.4, and 2^-21.9 in place of
+// 2^-22.1 at worst; with 2^t of a rounded t = -g log2 e 40.7, but then t's rounding grows with g to 2^-18.
+// A quarter of both, so that the reciprocal is a normal number wherever e^-g is finite; beyond (g < -88.7) it is 0, as is h.
 __device__ __forceinline__ float silu_mul(float g, float u) {
     float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(expf(-g), 0.25f, 0.25f)));
-    return g * 0.25f * r * u;
+    const float d = fminf(fmaf(expf(-g), 0.25f, 0.25f), 3.402823466e38f), n = g * 0.25f;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+    const float y = n * r;
+    return fmaf(fmaf(-d, y, n), r, y) * u;
 }
 
 // A thread's run of 32 features of row t: codes and exponent. Features from M on are zeros.

@@ -567,7 +567,7 @@ qw_status qw_mx_linear(const qw_mx* x, const qw_mx* w, void* dev_out, size_t ld_
                        void* stream);
 
 /* out = quantise(SiLU(x w_gate^T) * (x w_up^T)): x [T][K], w_gate and w_up [I][K] of the same bits, out [T][I] in 8
- * or 4 bits. The products as in qw_mx_linear; SiLU and the product of the two in fp32 (2^-21 relative
+ * or 4 bits. The products as in qw_mx_linear; SiLU and the product of the two in fp32 (within 5 2^-24
  * where both are normal numbers; 0 for gates below -88.7), then quantised. */
 qw_status qw_mx_swiglu(const qw_mx* x, const qw_mx* w_gate, const qw_mx* w_up, const qw_mx* out, int32_t* dev_status,
                        void* stream);
