@@ -11,11 +11,15 @@
 // type of its own: the codes are those of the real y, whatever the order of the sums. y is computed in fp32 with a
 // relative error d below 18 2^-24; a run in which a value between y (1 - d) and y (1 + d) could get another code or
 // exponent, one in 1300, is computed again: the row's sum of squares as an unevaluated pair of floats (the
-// products' and sums' errors are added up), 1 / sqrt and the products as pairs, 2^-43 in all. (1 / sqrt in fp64, whose
-// rate is low here: 2048 x 8192 35.0 us, as pairs 31.2.) Instructions bound the kernel, 40 an element, and the runs in
-// doubt take a tenth to a fifth of the time: 8192 x 1024 fp32 with a bf16 branch 16.6 us, 92 MB; 2048 x 4096 bf16 15.9. Pairs
-// for every value would double the instructions; persistent CTAs that had the next row copied ahead took 22.3 us. One CTA
-// a row (up to 256 columns one warp); a row's elements stay in registers between the passes.
+// products' and sums' errors are added up, by Dekker's and Knuth's methods), 1 / sqrt and the products as pairs, 2^-43 in all.
+// Where fp32 cannot hold the pairs (runs below 2^-30, weights above 2^50) the products are in 64 bits, and so is a whole row whose
+// squares leave fp32. (1 / sqrt in fp64, whose rate is low here: 2048 x 8192 35.0 us, as pairs 31.2.)
+// 8192 x 1024 fp32 with a bf16 branch 17.1 us, 92 MB (bytes alone 13.6); 2048 x 4096 18.2, 88 MB (13.0); bf16 with a bf16 branch
+// 17.3. Neither bytes nor instructions fill it: 43 instructions an element take 67% (half at 4096 columns) of the issue slots, and a
+// warp waits, in this order, for its row's loads, for shuffles and conversions, and at the row's two barriers, with 65% (45%) of
+// the warps that fit. Pairs for every value would double the instructions; persistent CTAs that had the next row copied ahead took 22.3 us.
+// One CTA a row (up to 256 columns one warp); up to 16384 columns a row's elements stay in registers between the passes. Longer rows
+// are read twice and summed in pairs: 1024 x 20000 bf16 with a bf16 branch 52 us, 225 MB with the second reading (33).
 #include <algorithm>
 
 #include "mx.cuh"
@@ -452,6 +456,8 @@ __device__ __forceinline__ Pair block_sum(Pair t, Pair* part) {
 }
 
 // VPT: vectors of 8 columns a thread keeps in registers; 0: any number, read twice.
+// The bounds of VPT 1 hold a thread to 40 registers; 16 to 24 bytes a thread wait on the stack while a run is redone. 8192 x 1024
+// 17.1 us, with 48 registers and none on the stack 17.8.
 template <int DT, int BITS, int VPT>
 __global__ void __launch_bounds__(VPT == 1 ? 128 : 512, VPT == 1 ? 12 : VPT == 2 ? 2 : 1) k_mx_rmsnorm(const __grid_constant__ MxNormP p) {
     constexpr int N = VPT ? VPT : 1;
@@ -628,11 +634,12 @@ template <int DT, int BITS>
 cudaError_t launch_norm(const MxNormP& p, cudaStream_t st) {
     const LaunchCtx c = {st, true, nullptr};
     const int vecs = p.atoms * (MX_ATOM / 8);
-    // up to 1024 columns a thread has 8 of them, to 8192 16, to 16384 32. Measured (us): 8192 x 1024 16.6 and 17.0 with 16 a
-    // thread; 4096 x 2048 18.7 with 8, 18.1 with 16; 2048 x 4096 24.9 with 8, 18.3 with 16, 20.1 with 32 (1 / sqrt in fp64)
+    // up to 1024 columns a thread has 8 of them, to 8192 16, to 16384 32. Measured (us; fp32 with a bf16 branch): 1 x 1024 1.75 with 8,
+    // 2.2 with 16; 8192 x 1024 17.0 both; 4096 x 2048 18.6 with 8, 17.6 with 16, 21.3 with 32; 2048 x 4096 20.9, 19.0 and 22.0; 1024 x
+    // 16384 (bf16) 40.3 with 32, read twice 43.1
     const int vpt = vecs <= 128 ? 1 : vecs <= 1024 ? 2 : vecs <= 2048 ? 4 : 0;
     const unsigned threads = vpt ? ((vecs + vpt - 1) / vpt + 31) / 32 * 32 : 512;
-    // many rows of one warp: four a CTA (16384 x 256 7.7 us, one a CTA 17.1)
+    // many rows of one warp: four a CTA (16384 x 256 bf16 7.9 us, one a CTA 17.2)
     const unsigned rows = threads == 32 && p.rows >= 4096 ? 4 : 1;
     const dim3 block(threads, rows), grid(((unsigned)p.rows + rows - 1) / rows);
     switch (vpt) {

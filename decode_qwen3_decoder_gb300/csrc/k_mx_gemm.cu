@@ -935,8 +935,8 @@ cudaError_t launch_few_formats(int xb, int wb, const MfMaps& m, MfP& p, cudaStre
 
 // Whether k_mx_gemm_few serves a product of nk stages and tiles of W. Measured against k_mx_gemm (us, 8 by 4 bits): linear, 64 rows
 // by 4096 x 4096 8.1 and 13.5, by 151936 x 1024 25 and 38; 128 rows by 1024 x 8192 9.0 and 22.9, by 4096 x 2048 8.3 and 9.0,
-// by 4096 x 1024 7.6 and 6.6. SwiGLU, whose runs lie across lanes here: 16 rows by 3072 x 1024 5.5 and 6.7; 64 rows by 4096 x 4096
-// 11.7 and 14.1, by 4096 x 1024 8.8 and 6.8, by 6144 x 2048 (two CTAs a tile) 12.6 and 9.7.
+// by 4096 x 1024 7.6 and 6.6. SwiGLU, whose runs lie across lanes here: 16 rows by 3072 x 1024 6.1 and 7.5; 64 rows by 4096 x 4096
+// 12.3 and 14.9, by 3072 x 1024 9.3 and 7.5, by 6144 x 2048 (two CTAs a tile) 13.5 and 10.2.
 bool few(const qw_mx& x, const qw_mx& w, bool glu) {
     const size_t nk = x.bits == 4 ? (mx_atoms(x.cols) + 1) / 2 : mx_atoms(x.cols);
     if (glu) return x.rows <= 16 || (x.rows <= 64 && nk >= 32 && 4 * mx_atoms(w.rows) <= (size_t)device().sms);
