@@ -561,7 +561,7 @@ qw_status qw_mx_rmsnorm(const qw_mx* out, const void* dev_x, size_t ld_x, int x_
 
 /* out[t][m] = sum_k x[t][k] w[m][k], rounded once to `dtype`: x [T][K], w [M][K], out [T] rows of M. Products of
  * codes are exact and sums are kept in fp32, in which the tensor cores drop what an addition does not hold: within
- * (K / 16 + 17) 2^-23 sum|x w| (seen with 4096 columns of 8 by 8 bits: 3e-7 of the sums). x and w in 8 and 4, 4 and 4
+ * (K / 16 + 18) 2^-23 sum|x w| (seen with 4096 columns of 8 by 8 bits: 3e-7 of the sums). x and w in 8 and 4, 4 and 4
  * or 8 and 8 bits (4 and 8: QW_ERR_UNSUPPORTED). The order of the sums is fixed for given sizes: equal inputs give
  * equal bits. More than 2^31 tiles of 256 rows of x by 128 of w (QW_ERR_UNSUPPORTED) need more memory than there is. */
 qw_status qw_mx_linear(const qw_mx* x, const qw_mx* w, void* dev_out, size_t ld_out, int dtype, int32_t* dev_status,
